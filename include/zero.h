@@ -36,8 +36,8 @@
  *    valid until the next call on the same thread).
  *  - All arguments are validated before anything is launched; a call that
  *    fails validation launches nothing and leaves every output untouched.
- *  - Device pointers must be 16-byte aligned (ZERO_ERR_ALIGN otherwise);
- *    torch allocations are 256-byte aligned.
+ *  - Device pointers must be 16-byte aligned (ZERO_ERR_ALIGN otherwise)
+ *    unless the call says otherwise; torch allocations are 256-byte aligned.
  *  - Asynchronous device errors surface as ZERO_ERR_CUDA from the next call
  *    or from zero_sync().
  *  - At most 64 virtual ranks; rank_mask bit r selects rank r.  Pointer
@@ -74,7 +74,9 @@ typedef enum {
   ZERO_ERR_UNSUPPORTED = 6  /* valid request this build does not implement       */
 } zero_status;
 
-typedef enum { ZERO_FP16 = 0, ZERO_BF16 = 1 } zero_dtype;
+/* ZERO_FP32 belongs to the gradient-list, block and expert calls below; the
+ * optimizer's calls take the two 16-bit types. */
+typedef enum { ZERO_FP16 = 0, ZERO_BF16 = 1, ZERO_FP32 = 2 } zero_dtype;
 typedef enum { ZERO_PART_FLAT = 0, ZERO_PART_ROUND_ROBIN = 1 } zero_part_mode;
 typedef enum { ZERO_REDUCE_SUM = 0, ZERO_REDUCE_AVG = 1 } zero_reduce_op;
 
@@ -566,6 +568,176 @@ zero_status zero_step_amp_noalloc(const zero_plan* plan, const void* const* grad
                                   const zero_adamw_hparams* hp, const zero_amp_config* cfg,
                                   void* d_state, uint64_t rank_mask, int64_t bucket_elems,
                                   void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gradient norm and clipping over many tensors                             */
+/* ------------------------------------------------------------------------ */
+/*
+ * The pages' gradient_clipping ("ZeRO ... 实操" (wmrh.cn) §3.1) for gradients
+ * that are still one tensor each (a training loop without the loss-scaled
+ * step, gradients accumulated in fp32, parameters outside the plan):
+ *   norm = sqrt(sum of g^2) over all elements of all tensors (ZERO_NORM_L2),
+ *          or max |g| (ZERO_NORM_INF);
+ *   coef = min(1, max_norm / (norm + 1e-6)), formed in binary64, rounded once
+ *          to binary32; 1 when the norm is not finite;
+ *   dst[i] = src[i] * coef, the product in binary32, rounded once to dst.
+ * A non-finite norm (an infinity or NaN anywhere) is flagged in the record
+ * and scales nothing, so that the caller can skip the step as zero_step_amp
+ * does.  No finite gradients make the norm infinite (squares are summed in
+ * two exactly scaled ranges); values below 2^-103 may count as zero in it.
+ * Sums run in a fixed order: the same call gives the same bits.  Nothing is
+ * read back by the host.
+ */
+typedef enum { ZERO_NORM_L2 = 0, ZERO_NORM_INF = 1 } zero_norm_kind;
+
+/* One tensor.  Pointers need their element's alignment only (a view into a
+ * flat buffer at any offset).  dst (clipping only): src itself, for clipping
+ * in place with equal types, or memory that overlaps no tensor's src or dst,
+ * of any of the three types.  An empty tensor's pointers may be NULL. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t numel;
+  int32_t src_dtype, dst_dtype;
+} zero_grad_tensor;
+
+/* The record a call leaves in caller-owned DEVICE memory (16-byte aligned). */
+typedef struct {
+  double norm;       /* 0 for an empty list                          */
+  float norm32;      /* norm rounded to binary32                     */
+  float coef;        /* 1 after zero_grad_norm                       */
+  int32_t nonfinite; /* 1: the norm is infinite or NaN               */
+  int32_t pad_[3];
+} zero_norm_result;
+
+/* Device workspace of either call for this list. */
+zero_status zero_grad_norm_workspace_bytes(const zero_grad_tensor* tensors, int32_t n_tensors,
+                                           int64_t* bytes);
+
+/* The norm alone (dst and dst_dtype are not read).  `tensors` is host memory,
+ * read during the call; workspace: 16-byte aligned device scratch. */
+zero_status zero_grad_norm(const zero_grad_tensor* tensors, int32_t n_tensors, int32_t kind,
+                           void* d_result, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
+/* Norm and clipping.  max_norm: finite, >= 0. */
+zero_status zero_clip_grad_norm(const zero_grad_tensor* tensors, int32_t n_tensors, int32_t kind,
+                                double max_norm, void* d_result, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Block join: norms before and after a block, its gate and residual scale  */
+/* ------------------------------------------------------------------------ */
+/*
+ * Between two blocks of a model, for every row of `hidden` channels:
+ *   u = N_post(b)     b: the block's output; u = b without w_post
+ *   o = x + scale * g * u   x: the residual stream; g = 1 without a gate
+ *   n = N_pre(o)      the next block's input, from o before its rounding
+ *   N(v) = (v - mean) / sqrt(mean((v - mean)^2) + eps) * w + bias
+ * ZERO_JOIN_RMS has no mean and no bias.  Statistics, products and sums are
+ * binary32; o and n are rounded once.  With b NULL, o = x: the norm alone.
+ * Pointers need their element's alignment only; rows of 16-byte multiples on
+ * 16-byte boundaries take the wide path.
+ */
+typedef enum { ZERO_JOIN_RMS = 0, ZERO_JOIN_LAYER = 1 } zero_join_kind;
+typedef enum {
+  ZERO_GATE_NONE = 0,
+  ZERO_GATE_CHANNEL = 1, /* gate[hidden], shared by the rows    */
+  ZERO_GATE_ROW = 2,     /* one number a row                    */
+  ZERO_GATE_FULL = 3     /* one number an element               */
+} zero_gate_kind;
+
+typedef struct {
+  int64_t rows, hidden;
+  int32_t act_dtype;   /* b, n, d_n, db                                   */
+  int32_t res_dtype;   /* x, o, d_o, dx: act_dtype or ZERO_FP32           */
+  int32_t param_dtype; /* weights and biases: act_dtype or ZERO_FP32      */
+  int32_t gate_dtype;  /* act_dtype or ZERO_FP32                          */
+  int32_t kind, gate_kind;
+  double eps;          /* > 0                                             */
+  double scale;
+  /* elements between rows of the inputs (outputs are contiguous); of row
+   * gates, between two rows' numbers */
+  int64_t x_stride, b_stride, gate_stride, do_stride, dn_stride;
+} zero_join_desc;
+
+typedef struct {
+  const void *x, *b, *gate;
+  const void *w_post, *bias_post; /* NULL: no post norm / no bias */
+  const void *w_pre, *bias_pre;   /* NULL: no pre norm / no bias  */
+} zero_join_inputs;
+
+/* Any entry may be NULL: that gradient is not formed.  dgate has the gate's
+ * type and (contiguous) shape, the parameters' gradients the parameters'. */
+typedef struct {
+  void *dx, *db, *dgate, *dw_post, *dbias_post, *dw_pre, *dbias_pre;
+} zero_join_grads;
+
+/* o (res_dtype) and n (act_dtype, needs w_pre): [rows, hidden], one of them
+ * may be NULL.  o may be x and n may be b when nothing is kept for a backward
+ * pass.  stats (nullable, 16-byte aligned): float[rows][4], which the
+ * backward pass takes.  rows == 0 does nothing. */
+zero_status zero_block_join(const zero_join_desc* desc, const zero_join_inputs* inputs, void* o,
+                            void* n, float* stats, void* stream);
+
+/* Device workspace of the backward call (16-byte aligned). */
+zero_status zero_block_join_workspace_bytes(const zero_join_desc* desc, int64_t* bytes);
+
+/* The gradients of the same inputs from d_o and d_n (either may be NULL: no
+ * gradient comes that way) and the forward call's stats.  x and b still hold
+ * what the forward call read.  The parameters' gradients are summed over the
+ * rows in a fixed order; with rows == 0 they are zero.  The workspace is
+ * needed when any of them, or a channel gate's, is wanted. */
+zero_status zero_block_join_backward(const zero_join_desc* desc, const zero_join_inputs* inputs,
+                                     const void* d_o, const void* d_n, const float* stats,
+                                     const zero_join_grads* grads, void* workspace,
+                                     int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Expert permutation: tokens sorted by expert, brought back with weights   */
+/* ------------------------------------------------------------------------ */
+/*
+ * Choice k of token t is pair p = t*topk + k, of expert ids[p]; a choice
+ * outside [0, n_experts) is dropped.  The kept pairs in order of (expert,
+ * pair) take the rows 0 .. M-1 of a buffer of tokens*topk rows:
+ *   offsets[e] = first row of expert e (n_experts + 1 entries, the last is M)
+ *   rows[p]    = the row of pair p, -1 when dropped
+ *   pairs[i]   = the pair of row i, -1 for i >= M
+ * ids: int32 (id_bytes 4) or int64 (8).  n_experts at most 4096, tokens*topk
+ * below 2^31.  The order is stable.  Nothing is read back by the host.
+ */
+zero_status zero_expert_sort(const void* ids, int32_t id_bytes, int64_t tokens, int32_t topk,
+                             int32_t n_experts, int32_t* offsets, int32_t* rows, int32_t* pairs,
+                             void* stream);
+
+/* xs[rows[p]] = x[t]; the rows of xs past M are zero.  x_stride: elements
+ * between rows of x; xs is [tokens*topk, hidden], contiguous. */
+zero_status zero_expert_dispatch(const void* x, int64_t x_stride, zero_dtype dtype, int64_t tokens,
+                                 int32_t topk, int64_t hidden, const int32_t* offsets,
+                                 int32_t n_experts, const int32_t* rows, void* xs, void* stream);
+
+/* dx[t] = sum of dxs[rows[p]] over the token's kept pairs, in binary32, k in
+ * order, rounded once.  The rows of dxs past M are not read. */
+zero_status zero_expert_dispatch_backward(const void* dxs, zero_dtype dtype, int64_t tokens,
+                                          int32_t topk, int64_t hidden, const int32_t* rows,
+                                          void* dx, void* stream);
+
+/* y[t] = sum of weights[p] * ys[rows[p]] over the token's kept pairs, in
+ * binary32, k in order, rounded once; zero for a token without any.  weights:
+ * [tokens, topk] of weight_dtype (dtype or ZERO_FP32).  The rows of ys past M
+ * are not read. */
+zero_status zero_expert_combine(const void* ys, zero_dtype dtype, const void* weights,
+                                zero_dtype weight_dtype, int64_t tokens, int32_t topk,
+                                int64_t hidden, const int32_t* rows, void* y, void* stream);
+
+/* dys[rows[p]] = weights[p] * dy[t], zero past M; dweights[p] (nullable) =
+ * <dy[t], ys[rows[p]]> in binary32, zero for a dropped pair. */
+zero_status zero_expert_combine_backward(const void* dy, int64_t dy_stride, const void* ys,
+                                         zero_dtype dtype, const void* weights,
+                                         zero_dtype weight_dtype, int64_t tokens, int32_t topk,
+                                         int64_t hidden, const int32_t* offsets,
+                                         int32_t n_experts, const int32_t* rows, void* dys,
+                                         void* dweights, void* stream);
 
 /*
  * Measurement helper; the pages have no counterpart.  Launches, on `stream`,

@@ -2,8 +2,10 @@
 
 The compute lives in libzero.so (C ABI: include/zero.h; CUDA kernels for
 sm_103a in csrc/); this package is its Python binding.  ``engine`` wires a
-model's backward pass into it; ``workloads`` holds the seeded synthetic
-parameter groups used by the tests and the benchmark.
+model's backward pass into it; ``train_ops`` holds the operators of a
+training step around it (gradient norm and clipping, block join, expert
+permutation); ``workloads`` holds the seeded synthetic parameter groups used
+by the tests and the benchmark.
 """
 from .zero import (AMP_STATE_BYTES, ZERO_BF16, ZERO_FP16, ZERO_PART_FLAT,  # noqa: F401
                    ZERO_PART_ROUND_ROBIN, ZERO_REDUCE_AVG, ZERO_REDUCE_SUM, AdamW, AmpConfig,
@@ -19,3 +21,20 @@ from .zero import (AMP_STATE_BYTES, ZERO_BF16, ZERO_FP16, ZERO_PART_FLAT,  # noq
                    zero_floor_probe, zero_selftest_wait_timeout, zero_step, zero_step_amp,
                    zero_step_amp_noalloc, zero_step_amp_reduced, zero_step_amp_shards,
                    zero_sync, zero_version, zero_zero3_pass)
+
+
+_TRAIN_OPS = ("ClipGradNorm", "ExpertOrder", "GradNorm", "NormResult", "block_join",
+              "expert_combine", "expert_dispatch", "read_norm_result", "zero_block_join",
+              "zero_block_join_backward", "zero_clip_grad_norm", "zero_expert_combine",
+              "zero_expert_combine_backward", "zero_expert_dispatch",
+              "zero_expert_dispatch_backward", "zero_expert_sort", "zero_grad_norm")
+
+
+def __getattr__(name):
+    # train_ops needs torch at import time, this package does not
+    if name in _TRAIN_OPS:
+        from . import train_ops
+        value = getattr(train_ops, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -20,7 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzero.so")
 
 SOURCES = ["zero_plan.cpp", "zero_capi.cpp", "zero_launch.cu", "zero_kernels_fp16.cu",
-           "zero_kernels_bf16.cu", "zero_noalloc.cu", "zero_cpu_adam.cpp"]
+           "zero_kernels_bf16.cu", "zero_noalloc.cu", "zero_cpu_adam.cpp", "zero_gradnorm.cu",
+           "zero_join.cu", "zero_experts.cu"]
 # extra host-compiler flags per source: the host AdamW loop is vectorised at
 # -O3; -fno-math-errno lets sqrtf be the plain instruction (results unchanged)
 EXTRA = {"zero_cpu_adam.cpp": ["-Xcompiler", "-O3,-fno-math-errno"]}

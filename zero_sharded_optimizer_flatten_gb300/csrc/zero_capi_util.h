@@ -5,12 +5,17 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "zero.h"
 
 namespace zero {
 
 // Thread-local message of the last failed call (see zero_last_error).
 char* error_buffer();
+
+// Launches issued since load (zero_launch_count).
+extern std::atomic<int64_t> g_launches;
 
 inline void clear_error() { error_buffer()[0] = '\0'; }
 

@@ -1,0 +1,136 @@
+// Element access and small reductions shared by the kernels that work on
+// rows of activations and on lists of gradient tensors.  Values are widened
+// to binary32 on load and rounded once, to nearest even, on store.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "zero.h"
+
+namespace zero {
+
+constexpr int kSMs = 152;  // SMs of a GB300: persistent grids are multiples of it
+constexpr unsigned kFull = 0xffffffffu;
+
+// One element and eight consecutive elements ("an octet"; 16 bytes of 16-bit
+// data, 32 bytes of fp32 data, the address 16-byte aligned).
+template <class T>
+struct Elem;
+
+template <>
+struct Elem<float> {
+  static constexpr zero_dtype kType = ZERO_FP32;
+  static __device__ __forceinline__ float widen(float x) { return x; }
+  static __device__ __forceinline__ float narrow(float x) { return x; }
+  static __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  static __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+template <>
+struct Elem<__half> {
+  static constexpr zero_dtype kType = ZERO_FP16;
+  static __device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half narrow(float x) { return __float2half_rn(x); }
+  static __device__ __forceinline__ void unpack(uint32_t w, float& lo, float& hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x, hi = f.y;
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    unpack(w.x, v[0], v[1]), unpack(w.y, v[2], v[3]);
+    unpack(w.z, v[4], v[5]), unpack(w.w, v[6], v[7]);
+  }
+  static __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+  }
+};
+
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr zero_dtype kType = ZERO_BF16;
+  static __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ __nv_bfloat16 narrow(float x) { return __float2bfloat16_rn(x); }
+  static __device__ __forceinline__ void unpack(uint32_t w, float& lo, float& hi) {
+    lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    unpack(w.x, v[0], v[1]), unpack(w.y, v[2], v[3]);
+    unpack(w.z, v[4], v[5]), unpack(w.w, v[6], v[7]);
+  }
+  static __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+  }
+};
+
+// Element i of an array whose type is known only at run time (parameters,
+// gates, weights: read rarely, the branch is uniform).
+__device__ __forceinline__ float load_any(const void* p, int64_t i, int type) {
+  if (type == ZERO_FP32) return static_cast<const float*>(p)[i];
+  if (type == ZERO_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+__device__ __forceinline__ void store_any(void* p, int64_t i, int type, float v) {
+  if (type == ZERO_FP32)
+    static_cast<float*>(p)[i] = v;
+  else if (type == ZERO_BF16)
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ void load8_any(const void* p, int64_t i, int type, float (&v)[8]) {
+  if (type == ZERO_FP32)
+    Elem<float>::load8(static_cast<const float*>(p) + i, v);
+  else if (type == ZERO_BF16)
+    Elem<__nv_bfloat16>::load8(static_cast<const __nv_bfloat16*>(p) + i, v);
+  else
+    Elem<__half>::load8(static_cast<const __half*>(p) + i, v);
+}
+
+__device__ __forceinline__ void store8_any(void* p, int64_t i, int type, const float (&v)[8]) {
+  if (type == ZERO_FP32)
+    Elem<float>::store8(static_cast<float*>(p) + i, v);
+  else if (type == ZERO_BF16)
+    Elem<__nv_bfloat16>::store8(static_cast<__nv_bfloat16*>(p) + i, v);
+  else
+    Elem<__half>::store8(static_cast<__half*>(p) + i, v);
+}
+
+__host__ __device__ __forceinline__ int type_bytes(int type) { return type == ZERO_FP32 ? 4 : 2; }
+
+// Sum over the warp, the same value in every lane (a fixed butterfly).
+template <class V>
+__device__ __forceinline__ V warp_all_sum(V v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// Host checks shared by the operators' entry points.
+inline bool known_type(int t) { return t == ZERO_FP16 || t == ZERO_BF16 || t == ZERO_FP32; }
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace zero

@@ -1,0 +1,610 @@
+"""Operators of a training step around the sharded optimizer: gradient norm
+and clipping over many tensors, the block join, the expert permutation.
+
+The ``zero_*`` functions bind the C calls of include/zero.h under their own
+names (argument checks and marshalling only; the current CUDA stream unless
+``stream`` is given; no fallback).  ``GradNorm`` and ``ClipGradNorm`` are the
+prepared forms for gradients whose buffers stay in place from step to step.
+``block_join``, ``expert_dispatch`` and ``expert_combine`` are the same calls
+with autograd.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+from typing import Optional
+
+import torch
+
+from .zero import _addr, _check, _stream, lib
+
+ZERO_FP32 = 2
+_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: ZERO_FP32}
+_NORMS = {"l2": 0, "inf": 1}
+_KINDS = {"rms": 0, "layer": 1}
+GATE_NONE, GATE_CHANNEL, GATE_ROW, GATE_FULL = range(4)
+
+
+def _type(t, what: str) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: expected float16, bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+def _choice(table, value, what: str) -> int:
+    if value not in table:
+        raise ValueError(f"{what} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def _on(t, what: str, device=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: tensor must be on a CUDA device")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    return t
+
+
+def _current(t, what: str):
+    """The tensor's device, which has to be the current one (launches go there)."""
+    _on(t, what)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _keep_for(stream, *tensors):
+    """Tensors allocated here and used on another stream than the current one."""
+    if stream is None:
+        return
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def _result(t, what: str, shape, dtype, device):
+    """A caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _on(t, what, device)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+# ----------------------------------------------------------------------------
+# gradient norm and clipping
+
+
+class GradTensorC(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
+
+
+class NormResult(ctypes.Structure):
+    """Host image of zero_norm_result (32 bytes)."""
+    _fields_ = [("norm", ctypes.c_double), ("norm32", ctypes.c_float), ("coef", ctypes.c_float),
+                ("nonfinite", ctypes.c_int32), ("pad_", ctypes.c_int32 * 3)]
+
+
+NORM_RESULT_BYTES = ctypes.sizeof(NormResult)
+
+
+def read_norm_result(result) -> NormResult:
+    """The record on the host (this synchronises with the current stream)."""
+    return NormResult.from_buffer_copy(bytes(result.cpu().numpy().tobytes()))
+
+
+def _dense(t) -> bool:
+    """Whether the tensor's elements fill one run of memory, in any order."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def _grad_tensor(t, what: str):
+    if not isinstance(t, torch.Tensor) or t.layout != torch.strided:
+        raise TypeError(f"{what}: expected a dense torch.Tensor")
+    if t.numel() and not t.is_cuda and not t.is_pinned():
+        raise ValueError(f"{what}: tensor must be on a CUDA device or in pinned host memory")
+    if not _dense(t):
+        raise ValueError(f"{what}: the elements must fill one run of memory")
+    return _type(t, what)
+
+
+def _check_disjoint(entries):
+    """No output overlaps another tensor (entries: lo, hi, written)."""
+    end = {False: 0, True: 0}
+    for lo, hi, written in sorted(entries):
+        if lo < end[True] or (written and lo < end[False]):
+            raise ValueError("out: a tensor to be written overlaps another one")
+        end[written] = max(end[written], hi)
+
+
+class GradNorm:
+    """A prepared zero_grad_norm over `grads` (None entries are left out):
+    the list is checked and marshalled once, each call takes the norm of what
+    the tensors hold then.  Returns the norm as a float32 tensor without
+    dimensions, a view of `result`, which the next call overwrites."""
+
+    def __init__(self, grads, kind: str = "l2"):
+        self._prepare([g for g in grads if g is not None], None, kind)
+
+    def _prepare(self, grads, out, kind):
+        self.kind = _choice(_NORMS, kind, "kind")
+        self._keep = (grads, out)
+        self._list = (GradTensorC * max(1, len(grads)))()
+        self.n = len(grads)
+        device = None
+        spans = []
+        for k, g in enumerate(grads):
+            what = f"grads[{k}]"
+            e = self._list[k]
+            e.src_dtype, e.numel = _grad_tensor(g, what), g.numel()
+            e.src = g.data_ptr() if g.numel() else None
+            if g.is_cuda:
+                device = device or _current(g, what)
+                if g.device != device:
+                    raise ValueError(f"{what}: on {g.device}, expected {device}")
+            if out is None:
+                continue
+            d = out[k]
+            if d is not g:
+                _grad_tensor(d, f"out[{k}]")
+                if d.shape != g.shape or (d.stride() != g.stride() and not
+                                          (d.is_contiguous() and g.is_contiguous())):
+                    raise ValueError(f"out[{k}]: shape and order must be those of grads[{k}]")
+                if d.is_cuda and device is not None and d.device != device:
+                    raise ValueError(f"out[{k}]: on {d.device}, expected {device}")
+            e.dst_dtype = _type(d, f"out[{k}]")
+            e.dst = d.data_ptr() if d.numel() else None
+            if g.numel():
+                spans.append((e.dst, e.dst + d.numel() * d.element_size(), True))
+                if e.dst != e.src:
+                    spans.append((e.src, e.src + g.numel() * g.element_size(), False))
+        _check_disjoint(spans)
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        need = ctypes.c_int64()
+        _check(lib().zero_grad_norm_workspace_bytes(self._list, self.n, ctypes.byref(need)))
+        self.result = torch.empty(NORM_RESULT_BYTES, dtype=torch.uint8, device=device)
+        self._workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+        self._norm = self.result[8:12].view(torch.float32)[0]
+        self._args = (self.result.data_ptr(), self._workspace.data_ptr(), need.value)
+
+    def __call__(self, stream=None):
+        _check(lib().zero_grad_norm(self._list, self.n, self.kind, *self._args, _stream(stream)))
+        return self._norm
+
+    def read(self) -> NormResult:
+        return read_norm_result(self.result)
+
+
+class ClipGradNorm(GradNorm):
+    """A prepared zero_clip_grad_norm: the norm of `grads`, and each gradient
+    times min(1, max_norm / (norm + 1e-6)) into `out` (None: in place).
+    `out` may have other types, for instance the views of a 16-bit replica
+    that fp32 gradients go to.  `max_norm` may be changed between calls."""
+
+    def __init__(self, grads, max_norm: float, kind: str = "l2", out=None):
+        grads = list(grads)
+        self.max_norm = float(max_norm)
+        if out is None:
+            grads = out = [g for g in grads if g is not None]
+        else:
+            out = list(out)
+            if len(out) != len(grads):
+                raise ValueError(f"out: expected {len(grads)} entries, got {len(out)}")
+            pairs = [(g, d) for g, d in zip(grads, out) if g is not None]
+            grads, out = [g for g, _ in pairs], [d for _, d in pairs]
+        self._prepare(grads, out, kind)
+
+    def __call__(self, stream=None):
+        _check(lib().zero_clip_grad_norm(self._list, self.n, self.kind, self.max_norm,
+                                         *self._args, _stream(stream)))
+        return self._norm
+
+
+def zero_grad_norm(grads, kind: str = "l2", stream=None):
+    """Norm of all gradients as one vector (see zero.h); a float32 tensor."""
+    call = GradNorm(grads, kind)
+    _keep_for(stream, call.result, call._workspace)
+    return call(stream)
+
+
+def zero_clip_grad_norm(grads, max_norm: float, kind: str = "l2", out=None, stream=None):
+    """Norm and clipping (see zero.h); returns the norm before clipping."""
+    call = ClipGradNorm(grads, max_norm, kind, out)
+    _keep_for(stream, call.result, call._workspace)
+    return call(stream)
+
+
+# ----------------------------------------------------------------------------
+# block join
+
+
+class JoinDescC(ctypes.Structure):
+    _fields_ = ([("rows", ctypes.c_int64), ("hidden", ctypes.c_int64)]
+                + [(k, ctypes.c_int32) for k in ("act_dtype", "res_dtype", "param_dtype",
+                                                 "gate_dtype", "kind", "gate_kind")]
+                + [("eps", ctypes.c_double), ("scale", ctypes.c_double)]
+                + [(k, ctypes.c_int64) for k in ("x_stride", "b_stride", "gate_stride",
+                                                 "do_stride", "dn_stride")])
+
+
+class JoinInputsC(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("x", "b", "gate", "w_post", "bias_post", "w_pre",
+                                               "bias_pre")]
+
+
+class JoinGradsC(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dx", "db", "dgate", "dw_post", "dbias_post",
+                                               "dw_pre", "dbias_pre")]
+
+
+_PARAMS = ("w_post", "bias_post", "w_pre", "bias_pre")
+
+
+def _row_stride(t, what: str, shape, device) -> int:
+    """Elements between rows of a tensor [..., hidden] whose rows are
+    contiguous and evenly spaced."""
+    _on(t, what, device)
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    hidden = shape[-1]
+    if t.is_contiguous():
+        return hidden
+    if t.stride(-1) == 1 or hidden == 1:
+        if t.dim() == 2:
+            return t.stride(0)
+        try:
+            return t.view(-1, hidden).stride(0)
+        except RuntimeError:
+            pass
+    raise ValueError(f"{what}: rows must be contiguous and evenly spaced (use .contiguous())")
+
+
+def _join_args(x, b, gate, params, kind, scale, eps, act):
+    """(desc, inputs, device, act dtype) of a join's arguments."""
+    device = _current(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x: expected [..., hidden]")
+    shape = x.shape
+    d, p = JoinDescC(), JoinInputsC()
+    hidden = shape[-1]
+    d.hidden = hidden
+    d.rows = x.numel() // hidden if hidden else 0
+    d.res_dtype = _type(x, "x")
+    d.x_stride = _row_stride(x, "x", shape, device)
+    p.x = x.data_ptr()
+    if b is not None:
+        act = b.dtype
+        d.b_stride = _row_stride(b, "b", shape, device)
+        p.b = b.data_ptr()
+    elif act is None:
+        w = params[2]
+        act = w.dtype if x.dtype == torch.float32 and w is not None else x.dtype
+    code = _TYPES.get(act)
+    if code is None:
+        raise TypeError(f"b: expected float16, bfloat16 or float32, got {act}")
+    d.act_dtype = d.param_dtype = d.gate_dtype = code
+    first = None
+    for name, t in zip(_PARAMS, params):
+        if t is None:
+            continue
+        _on(t, name, device)
+        if t.dim() != 1 or t.shape[0] != hidden or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous vector of {hidden}")
+        if first is None:
+            first = t.dtype
+            d.param_dtype = _type(t, name)
+        elif t.dtype != first:
+            raise TypeError(f"{name}: {t.dtype}, but another parameter is {first}")
+        setattr(p, name, t.data_ptr())
+    if gate is not None:
+        _on(gate, "gate", device)
+        d.gate_dtype = _type(gate, "gate")
+        if gate.dim() == 1 and gate.shape[0] == hidden and x.dim() != 1:
+            if not gate.is_contiguous():
+                raise ValueError("gate: expected a contiguous vector")
+            d.gate_kind = GATE_CHANNEL
+        elif gate.shape == shape:
+            d.gate_kind = GATE_FULL
+            d.gate_stride = _row_stride(gate, "gate", shape, device)
+        elif gate.shape == shape[:-1] + (1,):
+            d.gate_kind = GATE_ROW
+            d.gate_stride = _row_stride(gate, "gate", gate.shape, device)
+        else:
+            raise ValueError(f"gate: shape {tuple(gate.shape)}, expected ({hidden},), "
+                             f"{tuple(shape[:-1]) + (1,)} or {tuple(shape)}")
+        p.gate = gate.data_ptr()
+    d.kind = _choice(_KINDS, kind, "kind")
+    d.eps, d.scale = eps, scale
+    return d, p, device, act
+
+
+def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_pre=None,
+                    gate=None, kind: str = "rms", scale: float = 1.0, eps: float = 1e-6, o=None,
+                    n=None, want_o: bool = True, want_stats: bool = False, stream=None):
+    """o = x + scale * gate * norm(b; w_post) and n = norm(o; w_pre) (see
+    zero.h): (o, n, stats).  Without w_post there is no norm before the gate,
+    without w_pre no n (None); b None takes the norm of x alone, and o is x.
+    x, b, gate: [..., hidden]; the gate also [hidden] or [..., 1].  stats is
+    what the backward call takes (None unless want_stats)."""
+    d, p, device, act = _join_args(x, b, gate, (w_post, bias_post, w_pre, bias_pre), kind, scale,
+                                   eps, None if n is None else n.dtype)
+    kept_o, kept_n = o, n
+    if b is None and o is None:
+        want_o = False
+    o = _result(o, "o", x.shape, x.dtype, device) if want_o else None
+    if n is not None and w_pre is None:
+        raise ValueError("n: needs w_pre")
+    n = _result(n, "n", x.shape, act, device) if w_pre is not None else None
+    stats = torch.empty(d.rows, 4, dtype=torch.float32, device=device) if want_stats else None
+    if stream is not None:
+        _keep_for(stream, o if kept_o is None else None, n if kept_n is None else None, stats)
+    _check(lib().zero_block_join(ctypes.byref(d), ctypes.byref(p),
+                                 None if o is None else o.data_ptr(),
+                                 None if n is None else n.data_ptr(),
+                                 None if stats is None else stats.data_ptr(), _stream(stream)))
+    return x if b is None and o is None else o, n, stats
+
+
+def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=None, w_pre=None,
+                             bias_pre=None, gate=None, kind: str = "rms", scale: float = 1.0,
+                             eps: float = 1e-6, want=None, stream=None):
+    """Gradients of zero_block_join's inputs from those of o and n (either
+    may be None) and its stats: a dict with dx, db, dgate, dw_post,
+    dbias_post, dw_pre and dbias_pre, None for what has no input or is not in
+    `want` (a set of those names; None: all)."""
+    params = (w_post, bias_post, w_pre, bias_pre)
+    act = None if d_n is None else d_n.dtype
+    d, p, device, act = _join_args(x, b, gate, params, kind, scale, eps, act)
+    if d_o is not None:
+        if d_o.dtype != x.dtype:
+            raise TypeError(f"d_o: expected {x.dtype}, got {d_o.dtype}")
+        d.do_stride = _row_stride(d_o, "d_o", x.shape, device)
+    if d_n is not None:
+        if d_n.dtype != act:
+            raise TypeError(f"d_n: expected {act}, got {d_n.dtype}")
+        d.dn_stride = _row_stride(d_n, "d_n", x.shape, device)
+    if stats is not None:
+        _result(stats, "stats", (d.rows, 4), torch.float32, device)
+    out = {"dx": x, "db": b, "dgate": gate, "dw_post": w_post, "dbias_post": bias_post,
+           "dw_pre": w_pre, "dbias_pre": bias_pre}
+    g = JoinGradsC()
+    sums = d.gate_kind == GATE_CHANNEL
+    for name, like in out.items():
+        if like is None or (want is not None and name not in want):
+            out[name] = None
+            continue
+        if d_n is None and name in ("dw_pre", "dbias_pre"):
+            out[name] = t = torch.zeros_like(like)  # n was not used
+            _keep_for(stream, t)
+            continue
+        out[name] = t = torch.empty(like.shape, dtype=like.dtype, device=device)
+        setattr(g, name, t.data_ptr())
+        sums = sums or like.dim() == 1
+        _keep_for(stream, t)
+    need = ctypes.c_int64()
+    ws = None
+    if sums:
+        _check(lib().zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
+        ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+        _keep_for(stream, ws)
+    if any(getattr(g, name) for name in out):
+        _check(lib().zero_block_join_backward(
+            ctypes.byref(d), ctypes.byref(p), None if d_o is None else d_o.data_ptr(),
+            None if d_n is None else d_n.data_ptr(), None if stats is None else stats.data_ptr(),
+            ctypes.byref(g), None if ws is None else ws.data_ptr(), need.value, _stream(stream)))
+    return out
+
+
+def _even_rows(t):
+    """A gradient as the calls take it (autograd may hand out expanded ones)."""
+    if t is None or t.is_contiguous() or (t.dim() == 2 and t.stride(1) == 1
+                                          and t.stride(0) >= t.shape[1]):
+        return t
+    return t.contiguous()
+
+
+class _BlockJoin(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, b, gate, w_post, bias_post, w_pre, bias_pre, kind, scale, eps):
+        ctx.set_materialize_grads(False)
+        ctx.how = dict(kind=kind, scale=scale, eps=eps)
+        o, n, stats = zero_block_join(x, b, w_post=w_post, bias_post=bias_post, w_pre=w_pre,
+                                      bias_pre=bias_pre, gate=gate, want_stats=True, **ctx.how)
+        ctx.save_for_backward(x, b, gate, w_post, bias_post, w_pre, bias_pre, stats)
+        if o is x:
+            o = x.view_as(x)
+        return o, n
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_o, d_n):
+        x, b, gate, w_post, bias_post, w_pre, bias_pre, stats = ctx.saved_tensors
+        names = ("dx", "db", "dgate", "dw_post", "dbias_post", "dw_pre", "dbias_pre")
+        want = {k for k, needed in zip(names, ctx.needs_input_grad) if needed}
+        if d_o is None and d_n is None:
+            return (None,) * 10
+        g = zero_block_join_backward(x, b, _even_rows(d_o), _even_rows(d_n), stats, w_post=w_post,
+                                     bias_post=bias_post, w_pre=w_pre, bias_pre=bias_pre,
+                                     gate=gate, want=want, **ctx.how)
+        return tuple(g[k] for k in names) + (None, None, None)
+
+
+def block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_pre=None, gate=None,
+               kind: str = "rms", scale: float = 1.0, eps: float = 1e-6):
+    """zero_block_join with autograd: (o, n), n None without w_pre."""
+    return _BlockJoin.apply(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind, scale, eps)
+
+
+# ----------------------------------------------------------------------------
+# expert permutation
+
+
+@dataclasses.dataclass
+class ExpertOrder:
+    """What zero_expert_sort leaves on the device: offsets [n_experts + 1],
+    rows [tokens, topk] (-1: dropped), pairs [tokens * topk] (-1: past the
+    end), all int32."""
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    pairs: torch.Tensor
+    n_experts: int
+    tokens: int
+    topk: int
+
+
+def zero_expert_sort(ids, n_experts: int, stream=None) -> ExpertOrder:
+    """Rows of every token's choices in expert order (see zero.h).  ids:
+    [tokens, topk] int32 or int64; a choice outside [0, n_experts) is
+    dropped."""
+    device = _current(ids, "ids")
+    if ids.dim() != 2 or not ids.is_contiguous():
+        raise ValueError("ids: expected a contiguous [tokens, topk] tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids: expected int32 or int64, got {ids.dtype}")
+    tokens, topk = ids.shape
+    if topk < 1:
+        raise ValueError("ids: topk must be at least 1")
+    offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=device)
+    rows = torch.empty(tokens, topk, dtype=torch.int32, device=device)
+    pairs = torch.empty(tokens * topk, dtype=torch.int32, device=device)
+    _keep_for(stream, offsets, rows, pairs)
+    _check(lib().zero_expert_sort(ids.data_ptr() or None, ids.element_size(), tokens, topk,
+                                  n_experts, offsets.data_ptr(), rows.data_ptr() or None,
+                                  pairs.data_ptr() or None, _stream(stream)))
+    return ExpertOrder(offsets, rows, pairs, n_experts, tokens, topk)
+
+
+def _sorted_rows(t, what: str, order: ExpertOrder):
+    _current(t, what)
+    _on(order.rows, "order", t.device)
+    if t.dim() != 2 or t.shape[0] != order.tokens * order.topk or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous [{order.tokens * order.topk}, hidden] "
+                         "tensor")
+    return _type(t, what)
+
+
+def _token_rows(t, what: str, order: ExpertOrder, hidden=None):
+    """(type, row stride) of a tensor [tokens, hidden]."""
+    _current(t, what)
+    _on(order.rows, "order", t.device)
+    if t.dim() != 2 or t.shape[0] != order.tokens or (hidden is not None and t.shape[1] != hidden):
+        raise ValueError(f"{what}: expected [{order.tokens}, {hidden or 'hidden'}], got "
+                         f"{tuple(t.shape)}")
+    return _type(t, what), _row_stride(t, what, t.shape, t.device)
+
+
+def _expert_weights(weights, order: ExpertOrder, device):
+    _on(weights, "weights", device)
+    if tuple(weights.shape) != (order.tokens, order.topk) or not weights.is_contiguous():
+        raise ValueError(f"weights: expected a contiguous [{order.tokens}, {order.topk}] tensor")
+    return _type(weights, "weights")
+
+
+def zero_expert_dispatch(x, order: ExpertOrder, out=None, stream=None):
+    """Tokens copied to their rows in expert order, [tokens * topk, hidden];
+    the rows past the last kept choice are zero."""
+    code, stride = _token_rows(x, "x", order)
+    hidden = x.shape[1]
+    xs = _result(out, "out", (order.tokens * order.topk, hidden), x.dtype, x.device)
+    _keep_for(stream, xs if out is None else None)
+    _check(lib().zero_expert_dispatch(x.data_ptr(), stride, code, order.tokens, order.topk, hidden,
+                                      order.offsets.data_ptr(), order.n_experts,
+                                      order.rows.data_ptr(), xs.data_ptr(), _stream(stream)))
+    return xs
+
+
+def zero_expert_dispatch_backward(dxs, order: ExpertOrder, out=None, stream=None):
+    """Each token's gradient: the sum of its rows'."""
+    code = _sorted_rows(dxs, "dxs", order)
+    hidden = dxs.shape[1]
+    dx = _result(out, "out", (order.tokens, hidden), dxs.dtype, dxs.device)
+    _keep_for(stream, dx if out is None else None)
+    _check(lib().zero_expert_dispatch_backward(dxs.data_ptr(), code, order.tokens, order.topk,
+                                               hidden, order.rows.data_ptr(), dx.data_ptr(),
+                                               _stream(stream)))
+    return dx
+
+
+def zero_expert_combine(ys, weights, order: ExpertOrder, out=None, stream=None):
+    """Each token's weighted sum of its rows; zero when all its choices were
+    dropped."""
+    code = _sorted_rows(ys, "ys", order)
+    hidden = ys.shape[1]
+    wcode = _expert_weights(weights, order, ys.device)
+    y = _result(out, "out", (order.tokens, hidden), ys.dtype, ys.device)
+    _keep_for(stream, y if out is None else None)
+    _check(lib().zero_expert_combine(ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
+                                     order.topk, hidden, order.rows.data_ptr(), y.data_ptr(),
+                                     _stream(stream)))
+    return y
+
+
+def zero_expert_combine_backward(dy, ys, weights, order: ExpertOrder, want_weights: bool = True,
+                                 stream=None):
+    """(dys, dweights) of zero_expert_combine; dweights None unless wanted."""
+    code = _sorted_rows(ys, "ys", order)
+    hidden = ys.shape[1]
+    dcode, stride = _token_rows(dy, "dy", order, hidden)
+    if dcode != code:
+        raise TypeError(f"dy: expected {ys.dtype}, got {dy.dtype}")
+    wcode = _expert_weights(weights, order, ys.device)
+    dys = torch.empty_like(ys)
+    dweights = torch.empty_like(weights) if want_weights else None
+    _keep_for(stream, dys, dweights)
+    _check(lib().zero_expert_combine_backward(
+        dy.data_ptr(), stride, ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
+        order.topk, hidden, order.offsets.data_ptr(), order.n_experts, order.rows.data_ptr(),
+        dys.data_ptr(), None if dweights is None else dweights.data_ptr(), _stream(stream)))
+    return dys, dweights
+
+
+class _ExpertDispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, order):
+        ctx.order = order
+        return zero_expert_dispatch(x, order)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dxs):
+        return zero_expert_dispatch_backward(dxs.contiguous(), ctx.order), None
+
+
+class _ExpertCombine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ys, weights, order):
+        ctx.order = order
+        ctx.save_for_backward(ys, weights)
+        return zero_expert_combine(ys, weights, order)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        ys, weights = ctx.saved_tensors
+        dys, dw = zero_expert_combine_backward(_even_rows(dy), ys, weights, ctx.order,
+                                               want_weights=ctx.needs_input_grad[1])
+        return dys if ctx.needs_input_grad[0] else None, dw, None
+
+
+def expert_dispatch(x, order: ExpertOrder):
+    """zero_expert_dispatch with autograd."""
+    return _ExpertDispatch.apply(x, order)
+
+
+def expert_combine(ys, weights, order: ExpertOrder):
+    """zero_expert_combine with autograd (of ys and of the weights)."""
+    return _ExpertCombine.apply(ys, weights, order)

@@ -112,6 +112,20 @@ def lib():
                 "zero_step_amp_noalloc": [vp, vpp, ctypes.c_int, ctypes.c_int, vpp, vpp, vpp,
                                           vpp, vp, vpp, hp, ctypes.POINTER(AmpConfigC), vp, u64,
                                           i64, vp],
+                "zero_grad_norm_workspace_bytes": [vp, i32, i64p],
+                "zero_grad_norm": [vp, i32, i32, vp, vp, i64, vp],
+                "zero_clip_grad_norm": [vp, i32, i32, ctypes.c_double, vp, vp, i64, vp],
+                "zero_block_join": [vp, vp, vp, vp, vp, vp],
+                "zero_block_join_workspace_bytes": [vp, i64p],
+                "zero_block_join_backward": [vp, vp, vp, vp, vp, vp, vp, i64, vp],
+                "zero_expert_sort": [vp, i32, i64, i32, i32, vp, vp, vp, vp],
+                "zero_expert_dispatch": [vp, i64, ctypes.c_int, i64, i32, i64, vp, i32, vp, vp,
+                                         vp],
+                "zero_expert_dispatch_backward": [vp, ctypes.c_int, i64, i32, i64, vp, vp, vp],
+                "zero_expert_combine": [vp, ctypes.c_int, vp, ctypes.c_int, i64, i32, i64, vp, vp,
+                                        vp],
+                "zero_expert_combine_backward": [vp, i64, vp, ctypes.c_int, vp, ctypes.c_int, i64,
+                                                 i32, i64, vp, i32, vp, vp, vp, vp],
                 "zero_zero3_pass": [vp, ctypes.POINTER(_LayerC), i32, vpp, i32, ctypes.c_int,
                                     ctypes.c_int, hp, i64, vp, vp],
             }
