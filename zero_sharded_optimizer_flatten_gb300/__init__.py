@@ -25,9 +25,10 @@ from .zero import (AMP_STATE_BYTES, ZERO_BF16, ZERO_FP16, ZERO_PART_FLAT,  # noq
 
 _TRAIN_OPS = ("ClipGradNorm", "ExpertOrder", "GradNorm", "NormResult", "block_join",
               "expert_combine", "expert_dispatch", "read_norm_result", "zero_block_join",
-              "zero_block_join_backward", "zero_clip_grad_norm", "zero_expert_combine",
-              "zero_expert_combine_backward", "zero_expert_dispatch",
-              "zero_expert_dispatch_backward", "zero_expert_sort", "zero_grad_norm")
+              "zero_block_join_backward", "zero_block_join_workspace_bytes",
+              "zero_clip_grad_norm", "zero_expert_combine", "zero_expert_combine_backward",
+              "zero_expert_dispatch", "zero_expert_dispatch_backward", "zero_expert_sort",
+              "zero_grad_norm", "zero_grad_norm_workspace_bytes")
 
 
 def __getattr__(name):

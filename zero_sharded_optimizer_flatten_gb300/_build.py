@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libzero.so")
 
 SOURCES = ["zero_plan.cpp", "zero_capi.cpp", "zero_launch.cu", "zero_kernels_fp16.cu",
            "zero_kernels_bf16.cu", "zero_noalloc.cu", "zero_cpu_adam.cpp", "zero_gradnorm.cu",
-           "zero_join.cu", "zero_experts.cu"]
+           "zero_join.cu", "zero_join_ff.cu", "zero_join_hh.cu", "zero_join_hf.cu",
+           "zero_join_bb.cu", "zero_join_bf.cu", "zero_experts.cu"]
 # extra host-compiler flags per source: the host AdamW loop is vectorised at
 # -O3; -fno-math-errno lets sqrtf be the plain instruction (results unchanged)
 EXTRA = {"zero_cpu_adam.cpp": ["-Xcompiler", "-O3,-fno-math-errno"]}

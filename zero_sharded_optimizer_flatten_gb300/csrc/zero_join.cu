@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_join_backward_any(const __grid_
   __shared__ float part[3 * kAnyThreads / 32];
   const int64_t H = a.d.hidden;
   float* mine = a.partial + static_cast<int64_t>(blockIdx.x) * a.n_sums * H;
+  const bool by_row = a.d.gate_kind == ZERO_GATE_ROW || a.d.gate_kind == ZERO_GATE_FULL;
   for (int64_t r = blockIdx.x; r < a.d.rows; r += gridDim.x) {
     const bool first = r == blockIdx.x;
     Row<A, R> row(a, r);
@@ -197,16 +198,14 @@ __global__ void __launch_bounds__(kAnyThreads) k_join_backward_any(const __grid_
       };
       if (d_n) {
         const float dn = Elem<A>::widen(d_n[c]);
-        add(kSumWPre, dn * row.o_hat(c));
-        add(kSumBiasPre, dn);
+        add(kSumP, dn * row.o_hat(c));
+        add(kSumQ, dn);
       }
       if (a.in.b) {
         const float du = row.gate(c) * go;
-        if (a.in.w_post) {
-          add(kSumWPost, du * row.b_hat(c));
-          add(kSumBiasPost, du);
-        }
-        if (a.d.gate_kind == ZERO_GATE_CHANNEL) add(kSumGate, a.scale * go * row.u(c));
+        const float y = by_row ? du : go;
+        add(kSumS, y * (a.in.w_post ? row.b_hat(c) : row.block(c)));
+        add(kSumB, y);
         if (a.d.gate_kind == ZERO_GATE_FULL && a.dgate)
           store_any(a.dgate, r * H + c, a.d.gate_dtype, a.scale * go * row.u(c));
         if (a.db) {
@@ -225,28 +224,60 @@ __global__ void __launch_bounds__(kAnyThreads) k_join_backward_any(const __grid_
 // of them added side by side and then joined, so the order is fixed.
 constexpr int kSumRows = 8;
 
-__global__ void __launch_bounds__(32 * kSumRows) k_join_sums(const __grid_constant__ JoinSumArgs a) {
-  __shared__ float part[kSumRows][33];
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-  const int slot = blockIdx.y;
-  float s = 0.f;
-  if (c < a.hidden)
-    for (int w = threadIdx.y; w < a.workers; w += kSumRows)
-      s += a.partial[(static_cast<int64_t>(w) * a.n_sums + slot) * a.hidden + c];
-  part[threadIdx.y][threadIdx.x] = s;
+__global__ void __launch_bounds__(32 * kSumRows) k_join_sums(const __grid_constant__ JoinSumArgs g) {
+  __shared__ float part[kSumRows][kJoinSums][33];
+  const JoinArgs& a = g.a;
+  const int64_t H = a.d.hidden, c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+  float s[kJoinSums];
+#pragma unroll
+  for (int k = 0; k < kJoinSums; ++k) {
+    s[k] = 0.f;
+    if (a.slot[k] < 0) continue;
+    const float* p = a.partial + a.slot[k] * H + c;
+    if (c < H)
+      for (int w = threadIdx.y; w < g.workers; w += kSumRows) s[k] += p[static_cast<int64_t>(w) * a.n_sums * H];
+    part[threadIdx.y][k][threadIdx.x] = s[k];
+  }
   __syncthreads();
-  if (threadIdx.y == 0 && c < a.hidden) {
-    for (int k = 1; k < kSumRows; ++k) s += part[k][threadIdx.x];
-    store_any(a.out[slot], c, a.type[slot], s);
+  if (threadIdx.y != 0 || c >= H) return;
+#pragma unroll
+  for (int k = 0; k < kJoinSums; ++k)
+    if (a.slot[k] >= 0)
+      for (int y = 1; y < kSumRows; ++y) s[k] += part[y][k][threadIdx.x];
+  const int pt = a.d.param_dtype;
+  if (g.dw_pre) store_any(g.dw_pre, c, pt, s[kSumP]);
+  if (g.dbias_pre) store_any(g.dbias_pre, c, pt, s[kSumQ]);
+  float gate = a.scale;
+  // row and full gates are in the sums already, with the scale
+  if (a.d.gate_kind == ZERO_GATE_ROW || a.d.gate_kind == ZERO_GATE_FULL) gate = 1.f;
+  if (a.d.gate_kind == ZERO_GATE_CHANNEL) gate *= load_any(a.in.gate, c, a.d.gate_dtype);
+  if (g.dw_post) store_any(g.dw_post, c, pt, gate * s[kSumS]);
+  if (g.dbias_post) store_any(g.dbias_post, c, pt, gate * s[kSumB]);
+  if (g.dgate) {
+    float v = s[kSumS];
+    if (a.in.w_post) v *= load_any(a.in.w_post, c, pt);
+    if (a.in.bias_post) v = fmaf(load_any(a.in.bias_post, c, pt), s[kSumB], v);
+    store_any(g.dgate, c, a.d.gate_dtype, a.scale * v);
   }
 }
 
+// CTAs that leave partials, at most.
+int join_workers(const zero_join_desc& d) {
+  int64_t most = kAnyWorkers;
+  if (d.hidden <= kJoinRowMost) {
+    const int64_t threads = (d.hidden + 255) / 256 * 32;
+    most = kSMs * std::max<int64_t>(1, std::min<int64_t>(16, kJoinThreadsBackward / threads));
+  }
+  return static_cast<int>(std::min(d.rows, most));
+}
+
 template <class A, class R>
-int launch_any(const JoinArgs& a, int workers, bool backward, cudaStream_t s) {
+int launch_any(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
   void* args[] = {const_cast<JoinArgs*>(&a)};
   const void* fn = backward ? reinterpret_cast<const void*>(&k_join_backward_any<A, R>)
                             : reinterpret_cast<const void*>(&k_join_any<A, R>);
-  const int grid = static_cast<int>(std::min<int64_t>(a.d.rows, backward ? workers : 16 * kSMs));
+  const int grid = static_cast<int>(std::min<int64_t>(a.d.rows, backward ? join_workers(a.d) : 16 * kSMs));
+  *workers = grid;
   return static_cast<int>(cudaLaunchKernel(fn, dim3(grid), dim3(kAnyThreads), args, 0, s));
 }
 
@@ -263,17 +294,13 @@ int by_types(const zero_join_desc& d, F f) {
 
 }  // namespace
 
-int join_workers(const JoinArgs& a) {
-  return static_cast<int>(std::min<int64_t>(a.d.rows, kAnyWorkers));
-}
-
-int launch_join(const JoinArgs& a, cudaStream_t s) {
-  return by_types(a.d, [&](auto act, auto res) { return launch_any<decltype(act), decltype(res)>(a, 0, false, s); });
-}
-
-int launch_join_backward(const JoinArgs& a, int workers, cudaStream_t s) {
-  return by_types(a.d,
-                  [&](auto act, auto res) { return launch_any<decltype(act), decltype(res)>(a, workers, true, s); });
+static int launch_join(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
+  return by_types(a.d, [&](auto act, auto res) {
+    using A = decltype(act);
+    using R = decltype(res);
+    const int e = launch_join_rows<A, R>(a, backward, workers, s);
+    return e == -1 ? launch_any<A, R>(a, backward, workers, s) : e;
+  });
 }
 
 namespace {
@@ -401,7 +428,8 @@ extern "C" zero_status zero_block_join(const zero_join_desc* desc, const zero_jo
   a.n = n;
   a.stats = reinterpret_cast<float4*>(stats);
   if (!n && !stats) a.in.w_pre = nullptr;  // its statistics go nowhere
-  return launched(fn, launch_join(a, static_cast<cudaStream_t>(stream)));
+  int workers = 0;
+  return launched(fn, launch_join(a, false, &workers, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" zero_status zero_block_join_workspace_bytes(const zero_join_desc* desc, int64_t* bytes) {
@@ -409,9 +437,7 @@ extern "C" zero_status zero_block_join_workspace_bytes(const zero_join_desc* des
   clear_error();
   if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
   JOIN_TRY(check_desc(fn, desc));
-  JoinArgs a = {};
-  a.d = *desc;
-  *bytes = std::max<int64_t>(16, static_cast<int64_t>(join_workers(a)) * kJoinSums * desc->hidden * 4);
+  *bytes = std::max<int64_t>(16, static_cast<int64_t>(join_workers(*desc)) * kJoinSums * desc->hidden * 4);
   return ZERO_OK;
 }
 
@@ -448,41 +474,37 @@ extern "C" zero_status zero_block_join_backward(const zero_join_desc* desc, cons
   a.stats = reinterpret_cast<float4*>(const_cast<float*>(stats));
   a.dx = grads->dx;
   a.db = grads->db;
-  JoinSumArgs sums = {};
+  const bool channel = d.gate_kind == ZERO_GATE_CHANNEL;
   struct Want {
-    int which;
     const char* name;
     void* out;
     const void* of;
     int type;
+    bool pre, bias;
   };
-  const Want wants[kJoinSums] = {
-      {kSumWPre, "dw_pre", grads->dw_pre, in.w_pre, d.param_dtype},
-      {kSumBiasPre, "dbias_pre", grads->dbias_pre, in.w_pre, d.param_dtype},
-      {kSumWPost, "dw_post", grads->dw_post, in.w_post, d.param_dtype},
-      {kSumBiasPost, "dbias_post", grads->dbias_post, in.w_post, d.param_dtype},
-      {kSumGate, "dgate", d.gate_kind == ZERO_GATE_CHANNEL ? grads->dgate : nullptr, in.gate, d.gate_dtype}};
+  const Want wants[] = {{"dw_pre", grads->dw_pre, in.w_pre, d.param_dtype, true, false},
+                        {"dbias_pre", grads->dbias_pre, in.w_pre, d.param_dtype, true, true},
+                        {"dw_post", grads->dw_post, in.w_post, d.param_dtype, false, false},
+                        {"dbias_post", grads->dbias_post, in.w_post, d.param_dtype, false, true}};
   for (const Want& w : wants) {
     if (!w.out) continue;
     JOIN_TRY(check_array(fn, w.name, w.out, w.type, false));
     if (rows && !w.of) return fail(ZERO_ERR_INVALID, "%s: %s needs its parameter", fn, w.name);
-    if (d.kind == ZERO_JOIN_RMS && (w.which == kSumBiasPre || w.which == kSumBiasPost))
-      return fail(ZERO_ERR_INVALID, "%s: ZERO_JOIN_RMS has no biases", fn);
-    if (rows && !d_n && (w.which == kSumWPre || w.which == kSumBiasPre))
-      return fail(ZERO_ERR_INVALID, "%s: %s needs d_n", fn, w.name);
-    a.slot[w.which] = a.n_sums;
-    sums.out[a.n_sums] = w.out;
-    sums.type[a.n_sums] = w.type;
-    ++a.n_sums;
+    if (d.kind == ZERO_JOIN_RMS && w.bias) return fail(ZERO_ERR_INVALID, "%s: ZERO_JOIN_RMS has no biases", fn);
+    if (rows && !d_n && w.pre) return fail(ZERO_ERR_INVALID, "%s: %s needs d_n", fn, w.name);
   }
+  void* const dgate = channel ? grads->dgate : nullptr;
+  const bool wanted[kJoinSums] = {grads->dw_pre != nullptr, grads->dbias_pre != nullptr,
+                                  grads->dw_post || dgate, grads->dbias_post || (dgate && in.bias_post)};
+  for (int k = 0; k < kJoinSums; ++k)
+    if (wanted[k]) a.slot[k] = a.n_sums++;
   if (d.gate_kind == ZERO_GATE_ROW || d.gate_kind == ZERO_GATE_FULL) a.dgate = grads->dgate;
   if (!a.dx && !a.db && !a.dgate && a.n_sums == 0)
     return rows ? fail(ZERO_ERR_INVALID, "%s: no gradient is wanted", fn) : ZERO_OK;
-  const int workers = join_workers(a);
   if (a.n_sums > 0) {
     if (!workspace) return fail(ZERO_ERR_INVALID, "%s: workspace is NULL", fn);
     if (!aligned_to(workspace, 16)) return fail(ZERO_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
-    const int64_t need = static_cast<int64_t>(workers) * a.n_sums * d.hidden * 4;
+    const int64_t need = static_cast<int64_t>(join_workers(d)) * a.n_sums * d.hidden * 4;
     if (workspace_bytes < need)
       return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn,
                   workspace_bytes, need);
@@ -490,13 +512,11 @@ extern "C" zero_status zero_block_join_backward(const zero_join_desc* desc, cons
   }
   JOIN_TRY(pending(fn));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (rows) JOIN_TRY(launched(fn, launch_join_backward(a, workers, s)));
+  int workers = 0;
+  if (rows) JOIN_TRY(launched(fn, launch_join(a, true, &workers, s)));
   if (a.n_sums > 0) {
-    sums.partial = a.partial;
-    sums.hidden = d.hidden;
-    sums.workers = workers;
-    sums.n_sums = a.n_sums;
-    k_join_sums<<<dim3(static_cast<unsigned>((d.hidden + 31) / 32), a.n_sums), dim3(32, kSumRows), 0, s>>>(sums);
+    JoinSumArgs g = {a, workers, grads->dw_pre, grads->dbias_pre, grads->dw_post, grads->dbias_post, dgate};
+    k_join_sums<<<dim3(static_cast<unsigned>((d.hidden + 31) / 32)), dim3(32, kSumRows), 0, s>>>(g);
     JOIN_TRY(launched(fn, static_cast<int>(cudaGetLastError())));
   }
   return ZERO_OK;

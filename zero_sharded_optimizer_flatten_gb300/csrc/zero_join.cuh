@@ -6,8 +6,13 @@
 
 namespace zero {
 
-// Column sums of the backward pass (gradients of the parameters).
-enum JoinSum { kSumWPre = 0, kSumBiasPre, kSumWPost, kSumBiasPost, kSumGate, kJoinSums };
+// Column sums of the backward pass over its rows (see zero_join_rows.cuh):
+// sum dn oh, sum dn, sum y go v, sum y go.
+enum JoinSum { kSumP = 0, kSumQ, kSumS, kSumB, kJoinSums };
+
+constexpr int kJoinRowMost = 8192;         // channels of the kernels that hold rows in registers
+constexpr int kJoinThreadsForward = 1024;  // threads of an SM's CTAs there
+constexpr int kJoinThreadsBackward = 768;
 
 struct JoinArgs {
   zero_join_desc d;
@@ -19,7 +24,7 @@ struct JoinArgs {
   float4* stats;       // per row: mean and 1/deviation of b, then of o
   void* dx;
   void* db;
-  void* dgate;         // row and full gates (a channel gate's goes through sums)
+  void* dgate;         // row and full gates (a channel gate's comes from the sums)
   float* partial;      // [workers][n_sums][hidden]
   int32_t slot[kJoinSums];  // place among the partials, -1: not wanted
   int32_t n_sums;
@@ -29,16 +34,14 @@ struct JoinArgs {
 
 // The parameter gradients from the workers' partials.
 struct JoinSumArgs {
-  const float* partial;
-  int64_t hidden;
-  int32_t workers, n_sums;
-  void* out[kJoinSums];     // by slot
-  int32_t type[kJoinSums];  // by slot
+  JoinArgs a;
+  int32_t workers;
+  void *dw_pre, *dbias_pre, *dw_post, *dbias_post, *dgate;  // dgate: channel gates only
 };
 
-int launch_join(const JoinArgs& a, cudaStream_t s);
-// workers: CTAs that leave partials (join_workers of the same arguments).
-int launch_join_backward(const JoinArgs& a, int workers, cudaStream_t s);
-int join_workers(const JoinArgs& a);
+// Kernels for rows of up to kJoinRowMost channels; -1: the rows do not fit.
+// *workers: CTAs launched, each leaving its partials.
+template <class A, class R>
+int launch_join_rows(const JoinArgs& a, bool backward, int* workers, cudaStream_t s);
 
 }  // namespace zero

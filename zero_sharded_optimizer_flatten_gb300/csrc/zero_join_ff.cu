@@ -1,0 +1,6 @@
+// The block join's row kernels: activations float, residual stream float.
+#include "zero_join_rows.cuh"
+
+namespace zero {
+template int launch_join_rows<float, float>(const JoinArgs&, bool, int*, cudaStream_t);
+}  // namespace zero

@@ -131,16 +131,40 @@ def _check_disjoint(entries):
         end[written] = max(end[written], hi)
 
 
+def zero_grad_norm_workspace_bytes(grads) -> int:
+    """Device workspace of zero_grad_norm or zero_clip_grad_norm for this list."""
+    kept = [g for g in grads if g is not None]
+    tensors = (GradTensorC * max(1, len(kept)))()
+    for k, g in enumerate(kept):
+        tensors[k].src_dtype, tensors[k].numel = _grad_tensor(g, f"grads[{k}]"), g.numel()
+        tensors[k].src = g.data_ptr() if g.numel() else None
+    need = ctypes.c_int64()
+    _check(lib().zero_grad_norm_workspace_bytes(tensors, len(kept), ctypes.byref(need)))
+    return need.value
+
+
+def _workspace(t, need: int, device):
+    """A caller's workspace, checked, or a new one."""
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _on(t, "workspace", device)
+    if not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError(f"workspace: needs {need} contiguous bytes")
+    return t
+
+
 class GradNorm:
     """A prepared zero_grad_norm over `grads` (None entries are left out):
     the list is checked and marshalled once, each call takes the norm of what
     the tensors hold then.  Returns the norm as a float32 tensor without
-    dimensions, a view of `result`, which the next call overwrites."""
+    dimensions, a view of `result`, which the next call overwrites.
+    workspace: device scratch of zero_grad_norm_workspace_bytes (None: its
+    own)."""
 
-    def __init__(self, grads, kind: str = "l2"):
-        self._prepare([g for g in grads if g is not None], None, kind)
+    def __init__(self, grads, kind: str = "l2", workspace=None):
+        self._prepare([g for g in grads if g is not None], None, kind, workspace)
 
-    def _prepare(self, grads, out, kind):
+    def _prepare(self, grads, out, kind, workspace):
         self.kind = _choice(_NORMS, kind, "kind")
         self._keep = (grads, out)
         self._list = (GradTensorC * max(1, len(grads)))()
@@ -177,7 +201,7 @@ class GradNorm:
         need = ctypes.c_int64()
         _check(lib().zero_grad_norm_workspace_bytes(self._list, self.n, ctypes.byref(need)))
         self.result = torch.empty(NORM_RESULT_BYTES, dtype=torch.uint8, device=device)
-        self._workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+        self._workspace = _workspace(workspace, need.value, device)
         self._norm = self.result[8:12].view(torch.float32)[0]
         self._args = (self.result.data_ptr(), self._workspace.data_ptr(), need.value)
 
@@ -195,7 +219,7 @@ class ClipGradNorm(GradNorm):
     `out` may have other types, for instance the views of a 16-bit replica
     that fp32 gradients go to.  `max_norm` may be changed between calls."""
 
-    def __init__(self, grads, max_norm: float, kind: str = "l2", out=None):
+    def __init__(self, grads, max_norm: float, kind: str = "l2", out=None, workspace=None):
         grads = list(grads)
         self.max_norm = float(max_norm)
         if out is None:
@@ -206,7 +230,7 @@ class ClipGradNorm(GradNorm):
                 raise ValueError(f"out: expected {len(grads)} entries, got {len(out)}")
             pairs = [(g, d) for g, d in zip(grads, out) if g is not None]
             grads, out = [g for g, _ in pairs], [d for _, d in pairs]
-        self._prepare(grads, out, kind)
+        self._prepare(grads, out, kind, workspace)
 
     def __call__(self, stream=None):
         _check(lib().zero_clip_grad_norm(self._list, self.n, self.kind, self.max_norm,
@@ -359,13 +383,24 @@ def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_
     return x if b is None and o is None else o, n, stats
 
 
+def zero_block_join_workspace_bytes(x, b=None, *, w_post=None, bias_post=None, w_pre=None,
+                                    bias_pre=None, gate=None, kind: str = "rms",
+                                    scale: float = 1.0, eps: float = 1e-6) -> int:
+    """Device workspace of zero_block_join_backward for these arguments."""
+    d = _join_args(x, b, gate, (w_post, bias_post, w_pre, bias_pre), kind, scale, eps, None)[0]
+    need = ctypes.c_int64()
+    _check(lib().zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
+    return need.value
+
+
 def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=None, w_pre=None,
                              bias_pre=None, gate=None, kind: str = "rms", scale: float = 1.0,
-                             eps: float = 1e-6, want=None, stream=None):
+                             eps: float = 1e-6, want=None, workspace=None, stream=None):
     """Gradients of zero_block_join's inputs from those of o and n (either
     may be None) and its stats: a dict with dx, db, dgate, dw_post,
     dbias_post, dw_pre and dbias_pre, None for what has no input or is not in
-    `want` (a set of those names; None: all)."""
+    `want` (a set of those names; None: all).  workspace: device scratch of
+    zero_block_join_workspace_bytes (None: allocated here)."""
     params = (w_post, bias_post, w_pre, bias_pre)
     act = None if d_n is None else d_n.dtype
     d, p, device, act = _join_args(x, b, gate, params, kind, scale, eps, act)
@@ -399,8 +434,8 @@ def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=No
     ws = None
     if sums:
         _check(lib().zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-        _keep_for(stream, ws)
+        ws = _workspace(workspace, need.value, device)
+        _keep_for(stream, ws if workspace is None else None)
     if any(getattr(g, name) for name in out):
         _check(lib().zero_block_join_backward(
             ctypes.byref(d), ctypes.byref(p), None if d_o is None else d_o.data_ptr(),
