@@ -84,6 +84,10 @@ struct Row {
       return a.scale * load_any(a.in.gate, row * a.d.gate_stride + c, a.d.gate_dtype);
     return g_row;
   }
+  // the row's or the element's own gate, without the scale
+  __device__ __forceinline__ float own_gate(int64_t c) const {
+    return load_any(a.in.gate, row * a.d.gate_stride + (a.d.gate_kind == ZERO_GATE_FULL ? c : 0), a.d.gate_dtype);
+  }
   __device__ __forceinline__ float block(int64_t c) const { return Elem<A>::widen(b[c]); }
   __device__ __forceinline__ float b_hat(int64_t c) const { return (block(c) - mb) * rb; }
   __device__ __forceinline__ float u(int64_t c) const {
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_join_backward_any(const __grid_
       }
       if (a.in.b) {
         const float du = row.gate(c) * go;
-        const float y = by_row ? du : go;
+        const float y = by_row ? row.own_gate(c) * go : go;
         add(kSumS, y * (a.in.w_post ? row.b_hat(c) : row.block(c)));
         add(kSumB, y);
         if (a.d.gate_kind == ZERO_GATE_FULL && a.dgate)
@@ -248,8 +252,7 @@ __global__ void __launch_bounds__(32 * kSumRows) k_join_sums(const __grid_consta
   if (g.dw_pre) store_any(g.dw_pre, c, pt, s[kSumP]);
   if (g.dbias_pre) store_any(g.dbias_pre, c, pt, s[kSumQ]);
   float gate = a.scale;
-  // row and full gates are in the sums already, with the scale
-  if (a.d.gate_kind == ZERO_GATE_ROW || a.d.gate_kind == ZERO_GATE_FULL) gate = 1.f;
+  // (row and full gates are in the sums already)
   if (a.d.gate_kind == ZERO_GATE_CHANNEL) gate *= load_any(a.in.gate, c, a.d.gate_dtype);
   if (g.dw_post) store_any(g.dw_post, c, pt, gate * s[kSumS]);
   if (g.dbias_post) store_any(g.dbias_post, c, pt, gate * s[kSumB]);
@@ -265,8 +268,8 @@ __global__ void __launch_bounds__(32 * kSumRows) k_join_sums(const __grid_consta
 int join_workers(const zero_join_desc& d) {
   int64_t most = kAnyWorkers;
   if (d.hidden <= kJoinRowMost) {
-    const int64_t threads = (d.hidden + 255) / 256 * 32;
-    most = kSMs * std::max<int64_t>(1, std::min<int64_t>(16, kJoinThreadsBackward / threads));
+    const int64_t threads = std::max<int64_t>(d.hidden <= 256 ? 128 : 0, (d.hidden + 255) / 256 * 32);
+    most = kSMs * std::max<int64_t>(1, kJoinThreadsBackward / threads);
   }
   return static_cast<int>(std::min(d.rows, most));
 }
