@@ -26,9 +26,17 @@
 #include <algorithm>
 
 #include "zero_capi_util.h"
-#include "zero_join.cuh"
+#include "zero_join_rows.cuh"
 
 namespace zero {
+
+// one translation unit a pair of types (zero_join_*.cu)
+extern template int launch_join_rows<float, float>(const JoinArgs&, bool, int*, cudaStream_t);
+extern template int launch_join_rows<__half, __half>(const JoinArgs&, bool, int*, cudaStream_t);
+extern template int launch_join_rows<__half, float>(const JoinArgs&, bool, int*, cudaStream_t);
+extern template int launch_join_rows<__nv_bfloat16, __nv_bfloat16>(const JoinArgs&, bool, int*, cudaStream_t);
+extern template int launch_join_rows<__nv_bfloat16, float>(const JoinArgs&, bool, int*, cudaStream_t);
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -224,30 +232,55 @@ __global__ void __launch_bounds__(kAnyThreads) k_join_backward_any(const __grid_
   }
 }
 
-// Parameter gradients: a column's partials in worker order, kSumRows strands
-// of them added side by side and then joined, so the order is fixed.
-constexpr int kSumRows = 8;
+// Parameter gradients: a column's partials in kSumRows strands, each in
+// worker order, then the strands in order.  A CTA has 16 columns, so that
+// short rows make enough CTAs; a strand's loads of all sums are in flight
+// together (with 8 strands of 32 columns this took 20 us for 760 workers).
+constexpr int kSumRows = 64, kSumCols = 16, kSumAhead = 4;
 
-__global__ void __launch_bounds__(32 * kSumRows) k_join_sums(const __grid_constant__ JoinSumArgs g) {
-  __shared__ float part[kSumRows][kJoinSums][33];
+__global__ void __launch_bounds__(kSumCols * kSumRows) k_join_sums(const __grid_constant__ JoinSumArgs g) {
+  __shared__ float part[kJoinSums][kSumRows][kSumCols + 1];
   const JoinArgs& a = g.a;
-  const int64_t H = a.d.hidden, c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-  float s[kJoinSums];
+  const int64_t H = a.d.hidden, c = static_cast<int64_t>(blockIdx.x) * kSumCols + threadIdx.x;
+  float s[kJoinSums] = {0.f, 0.f, 0.f, 0.f};
+  const float* p = a.partial + c;
+  const int64_t worker = a.n_sums * H;
+  if (c < H) {
+    for (int w = threadIdx.y; w < g.workers; w += kSumAhead * kSumRows) {
+      float v[kJoinSums][kSumAhead];
 #pragma unroll
-  for (int k = 0; k < kJoinSums; ++k) {
-    s[k] = 0.f;
-    if (a.slot[k] < 0) continue;
-    const float* p = a.partial + a.slot[k] * H + c;
-    if (c < H)
-      for (int w = threadIdx.y; w < g.workers; w += kSumRows) s[k] += p[static_cast<int64_t>(w) * a.n_sums * H];
-    part[threadIdx.y][k][threadIdx.x] = s[k];
+      for (int k = 0; k < kJoinSums; ++k)
+#pragma unroll
+        for (int i = 0; i < kSumAhead; ++i) {
+          const int x = w + i * kSumRows;
+          v[k][i] = a.slot[k] >= 0 && x < g.workers ? p[x * worker + a.slot[k] * H] : 0.f;
+        }
+#pragma unroll
+      for (int k = 0; k < kJoinSums; ++k)
+#pragma unroll
+        for (int i = 0; i < kSumAhead; ++i) s[k] += v[k][i];
+    }
   }
-  __syncthreads();
-  if (threadIdx.y != 0 || c >= H) return;
 #pragma unroll
-  for (int k = 0; k < kJoinSums; ++k)
-    if (a.slot[k] >= 0)
-      for (int y = 1; y < kSumRows; ++y) s[k] += part[y][k][threadIdx.x];
+  for (int k = 0; k < kJoinSums; ++k) part[k][threadIdx.y][threadIdx.x] = s[k];
+  __syncthreads();
+  // strands 8 at a time, twice
+  for (int rows = kSumRows / 8; rows > 0; rows /= 8) {
+    float t[kJoinSums] = {0.f, 0.f, 0.f, 0.f};
+    if (threadIdx.y < rows) {
+#pragma unroll
+      for (int k = 0; k < kJoinSums; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[k] += part[k][threadIdx.y * 8 + i][threadIdx.x];
+    }
+    __syncthreads();
+    if (threadIdx.y < rows) {
+#pragma unroll
+      for (int k = 0; k < kJoinSums; ++k) part[k][threadIdx.y][threadIdx.x] = s[k] = t[k];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.y != 0 || c >= H) return;
   const int pt = a.d.param_dtype;
   if (g.dw_pre) store_any(g.dw_pre, c, pt, s[kSumP]);
   if (g.dbias_pre) store_any(g.dbias_pre, c, pt, s[kSumQ]);
@@ -268,8 +301,8 @@ __global__ void __launch_bounds__(32 * kSumRows) k_join_sums(const __grid_consta
 int join_workers(const zero_join_desc& d) {
   int64_t most = kAnyWorkers;
   if (d.hidden <= kJoinRowMost) {
-    const int64_t threads = std::max<int64_t>(d.hidden <= 256 ? 128 : 0, (d.hidden + 255) / 256 * 32);
-    most = kSMs * std::max<int64_t>(1, kJoinThreadsBackward / threads);
+    const int threads = std::min(join_threads(d.hidden, true, true), join_threads(d.hidden, false, true));
+    most = kSMs * std::max(1, kJoinThreadsBackward / threads);
   }
   return static_cast<int>(std::min(d.rows, most));
 }
@@ -519,7 +552,7 @@ extern "C" zero_status zero_block_join_backward(const zero_join_desc* desc, cons
   if (rows) JOIN_TRY(launched(fn, launch_join(a, true, &workers, s)));
   if (a.n_sums > 0) {
     JoinSumArgs g = {a, workers, grads->dw_pre, grads->dbias_pre, grads->dw_post, grads->dbias_post, dgate};
-    k_join_sums<<<dim3(static_cast<unsigned>((d.hidden + 31) / 32)), dim3(32, kSumRows), 0, s>>>(g);
+    k_join_sums<<<static_cast<unsigned>((d.hidden + kSumCols - 1) / kSumCols), dim3(kSumCols, kSumRows), 0, s>>>(g);
     JOIN_TRY(launched(fn, static_cast<int>(cudaGetLastError())));
   }
   return ZERO_OK;

@@ -11,6 +11,7 @@ namespace zero {
 enum JoinSum { kSumP = 0, kSumQ, kSumS, kSumB, kJoinSums };
 
 constexpr int kJoinRowMost = 8192;         // channels of the kernels that hold rows in registers
+constexpr int kJoinNarrow = 4096;          // backward rows above it: 16 columns a thread
 constexpr int kJoinThreadsForward = 1024;  // threads of an SM's CTAs there
 constexpr int kJoinThreadsBackward = 768;
 

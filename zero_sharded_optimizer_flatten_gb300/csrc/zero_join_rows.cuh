@@ -1,21 +1,24 @@
 // The block join for rows of at most 8192 channels: a row's values stay in
-// registers, eight columns a thread, from the one read to the one write.
+// registers, 8 or 16 columns a thread, from the one read to the one write.
 //
-// Row split.  Above 256 channels a CTA of ceil(hidden / 8) threads (whole
-// warps) takes a row at a time; a row's sums go through one shuffle tree a
-// warp and one barrier.  Up to 256 channels 8, 16 or 32 lanes take a row and
-// a CTA of 128 threads several rows, without barriers.  Rows are handed out
-// grid-stride.
+// Row split.  Above 256 channels a CTA of whole warps takes a row at a time; a
+// row's sums go through one shuffle tree a warp and one barrier.  Shorter rows
+// (up to 512 channels with 16 columns a thread) are taken by 4 to 32 lanes
+// and a CTA of 128 threads has several.  Rows are handed out grid-stride.
 //
-// Column maps.  kOct: thread t of a row's T has columns 8t..8t+7, one 16-byte
-// access of 16-bit data.  kQuad (a 32-bit array takes part): columns 4t..4t+3
-// and 4(T+t)..+3, so fp32 accesses are whole 512-byte runs a warp.  kAny:
-// columns t + kT, element accesses, for odd row lengths and unaligned rows.
+// Column maps.  A thread's columns come in units of u neighbours, unit j of
+// thread t of a row's T at column u (t + j T): u = 8 (kOct) where all rows are
+// 16-bit, 16-byte accesses; u = 4 (kQuad) where a 32-bit array takes part, so
+// fp32 accesses are whole 512-byte runs a warp; and for rows that start
+// anywhere (odd lengths, views) u = 2 (kPair) for 16-bit rows, u = 1 (kLone)
+// with 32-bit ones.
 //
-// Loads.  kOct and kQuad read ahead through a ring of rows in shared memory
-// filled by asynchronous copies; every thread copies just the columns that it
-// will use, so the ring needs no barrier, and waits for its own copies only.
-// kAny reads its row directly and relies on other CTAs of the SM to overlap.
+// Loads.  Rows are read ahead through a ring in shared memory filled by
+// asynchronous copies.  kOct and kQuad: every thread copies just the columns
+// that it will use, so the ring needs no barrier.  kPair and kLone: the row's
+// covering 16-byte chunks are copied as they lie, with one barrier a row;
+// chunks that reach outside the tensor (its first and last rows) go element
+// by element.
 //
 // Arithmetic is in pairs of binary32 (two elements an instruction): with the
 // loads asynchronous, the instructions issued a row are what stands beside
@@ -35,6 +38,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "zero_join.cuh"
 
@@ -45,7 +49,7 @@ constexpr int kJoinSmemMost = 224 * 1024;  // of one SM's CTAs together
 constexpr int kJoinScratch = 2 * 2 * 32 * 4;  // two buffers of two sums a warp
 constexpr int kJoinSmallCta = 128;         // threads of a CTA of several rows
 
-enum JoinMap { kOct, kQuad, kAny };
+enum JoinMap { kOct, kQuad, kPair, kLone };
 
 // What lies in the ring and in the vectors' part of shared memory; offsets in
 // bytes, -1: absent.
@@ -55,6 +59,8 @@ struct JoinLayout {
   int32_t x, b, d_o, d_n, gate;     // within a stage
   int32_t w1, b1, w2, b2;           // from the vectors' start
   int32_t vec_bytes;
+  // ends of the inputs: kPair and kLone read whole chunks up to there
+  const char *x_end, *b_end, *do_end, *dn_end, *gate_end;
 };
 
 // Two binary32 values that go through one instruction.
@@ -114,6 +120,18 @@ __device__ __forceinline__ void copies_wait(int ahead) {
     asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
+// Bytes [from, to) of elements of E bytes, one by one.
+template <int E>
+__device__ __noinline__ void copy_elements(char* dst, const char* src, int from, int to) {
+#pragma unroll 1
+  for (int e = from; e < to; e += E) {
+    if constexpr (E == 4)
+      *reinterpret_cast<uint32_t*>(dst + e) = *reinterpret_cast<const uint32_t*>(src + e);
+    else
+      *reinterpret_cast<uint16_t*>(dst + e) = *reinterpret_cast<const uint16_t*>(src + e);
+  }
+}
+
 template <class T>
 __device__ __forceinline__ F2 widen2(uint32_t w) {
   float lo, hi;
@@ -130,120 +148,145 @@ __device__ __forceinline__ uint32_t pack2(F2 v) {
   return Elem<T>::pack(lo, hi);
 }
 
-// A thread's eight columns of a row; in registers they are four pairs.
-template <int MAP>
+// A thread's 2 NP columns of a row; in registers they are NP pairs.
+template <int MAP, int NP>
 struct JoinCols {
+  static constexpr bool kWide = MAP == kOct || MAP == kQuad;
+  static constexpr int kUnit = MAP == kOct ? 8 : MAP == kQuad ? 4 : MAP == kPair ? 2 : 1;
+  static constexpr int kUnits = 2 * NP / kUnit;
   int t, T;        // place among the row's threads
   int tid, n;      // place in the CTA: where its slots are
+  int group;       // the thread's row among the CTA's
   int hidden;
-  __device__ __forceinline__ int col(int k) const {
-    if constexpr (MAP == kOct) return 8 * t + k;
-    if constexpr (MAP == kQuad) return k < 4 ? 4 * t + k : 4 * (T + t) + k - 4;
-    return t + k * T;
-  }
+  __device__ __forceinline__ int col(int k) const { return kUnit * (t + k / kUnit * T) + k % kUnit; }
   __device__ __forceinline__ bool has(int k) const { return col(k) < hidden; }
-  __device__ __forceinline__ bool ragged() const { return !has(7); }
+  __device__ __forceinline__ bool ragged() const { return !has(2 * NP - 1); }
 
-  // This thread's part of a row of elements of `type` into its slots at
-  // shared-memory address `slot`.
-  __device__ __forceinline__ void fetch(uint32_t slot, const void* row, int type) const {
+  // A row's copy into its place `at` in shared memory.
+  template <int TYPE>
+  __device__ __forceinline__ void fetch(char* at, const void* row, const void* first, const char* end) const {
+    constexpr int E = TYPE == ZERO_FP32 ? 4 : 2;
     const char* p = static_cast<const char*>(row);
-    if constexpr (MAP == kOct) {
-      if (!has(0)) return;
-      if (type == ZERO_FP32) {
-        copy_async<16>(slot + 16 * tid, p + 32 * t);
-        copy_async<16>(slot + 16 * (n + tid), p + 32 * t + 16);
-      } else {
-        copy_async<16>(slot + 16 * tid, p + 16 * t);
-      }
-    } else if constexpr (MAP == kQuad) {
-      if (type == ZERO_FP32) {
-        if (has(0)) copy_async<16>(slot + 16 * tid, p + 16 * t);
-        if (has(4)) copy_async<16>(slot + 16 * (n + tid), p + 16 * (T + t));
-      } else {
-        if (has(0)) copy_async<8>(slot + 8 * tid, p + 8 * t);
-        if (has(4)) copy_async<8>(slot + 8 * (n + tid), p + 8 * (T + t));
-      }
-    }
-  }
-  // The same slots (cleared once where there is no column).
-  template <class E>
-  __device__ __forceinline__ void read(const char* slot, F2 (&v)[4]) const {
-    if constexpr (Elem<E>::kType == ZERO_FP32) {
+    if constexpr (kWide) {
+      constexpr int B = kUnit * E, W = B < 16 ? B : 16;
+      const uint32_t slot = smem_of(at);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) quad32(slot + 16 * (h * n + tid), v + 2 * h);
-    } else if constexpr (MAP == kOct) {
-      const uint4 w = *reinterpret_cast<const uint4*>(slot + 16 * tid);
-      v[0] = widen2<E>(w.x), v[1] = widen2<E>(w.y), v[2] = widen2<E>(w.z), v[3] = widen2<E>(w.w);
+      for (int j = 0; j < kUnits; ++j)
+        if (has(j * kUnit)) {
+#pragma unroll
+          for (int h = 0; h < B / W; ++h)
+            copy_async<W>(slot + W * ((j * (B / W) + h) * n + tid), p + B * (t + j * T) + W * h);
+        }
     } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 w = *reinterpret_cast<const uint2*>(slot + 8 * (h * n + tid));
-        v[2 * h] = widen2<E>(w.x), v[2 * h + 1] = widen2<E>(w.y);
+      // chunks as they lie, the row's first byte at its own place in a chunk
+      const int bytes = hidden * E, skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+      char* row_at = at + group * row_bytes(E);
+#pragma unroll 1
+      for (int i = 16 * t; i < skip + bytes; i += 16 * T) {
+        const char* q = p - skip + i;
+        if (q >= static_cast<const char*>(first) && q + 16 <= end) {
+          copy_async<16>(smem_of(row_at + i), q);
+        } else {
+          copy_elements<E>(row_at, p - skip, max(i, skip), min(i + 16, skip + bytes));
+        }
       }
     }
   }
-  __device__ __forceinline__ void read_any(const char* slot, int type, F2 (&v)[4]) const {
-    if (type == ZERO_FP32)
-      read<float>(slot, v);
-    else if (type == ZERO_BF16)
-      read<__nv_bfloat16>(slot, v);
-    else
-      read<__half>(slot, v);
-  }
-  // Straight from global memory, element by element.
+  __host__ __device__ __forceinline__ int row_bytes(int elem) const { return (hidden * elem + 15) / 16 * 16 + 16; }
+
+  // The same row's columns, zero past its end (kWide: slots without a column
+  // are cleared once).  row: where it was copied from.
   template <class E>
-  __device__ __forceinline__ void read_global(const E* row, F2 (&v)[4]) const {
-    float f[8];
+  __device__ __forceinline__ void read(const char* at, const void* row, F2 (&v)[NP]) const {
+    constexpr int B = sizeof(E);
+    if constexpr (kWide) {
+      constexpr int W = kUnit * B < 16 ? 8 : 16;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = has(k) ? Elem<E>::widen(row[col(k)]) : 0.f;
+      for (int j = 0; j < 2 * NP * B / W; ++j) {
+        const char* p = at + W * (j * n + tid);
+        if constexpr (B == 4) {
+          quad32(p, v + 2 * j);
+        } else if constexpr (W == 16) {
+          const uint4 w = *reinterpret_cast<const uint4*>(p);
+          v[4 * j] = widen2<E>(w.x), v[4 * j + 1] = widen2<E>(w.y);
+          v[4 * j + 2] = widen2<E>(w.z), v[4 * j + 3] = widen2<E>(w.w);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          v[2 * j] = widen2<E>(w.x), v[2 * j + 1] = widen2<E>(w.y);
+        }
+      }
+    } else {
+      const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+      const char* p = at + group * row_bytes(B) + skip;
+      if (MAP == kPair && (skip & 3) == 0 && B == 2) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = f2(f[2 * k], f[2 * k + 1]);
+        for (int k = 0; k < NP; ++k) {
+          uint32_t w = 0;
+          if (has(2 * k + 1))
+            w = *reinterpret_cast<const uint32_t*>(p + 2 * col(2 * k));
+          else if (has(2 * k))
+            w = *reinterpret_cast<const uint16_t*>(p + 2 * col(2 * k));
+          if constexpr (B == 2) v[k] = widen2<E>(w);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const E* e = reinterpret_cast<const E*>(p);
+          v[k] = f2(has(2 * k) ? Elem<E>::widen(e[col(2 * k)]) : 0.f,
+                    has(2 * k + 1) ? Elem<E>::widen(e[col(2 * k + 1)]) : 0.f);
+        }
+      }
+    }
   }
-  __device__ __forceinline__ void read_global_any(const void* row, int64_t at, int type, F2 (&v)[4]) const {
-    if (type == ZERO_FP32)
-      read_global(static_cast<const float*>(row) + at, v);
-    else if (type == ZERO_BF16)
-      read_global(static_cast<const __nv_bfloat16*>(row) + at, v);
-    else
-      read_global(static_cast<const __half*>(row) + at, v);
+  // A vector's slots: this thread's binary32 values, planes of four.
+  __device__ __forceinline__ void vector_in(char* vec, const float (&f)[2 * NP]) const {
+#pragma unroll
+    for (int q = 0; q < NP / 2; ++q)
+      *reinterpret_cast<float4*>(vec + 16 * (q * n + tid)) =
+          make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
   }
-  // A vector's slots: this thread's eight binary32 values, two planes.
-  __device__ __forceinline__ void vector_in(char* vec, const float (&f)[8]) const {
-    *reinterpret_cast<float4*>(vec + 16 * tid) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(vec + 16 * (n + tid)) = make_float4(f[4], f[5], f[6], f[7]);
-  }
-  __device__ __forceinline__ void vector(const char* vec, F2 (&v)[4]) const {
-    quad32(vec + 16 * tid, v);
-    quad32(vec + 16 * (n + tid), v + 2);
+  __device__ __forceinline__ void vector(const char* vec, F2 (&v)[NP]) const {
+#pragma unroll
+    for (int q = 0; q < NP / 2; ++q) quad32(vec + 16 * (q * n + tid), v + 2 * q);
   }
   template <class E>
-  __device__ __forceinline__ void write(E* row, const F2 (&v)[4]) const {
-    if constexpr (MAP == kAny) {
+  __device__ __forceinline__ void write(E* row, const F2 (&v)[NP]) const {
+    if constexpr (kWide) {
+      constexpr int Q = kUnit / 4;  // quads of a unit
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int j = 0; j < kUnits; ++j) {
+        if (!has(j * kUnit)) continue;
+        E* p = row + col(j * kUnit);
+        if constexpr (sizeof(E) == 4) {
+#pragma unroll
+          for (int h = 0; h < Q; ++h)
+            *reinterpret_cast<ulonglong2*>(p + 4 * h) =
+                make_ulonglong2(v[2 * (j * Q + h)].w, v[2 * (j * Q + h) + 1].w);
+        } else if constexpr (MAP == kOct) {
+          *reinterpret_cast<uint4*>(p) = make_uint4(pack2<E>(v[4 * j]), pack2<E>(v[4 * j + 1]),
+                                                    pack2<E>(v[4 * j + 2]), pack2<E>(v[4 * j + 3]));
+        } else {
+          *reinterpret_cast<uint2*>(p) = make_uint2(pack2<E>(v[2 * j]), pack2<E>(v[2 * j + 1]));
+        }
+      }
+    } else {
+      const bool whole = MAP == kPair && sizeof(E) == 2 && (reinterpret_cast<uintptr_t>(row) & 3) == 0;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        if constexpr (MAP == kPair && sizeof(E) == 2) {
+          if (whole && has(2 * k + 1)) {
+            *reinterpret_cast<uint32_t*>(row + col(2 * k)) = pack2<E>(v[k]);
+            continue;
+          }
+        }
         float lo, hi;
         f2_out(v[k], lo, hi);
         if (has(2 * k)) row[col(2 * k)] = Elem<E>::narrow(lo);
         if (has(2 * k + 1)) row[col(2 * k + 1)] = Elem<E>::narrow(hi);
       }
-    } else if constexpr (Elem<E>::kType == ZERO_FP32) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (has(4 * h))
-          *reinterpret_cast<ulonglong2*>(row + col(4 * h)) = make_ulonglong2(v[2 * h].w, v[2 * h + 1].w);
-    } else if constexpr (MAP == kOct) {
-      if (has(0))
-        *reinterpret_cast<uint4*>(row + col(0)) =
-            make_uint4(pack2<E>(v[0]), pack2<E>(v[1]), pack2<E>(v[2]), pack2<E>(v[3]));
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (has(4 * h))
-          *reinterpret_cast<uint2*>(row + col(4 * h)) = make_uint2(pack2<E>(v[2 * h]), pack2<E>(v[2 * h + 1]));
     }
   }
-  __device__ __forceinline__ void write_any(void* row, int64_t at, int type, const F2 (&v)[4]) const {
+  __device__ __forceinline__ void write_any(void* row, int64_t at, int type, const F2 (&v)[NP]) const {
     if (type == ZERO_FP32)
       write(static_cast<float*>(row) + at, v);
     else if (type == ZERO_BF16)
@@ -258,6 +301,12 @@ struct JoinCols {
     v[0].w = f.x, v[1].w = f.y;
   }
 };
+
+template <int NP>
+__device__ __forceinline__ void clear(F2 (&v)[NP]) {
+#pragma unroll
+  for (int k = 0; k < NP; ++k) v[k] = f2(0.f);
+}
 
 // Sums of N <= 2 values over a row's threads, the same in all of them, in a
 // fixed order: a butterfly over the row's lanes of a warp, then (rows of
@@ -298,14 +347,14 @@ __device__ __forceinline__ void join_sums(float (&v)[N], float* scratch, int& fl
 }
 
 // w1, b1, w2, b2 (see above) to this thread's slots.
-template <int MAP>
-__device__ __forceinline__ void fold_vectors(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP>& c,
+template <int MAP, int NP>
+__device__ __forceinline__ void fold_vectors(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
                                              char* vec) {
-  float f[8];
   auto each = [&](int at, auto value) {
     if (at < 0) return;
+    float f[2 * NP];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = c.has(k) ? value(c.col(k)) : 0.f;
+    for (int k = 0; k < 2 * NP; ++k) f[k] = c.has(k) ? value(c.col(k)) : 0.f;
     c.vector_in(vec + at, f);
   };
   const int pt = a.d.param_dtype;
@@ -318,72 +367,112 @@ __device__ __forceinline__ void fold_vectors(const JoinArgs& a, const JoinLayout
   each(l.b2, [&](int k) { return load_any(a.in.bias_pre, k, pt); });
 }
 
-// Row r's inputs into stage `stage`.
-template <class A, class R, int MAP>
-__device__ __forceinline__ void fetch_row(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP>& c,
-                                          char* ring, int stage, int64_t r) {
-  if constexpr (MAP != kAny) {
-    if (r < a.d.rows) {
-      const uint32_t s = smem_of(ring) + stage * l.stage_bytes;
-      c.fetch(s + l.x, static_cast<const R*>(a.in.x) + r * a.d.x_stride, Elem<R>::kType);
-      if (l.b >= 0) c.fetch(s + l.b, static_cast<const A*>(a.in.b) + r * a.d.b_stride, Elem<A>::kType);
-      if (l.d_o >= 0) c.fetch(s + l.d_o, static_cast<const R*>(a.d_o) + r * a.d.do_stride, Elem<R>::kType);
-      if (l.d_n >= 0) c.fetch(s + l.d_n, static_cast<const A*>(a.d_n) + r * a.d.dn_stride, Elem<A>::kType);
-      if (l.gate >= 0)
-        c.fetch(s + l.gate,
-                static_cast<const char*>(a.in.gate) + r * a.d.gate_stride * type_bytes(a.d.gate_dtype),
-                a.d.gate_dtype);
-    }
-    copies_commit();
-  }
+// Where row r of an input lies.
+template <class E>
+__device__ __forceinline__ const E* row_of(const void* p, int64_t r, int64_t stride) {
+  return static_cast<const E*>(p) + r * stride;
+}
+__device__ __forceinline__ const char* gate_row_of(const JoinArgs& a, int64_t r) {
+  return static_cast<const char*>(a.in.gate) + r * a.d.gate_stride * type_bytes(a.d.gate_dtype);
 }
 
-// One input of row r: from the ring, or from global memory.
-template <class E, int MAP>
-__device__ __forceinline__ void row_input(const JoinCols<MAP>& c, const char* stage, int at, const void* p,
-                                          int64_t r, int64_t stride, F2 (&v)[4]) {
-  if constexpr (MAP == kAny)
-    c.read_global(static_cast<const E*>(p) + r * stride, v);
-  else
-    c.template read<E>(stage + at, v);
+// Row r's inputs into stage `stage`.
+template <class A, class R, bool OWN, int MAP, int NP>
+__device__ __forceinline__ void fetch_row(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
+                                          char* ring, int stage, int64_t r) {
+  if (r < a.d.rows) {
+    char* s = ring + stage * l.stage_bytes;
+    c.template fetch<Elem<R>::kType>(s + l.x, row_of<R>(a.in.x, r, a.d.x_stride), a.in.x, l.x_end);
+    if (l.b >= 0)
+      c.template fetch<Elem<A>::kType>(s + l.b, row_of<A>(a.in.b, r, a.d.b_stride), a.in.b, l.b_end);
+    if (l.d_o >= 0)
+      c.template fetch<Elem<R>::kType>(s + l.d_o, row_of<R>(a.d_o, r, a.d.do_stride), a.d_o, l.do_end);
+    if (l.d_n >= 0)
+      c.template fetch<Elem<A>::kType>(s + l.d_n, row_of<A>(a.d_n, r, a.d.dn_stride), a.d_n, l.dn_end);
+    if (OWN && l.gate >= 0) {
+      if (a.d.gate_dtype == ZERO_FP32)
+        c.template fetch<ZERO_FP32>(s + l.gate, gate_row_of(a, r), a.in.gate, l.gate_end);
+      else
+        c.template fetch<ZERO_BF16>(s + l.gate, gate_row_of(a, r), a.in.gate, l.gate_end);  // or fp16
+    }
+  }
+  copies_commit();
 }
 
 // y w1: what multiplies the normalised block output, and y itself where rows
 // or elements have their own gates (OWN).
-template <bool OWN, int MAP>
-__device__ __forceinline__ void row_gate(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP>& c,
-                                         const char* stage, const char* vec, int64_t r, F2 (&y)[4],
-                                         F2 (&w)[4]) {
+template <class A, bool OWN, int MAP, int NP>
+__device__ __forceinline__ void row_gate(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
+                                         const char* stage, const char* vec, int64_t r, F2 (&y)[NP],
+                                         F2 (&w)[NP]) {
   c.vector(vec + l.w1, w);
   if constexpr (OWN) {
     if (a.d.gate_kind == ZERO_GATE_FULL) {
-      if constexpr (MAP == kAny)
-        c.read_global_any(a.in.gate, r * a.d.gate_stride, a.d.gate_dtype, y);
+      if (a.d.gate_dtype == ZERO_FP32)
+        c.template read<float>(stage + l.gate, gate_row_of(a, r), y);
       else
-        c.read_any(stage + l.gate, a.d.gate_dtype, y);
+        c.template read<A>(stage + l.gate, gate_row_of(a, r), y);
     } else {
-      y[0] = y[1] = y[2] = y[3] = f2(load_any(a.in.gate, r * a.d.gate_stride, a.d.gate_dtype));
+      const F2 one = f2(load_any(a.in.gate, r * a.d.gate_stride, a.d.gate_dtype));
+#pragma unroll
+      for (int k = 0; k < NP; ++k) y[k] = one;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = mul2(w[k], y[k]);
+    for (int k = 0; k < NP; ++k) w[k] = mul2(w[k], y[k]);
   }
 }
 
+// The ring's step at the start of row i: its copies have arrived, and the
+// slots of the row before it are free for the row `stages` behind that one.
+// kWide refills its own slots later, when it has read them.
+template <class A, class R, bool OWN, bool MANY, int MAP, int NP>
+__device__ __forceinline__ void ring_step(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
+                                          char* ring, int stage, int64_t r, int64_t step) {
+  auto meet = [] {  // the threads of a row
+    if constexpr (MANY)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  if constexpr (JoinCols<MAP, NP>::kWide) {
+    copies_wait(l.stages - 1);
+  } else if (l.stages == 1) {
+    meet();
+    fetch_row<A, R, OWN>(a, l, c, ring, 0, r);
+    copies_wait(0);
+    meet();
+  } else {
+    copies_wait(l.stages - 2);
+    meet();
+    const int free = stage == 0 ? l.stages - 1 : stage - 1;
+    fetch_row<A, R, OWN>(a, l, c, ring, free, r + (l.stages - 1) * step);
+  }
+}
+template <class A, class R, bool OWN, int MAP, int NP>
+__device__ __forceinline__ void ring_start(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
+                                           char* ring, int64_t r, int64_t step) {
+  const int ahead = JoinCols<MAP, NP>::kWide ? l.stages : l.stages - 1;
+  for (int s = 0; s < ahead; ++s) fetch_row<A, R, OWN>(a, l, c, ring, s, r + s * step);
+}
+
 // Mean (layer only) and 1/deviation of a row; v becomes the normalised row.
-template <bool LAYER, int QUADS, int MAP>
-__device__ __forceinline__ void normalise(const JoinArgs& a, const JoinCols<MAP>& c, float* scratch, int& flip,
-                                          F2 (&v)[4], float& mean, float& r) {
+template <bool LAYER, int QUADS, int MAP, int NP>
+__device__ __forceinline__ void normalise(const JoinArgs& a, const JoinCols<MAP, NP>& c, float* scratch,
+                                          int& flip, F2 (&v)[NP], float& mean, float& r) {
   mean = 0.f;
   if constexpr (LAYER) {
-    float s[1] = {sum2(add2(add2(v[0], v[1]), add2(v[2], v[3])))};
+    F2 q = v[0];
+#pragma unroll
+    for (int k = 1; k < NP; ++k) q = add2(q, v[k]);
+    float s[1] = {sum2(q)};
     join_sums<QUADS>(s, scratch, flip, c.T);
     mean = s[0] * a.inv_h;
     const F2 m = f2(-mean);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = add2(v[k], m);
+    for (int k = 0; k < NP; ++k) v[k] = add2(v[k], m);
     if (c.ragged()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < NP; ++k) {
         float lo, hi;
         f2_out(v[k], lo, hi);
         v[k] = f2(c.has(2 * k) ? lo : 0.f, c.has(2 * k + 1) ? hi : 0.f);
@@ -391,92 +480,94 @@ __device__ __forceinline__ void normalise(const JoinArgs& a, const JoinCols<MAP>
     }
   }
   F2 q = mul2(v[0], v[0]), p = mul2(v[1], v[1]);
-  q = fma2(v[2], v[2], q), p = fma2(v[3], v[3], p);
+#pragma unroll
+  for (int k = 2; k < NP; k += 2) q = fma2(v[k], v[k], q), p = fma2(v[k + 1], v[k + 1], p);
   float s[1] = {sum2(add2(q, p))};
   join_sums<QUADS>(s, scratch, flip, c.T);
   r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
   const F2 rr = f2(r);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], rr);
+  for (int k = 0; k < NP; ++k) v[k] = mul2(v[k], rr);
 }
 
 // What both kernels set up.
-template <int MAP, bool MANY>
+template <int MAP, int NP, bool MANY>
 struct JoinCta {
   float* scratch;
   char *vec, *ring;
-  JoinCols<MAP> c;
-  int64_t first, step;  // rows: first + i * step, while the CTA has any
-  int group;            // this thread's row among the CTA's
+  JoinCols<MAP, NP> c;
+  int64_t first, step;  // rows: first + group + i * step, while first + i * step is one
   __device__ __forceinline__ JoinCta(const JoinArgs& a, const JoinLayout& l, char* smem) {
     scratch = reinterpret_cast<float*>(smem);
     vec = smem + kJoinScratch;
     ring = vec + l.vec_bytes;
     const int tid = static_cast<int>(threadIdx.x), n = static_cast<int>(blockDim.x);
     const int groups = MANY ? n / l.lanes : 1;
-    group = MANY ? tid / l.lanes : 0;
-    c.t = MANY ? tid % l.lanes : tid, c.T = MANY ? l.lanes : n, c.tid = tid, c.n = n, c.hidden = static_cast<int>(a.d.hidden);
+    c.group = MANY ? tid / l.lanes : 0;
+    c.t = MANY ? tid % l.lanes : tid, c.T = MANY ? l.lanes : n, c.tid = tid, c.n = n;
+    c.hidden = static_cast<int>(a.d.hidden);
     first = static_cast<int64_t>(blockIdx.x) * groups;
     step = static_cast<int64_t>(gridDim.x) * groups;
     // sums of warps the CTA lacks, and slots of columns a row lacks
     for (int i = tid; i < kJoinScratch / 4; i += n) scratch[i] = 0.f;
-    for (int i = tid; i < l.stages * l.stage_bytes / 16; i += n)
-      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (JoinCols<MAP, NP>::kWide)
+      for (int i = tid; i < l.stages * l.stage_bytes / 16; i += n)
+        reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
 };
 
-template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT>
-__global__ void __launch_bounds__(MAXT, kJoinThreadsForward / MAXT) k_join_rows(
+template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT, int NP>
+__global__ void __launch_bounds__(MAXT, NP == 4 ? kJoinThreadsForward / MAXT : 512 / MAXT) k_join_rows(
     const __grid_constant__ JoinArgs a, const __grid_constant__ JoinLayout l) {
   extern __shared__ __align__(16) char smem[];
   constexpr bool kMany = MAXT == kJoinSmallCta;  // several rows a CTA
   constexpr int kQuads = MAXT / 128;              // a row's warps in fours
-  JoinCta<MAP, kMany> cta(a, l, smem);
-  const JoinCols<MAP>& c = cta.c;
+  constexpr bool kWide = JoinCols<MAP, NP>::kWide;
+  JoinCta<MAP, NP, kMany> cta(a, l, smem);
+  const JoinCols<MAP, NP>& c = cta.c;
   int flip = 0, stage = 0;
-  for (int s = 0; s < l.stages; ++s)
-    fetch_row<A, R>(a, l, c, cta.ring, s, cta.first + cta.group + s * cta.step);
+  ring_start<A, R, OWN>(a, l, c, cta.ring, cta.first + c.group, cta.step);
   fold_vectors(a, l, c, cta.vec);
   for (int64_t base = cta.first; base < a.d.rows; base += cta.step) {
     // a group past the last row works on it once more and writes nothing
-    const int64_t r = kMany ? min(base + cta.group, a.d.rows - 1) : base;
-    const bool live = !kMany || base + cta.group < a.d.rows;
-    if constexpr (MAP != kAny) copies_wait(l.stages - 1);
+    const int64_t r = kMany ? min(base + c.group, a.d.rows - 1) : base;
+    const bool live = !kMany || base + c.group < a.d.rows;
+    ring_step<A, R, OWN, kMany>(a, l, c, cta.ring, stage, base + c.group, cta.step);
     const char* in = cta.ring + stage * l.stage_bytes;
-    F2 o[4];
+    F2 o[NP];
     float mb = 0.f, rb = 1.f, mo = 0.f, ro = 1.f;
-    row_input<R>(c, in, l.x, a.in.x, r, a.d.x_stride, o);
+    c.template read<R>(in + l.x, row_of<R>(a.in.x, r, a.d.x_stride), o);
     if (a.in.b) {
-      F2 v[4], y[4], w[4];
-      row_input<A>(c, in, l.b, a.in.b, r, a.d.b_stride, v);
+      F2 v[NP], y[NP], w[NP];
+      c.template read<A>(in + l.b, row_of<A>(a.in.b, r, a.d.b_stride), v);
       if (a.in.w_post) normalise<LAYER, kQuads>(a, c, cta.scratch, flip, v, mb, rb);
-      row_gate<OWN>(a, l, c, in, cta.vec, r, y, w);
+      row_gate<A, OWN>(a, l, c, in, cta.vec, r, y, w);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = fma2(w[k], v[k], o[k]);
+      for (int k = 0; k < NP; ++k) o[k] = fma2(w[k], v[k], o[k]);
       if (LAYER && l.b1 >= 0) {
         c.vector(cta.vec + l.b1, w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = OWN ? fma2(w[k], y[k], o[k]) : add2(w[k], o[k]);
+        for (int k = 0; k < NP; ++k) o[k] = OWN ? fma2(w[k], y[k], o[k]) : add2(w[k], o[k]);
       }
     }
     // this thread has read its slots of the stage: the row `stages` ahead
-    fetch_row<A, R>(a, l, c, cta.ring, stage, base + cta.group + l.stages * cta.step);
+    if constexpr (kWide) fetch_row<A, R, OWN>(a, l, c, cta.ring, stage, base + c.group + l.stages * cta.step);
     stage = stage + 1 == l.stages ? 0 : stage + 1;
     if (a.o && live) c.write(static_cast<R*>(a.o) + r * a.d.hidden, o);
     if (a.in.w_pre) {
       normalise<LAYER, kQuads>(a, c, cta.scratch, flip, o, mo, ro);
       if (a.n && live) {
-        F2 w[4];
+        F2 w[NP];
         c.vector(cta.vec + l.w2, w);
         if (LAYER && l.b2 >= 0) {
-          F2 d[4];
+          F2 d[NP];
           c.vector(cta.vec + l.b2, d);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = fma2(o[k], w[k], d[k]);
+          for (int k = 0; k < NP; ++k) o[k] = fma2(o[k], w[k], d[k]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = mul2(o[k], w[k]);
+          for (int k = 0; k < NP; ++k) o[k] = mul2(o[k], w[k]);
         }
         c.write(static_cast<A*>(a.n) + r * a.d.hidden, o);
       }
@@ -485,170 +576,165 @@ __global__ void __launch_bounds__(MAXT, kJoinThreadsForward / MAXT) k_join_rows(
   }
 }
 
-template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT>
+// Sum of e (layer only) and of e h over the row, over -hidden: what leaves
+// e's gradient through a norm of normalised row h.
+template <bool LAYER, int QUADS, int MAP, int NP>
+__device__ __forceinline__ void norm_means(const JoinArgs& a, const JoinCols<MAP, NP>& c, float* scratch,
+                                           int& flip, const F2 (&e)[NP], const F2 (&h)[NP], F2& s0, F2& s1) {
+  F2 p = mul2(e[0], h[0]), q = e[0];
+#pragma unroll
+  for (int k = 1; k < NP; ++k) {
+    if (LAYER) q = add2(q, e[k]);
+    p = fma2(e[k], h[k], p);
+  }
+  if constexpr (LAYER) {
+    float s[2] = {sum2(p), sum2(q)};
+    join_sums<QUADS>(s, scratch, flip, c.T);
+    s1 = f2(-s[0] * a.inv_h), s0 = f2(-s[1] * a.inv_h);
+  } else {
+    float s[1] = {sum2(p)};
+    join_sums<QUADS>(s, scratch, flip, c.T);
+    s1 = f2(-s[0] * a.inv_h);
+  }
+}
+
+template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT, int NP>
 __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_constant__ JoinArgs a,
                                                              const __grid_constant__ JoinLayout l) {
   extern __shared__ __align__(16) char smem[];
   constexpr bool kMany = MAXT == kJoinSmallCta;  // several rows a CTA
   constexpr int kQuads = MAXT / 128;              // a row's warps in fours
-  JoinCta<MAP, kMany> cta(a, l, smem);
-  const JoinCols<MAP>& c = cta.c;
+  constexpr bool kWide = JoinCols<MAP, NP>::kWide;
+  JoinCta<MAP, NP, kMany> cta(a, l, smem);
+  const JoinCols<MAP, NP>& c = cta.c;
   int flip = 0, stage = 0;
-  for (int s = 0; s < l.stages; ++s)
-    fetch_row<A, R>(a, l, c, cta.ring, s, cta.first + cta.group + s * cta.step);
+  ring_start<A, R, OWN>(a, l, c, cta.ring, cta.first + c.group, cta.step);
   fold_vectors(a, l, c, cta.vec);
   const bool gate_row = OWN && a.d.gate_kind == ZERO_GATE_ROW && a.dgate;
   const bool gate_full = OWN && a.d.gate_kind == ZERO_GATE_FULL && a.dgate;
-  F2 P[4], Q[4], S[4], B[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) P[k] = Q[k] = S[k] = B[k] = f2(0.f);
+  F2 P[NP], Q[NP], S[NP], B[NP];
+  clear(P), clear(Q), clear(S), clear(B);
   float4 st = make_float4(0.f, 1.f, 0.f, 1.f);
-  if (a.stats && cta.first < a.d.rows) st = __ldg(a.stats + min(cta.first + cta.group, a.d.rows - 1));
+  if (a.stats && cta.first < a.d.rows) st = __ldg(a.stats + min(cta.first + c.group, a.d.rows - 1));
   for (int64_t base = cta.first; base < a.d.rows; base += cta.step) {
-    const int64_t r = kMany ? min(base + cta.group, a.d.rows - 1) : base;
-    const bool live = !kMany || base + cta.group < a.d.rows;
+    const int64_t r = kMany ? min(base + c.group, a.d.rows - 1) : base;
+    const bool live = !kMany || base + c.group < a.d.rows;
     const float4 now = st;
     if (a.stats) st = __ldg(a.stats + min(r + cta.step, a.d.rows - 1));  // the next row's
-    if constexpr (MAP != kAny) copies_wait(l.stages - 1);
+    ring_step<A, R, OWN, kMany>(a, l, c, cta.ring, stage, base + c.group, cta.step);
     const char* in = cta.ring + stage * l.stage_bytes;
-    F2 go[4], bh[4], y[4], w1[4];
-    if (a.d_o) {
-      row_input<R>(c, in, l.d_o, a.d_o, r, a.d.do_stride, go);
-    } else {
-      go[0] = go[1] = go[2] = go[3] = f2(0.f);
-    }
+    F2 go[NP], bh[NP], y[NP];
+    if (a.d_o)
+      c.template read<R>(in + l.d_o, row_of<R>(a.d_o, r, a.d.do_stride), go);
+    else
+      clear(go);
     if (a.in.b) {
-      row_gate<OWN>(a, l, c, in, cta.vec, r, y, w1);
-      row_input<A>(c, in, l.b, a.in.b, r, a.d.b_stride, bh);
+      c.template read<A>(in + l.b, row_of<A>(a.in.b, r, a.d.b_stride), bh);
       if (a.in.w_post) {
         const F2 rr = f2(now.y), m = f2(-now.x);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) bh[k] = mul2(LAYER ? add2(bh[k], m) : bh[k], rr);
+        for (int k = 0; k < NP; ++k) bh[k] = mul2(LAYER ? add2(bh[k], m) : bh[k], rr);
       }
     }
+    F2 w1[NP];
+    if (a.in.b) row_gate<A, OWN>(a, l, c, in, cta.vec, r, y, w1);
     if (a.d_n) {
-      F2 oh[4], t[4], w[4];
-      row_input<R>(c, in, l.x, a.in.x, r, a.d.x_stride, oh);
-      row_input<A>(c, in, l.d_n, a.d_n, r, a.d.dn_stride, t);
+      F2 oh[NP], t[NP], w[NP];
+      c.template read<R>(in + l.x, row_of<R>(a.in.x, r, a.d.x_stride), oh);
+      c.template read<A>(in + l.d_n, row_of<A>(a.d_n, r, a.d.dn_stride), t);
       if (a.in.b) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) oh[k] = fma2(w1[k], bh[k], oh[k]);
+        for (int k = 0; k < NP; ++k) oh[k] = fma2(w1[k], bh[k], oh[k]);
         if (LAYER && l.b1 >= 0) {
           c.vector(cta.vec + l.b1, w);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) oh[k] = OWN ? fma2(w[k], y[k], oh[k]) : add2(w[k], oh[k]);
+          for (int k = 0; k < NP; ++k) oh[k] = OWN ? fma2(w[k], y[k], oh[k]) : add2(w[k], oh[k]);
         }
       }
       c.vector(cta.vec + l.w2, w);
       const F2 rr = f2(now.w), m = f2(-now.z);
-      F2 s0 = f2(0.f), s1 = f2(0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < NP; ++k) {
         oh[k] = mul2(LAYER ? add2(oh[k], m) : oh[k], rr);
         if (live) {
           P[k] = fma2(t[k], oh[k], P[k]);
           if (LAYER) Q[k] = add2(Q[k], t[k]);
         }
         t[k] = mul2(t[k], w[k]);  // zero past the row's end, as dn and w2 are
-        if (LAYER) s0 = add2(s0, t[k]);
-        s1 = fma2(t[k], oh[k], s1);
       }
-      if constexpr (LAYER) {
-        float s[2] = {sum2(s1), sum2(s0)};
-        join_sums<kQuads>(s, cta.scratch, flip, c.T);
-        s1 = f2(-s[0] * a.inv_h), s0 = f2(-s[1] * a.inv_h);
-      } else {
-        float s[1] = {sum2(s1)};
-        join_sums<kQuads>(s, cta.scratch, flip, c.T);
-        s1 = f2(-s[0] * a.inv_h);
-      }
+      F2 s0, s1;
+      norm_means<LAYER, kQuads>(a, c, cta.scratch, flip, t, oh, s0, s1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < NP; ++k) {
         F2 e = fma2(oh[k], s1, t[k]);
         if (LAYER) e = add2(e, s0);
         go[k] = fma2(e, rr, go[k]);
       }
     }
-    fetch_row<A, R>(a, l, c, cta.ring, stage, base + cta.group + l.stages * cta.step);
+    if constexpr (kWide) fetch_row<A, R, OWN>(a, l, c, cta.ring, stage, base + c.group + l.stages * cta.step);
     stage = stage + 1 == l.stages ? 0 : stage + 1;
     if (a.dx && live) c.write(static_cast<R*>(a.dx) + r * a.d.hidden, go);
     if (!a.in.b) continue;
     if (live) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < NP; ++k) {
         const F2 yg = OWN ? mul2(y[k], go[k]) : go[k];
         S[k] = fma2(yg, bh[k], S[k]);
         if (LAYER) B[k] = add2(B[k], yg);
       }
     }
-    float s2 = 0.f;
     if (gate_row || gate_full) {
-      F2 u[4], w[4], sum = f2(0.f);
+      F2 u[NP], w[NP], sum = f2(0.f);
       c.vector(cta.vec + l.w1, w);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) u[k] = mul2(w[k], bh[k]);
+      for (int k = 0; k < NP; ++k) u[k] = mul2(w[k], bh[k]);
       if (LAYER && l.b1 >= 0) {
         c.vector(cta.vec + l.b1, w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = add2(u[k], w[k]);
+        for (int k = 0; k < NP; ++k) u[k] = add2(u[k], w[k]);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < NP; ++k) {
         u[k] = mul2(u[k], go[k]);
         sum = add2(sum, u[k]);
       }
-      s2 = sum2(sum);
       if (gate_full && live) c.write_any(a.dgate, r * a.d.hidden, a.d.gate_dtype, u);
-    }
-    if (gate_row) {
-      float one[1] = {s2};
-      join_sums<kQuads>(one, cta.scratch, flip, c.T);
-      if (live && c.t == 0) store_any(a.dgate, r, a.d.gate_dtype, one[0]);
+      if (gate_row) {
+        float s[1] = {sum2(sum)};
+        join_sums<kQuads>(s, cta.scratch, flip, c.T);
+        if (live && c.t == 0) store_any(a.dgate, r, a.d.gate_dtype, s[0]);
+      }
     }
     if (!a.db) continue;
-    F2 q[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) q[k] = mul2(w1[k], go[k]);  // zero past the row's end, as w1 is
+    for (int k = 0; k < NP; ++k) go[k] = mul2(w1[k], go[k]);  // zero past the row's end, as w1 is
     if (a.in.w_post) {
-      F2 s0 = f2(0.f), s1 = f2(0.f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (LAYER) s0 = add2(s0, q[k]);
-        s1 = fma2(q[k], bh[k], s1);
-      }
-      if constexpr (LAYER) {
-        float s[2] = {sum2(s1), sum2(s0)};
-        join_sums<kQuads>(s, cta.scratch, flip, c.T);
-        s1 = f2(-s[0] * a.inv_h), s0 = f2(-s[1] * a.inv_h);
-      } else {
-        float s[1] = {sum2(s1)};
-        join_sums<kQuads>(s, cta.scratch, flip, c.T);
-        s1 = f2(-s[0] * a.inv_h);
-      }
+      F2 s0, s1;
+      norm_means<LAYER, kQuads>(a, c, cta.scratch, flip, go, bh, s0, s1);
       const F2 rr = f2(now.y);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        F2 e = fma2(bh[k], s1, q[k]);
+      for (int k = 0; k < NP; ++k) {
+        F2 e = fma2(bh[k], s1, go[k]);
         if (LAYER) e = add2(e, s0);
-        q[k] = mul2(e, rr);
+        go[k] = mul2(e, rr);
       }
     }
-    if (live) c.write(static_cast<A*>(a.db) + r * a.d.hidden, q);
+    if (live) c.write(static_cast<A*>(a.db) + r * a.d.hidden, go);
   }
+  copies_wait(0);
   if (a.n_sums == 0) return;
   float* mine = a.partial + static_cast<int64_t>(blockIdx.x) * a.n_sums * a.d.hidden;
   const int groups = kMany ? c.n / c.T : 1;
   char* hold = cta.vec;  // the CTA's rows are done: room for its groups' sums
-  if constexpr (MAP != kAny) copies_wait(0);
-  auto leave = [&](int which, F2 (&v)[4]) {
+  auto leave = [&](int which, F2 (&v)[NP]) {
     if (a.slot[which] < 0) return;
-    if (groups > 1) {  // the groups' sums in order
+    if constexpr (kMany) {  // the groups' sums in order
       __syncthreads();
-      for (int k = 0; k < 4; ++k) reinterpret_cast<uint64_t*>(hold)[k * c.n + c.tid] = v[k].w;
+      for (int k = 0; k < NP; ++k) reinterpret_cast<uint64_t*>(hold)[k * c.n + c.tid] = v[k].w;
       __syncthreads();
-      if (cta.group > 0) return;
+      if (c.group > 0) return;
       for (int g = 1; g < groups; ++g)
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < NP; ++k) {
           F2 e;
           e.w = reinterpret_cast<uint64_t*>(hold)[k * c.n + g * c.T + c.t];
           v[k] = add2(v[k], e);
@@ -667,13 +753,26 @@ __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_consta
 // ---------------------------------------------------------------------------
 // host: the layout and the launch of one type pair
 
-// Threads of a row, and of a CTA.
-inline int join_lanes(int64_t hidden) {
-  if (hidden <= 64) return 8;
-  if (hidden <= 128) return 16;
-  return static_cast<int>((hidden + 255) / 256 * 32);
+// Columns of a thread.  16 halve what a row costs beside its columns: taken
+// for rows of a warp or less (up to 512 channels then need no barrier), and
+// for the longer rows backward, where they leave 128 registers a thread.
+// Rows that start anywhere keep 8: their element accesses need the threads.
+inline int join_columns(int64_t hidden, bool wide, bool backward) {
+  return wide && (hidden <= 512 || (backward && hidden > kJoinNarrow)) ? 16 : 8;
 }
-inline int join_threads(int64_t hidden) { return std::max(hidden <= 256 ? kJoinSmallCta : 0, join_lanes(hidden)); }
+
+// Threads of a row, and of a CTA.
+inline int join_lanes(int64_t hidden, bool wide, bool backward) {
+  const int64_t warp = 32 * join_columns(hidden, wide, backward);
+  if (hidden * 8 <= warp) return 4;
+  if (hidden * 4 <= warp) return 8;
+  if (hidden * 2 <= warp) return 16;
+  return static_cast<int>((hidden + warp - 1) / warp * 32);
+}
+inline int join_threads(int64_t hidden, bool wide, bool backward) {
+  const int lanes = join_lanes(hidden, wide, backward);
+  return lanes <= 32 ? kJoinSmallCta : lanes;
+}
 
 inline bool join_row_fits(const void* p, int64_t stride, int type, bool oct) {
   if (!p) return true;
@@ -682,82 +781,80 @@ inline bool join_row_fits(const void* p, int64_t stride, int type, bool oct) {
   return aligned_to(p, unit) && stride * bytes % unit == 0;
 }
 
-// The column map these pointers and strides allow.
+// Whether pointers and strides allow whole 16-byte (kQuad: 8-byte) accesses.
 template <class A, class R>
-JoinMap join_map(const JoinArgs& a) {
+bool join_wide(const JoinArgs& a) {
   const zero_join_desc& d = a.d;
   const bool oct = sizeof(A) == 2 && sizeof(R) == 2;
-  if (d.hidden % (oct ? 8 : 4)) return kAny;
   const int64_t H = d.hidden;
+  if (H % (oct ? 8 : 4)) return false;
   auto ok = [&](const void* p, int64_t stride, int type) { return join_row_fits(p, stride, type, oct); };
-  const bool rows = ok(a.in.x, d.x_stride, d.res_dtype) && ok(a.in.b, d.b_stride, d.act_dtype) &&
-                    ok(a.d_o, d.do_stride, d.res_dtype) && ok(a.d_n, d.dn_stride, d.act_dtype) &&
-                    ok(a.o, H, d.res_dtype) && ok(a.n, H, d.act_dtype) && ok(a.dx, H, d.res_dtype) &&
-                    ok(a.db, H, d.act_dtype);
   const bool full = d.gate_kind == ZERO_GATE_FULL;
-  const bool gate = !full || (ok(a.in.gate, d.gate_stride, d.gate_dtype) && ok(a.dgate, H, d.gate_dtype));
-  const void* vectors[] = {a.in.w_post, a.in.bias_post, a.in.w_pre, a.in.bias_pre,
-                           d.gate_kind == ZERO_GATE_CHANNEL ? a.in.gate : nullptr};
-  bool vec = true;
-  for (const void* p : vectors) vec = vec && aligned_to(p, 16);
-  if (!rows || !gate || !vec) return kAny;
-  return oct ? kOct : kQuad;
+  return ok(a.in.x, d.x_stride, d.res_dtype) && ok(a.in.b, d.b_stride, d.act_dtype) &&
+         ok(a.d_o, d.do_stride, d.res_dtype) && ok(a.d_n, d.dn_stride, d.act_dtype) &&
+         ok(a.o, H, d.res_dtype) && ok(a.n, H, d.act_dtype) && ok(a.dx, H, d.res_dtype) &&
+         ok(a.db, H, d.act_dtype) &&
+         (!full || (ok(a.in.gate, d.gate_stride, d.gate_dtype) && ok(a.dgate, H, d.gate_dtype)));
 }
 
-inline JoinLayout join_layout(const JoinArgs& a, JoinMap map, bool backward, int ctas) {
+inline JoinLayout join_layout(const JoinArgs& a, bool wide, bool backward, int ctas) {
   JoinLayout l = {};
-  l.lanes = join_lanes(a.d.hidden);
-  const int T8 = join_threads(a.d.hidden) * 8;
+  const zero_join_desc& d = a.d;
+  l.lanes = join_lanes(d.hidden, wide, backward);
+  const int threads = join_threads(d.hidden, wide, backward), slots = threads * join_columns(d.hidden, wide, backward);
   auto vector = [&](bool present) {
     if (!present) return -1;
     const int at = l.vec_bytes;
-    l.vec_bytes += T8 * 4;
+    l.vec_bytes += slots * 4;
     return at;
   };
   l.w1 = vector(a.in.b != nullptr);
   l.b1 = vector(a.in.bias_post != nullptr);
   l.w2 = vector(backward ? a.d_n != nullptr : a.in.w_pre != nullptr);
   l.b2 = vector(!backward && a.in.bias_pre != nullptr);
-  if (backward && l.vec_bytes == 0) l.vec_bytes = T8 * 4;  // holds the groups' sums at the end
-  auto row = [&](const void* p, int type) {
-    if (!p || map == kAny) return -1;
-    const int at = l.stage_bytes;
-    l.stage_bytes += T8 * type_bytes(type);
+  if (backward && l.vec_bytes == 0) l.vec_bytes = slots * 4;  // holds the groups' sums at the end
+  auto row = [&](const void* p, int type, int64_t stride, const char** end) {
+    if (!p) return -1;
+    const int at = l.stage_bytes, bytes = type_bytes(type);
+    l.stage_bytes += wide ? slots * bytes
+                          : static_cast<int>((d.hidden * bytes + 15) / 16 * 16 + 16) * (threads / l.lanes);
+    *end = static_cast<const char*>(p) + ((d.rows - 1) * stride + d.hidden) * bytes;
     return at;
   };
-  l.x = row(a.in.x, a.d.res_dtype);
-  l.b = row(a.in.b, a.d.act_dtype);
-  l.d_o = row(a.d_o, a.d.res_dtype);
-  l.d_n = row(a.d_n, a.d.act_dtype);
-  l.gate = row(a.d.gate_kind == ZERO_GATE_FULL ? a.in.gate : nullptr, a.d.gate_dtype);
-  if (map != kAny) {
-    const int room = kJoinSmemMost / ctas - 1024 - kJoinScratch - l.vec_bytes;
-    l.stages = std::max(0, std::min(kJoinStagesMost, room / l.stage_bytes));
-  }
+  l.x = row(a.in.x, d.res_dtype, d.x_stride, &l.x_end);
+  l.b = row(a.in.b, d.act_dtype, d.b_stride, &l.b_end);
+  l.d_o = row(a.d_o, d.res_dtype, d.do_stride, &l.do_end);
+  l.d_n = row(a.d_n, d.act_dtype, d.dn_stride, &l.dn_end);
+  l.gate = row(d.gate_kind == ZERO_GATE_FULL ? a.in.gate : nullptr, d.gate_dtype, d.gate_stride, &l.gate_end);
+  const int room = kJoinSmemMost / ctas - 1024 - kJoinScratch - l.vec_bytes;
+  l.stages = std::max(0, std::min(kJoinStagesMost, room / l.stage_bytes));
   return l;
 }
 
 inline int join_smem(const JoinLayout& l) { return kJoinScratch + l.vec_bytes + l.stages * l.stage_bytes; }
 
-template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT>
-int launch_join_rows_as(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
-  const void* fn = backward ? reinterpret_cast<const void*>(&k_join_rows_backward<A, R, LAYER, OWN, MAP, MAXT>)
-                            : reinterpret_cast<const void*>(&k_join_rows<A, R, LAYER, OWN, MAP, MAXT>);
-  const int threads = join_threads(a.d.hidden), groups = threads / join_lanes(a.d.hidden);
-  int fit = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, 0);
-  if (e != cudaSuccess) return static_cast<int>(e);
-  // what the registers let run at once
-  int ctas = std::max(1, std::min(fit, (backward ? kJoinThreadsBackward : kJoinThreadsForward) / threads));
-  JoinLayout l = join_layout(a, static_cast<JoinMap>(MAP), backward, ctas);
-  // two rows ahead before one more CTA
-  while (ctas > 1 && ((MAP != kAny && l.stages < 2) || join_smem(l) > kJoinSmemMost / ctas - 1024)) {
-    --ctas;
-    l = join_layout(a, static_cast<JoinMap>(MAP), backward, ctas);
+// fn: the kernel, of at most MAXT threads a CTA; known: its CTAs of an SM by
+// registers, asked once a CTA size (devices of one kind answer the same).
+template <int MAXT>
+int launch_join_rows_fn(const void* fn, std::atomic<int>* known, const JoinArgs& a, bool wide, bool backward,
+                        int* workers, cudaStream_t s) {
+  const int threads = join_threads(a.d.hidden, wide, backward);
+  const int groups = threads / join_lanes(a.d.hidden, wide, backward);
+  int fit = known[threads / 32].load(std::memory_order_relaxed);
+  if (fit == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, 0);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    fit = std::max(1, fit);
+    known[threads / 32].store(fit, std::memory_order_relaxed);
   }
-  if ((MAP != kAny && l.stages < 1) || join_smem(l) > kJoinSmemMost) return -1;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmemMost);
-  if (e != cudaSuccess) return static_cast<int>(e);
+  int ctas = std::max(1, std::min(fit, (backward ? kJoinThreadsBackward : kJoinThreadsForward) / threads));
+  JoinLayout l = join_layout(a, wide, backward, ctas);
+  while (ctas > 1 && l.stages < 2) l = join_layout(a, wide, backward, --ctas);  // a row ahead before one more CTA
+  if (l.stages < 1) return -1;
+  if (join_smem(l) > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmemMost);
+    if (e != cudaSuccess) return static_cast<int>(e);
+  }
   const int64_t work = (a.d.rows + groups - 1) / groups;
   const int grid = static_cast<int>(std::min<int64_t>(work, static_cast<int64_t>(ctas) * kSMs));
   *workers = grid;
@@ -766,23 +863,43 @@ int launch_join_rows_as(const JoinArgs& a, bool backward, int* workers, cudaStre
   return static_cast<int>(cudaLaunchKernel(fn, dim3(grid), dim3(threads), args, join_smem(l), s));
 }
 
+template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT, int NP>
+int launch_join_rows_as(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
+  static std::atomic<int> known[2][MAXT / 32 + 1];
+  constexpr bool wide = JoinCols<MAP, NP>::kWide;
+  if (backward) {
+    // wide backward rows above 4096 have 16 columns a thread: 512 threads
+    constexpr int kMost = wide && MAXT > 512 ? 512 : MAXT;
+    return launch_join_rows_fn<kMost>(
+        reinterpret_cast<const void*>(&k_join_rows_backward<A, R, LAYER, OWN, MAP, kMost, NP>), known[1], a, wide,
+        true, workers, s);
+  }
+  return launch_join_rows_fn<MAXT>(reinterpret_cast<const void*>(&k_join_rows<A, R, LAYER, OWN, MAP, MAXT, NP>),
+                                   known[0], a, wide, false, workers, s);
+}
+
 template <class A, class R, bool LAYER, bool OWN, int MAP>
 int launch_join_rows_map(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
-  if (a.d.hidden <= 256)
-    return launch_join_rows_as<A, R, LAYER, OWN, MAP, kJoinSmallCta>(a, backward, workers, s);
-  // up to 512 threads a CTA leave 128 registers a thread, 1024 leave 64
-  if (join_threads(a.d.hidden) <= 512)
-    return launch_join_rows_as<A, R, LAYER, OWN, MAP, 512>(a, backward, workers, s);
-  return launch_join_rows_as<A, R, LAYER, OWN, MAP, 1024>(a, backward, workers, s);
+  constexpr bool wide = JoinCols<MAP, 4>::kWide;
+  if (join_lanes(a.d.hidden, wide, backward) <= 32)
+    return launch_join_rows_as<A, R, LAYER, OWN, MAP, kJoinSmallCta, wide ? 8 : 4>(a, backward, workers, s);
+  if constexpr (wide)
+    if (backward && join_columns(a.d.hidden, true, true) == 16) {
+      static std::atomic<int> known[17];
+      return launch_join_rows_fn<512>(
+          reinterpret_cast<const void*>(&k_join_rows_backward<A, R, LAYER, OWN, MAP, 512, 8>), known, a, true, true,
+          workers, s);
+    }
+  if (join_threads(a.d.hidden, wide, backward) <= 512)
+    return launch_join_rows_as<A, R, LAYER, OWN, MAP, 512, 4>(a, backward, workers, s);
+  return launch_join_rows_as<A, R, LAYER, OWN, MAP, 1024, 4>(a, backward, workers, s);
 }
 
 template <class A, class R, bool LAYER, bool OWN>
 int launch_join_rows_kind(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
-  constexpr int kWide = sizeof(A) == 2 && sizeof(R) == 2 ? kOct : kQuad;
-  int e = -1;
-  if (join_map<A, R>(a) != kAny) e = launch_join_rows_map<A, R, LAYER, OWN, kWide>(a, backward, workers, s);
-  if (e == -1) e = launch_join_rows_map<A, R, LAYER, OWN, kAny>(a, backward, workers, s);
-  return e;
+  constexpr bool k16 = sizeof(A) == 2 && sizeof(R) == 2;
+  if (join_wide<A, R>(a)) return launch_join_rows_map<A, R, LAYER, OWN, k16 ? kOct : kQuad>(a, backward, workers, s);
+  return launch_join_rows_map<A, R, LAYER, OWN, k16 ? kPair : kLone>(a, backward, workers, s);
 }
 
 // -1: these rows do not fit here.

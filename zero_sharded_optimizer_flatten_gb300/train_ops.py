@@ -12,11 +12,11 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-from typing import Optional
 
 import torch
 
-from .zero import _addr, _check, _stream, lib
+from .zero import _check, lib
+from .zero import _stream as _any_stream
 
 ZERO_FP32 = 2
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: ZERO_FP32}
@@ -38,23 +38,37 @@ def _choice(table, value, what: str) -> int:
     return table[value]
 
 
-def _on(t, what: str, device=None):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, device: int):
+    """Handle of the given stream, or of the device's current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _any_stream(stream)
+
+
+def _on(t, what: str, device: int):
+    """A CUDA tensor on device `device`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: tensor must be on a CUDA device")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
     return t
 
 
-def _current(t, what: str):
-    """The tensor's device, which has to be the current one (launches go there)."""
-    _on(t, what)
-    if t.device.index != torch.cuda.current_device():
+def _current(t, what: str) -> int:
+    """Index of the tensor's device, which has to be the current one (launches
+    go there)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{what}: tensor must be on a CUDA device")
+    if device != torch.cuda.current_device():
         raise ValueError(f"{what}: on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return t.device
+    return device
 
 
 def _keep_for(stream, *tensors):
@@ -67,12 +81,21 @@ def _keep_for(stream, *tensors):
             t.record_stream(s)
 
 
-def _result(t, what: str, shape, dtype, device):
-    """A caller's output tensor, checked, or a new one."""
+def _new(like):
+    """A new contiguous tensor of `like`'s shape and type."""
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
+def _result(t, what: str, like, shape, dtype):
+    """A caller's output tensor, checked, or a new one beside `like`."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _on(t, what, device)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        if like.shape == shape and like.dtype == dtype:
+            return _new(like)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _on(t, what, like.get_device())
+    if t.dtype != dtype or t.shape != torch.Size(shape) or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
 
@@ -143,7 +166,7 @@ def zero_grad_norm_workspace_bytes(grads) -> int:
     return need.value
 
 
-def _workspace(t, need: int, device):
+def _workspace(t, need: int, device: int):
     """A caller's workspace, checked, or a new one."""
     if t is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
@@ -177,9 +200,9 @@ class GradNorm:
             e.src_dtype, e.numel = _grad_tensor(g, what), g.numel()
             e.src = g.data_ptr() if g.numel() else None
             if g.is_cuda:
-                device = device or _current(g, what)
-                if g.device != device:
-                    raise ValueError(f"{what}: on {g.device}, expected {device}")
+                if device is None:
+                    device = _current(g, what)
+                _on(g, what, device)
             if out is None:
                 continue
             d = out[k]
@@ -188,8 +211,8 @@ class GradNorm:
                 if d.shape != g.shape or (d.stride() != g.stride() and not
                                           (d.is_contiguous() and g.is_contiguous())):
                     raise ValueError(f"out[{k}]: shape and order must be those of grads[{k}]")
-                if d.is_cuda and device is not None and d.device != device:
-                    raise ValueError(f"out[{k}]: on {d.device}, expected {device}")
+                if d.is_cuda and device is not None:
+                    _on(d, f"out[{k}]", device)
             e.dst_dtype = _type(d, f"out[{k}]")
             e.dst = d.data_ptr() if d.numel() else None
             if g.numel():
@@ -197,16 +220,19 @@ class GradNorm:
                 if e.dst != e.src:
                     spans.append((e.src, e.src + g.numel() * g.element_size(), False))
         _check_disjoint(spans)
-        device = device or torch.device("cuda", torch.cuda.current_device())
+        if device is None:
+            device = torch.cuda.current_device()
         need = ctypes.c_int64()
         _check(lib().zero_grad_norm_workspace_bytes(self._list, self.n, ctypes.byref(need)))
         self.result = torch.empty(NORM_RESULT_BYTES, dtype=torch.uint8, device=device)
         self._workspace = _workspace(workspace, need.value, device)
         self._norm = self.result[8:12].view(torch.float32)[0]
         self._args = (self.result.data_ptr(), self._workspace.data_ptr(), need.value)
+        self.device = device
 
     def __call__(self, stream=None):
-        _check(lib().zero_grad_norm(self._list, self.n, self.kind, *self._args, _stream(stream)))
+        _check(lib().zero_grad_norm(self._list, self.n, self.kind, *self._args,
+                                    _stream(stream, self.device)))
         return self._norm
 
     def read(self) -> NormResult:
@@ -234,7 +260,7 @@ class ClipGradNorm(GradNorm):
 
     def __call__(self, stream=None):
         _check(lib().zero_clip_grad_norm(self._list, self.n, self.kind, self.max_norm,
-                                         *self._args, _stream(stream)))
+                                         *self._args, _stream(stream, self.device)))
         return self._norm
 
 
@@ -275,18 +301,16 @@ class JoinGradsC(ctypes.Structure):
                                                "dw_pre", "dbias_pre")]
 
 
-_PARAMS = ("w_post", "bias_post", "w_pre", "bias_pre")
-
-
-def _row_stride(t, what: str, shape, device) -> int:
+def _row_stride(t, what: str, shape, device: int) -> int:
     """Elements between rows of a tensor [..., hidden] whose rows are
     contiguous and evenly spaced."""
-    _on(t, what, device)
+    if t.get_device() != device:
+        _on(t, what, device)
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    hidden = shape[-1]
     if t.is_contiguous():
-        return hidden
+        return shape[-1]
+    hidden = shape[-1]
     if t.stride(-1) == 1 or hidden == 1:
         if t.dim() == 2:
             return t.stride(0)
@@ -297,63 +321,76 @@ def _row_stride(t, what: str, shape, device) -> int:
     raise ValueError(f"{what}: rows must be contiguous and evenly spaced (use .contiguous())")
 
 
-def _join_args(x, b, gate, params, kind, scale, eps, act):
-    """(desc, inputs, device, act dtype) of a join's arguments."""
+def _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind, scale, eps, act,
+               d_o=None, d_n=None):
+    """(desc, inputs, device, act dtype, hidden) of a join's arguments."""
     device = _current(x, "x")
-    if x.dim() < 1:
-        raise ValueError("x: expected [..., hidden]")
     shape = x.shape
-    d, p = JoinDescC(), JoinInputsC()
+    if not shape:
+        raise ValueError("x: expected [..., hidden]")
     hidden = shape[-1]
-    d.hidden = hidden
-    d.rows = x.numel() // hidden if hidden else 0
-    d.res_dtype = _type(x, "x")
-    d.x_stride = _row_stride(x, "x", shape, device)
-    p.x = x.data_ptr()
+    x_stride = _row_stride(x, "x", shape, device)
+    b_stride = gate_stride = do_stride = dn_stride = 0
+    p_b = p_gate = None
     if b is not None:
         act = b.dtype
-        d.b_stride = _row_stride(b, "b", shape, device)
-        p.b = b.data_ptr()
+        b_stride = _row_stride(b, "b", shape, device)
+        p_b = b.data_ptr()
     elif act is None:
-        w = params[2]
-        act = w.dtype if x.dtype == torch.float32 and w is not None else x.dtype
-    code = _TYPES.get(act)
-    if code is None:
+        act = w_pre.dtype if x.dtype == torch.float32 and w_pre is not None else x.dtype
+    act_code = _TYPES.get(act)
+    if act_code is None:
         raise TypeError(f"b: expected float16, bfloat16 or float32, got {act}")
-    d.act_dtype = d.param_dtype = d.gate_dtype = code
-    first = None
-    for name, t in zip(_PARAMS, params):
+    param = None
+    for name, t in (("w_post", w_post), ("bias_post", bias_post), ("w_pre", w_pre),
+                    ("bias_pre", bias_pre)):
         if t is None:
             continue
-        _on(t, name, device)
+        if t.get_device() != device:
+            _on(t, name, device)
         if t.dim() != 1 or t.shape[0] != hidden or not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous vector of {hidden}")
-        if first is None:
-            first = t.dtype
-            d.param_dtype = _type(t, name)
-        elif t.dtype != first:
-            raise TypeError(f"{name}: {t.dtype}, but another parameter is {first}")
-        setattr(p, name, t.data_ptr())
+        if param is None:
+            param = t.dtype
+        elif t.dtype != param:
+            raise TypeError(f"{name}: {t.dtype}, but another parameter is {param}")
+    param_code = act_code if param is None else _TYPES.get(param)
+    if param_code is None:
+        raise TypeError(f"parameters: expected float16, bfloat16 or float32, got {param}")
+    gate_kind, gate_code = GATE_NONE, act_code
     if gate is not None:
         _on(gate, "gate", device)
-        d.gate_dtype = _type(gate, "gate")
-        if gate.dim() == 1 and gate.shape[0] == hidden and x.dim() != 1:
+        gate_code = _type(gate, "gate")
+        if gate.dim() == 1 and gate.shape[0] == hidden and len(shape) != 1:
             if not gate.is_contiguous():
                 raise ValueError("gate: expected a contiguous vector")
-            d.gate_kind = GATE_CHANNEL
+            gate_kind = GATE_CHANNEL
         elif gate.shape == shape:
-            d.gate_kind = GATE_FULL
-            d.gate_stride = _row_stride(gate, "gate", shape, device)
+            gate_kind = GATE_FULL
+            gate_stride = _row_stride(gate, "gate", shape, device)
         elif gate.shape == shape[:-1] + (1,):
-            d.gate_kind = GATE_ROW
-            d.gate_stride = _row_stride(gate, "gate", gate.shape, device)
+            gate_kind = GATE_ROW
+            gate_stride = _row_stride(gate, "gate", gate.shape, device)
         else:
             raise ValueError(f"gate: shape {tuple(gate.shape)}, expected ({hidden},), "
                              f"{tuple(shape[:-1]) + (1,)} or {tuple(shape)}")
-        p.gate = gate.data_ptr()
-    d.kind = _choice(_KINDS, kind, "kind")
-    d.eps, d.scale = eps, scale
-    return d, p, device, act
+        p_gate = gate.data_ptr()
+    if d_o is not None:
+        if d_o.dtype != x.dtype:
+            raise TypeError(f"d_o: expected {x.dtype}, got {d_o.dtype}")
+        do_stride = _row_stride(d_o, "d_o", shape, device)
+    if d_n is not None:
+        if d_n.dtype != act:
+            raise TypeError(f"d_n: expected {act}, got {d_n.dtype}")
+        dn_stride = _row_stride(d_n, "d_n", shape, device)
+    d = JoinDescC(x.numel() // hidden if hidden else 0, hidden, act_code, _type(x, "x"),
+                  param_code, gate_code, _choice(_KINDS, kind, "kind"), gate_kind, eps, scale,
+                  x_stride, b_stride, gate_stride, do_stride, dn_stride)
+    p = JoinInputsC(x.data_ptr(), p_b, p_gate, None if w_post is None else w_post.data_ptr(),
+                    None if bias_post is None else bias_post.data_ptr(),
+                    None if w_pre is None else w_pre.data_ptr(),
+                    None if bias_pre is None else bias_pre.data_ptr())
+    return d, p, device, act, hidden
 
 
 def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_pre=None,
@@ -364,30 +401,42 @@ def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_
     without w_pre no n (None); b None takes the norm of x alone, and o is x.
     x, b, gate: [..., hidden]; the gate also [hidden] or [..., 1].  stats is
     what the backward call takes (None unless want_stats)."""
-    d, p, device, act = _join_args(x, b, gate, (w_post, bias_post, w_pre, bias_pre), kind, scale,
-                                   eps, None if n is None else n.dtype)
-    kept_o, kept_n = o, n
-    if b is None and o is None:
-        want_o = False
-    o = _result(o, "o", x.shape, x.dtype, device) if want_o else None
+    d, p, device, act, hidden = _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind,
+                                           scale, eps, None if n is None else n.dtype)
     if n is not None and w_pre is None:
         raise ValueError("n: needs w_pre")
-    n = _result(n, "n", x.shape, act, device) if w_pre is not None else None
-    stats = torch.empty(d.rows, 4, dtype=torch.float32, device=device) if want_stats else None
+    if b is None and o is None:
+        want_o = False
+    given_o, given_n = o, n
+    p_o = p_n = p_stats = stats = None
+    if want_o:
+        o = _result(o, "o", x, x.shape, x.dtype)
+        p_o = o.data_ptr()
+    if w_pre is not None:
+        n = _result(n, "n", x, x.shape, act)
+        p_n = n.data_ptr()
+    if want_stats:
+        stats = torch.empty((d.rows, 4), dtype=torch.float32, device=x.device)
+        p_stats = stats.data_ptr()
     if stream is not None:
-        _keep_for(stream, o if kept_o is None else None, n if kept_n is None else None, stats)
-    _check(lib().zero_block_join(ctypes.byref(d), ctypes.byref(p),
-                                 None if o is None else o.data_ptr(),
-                                 None if n is None else n.data_ptr(),
-                                 None if stats is None else stats.data_ptr(), _stream(stream)))
-    return x if b is None and o is None else o, n, stats
+        _keep_for(stream, o if given_o is None and want_o else None,
+                  n if given_n is None else None, stats)
+    _check(lib().zero_block_join(ctypes.byref(d), ctypes.byref(p), p_o, p_n, p_stats,
+                                 _stream(stream, device)))
+    if not want_o:
+        o = x if b is None else None
+    return o, n, stats
 
 
 def zero_block_join_workspace_bytes(x, b=None, *, w_post=None, bias_post=None, w_pre=None,
                                     bias_pre=None, gate=None, kind: str = "rms",
                                     scale: float = 1.0, eps: float = 1e-6) -> int:
     """Device workspace of zero_block_join_backward for these arguments."""
-    d = _join_args(x, b, gate, (w_post, bias_post, w_pre, bias_pre), kind, scale, eps, None)[0]
+    d = _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind, scale, eps, None)[0]
+    return _join_need(d)
+
+
+def _join_need(d) -> int:
     need = ctypes.c_int64()
     _check(lib().zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
     return need.value
@@ -401,46 +450,41 @@ def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=No
     dbias_post, dw_pre and dbias_pre, None for what has no input or is not in
     `want` (a set of those names; None: all).  workspace: device scratch of
     zero_block_join_workspace_bytes (None: allocated here)."""
-    params = (w_post, bias_post, w_pre, bias_pre)
-    act = None if d_n is None else d_n.dtype
-    d, p, device, act = _join_args(x, b, gate, params, kind, scale, eps, act)
-    if d_o is not None:
-        if d_o.dtype != x.dtype:
-            raise TypeError(f"d_o: expected {x.dtype}, got {d_o.dtype}")
-        d.do_stride = _row_stride(d_o, "d_o", x.shape, device)
-    if d_n is not None:
-        if d_n.dtype != act:
-            raise TypeError(f"d_n: expected {act}, got {d_n.dtype}")
-        d.dn_stride = _row_stride(d_n, "d_n", x.shape, device)
+    d, p, device, act, hidden = _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind,
+                                           scale, eps, None if d_n is None else d_n.dtype, d_o,
+                                           d_n)
+    p_stats = None
     if stats is not None:
-        _result(stats, "stats", (d.rows, 4), torch.float32, device)
+        p_stats = _result(stats, "stats", x, (d.rows, 4), torch.float32).data_ptr()
     out = {"dx": x, "db": b, "dgate": gate, "dw_post": w_post, "dbias_post": bias_post,
            "dw_pre": w_pre, "dbias_pre": bias_pre}
-    g = JoinGradsC()
-    sums = d.gate_kind == GATE_CHANNEL
+    at = []
+    sums = unused = False
     for name, like in out.items():
         if like is None or (want is not None and name not in want):
             out[name] = None
-            continue
-        if d_n is None and name in ("dw_pre", "dbias_pre"):
-            out[name] = t = torch.zeros_like(like)  # n was not used
-            _keep_for(stream, t)
-            continue
-        out[name] = t = torch.empty(like.shape, dtype=like.dtype, device=device)
-        setattr(g, name, t.data_ptr())
-        sums = sums or like.dim() == 1
-        _keep_for(stream, t)
-    need = ctypes.c_int64()
-    ws = None
+            at.append(None)
+        elif d_n is None and name in ("dw_pre", "dbias_pre"):
+            out[name] = torch.zeros_like(like)  # n was not used
+            at.append(None)
+            unused = True
+        else:
+            out[name] = t = _new(like)
+            at.append(t.data_ptr())
+            sums = sums or (like is not x and like is not b and like.dim() == 1)
+    p_ws, need, ws = None, 0, None
     if sums:
-        _check(lib().zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
-        ws = _workspace(workspace, need.value, device)
-        _keep_for(stream, ws if workspace is None else None)
-    if any(getattr(g, name) for name in out):
-        _check(lib().zero_block_join_backward(
-            ctypes.byref(d), ctypes.byref(p), None if d_o is None else d_o.data_ptr(),
-            None if d_n is None else d_n.data_ptr(), None if stats is None else stats.data_ptr(),
-            ctypes.byref(g), None if ws is None else ws.data_ptr(), need.value, _stream(stream)))
+        need = _join_need(d)
+        ws = _workspace(workspace, need, device)
+        p_ws = ws.data_ptr()
+    if stream is not None:
+        _keep_for(stream, *out.values(), ws if workspace is None else None)
+    if unused and not any(at):
+        return out
+    _check(lib().zero_block_join_backward(
+        ctypes.byref(d), ctypes.byref(p), None if d_o is None else d_o.data_ptr(),
+        None if d_n is None else d_n.data_ptr(), p_stats, ctypes.byref(JoinGradsC(*at)), p_ws,
+        need, _stream(stream, device)))
     return out
 
 
@@ -513,38 +557,42 @@ def zero_expert_sort(ids, n_experts: int, stream=None) -> ExpertOrder:
     tokens, topk = ids.shape
     if topk < 1:
         raise ValueError("ids: topk must be at least 1")
-    offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=device)
-    rows = torch.empty(tokens, topk, dtype=torch.int32, device=device)
-    pairs = torch.empty(tokens * topk, dtype=torch.int32, device=device)
+    where = ids.device
+    offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=where)
+    rows = torch.empty(ids.shape, dtype=torch.int32, device=where)
+    pairs = torch.empty(tokens * topk, dtype=torch.int32, device=where)
     _keep_for(stream, offsets, rows, pairs)
     _check(lib().zero_expert_sort(ids.data_ptr() or None, ids.element_size(), tokens, topk,
                                   n_experts, offsets.data_ptr(), rows.data_ptr() or None,
-                                  pairs.data_ptr() or None, _stream(stream)))
+                                  pairs.data_ptr() or None, _stream(stream, device)))
     return ExpertOrder(offsets, rows, pairs, n_experts, tokens, topk)
 
 
 def _sorted_rows(t, what: str, order: ExpertOrder):
-    _current(t, what)
-    _on(order.rows, "order", t.device)
+    """(device, type, hidden) of a tensor [tokens * topk, hidden]."""
+    device = _current(t, what)
+    if order.rows.get_device() != device:
+        _on(order.rows, "order", device)
     if t.dim() != 2 or t.shape[0] != order.tokens * order.topk or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous [{order.tokens * order.topk}, hidden] "
                          "tensor")
-    return _type(t, what)
+    return device, _type(t, what), t.shape[1]
 
 
-def _token_rows(t, what: str, order: ExpertOrder, hidden=None):
-    """(type, row stride) of a tensor [tokens, hidden]."""
-    _current(t, what)
-    _on(order.rows, "order", t.device)
-    if t.dim() != 2 or t.shape[0] != order.tokens or (hidden is not None and t.shape[1] != hidden):
-        raise ValueError(f"{what}: expected [{order.tokens}, {hidden or 'hidden'}], got "
-                         f"{tuple(t.shape)}")
-    return _type(t, what), _row_stride(t, what, t.shape, t.device)
+def _token_rows(t, what: str, order: ExpertOrder):
+    """(device, type, hidden, row stride) of a tensor [tokens, hidden]."""
+    device = _current(t, what)
+    if order.rows.get_device() != device:
+        _on(order.rows, "order", device)
+    if t.dim() != 2 or t.shape[0] != order.tokens:
+        raise ValueError(f"{what}: expected [{order.tokens}, hidden], got {tuple(t.shape)}")
+    return device, _type(t, what), t.shape[1], _row_stride(t, what, t.shape, device)
 
 
-def _expert_weights(weights, order: ExpertOrder, device):
-    _on(weights, "weights", device)
-    if tuple(weights.shape) != (order.tokens, order.topk) or not weights.is_contiguous():
+def _expert_weights(weights, order: ExpertOrder, device: int):
+    if weights.get_device() != device:
+        _on(weights, "weights", device)
+    if weights.shape != order.rows.shape or not weights.is_contiguous():
         raise ValueError(f"weights: expected a contiguous [{order.tokens}, {order.topk}] tensor")
     return _type(weights, "weights")
 
@@ -552,58 +600,56 @@ def _expert_weights(weights, order: ExpertOrder, device):
 def zero_expert_dispatch(x, order: ExpertOrder, out=None, stream=None):
     """Tokens copied to their rows in expert order, [tokens * topk, hidden];
     the rows past the last kept choice are zero."""
-    code, stride = _token_rows(x, "x", order)
-    hidden = x.shape[1]
-    xs = _result(out, "out", (order.tokens * order.topk, hidden), x.dtype, x.device)
+    device, code, hidden, stride = _token_rows(x, "x", order)
+    xs = _result(out, "out", x, (order.tokens * order.topk, hidden), x.dtype)
     _keep_for(stream, xs if out is None else None)
     _check(lib().zero_expert_dispatch(x.data_ptr(), stride, code, order.tokens, order.topk, hidden,
                                       order.offsets.data_ptr(), order.n_experts,
-                                      order.rows.data_ptr(), xs.data_ptr(), _stream(stream)))
+                                      order.rows.data_ptr(), xs.data_ptr(),
+                                      _stream(stream, device)))
     return xs
 
 
 def zero_expert_dispatch_backward(dxs, order: ExpertOrder, out=None, stream=None):
     """Each token's gradient: the sum of its rows'."""
-    code = _sorted_rows(dxs, "dxs", order)
-    hidden = dxs.shape[1]
-    dx = _result(out, "out", (order.tokens, hidden), dxs.dtype, dxs.device)
+    device, code, hidden = _sorted_rows(dxs, "dxs", order)
+    dx = _result(out, "out", dxs, (order.tokens, hidden), dxs.dtype)
     _keep_for(stream, dx if out is None else None)
     _check(lib().zero_expert_dispatch_backward(dxs.data_ptr(), code, order.tokens, order.topk,
                                                hidden, order.rows.data_ptr(), dx.data_ptr(),
-                                               _stream(stream)))
+                                               _stream(stream, device)))
     return dx
 
 
 def zero_expert_combine(ys, weights, order: ExpertOrder, out=None, stream=None):
     """Each token's weighted sum of its rows; zero when all its choices were
     dropped."""
-    code = _sorted_rows(ys, "ys", order)
-    hidden = ys.shape[1]
-    wcode = _expert_weights(weights, order, ys.device)
-    y = _result(out, "out", (order.tokens, hidden), ys.dtype, ys.device)
+    device, code, hidden = _sorted_rows(ys, "ys", order)
+    wcode = _expert_weights(weights, order, device)
+    y = _result(out, "out", ys, (order.tokens, hidden), ys.dtype)
     _keep_for(stream, y if out is None else None)
     _check(lib().zero_expert_combine(ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
                                      order.topk, hidden, order.rows.data_ptr(), y.data_ptr(),
-                                     _stream(stream)))
+                                     _stream(stream, device)))
     return y
 
 
 def zero_expert_combine_backward(dy, ys, weights, order: ExpertOrder, want_weights: bool = True,
                                  stream=None):
     """(dys, dweights) of zero_expert_combine; dweights None unless wanted."""
-    code = _sorted_rows(ys, "ys", order)
-    hidden = ys.shape[1]
-    dcode, stride = _token_rows(dy, "dy", order, hidden)
-    if dcode != code:
-        raise TypeError(f"dy: expected {ys.dtype}, got {dy.dtype}")
-    wcode = _expert_weights(weights, order, ys.device)
-    dys = torch.empty_like(ys)
-    dweights = torch.empty_like(weights) if want_weights else None
+    device, code, hidden = _sorted_rows(ys, "ys", order)
+    _, dcode, dhidden, stride = _token_rows(dy, "dy", order)
+    if dcode != code or dhidden != hidden:
+        raise TypeError(f"dy: expected {ys.dtype} rows of {hidden}, got {dy.dtype} of {dhidden}")
+    wcode = _expert_weights(weights, order, device)
+    dys = _new(ys)
+    dweights = _new(weights) if want_weights else None
     _keep_for(stream, dys, dweights)
     _check(lib().zero_expert_combine_backward(
         dy.data_ptr(), stride, ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
         order.topk, hidden, order.offsets.data_ptr(), order.n_experts, order.rows.data_ptr(),
-        dys.data_ptr(), None if dweights is None else dweights.data_ptr(), _stream(stream)))
+        dys.data_ptr(), None if dweights is None else dweights.data_ptr(),
+        _stream(stream, device)))
     return dys, dweights
 
 
