@@ -578,13 +578,13 @@ zero_status zero_step_amp_noalloc(const zero_plan* plan, const void* const* grad
  * step, gradients accumulated in fp32, parameters outside the plan):
  *   norm = sqrt(sum of g^2) over all elements of all tensors (ZERO_NORM_L2),
  *          or max |g| (ZERO_NORM_INF);
- *   coef = min(1, max_norm / (norm + 1e-6)), formed in binary64, rounded once
- *          to binary32; 1 when the norm is not finite;
+ *   coef = min(1, max_norm / (norm + 1e-6)), formed in binary32; 1 when the
+ *          norm is not finite;
  *   dst[i] = src[i] * coef, the product in binary32, rounded once to dst.
  * A non-finite norm (an infinity or NaN anywhere) is flagged in the record
  * and scales nothing, so that the caller can skip the step as zero_step_amp
  * does.  No finite gradients make the norm infinite (squares are summed in
- * two exactly scaled ranges); values below 2^-103 may count as zero in it.
+ * two exactly scaled ranges); values below 2^-83 may count as zero in it.
  * Sums run in a fixed order: the same call gives the same bits.  Nothing is
  * read back by the host.
  */

@@ -9,13 +9,14 @@
 // reads them again and writes them; nothing can be written before the last
 // element is read.
 //
-// Work split: a tensor is cut into tiles of 4096 elements, a CTA takes a
-// contiguous run of tiles (of any tensors) and leaves one binary64 partial,
+// Work split.  A tensor is cut into tiles of 4096 elements, a CTA takes a
+// contiguous run of tiles (of any tensors) and leaves one partial,
 // so the partials are few (at most kGrid a launch) and every CTA of the
 // clipping adds them up itself, in the same fixed order: no kernel between
-// the two passes, no atomics, the same norm in every run.  The clipping walks
-// the tiles from the last to the first, so what the norm read last is still
-// in L2.
+// the two passes, no atomics, the same norm in every run.  A thread has four
+// octets (16 or 32 bytes each) in flight.  The clipping walks the tiles from
+// the last to the first, so what the norm read last is still in L2, and it is
+// launched early (its CTAs wait for the norm's on the device).
 #include <cuda_runtime.h>
 #include <inttypes.h>
 #include <math.h>
@@ -30,20 +31,25 @@
 namespace zero {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 128;
 constexpr int kNormTile = 4096;                        // elements a CTA takes at once
-constexpr int kTileOctets = kNormTile / 8;             // 512: two octets a thread
-constexpr int kGrid = 8 * kSMs;                        // CTAs of one launch at most
+constexpr int kTileOctets = kNormTile / 8;             // 512
+constexpr int kAhead = kTileOctets / kNormThreads;     // octets of a thread in flight: 4
+constexpr int kNormCtas = 8;                           // of an SM, at least
+constexpr int kGrid = 16 * kSMs;                       // CTAs of one launch at most
 constexpr int kJobsMost = 1000;                        // tensors of one launch at most
 
-// One tensor.  head: elements before the first 16-byte boundary of src (they
-// go one by one, as do the elements after the last whole octet).
+struct Partial;
+
+// One tensor.  Octets start at element `head` for the norm (a 16-byte boundary
+// of src), `dst_head` for the clipping (one of dst); the elements before it
+// and after the last whole octet go one by one.
 struct GradJob {
   const void* src;
   void* dst;
   int64_t numel;
   int32_t tile_begin;
-  uint8_t src_type, dst_type, head, vec_store;
+  uint8_t src_type, dst_type, head, dst_head;
 };
 static_assert(sizeof(GradJob) == 32, "job table entries");
 
@@ -51,9 +57,9 @@ static_assert(sizeof(GradJob) == 32, "job table entries");
 // needs no device memory; three sizes, as a launch's cost grows with them.
 template <int CAP>
 struct GradArgs {
-  double* partials;       // of every launch of the call
+  Partial* partials;  // of every launch of the call
   zero_norm_result* result;
-  double max_norm;
+  float max_norm;         // negative: no factor is wanted
   int32_t n_partials;     // of every launch of the call
   int32_t partial_base;   // this launch's first partial
   int32_t n_jobs, n_tiles;
@@ -61,13 +67,18 @@ struct GradArgs {
   GradJob jobs[CAP];
 };
 
-// Squares of binary32 values without overflow or underflow that could show:
-// |g| < 2^20 goes to a as (2^40 g)^2, the rest to b as (2^-68 g)^2.  Both
-// scalings are exact; 64 squares of either range stay finite, values down to
-// 2^-103 keep normal squares, an infinity or NaN makes its sum non-finite.
-// fp16 values never leave the first range.
+// Sums of squares of binary32 values without overflow or underflow that could
+// show: |g| < 2^20 goes to a as (2^20 g)^2 < 2^80, the rest to b as
+// (2^-84 g)^2 < 2^88.  Both scalings are exact; no number of squares that fits
+// the device overflows, values down to 2^-83 keep normal squares, an infinity
+// or NaN makes its sum non-finite.  fp16 values never leave the first range.
+// binary64 would need no ranges, but its units are few here: with binary64
+// sums in every thread the norm of 101M bf16 values took 75 us in place of 40.
+constexpr float kMidScale = 0x1p20f, kBigFrom = 0x1p20f, kBigScale = 0x1p-84f;
+
 struct Squares {
-  float a[2], b;
+  F2 a[2];
+  float b;
 };
 
 template <class T>
@@ -76,23 +87,48 @@ __device__ __forceinline__ void add_squares(Squares& s, const float (&v)[8]) {
     float m = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
-    if (!(m < 0x1p20f)) {
-#pragma unroll 1
+    if (!(m < kBigFrom)) {
+#pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (fabsf(v[k]) < 0x1p20f)
-          s.a[0] = fmaf(v[k] * 0x1p40f, v[k] * 0x1p40f, s.a[0]);
+        const bool big = !(fabsf(v[k]) < kBigFrom);
+        const float w = v[k] * (big ? kBigScale : kMidScale);
+        if (big)
+          s.b = fmaf(w, w, s.b);
         else
-          s.b = fmaf(v[k] * 0x1p-68f, v[k] * 0x1p-68f, s.b);
+          s.a[k & 1] = fma2(f2(w, 0.f), f2(w, 0.f), s.a[k & 1]);
       }
       return;
     }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float w = v[k] * 0x1p40f;
-    s.a[k & 1] = fmaf(w, w, s.a[k & 1]);
+  for (int k = 0; k < 4; ++k) {
+    const F2 w = mul2(f2(v[2 * k], v[2 * k + 1]), f2(kMidScale));
+    s.a[k & 1] = fma2(w, w, s.a[k & 1]);
   }
 }
+
+// A sum held as two binary32 numbers (about 48 bits); sums of long chains of
+// parts are kept this way.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair pair_add(Pair x, Pair y) {
+  const float s = x.hi + y.hi;
+  const float t = s - x.hi;
+  const float e = (x.hi - (s - t)) + (y.hi - t) + (x.lo + y.lo);
+  // an infinity or NaN stays what it is
+  if (!(fabsf(s) < INFINITY)) return {s, 0.f};
+  const float hi = s + e;
+  return {hi, e - (hi - s)};
+}
+__device__ __forceinline__ Pair pair_xor(Pair x, int o) {
+  return {__shfl_xor_sync(kFull, x.hi, o), __shfl_xor_sync(kFull, x.lo, o)};
+}
+
+// What a CTA leaves: its sums, or the largest |g| as a's hi.
+struct alignas(16) Partial {
+  Pair a, b;
+};
 
 // The bits of |g| order as unsigned integers, NaN above infinity.
 __device__ __forceinline__ void add_max(uint32_t& m, const float (&v)[8]) {
@@ -100,25 +136,31 @@ __device__ __forceinline__ void add_max(uint32_t& m, const float (&v)[8]) {
   for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
 }
 
-__device__ __forceinline__ double nan_max(double x, double y) {
-  return x != x || y != y ? x + y : fmax(x, y);
+__device__ __forceinline__ float bits_max(float x, float y) {  // of magnitudes, NaN above all
+  return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
 }
 
-// The CTA's sum (or maximum) of one binary64 value a thread, in a fixed
-// order; the same value in every thread.
-__device__ __forceinline__ double block_join(double x, bool inf_norm, double* part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double y = __shfl_xor_sync(kFull, x, o);
-    x = inf_norm ? nan_max(x, y) : x + y;
+__device__ __forceinline__ Partial join(Partial x, const Partial& y, bool inf_norm) {
+  if (inf_norm) {
+    x.a.hi = bits_max(x.a.hi, y.a.hi);
+  } else {
+    x.a = pair_add(x.a, y.a);
+    x.b = pair_add(x.b, y.b);
   }
+  return x;
+}
+
+// The CTA's partial from its threads', in a fixed order; the same in every thread.
+__device__ __forceinline__ Partial block_join(Partial x, bool inf_norm, Partial* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = join(x, Partial{pair_xor(x.a, o), pair_xor(x.b, o)}, inf_norm);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
   __syncthreads();
-  double t = part[0];
+  x = part[0];
 #pragma unroll
-  for (int w = 1; w < kNormThreads / 32; ++w) t = inf_norm ? nan_max(t, part[w]) : t + part[w];
+  for (int w = 1; w < kNormThreads / 32; ++w) x = join(x, part[w], inf_norm);
   __syncthreads();
-  return t;
+  return x;
 }
 
 template <int CAP>
@@ -134,53 +176,144 @@ __device__ __forceinline__ int find_grad_job(const GradArgs<CAP>& a, int tile) {
   return lo;
 }
 
-// Elements [e0, e0 + cnt) of a tensor, zero elsewhere.
+// An octet as it was loaded: whole 16-byte chunks, widened when it is used,
+// so that the loads of a thread's octets go out together.
 template <class T>
-__device__ __forceinline__ void load_octet(const T* src, int64_t e0, int cnt, float (&v)[8]) {
-  if (cnt == 8) {
-    Elem<T>::load8(src + e0, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < cnt ? Elem<T>::widen(src[e0 + k]) : 0.f;
+struct Octet {
+  static constexpr int kChunks = sizeof(T) == 4 ? 2 : 1;
+  uint4 w[kChunks];
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(w[0].x), v[1] = __uint_as_float(w[0].y);
+      v[2] = __uint_as_float(w[0].z), v[3] = __uint_as_float(w[0].w);
+      v[4] = __uint_as_float(w[1].x), v[5] = __uint_as_float(w[1].y);
+      v[6] = __uint_as_float(w[1].z), v[7] = __uint_as_float(w[1].w);
+    } else {
+      Elem<T>::unpack(w[0].x, v[0], v[1]), Elem<T>::unpack(w[0].y, v[2], v[3]);
+      Elem<T>::unpack(w[0].z, v[4], v[5]), Elem<T>::unpack(w[0].w, v[6], v[7]);
+    }
   }
+  __device__ __forceinline__ void load(const T* p) {  // 16-byte aligned
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
+  }
+  // From an address that is not: the covering chunks, shifted by whole words
+  // and, for 16-bit elements, by half a word.  All chunks lie in the tensor.
+  __device__ __forceinline__ void load_shifted(const T* p) {
+    const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - skip);
+    uint32_t x[4 * kChunks + 5];
+#pragma unroll
+    for (int k = 0; k <= kChunks; ++k) {
+      const uint4 c = __ldg(q + k);
+      x[4 * k] = c.x, x[4 * k + 1] = c.y, x[4 * k + 2] = c.z, x[4 * k + 3] = c.w;
+    }
+    x[4 * kChunks + 4] = 0;
+    uint32_t y[4 * kChunks + 1];
+#pragma unroll
+    for (int k = 0; k <= 4 * kChunks; ++k) {  // a word more than the octet's, for the half shift
+      const uint32_t lo = skip & 4 ? x[k + 1] : x[k];
+      const uint32_t hi = k + 3 < 4 * kChunks + 5 ? (skip & 4 ? x[k + 3] : x[k + 2]) : 0;
+      y[k] = skip & 8 ? hi : lo;
+    }
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < 4 * kChunks; ++k) y[k] = __funnelshift_r(y[k], y[k + 1], 8 * (skip & 2));
+    }
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+      w[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+  }
+};
+
+// Elements [e0, e0 + cnt) of a tensor, one by one, zero elsewhere.
+template <class T>
+__device__ __forceinline__ void load_some(const T* src, int e0, int cnt, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = k < cnt ? Elem<T>::widen(src[e0 + k]) : 0.f;
 }
 
-// Calls body(e0, cnt) for the thread's octets of tile `t` of a tensor: whole
-// octets start at element `head`; the elements before it are an octet of
-// their own, of the first tile's thread 0.
-template <class Body>
-__device__ __forceinline__ void for_octets(const GradJob& j, int t, Body body) {
-  if (t == 0 && threadIdx.x == 0 && j.head)
-    body(static_cast<int64_t>(0), static_cast<int>(min(static_cast<int64_t>(j.head), j.numel)));
-#pragma unroll
-  for (int k = 0; k < kTileOctets / kNormThreads; ++k) {
-    const int64_t e0 = j.head + (static_cast<int64_t>(t) * kTileOctets + k * kNormThreads + threadIdx.x) * 8;
-    if (e0 < j.numel) body(e0, static_cast<int>(min(static_cast<int64_t>(8), j.numel - e0)));
+// A tile of a tensor in its own elements: octets lie at 8 * thread + 1024 k,
+// elements [0, left) exist.  The tile of element 0 has `before` elements in
+// front, down to the tensor's start.
+struct Tile {
+  int64_t base;
+  int left, before;
+  __device__ __forceinline__ Tile(const GradJob& j, int head, int t) {
+    base = head + static_cast<int64_t>(t) * kNormTile;
+    left = static_cast<int>(max(static_cast<int64_t>(-1), min(j.numel - base, static_cast<int64_t>(kNormTile + 64))));
+    before = t == 0 ? static_cast<int>(min(static_cast<int64_t>(head), j.numel)) : kNormTile;
+  }
+  static __device__ __forceinline__ int at(int k) { return (k * kNormThreads + static_cast<int>(threadIdx.x)) * 8; }
+};
+
+// The octets of a tile that is not whole, one after the other: octet(e) for a
+// whole one, some(e, cnt) for single elements, e relative to the tile.
+// good(e): the octet at e may be taken whole.
+template <class Good, class One, class Some>
+__device__ __forceinline__ void part_of_tile(const Tile& tile, int t, Good good, One octet, Some some) {
+  if (t == 0 && threadIdx.x == 0 && tile.before > 0) some(-static_cast<int>(tile.base), tile.before);
+#pragma unroll 1
+  for (int e = Tile::at(0); e < min(tile.left, kNormTile); e += kNormThreads * 8) {
+    if (good(e))
+      octet(e);
+    else
+      some(e, min(8, tile.left - e));
   }
 }
 
 template <class T>
 __device__ __forceinline__ void norm_tile(const GradJob& j, int t, bool inf_norm, Squares& s, uint32_t& m) {
-  const T* src = static_cast<const T*>(j.src);
-  for_octets(j, t, [&](int64_t e0, int cnt) {
-    float v[8];
-    load_octet(src, e0, cnt, v);
+  const Tile tile(j, j.head, t);
+  const T* src = static_cast<const T*>(j.src) + tile.base;
+  auto take = [&](const float (&v)[8]) {
     if (inf_norm)
       add_max(m, v);
     else
       add_squares<T>(s, v);
-  });
+  };
+  if (tile.left >= kNormTile && (t > 0 || j.head == 0)) {
+    Octet<T> o[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) o[k].load(src + Tile::at(k));
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      float v[8];
+      o[k].widen(v);
+      take(v);
+    }
+    return;
+  }
+  part_of_tile(
+      tile, t, [&](int e) { return e + 8 <= tile.left; },
+      [&](int e) {
+        Octet<T> o;
+        o.load(src + e);
+        float v[8];
+        o.widen(v);
+        take(v);
+      },
+      [&](int e, int cnt) {
+        float v[8];
+        load_some(src, e, cnt, v);
+        take(v);
+      });
 }
 
+// The launch that follows may start its CTAs; they wait for this grid's end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int CAP>
-__global__ void __launch_bounds__(kNormThreads) k_grad_norm(const __grid_constant__ GradArgs<CAP> a) {
-  __shared__ double part[kNormThreads / 32];
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_norm(const __grid_constant__ GradArgs<CAP> a) {
+  __shared__ Partial part[kNormThreads / 32];
+  let_next_start();
   const int lo = static_cast<int>(static_cast<int64_t>(a.n_tiles) * blockIdx.x / gridDim.x);
   const int hi = static_cast<int>(static_cast<int64_t>(a.n_tiles) * (blockIdx.x + 1) / gridDim.x);
   const bool inf_norm = a.inf_norm != 0;
-  double sum = 0.0;
+  Partial sum = {{0.f, 0.f}, {0.f, 0.f}};
+  Squares s = {{f2(0.f), f2(0.f)}, 0.f};
   uint32_t m = 0;
-  Squares s = {{0.f, 0.f}, 0.f};
   int held = 0;
   int q = find_grad_job(a, lo);
   for (int tile = lo; tile < hi; ++tile) {
@@ -193,44 +326,59 @@ __global__ void __launch_bounds__(kNormThreads) k_grad_norm(const __grid_constan
       norm_tile<__nv_bfloat16>(j, t, inf_norm, s, m);
     else
       norm_tile<__half>(j, t, inf_norm, s, m);
-    // at most 3 tiles of up to 17..24 squares in binary32 before they join
-    // the binary64 sum (head octets included: 3 * 24 = 72 squares over three
-    // accumulators, none above 64)
-    if (++held == 3 || tile + 1 == hi) {
-      sum += static_cast<double>(s.a[0] + s.a[1]) * 0x1p-80;
-      if (s.b != 0.f) sum += static_cast<double>(s.b) * 0x1p136;
-      s = {{0.f, 0.f}, 0.f};
+    // two tiles are at most 2 * 39 squares in binary32 before they join a pair
+    if (++held == 2 || tile + 1 == hi) {
+      sum.a = pair_add(sum.a, {sum2(add2(s.a[0], s.a[1])), 0.f});
+      if (s.b != 0.f) sum.b = pair_add(sum.b, {s.b, 0.f});
+      s = {{f2(0.f), f2(0.f)}, 0.f};
       held = 0;
     }
   }
-  if (inf_norm) sum = static_cast<double>(__uint_as_float(m));
+  if (inf_norm) sum.a.hi = __uint_as_float(m);
   sum = block_join(sum, inf_norm, part);
   if (threadIdx.x == 0) a.partials[a.partial_base + blockIdx.x] = sum;
 }
 
-// The norm from every partial of the call, the same in every CTA, and the
-// factor; the leader's first CTA writes the record.
+// The factor from every partial of the call, the same in every CTA, in
+// binary32; the leader's first CTA writes the record.
 template <int CAP>
-__device__ __forceinline__ float decide(const GradArgs<CAP>& a, double* part) {
+__device__ __forceinline__ float decide(const GradArgs<CAP>& a, Partial* part) {
   const bool inf_norm = a.inf_norm != 0;
-  double x = 0.0;
-  for (int p = threadIdx.x; p < a.n_partials; p += kNormThreads) {
-    const double y = __ldcg(a.partials + p);
-    x = inf_norm ? nan_max(x, y) : x + y;
+  wait_for_previous();
+  Partial x = {{0.f, 0.f}, {0.f, 0.f}};
+  for (int p = threadIdx.x; p < a.n_partials; p += 4 * kNormThreads) {
+    float4 y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      y[k] = p + k * kNormThreads < a.n_partials
+                 ? __ldcg(reinterpret_cast<const float4*>(a.partials) + p + k * kNormThreads)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x = join(x, Partial{{y[k].x, y[k].y}, {y[k].z, y[k].w}}, inf_norm);
   }
   x = block_join(x, inf_norm, part);
-  const double norm = inf_norm ? x : sqrt(x);
-  const bool fine = isfinite(norm);
-  double c = 1.0;
-  if (fine && a.max_norm >= 0.0) {
-    const double f = a.max_norm / (norm + 1e-6);
-    if (f < 1.0) c = f;
+  // the norm times `unit`, which keeps it in range: the sum of two ranges'
+  // squares is that of the larger one's, the other's scaled to it
+  float norm, unit = 1.f;
+  if (inf_norm) {
+    norm = x.a.hi;
+  } else if (x.b.hi == 0.f) {
+    norm = sqrtf(x.a.hi) * 0x1p-20f;
+  } else {
+    norm = sqrtf(x.b.hi + x.a.hi * 0x1p-104f * 0x1p-104f) * 0x1p20f;
+    unit = 0x1p-64f;
   }
-  const float coef = static_cast<float>(c);
+  const bool fine = norm < INFINITY;
+  float coef = 1.f;
+  if (fine && a.max_norm >= 0.f) coef = fminf(1.f, a.max_norm * unit / (norm + 1e-6f * unit));
   if (a.leader && blockIdx.x == 0 && threadIdx.x == 0) {
     zero_norm_result r = {};
-    r.norm = norm;
-    r.norm32 = static_cast<float>(norm);
+    if (inf_norm)
+      r.norm = x.a.hi;
+    else
+      r.norm = sqrt((static_cast<double>(x.a.hi) + x.a.lo) * 0x1p-40 +
+                    (static_cast<double>(x.b.hi) + x.b.lo) * 0x1p168);
+    r.norm32 = static_cast<float>(r.norm);
     r.coef = coef;
     r.nonfinite = fine ? 0 : 1;
     *a.result = r;
@@ -240,28 +388,74 @@ __device__ __forceinline__ float decide(const GradArgs<CAP>& a, double* part) {
 
 template <int CAP>
 __global__ void __launch_bounds__(kNormThreads) k_norm_result(const __grid_constant__ GradArgs<CAP> a) {
-  __shared__ double part[kNormThreads / 32];
+  __shared__ Partial part[kNormThreads / 32];
   decide(a, part);
+}
+
+// An octet to a 16-byte boundary, not kept in L2: nothing here reads it.
+template <class D>
+__device__ __forceinline__ void store_octet(D* p, const float (&v)[8]) {
+  if constexpr (sizeof(D) == 4) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+  } else {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(Elem<D>::pack(v[0], v[1]), Elem<D>::pack(v[2], v[3]),
+                                                   Elem<D>::pack(v[4], v[5]), Elem<D>::pack(v[6], v[7])));
+  }
 }
 
 template <class S, class D>
 __device__ __forceinline__ void clip_tile(const GradJob& j, int t, float coef) {
-  const S* src = static_cast<const S*>(j.src);
-  D* dst = static_cast<D*>(j.dst);
-  const bool vec = j.vec_store != 0;
-  for_octets(j, t, [&](int64_t e0, int cnt) {
+  const Tile tile(j, j.dst_head, t);
+  const S* src = static_cast<const S*>(j.src) + tile.base;
+  D* dst = static_cast<D*>(j.dst) + tile.base;
+  // octets lie on dst's boundaries; src's then lie there too or all off by as
+  // much, and the chunks of those at either end of the tensor reach past it
+  const bool straight = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  auto scaled = [&](const Octet<S>& o, int e) {
     float v[8];
-    load_octet(src, e0, cnt, v);
+    o.widen(v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= coef;
-    if (cnt == 8 && vec) {
-      Elem<D>::store8(dst + e0, v);
+    for (int i = 0; i < 8; ++i) v[i] *= coef;
+    store_octet(dst + e, v);
+  };
+  if (tile.left >= kNormTile + 16 && t > 0) {
+    if (straight) {
+      Octet<S> o[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) o[k].load(src + Tile::at(k));
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) scaled(o[k], Tile::at(k));
     } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < cnt) dst[e0 + k] = Elem<D>::narrow(v[k]);
+#pragma unroll 1
+      for (int k = 0; k < kAhead; k += 2) {
+        Octet<S> o[2];
+        o[0].load_shifted(src + Tile::at(k));
+        o[1].load_shifted(src + Tile::at(k + 1));
+        scaled(o[0], Tile::at(k));
+        scaled(o[1], Tile::at(k + 1));
+      }
     }
-  });
+    return;
+  }
+  part_of_tile(
+      tile, t,
+      [&](int e) { return straight ? e + 8 <= tile.left : e + tile.before >= 8 && e + 16 <= tile.left; },
+      [&](int e) {
+        Octet<S> o;
+        if (straight)
+          o.load(src + e);
+        else
+          o.load_shifted(src + e);
+        scaled(o, e);
+      },
+      [&](int e, int cnt) {
+        float v[8];
+        load_some(src, e, cnt, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < cnt) dst[e + k] = Elem<D>::narrow(v[k] * coef);
+      });
 }
 
 template <class S>
@@ -275,8 +469,8 @@ __device__ __forceinline__ void clip_tile_to(const GradJob& j, int t, float coef
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kNormThreads) k_grad_clip(const __grid_constant__ GradArgs<CAP> a) {
-  __shared__ double part[kNormThreads / 32];
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_clip(const __grid_constant__ GradArgs<CAP> a) {
+  __shared__ Partial part[kNormThreads / 32];
   const float coef = decide(a, part);
   const int lo = static_cast<int>(static_cast<int64_t>(a.n_tiles) * blockIdx.x / gridDim.x);
   const int hi = static_cast<int>(static_cast<int64_t>(a.n_tiles) * (blockIdx.x + 1) / gridDim.x);
@@ -309,7 +503,7 @@ struct Call {
   double max_norm = -1.0;
   bool inf_norm = false;
   zero_norm_result* result = nullptr;
-  double* partials = nullptr;
+  Partial* partials = nullptr;
   int n_partials = 0;
   cudaStream_t stream = nullptr;
 };
@@ -317,12 +511,12 @@ struct Call {
 enum class Pass { kNorm, kClip, kResult };
 
 template <int CAP>
-int launch_pass(const Call& c, const Batch* b, int base, bool leader, Pass pass) {
+int launch_pass(const Call& c, const Batch* b, int base, bool leader, bool early, Pass pass) {
   auto* a = new (std::nothrow) GradArgs<CAP>();
   if (!a) return static_cast<int>(cudaErrorMemoryAllocation);
   a->partials = c.partials;
   a->result = c.result;
-  a->max_norm = c.max_norm;
+  a->max_norm = static_cast<float>(c.max_norm);
   a->n_partials = c.n_partials;
   a->partial_base = base;
   a->inf_norm = c.inf_norm;
@@ -338,17 +532,33 @@ int launch_pass(const Call& c, const Batch* b, int base, bool leader, Pass pass)
   const void* fn = pass == Pass::kNorm   ? reinterpret_cast<const void*>(&k_grad_norm<CAP>)
                    : pass == Pass::kClip ? reinterpret_cast<const void*>(&k_grad_clip<CAP>)
                                          : reinterpret_cast<const void*>(&k_norm_result<CAP>);
-  const cudaError_t e = cudaLaunchKernel(fn, dim3(grid), dim3(kNormThreads), args, 0, c.stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kNormThreads);
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[1];
+  if (early) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
   delete a;
   if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
   return static_cast<int>(e);
 }
 
-int launch_sized(const Call& c, const Batch* b, int base, bool leader, Pass pass) {
+int launch_sized(const Call& c, const Batch* b, int base, bool leader, bool early, Pass pass) {
   const size_t n = b ? b->jobs.size() : 0;
-  if (n <= 64) return launch_pass<64>(c, b, base, leader, pass);
-  if (n <= 256) return launch_pass<256>(c, b, base, leader, pass);
-  return launch_pass<kJobsMost>(c, b, base, leader, pass);
+  if (n <= 64) return launch_pass<64>(c, b, base, leader, early, pass);
+  if (n <= 256) return launch_pass<256>(c, b, base, leader, early, pass);
+  return launch_pass<kJobsMost>(c, b, base, leader, early, pass);
+}
+
+// Elements before the first 16-byte boundary.
+int head_of(const void* p, int type) {
+  return static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16) / type_bytes(type);
 }
 
 int64_t tiles_of(const zero_grad_tensor& t, int head) {
@@ -384,7 +594,7 @@ zero_status check_list(const char* fn, const zero_grad_tensor* t, int32_t n, boo
 int64_t workspace_bytes(const zero_grad_tensor* t, int32_t n) {
   int64_t kept = 0;
   for (int32_t k = 0; k < n; ++k) kept += t[k].numel > 0;
-  return std::max<int64_t>(1, (kept + kJobsMost - 1) / kJobsMost) * kGrid * static_cast<int64_t>(sizeof(double));
+  return std::max<int64_t>(1, (kept + kJobsMost - 1) / kJobsMost) * kGrid * static_cast<int64_t>(sizeof(Partial));
 }
 
 zero_status norm_call(const char* fn, const zero_grad_tensor* t, int32_t n, int32_t kind, bool clip,
@@ -413,15 +623,13 @@ zero_status norm_call(const char* fn, const zero_grad_tensor* t, int32_t n, int3
   c.max_norm = clip ? max_norm : -1.0;
   c.inf_norm = kind == ZERO_NORM_INF;
   c.result = static_cast<zero_norm_result*>(d_result);
-  c.partials = static_cast<double*>(workspace);
+  c.partials = static_cast<Partial*>(workspace);
   c.stream = static_cast<cudaStream_t>(stream);
   try {
     for (int32_t k = 0; k < n; ++k) {
       if (t[k].numel == 0) continue;
       if (c.batches.empty() || c.batches.back().jobs.size() == kJobsMost) c.batches.emplace_back();
       Batch& b = c.batches.back();
-      const int sb = type_bytes(t[k].src_dtype);
-      const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(t[k].src) & 15)) % 16) / sb;
       GradJob j = {};
       j.src = t[k].src;
       j.dst = clip ? t[k].dst : nullptr;
@@ -429,10 +637,11 @@ zero_status norm_call(const char* fn, const zero_grad_tensor* t, int32_t n, int3
       j.tile_begin = static_cast<int32_t>(b.tiles);
       j.src_type = static_cast<uint8_t>(t[k].src_dtype);
       j.dst_type = static_cast<uint8_t>(clip ? t[k].dst_dtype : t[k].src_dtype);
+      const int head = head_of(j.src, j.src_type), dst_head = clip ? head_of(j.dst, j.dst_type) : head;
       j.head = static_cast<uint8_t>(head);
-      j.vec_store = clip && aligned_to(static_cast<char*>(t[k].dst) + head * type_bytes(t[k].dst_dtype), 16);
+      j.dst_head = static_cast<uint8_t>(dst_head);
       b.jobs.push_back(j);
-      b.tiles += tiles_of(t[k], head);
+      b.tiles += tiles_of(t[k], std::min(head, dst_head));  // enough for either pass
       if (b.tiles > INT32_MAX / 2)
         return fail(ZERO_ERR_INVALID, "%s: the tensors hold too many elements for one call", fn);
     }
@@ -442,14 +651,18 @@ zero_status norm_call(const char* fn, const zero_grad_tensor* t, int32_t n, int3
   for (const Batch& b : c.batches) c.n_partials += b.grid();
   int e = 0, base = 0;
   for (const Batch& b : c.batches) {
-    if (!e) e = launch_sized(c, &b, base, false, Pass::kNorm);
+    if (!e) e = launch_sized(c, &b, base, false, false, Pass::kNorm);
     base += b.grid();
   }
+  // The first launch after the norm's starts early: it waits for them on the
+  // device.  (A further launch of the clipping is an ordinary one.)
+  const bool one = !c.batches.empty();
   if (!clip || c.batches.empty()) {
-    if (!e) e = launch_sized(c, nullptr, 0, true, Pass::kResult);
+    if (!e) e = launch_sized(c, nullptr, 0, true, one, Pass::kResult);
   } else {
-    for (size_t k = c.batches.size(); k-- > 0;)
-      if (!e) e = launch_sized(c, &c.batches[k], 0, k == 0, Pass::kClip);
+    const size_t last = c.batches.size() - 1;
+    for (size_t k = last + 1; k-- > 0;)
+      if (!e) e = launch_sized(c, &c.batches[k], 0, k == last, k == last, Pass::kClip);
   }
   if (e)
     return fail(ZERO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(static_cast<cudaError_t>(e)));

@@ -63,40 +63,6 @@ struct JoinLayout {
   const char *x_end, *b_end, *do_end, *dn_end, *gate_end;
 };
 
-// Two binary32 values that go through one instruction.
-struct F2 {
-  uint64_t w;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.w) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
-__device__ __forceinline__ void f2_out(F2 a, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.w));
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.w) : "l"(a.w), "l"(b.w), "l"(c.w));
-  return r;
-}
-__device__ __forceinline__ float sum2(F2 a) {
-  float lo, hi;
-  f2_out(a, lo, hi);
-  return lo + hi;
-}
-
 __device__ __forceinline__ uint32_t smem_of(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -121,6 +121,40 @@ __device__ __forceinline__ void store8_any(void* p, int64_t i, int type, const f
 
 __host__ __device__ __forceinline__ int type_bytes(int type) { return type == ZERO_FP32 ? 4 : 2; }
 
+// Two binary32 values that go through one instruction.
+struct F2 {
+  uint64_t w;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.w) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
+__device__ __forceinline__ void f2_out(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.w));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.w) : "l"(a.w), "l"(b.w), "l"(c.w));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  float lo, hi;
+  f2_out(a, lo, hi);
+  return lo + hi;
+}
+
 // Sum over the warp, the same value in every lane (a fixed butterfly).
 template <class V>
 __device__ __forceinline__ V warp_all_sum(V v) {
