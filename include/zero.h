@@ -704,11 +704,15 @@ zero_status zero_block_join_backward(const zero_join_desc* desc, const zero_join
  *   rows[p]    = the row of pair p, -1 when dropped
  *   pairs[i]   = the pair of row i, -1 for i >= M
  * ids: int32 (id_bytes 4) or int64 (8).  n_experts at most 4096, tokens*topk
- * below 2^31.  The order is stable.  Nothing is read back by the host.
+ * below 2^31.  The order is stable.  workspace: 4-byte aligned device scratch
+ * (NULL when zero_expert_sort_workspace_bytes says 0).  Nothing is read back
+ * by the host.
  */
 zero_status zero_expert_sort(const void* ids, int32_t id_bytes, int64_t tokens, int32_t topk,
                              int32_t n_experts, int32_t* offsets, int32_t* rows, int32_t* pairs,
-                             void* stream);
+                             void* workspace, int64_t workspace_bytes, void* stream);
+zero_status zero_expert_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t n_experts,
+                                             int64_t* bytes);
 
 /* xs[rows[p]] = x[t]; the rows of xs past M are zero.  x_stride: elements
  * between rows of x; xs is [tokens*topk, hidden], contiguous. */

@@ -28,7 +28,7 @@ _TRAIN_OPS = ("ClipGradNorm", "ExpertOrder", "GradNorm", "NormResult", "block_jo
               "zero_block_join_backward", "zero_block_join_workspace_bytes",
               "zero_clip_grad_norm", "zero_expert_combine", "zero_expert_combine_backward",
               "zero_expert_dispatch", "zero_expert_dispatch_backward", "zero_expert_sort",
-              "zero_grad_norm", "zero_grad_norm_workspace_bytes")
+              "zero_expert_sort_workspace_bytes", "zero_grad_norm", "zero_grad_norm_workspace_bytes")
 
 
 def __getattr__(name):

@@ -32,20 +32,25 @@ namespace zero {
 namespace {
 
 // ---------------------------------------------------------------------------
-// The sort: a stable counting sort by one thread-block cluster.  The pairs
-// are cut into one contiguous segment a warp; a warp counts its segment's
-// experts in its own shared-memory row, the rows are scanned across the
-// cluster's warps (through distributed shared memory) and the experts, and
+// The sort: a stable counting sort.  The pairs are cut into one contiguous
+// segment a warp; a warp counts its segment's experts in its own shared-memory
+// row, the rows are scanned across the warps of all CTAs and the experts, and
 // the warp walks its segment again giving out places.  Lanes with the same
 // expert find their rank by a warp match, so the order is stable and nothing
 // depends on timing.
 //
-// One launch and no global scratch.  It is bound by the walk's latency
-// (32 pairs a step and warp), not by bytes: a cluster of up to kSortCtas
-// CTAs shortens the segments.
+// What bounds it is the walk's latency (32 pairs a step and warp), not bytes.
+// Up to kClusterPairs pairs one thread-block cluster does it in one launch,
+// its CTAs reading one another's counts through distributed shared memory;
+// above, a first launch leaves every CTA's counts in the workspace and up to
+// kTableCtas CTAs share the walk (240,000 pairs, 256 experts, took 72 us in
+// one cluster).
 
-constexpr int kSortCtas = 8;           // CTAs of the largest cluster (portable size)
+constexpr int kClusterCtas = 8;        // CTAs of the largest cluster (portable size)
+constexpr int64_t kClusterPairs = 49152;
+constexpr int kTableCtas = 128;
 constexpr int kSortWarpsMost = 32;
+constexpr int kIdsAhead = 8;
 constexpr int kMaxExperts = 4096;
 constexpr int kSortSmemMost = 200 * 1024;
 
@@ -56,6 +61,7 @@ struct SortArgs {
   int32_t* offsets;
   int32_t* rows;
   int32_t* pairs;
+  int32_t* table;      // [CTAs][n_experts]: counts of each CTA's pairs, or null: a cluster
 };
 
 __device__ __forceinline__ int load_id(const SortArgs& a, int64_t p) {
@@ -67,30 +73,66 @@ __device__ __forceinline__ int load_id(const SortArgs& a, int64_t p) {
   return v >= 0 && v < a.n_experts ? static_cast<int>(v) : -1;
 }
 
+// A warp's pairs among `ctas` CTAs of as many warps: whole groups of 32 but
+// for the last warp.
+struct Segment {
+  int64_t lo, hi;
+  __device__ __forceinline__ Segment(int64_t n, int cta, int ctas) {
+    const int warps = blockDim.x >> 5;
+    const int64_t all = static_cast<int64_t>(ctas) * warps;
+    const int64_t size = (((n + all - 1) / all) + 31) / 32 * 32;
+    lo = min(n, (static_cast<int64_t>(cta) * warps + (threadIdx.x >> 5)) * size);
+    hi = min(n, lo + size);
+  }
+  // step(expert, pair) for each lane's pairs (expert -1: none or dropped), the
+  // ids loaded kIdsAhead groups at a time: the steps depend on one another,
+  // their loads need not.
+  template <class Step>
+  __device__ __forceinline__ void walk(const SortArgs& a, Step step) const {
+    const int lane = threadIdx.x & 31;
+    for (int64_t p = lo; p < hi; p += 32 * kIdsAhead) {
+      int e[kIdsAhead];
+#pragma unroll
+      for (int i = 0; i < kIdsAhead; ++i) e[i] = p + 32 * i + lane < hi ? load_id(a, p + 32 * i + lane) : -1;
+#pragma unroll
+      for (int i = 0; i < kIdsAhead; ++i)
+        if (p + 32 * i < hi) step(e[i], p + 32 * i + lane);
+    }
+  }
+};
+
+// Every CTA's counts for the walk of many CTAs.
+__global__ void __launch_bounds__(32 * kSortWarpsMost) k_expert_count(const SortArgs a) {
+  extern __shared__ int smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int e = threadIdx.x; e < a.n_experts; e += blockDim.x) smem[e] = 0;
+  __syncthreads();
+  Segment(a.n, blockIdx.x, gridDim.x).walk(a, [&](int e, int64_t) {
+    if (e >= 0) atomicAdd(smem + e, 1);
+  });
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.n_experts; e += blockDim.x)
+    a.table[static_cast<int64_t>(blockIdx.x) * a.n_experts + e] = smem[e];
+}
+
+template <bool TABLE>
 __global__ void __launch_bounds__(32 * kSortWarpsMost) k_expert_sort(const SortArgs a) {
   extern __shared__ int smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int E = a.n_experts;
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ctas = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
+  const int ctas = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
   int* count = smem;               // [warps][E]
   int* total = smem + warps * E;   // [E]: this CTA's pairs of each expert
   int* start = total + E;          // [E]: first row of each expert for this CTA
   int* scan = start + E;           // [warps]
   for (int i = threadIdx.x; i < warps * E; i += blockDim.x) count[i] = 0;
   __syncthreads();
-  // this warp's pairs: whole groups of 32 but for the last warp
-  const int64_t all = static_cast<int64_t>(ctas) * warps;
-  const int64_t seg = (((a.n + all - 1) / all) + 31) / 32 * 32;
-  const int64_t lo = min(a.n, (static_cast<int64_t>(me) * warps + warp) * seg);
-  const int64_t hi = min(a.n, lo + seg);
+  const Segment seg(a.n, me, ctas);
   int* mine = count + warp * E;
-  for (int64_t p = lo; p < hi; p += 32) {
-    const int e = p + lane < hi ? load_id(a, p + lane) : -1;
-    const unsigned same = __match_any_sync(kFull, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-  }
+  seg.walk(a, [&](int e, int64_t) {
+    if (e >= 0) atomicAdd(mine + e, 1);  // only counted here: no order
+  });
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int s = 0;
@@ -101,7 +143,10 @@ __global__ void __launch_bounds__(32 * kSortWarpsMost) k_expert_sort(const SortA
     }
     total[e] = s;
   }
-  cluster.sync();
+  if constexpr (TABLE)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  else
+    cluster.sync();
   // the pairs of all CTAs below this one, and of all CTAs, expert by expert;
   // then an exclusive scan of the latter over the experts
   int carry = 0;
@@ -109,10 +154,23 @@ __global__ void __launch_bounds__(32 * kSortWarpsMost) k_expert_sort(const SortA
     const int e = e0 + threadIdx.x;
     int below = 0, sum = 0;
     if (e < E) {
-      for (int c = 0; c < ctas; ++c) {
-        const int v = cluster.map_shared_rank(total, c)[e];
-        if (c < me) below += v;
-        sum += v;
+      if constexpr (TABLE) {
+        for (int c0 = 0; c0 < ctas; c0 += 8) {
+          int v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = c0 + i < ctas ? __ldcg(a.table + static_cast<int64_t>(c0 + i) * E + e) : 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (c0 + i < me) below += v[i];
+            sum += v[i];
+          }
+        }
+      } else {
+        for (int c = 0; c < ctas; ++c) {
+          const int v = cluster.map_shared_rank(total, c)[e];
+          if (c < me) below += v;
+          sum += v;
+        }
       }
     }
     int inc = sum;
@@ -140,25 +198,49 @@ __global__ void __launch_bounds__(32 * kSortWarpsMost) k_expert_sort(const SortA
   if (me == 0 && threadIdx.x == 0) a.offsets[E] = M;
   for (int i = threadIdx.x; i < warps * E; i += blockDim.x) count[i] += start[i % E];
   __syncthreads();
-  for (int64_t p = lo; p < hi; p += 32) {
-    const int e = p + lane < hi ? load_id(a, p + lane) : -1;
+  seg.walk(a, [&](int e, int64_t p) {
     const unsigned same = __match_any_sync(kFull, e);
     int row = -1;
     if (e >= 0) row = mine[e] + __popc(same & ((1u << lane) - 1));
     __syncwarp();
     if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
     __syncwarp();
-    if (p + lane < hi) a.rows[p + lane] = row;
-    if (row >= 0) a.pairs[row] = static_cast<int>(p + lane);
-  }
+    if (p < seg.hi) a.rows[p] = row;
+    if (row >= 0) a.pairs[row] = static_cast<int>(p);
+  });
   for (int64_t i = M + static_cast<int64_t>(me) * blockDim.x + threadIdx.x; i < a.n;
        i += static_cast<int64_t>(ctas) * blockDim.x)
     a.pairs[i] = -1;
-  cluster.sync();  // no CTA leaves while another may still read its totals
+  if constexpr (!TABLE) cluster.sync();  // no CTA leaves while another may still read its totals
 }
 
+// How a sort is launched.
+struct SortShape {
+  int ctas, warps, smem;
+  bool table;
+  SortShape(int64_t n, int n_experts) {
+    const int64_t groups = std::max<int64_t>(1, (n + 31) / 32);
+    table = n > kClusterPairs;
+    // as many warps a CTA as their counters fit, no more than there are groups
+    // of 32 pairs, and CTAs until a warp has four groups
+    warps = kSortWarpsMost;
+    while (warps > 1 && ((warps + 2) * n_experts + warps) * 4 > kSortSmemMost) warps /= 2;
+    while (warps > 1 && warps / 2 >= groups) warps /= 2;
+    const int most = table ? kTableCtas : kClusterCtas;
+    ctas = 1;
+    while (ctas < most && static_cast<int64_t>(ctas) * warps * 4 < groups) ctas *= 2;
+    smem = ((warps + 2) * n_experts + warps) * 4;
+  }
+  int64_t table_bytes(int n_experts) const { return table ? static_cast<int64_t>(ctas) * n_experts * 4 : 0; }
+};
+
 // ---------------------------------------------------------------------------
-// The rows.  A group of 1, 2, 4 or 8 warps takes a token.
+// The rows.  A group of 4 to 256 lanes takes a token, octet by octet
+// (16-byte aligned rows) or eight single columns at a time, `lanes` apart.
+// Four rows' octets are in flight in a thread: 1, 2 or 4 choices times 4, 2
+// or 1 octets of each, by topk.  (One at a time, the combination of two of 64
+// experts' rows of 4096 bf16, 16384 tokens, took 85 us; with more than four
+// the registers cost more than the loads gained, 138 us.)
 
 constexpr int kRowThreads = 256;
 
@@ -171,133 +253,229 @@ struct RowArgs {
   const int32_t* rows;
   const int32_t* total;    // offsets + n_experts
   int64_t tokens, hidden, stride;  // stride: of in's rows (x, dy)
-  int32_t topk, weight_type;
+  int32_t topk, weight_type, lanes;
 };
 
-// Columns of one row: octets when VEC (16-byte aligned rows), else elements.
+// Eight columns of a row, as they were loaded.
 template <class T, bool VEC>
 struct Cols {
-  static constexpr int kN = VEC ? 8 : 1;
-  static __device__ __forceinline__ void load(const T* p, float (&v)[kN]) {
-    if constexpr (VEC)
-      Elem<T>::load8(p, v);
-    else
-      v[0] = Elem<T>::widen(*p);
+  Octet<T> o;
+  T e[8];
+  __device__ __forceinline__ void load(const T* row, int c, int lanes, int hidden) {
+    if constexpr (VEC) {
+      o.load(row + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i * lanes < hidden) e[i] = row[c + i * lanes];
+    }
   }
-  static __device__ __forceinline__ void store(T* p, const float (&v)[kN]) {
-    if constexpr (VEC)
-      Elem<T>::store8(p, v);
-    else
-      *p = Elem<T>::narrow(v[0]);
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    if constexpr (VEC) {
+      o.widen(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = Elem<T>::widen(e[i]);
+    }
+  }
+  __device__ __forceinline__ void copy_to(T* row, int c, int lanes, int hidden) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < Octet<T>::kChunks; ++k) reinterpret_cast<uint4*>(row + c)[k] = o.w[k];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i * lanes < hidden) row[c + i * lanes] = e[i];
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int c, int lanes, int hidden, const float (&v)[8]) {
+    if constexpr (VEC) {
+      Elem<T>::store8(row + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i * lanes < hidden) row[c + i * lanes] = Elem<T>::narrow(v[i]);
+    }
   }
 };
 
-// The group's token and the thread's place in the group.
+// The group's token, the thread's first column and the columns of a round.
+template <bool VEC>
 struct Place {
   int64_t token;
-  int lane, size;
-  __device__ __forceinline__ explicit Place(int group_warps) {
-    size = 32 * group_warps;
-    token = static_cast<int64_t>(blockIdx.x) * (kRowThreads / size) + threadIdx.x / size;
-    lane = threadIdx.x % size;
+  int lane, lanes, first, round;
+  __device__ __forceinline__ explicit Place(int lanes_) : lanes(lanes_) {
+    token = static_cast<int64_t>(blockIdx.x) * (kRowThreads / lanes) + threadIdx.x / lanes;
+    lane = threadIdx.x % lanes;
+    first = VEC ? 8 * lane : lane;
+    round = 8 * lanes;
   }
 };
 
 // Rows past the last kept pair are zero: the token's own share of them.
 template <class T, bool VEC>
-__device__ __forceinline__ void clear_past_end(const RowArgs& a, const Place& me, T* out) {
-  constexpr int N = Cols<T, VEC>::kN;
+__device__ __forceinline__ void clear_past_end(const RowArgs& a, const Place<VEC>& me, T* out) {
   const int64_t M = __ldg(a.total);
-  const float z[N] = {};
+  const int H = static_cast<int>(a.hidden);
+  const float z[8] = {};
   for (int k = 0; k < a.topk; ++k) {
     const int64_t i = me.token * a.topk + k;
     if (i < M) continue;
-    for (int64_t c = static_cast<int64_t>(me.lane) * N; c < a.hidden; c += static_cast<int64_t>(me.size) * N)
-      Cols<T, VEC>::store(out + i * a.hidden + c, z);
+    for (int c = me.first; c < H; c += me.round) Cols<T, VEC>::store(out + i * H, c, me.lanes, H, z);
   }
 }
 
-template <class T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) k_dispatch(const RowArgs a, int group_warps) {
-  constexpr int N = Cols<T, VEC>::kN;
-  const Place me(group_warps);
+// Rows and weights of choices k0 .. k0 + K - 1 of the token whose pairs start
+// at p0; -1 past topk.
+template <int K>
+struct Choices {
+  int32_t row[K];
+  float weight[K];
+  __device__ __forceinline__ Choices(const RowArgs& a, int64_t p0, int k0, bool live) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const bool there = live && k0 + i < a.topk;
+      row[i] = there ? __ldg(a.rows + p0 + k0 + i) : -1;
+      weight[i] = row[i] >= 0 && a.weights ? load_any(a.weights, p0 + k0 + i, a.weight_type) : 1.f;
+    }
+  }
+};
+
+template <class T, bool VEC, int K>
+__global__ void __launch_bounds__(kRowThreads, VEC ? 5 : 3) k_dispatch(const RowArgs a) {
+  constexpr int kParts = 4 / K;
+  const Place<VEC> me(a.lanes);
   if (me.token >= a.tokens) return;
+  const int H = static_cast<int>(a.hidden);
   const T* x = static_cast<const T*>(a.in) + me.token * a.stride;
   T* xs = static_cast<T*>(a.out);
-  const int32_t* rows = a.rows + me.token * a.topk;
-  for (int64_t c = static_cast<int64_t>(me.lane) * N; c < a.hidden; c += static_cast<int64_t>(me.size) * N) {
-    float v[N];
-    Cols<T, VEC>::load(x + c, v);
-    for (int k = 0; k < a.topk; ++k) {
-      const int64_t r = __ldg(rows + k);
-      if (r >= 0) Cols<T, VEC>::store(xs + r * a.hidden + c, v);
+  const int64_t p0 = me.token * a.topk;
+  const Choices<K> ch(a, p0, 0, true);
+  for (int c0 = me.first; c0 < H; c0 += kParts * me.round) {
+    Cols<T, VEC> v[kParts];
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      if (c0 + q * me.round < H) v[q].load(x, c0 + q * me.round, me.lanes, H);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      const int c = c0 + q * me.round;
+      if (c >= H) continue;
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if (ch.row[i] >= 0) v[q].copy_to(xs + ch.row[i] * static_cast<int64_t>(H), c, me.lanes, H);
+      for (int k = K; k < a.topk; ++k) {
+        const int64_t r = __ldg(a.rows + p0 + k);
+        if (r >= 0) v[q].copy_to(xs + r * H, c, me.lanes, H);
+      }
     }
   }
   clear_past_end<T, VEC>(a, me, xs);
 }
 
-template <class T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) k_combine(const RowArgs a, int group_warps) {
-  constexpr int N = Cols<T, VEC>::kN;
-  const Place me(group_warps);
+template <class T, bool VEC, int K>
+__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) k_combine(const RowArgs a) {
+  constexpr int kParts = 4 / K;
+  const Place<VEC> me(a.lanes);
   if (me.token >= a.tokens) return;
+  const int H = static_cast<int>(a.hidden);
   const T* in = static_cast<const T*>(a.in);
-  T* y = static_cast<T*>(a.out) + me.token * a.hidden;
+  T* y = static_cast<T*>(a.out) + me.token * H;
   const int64_t p0 = me.token * a.topk;
-  for (int64_t c = static_cast<int64_t>(me.lane) * N; c < a.hidden; c += static_cast<int64_t>(me.size) * N) {
-    float s[N] = {};
-    for (int k = 0; k < a.topk; ++k) {
-      const int64_t r = __ldg(a.rows + p0 + k);
-      if (r < 0) continue;
-      const float w = a.weights ? load_any(a.weights, p0 + k, a.weight_type) : 1.f;
-      float v[N];
-      Cols<T, VEC>::load(in + r * a.hidden + c, v);
+  const Choices<K> first(a, p0, 0, true);
+  for (int c0 = me.first; c0 < H; c0 += kParts * me.round) {
+    float s[kParts][8];
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[i] = fmaf(w, v[i], s[i]);
-    }
-    Cols<T, VEC>::store(y + c, s);
+    for (int q = 0; q < kParts; ++q)
+#pragma unroll
+      for (int n = 0; n < 8; ++n) s[q][n] = 0.f;
+    auto add = [&](const Choices<K>& ch) {
+      Cols<T, VEC> v[kParts][K];
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (ch.row[i] >= 0 && c0 + q * me.round < H)
+            v[q][i].load(in + ch.row[i] * static_cast<int64_t>(H), c0 + q * me.round, me.lanes, H);
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (ch.row[i] >= 0 && c0 + q * me.round < H) {
+            float f[8];
+            v[q][i].widen(f);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) s[q][n] = fmaf(ch.weight[i], f[n], s[q][n]);
+          }
+    };
+    add(first);
+    for (int k0 = K; k0 < a.topk; k0 += K) add(Choices<K>(a, p0, k0, true));
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      if (c0 + q * me.round < H) Cols<T, VEC>::store(y, c0 + q * me.round, me.lanes, H, s[q]);
   }
 }
 
-template <class T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) k_combine_backward(const RowArgs a, int group_warps) {
-  constexpr int N = Cols<T, VEC>::kN;
-  __shared__ float part[2][kRowThreads / 32];
-  const Place me(group_warps);
+template <class T, bool VEC, int K>
+__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) k_combine_backward(const RowArgs a) {
+  __shared__ float part[2][K][kRowThreads / 32];
+  const Place<VEC> me(a.lanes);
   const bool live = me.token < a.tokens;  // every thread meets the barriers below
+  const int H = static_cast<int>(a.hidden);
   const T* dy = static_cast<const T*>(a.in) + (live ? me.token : 0) * a.stride;
   const T* ys = static_cast<const T*>(a.ys);
   T* dys = static_cast<T*>(a.out);
   const int64_t p0 = (live ? me.token : 0) * a.topk;
-  const int warp = threadIdx.x >> 5;
-  for (int k = 0; k < a.topk; ++k) {
-    const int64_t r = live ? __ldg(a.rows + p0 + k) : -1;
-    float dot = 0.f;
-    if (r >= 0) {
-      const float w = load_any(a.weights, p0 + k, a.weight_type);
-      for (int64_t c = static_cast<int64_t>(me.lane) * N; c < a.hidden;
-           c += static_cast<int64_t>(me.size) * N) {
-        float g[N], v[N];
-        Cols<T, VEC>::load(dy + c, g);
-        Cols<T, VEC>::load(ys + r * a.hidden + c, v);
+  int flip = 0;
+  for (int k0 = 0; k0 < a.topk; k0 += K, flip ^= 1) {
+    const Choices<K> ch(a, p0, k0, live);
+    float dot[K] = {};
+    if (live) {
+      for (int c = me.first; c < H; c += me.round) {
+        Cols<T, VEC> g, v[K];
+        g.load(dy, c, me.lanes, H);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          dot = fmaf(g[i], v[i], dot);
-          g[i] *= w;
-        }
-        Cols<T, VEC>::store(dys + r * a.hidden + c, g);
+        for (int i = 0; i < K; ++i)
+          if (ch.row[i] >= 0) v[i].load(ys + ch.row[i] * static_cast<int64_t>(H), c, me.lanes, H);
+        float d[8];
+        g.widen(d);
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (ch.row[i] >= 0) {
+            float f[8];
+            v[i].widen(f);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              if (VEC || c + n * me.lanes < H) dot[i] = fmaf(d[n], f[n], dot[i]);
+              f[n] = d[n] * ch.weight[i];
+            }
+            Cols<T, VEC>::store(dys + ch.row[i] * static_cast<int64_t>(H), c, me.lanes, H, f);
+          }
       }
     }
-    dot = warp_all_sum(dot);
-    if (group_warps > 1) {
-      float* buf = part[k & 1];  // the next choice's sums go to the other half
-      if ((threadIdx.x & 31) == 0) buf[warp] = dot;
+    if (!a.dweights) continue;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      for (int o = min(me.lanes, 32) >> 1; o > 0; o >>= 1) dot[i] += __shfl_xor_sync(kFull, dot[i], o);
+    if (me.lanes > 32) {
+      // the next choices' sums go to the other half
+      const int warp = threadIdx.x >> 5;
+      if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) part[flip][i][warp] = dot[i];
+      }
       __syncthreads();
-      dot = 0.f;
-      const int first = warp / group_warps * group_warps;
-      for (int w = 0; w < group_warps; ++w) dot += buf[first + w];
+      const int warps = me.lanes >> 5, w0 = warp / warps * warps;
+      if (me.lane < K) {
+        dot[0] = 0.f;
+        for (int w = 0; w < warps; ++w) dot[0] += part[flip][me.lane][w0 + w];
+      }
+    } else {
+#pragma unroll
+      for (int i = 1; i < K; ++i)
+        if (me.lane == i) dot[0] = dot[i];
     }
-    if (live && me.lane == 0 && a.dweights) store_any(a.dweights, p0 + k, a.weight_type, dot);
+    if (live && me.lane < K && k0 + me.lane < a.topk)
+      store_any(a.dweights, p0 + k0 + me.lane, a.weight_type, dot[0]);
   }
   if (live) clear_past_end<T, VEC>(a, me, dys);
 }
@@ -307,21 +485,27 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward(const RowArgs 
 
 enum class RowOp { kDispatch, kCombine, kCombineBackward };
 
+template <class T, bool VEC, int K>
+int launch_rows_k(RowOp op, const RowArgs& a, cudaStream_t s) {
+  // lanes of a token's group: one octet (eight columns) each for as long a
+  // row as the CTA allows, a power of two; the gradient's dot wants K lanes
+  RowArgs copy = a;
+  copy.lanes = 4;
+  while (copy.lanes < kRowThreads && static_cast<int64_t>(copy.lanes) * 8 < a.hidden) copy.lanes *= 2;
+  const int64_t per_cta = kRowThreads / copy.lanes;
+  const int64_t grid = (a.tokens + per_cta - 1) / per_cta;
+  void* args[] = {&copy};
+  const void* fn = op == RowOp::kDispatch  ? reinterpret_cast<const void*>(&k_dispatch<T, VEC, K>)
+                   : op == RowOp::kCombine ? reinterpret_cast<const void*>(&k_combine<T, VEC, K>)
+                                           : reinterpret_cast<const void*>(&k_combine_backward<T, VEC, K>);
+  return static_cast<int>(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), args, 0, s));
+}
+
 template <class T, bool VEC>
 int launch_rows(RowOp op, const RowArgs& a, cudaStream_t s) {
-  // warps of a token's group: enough for the row at one octet (element) a
-  // thread, a power of two up to the CTA
-  const int64_t units = VEC ? a.hidden / 8 : a.hidden;
-  int gw = 1;
-  while (gw < kRowThreads / 32 && static_cast<int64_t>(gw) * 32 < units) gw *= 2;
-  const int64_t per_cta = kRowThreads / (32 * gw);
-  const int64_t grid = (a.tokens + per_cta - 1) / per_cta;
-  RowArgs copy = a;
-  void* args[] = {&copy, &gw};
-  const void* fn = op == RowOp::kDispatch  ? reinterpret_cast<const void*>(&k_dispatch<T, VEC>)
-                   : op == RowOp::kCombine ? reinterpret_cast<const void*>(&k_combine<T, VEC>)
-                                           : reinterpret_cast<const void*>(&k_combine_backward<T, VEC>);
-  return static_cast<int>(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), args, 0, s));
+  return a.topk == 1   ? launch_rows_k<T, VEC, 1>(op, a, s)
+         : a.topk == 2 ? launch_rows_k<T, VEC, 2>(op, a, s)
+                       : launch_rows_k<T, VEC, 4>(op, a, s);
 }
 
 template <class T>
@@ -361,8 +545,8 @@ zero_status check_experts(const char* fn, int32_t n_experts) {
 zero_status check_rows(const char* fn, int64_t tokens, int32_t topk, int64_t hidden, int dtype) {
   const zero_status st = check_sizes(fn, tokens, topk);
   if (st != ZERO_OK) return st;
-  if (hidden < 1 || hidden > INT32_MAX)
-    return fail(ZERO_ERR_INVALID, "%s: hidden must lie in [1, 2^31-1]", fn);
+  if (hidden < 1 || hidden > INT64_C(1) << 30)
+    return fail(ZERO_ERR_INVALID, "%s: hidden must lie in [1, 2^30]", fn);
   if (!known_type(dtype)) return fail(ZERO_ERR_INVALID, "%s: unknown dtype", fn);
   return ZERO_OK;
 }
@@ -390,9 +574,20 @@ zero_status check_weights(const char* fn, zero_dtype dtype, zero_dtype weight_dt
 
 using namespace zero;
 
+extern "C" zero_status zero_expert_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t n_experts,
+                                                        int64_t* bytes) {
+  const char* fn = "zero_expert_sort_workspace_bytes";
+  clear_error();
+  if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
+  EXPERT_TRY(check_sizes(fn, tokens, topk));
+  EXPERT_TRY(check_experts(fn, n_experts));
+  *bytes = SortShape(tokens * topk, n_experts).table_bytes(n_experts);
+  return ZERO_OK;
+}
+
 extern "C" zero_status zero_expert_sort(const void* ids, int32_t id_bytes, int64_t tokens, int32_t topk,
                                         int32_t n_experts, int32_t* offsets, int32_t* rows, int32_t* pairs,
-                                        void* stream) {
+                                        void* workspace, int64_t workspace_bytes, void* stream) {
   const char* fn = "zero_expert_sort";
   clear_error();
   NvtxRange range(fn);
@@ -404,35 +599,49 @@ extern "C" zero_status zero_expert_sort(const void* ids, int32_t id_bytes, int64
   EXPERT_TRY(check_ptr(fn, "offsets", offsets, 4, true));
   EXPERT_TRY(check_ptr(fn, "rows", rows, 4, any));
   EXPERT_TRY(check_ptr(fn, "pairs", pairs, 4, any));
+  const SortShape shape(tokens * topk, n_experts);
+  const int64_t need = shape.table_bytes(n_experts);
+  if (need > 0) {
+    EXPERT_TRY(check_ptr(fn, "workspace", workspace, 4, true));
+    if (workspace_bytes < need)
+      return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes,
+                  need);
+  }
   const cudaError_t pending = cudaGetLastError();
   if (pending != cudaSuccess)
     return fail(ZERO_ERR_CUDA, "%s: pending CUDA error: %s", fn, cudaGetErrorString(pending));
-  SortArgs a = {ids, tokens * topk, id_bytes, n_experts, offsets, rows, pairs};
-  // as many warps a CTA as their counters fit, no more than there are groups
-  // of 32 pairs, and CTAs until a warp has four groups
-  const int64_t groups = std::max<int64_t>(1, (a.n + 31) / 32);
-  int warps = kSortWarpsMost;
-  while (warps > 1 && (static_cast<int64_t>(warps) + 2) * n_experts * 4 + 4 * warps > kSortSmemMost) warps /= 2;
-  while (warps > 1 && warps / 2 >= groups) warps /= 2;
-  int ctas = 1;
-  while (ctas < kSortCtas && static_cast<int64_t>(ctas) * warps * 4 < groups) ctas *= 2;
-  const int smem = ((warps + 2) * n_experts + warps) * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMost);
-  if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+  const SortArgs a = {ids,  tokens * topk, id_bytes, n_experts,
+                      offsets, rows, pairs, shape.table ? static_cast<int32_t*>(workspace) : nullptr};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(shape.ctas);
+  cfg.blockDim = dim3(32 * shape.warps);
+  cfg.dynamicSmemBytes = shape.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaSuccess;
+  const void* sort = shape.table ? reinterpret_cast<const void*>(&k_expert_sort<true>)
+                                 : reinterpret_cast<const void*>(&k_expert_sort<false>);
+  if (shape.smem > 48 * 1024)
+    e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMost);
+  if (e == cudaSuccess && shape.table) {
+    k_expert_count<<<cfg.gridDim, cfg.blockDim, n_experts * 4, s>>>(a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
+    // the walk counts its own warps while the counts of the others arrive
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.x = shape.ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_expert_sort, a);
   }
+  if (e == cudaSuccess)
+    e = shape.table ? cudaLaunchKernelEx(&cfg, k_expert_sort<true>, a)
+                    : cudaLaunchKernelEx(&cfg, k_expert_sort<false>, a);
   if (e != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return ZERO_OK;

@@ -9,12 +9,12 @@
 // reads them again and writes them; nothing can be written before the last
 // element is read.
 //
-// Work split.  A tensor is cut into tiles of 4096 elements, a CTA takes a
+// Work split.  A tensor is cut into tiles of 8192 elements, a CTA takes a
 // contiguous run of tiles (of any tensors) and leaves one partial,
 // so the partials are few (at most kGrid a launch) and every CTA of the
 // clipping adds them up itself, in the same fixed order: no kernel between
-// the two passes, no atomics, the same norm in every run.  A thread has four
-// octets (16 or 32 bytes each) in flight.  The clipping walks the tiles from
+// the two passes, no atomics, the same norm in every run.  A thread has
+// 128 bytes of loads in flight.  The clipping walks the tiles from
 // the last to the first, so what the norm read last is still in L2, and it is
 // launched early (its CTAs wait for the norm's on the device).
 #include <cuda_runtime.h>
@@ -32,9 +32,10 @@ namespace zero {
 namespace {
 
 constexpr int kNormThreads = 128;
-constexpr int kNormTile = 4096;                        // elements a CTA takes at once
-constexpr int kTileOctets = kNormTile / 8;             // 512
-constexpr int kAhead = kTileOctets / kNormThreads;     // octets of a thread in flight: 4
+constexpr int kNormTile = 8192;                        // elements a CTA takes at once
+constexpr int kTileOctets = kNormTile / 8;             // 1024
+constexpr int kAhead = kTileOctets / kNormThreads;     // octets of a thread: 8
+constexpr int kBytesAhead = 128;                       // of a thread's loads in flight
 constexpr int kNormCtas = 8;                           // of an SM, at least
 constexpr int kGrid = 16 * kSMs;                       // CTAs of one launch at most
 constexpr int kJobsMost = 1000;                        // tensors of one launch at most
@@ -176,55 +177,35 @@ __device__ __forceinline__ int find_grad_job(const GradArgs<CAP>& a, int tile) {
   return lo;
 }
 
-// An octet as it was loaded: whole 16-byte chunks, widened when it is used,
-// so that the loads of a thread's octets go out together.
+// An octet from an address off the 16-byte boundaries: the covering chunks,
+// shifted by whole words and, for 16-bit elements, by half a word.  All chunks
+// lie in the tensor.
 template <class T>
-struct Octet {
-  static constexpr int kChunks = sizeof(T) == 4 ? 2 : 1;
-  uint4 w[kChunks];
-  __device__ __forceinline__ void widen(float (&v)[8]) const {
-    if constexpr (sizeof(T) == 4) {
-      v[0] = __uint_as_float(w[0].x), v[1] = __uint_as_float(w[0].y);
-      v[2] = __uint_as_float(w[0].z), v[3] = __uint_as_float(w[0].w);
-      v[4] = __uint_as_float(w[1].x), v[5] = __uint_as_float(w[1].y);
-      v[6] = __uint_as_float(w[1].z), v[7] = __uint_as_float(w[1].w);
-    } else {
-      Elem<T>::unpack(w[0].x, v[0], v[1]), Elem<T>::unpack(w[0].y, v[2], v[3]);
-      Elem<T>::unpack(w[0].z, v[4], v[5]), Elem<T>::unpack(w[0].w, v[6], v[7]);
-    }
+__device__ __forceinline__ void load_shifted(Octet<T>& o, const T* p) {
+  const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - skip);
+  uint32_t x[4 * Octet<T>::kChunks + 5];
+#pragma unroll
+  for (int k = 0; k <= Octet<T>::kChunks; ++k) {
+    const uint4 c = __ldg(q + k);
+    x[4 * k] = c.x, x[4 * k + 1] = c.y, x[4 * k + 2] = c.z, x[4 * k + 3] = c.w;
   }
-  __device__ __forceinline__ void load(const T* p) {  // 16-byte aligned
+  x[4 * Octet<T>::kChunks + 4] = 0;
+  uint32_t y[4 * Octet<T>::kChunks + 1];
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
+  for (int k = 0; k <= 4 * Octet<T>::kChunks; ++k) {  // a word more than the octet's, for the half shift
+    const uint32_t lo = skip & 4 ? x[k + 1] : x[k];
+    const uint32_t hi = k + 3 < 4 * Octet<T>::kChunks + 5 ? (skip & 4 ? x[k + 3] : x[k + 2]) : 0;
+    y[k] = skip & 8 ? hi : lo;
   }
-  // From an address that is not: the covering chunks, shifted by whole words
-  // and, for 16-bit elements, by half a word.  All chunks lie in the tensor.
-  __device__ __forceinline__ void load_shifted(const T* p) {
-    const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - skip);
-    uint32_t x[4 * kChunks + 5];
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int k = 0; k <= kChunks; ++k) {
-      const uint4 c = __ldg(q + k);
-      x[4 * k] = c.x, x[4 * k + 1] = c.y, x[4 * k + 2] = c.z, x[4 * k + 3] = c.w;
-    }
-    x[4 * kChunks + 4] = 0;
-    uint32_t y[4 * kChunks + 1];
-#pragma unroll
-    for (int k = 0; k <= 4 * kChunks; ++k) {  // a word more than the octet's, for the half shift
-      const uint32_t lo = skip & 4 ? x[k + 1] : x[k];
-      const uint32_t hi = k + 3 < 4 * kChunks + 5 ? (skip & 4 ? x[k + 3] : x[k + 2]) : 0;
-      y[k] = skip & 8 ? hi : lo;
-    }
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int k = 0; k < 4 * kChunks; ++k) y[k] = __funnelshift_r(y[k], y[k + 1], 8 * (skip & 2));
-    }
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k)
-      w[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    for (int k = 0; k < 4 * Octet<T>::kChunks; ++k) y[k] = __funnelshift_r(y[k], y[k + 1], 8 * (skip & 2));
   }
-};
+#pragma unroll
+  for (int k = 0; k < Octet<T>::kChunks; ++k)
+    o.w[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+}
 
 // Elements [e0, e0 + cnt) of a tensor, one by one, zero elsewhere.
 template <class T>
@@ -247,18 +228,26 @@ struct Tile {
   static __device__ __forceinline__ int at(int k) { return (k * kNormThreads + static_cast<int>(threadIdx.x)) * 8; }
 };
 
-// The octets of a tile that is not whole, one after the other: octet(e) for a
-// whole one, some(e, cnt) for single elements, e relative to the tile.
-// good(e): the octet at e may be taken whole.
-template <class Good, class One, class Some>
-__device__ __forceinline__ void part_of_tile(const Tile& tile, int t, Good good, One octet, Some some) {
+// The octets of a tile that is not whole, two at a time: octets(e, f) for whole
+// ones (f -1: one only), some(e, cnt) for single elements, e relative to the
+// tile.  good(e): the octet at e may be taken whole.
+template <class Good, class Two, class Some>
+__device__ __forceinline__ void part_of_tile(const Tile& tile, int t, Good good, Two octets, Some some) {
   if (t == 0 && threadIdx.x == 0 && tile.before > 0) some(-static_cast<int>(tile.base), tile.before);
 #pragma unroll 1
-  for (int e = Tile::at(0); e < min(tile.left, kNormTile); e += kNormThreads * 8) {
-    if (good(e))
-      octet(e);
-    else
-      some(e, min(8, tile.left - e));
+  for (int e = Tile::at(0); e < min(tile.left, kNormTile); e += 2 * kNormThreads * 8) {
+    const int f = e + kNormThreads * 8;
+    if (good(e) && good(f) && f < kNormTile) {
+      octets(e, f);
+      continue;
+    }
+#pragma unroll 1
+    for (int x = e; x < min(tile.left, min(f + 1, kNormTile)); x += kNormThreads * 8) {
+      if (good(x))
+        octets(x, -1);
+      else
+        some(x, min(8, tile.left - x));
+    }
   }
 }
 
@@ -273,25 +262,34 @@ __device__ __forceinline__ void norm_tile(const GradJob& j, int t, bool inf_norm
       add_squares<T>(s, v);
   };
   if (tile.left >= kNormTile && (t > 0 || j.head == 0)) {
-    Octet<T> o[kAhead];
+    constexpr int kTogether = kBytesAhead / 8 / sizeof(T);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) o[k].load(src + Tile::at(k));
+    for (int k0 = 0; k0 < kAhead; k0 += kTogether) {
+      Octet<T> o[kTogether];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      float v[8];
-      o[k].widen(v);
-      take(v);
+      for (int k = 0; k < kTogether; ++k) o[k].load(src + Tile::at(k0 + k));
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        float v[8];
+        o[k].widen(v);
+        take(v);
+      }
     }
     return;
   }
   part_of_tile(
       tile, t, [&](int e) { return e + 8 <= tile.left; },
-      [&](int e) {
-        Octet<T> o;
+      [&](int e, int f) {
+        Octet<T> o, p;
         o.load(src + e);
+        if (f >= 0) p.load(src + f);
         float v[8];
         o.widen(v);
         take(v);
+        if (f >= 0) {
+          p.widen(v);
+          take(v);
+        }
       },
       [&](int e, int cnt) {
         float v[8];
@@ -314,7 +312,6 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_norm(const __g
   Partial sum = {{0.f, 0.f}, {0.f, 0.f}};
   Squares s = {{f2(0.f), f2(0.f)}, 0.f};
   uint32_t m = 0;
-  int held = 0;
   int q = find_grad_job(a, lo);
   for (int tile = lo; tile < hi; ++tile) {
     while (q + 1 < a.n_jobs && a.jobs[q + 1].tile_begin <= tile) ++q;
@@ -326,12 +323,12 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_norm(const __g
       norm_tile<__nv_bfloat16>(j, t, inf_norm, s, m);
     else
       norm_tile<__half>(j, t, inf_norm, s, m);
-    // two tiles are at most 2 * 39 squares in binary32 before they join a pair
-    if (++held == 2 || tile + 1 == hi) {
+    // a tile is at most 71 squares, 20 of them at most in one binary32 sum,
+    // before they join a pair
+    {
       sum.a = pair_add(sum.a, {sum2(add2(s.a[0], s.a[1])), 0.f});
       if (s.b != 0.f) sum.b = pair_add(sum.b, {s.b, 0.f});
       s = {{f2(0.f), f2(0.f)}, 0.f};
-      held = 0;
     }
   }
   if (inf_norm) sum.a.hi = __uint_as_float(m);
@@ -421,17 +418,21 @@ __device__ __forceinline__ void clip_tile(const GradJob& j, int t, float coef) {
   };
   if (tile.left >= kNormTile + 16 && t > 0) {
     if (straight) {
-      Octet<S> o[kAhead];
+      constexpr int kTogether = kBytesAhead / 8 / sizeof(S);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) o[k].load(src + Tile::at(k));
+      for (int k0 = 0; k0 < kAhead; k0 += kTogether) {
+        Octet<S> o[kTogether];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) scaled(o[k], Tile::at(k));
+        for (int k = 0; k < kTogether; ++k) o[k].load(src + Tile::at(k0 + k));
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) scaled(o[k], Tile::at(k0 + k));
+      }
     } else {
 #pragma unroll 1
       for (int k = 0; k < kAhead; k += 2) {
         Octet<S> o[2];
-        o[0].load_shifted(src + Tile::at(k));
-        o[1].load_shifted(src + Tile::at(k + 1));
+        load_shifted(o[0], src + Tile::at(k));
+        load_shifted(o[1], src + Tile::at(k + 1));
         scaled(o[0], Tile::at(k));
         scaled(o[1], Tile::at(k + 1));
       }
@@ -441,13 +442,17 @@ __device__ __forceinline__ void clip_tile(const GradJob& j, int t, float coef) {
   part_of_tile(
       tile, t,
       [&](int e) { return straight ? e + 8 <= tile.left : e + tile.before >= 8 && e + 16 <= tile.left; },
-      [&](int e) {
-        Octet<S> o;
-        if (straight)
+      [&](int e, int f) {
+        Octet<S> o, p;
+        if (straight) {
           o.load(src + e);
-        else
-          o.load_shifted(src + e);
+          if (f >= 0) p.load(src + f);
+        } else {
+          load_shifted(o, src + e);
+          if (f >= 0) load_shifted(p, src + f);
+        }
         scaled(o, e);
+        if (f >= 0) scaled(p, f);
       },
       [&](int e, int cnt) {
         float v[8];

@@ -84,6 +84,29 @@ struct Elem<__nv_bfloat16> {
   }
 };
 
+// An octet as it was loaded: whole 16-byte chunks, widened when it is used,
+// so that the loads of a thread's octets go out together.
+template <class T>
+struct Octet {
+  static constexpr int kChunks = sizeof(T) == 4 ? 2 : 1;
+  uint4 w[kChunks];
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(w[0].x), v[1] = __uint_as_float(w[0].y);
+      v[2] = __uint_as_float(w[0].z), v[3] = __uint_as_float(w[0].w);
+      v[4] = __uint_as_float(w[1].x), v[5] = __uint_as_float(w[1].y);
+      v[6] = __uint_as_float(w[1].z), v[7] = __uint_as_float(w[1].w);
+    } else {
+      Elem<T>::unpack(w[0].x, v[0], v[1]), Elem<T>::unpack(w[0].y, v[2], v[3]);
+      Elem<T>::unpack(w[0].z, v[4], v[5]), Elem<T>::unpack(w[0].w, v[6], v[7]);
+    }
+  }
+  __device__ __forceinline__ void load(const T* p) {  // 16-byte aligned
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
+  }
+};
+
 // Element i of an array whose type is known only at run time (parameters,
 // gates, weights: read rarely, the branch is uniform).
 __device__ __forceinline__ float load_any(const void* p, int64_t i, int type) {

@@ -545,10 +545,18 @@ class ExpertOrder:
     topk: int
 
 
-def zero_expert_sort(ids, n_experts: int, stream=None) -> ExpertOrder:
+def zero_expert_sort_workspace_bytes(tokens: int, topk: int, n_experts: int) -> int:
+    """Device workspace of zero_expert_sort (0 up to some tens of thousands of choices)."""
+    need = ctypes.c_int64()
+    _check(lib().zero_expert_sort_workspace_bytes(tokens, topk, n_experts, ctypes.byref(need)))
+    return need.value
+
+
+def zero_expert_sort(ids, n_experts: int, workspace=None, stream=None) -> ExpertOrder:
     """Rows of every token's choices in expert order (see zero.h).  ids:
     [tokens, topk] int32 or int64; a choice outside [0, n_experts) is
-    dropped."""
+    dropped.  workspace: device scratch of zero_expert_sort_workspace_bytes
+    (None: allocated here)."""
     device = _current(ids, "ids")
     if ids.dim() != 2 or not ids.is_contiguous():
         raise ValueError("ids: expected a contiguous [tokens, topk] tensor")
@@ -561,10 +569,14 @@ def zero_expert_sort(ids, n_experts: int, stream=None) -> ExpertOrder:
     offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=where)
     rows = torch.empty(ids.shape, dtype=torch.int32, device=where)
     pairs = torch.empty(tokens * topk, dtype=torch.int32, device=where)
-    _keep_for(stream, offsets, rows, pairs)
+    need = zero_expert_sort_workspace_bytes(tokens, topk, n_experts)
+    ws = _workspace(workspace, need, device) if need else None
+    _keep_for(stream, offsets, rows, pairs, ws if workspace is None else None)
     _check(lib().zero_expert_sort(ids.data_ptr() or None, ids.element_size(), tokens, topk,
                                   n_experts, offsets.data_ptr(), rows.data_ptr() or None,
-                                  pairs.data_ptr() or None, _stream(stream, device)))
+                                  pairs.data_ptr() or None,
+                                  None if ws is None else ws.data_ptr(), need,
+                                  _stream(stream, device)))
     return ExpertOrder(offsets, rows, pairs, n_experts, tokens, topk)
 
 

@@ -118,7 +118,8 @@ def lib():
                 "zero_block_join": [vp, vp, vp, vp, vp, vp],
                 "zero_block_join_workspace_bytes": [vp, i64p],
                 "zero_block_join_backward": [vp, vp, vp, vp, vp, vp, vp, i64, vp],
-                "zero_expert_sort": [vp, i32, i64, i32, i32, vp, vp, vp, vp],
+                "zero_expert_sort": [vp, i32, i64, i32, i32, vp, vp, vp, vp, i64, vp],
+                "zero_expert_sort_workspace_bytes": [i64, i32, i32, i64p],
                 "zero_expert_dispatch": [vp, i64, ctypes.c_int, i64, i32, i64, vp, i32, vp, vp,
                                          vp],
                 "zero_expert_dispatch_backward": [vp, ctypes.c_int, i64, i32, i64, vp, vp, vp],
