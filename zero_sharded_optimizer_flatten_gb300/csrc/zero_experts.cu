@@ -235,14 +235,22 @@ struct SortShape {
 };
 
 // ---------------------------------------------------------------------------
-// The rows.  A group of 4 to 256 lanes takes a token, octet by octet
+// The rows.  A group of 8 to 256 lanes takes a token, octet by octet
 // (16-byte aligned rows) or eight single columns at a time, `lanes` apart.
-// Four rows' octets are in flight in a thread: 1, 2 or 4 choices times 4, 2
-// or 1 octets of each, by topk.  (One at a time, the combination of two of 64
-// experts' rows of 4096 bf16, 16384 tokens, took 85 us; with more than four
-// the registers cost more than the loads gained, 138 us.)
+// The rows of all its choices are in flight together, up to 4 (MORE: 4 at a
+// time).  (One after the other, the combination of two of 64 experts'
+// rows of 4096 bf16, 16384 tokens, took 85 us; together 75; with two columns'
+// parts of each as well the registers cost more than the loads gained, 102.)
 
 constexpr int kRowThreads = 256;
+constexpr int kTogether = 4;
+
+// CTAs of an SM that K rows' octets leave registers for; single columns need
+// a register each.
+constexpr int row_ctas(bool vec, int k, size_t elem, int most) {
+  const int held = vec ? k * static_cast<int>(elem) : 4 * k;  // of a row's eight columns, in pairs of registers
+  return held >= 32 ? 2 : held >= 16 ? 3 : held >= 8 ? 4 : most;
+}
 
 struct RowArgs {
   const void* in;          // x, ys, dxs or dy
@@ -341,9 +349,9 @@ struct Choices {
   }
 };
 
-template <class T, bool VEC, int K>
-__global__ void __launch_bounds__(kRowThreads, VEC ? 5 : 3) k_dispatch(const RowArgs a) {
-  constexpr int kParts = 4 / K;
+template <class T, bool VEC, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads, VEC ? 6 : 3) k_dispatch(const RowArgs a) {
+  constexpr int kParts = K == 1 ? 2 : 1;
   const Place<VEC> me(a.lanes);
   if (me.token >= a.tokens) return;
   const int H = static_cast<int>(a.hidden);
@@ -363,7 +371,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 5 : 3) k_dispatch(const Row
 #pragma unroll
       for (int i = 0; i < K; ++i)
         if (ch.row[i] >= 0) v[q].copy_to(xs + ch.row[i] * static_cast<int64_t>(H), c, me.lanes, H);
-      for (int k = K; k < a.topk; ++k) {
+      for (int k = K; MORE && k < a.topk; ++k) {
         const int64_t r = __ldg(a.rows + p0 + k);
         if (r >= 0) v[q].copy_to(xs + r * H, c, me.lanes, H);
       }
@@ -372,16 +380,16 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 5 : 3) k_dispatch(const Row
   clear_past_end<T, VEC>(a, me, xs);
 }
 
-template <class T, bool VEC, int K>
-__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) k_combine(const RowArgs a) {
-  constexpr int kParts = 4 / K;
+template <class T, bool VEC, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 6)) k_combine(const RowArgs a) {
+  constexpr int kParts = K == 1 ? 2 : 1;
   const Place<VEC> me(a.lanes);
   if (me.token >= a.tokens) return;
   const int H = static_cast<int>(a.hidden);
   const T* in = static_cast<const T*>(a.in);
   T* y = static_cast<T*>(a.out) + me.token * H;
   const int64_t p0 = me.token * a.topk;
-  const Choices<K> first(a, p0, 0, true);
+  const Choices<K> first(a, p0, 0, !MORE);
   for (int c0 = me.first; c0 < H; c0 += kParts * me.round) {
     float s[kParts][8];
 #pragma unroll
@@ -407,16 +415,20 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) k_combine(const RowA
             for (int n = 0; n < 8; ++n) s[q][n] = fmaf(ch.weight[i], f[n], s[q][n]);
           }
     };
-    add(first);
-    for (int k0 = K; k0 < a.topk; k0 += K) add(Choices<K>(a, p0, k0, true));
+    if constexpr (MORE) {
+#pragma unroll 1
+      for (int k0 = 0; k0 < a.topk; k0 += K) add(Choices<K>(a, p0, k0, true));
+    } else {
+      add(first);
+    }
 #pragma unroll
     for (int q = 0; q < kParts; ++q)
       if (c0 + q * me.round < H) Cols<T, VEC>::store(y, c0 + q * me.round, me.lanes, H, s[q]);
   }
 }
 
-template <class T, bool VEC, int K>
-__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) k_combine_backward(const RowArgs a) {
+template <class T, bool VEC, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 5)) k_combine_backward(const RowArgs a) {
   __shared__ float part[2][K][kRowThreads / 32];
   const Place<VEC> me(a.lanes);
   const bool live = me.token < a.tokens;  // every thread meets the barriers below
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) k_combine_backward(c
   T* dys = static_cast<T*>(a.out);
   const int64_t p0 = (live ? me.token : 0) * a.topk;
   int flip = 0;
-  for (int k0 = 0; k0 < a.topk; k0 += K, flip ^= 1) {
+  for (int k0 = 0; k0 == 0 || (MORE && k0 < a.topk); k0 += K, flip ^= 1) {
     const Choices<K> ch(a, p0, k0, live);
     float dot[K] = {};
     if (live) {
@@ -485,27 +497,28 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) k_combine_backward(c
 
 enum class RowOp { kDispatch, kCombine, kCombineBackward };
 
-template <class T, bool VEC, int K>
+template <class T, bool VEC, int K, bool MORE>
 int launch_rows_k(RowOp op, const RowArgs& a, cudaStream_t s) {
   // lanes of a token's group: one octet (eight columns) each for as long a
-  // row as the CTA allows, a power of two; the gradient's dot wants K lanes
+  // row as the CTA allows, a power of two; the gradient's dots want a lane each
   RowArgs copy = a;
-  copy.lanes = 4;
+  copy.lanes = 8;
   while (copy.lanes < kRowThreads && static_cast<int64_t>(copy.lanes) * 8 < a.hidden) copy.lanes *= 2;
   const int64_t per_cta = kRowThreads / copy.lanes;
   const int64_t grid = (a.tokens + per_cta - 1) / per_cta;
   void* args[] = {&copy};
-  const void* fn = op == RowOp::kDispatch  ? reinterpret_cast<const void*>(&k_dispatch<T, VEC, K>)
-                   : op == RowOp::kCombine ? reinterpret_cast<const void*>(&k_combine<T, VEC, K>)
-                                           : reinterpret_cast<const void*>(&k_combine_backward<T, VEC, K>);
+  const void* fn = op == RowOp::kDispatch  ? reinterpret_cast<const void*>(&k_dispatch<T, VEC, K, MORE>)
+                   : op == RowOp::kCombine ? reinterpret_cast<const void*>(&k_combine<T, VEC, K, MORE>)
+                                           : reinterpret_cast<const void*>(&k_combine_backward<T, VEC, K, MORE>);
   return static_cast<int>(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), args, 0, s));
 }
 
 template <class T, bool VEC>
 int launch_rows(RowOp op, const RowArgs& a, cudaStream_t s) {
-  return a.topk == 1   ? launch_rows_k<T, VEC, 1>(op, a, s)
-         : a.topk == 2 ? launch_rows_k<T, VEC, 2>(op, a, s)
-                       : launch_rows_k<T, VEC, 4>(op, a, s);
+  return a.topk == 1           ? launch_rows_k<T, VEC, 1, false>(op, a, s)
+         : a.topk == 2         ? launch_rows_k<T, VEC, 2, false>(op, a, s)
+         : a.topk <= kTogether ? launch_rows_k<T, VEC, kTogether, false>(op, a, s)
+                               : launch_rows_k<T, VEC, kTogether, true>(op, a, s);
 }
 
 template <class T>
