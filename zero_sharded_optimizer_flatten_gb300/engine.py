@@ -42,6 +42,11 @@ NVLink-C2C (no host synchronisation).  Both give the device engine's results
 bit for bit.  ``host_threads`` sets the CPU optimizer's threads (0: every
 hardware thread but one).
 
+Without ``amp``, ``clip_grad_norm(max_norm)`` between the last backward and
+``step()`` takes the global norm of the reduced gradient over every rank's
+shard and scales the shards (the ds_config's gradient_clipping for runs
+without a loss scale).
+
 The arithmetic is the library's (no compute happens here); this module only
 does bookkeeping and launches.
 """
@@ -135,6 +140,7 @@ class ZeroEngine:
             self._reduce_amp = Z.ReduceScatterBucketAmp(plan, self.grads, op, self.grad_shards,
                                                         self.hp, self.amp_state, self._workspace,
                                                         bucket_elems=B)
+        self._clips = {}
         self.step_count = 0
         self.launched_during_backward = 0
         self._current: Optional[int] = None
@@ -199,8 +205,9 @@ class ZeroEngine:
             if need == 0 and not self._launched[b] and all(self._seen):
                 self._launch(b)  # buckets of padding only
 
-    def step(self):
-        """Wait for the reductions, then AdamW + cast + all-gather."""
+    def _reductions_done(self):
+        """Every bucket's reduction is launched, and the current stream waits
+        for them."""
         if not all(self._seen):
             missing = [q for q in range(self.n_ranks) if not self._seen[q]]
             raise RuntimeError(f"ranks {missing} did not run backward in this iteration")
@@ -210,6 +217,27 @@ class ZeroEngine:
                                    "received no gradient?)")
         if self.reduction_stream is not None:
             torch.cuda.current_stream().wait_stream(self.reduction_stream)
+
+    def clip_grad_norm(self, max_norm: float, kind: str = "l2") -> torch.Tensor:
+        """Scale the reduced gradient by min(1, max_norm / (norm + 1e-6)) and
+        return the norm before that (a float32 tensor on the device, valid
+        until the next call; nothing waits for the host).  Call it between
+        the last backward() of an iteration and step().  An infinite or NaN
+        norm scales nothing.  With amp the step itself clips
+        (AmpConfig.max_norm)."""
+        if self.amp is not None:
+            raise RuntimeError("with amp the step clips: set AmpConfig.max_norm")
+        self._reductions_done()
+        from .train_ops import ClipGradNorm
+        call = self._clips.get(kind)
+        if call is None:  # the shards keep their buffers: marshalled once
+            call = self._clips[kind] = ClipGradNorm(self.grad_shards, max_norm, kind)
+        call.max_norm = float(max_norm)
+        return call()
+
+    def step(self):
+        """Wait for the reductions, then AdamW + cast + all-gather."""
+        self._reductions_done()
         self.step_count += 1
         if self.amp is not None and self.offload == "cpu":
             # the device decides (skip, loss scale, clipping); the host reads
