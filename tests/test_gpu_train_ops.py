@@ -789,3 +789,89 @@ def test_refusals():
                 lambda: Z.zero_expert_dispatch_backward(torch.ones(7, 16, device="cuda"), order)):
         with pytest.raises((ValueError, TypeError, Z.ZeroError)):
             bad()
+
+
+# ---------------------------------------------------------------------------
+# rows and tensors that start anywhere
+
+
+def shifted(t, by):
+    """The same values in memory that starts `by` elements after an allocation."""
+    if t is None:
+        return None
+    store = torch.full((t.numel() + by + 16,), float("nan"), dtype=t.dtype, device="cuda")
+    view = store[by:by + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("by", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("R,H", [(7, 512), (33, 96), (1, 4096), (160, 61), (12, 1536)])
+@pytest.mark.parametrize("act,res,gate_type", [(B16, B16, B16), (H16, H16, F32), (B16, F32, F32),
+                                               (F32, F32, F32)], ids=lambda t: str(t)[6:])
+def test_join_tensors_that_start_anywhere(by, R, H, act, res, gate_type):
+    """Every tensor a view at an odd offset; values past the views are NaN,
+    so a read that strays shows."""
+    v = join_inputs(R, H, act, res, F32, "full", True, True, True, by)
+    v["gate"] = v["gate"].to(gate_type)
+    check_join({k: shifted(t, by) for k, t in v.items()}, "layer")
+    v = join_inputs(R, H, act, res, act, "channel", True, True, False, by)
+    check_join({k: shifted(t, by) for k, t in v.items()}, "rms")
+
+
+@pytest.mark.parametrize("H", [100, 128, 1000, 1024, 4001])
+def test_join_aligned_and_shifted_rows_agree(H):
+    """Whole and single accesses of the same rows: the same sums in another
+    order, so equal within 2 E of a row's size."""
+    v = join_inputs(50, H, F32, F32, F32, "row", True, True, False, H)
+    params = {k: t for k, t in v.items() if k not in ("x", "b")}
+    o, n, _ = Z.zero_block_join(v["x"], v["b"], **params)
+    o2, n2, _ = Z.zero_block_join(shifted(v["x"], 1), shifted(v["b"], 3), **params)
+    close(o2, o.double(), 2 * E * top(o), "o")
+    close(n2, n.double(), 2 * E * top(n), "n")
+
+
+@pytest.mark.parametrize("by", [1, 3, 8])
+def test_expert_rows_that_start_anywhere(by):
+    T, K, n_experts = 60, 3, 7
+    for Hd, dtype in ((256, B16), (255, B16), (130, F32), (64, H16)):
+        order = Z.zero_expert_sort(choose(T, K, n_experts, by, 0.2), n_experts)
+        g = gen(by)
+        x = torch.randn(T, Hd, device="cuda", generator=g).to(dtype)
+        ys = torch.randn(T * K, Hd, device="cuda", generator=g).to(dtype)
+        w = torch.rand(T, K, device="cuda", generator=g)
+        xs = Z.zero_expert_dispatch(shifted(x, by), order)
+        assert torch.equal(xs, Z.zero_expert_dispatch(x, order))
+        y, y2 = (Z.zero_expert_combine(t, w, order) for t in (ys, shifted(ys, by)))
+        close(y2, y.double(), 2 * UNIT[dtype] * y.double().abs() + 1e-6, "y")
+        dys, dw = Z.zero_expert_combine_backward(x, ys, w, order)
+        dys2, dw2 = Z.zero_expert_combine_backward(shifted(x, by), shifted(ys, by), w, order)
+        assert torch.equal(dys, dys2)
+        close(dw2, dw.double(), E * float((x.double().abs().max() * ys.double().abs().max()) * Hd), "dw")
+
+
+@pytest.mark.parametrize("dtype", [H16, B16, F32])
+def test_grads_that_start_anywhere_stay_in_bounds(dtype):
+    """Neighbours of every view are NaN and stay so."""
+    sizes = [1, 7, 8, 9, 15, 16, 17, 31, 1023, 1025, 8191, 8192, 8193, 8199, 16385, 25000]
+    g = gen(1)
+    for by in range(8):
+        grads = [shifted((torch.randn(n, device="cuda", generator=g)).to(dtype), by) for n in sizes]
+        for out_by in (0, 1, 5):
+            out = [shifted(torch.zeros(n, device="cuda").to(B16), out_by) for n in sizes]
+            norm = float(Z.zero_clip_grad_norm(grads, 2.0, out=out))
+            ref = exact_norm(grads)
+            assert abs(norm - ref) <= NORM_TOL * ref
+            f = min(1.0, 2.0 / (ref + 1e-6))
+            for a, b in zip(grads, out):
+                close(b, a.double() * f, (a.double() * f).abs() * 3e-6, "out")
+                base = b._base
+                assert bool(torch.isnan(base[:out_by]).all())
+                assert bool(torch.isnan(base[out_by + b.numel():]).all())
+
+
+def test_join_many_rows_of_one_cta_shape():
+    """More rows than the persistent grid holds, rows left over in a CTA's
+    groups, row gates read ahead."""
+    for R, H in ((40_001, 64), (9_999, 200), (5_003, 512), (3_001, 511)):
+        check_join(join_inputs(R, H, B16, B16, F32, "row", True, True, False, R), "rms")

@@ -477,8 +477,10 @@ template <int CAP>
 __global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_clip(const __grid_constant__ GradArgs<CAP> a) {
   __shared__ Partial part[kNormThreads / 32];
   const float coef = decide(a, part);
-  const int lo = static_cast<int>(static_cast<int64_t>(a.n_tiles) * blockIdx.x / gridDim.x);
-  const int hi = static_cast<int>(static_cast<int64_t>(a.n_tiles) * (blockIdx.x + 1) / gridDim.x);
+  // the last CTAs' tiles first: the norm read them last
+  const int block = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+  const int lo = static_cast<int>(static_cast<int64_t>(a.n_tiles) * block / gridDim.x);
+  const int hi = static_cast<int>(static_cast<int64_t>(a.n_tiles) * (block + 1) / gridDim.x);
   int q = find_grad_job(a, hi > lo ? hi - 1 : lo);
   for (int tile = hi - 1; tile >= lo; --tile) {
     while (a.jobs[q].tile_begin > tile) --q;

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) k_join_sums(const __grid_
 int join_workers(const zero_join_desc& d) {
   int64_t most = kAnyWorkers;
   if (d.hidden <= kJoinRowMost) {
-    const int threads = std::min(join_threads(d.hidden, true, true), join_threads(d.hidden, false, true));
+    const int threads = std::min(join_threads(d, true, true), join_threads(d, false, true));
     most = kSMs * std::max(1, kJoinThreadsBackward / threads);
   }
   return static_cast<int>(std::min(d.rows, most));

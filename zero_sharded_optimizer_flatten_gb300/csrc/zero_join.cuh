@@ -11,7 +11,8 @@ namespace zero {
 enum JoinSum { kSumP = 0, kSumQ, kSumS, kSumB, kJoinSums };
 
 constexpr int kJoinRowMost = 8192;         // channels of the kernels that hold rows in registers
-constexpr int kJoinNarrow = 4096;          // backward rows above it: 16 columns a thread
+constexpr int kJoinNarrow = 4096;          // rows above it: 16 columns a thread, rms
+constexpr int kJoinNarrowLayer = 2047;     // and layer norms forward
 constexpr int kJoinThreadsForward = 1024;  // threads of an SM's CTAs there
 constexpr int kJoinThreadsBackward = 768;
 

@@ -124,9 +124,18 @@ struct JoinCols {
   int tid, n;      // place in the CTA: where its slots are
   int group;       // the thread's row among the CTA's
   int hidden;
+  int whole;       // the thread's units that lie in the row
+  bool half;       // kPair: the unit after them does with its first column
   __device__ __forceinline__ int col(int k) const { return kUnit * (t + k / kUnit * T) + k % kUnit; }
-  __device__ __forceinline__ bool has(int k) const { return col(k) < hidden; }
-  __device__ __forceinline__ bool ragged() const { return !has(2 * NP - 1); }
+  __device__ __forceinline__ void count() {
+    const int units = hidden / kUnit;
+    whole = units > t ? (units - t + T - 1) / T : 0;
+    half = MAP == kPair && (hidden & 1) && units >= t && (units - t) % T == 0;
+  }
+  __device__ __forceinline__ bool has(int k) const {
+    return k / kUnit < whole || (MAP == kPair && half && k == 2 * whole);
+  }
+  __device__ __forceinline__ bool ragged() const { return whole < kUnits; }
 
   // A row's copy into its place `at` in shared memory.
   template <int TYPE>
@@ -158,7 +167,7 @@ struct JoinCols {
       }
     }
   }
-  __host__ __device__ __forceinline__ int row_bytes(int elem) const { return (hidden * elem + 15) / 16 * 16 + 16; }
+  __device__ __forceinline__ int row_bytes(int elem) const { return 2 * NP * T * elem + 16; }
 
   // The same row's columns, zero past its end (kWide: slots without a column
   // are cleared once).  row: where it was copied from.
@@ -184,22 +193,19 @@ struct JoinCols {
     } else {
       const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
       const char* p = at + group * row_bytes(B) + skip;
+      // (all the thread's columns have a place, whether the row has them or not)
       if (MAP == kPair && (skip & 3) == 0 && B == 2) {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          uint32_t w = 0;
-          if (has(2 * k + 1))
-            w = *reinterpret_cast<const uint32_t*>(p + 2 * col(2 * k));
-          else if (has(2 * k))
-            w = *reinterpret_cast<const uint16_t*>(p + 2 * col(2 * k));
-          if constexpr (B == 2) v[k] = widen2<E>(w);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(p + 2 * col(2 * k));
+          if constexpr (B == 2) v[k] = widen2<E>(has(2 * k + 1) ? w : has(2 * k) ? w & 0xffffu : 0u);
         }
       } else {
+        const E* e = reinterpret_cast<const E*>(p);
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          const E* e = reinterpret_cast<const E*>(p);
-          v[k] = f2(has(2 * k) ? Elem<E>::widen(e[col(2 * k)]) : 0.f,
-                    has(2 * k + 1) ? Elem<E>::widen(e[col(2 * k + 1)]) : 0.f);
+          const float lo = Elem<E>::widen(e[col(2 * k)]), hi = Elem<E>::widen(e[col(2 * k + 1)]);
+          v[k] = f2(has(2 * k) ? lo : 0.f, has(2 * k + 1) ? hi : 0.f);
         }
       }
     }
@@ -285,30 +291,30 @@ __device__ __forceinline__ void join_sums(float (&v)[N], float* scratch, int& fl
 #pragma unroll
     for (int k = 0; k < N; ++k)
       for (int o = lanes >> 1; o > 0; o >>= 1) v[k] += __shfl_xor_sync(kFull, v[k], o);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = warp_all_sum(v[k]);
-  float* part = scratch + flip * 64;
-  flip ^= 1;
-  if ((threadIdx.x & 31) == 0) {
+    for (int k = 0; k < N; ++k) v[k] = warp_all_sum(v[k]);
+    float* part = scratch + flip * 64;
+    flip ^= 1;
+    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) part[k * 32 + (threadIdx.x >> 5)] = v[k];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const ulonglong2* p = reinterpret_cast<const ulonglong2*>(part + k * 32);
-    F2 s[2];
-    s[0].w = p[0].x, s[1].w = p[0].y;
-#pragma unroll
-    for (int w = 1; w < QUADS; ++w) {
-      F2 q[2];
-      q[0].w = p[w].x, q[1].w = p[w].y;
-      s[0] = add2(s[0], q[0]);
-      s[1] = add2(s[1], q[1]);
+      for (int k = 0; k < N; ++k) part[k * 32 + (threadIdx.x >> 5)] = v[k];
     }
-    v[k] = sum2(add2(s[0], s[1]));
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const ulonglong2* p = reinterpret_cast<const ulonglong2*>(part + k * 32);
+      F2 s[2];
+      s[0].w = p[0].x, s[1].w = p[0].y;
+#pragma unroll
+      for (int w = 1; w < QUADS; ++w) {
+        F2 q[2];
+        q[0].w = p[w].x, q[1].w = p[w].y;
+        s[0] = add2(s[0], q[0]);
+        s[1] = add2(s[1], q[1]);
+      }
+      v[k] = sum2(add2(s[0], s[1]));
+    }
   }
 }
 
@@ -334,19 +340,26 @@ __device__ __forceinline__ void fold_vectors(const JoinArgs& a, const JoinLayout
 }
 
 // Where row r of an input lies.
+// (Row numbers and strides fit 31 bits here, so the product is one
+// instruction; their products do not.)
 template <class E>
-__device__ __forceinline__ const E* row_of(const void* p, int64_t r, int64_t stride) {
-  return static_cast<const E*>(p) + r * stride;
+__device__ __forceinline__ const E* row_of(const void* p, int r, int64_t stride) {
+  return static_cast<const E*>(p) + static_cast<int64_t>(r) * static_cast<int>(stride);
 }
-__device__ __forceinline__ const char* gate_row_of(const JoinArgs& a, int64_t r) {
-  return static_cast<const char*>(a.in.gate) + r * a.d.gate_stride * type_bytes(a.d.gate_dtype);
+template <class E>
+__device__ __forceinline__ E* out_row(void* p, int r, int64_t hidden) {
+  return static_cast<E*>(p) + static_cast<int64_t>(r) * static_cast<int>(hidden);
+}
+__device__ __forceinline__ const char* gate_row_of(const JoinArgs& a, int r) {
+  return static_cast<const char*>(a.in.gate) +
+         static_cast<int64_t>(r) * static_cast<int>(a.d.gate_stride) * type_bytes(a.d.gate_dtype);
 }
 
 // Row r's inputs into stage `stage`.
 template <class A, class R, bool OWN, int MAP, int NP>
 __device__ __forceinline__ void fetch_row(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
-                                          char* ring, int stage, int64_t r) {
-  if (r < a.d.rows) {
+                                          char* ring, int stage, int r) {
+  if (r < static_cast<int>(a.d.rows)) {
     char* s = ring + stage * l.stage_bytes;
     c.template fetch<Elem<R>::kType>(s + l.x, row_of<R>(a.in.x, r, a.d.x_stride), a.in.x, l.x_end);
     if (l.b >= 0)
@@ -365,11 +378,18 @@ __device__ __forceinline__ void fetch_row(const JoinArgs& a, const JoinLayout& l
   copies_commit();
 }
 
+// A row's own gate (1 without one), loaded a row ahead.
+template <bool OWN>
+__device__ __forceinline__ float own_gate(const JoinArgs& a, int r) {
+  if (!OWN || a.d.gate_kind != ZERO_GATE_ROW || r >= static_cast<int>(a.d.rows)) return 1.f;
+  return load_any(a.in.gate, static_cast<int64_t>(r) * static_cast<int>(a.d.gate_stride), a.d.gate_dtype);
+}
+
 // y w1: what multiplies the normalised block output, and y itself where rows
-// or elements have their own gates (OWN).
+// (`own`) or elements have their own gates (OWN).
 template <class A, bool OWN, int MAP, int NP>
 __device__ __forceinline__ void row_gate(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
-                                         const char* stage, const char* vec, int64_t r, F2 (&y)[NP],
+                                         const char* stage, const char* vec, int r, float own, F2 (&y)[NP],
                                          F2 (&w)[NP]) {
   c.vector(vec + l.w1, w);
   if constexpr (OWN) {
@@ -379,7 +399,7 @@ __device__ __forceinline__ void row_gate(const JoinArgs& a, const JoinLayout& l,
       else
         c.template read<A>(stage + l.gate, gate_row_of(a, r), y);
     } else {
-      const F2 one = f2(load_any(a.in.gate, r * a.d.gate_stride, a.d.gate_dtype));
+      const F2 one = f2(own);
 #pragma unroll
       for (int k = 0; k < NP; ++k) y[k] = one;
     }
@@ -393,7 +413,7 @@ __device__ __forceinline__ void row_gate(const JoinArgs& a, const JoinLayout& l,
 // kWide refills its own slots later, when it has read them.
 template <class A, class R, bool OWN, bool MANY, int MAP, int NP>
 __device__ __forceinline__ void ring_step(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
-                                          char* ring, int stage, int64_t r, int64_t step) {
+                                          char* ring, int stage, int r, int step) {
   auto meet = [] {  // the threads of a row
     if constexpr (MANY)
       __syncwarp();
@@ -416,7 +436,7 @@ __device__ __forceinline__ void ring_step(const JoinArgs& a, const JoinLayout& l
 }
 template <class A, class R, bool OWN, int MAP, int NP>
 __device__ __forceinline__ void ring_start(const JoinArgs& a, const JoinLayout& l, const JoinCols<MAP, NP>& c,
-                                           char* ring, int64_t r, int64_t step) {
+                                           char* ring, int r, int step) {
   const int ahead = JoinCols<MAP, NP>::kWide ? l.stages : l.stages - 1;
   for (int s = 0; s < ahead; ++s) fetch_row<A, R, OWN>(a, l, c, ring, s, r + s * step);
 }
@@ -462,7 +482,7 @@ struct JoinCta {
   float* scratch;
   char *vec, *ring;
   JoinCols<MAP, NP> c;
-  int64_t first, step;  // rows: first + group + i * step, while first + i * step is one
+  int first, step, rows;  // the CTA's rows: first + group + i * step, while first + i * step is one
   __device__ __forceinline__ JoinCta(const JoinArgs& a, const JoinLayout& l, char* smem) {
     scratch = reinterpret_cast<float*>(smem);
     vec = smem + kJoinScratch;
@@ -472,8 +492,10 @@ struct JoinCta {
     c.group = MANY ? tid / l.lanes : 0;
     c.t = MANY ? tid % l.lanes : tid, c.T = MANY ? l.lanes : n, c.tid = tid, c.n = n;
     c.hidden = static_cast<int>(a.d.hidden);
-    first = static_cast<int64_t>(blockIdx.x) * groups;
-    step = static_cast<int64_t>(gridDim.x) * groups;
+    c.count();
+    first = static_cast<int>(blockIdx.x) * groups;
+    step = static_cast<int>(gridDim.x) * groups;
+    rows = static_cast<int>(a.d.rows);
     // sums of warps the CTA lacks, and slots of columns a row lacks
     for (int i = tid; i < kJoinScratch / 4; i += n) scratch[i] = 0.f;
     if constexpr (JoinCols<MAP, NP>::kWide)
@@ -495,10 +517,13 @@ __global__ void __launch_bounds__(MAXT, NP == 4 ? kJoinThreadsForward / MAXT : 5
   int flip = 0, stage = 0;
   ring_start<A, R, OWN>(a, l, c, cta.ring, cta.first + c.group, cta.step);
   fold_vectors(a, l, c, cta.vec);
-  for (int64_t base = cta.first; base < a.d.rows; base += cta.step) {
+  float next_own = own_gate<OWN>(a, cta.first + c.group);
+  for (int base = cta.first; base < cta.rows; base += cta.step) {
+    const float own = next_own;
+    next_own = own_gate<OWN>(a, base + c.group + cta.step);
     // a group past the last row works on it once more and writes nothing
-    const int64_t r = kMany ? min(base + c.group, a.d.rows - 1) : base;
-    const bool live = !kMany || base + c.group < a.d.rows;
+    const int r = kMany ? min(base + c.group, cta.rows - 1) : base;
+    const bool live = !kMany || base + c.group < cta.rows;
     ring_step<A, R, OWN, kMany>(a, l, c, cta.ring, stage, base + c.group, cta.step);
     const char* in = cta.ring + stage * l.stage_bytes;
     F2 o[NP];
@@ -508,7 +533,7 @@ __global__ void __launch_bounds__(MAXT, NP == 4 ? kJoinThreadsForward / MAXT : 5
       F2 v[NP], y[NP], w[NP];
       c.template read<A>(in + l.b, row_of<A>(a.in.b, r, a.d.b_stride), v);
       if (a.in.w_post) normalise<LAYER, kQuads>(a, c, cta.scratch, flip, v, mb, rb);
-      row_gate<A, OWN>(a, l, c, in, cta.vec, r, y, w);
+      row_gate<A, OWN>(a, l, c, in, cta.vec, r, own, y, w);
 #pragma unroll
       for (int k = 0; k < NP; ++k) o[k] = fma2(w[k], v[k], o[k]);
       if (LAYER && l.b1 >= 0) {
@@ -520,7 +545,7 @@ __global__ void __launch_bounds__(MAXT, NP == 4 ? kJoinThreadsForward / MAXT : 5
     // this thread has read its slots of the stage: the row `stages` ahead
     if constexpr (kWide) fetch_row<A, R, OWN>(a, l, c, cta.ring, stage, base + c.group + l.stages * cta.step);
     stage = stage + 1 == l.stages ? 0 : stage + 1;
-    if (a.o && live) c.write(static_cast<R*>(a.o) + r * a.d.hidden, o);
+    if (a.o && live) c.write(out_row<R>(a.o, r, a.d.hidden), o);
     if (a.in.w_pre) {
       normalise<LAYER, kQuads>(a, c, cta.scratch, flip, o, mo, ro);
       if (a.n && live) {
@@ -535,7 +560,7 @@ __global__ void __launch_bounds__(MAXT, NP == 4 ? kJoinThreadsForward / MAXT : 5
 #pragma unroll
           for (int k = 0; k < NP; ++k) o[k] = mul2(o[k], w[k]);
         }
-        c.write(static_cast<A*>(a.n) + r * a.d.hidden, o);
+        c.write(out_row<A>(a.n, r, a.d.hidden), o);
       }
     }
     if (a.stats && live && c.t == 0) a.stats[r] = make_float4(mb, rb, mo, ro);
@@ -565,7 +590,7 @@ __device__ __forceinline__ void norm_means(const JoinArgs& a, const JoinCols<MAP
 }
 
 template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT, int NP>
-__global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_constant__ JoinArgs a,
+__global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_rows_backward(const __grid_constant__ JoinArgs a,
                                                              const __grid_constant__ JoinLayout l) {
   extern __shared__ __align__(16) char smem[];
   constexpr bool kMany = MAXT == kJoinSmallCta;  // several rows a CTA
@@ -581,12 +606,15 @@ __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_consta
   F2 P[NP], Q[NP], S[NP], B[NP];
   clear(P), clear(Q), clear(S), clear(B);
   float4 st = make_float4(0.f, 1.f, 0.f, 1.f);
-  if (a.stats && cta.first < a.d.rows) st = __ldg(a.stats + min(cta.first + c.group, a.d.rows - 1));
-  for (int64_t base = cta.first; base < a.d.rows; base += cta.step) {
-    const int64_t r = kMany ? min(base + c.group, a.d.rows - 1) : base;
-    const bool live = !kMany || base + c.group < a.d.rows;
+  if (a.stats && cta.first < cta.rows) st = __ldg(a.stats + min(cta.first + c.group, cta.rows - 1));
+  float next_own = own_gate<OWN>(a, cta.first + c.group);
+  for (int base = cta.first; base < cta.rows; base += cta.step) {
+    const float own = next_own;
+    next_own = own_gate<OWN>(a, base + c.group + cta.step);
+    const int r = kMany ? min(base + c.group, cta.rows - 1) : base;
+    const bool live = !kMany || base + c.group < cta.rows;
     const float4 now = st;
-    if (a.stats) st = __ldg(a.stats + min(r + cta.step, a.d.rows - 1));  // the next row's
+    if (a.stats) st = __ldg(a.stats + min(r + cta.step, cta.rows - 1));  // the next row's
     ring_step<A, R, OWN, kMany>(a, l, c, cta.ring, stage, base + c.group, cta.step);
     const char* in = cta.ring + stage * l.stage_bytes;
     F2 go[NP], bh[NP], y[NP];
@@ -603,7 +631,7 @@ __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_consta
       }
     }
     F2 w1[NP];
-    if (a.in.b) row_gate<A, OWN>(a, l, c, in, cta.vec, r, y, w1);
+    if (a.in.b) row_gate<A, OWN>(a, l, c, in, cta.vec, r, own, y, w1);
     if (a.d_n) {
       F2 oh[NP], t[NP], w[NP];
       c.template read<R>(in + l.x, row_of<R>(a.in.x, r, a.d.x_stride), oh);
@@ -639,7 +667,7 @@ __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_consta
     }
     if constexpr (kWide) fetch_row<A, R, OWN>(a, l, c, cta.ring, stage, base + c.group + l.stages * cta.step);
     stage = stage + 1 == l.stages ? 0 : stage + 1;
-    if (a.dx && live) c.write(static_cast<R*>(a.dx) + r * a.d.hidden, go);
+    if (a.dx && live) c.write(out_row<R>(a.dx, r, a.d.hidden), go);
     if (!a.in.b) continue;
     if (live) {
 #pragma unroll
@@ -664,7 +692,7 @@ __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_consta
         u[k] = mul2(u[k], go[k]);
         sum = add2(sum, u[k]);
       }
-      if (gate_full && live) c.write_any(a.dgate, r * a.d.hidden, a.d.gate_dtype, u);
+      if (gate_full && live) c.write_any(a.dgate, static_cast<int64_t>(r) * static_cast<int>(a.d.hidden), a.d.gate_dtype, u);
       if (gate_row) {
         float s[1] = {sum2(sum)};
         join_sums<kQuads>(s, cta.scratch, flip, c.T);
@@ -685,7 +713,7 @@ __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_consta
         go[k] = mul2(e, rr);
       }
     }
-    if (live) c.write(static_cast<A*>(a.db) + r * a.d.hidden, go);
+    if (live) c.write(out_row<A>(a.db, r, a.d.hidden), go);
   }
   copies_wait(0);
   if (a.n_sums == 0) return;
@@ -719,24 +747,34 @@ __global__ void __launch_bounds__(MAXT) k_join_rows_backward(const __grid_consta
 // ---------------------------------------------------------------------------
 // host: the layout and the launch of one type pair
 
-// Columns of a thread.  16 halve what a row costs beside its columns: taken
-// for rows of a warp or less (up to 512 channels then need no barrier), and
-// for the longer rows backward, where they leave 128 registers a thread.
-// Rows that start anywhere keep 8: their element accesses need the threads.
-inline int join_columns(int64_t hidden, bool wide, bool backward) {
-  return wide && (hidden <= 512 || (backward && hidden > kJoinNarrow)) ? 16 : 8;
+// Columns of a thread, 8 or 16.  16 halve what a row costs beside its columns
+// and take twice the registers.  Measured, bf16, with 8 and with 16:
+//   rows of a warp or less (16 let up to 512 channels go without a barrier):
+//     65536 x 256, rms, backward 74 -> 56 us;
+//   8192 x 8192, rms: forward 107 -> 90, backward 267 -> 197;
+//   16384 x 4096, rms: forward 92 -> 102, backward 156 -> 159: no gain;
+//   16384 x 4096, layer norms (four sums a row) forward 135 -> 118.
+// Backward layer norms hold four column sums, and rows' or elements' own gates
+// their values: they spill with 16 (layer, 16384 x 4096: 193 -> 348).  Rows
+// that start anywhere keep 8: their element accesses need the threads.
+inline int join_columns(const zero_join_desc& d, bool wide, bool backward) {
+  const bool layer = d.kind == ZERO_JOIN_LAYER;
+  const bool own = d.gate_kind == ZERO_GATE_ROW || d.gate_kind == ZERO_GATE_FULL;
+  if (!wide || (backward && layer)) return 8;
+  if (d.hidden <= 512) return backward && own ? 8 : 16;
+  return d.hidden > (layer ? kJoinNarrowLayer : kJoinNarrow) ? 16 : 8;
 }
 
 // Threads of a row, and of a CTA.
-inline int join_lanes(int64_t hidden, bool wide, bool backward) {
-  const int64_t warp = 32 * join_columns(hidden, wide, backward);
+inline int join_lanes(const zero_join_desc& d, bool wide, bool backward) {
+  const int64_t hidden = d.hidden, warp = 32 * join_columns(d, wide, backward);
   if (hidden * 8 <= warp) return 4;
   if (hidden * 4 <= warp) return 8;
   if (hidden * 2 <= warp) return 16;
   return static_cast<int>((hidden + warp - 1) / warp * 32);
 }
-inline int join_threads(int64_t hidden, bool wide, bool backward) {
-  const int lanes = join_lanes(hidden, wide, backward);
+inline int join_threads(const zero_join_desc& d, bool wide, bool backward) {
+  const int lanes = join_lanes(d, wide, backward);
   return lanes <= 32 ? kJoinSmallCta : lanes;
 }
 
@@ -766,8 +804,8 @@ bool join_wide(const JoinArgs& a) {
 inline JoinLayout join_layout(const JoinArgs& a, bool wide, bool backward, int ctas) {
   JoinLayout l = {};
   const zero_join_desc& d = a.d;
-  l.lanes = join_lanes(d.hidden, wide, backward);
-  const int threads = join_threads(d.hidden, wide, backward), slots = threads * join_columns(d.hidden, wide, backward);
+  l.lanes = join_lanes(d, wide, backward);
+  const int threads = join_threads(d, wide, backward), slots = threads * join_columns(d, wide, backward);
   auto vector = [&](bool present) {
     if (!present) return -1;
     const int at = l.vec_bytes;
@@ -782,8 +820,7 @@ inline JoinLayout join_layout(const JoinArgs& a, bool wide, bool backward, int c
   auto row = [&](const void* p, int type, int64_t stride, const char** end) {
     if (!p) return -1;
     const int at = l.stage_bytes, bytes = type_bytes(type);
-    l.stage_bytes += wide ? slots * bytes
-                          : static_cast<int>((d.hidden * bytes + 15) / 16 * 16 + 16) * (threads / l.lanes);
+    l.stage_bytes += slots * bytes + (wide ? 0 : 16 * (threads / l.lanes));  // room for a row's offset
     *end = static_cast<const char*>(p) + ((d.rows - 1) * stride + d.hidden) * bytes;
     return at;
   };
@@ -804,8 +841,8 @@ inline int join_smem(const JoinLayout& l) { return kJoinScratch + l.vec_bytes + 
 template <int MAXT>
 int launch_join_rows_fn(const void* fn, std::atomic<int>* known, const JoinArgs& a, bool wide, bool backward,
                         int* workers, cudaStream_t s) {
-  const int threads = join_threads(a.d.hidden, wide, backward);
-  const int groups = threads / join_lanes(a.d.hidden, wide, backward);
+  const int threads = join_threads(a.d, wide, backward);
+  const int groups = threads / join_lanes(a.d, wide, backward);
   int fit = known[threads / 32].load(std::memory_order_relaxed);
   if (fit == 0) {
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, 0);
@@ -829,49 +866,52 @@ int launch_join_rows_fn(const void* fn, std::atomic<int>* known, const JoinArgs&
   return static_cast<int>(cudaLaunchKernel(fn, dim3(grid), dim3(threads), args, join_smem(l), s));
 }
 
-template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT, int NP>
-int launch_join_rows_as(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
-  static std::atomic<int> known[2][MAXT / 32 + 1];
-  constexpr bool wide = JoinCols<MAP, NP>::kWide;
-  if (backward) {
-    // wide backward rows above 4096 have 16 columns a thread: 512 threads
-    constexpr int kMost = wide && MAXT > 512 ? 512 : MAXT;
-    return launch_join_rows_fn<kMost>(
-        reinterpret_cast<const void*>(&k_join_rows_backward<A, R, LAYER, OWN, MAP, kMost, NP>), known[1], a, wide,
-        true, workers, s);
-  }
-  return launch_join_rows_fn<MAXT>(reinterpret_cast<const void*>(&k_join_rows<A, R, LAYER, OWN, MAP, MAXT, NP>),
-                                   known[0], a, wide, false, workers, s);
+template <class A, class R, bool LAYER, bool OWN, bool BACKWARD, int MAP, int MAXT, int NP>
+int launch_join_rows_as(const JoinArgs& a, int* workers, cudaStream_t s) {
+  static std::atomic<int> known[MAXT / 32 + 1];
+  const void* fn;
+  if constexpr (BACKWARD)
+    fn = reinterpret_cast<const void*>(&k_join_rows_backward<A, R, LAYER, OWN, MAP, MAXT, NP>);
+  else
+    fn = reinterpret_cast<const void*>(&k_join_rows<A, R, LAYER, OWN, MAP, MAXT, NP>);
+  return launch_join_rows_fn<MAXT>(fn, known, a, JoinCols<MAP, NP>::kWide, BACKWARD, workers, s);
 }
 
-template <class A, class R, bool LAYER, bool OWN, int MAP>
-int launch_join_rows_map(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
+template <class A, class R, bool LAYER, bool OWN, bool BACKWARD, int MAP>
+int launch_join_rows_map(const JoinArgs& a, int* workers, cudaStream_t s) {
   constexpr bool wide = JoinCols<MAP, 4>::kWide;
-  if (join_lanes(a.d.hidden, wide, backward) <= 32)
-    return launch_join_rows_as<A, R, LAYER, OWN, MAP, kJoinSmallCta, wide ? 8 : 4>(a, backward, workers, s);
-  if constexpr (wide)
-    if (backward && join_columns(a.d.hidden, true, true) == 16) {
-      static std::atomic<int> known[17];
-      return launch_join_rows_fn<512>(
-          reinterpret_cast<const void*>(&k_join_rows_backward<A, R, LAYER, OWN, MAP, 512, 8>), known, a, true, true,
-          workers, s);
-    }
-  if (join_threads(a.d.hidden, wide, backward) <= 512)
-    return launch_join_rows_as<A, R, LAYER, OWN, MAP, 512, 4>(a, backward, workers, s);
-  return launch_join_rows_as<A, R, LAYER, OWN, MAP, 1024, 4>(a, backward, workers, s);
+  // what join_columns can say for these kernels
+  constexpr bool long16 = wide && !(BACKWARD && LAYER), short16 = long16 && !(BACKWARD && OWN);
+  if (join_lanes(a.d, wide, BACKWARD) <= 32)
+    return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, kJoinSmallCta, short16 ? 8 : 4>(a, workers, s);
+  if constexpr (long16)
+    if (join_columns(a.d, true, BACKWARD) == 16)
+      return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 512, 8>(a, workers, s);
+  if constexpr (!long16)
+    if (join_threads(a.d, wide, BACKWARD) > 512)
+      return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 1024, 4>(a, workers, s);
+  return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 512, 4>(a, workers, s);
 }
 
 template <class A, class R, bool LAYER, bool OWN>
 int launch_join_rows_kind(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
   constexpr bool k16 = sizeof(A) == 2 && sizeof(R) == 2;
-  if (join_wide<A, R>(a)) return launch_join_rows_map<A, R, LAYER, OWN, k16 ? kOct : kQuad>(a, backward, workers, s);
-  return launch_join_rows_map<A, R, LAYER, OWN, k16 ? kPair : kLone>(a, backward, workers, s);
+  constexpr int kWide = k16 ? kOct : kQuad, kAny = k16 ? kPair : kLone;
+  if (join_wide<A, R>(a))
+    return backward ? launch_join_rows_map<A, R, LAYER, OWN, true, kWide>(a, workers, s)
+                    : launch_join_rows_map<A, R, LAYER, OWN, false, kWide>(a, workers, s);
+  return backward ? launch_join_rows_map<A, R, LAYER, OWN, true, kAny>(a, workers, s)
+                  : launch_join_rows_map<A, R, LAYER, OWN, false, kAny>(a, workers, s);
 }
 
 // -1: these rows do not fit here.
 template <class A, class R>
 int launch_join_rows(const JoinArgs& a, bool backward, int* workers, cudaStream_t s) {
-  if (a.d.hidden > kJoinRowMost) return -1;
+  const zero_join_desc& d = a.d;
+  constexpr int64_t kMost = INT64_C(1) << 30;
+  if (d.hidden > kJoinRowMost || d.rows > kMost || d.x_stride > kMost || d.b_stride > kMost ||
+      d.gate_stride > kMost || d.do_stride > kMost || d.dn_stride > kMost)
+    return -1;
   const bool own = a.d.gate_kind == ZERO_GATE_ROW || a.d.gate_kind == ZERO_GATE_FULL;
   if (a.layer)
     return own ? launch_join_rows_kind<A, R, true, true>(a, backward, workers, s)
