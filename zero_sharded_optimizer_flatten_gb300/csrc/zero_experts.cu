@@ -104,7 +104,7 @@ struct Segment {
 // Every CTA's counts for the walk of many CTAs.
 __global__ void __launch_bounds__(32 * kSortWarpsMost) k_expert_count(const SortArgs a) {
   extern __shared__ int smem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   for (int e = threadIdx.x; e < a.n_experts; e += blockDim.x) smem[e] = 0;
   __syncthreads();
   Segment(a.n, blockIdx.x, gridDim.x).walk(a, [&](int e, int64_t) {
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(32 * kSortWarpsMost) k_expert_sort(const SortA
     total[e] = s;
   }
   if constexpr (TABLE)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
   else
     cluster.sync();
   // the pairs of all CTAs below this one, and of all CTAs, expert by expert;

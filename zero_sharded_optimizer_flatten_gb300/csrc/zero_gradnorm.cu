@@ -298,10 +298,6 @@ __device__ __forceinline__ void norm_tile(const GradJob& j, int t, bool inf_norm
       });
 }
 
-// The launch that follows may start its CTAs; they wait for this grid's end.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 template <int CAP>
 __global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_norm(const __grid_constant__ GradArgs<CAP> a) {
   __shared__ Partial part[kNormThreads / 32];
@@ -539,18 +535,7 @@ int launch_pass(const Call& c, const Batch* b, int base, bool leader, bool early
   const void* fn = pass == Pass::kNorm   ? reinterpret_cast<const void*>(&k_grad_norm<CAP>)
                    : pass == Pass::kClip ? reinterpret_cast<const void*>(&k_grad_clip<CAP>)
                                          : reinterpret_cast<const void*>(&k_norm_result<CAP>);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kNormThreads);
-  cfg.stream = c.stream;
-  cudaLaunchAttribute attr[1];
-  if (early) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  const cudaError_t e = launch_maybe_early(fn, dim3(grid), dim3(kNormThreads), args, early, c.stream);
   delete a;
   if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
   return static_cast<int>(e);

@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) k_join_sums(const __grid_
   float s[kJoinSums] = {0.f, 0.f, 0.f, 0.f};
   const float* p = a.partial + c;
   const int64_t worker = a.n_sums * H;
+  wait_for_previous();
   if (c < H) {
     for (int w = threadIdx.y; w < g.workers; w += kSumAhead * kSumRows) {
       float v[kJoinSums][kSumAhead];
@@ -552,8 +553,12 @@ extern "C" zero_status zero_block_join_backward(const zero_join_desc* desc, cons
   if (rows) JOIN_TRY(launched(fn, launch_join(a, true, &workers, s)));
   if (a.n_sums > 0) {
     JoinSumArgs g = {a, workers, grads->dw_pre, grads->dbias_pre, grads->dw_post, grads->dbias_post, dgate};
-    k_join_sums<<<static_cast<unsigned>((d.hidden + kSumCols - 1) / kSumCols), dim3(kSumCols, kSumRows), 0, s>>>(g);
-    JOIN_TRY(launched(fn, static_cast<int>(cudaGetLastError())));
+    void* args[] = {&g};
+    const int e = static_cast<int>(
+        launch_maybe_early(reinterpret_cast<const void*>(&k_join_sums),
+                           dim3(static_cast<unsigned>((d.hidden + kSumCols - 1) / kSumCols)),
+                           dim3(kSumCols, kSumRows), args, rows, s));
+    JOIN_TRY(launched(fn, e));
   }
   return ZERO_OK;
 }

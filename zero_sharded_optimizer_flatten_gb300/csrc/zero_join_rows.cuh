@@ -3,7 +3,7 @@
 //
 // Row split.  Above 256 channels a CTA of whole warps takes a row at a time; a
 // row's sums go through one shuffle tree a warp and one barrier.  Shorter rows
-// (up to 512 channels with 16 columns a thread) are taken by 4 to 32 lanes
+// (up to 512 channels with 16 columns a thread) are taken by 8 to 32 lanes
 // and a CTA of 128 threads has several.  Rows are handed out grid-stride.
 //
 // Column maps.  A thread's columns come in units of u neighbours, unit j of
@@ -46,7 +46,7 @@ namespace zero {
 
 constexpr int kJoinStagesMost = 4;
 constexpr int kJoinSmemMost = 224 * 1024;  // of one SM's CTAs together
-constexpr int kJoinScratch = 2 * 2 * 32 * 4;  // two buffers of two sums a warp
+constexpr int kJoinScratch = 2 * 8 * 32 * 4;  // two buffers of eight sums a warp
 constexpr int kJoinSmallCta = 128;         // threads of a CTA of several rows
 
 enum JoinMap { kOct, kQuad, kPair, kLone };
@@ -294,7 +294,7 @@ __device__ __forceinline__ void join_sums(float (&v)[N], float* scratch, int& fl
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = warp_all_sum(v[k]);
-    float* part = scratch + flip * 64;
+    float* part = scratch + flip * 256;
     flip ^= 1;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
@@ -567,42 +567,76 @@ __global__ void __launch_bounds__(MAXT, NP == 4 ? kJoinThreadsForward / MAXT : 5
   }
 }
 
-// Sum of e (layer only) and of e h over the row, over -hidden: what leaves
-// e's gradient through a norm of normalised row h.
-template <bool LAYER, int QUADS, int MAP, int NP>
-__device__ __forceinline__ void norm_means(const JoinArgs& a, const JoinCols<MAP, NP>& c, float* scratch,
-                                           int& flip, const F2 (&e)[NP], const F2 (&h)[NP], F2& s0, F2& s1) {
-  F2 p = mul2(e[0], h[0]), q = e[0];
+// Totals over a row's lanes (of a warp) of N values, N a power of two and at
+// most the lanes: lane (lanes / N) k of the row holds value k's.  Halves are
+// exchanged while a lane has several values, so eight values take 9 shuffles
+// over 32 lanes and not 40.
+template <int N>
+__device__ __forceinline__ float scatter_sums(float (&v)[N], int lanes) {
+  const int lane = threadIdx.x & 31;
+  int o = lanes >> 1;
 #pragma unroll
-  for (int k = 1; k < NP; ++k) {
-    if (LAYER) q = add2(q, e[k]);
-    p = fma2(e[k], h[k], p);
+  for (int n = N / 2; n > 0; n /= 2, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = upper ? v[i + n] : v[i], send = upper ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(kFull, send, o);
+    }
   }
-  if constexpr (LAYER) {
-    float s[2] = {sum2(p), sum2(q)};
-    join_sums<QUADS>(s, scratch, flip, c.T);
-    s1 = f2(-s[0] * a.inv_h), s0 = f2(-s[1] * a.inv_h);
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(kFull, v[0], o);
+  return v[0];
+}
+
+// join_sums for 4 or 8 values.
+template <int QUADS, int N>
+__device__ __forceinline__ void join_many_sums(float (&v)[N], float* scratch, int& flip, int lanes) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (QUADS == 1) {
+    const float total = scatter_sums(v, lanes);
+    const int first = lane & ~(lanes - 1), apart = lanes / N;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(kFull, total, first + k * apart);
   } else {
-    float s[1] = {sum2(p)};
-    join_sums<QUADS>(s, scratch, flip, c.T);
-    s1 = f2(-s[0] * a.inv_h);
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float* part = scratch + flip * 256;
+    flip ^= 1;
+    const float mine = scatter_sums(v, 32);
+    if (lane % (32 / N) == 0) part[warp * N + lane / (32 / N)] = mine;
+    __syncthreads();
+    const float4* p = reinterpret_cast<const float4*>(part + lane * N);
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+      const float4 q = lane < warps ? p[k / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
+    }
+    const float total = scatter_sums(v, 32);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(kFull, total, k * (32 / N));
   }
 }
 
+// The backward pass of a row in one round of sums.  With e = w1 bh (the
+// block's part of o without its own gate), h = oh and g' = do + R_o t, the
+// gradient of o is go = g' - R_o (mean(t) + h mean(t h)), so the sums over go
+// that the post norm needs follow from sums over g':
+//   sum e go = sum e g' - R_o mean(t) sum e - R_o mean(t h) sum e h,
+// and the same with w1 in place of e (layer only, as mean(t) is).  One barrier
+// a row in place of two: 16384 x 4096 bf16 took 156 us with two.
 template <class A, class R, bool LAYER, bool OWN, int MAP, int MAXT, int NP>
-__global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_rows_backward(const __grid_constant__ JoinArgs a,
-                                                             const __grid_constant__ JoinLayout l) {
+__global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_rows_backward(
+    const __grid_constant__ JoinArgs a, const __grid_constant__ JoinLayout l) {
   extern __shared__ __align__(16) char smem[];
   constexpr bool kMany = MAXT == kJoinSmallCta;  // several rows a CTA
   constexpr int kQuads = MAXT / 128;              // a row's warps in fours
   constexpr bool kWide = JoinCols<MAP, NP>::kWide;
+  let_next_start();  // the column sums' launch
   JoinCta<MAP, NP, kMany> cta(a, l, smem);
   const JoinCols<MAP, NP>& c = cta.c;
   int flip = 0, stage = 0;
   ring_start<A, R, OWN>(a, l, c, cta.ring, cta.first + c.group, cta.step);
   fold_vectors(a, l, c, cta.vec);
-  const bool gate_row = OWN && a.d.gate_kind == ZERO_GATE_ROW && a.dgate;
-  const bool gate_full = OWN && a.d.gate_kind == ZERO_GATE_FULL && a.dgate;
+  const bool full = OWN && a.d.gate_kind == ZERO_GATE_FULL, post = a.in.w_post != nullptr;
   F2 P[NP], Q[NP], S[NP], B[NP];
   clear(P), clear(Q), clear(S), clear(B);
   float4 st = make_float4(0.f, 1.f, 0.f, 1.f);
@@ -617,28 +651,44 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
     if (a.stats) st = __ldg(a.stats + min(r + cta.step, cta.rows - 1));  // the next row's
     ring_step<A, R, OWN, kMany>(a, l, c, cta.ring, stage, base + c.group, cta.step);
     const char* in = cta.ring + stage * l.stage_bytes;
-    F2 go[NP], bh[NP], y[NP];
+    F2 go[NP], bh[NP], y[NP], oh[NP];
+    // sums: t oh, e g', e oh; t, w1 g', w1 oh, e, w1 (layer)
+    constexpr int N = LAYER ? 8 : 4;
+    float s[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = 0.f;
+    clear(oh);
     if (a.d_o)
       c.template read<R>(in + l.d_o, row_of<R>(a.d_o, r, a.d.do_stride), go);
     else
       clear(go);
     if (a.in.b) {
       c.template read<A>(in + l.b, row_of<A>(a.in.b, r, a.d.b_stride), bh);
-      if (a.in.w_post) {
+      if (post) {
         const F2 rr = f2(now.y), m = f2(-now.x);
 #pragma unroll
         for (int k = 0; k < NP; ++k) bh[k] = mul2(LAYER ? add2(bh[k], m) : bh[k], rr);
       }
+      if (OWN) {
+        if (!full) {
+          const F2 one = f2(own);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) y[k] = one;
+        } else if (a.d.gate_dtype == ZERO_FP32) {
+          c.template read<float>(in + l.gate, gate_row_of(a, r), y);
+        } else {
+          c.template read<A>(in + l.gate, gate_row_of(a, r), y);
+        }
+      }
     }
-    F2 w1[NP];
-    if (a.in.b) row_gate<A, OWN>(a, l, c, in, cta.vec, r, own, y, w1);
     if (a.d_n) {
-      F2 oh[NP], t[NP], w[NP];
+      F2 t[NP], w[NP];
       c.template read<R>(in + l.x, row_of<R>(a.in.x, r, a.d.x_stride), oh);
       c.template read<A>(in + l.d_n, row_of<A>(a.d_n, r, a.d.dn_stride), t);
       if (a.in.b) {
+        c.vector(cta.vec + l.w1, w);
 #pragma unroll
-        for (int k = 0; k < NP; ++k) oh[k] = fma2(w1[k], bh[k], oh[k]);
+        for (int k = 0; k < NP; ++k) oh[k] = fma2(OWN ? mul2(w[k], y[k]) : w[k], bh[k], oh[k]);
         if (LAYER && l.b1 >= 0) {
           c.vector(cta.vec + l.b1, w);
 #pragma unroll
@@ -647,6 +697,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
       }
       c.vector(cta.vec + l.w2, w);
       const F2 rr = f2(now.w), m = f2(-now.z);
+      F2 s0 = f2(0.f), s1 = f2(0.f);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         oh[k] = mul2(LAYER ? add2(oh[k], m) : oh[k], rr);
@@ -655,18 +706,46 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
           if (LAYER) Q[k] = add2(Q[k], t[k]);
         }
         t[k] = mul2(t[k], w[k]);  // zero past the row's end, as dn and w2 are
+        s1 = fma2(t[k], oh[k], s1);
+        if (LAYER) s0 = add2(s0, t[k]);
+        go[k] = fma2(t[k], rr, go[k]);
       }
-      F2 s0, s1;
-      norm_means<LAYER, kQuads>(a, c, cta.scratch, flip, t, oh, s0, s1);
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        F2 e = fma2(oh[k], s1, t[k]);
-        if (LAYER) e = add2(e, s0);
-        go[k] = fma2(e, rr, go[k]);
-      }
+      s[0] = sum2(s1);
+      if constexpr (LAYER) s[3] = sum2(s0);
     }
+    // every input has been read: the row `stages` ahead
     if constexpr (kWide) fetch_row<A, R, OWN>(a, l, c, cta.ring, stage, base + c.group + l.stages * cta.step);
     stage = stage + 1 == l.stages ? 0 : stage + 1;
+    if (a.in.b && (post || OWN)) {
+      F2 w[NP], t1 = f2(0.f), t2 = f2(0.f), t4 = f2(0.f), t5 = f2(0.f), t6 = f2(0.f), t7 = f2(0.f);
+      c.vector(cta.vec + l.w1, w);  // zero past the row's end
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        if (full) w[k] = mul2(w[k], y[k]);
+        const F2 e = mul2(w[k], bh[k]);
+        t1 = fma2(e, go[k], t1);
+        t2 = fma2(e, oh[k], t2);
+        if constexpr (LAYER) {
+          t4 = fma2(w[k], go[k], t4);
+          t5 = fma2(w[k], oh[k], t5);
+          t6 = add2(t6, e);
+          t7 = add2(t7, w[k]);
+        }
+      }
+      s[1] = sum2(t1), s[2] = sum2(t2);
+      if constexpr (LAYER) s[4] = sum2(t4), s[5] = sum2(t5), s[6] = sum2(t6), s[7] = sum2(t7);
+    }
+    if (a.d_n || post || OWN) join_many_sums<kQuads>(s, cta.scratch, flip, c.T);
+    // -R_o mean(t h) and -R_o mean(t)
+    const float q1 = -now.w * (s[0] * a.inv_h), q0 = LAYER ? -now.w * (s[3 % N] * a.inv_h) : 0.f;
+    if (a.d_n) {
+      const F2 m1 = f2(q1), m0 = f2(q0);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        go[k] = fma2(oh[k], m1, go[k]);
+        if (LAYER) go[k] = add2(go[k], m0);
+      }
+    }
     if (a.dx && live) c.write(out_row<R>(a.dx, r, a.d.hidden), go);
     if (!a.in.b) continue;
     if (live) {
@@ -677,39 +756,53 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
         if (LAYER) B[k] = add2(B[k], yg);
       }
     }
-    if (gate_row || gate_full) {
-      F2 u[NP], w[NP], sum = f2(0.f);
-      c.vector(cta.vec + l.w1, w);
+    // sums over the gradient of o: e go, and w1 go
+    float e_go = fmaf(q1, s[2], s[1]), w_go = 0.f;
+    if constexpr (LAYER) {
+      e_go = fmaf(q0, s[6], e_go);
+      w_go = fmaf(q0, s[7], fmaf(q1, s[5], s[4]));
+    }
+    if constexpr (OWN) {
+      if (a.dgate) {
+        F2 u[NP], w[NP];
+        if (full) {
+          c.vector(cta.vec + l.w1, w);
 #pragma unroll
-      for (int k = 0; k < NP; ++k) u[k] = mul2(w[k], bh[k]);
-      if (LAYER && l.b1 >= 0) {
-        c.vector(cta.vec + l.b1, w);
+          for (int k = 0; k < NP; ++k) u[k] = mul2(w[k], bh[k]);
+          if (LAYER && l.b1 >= 0) {
+            c.vector(cta.vec + l.b1, w);
 #pragma unroll
-        for (int k = 0; k < NP; ++k) u[k] = add2(u[k], w[k]);
-      }
+            for (int k = 0; k < NP; ++k) u[k] = add2(u[k], w[k]);
+          }
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        u[k] = mul2(u[k], go[k]);
-        sum = add2(sum, u[k]);
-      }
-      if (gate_full && live) c.write_any(a.dgate, static_cast<int64_t>(r) * static_cast<int>(a.d.hidden), a.d.gate_dtype, u);
-      if (gate_row) {
-        float s[1] = {sum2(sum)};
-        join_sums<kQuads>(s, cta.scratch, flip, c.T);
-        if (live && c.t == 0) store_any(a.dgate, r, a.d.gate_dtype, s[0]);
+          for (int k = 0; k < NP; ++k) u[k] = mul2(u[k], go[k]);
+          if (live) c.write_any(a.dgate, static_cast<int64_t>(r) * static_cast<int>(a.d.hidden), a.d.gate_dtype, u);
+        } else {
+          float d[1] = {0.f};
+          if (LAYER && l.b1 >= 0) {  // b1 go over the row
+            F2 t = f2(0.f);
+            c.vector(cta.vec + l.b1, w);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) t = fma2(w[k], go[k], t);
+            d[0] = sum2(t);
+            join_sums<kQuads>(d, cta.scratch, flip, c.T);
+          }
+          if (live && c.t == 0) store_any(a.dgate, r, a.d.gate_dtype, e_go + d[0]);
+        }
       }
     }
     if (!a.db) continue;
+    F2 w[NP];
+    c.vector(cta.vec + l.w1, w);
 #pragma unroll
-    for (int k = 0; k < NP; ++k) go[k] = mul2(w1[k], go[k]);  // zero past the row's end, as w1 is
-    if (a.in.w_post) {
-      F2 s0, s1;
-      norm_means<LAYER, kQuads>(a, c, cta.scratch, flip, go, bh, s0, s1);
-      const F2 rr = f2(now.y);
+    for (int k = 0; k < NP; ++k) go[k] = mul2(OWN ? mul2(w[k], y[k]) : w[k], go[k]);  // the gradient of N(b)
+    if (post) {
+      const float by = OWN && !full ? own : 1.f;  // an element's gate is in the sums
+      const F2 rr = f2(now.y), m1 = f2(-by * e_go * a.inv_h), m0 = f2(-by * w_go * a.inv_h);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        F2 e = fma2(bh[k], s1, go[k]);
-        if (LAYER) e = add2(e, s0);
+        F2 e = fma2(bh[k], m1, go[k]);
+        if (LAYER) e = add2(e, m0);
         go[k] = mul2(e, rr);
       }
     }
@@ -750,25 +843,25 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
 // Columns of a thread, 8 or 16.  16 halve what a row costs beside its columns
 // and take twice the registers.  Measured, bf16, with 8 and with 16:
 //   rows of a warp or less (16 let up to 512 channels go without a barrier):
-//     65536 x 256, rms, backward 74 -> 56 us;
-//   8192 x 8192, rms: forward 107 -> 90, backward 267 -> 197;
-//   16384 x 4096, rms: forward 92 -> 102, backward 156 -> 159: no gain;
-//   16384 x 4096, layer norms (four sums a row) forward 135 -> 118.
-// Backward layer norms hold four column sums, and rows' or elements' own gates
-// their values: they spill with 16 (layer, 16384 x 4096: 193 -> 348).  Rows
-// that start anywhere keep 8: their element accesses need the threads.
+//     65536 x 256, rms, backward 72 -> 51 us; layer norms backward and rows'
+//     or elements' own gates spill with 16;
+//   8192 x 8192, rms: forward 107 -> 93, backward 267 -> 145; layer norms
+//     backward 277 -> 240;
+//   16384 x 4096, rms: forward 94 -> 102, backward 156 -> 153: no gain; layer
+//     norms (four sums a row) forward 135 -> 118, backward 195 -> 309.
+// Rows that start anywhere keep 8: their element accesses need the threads.
 inline int join_columns(const zero_join_desc& d, bool wide, bool backward) {
   const bool layer = d.kind == ZERO_JOIN_LAYER;
   const bool own = d.gate_kind == ZERO_GATE_ROW || d.gate_kind == ZERO_GATE_FULL;
-  if (!wide || (backward && layer)) return 8;
-  if (d.hidden <= 512) return backward && own ? 8 : 16;
-  return d.hidden > (layer ? kJoinNarrowLayer : kJoinNarrow) ? 16 : 8;
+  if (!wide) return 8;
+  if (d.hidden > kJoinNarrow) return 16;
+  if (backward) return d.hidden <= 512 && !layer && !own ? 16 : 8;
+  return d.hidden <= 512 || (layer && d.hidden > kJoinNarrowLayer) ? 16 : 8;
 }
 
 // Threads of a row, and of a CTA.
 inline int join_lanes(const zero_join_desc& d, bool wide, bool backward) {
   const int64_t hidden = d.hidden, warp = 32 * join_columns(d, wide, backward);
-  if (hidden * 8 <= warp) return 4;
   if (hidden * 4 <= warp) return 8;
   if (hidden * 2 <= warp) return 16;
   return static_cast<int>((hidden + warp - 1) / warp * 32);
@@ -880,16 +973,15 @@ int launch_join_rows_as(const JoinArgs& a, int* workers, cudaStream_t s) {
 template <class A, class R, bool LAYER, bool OWN, bool BACKWARD, int MAP>
 int launch_join_rows_map(const JoinArgs& a, int* workers, cudaStream_t s) {
   constexpr bool wide = JoinCols<MAP, 4>::kWide;
-  // what join_columns can say for these kernels
-  constexpr bool long16 = wide && !(BACKWARD && LAYER), short16 = long16 && !(BACKWARD && OWN);
-  if (join_lanes(a.d, wide, BACKWARD) <= 32)
-    return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, kJoinSmallCta, short16 ? 8 : 4>(a, workers, s);
-  if constexpr (long16)
+  if (join_lanes(a.d, wide, BACKWARD) <= 32)  // short rows, as join_columns has them
+    return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, kJoinSmallCta,
+                               wide && !(BACKWARD && (LAYER || OWN)) ? 8 : 4>(a, workers, s);
+  if constexpr (wide) {
     if (join_columns(a.d, true, BACKWARD) == 16)
       return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 512, 8>(a, workers, s);
-  if constexpr (!long16)
-    if (join_threads(a.d, wide, BACKWARD) > 512)
-      return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 1024, 4>(a, workers, s);
+  } else if (join_threads(a.d, wide, BACKWARD) > 512) {
+    return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 1024, 4>(a, workers, s);
+  }
   return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 512, 4>(a, workers, s);
 }
 

@@ -186,6 +186,27 @@ __device__ __forceinline__ V warp_all_sum(V v) {
   return v;
 }
 
+// The launch that follows may start its CTAs; they wait for this grid's end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Host: launch fn; early: its CTAs may start before the launch ahead of it has
+// ended (they call wait_for_previous before they read what it wrote).
+inline cudaError_t launch_maybe_early(const void* fn, dim3 grid, dim3 block, void** args, bool early,
+                                      cudaStream_t s) {
+  if (!early) return cudaLaunchKernel(fn, grid, block, args, 0, s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
 // Host checks shared by the operators' entry points.
 inline bool known_type(int t) { return t == ZERO_FP16 || t == ZERO_BF16 || t == ZERO_FP32; }
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
