@@ -637,8 +637,8 @@ extern "C" zero_status zero_expert_sort(const void* ids, int32_t id_bytes, int64
   cudaError_t e = cudaSuccess;
   const void* sort = shape.table ? reinterpret_cast<const void*>(&k_expert_sort<true>)
                                  : reinterpret_cast<const void*>(&k_expert_sort<false>);
-  if (shape.smem > 48 * 1024)
-    e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMost);
+  static KernelFacts facts[2];
+  e = facts[shape.table].allow(sort, shape.smem, kSortSmemMost);
   if (e == cudaSuccess && shape.table) {
     k_expert_count<<<cfg.gridDim, cfg.blockDim, n_experts * 4, s>>>(a);
     e = cudaGetLastError();

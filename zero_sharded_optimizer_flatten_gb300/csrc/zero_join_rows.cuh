@@ -38,7 +38,6 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 
 #include "zero_join.cuh"
 
@@ -929,28 +928,19 @@ inline JoinLayout join_layout(const JoinArgs& a, bool wide, bool backward, int c
 
 inline int join_smem(const JoinLayout& l) { return kJoinScratch + l.vec_bytes + l.stages * l.stage_bytes; }
 
-// fn: the kernel, of at most MAXT threads a CTA; known: its CTAs of an SM by
-// registers, asked once a CTA size (devices of one kind answer the same).
-template <int MAXT>
-int launch_join_rows_fn(const void* fn, std::atomic<int>* known, const JoinArgs& a, bool wide, bool backward,
-                        int* workers, cudaStream_t s) {
+inline int launch_join_rows_fn(const void* fn, KernelFacts& facts, const JoinArgs& a, bool wide, bool backward,
+                               int* workers, cudaStream_t s) {
   const int threads = join_threads(a.d, wide, backward);
   const int groups = threads / join_lanes(a.d, wide, backward);
-  int fit = known[threads / 32].load(std::memory_order_relaxed);
-  if (fit == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, 0);
-    if (e != cudaSuccess) return static_cast<int>(e);
-    fit = std::max(1, fit);
-    known[threads / 32].store(fit, std::memory_order_relaxed);
-  }
+  int fit = 0;
+  cudaError_t e = facts.ctas_of(fn, threads, &fit);
+  if (e != cudaSuccess) return static_cast<int>(e);
   int ctas = std::max(1, std::min(fit, (backward ? kJoinThreadsBackward : kJoinThreadsForward) / threads));
   JoinLayout l = join_layout(a, wide, backward, ctas);
   while (ctas > 1 && l.stages < 2) l = join_layout(a, wide, backward, --ctas);  // a row ahead before one more CTA
   if (l.stages < 1) return -1;
-  if (join_smem(l) > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmemMost);
-    if (e != cudaSuccess) return static_cast<int>(e);
-  }
+  e = facts.allow(fn, join_smem(l), kJoinSmemMost);
+  if (e != cudaSuccess) return static_cast<int>(e);
   const int64_t work = (a.d.rows + groups - 1) / groups;
   const int grid = static_cast<int>(std::min<int64_t>(work, static_cast<int64_t>(ctas) * kSMs));
   *workers = grid;
@@ -961,13 +951,13 @@ int launch_join_rows_fn(const void* fn, std::atomic<int>* known, const JoinArgs&
 
 template <class A, class R, bool LAYER, bool OWN, bool BACKWARD, int MAP, int MAXT, int NP>
 int launch_join_rows_as(const JoinArgs& a, int* workers, cudaStream_t s) {
-  static std::atomic<int> known[MAXT / 32 + 1];
+  static KernelFacts facts;
   const void* fn;
   if constexpr (BACKWARD)
     fn = reinterpret_cast<const void*>(&k_join_rows_backward<A, R, LAYER, OWN, MAP, MAXT, NP>);
   else
     fn = reinterpret_cast<const void*>(&k_join_rows<A, R, LAYER, OWN, MAP, MAXT, NP>);
-  return launch_join_rows_fn<MAXT>(fn, known, a, JoinCols<MAP, NP>::kWide, BACKWARD, workers, s);
+  return launch_join_rows_fn(fn, facts, a, JoinCols<MAP, NP>::kWide, BACKWARD, workers, s);
 }
 
 template <class A, class R, bool LAYER, bool OWN, bool BACKWARD, int MAP>

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "zero.h"
 
 namespace zero {
@@ -206,6 +208,39 @@ inline cudaError_t launch_maybe_early(const void* fn, dim3 grid, dim3 block, voi
   cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
+
+// What a kernel was told or asked once: for each CTA size the CTAs of an SM
+// that its registers allow, and whether it may use `most` bytes of shared
+// memory (a driver call each, 1 us beside a launch of 4).  Devices have one
+// set each, up to kDevices; beyond, every call asks.
+struct KernelFacts {
+  static constexpr int kDevices = 8, kSizes = 33;  // CTA sizes in warps
+  std::atomic<int> fit[kDevices][kSizes];
+  std::atomic<bool> large[kDevices];
+
+  cudaError_t ctas_of(const void* fn, int threads, int* ctas) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>* slot = dev < kDevices ? &fit[dev][threads / 32] : nullptr;
+    *ctas = slot ? slot->load(std::memory_order_relaxed) : 0;
+    if (*ctas > 0) return cudaSuccess;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fn, threads, 0);
+    if (e == cudaSuccess && *ctas < 1) *ctas = 1;
+    if (e == cudaSuccess && slot) slot->store(*ctas, std::memory_order_relaxed);
+    return e;
+  }
+  cudaError_t allow(const void* fn, int bytes, int most) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices && large[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && dev < kDevices) large[dev].store(true, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // Host checks shared by the operators' entry points.
 inline bool known_type(int t) { return t == ZERO_FP16 || t == ZERO_BF16 || t == ZERO_FP32; }

@@ -12,11 +12,12 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 
 import torch
 
-from .zero import _check, lib
-from .zero import _stream as _any_stream
+from . import zero as _zero
+from .zero import _check
 
 ZERO_FP32 = 2
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: ZERO_FP32}
@@ -38,14 +39,23 @@ def _choice(table, value, what: str) -> int:
     return table[value]
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_lib = None
+
+
+def _load():
+    """The library, kept here after the first call (these calls are made many
+    times a step: what they do on the host shows beside small kernels)."""
+    global _lib
+    _lib = _zero.lib()
+    return _lib
 
 
 def _stream(stream, device: int):
     """Handle of the given stream, or of the device's current one."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(device)
-    return _any_stream(stream)
+    return _raw_stream(device) if stream is None else _zero._stream(stream)
 
 
 def _on(t, what: str, device: int):
@@ -65,9 +75,8 @@ def _current(t, what: str) -> int:
     device = t.get_device()
     if device < 0:
         raise ValueError(f"{what}: tensor must be on a CUDA device")
-    if device != torch.cuda.current_device():
-        raise ValueError(f"{what}: on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if device != _device():
+        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{_device()}")
     return device
 
 
@@ -162,7 +171,7 @@ def zero_grad_norm_workspace_bytes(grads) -> int:
         tensors[k].src_dtype, tensors[k].numel = _grad_tensor(g, f"grads[{k}]"), g.numel()
         tensors[k].src = g.data_ptr() if g.numel() else None
     need = ctypes.c_int64()
-    _check(lib().zero_grad_norm_workspace_bytes(tensors, len(kept), ctypes.byref(need)))
+    _check((_lib or _load()).zero_grad_norm_workspace_bytes(tensors, len(kept), ctypes.byref(need)))
     return need.value
 
 
@@ -221,9 +230,9 @@ class GradNorm:
                     spans.append((e.src, e.src + g.numel() * g.element_size(), False))
         _check_disjoint(spans)
         if device is None:
-            device = torch.cuda.current_device()
+            device = _device()
         need = ctypes.c_int64()
-        _check(lib().zero_grad_norm_workspace_bytes(self._list, self.n, ctypes.byref(need)))
+        _check((_lib or _load()).zero_grad_norm_workspace_bytes(self._list, self.n, ctypes.byref(need)))
         self.result = torch.empty(NORM_RESULT_BYTES, dtype=torch.uint8, device=device)
         self._workspace = _workspace(workspace, need.value, device)
         self._norm = self.result[8:12].view(torch.float32)[0]
@@ -231,7 +240,7 @@ class GradNorm:
         self.device = device
 
     def __call__(self, stream=None):
-        _check(lib().zero_grad_norm(self._list, self.n, self.kind, *self._args,
+        _check((_lib or _load()).zero_grad_norm(self._list, self.n, self.kind, *self._args,
                                     _stream(stream, self.device)))
         return self._norm
 
@@ -259,7 +268,7 @@ class ClipGradNorm(GradNorm):
         self._prepare(grads, out, kind, workspace)
 
     def __call__(self, stream=None):
-        _check(lib().zero_clip_grad_norm(self._list, self.n, self.kind, self.max_norm,
+        _check((_lib or _load()).zero_clip_grad_norm(self._list, self.n, self.kind, self.max_norm,
                                          *self._args, _stream(stream, self.device)))
         return self._norm
 
@@ -267,14 +276,16 @@ class ClipGradNorm(GradNorm):
 def zero_grad_norm(grads, kind: str = "l2", stream=None):
     """Norm of all gradients as one vector (see zero.h); a float32 tensor."""
     call = GradNorm(grads, kind)
-    _keep_for(stream, call.result, call._workspace)
+    if stream is not None:
+        _keep_for(stream, call.result, call._workspace)
     return call(stream)
 
 
 def zero_clip_grad_norm(grads, max_norm: float, kind: str = "l2", out=None, stream=None):
     """Norm and clipping (see zero.h); returns the norm before clipping."""
     call = ClipGradNorm(grads, max_norm, kind, out)
-    _keep_for(stream, call.result, call._workspace)
+    if stream is not None:
+        _keep_for(stream, call.result, call._workspace)
     return call(stream)
 
 
@@ -421,7 +432,7 @@ def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_
     if stream is not None:
         _keep_for(stream, o if given_o is None and want_o else None,
                   n if given_n is None else None, stats)
-    _check(lib().zero_block_join(ctypes.byref(d), ctypes.byref(p), p_o, p_n, p_stats,
+    _check((_lib or _load()).zero_block_join(ctypes.byref(d), ctypes.byref(p), p_o, p_n, p_stats,
                                  _stream(stream, device)))
     if not want_o:
         o = x if b is None else None
@@ -438,7 +449,7 @@ def zero_block_join_workspace_bytes(x, b=None, *, w_post=None, bias_post=None, w
 
 def _join_need(d) -> int:
     need = ctypes.c_int64()
-    _check(lib().zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
+    _check((_lib or _load()).zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
     return need.value
 
 
@@ -456,22 +467,22 @@ def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=No
     p_stats = None
     if stats is not None:
         p_stats = _result(stats, "stats", x, (d.rows, 4), torch.float32).data_ptr()
-    out = {"dx": x, "db": b, "dgate": gate, "dw_post": w_post, "dbias_post": bias_post,
-           "dw_pre": w_pre, "dbias_pre": bias_pre}
-    at = []
-    sums = unused = False
-    for name, like in out.items():
-        if like is None or (want is not None and name not in want):
-            out[name] = None
-            at.append(None)
-        elif d_n is None and name in ("dw_pre", "dbias_pre"):
-            out[name] = torch.zeros_like(like)  # n was not used
-            at.append(None)
-            unused = True
-        else:
-            out[name] = t = _new(like)
-            at.append(t.data_ptr())
-            sums = sums or (like is not x and like is not b and like.dim() == 1)
+    out, at = {}, []
+    unused = False
+    for name, like in (("dx", x), ("db", b), ("dgate", gate), ("dw_post", w_post),
+                       ("dbias_post", bias_post), ("dw_pre", w_pre), ("dbias_pre", bias_pre)):
+        t = ptr = None
+        if like is not None and (want is None or name in want):
+            if d_n is None and name in ("dw_pre", "dbias_pre"):
+                t = torch.zeros_like(like)  # n was not used
+                unused = True
+            else:
+                t = (torch.empty_like(like) if like.is_contiguous() else
+                     torch.empty(like.shape, dtype=like.dtype, device=like.device))
+                ptr = t.data_ptr()
+        out[name] = t
+        at.append(ptr)
+    sums = any(at[3:]) or (d.gate_kind == GATE_CHANNEL and at[2])
     p_ws, need, ws = None, 0, None
     if sums:
         need = _join_need(d)
@@ -481,7 +492,7 @@ def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=No
         _keep_for(stream, *out.values(), ws if workspace is None else None)
     if unused and not any(at):
         return out
-    _check(lib().zero_block_join_backward(
+    _check((_lib or _load()).zero_block_join_backward(
         ctypes.byref(d), ctypes.byref(p), None if d_o is None else d_o.data_ptr(),
         None if d_n is None else d_n.data_ptr(), p_stats, ctypes.byref(JoinGradsC(*at)), p_ws,
         need, _stream(stream, device)))
@@ -548,8 +559,11 @@ class ExpertOrder:
 def zero_expert_sort_workspace_bytes(tokens: int, topk: int, n_experts: int) -> int:
     """Device workspace of zero_expert_sort (0 up to some tens of thousands of choices)."""
     need = ctypes.c_int64()
-    _check(lib().zero_expert_sort_workspace_bytes(tokens, topk, n_experts, ctypes.byref(need)))
+    _check((_lib or _load()).zero_expert_sort_workspace_bytes(tokens, topk, n_experts, ctypes.byref(need)))
     return need.value
+
+
+_sort_need = functools.lru_cache(maxsize=256)(zero_expert_sort_workspace_bytes)
 
 
 def zero_expert_sort(ids, n_experts: int, workspace=None, stream=None) -> ExpertOrder:
@@ -569,10 +583,11 @@ def zero_expert_sort(ids, n_experts: int, workspace=None, stream=None) -> Expert
     offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=where)
     rows = torch.empty(ids.shape, dtype=torch.int32, device=where)
     pairs = torch.empty(tokens * topk, dtype=torch.int32, device=where)
-    need = zero_expert_sort_workspace_bytes(tokens, topk, n_experts)
+    need = _sort_need(tokens, topk, n_experts)
     ws = _workspace(workspace, need, device) if need else None
-    _keep_for(stream, offsets, rows, pairs, ws if workspace is None else None)
-    _check(lib().zero_expert_sort(ids.data_ptr() or None, ids.element_size(), tokens, topk,
+    if stream is not None:
+        _keep_for(stream, offsets, rows, pairs, ws if workspace is None else None)
+    _check((_lib or _load()).zero_expert_sort(ids.data_ptr() or None, ids.element_size(), tokens, topk,
                                   n_experts, offsets.data_ptr(), rows.data_ptr() or None,
                                   pairs.data_ptr() or None,
                                   None if ws is None else ws.data_ptr(), need,
@@ -614,8 +629,9 @@ def zero_expert_dispatch(x, order: ExpertOrder, out=None, stream=None):
     the rows past the last kept choice are zero."""
     device, code, hidden, stride = _token_rows(x, "x", order)
     xs = _result(out, "out", x, (order.tokens * order.topk, hidden), x.dtype)
-    _keep_for(stream, xs if out is None else None)
-    _check(lib().zero_expert_dispatch(x.data_ptr(), stride, code, order.tokens, order.topk, hidden,
+    if stream is not None:
+        _keep_for(stream, xs if out is None else None)
+    _check((_lib or _load()).zero_expert_dispatch(x.data_ptr(), stride, code, order.tokens, order.topk, hidden,
                                       order.offsets.data_ptr(), order.n_experts,
                                       order.rows.data_ptr(), xs.data_ptr(),
                                       _stream(stream, device)))
@@ -626,8 +642,9 @@ def zero_expert_dispatch_backward(dxs, order: ExpertOrder, out=None, stream=None
     """Each token's gradient: the sum of its rows'."""
     device, code, hidden = _sorted_rows(dxs, "dxs", order)
     dx = _result(out, "out", dxs, (order.tokens, hidden), dxs.dtype)
-    _keep_for(stream, dx if out is None else None)
-    _check(lib().zero_expert_dispatch_backward(dxs.data_ptr(), code, order.tokens, order.topk,
+    if stream is not None:
+        _keep_for(stream, dx if out is None else None)
+    _check((_lib or _load()).zero_expert_dispatch_backward(dxs.data_ptr(), code, order.tokens, order.topk,
                                                hidden, order.rows.data_ptr(), dx.data_ptr(),
                                                _stream(stream, device)))
     return dx
@@ -639,8 +656,9 @@ def zero_expert_combine(ys, weights, order: ExpertOrder, out=None, stream=None):
     device, code, hidden = _sorted_rows(ys, "ys", order)
     wcode = _expert_weights(weights, order, device)
     y = _result(out, "out", ys, (order.tokens, hidden), ys.dtype)
-    _keep_for(stream, y if out is None else None)
-    _check(lib().zero_expert_combine(ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
+    if stream is not None:
+        _keep_for(stream, y if out is None else None)
+    _check((_lib or _load()).zero_expert_combine(ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
                                      order.topk, hidden, order.rows.data_ptr(), y.data_ptr(),
                                      _stream(stream, device)))
     return y
@@ -656,8 +674,9 @@ def zero_expert_combine_backward(dy, ys, weights, order: ExpertOrder, want_weigh
     wcode = _expert_weights(weights, order, device)
     dys = _new(ys)
     dweights = _new(weights) if want_weights else None
-    _keep_for(stream, dys, dweights)
-    _check(lib().zero_expert_combine_backward(
+    if stream is not None:
+        _keep_for(stream, dys, dweights)
+    _check((_lib or _load()).zero_expert_combine_backward(
         dy.data_ptr(), stride, ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
         order.topk, hidden, order.offsets.data_ptr(), order.n_experts, order.rows.data_ptr(),
         dys.data_ptr(), None if dweights is None else dweights.data_ptr(),
