@@ -85,15 +85,24 @@ __device__ __forceinline__ void copies_wait(int ahead) {
     asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// Bytes [from, to) of elements of E bytes, one by one.
+// A row whose covering chunks reach outside its tensor: whole chunks where
+// they do not, elements of E bytes one by one where they do.
 template <int E>
-__device__ __noinline__ void copy_elements(char* dst, const char* src, int from, int to) {
+__device__ __noinline__ void copy_edge_row(char* row_at, const char* q, int skip, int bytes, int from, int step,
+                                           const char* first, const char* end) {
 #pragma unroll 1
-  for (int e = from; e < to; e += E) {
-    if constexpr (E == 4)
-      *reinterpret_cast<uint32_t*>(dst + e) = *reinterpret_cast<const uint32_t*>(src + e);
-    else
-      *reinterpret_cast<uint16_t*>(dst + e) = *reinterpret_cast<const uint16_t*>(src + e);
+  for (int i = from; i < skip + bytes; i += step) {
+    if (q + i >= first && q + i + 16 <= end) {
+      copy_async<16>(smem_of(row_at + i), q + i);
+      continue;
+    }
+#pragma unroll 1
+    for (int e = max(i, skip); e < min(i + 16, skip + bytes); e += E) {
+      if constexpr (E == 4)
+        *reinterpret_cast<uint32_t*>(row_at + e) = *reinterpret_cast<const uint32_t*>(q + e);
+      else
+        *reinterpret_cast<uint16_t*>(row_at + e) = *reinterpret_cast<const uint16_t*>(q + e);
+    }
   }
 }
 
@@ -155,14 +164,12 @@ struct JoinCols {
       // chunks as they lie, the row's first byte at its own place in a chunk
       const int bytes = hidden * E, skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
       char* row_at = at + group * row_bytes(E);
-#pragma unroll 1
-      for (int i = 16 * t; i < skip + bytes; i += 16 * T) {
-        const char* q = p - skip + i;
-        if (q >= static_cast<const char*>(first) && q + 16 <= end) {
-          copy_async<16>(smem_of(row_at + i), q);
-        } else {
-          copy_elements<E>(row_at, p - skip, max(i, skip), min(i + 16, skip + bytes));
-        }
+      const char* q = p - skip;
+      if (q >= static_cast<const char*>(first) && q + ((skip + bytes + 15) & ~15) <= end) {
+        const uint32_t dst = smem_of(row_at);
+        for (int i = 16 * t; i < skip + bytes; i += 16 * T) copy_async<16>(dst + i, q + i);
+      } else {
+        copy_edge_row<E>(row_at, q, skip, bytes, 16 * t, 16 * T, static_cast<const char*>(first), end);
       }
     }
   }
