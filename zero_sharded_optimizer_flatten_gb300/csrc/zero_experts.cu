@@ -43,12 +43,14 @@ namespace {
 // Up to kClusterPairs pairs one thread-block cluster does it in one launch,
 // its CTAs reading one another's counts through distributed shared memory;
 // above, a first launch leaves every CTA's counts in the workspace and up to
-// kTableCtas CTAs share the walk (240,000 pairs, 256 experts, took 72 us in
-// one cluster).
+// kTableCtas CTAs share the walk.  Cluster and table, us, 64 / 512 experts:
+// 32768 pairs 9.9 / 13.5 and 10.9 / 13.7; 49152 pairs 12.1 / 15.6 and 10.1 /
+// 13.7; 131072 pairs 22.2 / 28.0 and 13.5 / 16.6.
 
 constexpr int kClusterCtas = 8;        // CTAs of the largest cluster (portable size)
-constexpr int64_t kClusterPairs = 49152;
+constexpr int64_t kClusterPairs = 32768;
 constexpr int kTableCtas = 128;
+constexpr int kTableEntries = 65536;   // every CTA reads the whole table
 constexpr int kSortWarpsMost = 32;
 constexpr int kIdsAhead = 8;
 constexpr int kMaxExperts = 4096;
@@ -226,7 +228,7 @@ struct SortShape {
     warps = kSortWarpsMost;
     while (warps > 1 && ((warps + 2) * n_experts + warps) * 4 > kSortSmemMost) warps /= 2;
     while (warps > 1 && warps / 2 >= groups) warps /= 2;
-    const int most = table ? kTableCtas : kClusterCtas;
+    const int most = table ? std::max(8, std::min(kTableCtas, kTableEntries / n_experts)) : kClusterCtas;
     ctas = 1;
     while (ctas < most && static_cast<int64_t>(ctas) * warps * 4 < groups) ctas *= 2;
     smem = ((warps + 2) * n_experts + warps) * 4;

@@ -2,9 +2,10 @@
 // registers, 8 or 16 columns a thread, from the one read to the one write.
 //
 // Row split.  Above 256 channels a CTA of whole warps takes a row at a time; a
-// row's sums go through one shuffle tree a warp and one barrier.  Shorter rows
-// (up to 512 channels with 16 columns a thread) are taken by 8 to 32 lanes
-// and a CTA of 128 threads has several.  Rows are handed out grid-stride.
+// row's sums go through one shuffle tree a warp and one barrier.  Rows that a
+// warp can hold (256 channels, 512 with 16 columns a thread) are taken by 8 to
+// 32 lanes and a CTA of 128 threads has several.  Rows are handed out
+// grid-stride.
 //
 // Column maps.  A thread's columns come in units of u neighbours, unit j of
 // thread t of a row's T at column u (t + j T): u = 8 (kOct) where all rows are
@@ -741,7 +742,16 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
       s[1] = sum2(t1), s[2] = sum2(t2);
       if constexpr (LAYER) s[4] = sum2(t4), s[5] = sum2(t5), s[6] = sum2(t6), s[7] = sum2(t7);
     }
-    if (a.d_n || post || OWN) join_many_sums<kQuads>(s, cta.scratch, flip, c.T);
+    if (post || OWN) {
+      join_many_sums<kQuads>(s, cta.scratch, flip, c.T);
+    } else if (a.d_n) {  // only the sums over t
+      float t[LAYER ? 2 : 1];
+      t[0] = s[0];
+      if constexpr (LAYER) t[1] = s[3];
+      join_sums<kQuads>(t, cta.scratch, flip, c.T);
+      s[0] = t[0];
+      if constexpr (LAYER) s[3] = t[1];
+    }
     // -R_o mean(t h) and -R_o mean(t)
     const float q1 = -now.w * (s[0] * a.inv_h), q0 = LAYER ? -now.w * (s[3 % N] * a.inv_h) : 0.f;
     if (a.d_n) {
@@ -847,22 +857,23 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
 // host: the layout and the launch of one type pair
 
 // Columns of a thread, 8 or 16.  16 halve what a row costs beside its columns
-// and take twice the registers.  Measured, bf16, with 8 and with 16:
-//   rows of a warp or less (16 let up to 512 channels go without a barrier):
-//     65536 x 256, rms, backward 72 -> 51 us; layer norms backward and rows'
-//     or elements' own gates spill with 16;
-//   8192 x 8192, rms: forward 107 -> 93, backward 267 -> 145; layer norms
-//     backward 277 -> 240;
-//   16384 x 4096, rms: forward 94 -> 102, backward 156 -> 153: no gain; layer
-//     norms (four sums a row) forward 135 -> 118, backward 195 -> 309.
-// Rows that start anywhere keep 8: their element accesses need the threads.
+// and take twice the registers.  Measured, bf16, us with 8 and with 16:
+//                              forward           backward
+//   65536 x 256, rms           31.8 -> 28.1      49.0 -> 49.9
+//   65536 x 256, layer norms   40.4 -> 33.9      62 -> 105
+//   65536 x 512, layer norms   69 -> 57          102 -> 183
+//   16384 x 4096, rms          94 -> 102         156 -> 153
+//   16384 x 4096, layer norms  135 -> 118        195 -> 309
+//   8192 x 8192, rms           107 -> 93         267 -> 145
+//   8192 x 8192, layer norms                     277 -> 240
+// (up to 512 channels 16 columns let a warp hold a row, without a barrier; up
+// to 8192, 16 keep a CTA within 512 threads and its registers).  Rows that
+// start anywhere keep 8: their element accesses need the threads.
 inline int join_columns(const zero_join_desc& d, bool wide, bool backward) {
-  const bool layer = d.kind == ZERO_JOIN_LAYER;
-  const bool own = d.gate_kind == ZERO_GATE_ROW || d.gate_kind == ZERO_GATE_FULL;
   if (!wide) return 8;
   if (d.hidden > kJoinNarrow) return 16;
-  if (backward) return d.hidden <= 512 && !layer && !own ? 16 : 8;
-  return d.hidden <= 512 || (layer && d.hidden > kJoinNarrowLayer) ? 16 : 8;
+  if (backward) return 8;
+  return d.hidden <= 512 || (d.kind == ZERO_JOIN_LAYER && d.hidden > kJoinNarrowLayer) ? 16 : 8;
 }
 
 // Threads of a row, and of a CTA.
@@ -971,8 +982,8 @@ template <class A, class R, bool LAYER, bool OWN, bool BACKWARD, int MAP>
 int launch_join_rows_map(const JoinArgs& a, int* workers, cudaStream_t s) {
   constexpr bool wide = JoinCols<MAP, 4>::kWide;
   if (join_lanes(a.d, wide, BACKWARD) <= 32)  // short rows, as join_columns has them
-    return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, kJoinSmallCta,
-                               wide && !(BACKWARD && (LAYER || OWN)) ? 8 : 4>(a, workers, s);
+    return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, kJoinSmallCta, wide && !BACKWARD ? 8 : 4>(a, workers,
+                                                                                                          s);
   if constexpr (wide) {
     if (join_columns(a.d, true, BACKWARD) == 16)
       return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 512, 8>(a, workers, s);
