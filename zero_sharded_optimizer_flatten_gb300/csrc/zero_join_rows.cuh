@@ -866,13 +866,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == kJoinSmallCta ? 4 : 1) k_join_ro
 //   16384 x 4096, layer norms  135 -> 118        195 -> 309
 //   8192 x 8192, rms           107 -> 93         267 -> 145
 //   8192 x 8192, layer norms                     277 -> 240
+//   8001 x 4097, rms           141 -> 102        206 -> 211
 // (up to 512 channels 16 columns let a warp hold a row, without a barrier; up
-// to 8192, 16 keep a CTA within 512 threads and its registers).  Rows that
-// start anywhere keep 8: their element accesses need the threads.
+// to 8192, 16 keep a CTA within 512 threads and its registers).  Shorter rows
+// that start anywhere keep 8: their element accesses need the threads.
 inline int join_columns(const zero_join_desc& d, bool wide, bool backward) {
-  if (!wide) return 8;
-  if (d.hidden > kJoinNarrow) return 16;
-  if (backward) return 8;
+  if (d.hidden > kJoinNarrow) return wide || !backward ? 16 : 8;
+  if (!wide || backward) return 8;
   return d.hidden <= 512 || (d.kind == ZERO_JOIN_LAYER && d.hidden > kJoinNarrowLayer) ? 16 : 8;
 }
 
@@ -984,8 +984,8 @@ int launch_join_rows_map(const JoinArgs& a, int* workers, cudaStream_t s) {
   if (join_lanes(a.d, wide, BACKWARD) <= 32)  // short rows, as join_columns has them
     return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, kJoinSmallCta, wide && !BACKWARD ? 8 : 4>(a, workers,
                                                                                                           s);
-  if constexpr (wide) {
-    if (join_columns(a.d, true, BACKWARD) == 16)
+  if constexpr (wide || !BACKWARD) {
+    if (join_columns(a.d, wide, BACKWARD) == 16)
       return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 512, 8>(a, workers, s);
   } else if (join_threads(a.d, wide, BACKWARD) > 512) {
     return launch_join_rows_as<A, R, LAYER, OWN, BACKWARD, MAP, 1024, 4>(a, workers, s);
