@@ -875,3 +875,88 @@ def test_join_many_rows_of_one_cta_shape():
     groups, row gates read ahead."""
     for R, H in ((40_001, 64), (9_999, 200), (5_003, 512), (3_001, 511)):
         check_join(join_inputs(R, H, B16, B16, F32, "row", True, True, False, R), "rms")
+
+
+# ---------------------------------------------------------------------------
+# launches that start early, in graphs and back to back
+
+
+def test_clip_in_a_graph_and_back_to_back():
+    """Several launches a pass (over 1000 tensors), captured once and replayed
+    on new values; then calls that follow one another without a wait."""
+    rng = np.random.default_rng(3)
+    sizes = [int(x) for x in rng.integers(1, 4000, 1300)]
+    grads = grads_of(sizes, [(F32, B16)[k % 2] for k in range(len(sizes))], 3)
+    out = [torch.empty(n, dtype=B16, device="cuda") for n in sizes]
+    call = Z.ClipGradNorm(grads, 0.3, out=out)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = call()
+    for scale in (1.0, 7.0, 0.01):
+        for g in grads:
+            g.mul_(scale)
+        ref = exact_norm(grads)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert abs(float(norm) - ref) <= NORM_TOL * ref
+        f = min(1.0, 0.3 / (ref + 1e-6))
+        for k in (0, 1, 999, 1000, 1299):
+            close(out[k], grads[k].double() * f, (grads[k].double() * f).abs() * 3e-6, f"tensor {k}")
+    big = [torch.full((3_000_000,), 1.0, device="cuda")]
+    halve = Z.ClipGradNorm(big, 1.0)
+    refs = []
+    for k in range(20):   # in place: each call's norm is the limit before it
+        halve.max_norm = 1000.0 / 2 ** k
+        refs.append(halve().clone())
+    torch.cuda.synchronize()
+    want = math.sqrt(3_000_000)
+    for k, r in enumerate(refs):
+        assert abs(float(r) - want) <= 1e-5 * want, k
+        want *= min(1.0, 1000.0 / 2 ** k / (want + 1e-6))
+
+
+def test_large_sort_and_join_in_a_graph():
+    ids = choose(60_000, 2, 100, 9)
+    v = join_inputs(700, 768, B16, B16, B16, "channel", True, True, False, 6)
+    params = {k: t for k, t in v.items() if k not in ("x", "b")}
+
+    def run():
+        order = Z.zero_expert_sort(ids, 100)
+        o, n, stats = Z.zero_block_join(v["x"], v["b"], want_stats=True, **params)
+        g = Z.zero_block_join_backward(v["x"], v["b"], o, n, stats, **params)
+        return [order.offsets, order.rows, order.pairs, o, n] + [t for t in g.values() if t is not None]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for seed in (1, 2):
+        ids.copy_(choose(60_000, 2, 100, seed, 0.1))
+        v["b"].mul_(0.9)
+        want = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held))
+
+
+def test_record_and_prepared_norm():
+    g = [torch.full((100,), 3.0, device="cuda"), torch.full((7,), -4.0, dtype=H16, device="cuda")]
+    call = Z.GradNorm(g)
+    want = math.sqrt(100 * 9 + 7 * 16)
+    assert abs(float(call()) - want) <= NORM_TOL * want
+    r = call.read()
+    assert abs(r.norm - want) <= NORM_TOL * want and r.coef == 1.0 and r.nonfinite == 0
+    clip = Z.ClipGradNorm(g, 0.5)
+    clip()
+    r = clip.read()
+    assert abs(r.norm - want) <= NORM_TOL * want
+    assert abs(r.coef - 0.5 / want) <= 1e-6 * 0.5 / want
+    mixed = Z.ClipGradNorm(g, 1e9, out=[g[0], torch.empty(7, device="cuda")])
+    assert float(mixed()) > 0   # one in place, one elsewhere
+    ws = torch.empty(Z.zero_grad_norm_workspace_bytes(g), dtype=torch.uint8, device="cuda")
+    assert float(Z.GradNorm(g, workspace=ws)()) == float(Z.GradNorm(g)())
+    with pytest.raises(ValueError):
+        Z.GradNorm(g, workspace=ws[:16])
