@@ -18,7 +18,8 @@
 // anyway, so o's own rounding enters no gradient.
 //
 // What bounds it: bytes (forward: x, b in, o, n out; backward: x, b, do, dn
-// in, dx, db out).
+// in, dx, db out).  The kernels here take rows above 8192 channels; the others
+// are in zero_join_rows.cuh.
 #include <cuda_runtime.h>
 #include <inttypes.h>
 #include <math.h>
