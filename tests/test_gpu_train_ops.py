@@ -960,3 +960,42 @@ def test_record_and_prepared_norm():
     assert float(Z.GradNorm(g, workspace=ws)()) == float(Z.GradNorm(g)())
     with pytest.raises(ValueError):
         Z.GradNorm(g, workspace=ws[:16])
+
+
+def test_calls_keep_nothing():
+    """Neither memory nor references stay behind, after refusals either."""
+    import gc
+    import sys
+    x, b, d = (torch.randn(6, 64, device="cuda") for _ in range(3))
+    w = torch.ones(64, device="cuda")
+    ids = torch.tensor([[0, 1], [1, 2], [2, 0], [0, 2], [1, 0], [2, 1]], dtype=torch.int32, device="cuda")
+    weights = torch.rand(6, 2, device="cuda")
+
+    def calls():
+        _, _, stats = Z.zero_block_join(x, b, w_post=w, w_pre=w, want_stats=True)
+        Z.zero_block_join_backward(x, b, d, d, stats, w_post=w, w_pre=w, want={"dx", "dw_pre"})
+        assert Z.zero_block_join(x, w_pre=w)[0] is x
+        order = Z.zero_expert_sort(ids, 3)
+        ys = Z.zero_expert_dispatch(x, order)
+        Z.zero_expert_combine(ys, weights, order)
+        Z.zero_expert_combine_backward(d, ys, weights, order)
+        Z.zero_expert_dispatch_backward(ys, order)
+        for bad in (lambda: Z.zero_block_join(x, b, w_post=w, scale="x"),
+                    lambda: Z.zero_block_join(x, b, w_post=w, eps=0.0),
+                    lambda: Z.zero_expert_combine(ys, weights[:3], order)):
+            with pytest.raises((TypeError, ValueError, Z.ZeroError)):
+                bad()
+
+    calls()
+    torch.cuda.synchronize()
+    gc.collect()
+    held = [sys.getrefcount(t) for t in (x, b, d, w, ids, weights)] + [sys.getrefcount(None)]
+    bytes_ = torch.cuda.memory_allocated()
+    for _ in range(200):
+        calls()
+    torch.cuda.synchronize()
+    gc.collect()
+    now = [sys.getrefcount(t) for t in (x, b, d, w, ids, weights)] + [sys.getrefcount(None)]
+    assert now[:-1] == held[:-1]
+    assert abs(now[-1] - held[-1]) < 100    # None: immortal, or within the interpreter's own use
+    assert torch.cuda.memory_allocated() == bytes_

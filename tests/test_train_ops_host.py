@@ -196,3 +196,23 @@ def test_cpu_tensors_are_refused():
             call()
     with pytest.raises(TypeError):
         T.zero_grad_norm([1.0])
+
+
+def test_compiled_binding_refuses_before_it_launches():
+    import torch
+    x, w = torch.ones(2, 8), torch.ones(8)
+    order = T.ExpertOrder(torch.zeros(3, dtype=torch.int32), torch.zeros(2, 1, dtype=torch.int32),
+                          torch.zeros(2, dtype=torch.int32), 2, 2, 1)
+    for call in (lambda: T.zero_block_join(x, w_pre=w), lambda: T.zero_expert_sort(order.rows, 2),
+                 lambda: T.zero_block_join_backward(x, x, x, None, None),
+                 lambda: T.zero_expert_dispatch(x, order),
+                 lambda: T.zero_expert_combine(x, torch.ones(2, 1), order),
+                 lambda: T.zero_expert_dispatch_backward(x, order),
+                 lambda: T.zero_expert_combine_backward(x, x, torch.ones(2, 1), order)):
+        with pytest.raises(ValueError):    # host tensors
+            call()
+    for call in (lambda: T.zero_block_join(None), lambda: T.zero_block_join([1.0], w_pre=w),
+                 lambda: T.zero_expert_dispatch(3, order),
+                 lambda: T.zero_expert_combine(None, None, order)):
+        with pytest.raises(TypeError):
+            call()

@@ -3,6 +3,9 @@
 Each translation unit is compiled in parallel, then linked into
 zero_sharded_optimizer_flatten_gb300/libzero.so.  No cmake, no torch
 extension machinery: the library has a plain C ABI and no torch types.
+_train_ops.so beside it is the compiled part of the Python binding of the
+training-step operators (csrc/train_ops_binding.cpp): it is linked against the
+library and the installed torch, and holds no arithmetic.
 """
 from __future__ import annotations
 
@@ -18,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzero.so")
+BINDING = os.path.join(HERE, "_train_ops.so")
+BINDING_SOURCE = "train_ops_binding.cpp"
 
 SOURCES = ["zero_plan.cpp", "zero_capi.cpp", "zero_launch.cu", "zero_kernels_fp16.cu",
            "zero_kernels_bf16.cu", "zero_noalloc.cu", "zero_cpu_adam.cpp", "zero_gradnorm.cu",
@@ -49,7 +54,39 @@ def _deps_mtime() -> float:
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
+    newest = _deps_mtime()
+    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING))
+
+
+def _compile_binding() -> str:
+    """Object file of the binding (the host compiler, torch's headers)."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, BINDING_SOURCE + ".o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], "-I", root, "-I",
+           os.path.join(root, "torch", "csrc", "api", "include"), "-I", cuda, "-c",
+           os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{' '.join(cmd)}\n{res.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libzero.so", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN",
+           f"-Wl,-rpath,{libs}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:
@@ -70,14 +107,17 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
             sys.stderr.write(res.stdout + res.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding = binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

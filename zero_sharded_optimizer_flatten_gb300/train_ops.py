@@ -2,7 +2,8 @@
 and clipping over many tensors, the block join, the expert permutation.
 
 The ``zero_*`` functions bind the C calls of include/zero.h under their own
-names (argument checks and marshalling only; the current CUDA stream unless
+names (argument checks and marshalling only, those of the join and the experts
+compiled, csrc/train_ops_binding.cpp; the current CUDA stream unless
 ``stream`` is given; no fallback).  ``GradNorm`` and ``ClipGradNorm`` are the
 prepared forms for gradients whose buffers stay in place from step to step.
 ``block_join``, ``expert_dispatch`` and ``expert_combine`` are the same calls
@@ -12,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-import functools
+import os
 
 import torch
 
@@ -22,8 +23,6 @@ from .zero import _check
 ZERO_FP32 = 2
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: ZERO_FP32}
 _NORMS = {"l2": 0, "inf": 1}
-_KINDS = {"rms": 0, "layer": 1}
-GATE_NONE, GATE_CHANNEL, GATE_ROW, GATE_FULL = range(4)
 
 
 def _type(t, what: str) -> int:
@@ -42,6 +41,7 @@ def _choice(table, value, what: str) -> int:
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_FAST_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_train_ops.so")
 _lib = None
 
 
@@ -51,6 +51,26 @@ def _load():
     global _lib
     _lib = _zero.lib()
     return _lib
+
+
+_fast = None
+
+
+def _load_fast():
+    """The compiled binding (built with the library, and linked against it)."""
+    global _fast
+    _load()
+    if not os.path.exists(_FAST_PATH):
+        raise RuntimeError(f"{_FAST_PATH} is not built: run `python -c 'import __graft_entry__ as "
+                           "g; g.build()'`; there is no fallback implementation")
+    from . import _train_ops
+    _train_ops.set_error(_zero.ZeroError)
+    _fast = _train_ops
+    return _fast
+
+
+def _handle(stream) -> int:
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _stream(stream, device: int):
@@ -88,25 +108,6 @@ def _keep_for(stream, *tensors):
     for t in tensors:
         if t is not None:
             t.record_stream(s)
-
-
-def _new(like):
-    """A new contiguous tensor of `like`'s shape and type."""
-    if like.is_contiguous():
-        return torch.empty_like(like)
-    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-
-
-def _result(t, what: str, like, shape, dtype):
-    """A caller's output tensor, checked, or a new one beside `like`."""
-    if t is None:
-        if like.shape == shape and like.dtype == dtype:
-            return _new(like)
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _on(t, what, like.get_device())
-    if t.dtype != dtype or t.shape != torch.Size(shape) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
-    return t
 
 
 # ----------------------------------------------------------------------------
@@ -294,6 +295,7 @@ def zero_clip_grad_norm(grads, max_norm: float, kind: str = "l2", out=None, stre
 
 
 class JoinDescC(ctypes.Structure):
+    """Host image of zero_join_desc."""
     _fields_ = ([("rows", ctypes.c_int64), ("hidden", ctypes.c_int64)]
                 + [(k, ctypes.c_int32) for k in ("act_dtype", "res_dtype", "param_dtype",
                                                  "gate_dtype", "kind", "gate_kind")]
@@ -312,98 +314,6 @@ class JoinGradsC(ctypes.Structure):
                                                "dw_pre", "dbias_pre")]
 
 
-def _row_stride(t, what: str, shape, device: int) -> int:
-    """Elements between rows of a tensor [..., hidden] whose rows are
-    contiguous and evenly spaced."""
-    if t.get_device() != device:
-        _on(t, what, device)
-    if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        return shape[-1]
-    hidden = shape[-1]
-    if t.stride(-1) == 1 or hidden == 1:
-        if t.dim() == 2:
-            return t.stride(0)
-        try:
-            return t.view(-1, hidden).stride(0)
-        except RuntimeError:
-            pass
-    raise ValueError(f"{what}: rows must be contiguous and evenly spaced (use .contiguous())")
-
-
-def _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind, scale, eps, act,
-               d_o=None, d_n=None):
-    """(desc, inputs, device, act dtype, hidden) of a join's arguments."""
-    device = _current(x, "x")
-    shape = x.shape
-    if not shape:
-        raise ValueError("x: expected [..., hidden]")
-    hidden = shape[-1]
-    x_stride = _row_stride(x, "x", shape, device)
-    b_stride = gate_stride = do_stride = dn_stride = 0
-    p_b = p_gate = None
-    if b is not None:
-        act = b.dtype
-        b_stride = _row_stride(b, "b", shape, device)
-        p_b = b.data_ptr()
-    elif act is None:
-        act = w_pre.dtype if x.dtype == torch.float32 and w_pre is not None else x.dtype
-    act_code = _TYPES.get(act)
-    if act_code is None:
-        raise TypeError(f"b: expected float16, bfloat16 or float32, got {act}")
-    param = None
-    for name, t in (("w_post", w_post), ("bias_post", bias_post), ("w_pre", w_pre),
-                    ("bias_pre", bias_pre)):
-        if t is None:
-            continue
-        if t.get_device() != device:
-            _on(t, name, device)
-        if t.dim() != 1 or t.shape[0] != hidden or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous vector of {hidden}")
-        if param is None:
-            param = t.dtype
-        elif t.dtype != param:
-            raise TypeError(f"{name}: {t.dtype}, but another parameter is {param}")
-    param_code = act_code if param is None else _TYPES.get(param)
-    if param_code is None:
-        raise TypeError(f"parameters: expected float16, bfloat16 or float32, got {param}")
-    gate_kind, gate_code = GATE_NONE, act_code
-    if gate is not None:
-        _on(gate, "gate", device)
-        gate_code = _type(gate, "gate")
-        if gate.dim() == 1 and gate.shape[0] == hidden and len(shape) != 1:
-            if not gate.is_contiguous():
-                raise ValueError("gate: expected a contiguous vector")
-            gate_kind = GATE_CHANNEL
-        elif gate.shape == shape:
-            gate_kind = GATE_FULL
-            gate_stride = _row_stride(gate, "gate", shape, device)
-        elif gate.shape == shape[:-1] + (1,):
-            gate_kind = GATE_ROW
-            gate_stride = _row_stride(gate, "gate", gate.shape, device)
-        else:
-            raise ValueError(f"gate: shape {tuple(gate.shape)}, expected ({hidden},), "
-                             f"{tuple(shape[:-1]) + (1,)} or {tuple(shape)}")
-        p_gate = gate.data_ptr()
-    if d_o is not None:
-        if d_o.dtype != x.dtype:
-            raise TypeError(f"d_o: expected {x.dtype}, got {d_o.dtype}")
-        do_stride = _row_stride(d_o, "d_o", shape, device)
-    if d_n is not None:
-        if d_n.dtype != act:
-            raise TypeError(f"d_n: expected {act}, got {d_n.dtype}")
-        dn_stride = _row_stride(d_n, "d_n", shape, device)
-    d = JoinDescC(x.numel() // hidden if hidden else 0, hidden, act_code, _type(x, "x"),
-                  param_code, gate_code, _choice(_KINDS, kind, "kind"), gate_kind, eps, scale,
-                  x_stride, b_stride, gate_stride, do_stride, dn_stride)
-    p = JoinInputsC(x.data_ptr(), p_b, p_gate, None if w_post is None else w_post.data_ptr(),
-                    None if bias_post is None else bias_post.data_ptr(),
-                    None if w_pre is None else w_pre.data_ptr(),
-                    None if bias_pre is None else bias_pre.data_ptr())
-    return d, p, device, act, hidden
-
-
 def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_pre=None,
                     gate=None, kind: str = "rms", scale: float = 1.0, eps: float = 1e-6, o=None,
                     n=None, want_o: bool = True, want_stats: bool = False, stream=None):
@@ -412,45 +322,20 @@ def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_
     without w_pre no n (None); b None takes the norm of x alone, and o is x.
     x, b, gate: [..., hidden]; the gate also [hidden] or [..., 1].  stats is
     what the backward call takes (None unless want_stats)."""
-    d, p, device, act, hidden = _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind,
-                                           scale, eps, None if n is None else n.dtype)
-    if n is not None and w_pre is None:
-        raise ValueError("n: needs w_pre")
-    if b is None and o is None:
-        want_o = False
-    given_o, given_n = o, n
-    p_o = p_n = p_stats = stats = None
-    if want_o:
-        o = _result(o, "o", x, x.shape, x.dtype)
-        p_o = o.data_ptr()
-    if w_pre is not None:
-        n = _result(n, "n", x, x.shape, act)
-        p_n = n.data_ptr()
-    if want_stats:
-        stats = torch.empty((d.rows, 4), dtype=torch.float32, device=x.device)
-        p_stats = stats.data_ptr()
+    got = (_fast or _load_fast()).block_join(x, b, w_post, bias_post, w_pre, bias_pre, gate, kind,
+                                             scale, eps, o, n, want_o, want_stats,
+                                             None if stream is None else _handle(stream))
     if stream is not None:
-        _keep_for(stream, o if given_o is None and want_o else None,
-                  n if given_n is None else None, stats)
-    _check((_lib or _load()).zero_block_join(ctypes.byref(d), ctypes.byref(p), p_o, p_n, p_stats,
-                                 _stream(stream, device)))
-    if not want_o:
-        o = x if b is None else None
-    return o, n, stats
+        _keep_for(stream, *got)
+    return got
 
 
 def zero_block_join_workspace_bytes(x, b=None, *, w_post=None, bias_post=None, w_pre=None,
                                     bias_pre=None, gate=None, kind: str = "rms",
                                     scale: float = 1.0, eps: float = 1e-6) -> int:
     """Device workspace of zero_block_join_backward for these arguments."""
-    d = _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind, scale, eps, None)[0]
-    return _join_need(d)
-
-
-def _join_need(d) -> int:
-    need = ctypes.c_int64()
-    _check((_lib or _load()).zero_block_join_workspace_bytes(ctypes.byref(d), ctypes.byref(need)))
-    return need.value
+    return (_fast or _load_fast()).block_join_workspace_bytes(x, b, w_post, bias_post, w_pre,
+                                                              bias_pre, gate, kind, scale, eps)
 
 
 def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=None, w_pre=None,
@@ -461,42 +346,20 @@ def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=No
     dbias_post, dw_pre and dbias_pre, None for what has no input or is not in
     `want` (a set of those names; None: all).  workspace: device scratch of
     zero_block_join_workspace_bytes (None: allocated here)."""
-    d, p, device, act, hidden = _join_args(x, b, gate, w_post, bias_post, w_pre, bias_pre, kind,
-                                           scale, eps, None if d_n is None else d_n.dtype, d_o,
-                                           d_n)
-    p_stats = None
-    if stats is not None:
-        p_stats = _result(stats, "stats", x, (d.rows, 4), torch.float32).data_ptr()
-    out, at = {}, []
-    unused = False
-    for name, like in (("dx", x), ("db", b), ("dgate", gate), ("dw_post", w_post),
-                       ("dbias_post", bias_post), ("dw_pre", w_pre), ("dbias_pre", bias_pre)):
-        t = ptr = None
-        if like is not None and (want is None or name in want):
-            if d_n is None and name in ("dw_pre", "dbias_pre"):
-                t = torch.zeros_like(like)  # n was not used
-                unused = True
-            else:
-                t = (torch.empty_like(like) if like.is_contiguous() else
-                     torch.empty(like.shape, dtype=like.dtype, device=like.device))
-                ptr = t.data_ptr()
-        out[name] = t
-        at.append(ptr)
-    sums = any(at[3:]) or (d.gate_kind == GATE_CHANNEL and at[2])
-    p_ws, need, ws = None, 0, None
-    if sums:
-        need = _join_need(d)
-        ws = _workspace(workspace, need, device)
-        p_ws = ws.data_ptr()
-    if stream is not None:
-        _keep_for(stream, *out.values(), ws if workspace is None else None)
-    if unused and not any(at):
-        return out
-    _check((_lib or _load()).zero_block_join_backward(
-        ctypes.byref(d), ctypes.byref(p), None if d_o is None else d_o.data_ptr(),
-        None if d_n is None else d_n.data_ptr(), p_stats, ctypes.byref(JoinGradsC(*at)), p_ws,
-        need, _stream(stream, device)))
-    return out
+    if stream is None:
+        return (_fast or _load_fast()).block_join_backward(
+            x, b, w_post, bias_post, w_pre, bias_pre, gate, kind, scale, eps, d_o, d_n, stats,
+            want, workspace, None)
+    own = workspace is None
+    if own:
+        workspace = torch.empty(zero_block_join_workspace_bytes(
+            x, b, w_post=w_post, bias_post=bias_post, w_pre=w_pre, bias_pre=bias_pre, gate=gate,
+            kind=kind, scale=scale, eps=eps), dtype=torch.uint8, device=x.device)
+    got = (_fast or _load_fast()).block_join_backward(
+        x, b, w_post, bias_post, w_pre, bias_pre, gate, kind, scale, eps, d_o, d_n, stats, want,
+        workspace, _handle(stream))
+    _keep_for(stream, *got.values(), workspace if own else None)
+    return got
 
 
 def _even_rows(t):
@@ -563,125 +426,63 @@ def zero_expert_sort_workspace_bytes(tokens: int, topk: int, n_experts: int) -> 
     return need.value
 
 
-_sort_need = functools.lru_cache(maxsize=256)(zero_expert_sort_workspace_bytes)
-
-
 def zero_expert_sort(ids, n_experts: int, workspace=None, stream=None) -> ExpertOrder:
     """Rows of every token's choices in expert order (see zero.h).  ids:
     [tokens, topk] int32 or int64; a choice outside [0, n_experts) is
     dropped.  workspace: device scratch of zero_expert_sort_workspace_bytes
     (None: allocated here)."""
-    device = _current(ids, "ids")
-    if ids.dim() != 2 or not ids.is_contiguous():
-        raise ValueError("ids: expected a contiguous [tokens, topk] tensor")
-    if ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"ids: expected int32 or int64, got {ids.dtype}")
-    tokens, topk = ids.shape
-    if topk < 1:
-        raise ValueError("ids: topk must be at least 1")
-    where = ids.device
-    offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=where)
-    rows = torch.empty(ids.shape, dtype=torch.int32, device=where)
-    pairs = torch.empty(tokens * topk, dtype=torch.int32, device=where)
-    need = _sort_need(tokens, topk, n_experts)
-    ws = _workspace(workspace, need, device) if need else None
+    if stream is not None and workspace is None and isinstance(ids, torch.Tensor) and ids.dim() == 2:
+        need = zero_expert_sort_workspace_bytes(*ids.shape, n_experts) if ids.shape[1] else 0
+        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=ids.device)
+        _keep_for(stream, workspace if ids.is_cuda else None)
+    got = (_fast or _load_fast()).expert_sort(ids, n_experts, workspace,
+                                              None if stream is None else _handle(stream))
     if stream is not None:
-        _keep_for(stream, offsets, rows, pairs, ws if workspace is None else None)
-    _check((_lib or _load()).zero_expert_sort(ids.data_ptr() or None, ids.element_size(), tokens, topk,
-                                  n_experts, offsets.data_ptr(), rows.data_ptr() or None,
-                                  pairs.data_ptr() or None,
-                                  None if ws is None else ws.data_ptr(), need,
-                                  _stream(stream, device)))
-    return ExpertOrder(offsets, rows, pairs, n_experts, tokens, topk)
-
-
-def _sorted_rows(t, what: str, order: ExpertOrder):
-    """(device, type, hidden) of a tensor [tokens * topk, hidden]."""
-    device = _current(t, what)
-    if order.rows.get_device() != device:
-        _on(order.rows, "order", device)
-    if t.dim() != 2 or t.shape[0] != order.tokens * order.topk or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous [{order.tokens * order.topk}, hidden] "
-                         "tensor")
-    return device, _type(t, what), t.shape[1]
-
-
-def _token_rows(t, what: str, order: ExpertOrder):
-    """(device, type, hidden, row stride) of a tensor [tokens, hidden]."""
-    device = _current(t, what)
-    if order.rows.get_device() != device:
-        _on(order.rows, "order", device)
-    if t.dim() != 2 or t.shape[0] != order.tokens:
-        raise ValueError(f"{what}: expected [{order.tokens}, hidden], got {tuple(t.shape)}")
-    return device, _type(t, what), t.shape[1], _row_stride(t, what, t.shape, device)
-
-
-def _expert_weights(weights, order: ExpertOrder, device: int):
-    if weights.get_device() != device:
-        _on(weights, "weights", device)
-    if weights.shape != order.rows.shape or not weights.is_contiguous():
-        raise ValueError(f"weights: expected a contiguous [{order.tokens}, {order.topk}] tensor")
-    return _type(weights, "weights")
+        _keep_for(stream, *got)
+    return ExpertOrder(*got, n_experts, ids.shape[0], ids.shape[1])
 
 
 def zero_expert_dispatch(x, order: ExpertOrder, out=None, stream=None):
     """Tokens copied to their rows in expert order, [tokens * topk, hidden];
     the rows past the last kept choice are zero."""
-    device, code, hidden, stride = _token_rows(x, "x", order)
-    xs = _result(out, "out", x, (order.tokens * order.topk, hidden), x.dtype)
+    xs = (_fast or _load_fast()).expert_dispatch(x, order.offsets, order.rows, order.n_experts,
+                                                 order.tokens, order.topk, out,
+                                                 None if stream is None else _handle(stream))
     if stream is not None:
-        _keep_for(stream, xs if out is None else None)
-    _check((_lib or _load()).zero_expert_dispatch(x.data_ptr(), stride, code, order.tokens, order.topk, hidden,
-                                      order.offsets.data_ptr(), order.n_experts,
-                                      order.rows.data_ptr(), xs.data_ptr(),
-                                      _stream(stream, device)))
+        _keep_for(stream, xs)
     return xs
 
 
 def zero_expert_dispatch_backward(dxs, order: ExpertOrder, out=None, stream=None):
     """Each token's gradient: the sum of its rows'."""
-    device, code, hidden = _sorted_rows(dxs, "dxs", order)
-    dx = _result(out, "out", dxs, (order.tokens, hidden), dxs.dtype)
+    dx = (_fast or _load_fast()).expert_dispatch_backward(
+        dxs, order.offsets, order.rows, order.n_experts, order.tokens, order.topk, out,
+        None if stream is None else _handle(stream))
     if stream is not None:
-        _keep_for(stream, dx if out is None else None)
-    _check((_lib or _load()).zero_expert_dispatch_backward(dxs.data_ptr(), code, order.tokens, order.topk,
-                                               hidden, order.rows.data_ptr(), dx.data_ptr(),
-                                               _stream(stream, device)))
+        _keep_for(stream, dx)
     return dx
 
 
 def zero_expert_combine(ys, weights, order: ExpertOrder, out=None, stream=None):
     """Each token's weighted sum of its rows; zero when all its choices were
     dropped."""
-    device, code, hidden = _sorted_rows(ys, "ys", order)
-    wcode = _expert_weights(weights, order, device)
-    y = _result(out, "out", ys, (order.tokens, hidden), ys.dtype)
+    y = (_fast or _load_fast()).expert_combine(ys, weights, order.offsets, order.rows,
+                                               order.n_experts, order.tokens, order.topk, out,
+                                               None if stream is None else _handle(stream))
     if stream is not None:
-        _keep_for(stream, y if out is None else None)
-    _check((_lib or _load()).zero_expert_combine(ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
-                                     order.topk, hidden, order.rows.data_ptr(), y.data_ptr(),
-                                     _stream(stream, device)))
+        _keep_for(stream, y)
     return y
 
 
 def zero_expert_combine_backward(dy, ys, weights, order: ExpertOrder, want_weights: bool = True,
                                  stream=None):
     """(dys, dweights) of zero_expert_combine; dweights None unless wanted."""
-    device, code, hidden = _sorted_rows(ys, "ys", order)
-    _, dcode, dhidden, stride = _token_rows(dy, "dy", order)
-    if dcode != code or dhidden != hidden:
-        raise TypeError(f"dy: expected {ys.dtype} rows of {hidden}, got {dy.dtype} of {dhidden}")
-    wcode = _expert_weights(weights, order, device)
-    dys = _new(ys)
-    dweights = _new(weights) if want_weights else None
+    got = (_fast or _load_fast()).expert_combine_backward(
+        dy, ys, weights, order.offsets, order.rows, order.n_experts, order.tokens, order.topk,
+        want_weights, None if stream is None else _handle(stream))
     if stream is not None:
-        _keep_for(stream, dys, dweights)
-    _check((_lib or _load()).zero_expert_combine_backward(
-        dy.data_ptr(), stride, ys.data_ptr(), code, weights.data_ptr(), wcode, order.tokens,
-        order.topk, hidden, order.offsets.data_ptr(), order.n_experts, order.rows.data_ptr(),
-        dys.data_ptr(), None if dweights is None else dweights.data_ptr(),
-        _stream(stream, device)))
-    return dys, dweights
+        _keep_for(stream, *got)
+    return got
 
 
 class _ExpertDispatch(torch.autograd.Function):
