@@ -999,3 +999,61 @@ def test_calls_keep_nothing():
     assert now[:-1] == held[:-1]
     assert abs(now[-1] - held[-1]) < 100    # None: immortal, or within the interpreter's own use
     assert torch.cuda.memory_allocated() == bytes_
+
+
+@pytest.mark.parametrize("dtype", [H16, B16, F32])
+@pytest.mark.parametrize("K", [1, 2, 3, 5])
+@pytest.mark.parametrize("Hd", [1, 7, 8, 9, 16, 17, 31, 33, 60, 517, 2051])
+def test_expert_rows_of_any_length_start_and_stride(Hd, K, dtype):
+    """Inputs and outputs start at odd elements, the tokens' rows are `pad`
+    apart, and what lies between and around them is NaN and stays so."""
+    T, n_experts = 11, 4
+    for by, pad in ((1, 0), (2, 3), (3, 1), (5, 8), (7, 5)):
+        g = gen(by + Hd)
+        order = Z.zero_expert_sort(choose(T, K, n_experts, by, 0.2), n_experts)
+        M = int(order.offsets[-1])
+        pairs = order.pairs[:M].long()
+        token = pairs // K
+
+        def rows(n, stride):
+            store = torch.full((by + n * stride + 24,), float("nan"), dtype=dtype, device="cuda")
+            view = store.as_strided((n, Hd), (stride, 1), by)
+            view.copy_(torch.randn(n, Hd, device="cuda", generator=g))
+            return view
+
+        def outputs(n):
+            store = torch.full((by + n * Hd + 24,), float("nan"), dtype=dtype, device="cuda")
+            return store, store[by:by + n * Hd].view(n, Hd)
+
+        def untouched(store, n):
+            return bool(store[:by].isnan().all() and store[by + n * Hd:].isnan().all())
+
+        x, dy = rows(T, Hd + pad), rows(T, Hd + pad)
+        ys, dxs = rows(T * K, Hd), rows(T * K, Hd)
+        ys[M:], dxs[M:] = float("nan"), float("nan")
+        w = torch.rand(T, K, device="cuda", generator=g)
+        wd = w.double().reshape(-1)[pairs][:, None]
+
+        def back(t):
+            return torch.zeros(T, Hd, dtype=torch.float64, device="cuda").index_add_(0, token, t)
+
+        step = 10 * 2.0 ** -24    # K products and sums in binary32
+        store, xs = outputs(T * K)
+        Z.zero_expert_dispatch(x, order, out=xs)
+        assert torch.equal(xs[:M], x[token]) and not xs[M:].any() and untouched(store, T * K)
+        store, y = outputs(T)
+        Z.zero_expert_combine(ys, w, order, out=y)
+        terms = wd * ys[:M].double()
+        close(y, back(terms), step * back(terms.abs()), "y")
+        assert untouched(store, T)
+        store, dx = outputs(T)
+        Z.zero_expert_dispatch_backward(dxs, order, out=dx)
+        close(dx, back(dxs[:M].double()), step * back(dxs[:M].double().abs()), "dx")
+        assert untouched(store, T)
+        dys, dw = Z.zero_expert_combine_backward(dy, ys, w, order)
+        close(dys[:M], wd * dy[token].double(), step * (wd * dy[token].double()).abs(), "dys")
+        assert not dys[M:].any()
+        ref, size = (torch.zeros(T * K, dtype=torch.float64, device="cuda") for _ in range(2))
+        prod = dy[token].double() * ys[:M].double()
+        ref[pairs], size[pairs] = prod.sum(1), prod.abs().sum(1)
+        close(dw.reshape(-1), ref, E * size, "dweights")

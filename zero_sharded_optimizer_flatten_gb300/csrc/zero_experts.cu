@@ -238,7 +238,7 @@ struct SortShape {
 
 // ---------------------------------------------------------------------------
 // The rows.  A group of 8 to 256 lanes takes a token, octet by octet
-// (16-byte aligned rows) or eight single columns at a time, `lanes` apart.
+// (16-byte aligned rows), or 16-byte pieces and single columns (other rows).
 // The rows of all its choices are in flight together, up to 4 (MORE: 4 at a
 // time).  (One after the other, the combination of two of 64 experts'
 // rows of 4096 bf16, 16384 tokens, took 85 us; together 75; with two columns'
@@ -251,10 +251,9 @@ struct SortShape {
 constexpr int kRowThreads = 256;
 constexpr int kTogether = 4;
 
-// CTAs of an SM that K rows' octets leave registers for; single columns need
-// a register each.
-constexpr int row_ctas(bool vec, int k, size_t elem, int most) {
-  const int held = vec ? k * static_cast<int>(elem) : 4 * k;  // of a row's eight columns, in pairs of registers
+// CTAs of an SM that K rows' octets leave registers for.
+constexpr int row_ctas(int k, size_t elem, int most) {
+  const int held = k * static_cast<int>(elem);  // of a row's eight columns, in pairs of registers
   return held >= 32 ? 2 : held >= 16 ? 3 : held >= 8 ? 4 : most;
 }
 
@@ -270,72 +269,112 @@ struct RowArgs {
   int32_t topk, weight_type, lanes;
 };
 
-// Eight columns of a row, as they were loaded.
-template <class T, bool VEC>
-struct Cols {
-  Octet<T> o;
-  T e[8];
-  __device__ __forceinline__ void load(const T* row, int c, int lanes, int hidden) {
-    if constexpr (VEC) {
-      o.load(row + c);
-    } else {
+// 16 bytes of a row.
+template <class T>
+struct Piece {
+  static constexpr int kCols = 16 / sizeof(T);
+  uint32_t w[4];
+  __device__ __forceinline__ void widen(float (&v)[kCols]) const {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i * lanes < hidden) e[i] = row[c + i * lanes];
-    }
+    for (int i = 0; i < 4; ++i)
+      if constexpr (sizeof(T) == 4)
+        v[i] = __uint_as_float(w[i]);
+      else
+        Elem<T>::unpack(w[i], v[2 * i], v[2 * i + 1]);
   }
-  __device__ __forceinline__ void widen(float (&v)[8]) const {
-    if constexpr (VEC) {
-      o.widen(v);
-    } else {
+  __device__ __forceinline__ void narrow(const float (&v)[kCols]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = Elem<T>::widen(e[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(v[i]);
+      else
+        w[i] = Elem<T>::pack(v[2 * i], v[2 * i + 1]);
   }
-  __device__ __forceinline__ void copy_to(T* row, int c, int lanes, int hidden) const {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int k = 0; k < Octet<T>::kChunks; ++k) reinterpret_cast<uint4*>(row + c)[k] = o.w[k];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i * lanes < hidden) row[c + i * lanes] = e[i];
-    }
-  }
-  static __device__ __forceinline__ void store(T* row, int c, int lanes, int hidden, const float (&v)[8]) {
-    if constexpr (VEC) {
-      Elem<T>::store8(row + c, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i * lanes < hidden) row[c + i * lanes] = Elem<T>::narrow(v[i]);
-    }
+  __device__ __forceinline__ void store(T* p) const {  // 16-byte aligned
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
-// The group's token, the thread's first column and the columns of a round.
-template <bool VEC>
+// 16 bytes that start at any element, as they were loaded: the one or two
+// aligned pieces that hold them.  `shifted` puts them together, so that the
+// loads of a thread's rows go out before any of them is waited for.
+template <class T>
+struct Window {
+  uint4 a, b;
+  __device__ __forceinline__ static int shift(const T* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15); }
+  __device__ __forceinline__ void load(const T* p) {
+    const int s = shift(p);
+    const char* at = reinterpret_cast<const char*>(p) - s;
+    a = *reinterpret_cast<const uint4*>(at);
+    b = *reinterpret_cast<const uint4*>(at + (s ? 16 : 0));
+  }
+  __device__ __forceinline__ Piece<T> shifted(int s) const {
+    uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = s & 8 ? v[i + 2] : v[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = s & 4 ? v[i + 1] : v[i];
+    Piece<T> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = sizeof(T) == 4 ? v[i] : __funnelshift_r(v[i], v[i + 1], (s & 2) * 8);
+    return r;
+  }
+};
+
+// How a row that is written falls into 16-byte pieces: `head` single columns,
+// `pieces`, and single columns again, `ends` of them in all.  A window reaches
+// less than 16 bytes past its columns on either side: into the row before or
+// after, but out of the storage from the first piece of its first row and the
+// last of its last.  Where such a row is read, `inner` makes single columns of
+// these two.
+template <class T>
+struct Frame {
+  int head, pieces, ends;
+  __device__ __forceinline__ Frame(const T* row, int hidden, bool inner) {
+    constexpr int P = Piece<T>::kCols;
+    head = min(hidden, static_cast<int>(-reinterpret_cast<uintptr_t>(row) & 15) / static_cast<int>(sizeof(T)));
+    pieces = (hidden - head) / P;
+    if (inner) {
+      head += min(pieces, 1) * P;
+      pieces = max(pieces - 2, 0);
+    }
+    ends = hidden - pieces * P;
+  }
+  __device__ __forceinline__ int column(int piece) const { return head + piece * Piece<T>::kCols; }
+  __device__ __forceinline__ int end_column(int e) const { return e < head ? e : e + pieces * Piece<T>::kCols; }
+};
+
+// The group's token, and the thread's first column and a round's columns
+// where rows are taken octet by octet.
 struct Place {
   int64_t token;
   int lane, lanes, first, round;
   __device__ __forceinline__ explicit Place(int lanes_) : lanes(lanes_) {
     token = static_cast<int64_t>(blockIdx.x) * (kRowThreads / lanes) + threadIdx.x / lanes;
     lane = threadIdx.x % lanes;
-    first = VEC ? 8 * lane : lane;
+    first = 8 * lane;
     round = 8 * lanes;
   }
 };
 
 // Rows past the last kept pair are zero: the token's own share of them.
 template <class T, bool VEC>
-__device__ __forceinline__ void clear_past_end(const RowArgs& a, const Place<VEC>& me, T* out) {
+__device__ __forceinline__ void clear_past_end(const RowArgs& a, const Place& me, T* out) {
   const int64_t M = __ldg(a.total);
   const int H = static_cast<int>(a.hidden);
   const float z[8] = {};
   for (int k = 0; k < a.topk; ++k) {
     const int64_t i = me.token * a.topk + k;
     if (i < M) continue;
-    for (int c = me.first; c < H; c += me.round) Cols<T, VEC>::store(out + i * H, c, me.lanes, H, z);
+    T* row = out + i * H;
+    if constexpr (VEC) {
+      for (int c = me.first; c < H; c += me.round) Elem<T>::store8(row + c, z);
+    } else {
+      const Frame<T> f(row, H, false);
+      for (int u = me.lane; u < f.pieces; u += me.lanes)
+        *reinterpret_cast<uint4*>(row + f.column(u)) = make_uint4(0, 0, 0, 0);
+      for (int e = me.lane; e < f.ends; e += me.lanes) row[f.end_column(e)] = Elem<T>::narrow(0.f);
+    }
   }
 }
 
@@ -355,10 +394,10 @@ struct Choices {
   }
 };
 
-template <class T, bool VEC, int K, bool MORE>
-__global__ void __launch_bounds__(kRowThreads, VEC ? 6 : 3) k_dispatch(const RowArgs a) {
+template <class T, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads, 6) k_dispatch(const RowArgs a) {
   constexpr int kParts = K == 1 ? 2 : 1;
-  const Place<VEC> me(a.lanes);
+  const Place me(a.lanes);
   if (me.token >= a.tokens) return;
   const int H = static_cast<int>(a.hidden);
   const T* x = static_cast<const T*>(a.in) + me.token * a.stride;
@@ -366,30 +405,30 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 6 : 3) k_dispatch(const Row
   const int64_t p0 = me.token * a.topk;
   const Choices<K> ch(a, p0, 0, true);
   for (int c0 = me.first; c0 < H; c0 += kParts * me.round) {
-    Cols<T, VEC> v[kParts];
+    Octet<T> v[kParts];
 #pragma unroll
     for (int q = 0; q < kParts; ++q)
-      if (c0 + q * me.round < H) v[q].load(x, c0 + q * me.round, me.lanes, H);
+      if (c0 + q * me.round < H) v[q].load(x + c0 + q * me.round);
 #pragma unroll
     for (int q = 0; q < kParts; ++q) {
       const int c = c0 + q * me.round;
       if (c >= H) continue;
 #pragma unroll
       for (int i = 0; i < K; ++i)
-        if (ch.row[i] >= 0) v[q].copy_to(xs + ch.row[i] * static_cast<int64_t>(H), c, me.lanes, H);
+        if (ch.row[i] >= 0) v[q].store(xs + ch.row[i] * static_cast<int64_t>(H) + c);
       for (int k = K; MORE && k < a.topk; ++k) {
         const int64_t r = __ldg(a.rows + p0 + k);
-        if (r >= 0) v[q].copy_to(xs + r * H, c, me.lanes, H);
+        if (r >= 0) v[q].store(xs + r * H + c);
       }
     }
   }
-  clear_past_end<T, VEC>(a, me, xs);
+  clear_past_end<T, true>(a, me, xs);
 }
 
-template <class T, bool VEC, int K, bool MORE>
-__global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 6)) k_combine(const RowArgs a) {
+template <class T, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads, row_ctas(K, sizeof(T), 6)) k_combine(const RowArgs a) {
   constexpr int kParts = K == 1 ? 2 : 1;
-  const Place<VEC> me(a.lanes);
+  const Place me(a.lanes);
   if (me.token >= a.tokens) return;
   const int H = static_cast<int>(a.hidden);
   const T* in = static_cast<const T*>(a.in);
@@ -403,13 +442,13 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 6)) k
 #pragma unroll
       for (int n = 0; n < 8; ++n) s[q][n] = 0.f;
     auto add = [&](const Choices<K>& ch) {
-      Cols<T, VEC> v[kParts][K];
+      Octet<T> v[kParts][K];
 #pragma unroll
       for (int q = 0; q < kParts; ++q)
 #pragma unroll
         for (int i = 0; i < K; ++i)
           if (ch.row[i] >= 0 && c0 + q * me.round < H)
-            v[q][i].load(in + ch.row[i] * static_cast<int64_t>(H), c0 + q * me.round, me.lanes, H);
+            v[q][i].load(in + ch.row[i] * static_cast<int64_t>(H) + c0 + q * me.round);
 #pragma unroll
       for (int q = 0; q < kParts; ++q)
 #pragma unroll
@@ -429,14 +468,44 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 6)) k
     }
 #pragma unroll
     for (int q = 0; q < kParts; ++q)
-      if (c0 + q * me.round < H) Cols<T, VEC>::store(y, c0 + q * me.round, me.lanes, H, s[q]);
+      if (c0 + q * me.round < H) Elem<T>::store8(y + c0 + q * me.round, s[q]);
   }
 }
 
-template <class T, bool VEC, int K, bool MORE>
-__global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 5)) k_combine_backward(const RowArgs a) {
+// Sums of the choices' dots over the group's lanes, to dweights; every thread
+// of the CTA is here.
+template <int K>
+__device__ __forceinline__ void store_dots(const RowArgs& a, const Place& me, bool live, int64_t p0, int k0,
+                                           float (&dot)[K], float (&part)[K][kRowThreads / 32]) {
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+    for (int o = min(me.lanes, 32) >> 1; o > 0; o >>= 1) dot[i] += __shfl_xor_sync(kFull, dot[i], o);
+  if (me.lanes > 32) {
+    // the next choices' sums go to the other half
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) part[i][warp] = dot[i];
+    }
+    __syncthreads();
+    const int warps = me.lanes >> 5, w0 = warp / warps * warps;
+    if (me.lane < K) {
+      dot[0] = 0.f;
+      for (int w = 0; w < warps; ++w) dot[0] += part[me.lane][w0 + w];
+    }
+  } else {
+#pragma unroll
+    for (int i = 1; i < K; ++i)
+      if (me.lane == i) dot[0] = dot[i];
+  }
+  if (live && me.lane < K && k0 + me.lane < a.topk)
+    store_any(a.dweights, p0 + k0 + me.lane, a.weight_type, dot[0]);
+}
+
+template <class T, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads, row_ctas(K, sizeof(T), 5)) k_combine_backward(const RowArgs a) {
   __shared__ float part[2][K][kRowThreads / 32];
-  const Place<VEC> me(a.lanes);
+  const Place me(a.lanes);
   const bool live = me.token < a.tokens;  // every thread meets the barriers below
   const int H = static_cast<int>(a.hidden);
   const T* dy = static_cast<const T*>(a.in) + (live ? me.token : 0) * a.stride;
@@ -449,11 +518,11 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 5)) k
     float dot[K] = {};
     if (live) {
       for (int c = me.first; c < H; c += me.round) {
-        Cols<T, VEC> g, v[K];
-        g.load(dy, c, me.lanes, H);
+        Octet<T> g, v[K];
+        g.load(dy + c);
 #pragma unroll
         for (int i = 0; i < K; ++i)
-          if (ch.row[i] >= 0) v[i].load(ys + ch.row[i] * static_cast<int64_t>(H), c, me.lanes, H);
+          if (ch.row[i] >= 0) v[i].load(ys + ch.row[i] * static_cast<int64_t>(H) + c);
         float d[8];
         g.widen(d);
 #pragma unroll
@@ -463,39 +532,209 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(VEC, K, sizeof(T), 5)) k
             v[i].widen(f);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-              if (VEC || c + n * me.lanes < H) dot[i] = fmaf(d[n], f[n], dot[i]);
+              dot[i] = fmaf(d[n], f[n], dot[i]);
               f[n] = d[n] * ch.weight[i];
             }
-            Cols<T, VEC>::store(dys + ch.row[i] * static_cast<int64_t>(H), c, me.lanes, H, f);
+            Elem<T>::store8(dys + ch.row[i] * static_cast<int64_t>(H) + c, f);
           }
       }
     }
-    if (!a.dweights) continue;
+    if (a.dweights) store_dots<K>(a, me, live, p0, k0, dot, part[flip]);
+  }
+  if (live) clear_past_end<T, true>(a, me, dys);
+}
+
+// The same for rows that start anywhere or end inside 16 bytes, by the pieces
+// of the rows that are written.
+//
+// Measured, 16384 tokens, 2 of 64, 4097 bf16, us and share of a plain copy's
+// bandwidth; in brackets with eight single columns a thread: dispatch 71
+// (0.83) [139], combine 97 (0.61) [119], its gradient 152 (0.65) [388].
+// 30000 tokens, 4 of 16, 1001 fp32: dispatch 97 (0.92) [119], the combination's
+// gradient 269 (0.58) [351].
+
+template <class T>
+__global__ void __launch_bounds__(kRowThreads, 8) k_dispatch_any(const RowArgs a) {
+  const Place me(a.lanes);
+  if (me.token >= a.tokens) return;
+  const int H = static_cast<int>(a.hidden);
+  const T* x = static_cast<const T*>(a.in) + me.token * a.stride;
+  const bool inner = me.token == 0 || me.token == a.tokens - 1;
+  T* xs = static_cast<T*>(a.out);
+  const int64_t p0 = me.token * a.topk;
+  for (int k = 0; k < a.topk; ++k) {
+    const int64_t r = __ldg(a.rows + p0 + k);
+    if (r < 0) continue;
+    T* row = xs + r * H;
+    const Frame<T> f(row, H, inner);
+    const int shift = Window<T>::shift(x + f.head);
+    T end;
+    if (me.lane < f.ends) end = x[f.end_column(me.lane)];
+    for (int u = me.lane; u < f.pieces; u += me.lanes) {
+      Window<T> v;
+      v.load(x + f.column(u));
+      v.shifted(shift).store(row + f.column(u));
+    }
+    if (me.lane < f.ends) row[f.end_column(me.lane)] = end;
+    for (int e = me.lane + me.lanes; e < f.ends; e += me.lanes) row[f.end_column(e)] = x[f.end_column(e)];
+  }
+  clear_past_end<T, false>(a, me, xs);
+}
+
+// A thread's single column is loaded before the pieces are waited for (107 us
+// at the first size with the loads after them).
+template <class T, int K>
+__global__ void __launch_bounds__(kRowThreads, K == 1 ? 6 : 5) k_combine_any(const RowArgs a) {
+  constexpr int P = Piece<T>::kCols;
+  const Place me(a.lanes);
+  if (me.token >= a.tokens) return;
+  const int H = static_cast<int>(a.hidden);
+  const T* in = static_cast<const T*>(a.in);
+  T* y = static_cast<T*>(a.out) + me.token * H;
+  const int64_t last = a.tokens * a.topk - 1;
+  const Choices<K> ch(a, me.token * a.topk, 0, true);
+  bool inner = false;
+#pragma unroll
+  for (int i = 0; i < K; ++i) inner |= ch.row[i] == 0 || ch.row[i] == last;
+  const Frame<T> f(y, H, inner);
+  T end[K];
+  if (me.lane < f.ends)
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      for (int o = min(me.lanes, 32) >> 1; o > 0; o >>= 1) dot[i] += __shfl_xor_sync(kFull, dot[i], o);
-    if (me.lanes > 32) {
-      // the next choices' sums go to the other half
-      const int warp = threadIdx.x >> 5;
-      if ((threadIdx.x & 31) == 0) {
+      if (ch.row[i] >= 0) end[i] = in[ch.row[i] * static_cast<int64_t>(H) + f.end_column(me.lane)];
+  for (int u = me.lane; u < f.pieces; u += me.lanes) {
+    const T* from = in + f.column(u);
+    float s[P] = {};
+    Window<T> v[K];
 #pragma unroll
-        for (int i = 0; i < K; ++i) part[flip][i][warp] = dot[i];
-      }
-      __syncthreads();
-      const int warps = me.lanes >> 5, w0 = warp / warps * warps;
-      if (me.lane < K) {
-        dot[0] = 0.f;
-        for (int w = 0; w < warps; ++w) dot[0] += part[flip][me.lane][w0 + w];
-      }
-    } else {
+    for (int i = 0; i < K; ++i)
+      if (ch.row[i] >= 0) v[i].load(from + ch.row[i] * static_cast<int64_t>(H));
 #pragma unroll
-      for (int i = 1; i < K; ++i)
-        if (me.lane == i) dot[0] = dot[i];
-    }
-    if (live && me.lane < K && k0 + me.lane < a.topk)
-      store_any(a.dweights, p0 + k0 + me.lane, a.weight_type, dot[0]);
+    for (int i = 0; i < K; ++i)
+      if (ch.row[i] >= 0) {
+        float w[P];
+        v[i].shifted(Window<T>::shift(from + ch.row[i] * static_cast<int64_t>(H))).widen(w);
+#pragma unroll
+        for (int n = 0; n < P; ++n) s[n] = fmaf(ch.weight[i], w[n], s[n]);
+      }
+    Piece<T> out;
+    out.narrow(s);
+    out.store(y + f.column(u));
   }
-  if (live) clear_past_end<T, VEC>(a, me, dys);
+  for (int e = me.lane; e < f.ends; e += me.lanes) {
+    const int c = f.end_column(e);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (ch.row[i] >= 0)
+        s = fmaf(ch.weight[i], Elem<T>::widen(e == me.lane ? end[i] : in[ch.row[i] * static_cast<int64_t>(H) + c]), s);
+    y[c] = Elem<T>::narrow(s);
+  }
+}
+
+// The combination by single columns, eight a thread, `lanes` apart: fp32 rows,
+// where a column is a full-rate access and the shift only adds work (30000
+// tokens, 4 of 16, 1001 fp32 115 us; by pieces 146), and more than two choices,
+// whose windows and sums leave few threads an SM (4 of 16, 1001 bf16 117, by
+// pieces 120; 8 of 64, 8000 tokens of 2047 bf16 101, by pieces 148).
+template <class T, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads, K == 4 ? 3 : 4) k_combine_columns(const RowArgs a) {
+  const Place me(a.lanes);
+  if (me.token >= a.tokens) return;
+  const int H = static_cast<int>(a.hidden);
+  const T* in = static_cast<const T*>(a.in);
+  T* y = static_cast<T*>(a.out) + me.token * H;
+  const int64_t p0 = me.token * a.topk;
+  const Choices<K> first(a, p0, 0, !MORE);
+  for (int c0 = me.lane; c0 < H; c0 += me.round) {
+    float s[8] = {};
+    auto add = [&](const Choices<K>& ch) {
+      T v[K][8];
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if (ch.row[i] >= 0) {
+          const T* row = in + ch.row[i] * static_cast<int64_t>(H);
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            if (c0 + n * me.lanes < H) v[i][n] = row[c0 + n * me.lanes];
+        }
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if (ch.row[i] >= 0)
+#pragma unroll
+          for (int n = 0; n < 8; ++n) s[n] = fmaf(ch.weight[i], Elem<T>::widen(v[i][n]), s[n]);
+    };
+    if constexpr (MORE) {
+#pragma unroll 1
+      for (int k0 = 0; k0 < a.topk; k0 += K) add(Choices<K>(a, p0, k0, true));
+    } else {
+      add(first);
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      if (c0 + n * me.lanes < H) y[c0 + n * me.lanes] = Elem<T>::narrow(s[n]);
+  }
+}
+
+template <class T, int K, bool MORE>
+__global__ void __launch_bounds__(kRowThreads) k_combine_backward_any(const RowArgs a) {
+  // a lane has eight columns: two fp32 windows, both in flight
+  constexpr int P = Piece<T>::kCols, kParts = sizeof(T) == 4 ? 2 : 1;
+  __shared__ float part[2][K][kRowThreads / 32];
+  const Place me(a.lanes);
+  const bool live = me.token < a.tokens;  // every thread meets the barriers of store_dots
+  const int H = static_cast<int>(a.hidden);
+  const T* dy = static_cast<const T*>(a.in) + (live ? me.token : 0) * a.stride;
+  const T* ys = static_cast<const T*>(a.ys);
+  const int64_t last = a.tokens * a.topk - 1;
+  T* dys = static_cast<T*>(a.out);
+  const int64_t p0 = (live ? me.token : 0) * a.topk;
+  int flip = 0;
+  for (int k0 = 0; k0 == 0 || (MORE && k0 < a.topk); k0 += K, flip ^= 1) {
+    const Choices<K> ch(a, p0, k0, live);
+    float dot[K] = {};
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if (ch.row[i] < 0) continue;
+      const int64_t at = ch.row[i] * static_cast<int64_t>(H);
+      const Frame<T> f(dys + at, H,
+                       me.token == 0 || me.token == a.tokens - 1 || ch.row[i] == 0 || ch.row[i] == last);
+      const int g_shift = Window<T>::shift(dy + f.head), v_shift = Window<T>::shift(ys + at + f.head);
+      for (int u = me.lane; u < f.pieces; u += kParts * me.lanes) {
+        Window<T> g[kParts], v[kParts];
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+          if (u + q * me.lanes < f.pieces) {
+            const int c = f.column(u + q * me.lanes);
+            g[q].load(dy + c);
+            v[q].load(ys + at + c);
+          }
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+          if (u + q * me.lanes < f.pieces) {
+            float d[P], w[P];
+            g[q].shifted(g_shift).widen(d);
+            v[q].shifted(v_shift).widen(w);
+#pragma unroll
+            for (int n = 0; n < P; ++n) {
+              dot[i] = fmaf(d[n], w[n], dot[i]);
+              w[n] = d[n] * ch.weight[i];
+            }
+            Piece<T> out;
+            out.narrow(w);
+            out.store(dys + at + f.column(u + q * me.lanes));
+          }
+      }
+      for (int e = me.lane; e < f.ends; e += me.lanes) {
+        const int c = f.end_column(e);
+        const float d = Elem<T>::widen(dy[c]);
+        dot[i] = fmaf(d, Elem<T>::widen(ys[at + c]), dot[i]);
+        dys[at + c] = Elem<T>::narrow(d * ch.weight[i]);
+      }
+    }
+    if (a.dweights) store_dots<K>(a, me, live, p0, k0, dot, part[flip]);
+  }
+  if (live) clear_past_end<T, false>(a, me, dys);
 }
 
 // ---------------------------------------------------------------------------
@@ -513,9 +752,20 @@ int launch_rows_k(RowOp op, const RowArgs& a, cudaStream_t s) {
   const int64_t per_cta = kRowThreads / copy.lanes;
   const int64_t grid = (a.tokens + per_cta - 1) / per_cta;
   void* args[] = {&copy};
-  const void* fn = op == RowOp::kDispatch  ? reinterpret_cast<const void*>(&k_dispatch<T, VEC, K, MORE>)
-                   : op == RowOp::kCombine ? reinterpret_cast<const void*>(&k_combine<T, VEC, K, MORE>)
-                                           : reinterpret_cast<const void*>(&k_combine_backward<T, VEC, K, MORE>);
+  const void* fn;
+  constexpr bool kByPieces = sizeof(T) == 2 && K <= 2;
+  if constexpr (VEC)
+    fn = op == RowOp::kDispatch  ? reinterpret_cast<const void*>(&k_dispatch<T, K, MORE>)
+         : op == RowOp::kCombine ? reinterpret_cast<const void*>(&k_combine<T, K, MORE>)
+                                 : reinterpret_cast<const void*>(&k_combine_backward<T, K, MORE>);
+  else if (op == RowOp::kDispatch)
+    fn = reinterpret_cast<const void*>(&k_dispatch_any<T>);
+  else if (op == RowOp::kCombineBackward)
+    fn = reinterpret_cast<const void*>(&k_combine_backward_any<T, K, MORE>);
+  else if constexpr (kByPieces)
+    fn = reinterpret_cast<const void*>(&k_combine_any<T, K>);
+  else
+    fn = reinterpret_cast<const void*>(&k_combine_columns<T, K, MORE>);
   return static_cast<int>(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), args, 0, s));
 }
 

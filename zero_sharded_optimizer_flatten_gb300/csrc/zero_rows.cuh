@@ -107,6 +107,10 @@ struct Octet {
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
   }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) reinterpret_cast<uint4*>(p)[k] = w[k];
+  }
 };
 
 // Element i of an array whose type is known only at run time (parameters,
