@@ -239,10 +239,21 @@ class GradNorm:
         self._norm = self.result[8:12].view(torch.float32)[0]
         self._args = (self.result.data_ptr(), self._workspace.data_ptr(), need.value)
         self.device = device
+        self._home = _raw_stream(device)  # the stream that the buffers were allocated on
+
+    def _on_stream(self, stream):
+        """Handle of the stream that a call runs on.  The object may be gone
+        before that stream has done the call's work, so another stream than
+        the buffers' own is recorded on them."""
+        handle = _stream(stream, self.device)
+        if handle != self._home:
+            _keep_for(torch.cuda.current_stream(self.device) if stream is None else stream,
+                      self.result, self._workspace)
+        return handle
 
     def __call__(self, stream=None):
         _check((_lib or _load()).zero_grad_norm(self._list, self.n, self.kind, *self._args,
-                                    _stream(stream, self.device)))
+                                                self._on_stream(stream)))
         return self._norm
 
     def read(self) -> NormResult:
@@ -270,24 +281,18 @@ class ClipGradNorm(GradNorm):
 
     def __call__(self, stream=None):
         _check((_lib or _load()).zero_clip_grad_norm(self._list, self.n, self.kind, self.max_norm,
-                                         *self._args, _stream(stream, self.device)))
+                                                     *self._args, self._on_stream(stream)))
         return self._norm
 
 
 def zero_grad_norm(grads, kind: str = "l2", stream=None):
     """Norm of all gradients as one vector (see zero.h); a float32 tensor."""
-    call = GradNorm(grads, kind)
-    if stream is not None:
-        _keep_for(stream, call.result, call._workspace)
-    return call(stream)
+    return GradNorm(grads, kind)(stream)
 
 
 def zero_clip_grad_norm(grads, max_norm: float, kind: str = "l2", out=None, stream=None):
     """Norm and clipping (see zero.h); returns the norm before clipping."""
-    call = ClipGradNorm(grads, max_norm, kind, out)
-    if stream is not None:
-        _keep_for(stream, call.result, call._workspace)
-    return call(stream)
+    return ClipGradNorm(grads, max_norm, kind, out)(stream)
 
 
 # ----------------------------------------------------------------------------
