@@ -72,3 +72,18 @@ def test_prepared_call_keeps_its_buffers_for_another_stream(cpu_calls, kind):
     call()
     assert cpu_calls.calls[-1][-1] == 9
     assert {t for s, t in cpu_calls.kept if s == 9} == own
+
+
+@pytest.mark.parametrize("kind", ["norm", "clip"])
+def test_prepared_call_refuses_another_current_device(cpu_calls, kind):
+    """Launches go to the current device: with another one than the buffers'
+    nothing is called."""
+    call = prepared(kind)
+    cpu_calls.device = 1
+    for stream in (None, cpu_calls.streams[9]):
+        with pytest.raises(ValueError, match="current device"):
+            call(stream)
+    assert cpu_calls.calls == []
+    cpu_calls.device = 0
+    call()
+    assert len(cpu_calls.calls) == 1

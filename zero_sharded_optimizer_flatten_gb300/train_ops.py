@@ -242,9 +242,12 @@ class GradNorm:
         self._home = _raw_stream(device)  # the stream that the buffers were allocated on
 
     def _on_stream(self, stream):
-        """Handle of the stream that a call runs on.  The object may be gone
-        before that stream has done the call's work, so another stream than
-        the buffers' own is recorded on them."""
+        """Handle of the stream that a call runs on; launches go to the current
+        device.  The object may be gone before that stream has done the call's
+        work, so another stream than the buffers' own is recorded on them."""
+        if _device() != self.device:
+            raise ValueError(f"prepared on cuda:{self.device}, but the current device is "
+                             f"cuda:{_device()}")
         handle = _stream(stream, self.device)
         if handle != self._home:
             _keep_for(torch.cuda.current_stream(self.device) if stream is None else stream,
