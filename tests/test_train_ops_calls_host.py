@@ -87,3 +87,28 @@ def test_prepared_call_refuses_another_current_device(cpu_calls, kind):
     cpu_calls.device = 0
     call()
     assert len(cpu_calls.calls) == 1
+
+
+class FakeTensor:
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_handles_of_the_default_stream_are_recorded_as_that_stream(monkeypatch):
+    """0 and 1 are the default stream's handles; a stream object made from
+    handle 0 would be a new stream of its own."""
+    made = []
+    default = object()
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda handle, device=None: made.append(handle) or ("external", handle))
+    t, given = FakeTensor(), FakeStream(9)
+    T._keep_for(0, t, None)
+    T._keep_for(1, t)
+    T._keep_for(64, t)
+    T._keep_for(given, t)
+    T._keep_for(None, t)
+    assert t.streams == [default, default, ("external", 64), given] and made == [64]

@@ -100,11 +100,19 @@ def _current(t, what: str) -> int:
     return device
 
 
+def _torch_stream(stream):
+    """A stream object for a stream or a handle.  0 and 1 are the default
+    stream's handles (ExternalStream(0) would be a new stream)."""
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.default_stream() if stream in (0, 1) else torch.cuda.ExternalStream(stream)
+
+
 def _keep_for(stream, *tensors):
     """Tensors allocated here and used on another stream than the current one."""
     if stream is None:
         return
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    s = _torch_stream(stream)
     for t in tensors:
         if t is not None:
             t.record_stream(s)
