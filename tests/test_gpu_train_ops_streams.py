@@ -54,3 +54,91 @@ def test_prepared_norm_dropped_right_after_its_call(given):
             assert held[-1].data_ptr() != at
         side.synchronize()
         assert abs(float(norm) - want) <= 1e-5 * want
+
+
+def small_join(rows=3000, hidden=1024):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, b = (torch.randn(rows, hidden, device="cuda", generator=g).bfloat16() for _ in range(2))
+    w = torch.ones(hidden, device="cuda", dtype=torch.bfloat16)
+    return x, b, w
+
+
+def test_gradients_of_an_unused_output_are_zero_on_the_given_stream():
+    """While the current stream is busy, a consumer on the given stream sees
+    the zeros of dw_pre and dbias_pre."""
+    x, b, w = small_join()
+    side = torch.cuda.Stream()
+    how = dict(w_post=w, bias_post=w, w_pre=w, bias_pre=w, kind="layer")
+    _, _, stats = Z.zero_block_join(x, b, want_stats=True, **how)
+    d_o = torch.ones_like(x)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        dirty = torch.full((64, 1024), 5.0, device="cuda", dtype=torch.bfloat16)
+        del dirty
+        busy(torch.cuda.current_stream())
+        g = Z.zero_block_join_backward(x, b, d_o, None, stats, stream=side, **how)
+        with torch.cuda.stream(side):
+            seen = g["dw_pre"].clone(), g["dbias_pre"].clone()
+        side.synchronize()
+        assert not seen[0].any() and not seen[1].any()
+        torch.cuda.synchronize()
+
+
+def test_calls_on_a_given_stream_leave_freed_memory_of_the_current_one_alone():
+    """Memory freed on the current stream may still be read by its queued
+    work; a call on another stream does not get it."""
+    x, b, w = small_join()
+    ids = torch.randint(0, 8, (3000, 2), device="cuda", dtype=torch.int32)
+    weights = torch.rand(3000, 2, device="cuda")
+    order = Z.zero_expert_sort(ids, 8)
+    ys = Z.zero_expert_dispatch(x, order)
+    _, _, stats = Z.zero_block_join(x, b, w_post=w, w_pre=w, want_stats=True)
+    side = torch.cuda.Stream()
+    grads = [torch.ones(100_000, device="cuda")]
+    torch.cuda.synchronize()
+    calls = [
+        lambda: Z.zero_block_join(x, b, w_post=w, w_pre=w, want_stats=True, stream=side),
+        lambda: Z.zero_block_join_backward(x, b, x, x, stats, w_post=w, w_pre=w, stream=side).values(),
+        lambda: (Z.zero_expert_dispatch(x, order, stream=side),),
+        lambda: (Z.zero_expert_dispatch_backward(ys, order, stream=side),),
+        lambda: (Z.zero_expert_combine(ys, weights, order, stream=side),),
+        lambda: Z.zero_expert_combine_backward(x, ys, weights, order, stream=side),
+        lambda: vars(Z.zero_expert_sort(ids, 8, stream=side)).values(),
+        lambda: (Z.zero_grad_norm(grads, stream=side),),
+    ]
+    for call in calls:
+        plain = [t for t in call() if isinstance(t, torch.Tensor)]
+        torch.cuda.synchronize()
+        sizes = [(t.shape, t.dtype) for t in plain]
+        want = [t.clone() for t in plain]
+        del plain
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        freed = [torch.full(s, 3, dtype=d, device="cuda") for s, d in sizes]
+        at = {t.untyped_storage().data_ptr() for t in freed}
+        busy(torch.cuda.current_stream())
+        del freed
+        got = [t for t in call() if isinstance(t, torch.Tensor)]
+        assert not at & {t.untyped_storage().data_ptr() for t in got}
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_results_of_a_given_stream_are_held_for_the_caller():
+    """Dropped while the caller's stream still reads it, a result is not
+    handed to the stream that made it."""
+    x, b, w = small_join()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o, _, _ = Z.zero_block_join(x, b, w_post=w, stream=side)
+    at = o.data_ptr()
+    torch.cuda.current_stream().wait_stream(side)
+    busy(torch.cuda.current_stream())
+    copy = o.clone()
+    want_first = o[0].clone()
+    del o
+    for _ in range(3):
+        again, _, _ = Z.zero_block_join(x, b, w_post=w, scale=9.0, stream=side)
+        assert again.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(copy[0], want_first)

@@ -112,3 +112,58 @@ def test_handles_of_the_default_stream_are_recorded_as_that_stream(monkeypatch):
     T._keep_for(given, t)
     T._keep_for(None, t)
     assert t.streams == [default, default, ("external", 64), given] and made == [64]
+
+
+def order_of(tokens, topk, n_experts):
+    i32 = dict(dtype=torch.int32)
+    return T.ExpertOrder(torch.zeros(n_experts + 1, **i32), torch.zeros(tokens, topk, **i32),
+                         torch.zeros(tokens * topk, **i32), n_experts, tokens, topk)
+
+
+def test_calls_on_a_given_stream_make_their_buffers_there(monkeypatch):
+    """Whatever a call allocates or fills, it does with the given stream
+    current; what it returns is recorded for the caller's stream too."""
+    class Made(FakeTensor):
+        def __init__(self):
+            super().__init__()
+            self.made_on = current[-1]
+
+    caller, side = FakeStream(7), FakeStream(9)
+    current = [caller]
+
+    class Use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *error):
+            current.pop()
+
+    def make(n):
+        return lambda *a: tuple(Made() for _ in range(n)) if n > 1 else Made()
+
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
+    fast = types.SimpleNamespace(
+        block_join=make(3), block_join_backward=lambda *a: {"dx": Made(), "dw_pre": Made(), "db": None},
+        block_join_workspace_bytes=lambda *a: 64, expert_sort=make(3), expert_dispatch=make(1),
+        expert_dispatch_backward=make(1), expert_combine=make(1), expert_combine_backward=make(2))
+    monkeypatch.setattr(T, "_fast", fast)
+    x, ids, order = torch.ones(4, 8), torch.zeros(4, 2, dtype=torch.int32), order_of(4, 2, 3)
+
+    def outputs(stream):
+        sort = T.zero_expert_sort(ids, 3, stream=stream)
+        grads = T.zero_block_join_backward(x, x, x, None, None, stream=stream)
+        return [*T.zero_block_join(x, x, stream=stream), grads["dx"], grads["dw_pre"],
+                sort.offsets, sort.rows, sort.pairs, T.zero_expert_dispatch(x, order, stream=stream),
+                T.zero_expert_dispatch_backward(x, order, stream=stream),
+                T.zero_expert_combine(x, x, order, stream=stream),
+                *T.zero_expert_combine_backward(x, x, x, order, stream=stream)]
+
+    for t in outputs(side):
+        assert t.made_on is side and caller in t.streams
+    for t in outputs(None):
+        assert t.made_on is caller and t.streams == []
+    assert current == [caller]

@@ -115,13 +115,7 @@ Tensor result(const Tensor& t, const char* what, at::IntArrayRef shape, at::Scal
 
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-// None: the device's current stream; else a stream's handle.
-void* stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-  void* s = PyLong_AsVoidPtr(o);
-  if (!s && PyErr_Occurred()) throw PythonError();
-  return s;
-}
+void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 int64_t number(PyObject* o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw PythonError();
@@ -274,10 +268,10 @@ struct Join {
 };
 
 // x, b, w_post, bias_post, w_pre, bias_pre, gate, kind, scale, eps, o, n,
-// want_o, want_stats, stream -> (o, n, stats)
+// want_o, want_stats -> (o, n, stats)
 PyObject* block_join(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 15);
+    expect_args(n_args, 14);
     Tensor o = maybe(a[10], "o"), n = maybe(a[11], "n"), stats;
     Join j(a, n);
     if (n.defined() && !j.w_pre.defined()) value_error("n", "needs w_pre");
@@ -288,7 +282,7 @@ PyObject* block_join(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       o = Tensor();
     if (j.w_pre.defined()) n = result(n, "n", j.x.sizes(), j.act, j.x);
     if (PyObject_IsTrue(a[13])) stats = at::empty({j.d.rows, 4}, j.x.options().dtype(at::kFloat));
-    void* stream = stream_of(a[14], j.dev);
+    void* stream = stream_of(j.dev);
     unlocked([&] { return zero_block_join(&j.d, &j.in, ptr(o), ptr(n), static_cast<float*>(ptr(stats)), stream); });
     if (!want_o && !j.b.defined()) o = j.x;
     return tuple_of({o, n, stats});
@@ -310,10 +304,10 @@ constexpr int kGrads = 7;
 PyObject* g_names[kGrads];  // "dx", "db", ...
 
 // x, b, w_post, bias_post, w_pre, bias_pre, gate, kind, scale, eps, d_o, d_n,
-// stats, want, workspace, stream -> {"dx": ..., ...}
+// stats, want, workspace -> {"dx": ..., ...}
 PyObject* block_join_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 16);
+    expect_args(n_args, 15);
     const Tensor d_o = maybe(a[10], "d_o"), d_n = maybe(a[11], "d_n"), stats = maybe(a[12], "stats");
     Join j(a, d_n);
     if (d_o.defined()) {
@@ -354,7 +348,7 @@ PyObject* block_join_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) 
         ws = workspace_of(a[14], need, j.x);
       }
       const zero_join_grads g = {at_[0], at_[1], at_[2], at_[3], at_[4], at_[5], at_[6]};
-      void* stream = stream_of(a[15], j.dev);
+      void* stream = stream_of(j.dev);
     unlocked([&] { return zero_block_join_backward(&j.d, &j.in, ptr(d_o), ptr(d_n), static_cast<const float*>(ptr(stats)), &g,
                                      ptr(ws), need, stream); });
     }
@@ -376,10 +370,10 @@ PyObject* block_join_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) 
 // ---------------------------------------------------------------------------
 // expert permutation
 
-// ids, n_experts, workspace, stream -> (offsets, rows, pairs)
+// ids, n_experts, workspace -> (offsets, rows, pairs)
 PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 4);
+    expect_args(n_args, 3);
     const Tensor ids = tensor(a[0], "ids");
     const int dev = device_of(ids, "ids");
     if (ids.dim() != 2 || !ids.is_contiguous()) value_error("ids", "expected a contiguous [tokens, topk] tensor");
@@ -394,7 +388,7 @@ PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const Tensor offsets = at::empty({static_cast<int64_t>(n_experts) + 1}, as), rows = at::empty(ids.sizes(), as),
                  pairs = at::empty({tokens * topk}, as);
     const Tensor ws = need ? workspace_of(a[2], need, ids) : Tensor();
-    void* stream = stream_of(a[3], dev);
+    void* stream = stream_of(dev);
     unlocked([&] { return zero_expert_sort(ptr(ids), static_cast<int32_t>(ids.element_size()), tokens, static_cast<int32_t>(topk),
                            n_experts, static_cast<int32_t*>(ptr(offsets)), static_cast<int32_t*>(ptr(rows)),
                            static_cast<int32_t*>(ptr(pairs)), ptr(ws), need, stream); });
@@ -438,43 +432,43 @@ struct Order {
   }
 };
 
-// x, (order's five), out, stream -> xs
+// x, (order's five), out -> xs
 PyObject* expert_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 8);
+    expect_args(n_args, 7);
     const Tensor x = tensor(a[0], "x");
     const int dev = device_of(x, "x"), type = type_of(x, "x");
     const Order order(a + 1, dev);
     const int64_t stride = order.by_token(x, "x", dev), hidden = x.size(1);
     const Tensor xs = result(maybe(a[6], "out"), "out", {order.tokens * order.topk, hidden}, x.scalar_type(), x);
-    void* stream = stream_of(a[7], dev);
+    void* stream = stream_of(dev);
     unlocked([&] { return zero_expert_dispatch(ptr(x), stride, static_cast<zero_dtype>(type), order.tokens, order.topk, hidden,
                                order.first(), order.n_experts, order.places(), ptr(xs), stream); });
     return wrapped(xs);
   });
 }
 
-// dxs, (order's five), out, stream -> dx
+// dxs, (order's five), out -> dx
 PyObject* expert_dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 8);
+    expect_args(n_args, 7);
     const Tensor dxs = tensor(a[0], "dxs");
     const int dev = device_of(dxs, "dxs"), type = type_of(dxs, "dxs");
     const Order order(a + 1, dev);
     order.sorted(dxs, "dxs");
     const int64_t hidden = dxs.size(1);
     const Tensor dx = result(maybe(a[6], "out"), "out", {order.tokens, hidden}, dxs.scalar_type(), dxs);
-    void* stream = stream_of(a[7], dev);
+    void* stream = stream_of(dev);
     unlocked([&] { return zero_expert_dispatch_backward(ptr(dxs), static_cast<zero_dtype>(type), order.tokens, order.topk, hidden,
                                         order.places(), ptr(dx), stream); });
     return wrapped(dx);
   });
 }
 
-// ys, weights, (order's five), out, stream -> y
+// ys, weights, (order's five), out -> y
 PyObject* expert_combine(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 9);
+    expect_args(n_args, 8);
     const Tensor ys = tensor(a[0], "ys"), weights = tensor(a[1], "weights");
     const int dev = device_of(ys, "ys"), type = type_of(ys, "ys");
     const Order order(a + 2, dev);
@@ -482,17 +476,17 @@ PyObject* expert_combine(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t hidden = ys.size(1);
     const int wtype = order.weights(weights, dev);
     const Tensor y = result(maybe(a[7], "out"), "out", {order.tokens, hidden}, ys.scalar_type(), ys);
-    void* stream = stream_of(a[8], dev);
+    void* stream = stream_of(dev);
     unlocked([&] { return zero_expert_combine(ptr(ys), static_cast<zero_dtype>(type), ptr(weights), static_cast<zero_dtype>(wtype),
                               order.tokens, order.topk, hidden, order.places(), ptr(y), stream); });
     return wrapped(y);
   });
 }
 
-// dy, ys, weights, (order's five), want_weights, stream -> (dys, dweights)
+// dy, ys, weights, (order's five), want_weights -> (dys, dweights)
 PyObject* expert_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 10);
+    expect_args(n_args, 9);
     const Tensor dy = tensor(a[0], "dy"), ys = tensor(a[1], "ys"), weights = tensor(a[2], "weights");
     const int dev = device_of(ys, "ys"), type = type_of(ys, "ys");
     const Order order(a + 3, dev);
@@ -505,7 +499,7 @@ PyObject* expert_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n_ar
     const int wtype = order.weights(weights, dev);
     const Tensor dys = at::empty(ys.sizes(), ys.options());
     const Tensor dw = PyObject_IsTrue(a[8]) ? at::empty(weights.sizes(), weights.options()) : Tensor();
-    void* stream = stream_of(a[9], dev);
+    void* stream = stream_of(dev);
     unlocked([&] { return zero_expert_combine_backward(ptr(dy), stride, ptr(ys), static_cast<zero_dtype>(type), ptr(weights),
                                        static_cast<zero_dtype>(wtype), order.tokens, order.topk, hidden,
                                        order.first(), order.n_experts, order.places(), ptr(dys), ptr(dw),

@@ -4,7 +4,8 @@ and clipping over many tensors, the block join, the expert permutation.
 The ``zero_*`` functions bind the C calls of include/zero.h under their own
 names (argument checks and marshalling only, those of the join and the experts
 compiled, csrc/train_ops_binding.cpp; the current CUDA stream unless
-``stream`` is given; no fallback).  ``GradNorm`` and ``ClipGradNorm`` are the
+``stream`` is given, which then makes the call's buffers too; inputs are the
+caller's to order; no fallback).  ``GradNorm`` and ``ClipGradNorm`` are the
 prepared forms for gradients whose buffers stay in place from step to step.
 ``block_join``, ``expert_dispatch`` and ``expert_combine`` are the same calls
 with autograd.
@@ -69,10 +70,6 @@ def _load_fast():
     return _fast
 
 
-def _handle(stream) -> int:
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
 def _stream(stream, device: int):
     """Handle of the given stream, or of the device's current one."""
     return _raw_stream(device) if stream is None else _zero._stream(stream)
@@ -116,6 +113,22 @@ def _keep_for(stream, *tensors):
     for t in tensors:
         if t is not None:
             t.record_stream(s)
+
+
+def _run_on(stream, call):
+    """call() with `stream` as the current one (None: as it is).  What the call
+    allocates then belongs to that stream, whose earlier work is done with the
+    memory, and what it fills is filled there; the results, which the caller's
+    stream goes on to use, are held for both."""
+    if stream is None:
+        return call()
+    stream, caller = _torch_stream(stream), torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        got = call()
+    made = got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,)
+    for s in (stream, caller):
+        _keep_for(s, *made)
+    return got
 
 
 # ----------------------------------------------------------------------------
@@ -298,12 +311,12 @@ class ClipGradNorm(GradNorm):
 
 def zero_grad_norm(grads, kind: str = "l2", stream=None):
     """Norm of all gradients as one vector (see zero.h); a float32 tensor."""
-    return GradNorm(grads, kind)(stream)
+    return _run_on(stream, lambda: GradNorm(grads, kind)())
 
 
 def zero_clip_grad_norm(grads, max_norm: float, kind: str = "l2", out=None, stream=None):
     """Norm and clipping (see zero.h); returns the norm before clipping."""
-    return ClipGradNorm(grads, max_norm, kind, out)(stream)
+    return _run_on(stream, lambda: ClipGradNorm(grads, max_norm, kind, out)())
 
 
 # ----------------------------------------------------------------------------
@@ -338,12 +351,12 @@ def zero_block_join(x, b=None, *, w_post=None, bias_post=None, w_pre=None, bias_
     without w_pre no n (None); b None takes the norm of x alone, and o is x.
     x, b, gate: [..., hidden]; the gate also [hidden] or [..., 1].  stats is
     what the backward call takes (None unless want_stats)."""
-    got = (_fast or _load_fast()).block_join(x, b, w_post, bias_post, w_pre, bias_pre, gate, kind,
-                                             scale, eps, o, n, want_o, want_stats,
-                                             None if stream is None else _handle(stream))
     if stream is not None:
-        _keep_for(stream, *got)
-    return got
+        return _run_on(stream, lambda: zero_block_join(
+            x, b, w_post=w_post, bias_post=bias_post, w_pre=w_pre, bias_pre=bias_pre, gate=gate,
+            kind=kind, scale=scale, eps=eps, o=o, n=n, want_o=want_o, want_stats=want_stats))
+    return (_fast or _load_fast()).block_join(x, b, w_post, bias_post, w_pre, bias_pre, gate, kind,
+                                              scale, eps, o, n, want_o, want_stats)
 
 
 def zero_block_join_workspace_bytes(x, b=None, *, w_post=None, bias_post=None, w_pre=None,
@@ -362,20 +375,9 @@ def zero_block_join_backward(x, b, d_o, d_n, stats, *, w_post=None, bias_post=No
     dbias_post, dw_pre and dbias_pre, None for what has no input or is not in
     `want` (a set of those names; None: all).  workspace: device scratch of
     zero_block_join_workspace_bytes (None: allocated here)."""
-    if stream is None:
-        return (_fast or _load_fast()).block_join_backward(
-            x, b, w_post, bias_post, w_pre, bias_pre, gate, kind, scale, eps, d_o, d_n, stats,
-            want, workspace, None)
-    own = workspace is None
-    if own:
-        workspace = torch.empty(zero_block_join_workspace_bytes(
-            x, b, w_post=w_post, bias_post=bias_post, w_pre=w_pre, bias_pre=bias_pre, gate=gate,
-            kind=kind, scale=scale, eps=eps), dtype=torch.uint8, device=x.device)
-    got = (_fast or _load_fast()).block_join_backward(
+    return _run_on(stream, lambda: (_fast or _load_fast()).block_join_backward(
         x, b, w_post, bias_post, w_pre, bias_pre, gate, kind, scale, eps, d_o, d_n, stats, want,
-        workspace, _handle(stream))
-    _keep_for(stream, *got.values(), workspace if own else None)
-    return got
+        workspace))
 
 
 def _even_rows(t):
@@ -447,58 +449,36 @@ def zero_expert_sort(ids, n_experts: int, workspace=None, stream=None) -> Expert
     [tokens, topk] int32 or int64; a choice outside [0, n_experts) is
     dropped.  workspace: device scratch of zero_expert_sort_workspace_bytes
     (None: allocated here)."""
-    if stream is not None and workspace is None and isinstance(ids, torch.Tensor) and ids.dim() == 2:
-        need = zero_expert_sort_workspace_bytes(*ids.shape, n_experts) if ids.shape[1] else 0
-        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=ids.device)
-        _keep_for(stream, workspace if ids.is_cuda else None)
-    got = (_fast or _load_fast()).expert_sort(ids, n_experts, workspace,
-                                              None if stream is None else _handle(stream))
-    if stream is not None:
-        _keep_for(stream, *got)
+    got = _run_on(stream, lambda: (_fast or _load_fast()).expert_sort(ids, n_experts, workspace))
     return ExpertOrder(*got, n_experts, ids.shape[0], ids.shape[1])
 
 
 def zero_expert_dispatch(x, order: ExpertOrder, out=None, stream=None):
     """Tokens copied to their rows in expert order, [tokens * topk, hidden];
     the rows past the last kept choice are zero."""
-    xs = (_fast or _load_fast()).expert_dispatch(x, order.offsets, order.rows, order.n_experts,
-                                                 order.tokens, order.topk, out,
-                                                 None if stream is None else _handle(stream))
-    if stream is not None:
-        _keep_for(stream, xs)
-    return xs
+    return _run_on(stream, lambda: (_fast or _load_fast()).expert_dispatch(
+        x, order.offsets, order.rows, order.n_experts, order.tokens, order.topk, out))
 
 
 def zero_expert_dispatch_backward(dxs, order: ExpertOrder, out=None, stream=None):
     """Each token's gradient: the sum of its rows'."""
-    dx = (_fast or _load_fast()).expert_dispatch_backward(
-        dxs, order.offsets, order.rows, order.n_experts, order.tokens, order.topk, out,
-        None if stream is None else _handle(stream))
-    if stream is not None:
-        _keep_for(stream, dx)
-    return dx
+    return _run_on(stream, lambda: (_fast or _load_fast()).expert_dispatch_backward(
+        dxs, order.offsets, order.rows, order.n_experts, order.tokens, order.topk, out))
 
 
 def zero_expert_combine(ys, weights, order: ExpertOrder, out=None, stream=None):
     """Each token's weighted sum of its rows; zero when all its choices were
     dropped."""
-    y = (_fast or _load_fast()).expert_combine(ys, weights, order.offsets, order.rows,
-                                               order.n_experts, order.tokens, order.topk, out,
-                                               None if stream is None else _handle(stream))
-    if stream is not None:
-        _keep_for(stream, y)
-    return y
+    return _run_on(stream, lambda: (_fast or _load_fast()).expert_combine(
+        ys, weights, order.offsets, order.rows, order.n_experts, order.tokens, order.topk, out))
 
 
 def zero_expert_combine_backward(dy, ys, weights, order: ExpertOrder, want_weights: bool = True,
                                  stream=None):
     """(dys, dweights) of zero_expert_combine; dweights None unless wanted."""
-    got = (_fast or _load_fast()).expert_combine_backward(
+    return _run_on(stream, lambda: (_fast or _load_fast()).expert_combine_backward(
         dy, ys, weights, order.offsets, order.rows, order.n_experts, order.tokens, order.topk,
-        want_weights, None if stream is None else _handle(stream))
-    if stream is not None:
-        _keep_for(stream, *got)
-    return got
+        want_weights))
 
 
 class _ExpertDispatch(torch.autograd.Function):
