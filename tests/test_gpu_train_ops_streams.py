@@ -10,7 +10,7 @@ import zero_sharded_optimizer_flatten_gb300 as Z
 
 pytestmark = pytest.mark.gpu
 
-BUSY = 100_000_000   # cycles a stream is kept busy: some 50 ms
+BUSY = 200_000_000   # cycles a stream is kept busy: some 100 ms
 
 
 @pytest.fixture(autouse=True)
@@ -37,8 +37,10 @@ def test_prepared_norm_dropped_right_after_its_call(given):
     want = math.sqrt(4 * 300_000 + 77)
     size = Z.zero_grad_norm_workspace_bytes(grads)
     side = torch.cuda.Stream()
-    torch.cuda.synchronize()
     for make in (lambda: Z.GradNorm(grads), lambda: Z.ClipGradNorm(grads, 1e9)):
+        make()(stream=side)   # the kernels' first use takes its time
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
         call = make()
         at = call._workspace.data_ptr()
         busy(side)
@@ -51,7 +53,7 @@ def test_prepared_norm_dropped_right_after_its_call(given):
         held = []
         for _ in range(4):
             held.append(torch.full((size,), 255, dtype=torch.uint8, device="cuda"))
-            assert held[-1].data_ptr() != at
+            assert held[-1].data_ptr() != at or side.query()
         side.synchronize()
         assert abs(float(norm) - want) <= 1e-5 * want
 
@@ -142,3 +144,51 @@ def test_results_of_a_given_stream_are_held_for_the_caller():
         assert again.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(copy[0], want_first)
+
+
+def test_prepared_norm_on_another_stream_waits_for_its_memory():
+    """The workspace takes over memory that queued work still reads: the call
+    on another stream runs after it."""
+    grads = [torch.full((300_000,), 2.0, device="cuda")]
+    size = Z.zero_grad_norm_workspace_bytes(grads)
+    side = torch.cuda.Stream()
+    Z.GradNorm(grads)(stream=side)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.full((size + 1024,), 3, dtype=torch.uint8, device="cuda")
+    at = before.data_ptr()
+    copy = torch.empty_like(before)
+    torch.cuda.synchronize()
+    busy(torch.cuda.current_stream())
+    copy.copy_(before)
+    del before
+    call = Z.GradNorm(grads)
+    assert at <= call._workspace.data_ptr() < at + 1024
+    norm = call(stream=side)
+    side.synchronize()
+    assert abs(float(norm) - math.sqrt(4 * 300_000)) <= 1e-2
+    assert bool((copy == 3).all())
+
+
+def test_prepared_clip_captured_and_called_elsewhere():
+    """One object: called, captured on the capture's stream, replayed, called
+    on a third stream; and one prepared inside the capture."""
+    g = [torch.full((5000,), 2.0, device="cuda")]
+    call = Z.ClipGradNorm(g, 1.0)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        inside = Z.GradNorm(g)
+        inside()
+    g[0].fill_(3.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert abs(float(call._norm) - 3 * math.sqrt(5000)) <= 1e-3
+    assert abs(float(inside._norm) - 1.0) <= 1e-4
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    norm = inside(stream=side)
+    side.synchronize()
+    assert abs(float(norm) - 1.0) <= 1e-4

@@ -1,6 +1,7 @@
 """Host side of the prepared norm calls and of calls on a given stream (no GPU
 needed): the device, the streams and the library are stand-ins that record
 what they are told."""
+import contextlib
 import types
 
 import pytest
@@ -45,6 +46,8 @@ def cpu_calls(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: seen.streams[seen.current])
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: seen.capturing)
     monkeypatch.setattr(torch.cuda, "Event", lambda: types.SimpleNamespace(record=lambda *a: None))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: seen.streams[handle])
     return seen
 
 
@@ -167,3 +170,36 @@ def test_calls_on_a_given_stream_make_their_buffers_there(monkeypatch):
     for t in outputs(None):
         assert t.made_on is caller and t.streams == []
     assert current == [caller]
+
+
+@pytest.mark.parametrize("kind", ["norm", "clip"])
+def test_first_call_on_another_stream_waits_for_the_buffers(cpu_calls, kind, monkeypatch):
+    """The memory of the buffers may have queued work of the stream it came
+    from; another stream waits for that once, but not while it is captured
+    (capture begins with the device idle, and may not wait on outside work)."""
+    marks = []
+    monkeypatch.setattr(torch.cuda, "Event", lambda: types.SimpleNamespace(
+        record=lambda *a: marks.append(cpu_calls.current)))
+    side = cpu_calls.streams[9]
+    call = prepared(kind)
+    assert marks == [7]
+    call()
+    assert not cpu_calls.streams[7].waited
+    cpu_calls.capturing = True
+    call(side)
+    assert side.waited == []
+    cpu_calls.capturing = False
+    for _ in range(3):
+        call(side)
+    assert len(side.waited) == 1
+    cpu_calls.current = 9
+    call()
+    assert len(side.waited) == 1 and not cpu_calls.streams[7].waited
+
+
+def test_a_call_prepared_inside_a_capture_waits_for_nothing(cpu_calls):
+    cpu_calls.capturing = True
+    call = prepared("norm")
+    cpu_calls.capturing = False
+    call(cpu_calls.streams[9])
+    assert cpu_calls.streams[9].waited == [] and cpu_calls.calls[-1][-1] == 9

@@ -215,7 +215,13 @@ class GradNorm:
     workspace: device scratch of zero_grad_norm_workspace_bytes (None: its
     own)."""
 
+    _ready = None
+
     def __init__(self, grads, kind: str = "l2", workspace=None):
+        self._fill(grads, kind, workspace)
+        self._mark()
+
+    def _fill(self, grads, kind="l2", workspace=None):
         self._prepare([g for g in grads if g is not None], None, kind, workspace)
 
     def _prepare(self, grads, out, kind, workspace):
@@ -262,17 +268,33 @@ class GradNorm:
         self.device = device
         self._home = _raw_stream(device)  # the stream that the buffers were allocated on
 
+    def _mark(self):
+        """Notes the own stream's work so far, which may have used the buffers'
+        memory before (nothing to wait for when they come from a capture)."""
+        self._joined = set()
+        if not torch.cuda.is_current_stream_capturing():
+            self._ready = torch.cuda.Event()
+            self._ready.record()
+
     def _on_stream(self, stream):
         """Handle of the stream that a call runs on; launches go to the current
-        device.  The object may be gone before that stream has done the call's
-        work, so another stream than the buffers' own is recorded on them."""
+        device.  Another stream than the buffers' own first waits for what used
+        their memory before (not when it is captured: that begins with the
+        device idle).  The object may be gone before the stream has done the
+        call's work, so it is recorded on them."""
         if _device() != self.device:
             raise ValueError(f"prepared on cuda:{self.device}, but the current device is "
                              f"cuda:{_device()}")
         handle = _stream(stream, self.device)
         if handle != self._home:
-            _keep_for(torch.cuda.current_stream(self.device) if stream is None else stream,
-                      self.result, self._workspace)
+            other = torch.cuda.current_stream() if stream is None else _torch_stream(stream)
+            if self._ready is not None and handle not in self._joined:
+                with torch.cuda.stream(other):
+                    captured = torch.cuda.is_current_stream_capturing()
+                if not captured:
+                    other.wait_event(self._ready)
+                    self._joined.add(handle)
+            _keep_for(other, self.result, self._workspace)
         return handle
 
     def __call__(self, stream=None):
@@ -291,6 +313,10 @@ class ClipGradNorm(GradNorm):
     that fp32 gradients go to.  `max_norm` may be changed between calls."""
 
     def __init__(self, grads, max_norm: float, kind: str = "l2", out=None, workspace=None):
+        self._fill(grads, max_norm, kind, out, workspace)
+        self._mark()
+
+    def _fill(self, grads, max_norm, kind="l2", out=None, workspace=None):
         grads = list(grads)
         self.max_norm = float(max_norm)
         if out is None:
@@ -309,14 +335,21 @@ class ClipGradNorm(GradNorm):
         return self._norm
 
 
+def _once(cls, *args):
+    """A call of a list that is used once, on the stream that it is made on."""
+    call = cls.__new__(cls)
+    call._fill(*args)
+    return call()
+
+
 def zero_grad_norm(grads, kind: str = "l2", stream=None):
     """Norm of all gradients as one vector (see zero.h); a float32 tensor."""
-    return _run_on(stream, lambda: GradNorm(grads, kind)())
+    return _run_on(stream, lambda: _once(GradNorm, grads, kind))
 
 
 def zero_clip_grad_norm(grads, max_norm: float, kind: str = "l2", out=None, stream=None):
     """Norm and clipping (see zero.h); returns the norm before clipping."""
-    return _run_on(stream, lambda: ClipGradNorm(grads, max_norm, kind, out)())
+    return _run_on(stream, lambda: _once(ClipGradNorm, grads, max_norm, kind, out))
 
 
 # ----------------------------------------------------------------------------
