@@ -553,6 +553,11 @@ extern "C" zero_status zero_block_join_backward(const zero_join_desc* desc, cons
   int workers = 0;
   if (rows) JOIN_TRY(launched(fn, launch_join(a, true, &workers, s)));
   if (a.n_sums > 0) {
+    if (!rows) {  // zeros, whatever the parameters and the gate hold (they may be NULL)
+      a.in = {};
+      a.d.gate_kind = ZERO_GATE_NONE;
+      a.scale = 1.f;
+    }
     JoinSumArgs g = {a, workers, grads->dw_pre, grads->dbias_pre, grads->dw_post, grads->dbias_post, dgate};
     void* args[] = {&g};
     const int e = static_cast<int>(
