@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "zero_capi_util.h"
+#include "zero_pieces.h"
 #include "zero_rows.cuh"
 
 namespace cg = cooperative_groups;
@@ -306,7 +307,7 @@ struct Window {
     const int s = shift(p);
     const char* at = reinterpret_cast<const char*>(p) - s;
     a = *reinterpret_cast<const uint4*>(at);
-    b = *reinterpret_cast<const uint4*>(at + (s ? 16 : 0));
+    b = *reinterpret_cast<const uint4*>(at + window_second(s));
   }
   __device__ __forceinline__ Piece<T> shifted(int s) const {
     uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -321,28 +322,19 @@ struct Window {
   }
 };
 
-// How a row that is written falls into 16-byte pieces: `head` single columns,
-// `pieces`, and single columns again, `ends` of them in all.  A window reaches
-// less than 16 bytes past its columns on either side: into the row before or
-// after, but out of the storage from the first piece of its first row and the
-// last of its last.  Where such a row is read, `inner` makes single columns of
-// these two.
+// A row of T's.  A window reaches less than 16 bytes past its columns on
+// either side: into the row before or after, but out of the storage from the
+// first piece of its first row and the last of its last, which become single
+// columns.  Of the rows in expert order the last kept one may end the storage
+// and is not known to the combination: there no window passes its row's end.
 template <class T>
-struct Frame {
-  int head, pieces, ends;
-  __device__ __forceinline__ Frame(const T* row, int hidden, bool inner) {
-    constexpr int P = Piece<T>::kCols;
-    head = min(hidden, static_cast<int>(-reinterpret_cast<uintptr_t>(row) & 15) / static_cast<int>(sizeof(T)));
-    pieces = (hidden - head) / P;
-    if (inner) {
-      head += min(pieces, 1) * P;
-      pieces = max(pieces - 2, 0);
-    }
-    ends = hidden - pieces * P;
-  }
-  __device__ __forceinline__ int column(int piece) const { return head + piece * Piece<T>::kCols; }
-  __device__ __forceinline__ int end_column(int e) const { return e < head ? e : e + pieces * Piece<T>::kCols; }
+struct Frame : RowPieces {
+  __device__ __forceinline__ Frame(const T* row, int hidden, bool drop_first, bool drop_last)
+      : RowPieces(reinterpret_cast<uintptr_t>(row), hidden, static_cast<int>(sizeof(T)), drop_first, drop_last) {}
 };
+__device__ __forceinline__ uint32_t low_bits(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+}
 
 // The group's token, and the thread's first column and a round's columns
 // where rows are taken octet by octet.
@@ -370,7 +362,7 @@ __device__ __forceinline__ void clear_past_end(const RowArgs& a, const Place& me
     if constexpr (VEC) {
       for (int c = me.first; c < H; c += me.round) Elem<T>::store8(row + c, z);
     } else {
-      const Frame<T> f(row, H, false);
+      const Frame<T> f(row, H, false, false);
       for (int u = me.lane; u < f.pieces; u += me.lanes)
         *reinterpret_cast<uint4*>(row + f.column(u)) = make_uint4(0, 0, 0, 0);
       for (int e = me.lane; e < f.ends; e += me.lanes) row[f.end_column(e)] = Elem<T>::narrow(0.f);
@@ -566,7 +558,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_dispatch_any(const RowArgs a
     const int64_t r = __ldg(a.rows + p0 + k);
     if (r < 0) continue;
     T* row = xs + r * H;
-    const Frame<T> f(row, H, inner);
+    const Frame<T> f(row, H, inner, inner);
     const int shift = Window<T>::shift(x + f.head);
     T end;
     if (me.lane < f.ends) end = x[f.end_column(me.lane)];
@@ -591,12 +583,16 @@ __global__ void __launch_bounds__(kRowThreads, K == 1 ? 6 : 5) k_combine_any(con
   const int H = static_cast<int>(a.hidden);
   const T* in = static_cast<const T*>(a.in);
   T* y = static_cast<T*>(a.out) + me.token * H;
-  const int64_t last = a.tokens * a.topk - 1;
   const Choices<K> ch(a, me.token * a.topk, 0, true);
-  bool inner = false;
+  const uint32_t row_bytes = static_cast<uint32_t>(H * sizeof(T));
+  const uint32_t y_end = low_bits(y) + row_bytes, in_end = low_bits(in) + row_bytes;
+  bool first = false, passes = false;
 #pragma unroll
-  for (int i = 0; i < K; ++i) inner |= ch.row[i] == 0 || ch.row[i] == last;
-  const Frame<T> f(y, H, inner);
+  for (int i = 0; i < K; ++i) {
+    first |= ch.row[i] == 0;
+    passes |= ch.row[i] >= 0 && window_passes(in_end + ch.row[i] * row_bytes, y_end);
+  }
+  const Frame<T> f(y, H, first, passes);
   T end[K];
   if (me.lane < f.ends)
 #pragma unroll
@@ -686,7 +682,6 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward_any(const RowA
   const int H = static_cast<int>(a.hidden);
   const T* dy = static_cast<const T*>(a.in) + (live ? me.token : 0) * a.stride;
   const T* ys = static_cast<const T*>(a.ys);
-  const int64_t last = a.tokens * a.topk - 1;
   T* dys = static_cast<T*>(a.out);
   const int64_t p0 = (live ? me.token : 0) * a.topk;
   int flip = 0;
@@ -697,8 +692,8 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward_any(const RowA
     for (int i = 0; i < K; ++i) {
       if (ch.row[i] < 0) continue;
       const int64_t at = ch.row[i] * static_cast<int64_t>(H);
-      const Frame<T> f(dys + at, H,
-                       me.token == 0 || me.token == a.tokens - 1 || ch.row[i] == 0 || ch.row[i] == last);
+      const Frame<T> f(dys + at, H, me.token == 0 || ch.row[i] == 0,
+                       me.token == a.tokens - 1 || window_passes(low_bits(ys + at + H), low_bits(dys + at + H)));
       const int g_shift = Window<T>::shift(dy + f.head), v_shift = Window<T>::shift(ys + at + f.head);
       for (int u = me.lane; u < f.pieces; u += kParts * me.lanes) {
         Window<T> g[kParts], v[kParts];
