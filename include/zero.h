@@ -637,7 +637,8 @@ zero_status zero_clip_grad_norm(const zero_grad_tensor* tensors, int32_t n_tenso
  * ZERO_JOIN_RMS has no mean and no bias.  Statistics, products and sums are
  * binary32; o and n are rounded once.  With b NULL, o = x: the norm alone.
  * Pointers need their element's alignment only; rows of 16-byte multiples on
- * 16-byte boundaries take the wide path.
+ * 16-byte boundaries take the wide path.  Outputs overlap no input and no
+ * other output but for the forms named below.
  */
 typedef enum { ZERO_JOIN_RMS = 0, ZERO_JOIN_LAYER = 1 } zero_join_kind;
 typedef enum {
@@ -674,9 +675,9 @@ typedef struct {
 } zero_join_grads;
 
 /* o (res_dtype) and n (act_dtype, needs w_pre): [rows, hidden], one of them
- * may be NULL.  o may be x and n may be b when nothing is kept for a backward
- * pass.  stats (nullable, 16-byte aligned): float[rows][4], which the
- * backward pass takes.  rows == 0 does nothing. */
+ * may be NULL.  o may be x and n may be b, each with contiguous rows, when
+ * nothing is kept for a backward pass.  stats (nullable, 16-byte aligned):
+ * float[rows][4], which the backward pass takes.  rows == 0 does nothing. */
 zero_status zero_block_join(const zero_join_desc* desc, const zero_join_inputs* inputs, void* o,
                             void* n, float* stats, void* stream);
 
@@ -685,9 +686,10 @@ zero_status zero_block_join_workspace_bytes(const zero_join_desc* desc, int64_t*
 
 /* The gradients of the same inputs from d_o and d_n (either may be NULL: no
  * gradient comes that way) and the forward call's stats.  x and b still hold
- * what the forward call read.  The parameters' gradients are summed over the
- * rows in a fixed order; with rows == 0 they are zero.  The workspace is
- * needed when any of them, or a channel gate's, is wanted. */
+ * what the forward call read.  dx may be d_o and db may be d_n, each with
+ * contiguous rows.  The parameters' gradients are summed over the rows in a
+ * fixed order; with rows == 0 they are zero.  The workspace is needed when any
+ * of them, or a channel gate's, is wanted. */
 zero_status zero_block_join_backward(const zero_join_desc* desc, const zero_join_inputs* inputs,
                                      const void* d_o, const void* d_n, const float* stats,
                                      const zero_join_grads* grads, void* workspace,
@@ -705,8 +707,9 @@ zero_status zero_block_join_backward(const zero_join_desc* desc, const zero_join
  *   pairs[i]   = the pair of row i, -1 for i >= M
  * ids: int32 (id_bytes 4) or int64 (8).  n_experts at most 4096, tokens*topk
  * below 2^31.  The order is stable.  workspace: 4-byte aligned device scratch
- * (NULL when zero_expert_sort_workspace_bytes says 0).  Nothing is read back
- * by the host.
+ * (NULL when zero_expert_sort_workspace_bytes says 0).  Outputs of this call
+ * and the next four overlap no input and no other output.  Nothing is read
+ * back by the host.
  */
 zero_status zero_expert_sort(const void* ids, int32_t id_bytes, int64_t tokens, int32_t topk,
                              int32_t n_experts, int32_t* offsets, int32_t* rows, int32_t* pairs,

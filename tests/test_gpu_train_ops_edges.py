@@ -58,3 +58,76 @@ def test_no_rows_need_no_inputs():
                                         ctypes.byref(g), ws.data_ptr(), need.value, None) == 0
     torch.cuda.synchronize()
     assert not out.any()
+
+
+def join_case(R, H, act, res, par, gate, post, pre, layer, seed=1, pad=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def t(*shape, dtype, scale, shift=0.0):
+        wide = torch.randn(*shape[:-1], shape[-1] + (pad if len(shape) == 2 and shape[1] > 1 else 0),
+                           device="cuda", generator=g)
+        return (wide * scale + shift).to(dtype)[..., :shape[-1]]
+
+    shape = {"none": None, "channel": (H,), "row": (R, 1), "full": (R, H)}[gate]
+    params = dict(gate=None if shape is None else t(*shape, dtype=act, scale=0.3, shift=0.5))
+    for k, there in (("w_post", post), ("w_pre", pre), ("bias_post", post and layer),
+                     ("bias_pre", pre and layer)):
+        params[k] = t(H, dtype=par, scale=0.1, shift=float(k[0] == "w")) if there else None
+    return t(R, H, dtype=res, scale=2.0), t(R, H, dtype=act, scale=0.5, shift=0.1), params
+
+
+def c_backward(x, b, d_o, d_n, stats, dx, db, kind, **params):
+    """zero_block_join_backward with the caller's own dx and db."""
+    code = {H16: 0, B16: 1, F32: 2}
+    R, H = x.shape
+    first = next((t for k, t in params.items() if k != "gate" and t is not None), None)
+    gate = params["gate"]
+    kinds = {None: 0, (H,): 1, (R, 1): 2, (R, H): 3}
+    d = T.JoinDescC(rows=R, hidden=H, act_dtype=code[b.dtype], res_dtype=code[x.dtype],
+                    param_dtype=code[b.dtype if first is None else first.dtype],
+                    gate_dtype=code[b.dtype if gate is None else gate.dtype],
+                    kind=int(kind == "layer"), gate_kind=kinds[None if gate is None else tuple(gate.shape)],
+                    eps=1e-6, scale=0.7, x_stride=H, b_stride=H,
+                    gate_stride=1 if gate is not None and gate.shape[-1] == 1 else H, do_stride=H,
+                    dn_stride=H)
+    p = T.JoinInputsC(x=x.data_ptr(), b=b.data_ptr(),
+                      **{k: None if t is None else t.data_ptr() for k, t in params.items()})
+    g = T.JoinGradsC(dx=dx.data_ptr(), db=db.data_ptr())
+    return Z.lib().zero_block_join_backward(
+        ctypes.byref(d), ctypes.byref(p), d_o.data_ptr(), d_n.data_ptr(), stats.data_ptr(),
+        ctypes.byref(g), None, 0, torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("gate", ["channel", "row", "full"])
+@pytest.mark.parametrize("act,res", [(B16, B16), (H16, F32), (F32, F32)], ids=lambda t: str(t)[6:])
+def test_join_gradients_in_place(act, res, kind, gate):
+    """dx over d_o and db over d_n, in every kernel: short rows, several warps,
+    rows that start anywhere, rows above 8192."""
+    for R, H in ((700, 96), (300, 1024), (200, 333), (40, 4096), (30, 8200), (9, 8203)):
+        x, b, params = join_case(R, H, act, res, act, gate, True, True, kind == "layer")
+        d_o, d_n = torch.randn_like(x), torch.randn_like(b)
+        _, _, stats = Z.zero_block_join(x, b, want_stats=True, kind=kind, scale=0.7, **params)
+        want = Z.zero_block_join_backward(x, b, d_o, d_n, stats, kind=kind, scale=0.7, want={"dx", "db"},
+                                          **params)
+        dx, db = d_o.clone(), d_n.clone()
+        assert c_backward(x, b, dx, db, stats, dx, db, kind, **params) == 0, Z.zero_last_error()
+        assert torch.equal(dx, want["dx"]) and torch.equal(db, want["db"]), (R, H)
+
+
+def test_outputs_between_the_rows_of_an_input():
+    """Memory between an input's rows is no part of it."""
+    big = torch.randn(2, 40, 64, device="cuda").bfloat16()
+    x, room = big[:, 0], big[0, 10:12]      # rows 0 and 40 of 64; o lies in rows 10 and 11
+    b, w = torch.randn_like(room), torch.ones(64, device="cuda", dtype=B16)
+    want, n, _ = Z.zero_block_join(x.contiguous(), b, w_pre=w)
+    got = Z.zero_block_join(x, b, w_pre=w, o=room)
+    assert torch.equal(got[0], want) and torch.equal(got[1], n) and torch.equal(room, want)
+    ids = torch.tensor([[0], [1]], device="cuda", dtype=torch.int32)
+    order = Z.zero_expert_sort(ids, 2)
+    xs = Z.zero_expert_dispatch(x, order, out=big[0, 20:22])
+    assert torch.equal(xs, x)
+    with pytest.raises(Z.ZeroError, match="xs overlaps x"):
+        Z.zero_expert_dispatch(x, order, out=big.view(-1, 64)[39:41])
+    with pytest.raises(Z.ZeroError, match="o overlaps x"):
+        Z.zero_block_join(x, b, w_pre=w, o=big.view(-1, 64)[40:42])

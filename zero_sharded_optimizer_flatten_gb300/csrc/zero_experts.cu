@@ -827,6 +827,19 @@ zero_status check_weights(const char* fn, zero_dtype dtype, zero_dtype weight_dt
   return ZERO_OK;
 }
 
+// [tokens, hidden] by a stride, [tokens, topk], [n_experts + 1].
+Extent token_rows(const char* name, const RowArgs& a, int64_t stride, const void* p, int type) {
+  return {name, p, a.tokens, stride * type_bytes(type), a.hidden * type_bytes(type)};
+}
+Extent choices(const char* name, const RowArgs& a, const void* p, int bytes) {
+  return Extent::block(name, p, a.tokens * a.topk * bytes);
+}
+// Rows in expert order: the last kept one, known on the device, may be the
+// last that exists, so only the first is looked at.
+Extent sorted_rows(const char* name, const RowArgs& a, const void* p, int type) {
+  return Extent::block(name, p, a.hidden * type_bytes(type));
+}
+
 #define EXPERT_TRY(x)               \
   do {                              \
     const zero_status st_ = (x);    \
@@ -871,6 +884,12 @@ extern "C" zero_status zero_expert_sort(const void* ids, int32_t id_bytes, int64
       return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes,
                   need);
   }
+  const int64_t n = tokens * topk;
+  EXPERT_TRY(check_overlaps(fn,
+                            {Extent::block("offsets", offsets, (n_experts + INT64_C(1)) * 4),
+                             Extent::block("rows", rows, n * 4), Extent::block("pairs", pairs, n * 4),
+                             Extent::block("workspace", need ? workspace : nullptr, need)},
+                            {Extent::block("ids", ids, n * id_bytes)}));
   const cudaError_t pending = cudaGetLastError();
   if (pending != cudaSuccess)
     return fail(ZERO_ERR_CUDA, "%s: pending CUDA error: %s", fn, cudaGetErrorString(pending));
@@ -930,6 +949,9 @@ extern "C" zero_status zero_expert_dispatch(const void* x, int64_t x_stride, zer
   RowArgs a = {};
   a.in = x, a.out = xs, a.rows = rows, a.total = offsets + n_experts;
   a.tokens = tokens, a.hidden = hidden, a.stride = x_stride, a.topk = topk;
+  EXPERT_TRY(check_overlaps(fn, {Extent::block("xs", xs, tokens * topk * hidden * type_bytes(dtype))},
+                            {token_rows("x", a, x_stride, x, dtype), choices("rows", a, rows, 4),
+                             Extent::block("offsets", offsets, (n_experts + INT64_C(1)) * 4)}));
   return run_rows(fn, RowOp::kDispatch, a, dtype, stream);
 }
 
@@ -948,6 +970,8 @@ extern "C" zero_status zero_expert_dispatch_backward(const void* dxs, zero_dtype
   RowArgs a = {};
   a.in = dxs, a.out = dx, a.rows = rows;
   a.tokens = tokens, a.hidden = hidden, a.stride = hidden, a.topk = topk;
+  EXPERT_TRY(check_overlaps(fn, {Extent::block("dx", dx, tokens * hidden * type_bytes(dtype))},
+                            {sorted_rows("dxs", a, dxs, dtype), choices("rows", a, rows, 4)}));
   return run_rows(fn, RowOp::kCombine, a, dtype, stream);
 }
 
@@ -968,6 +992,9 @@ extern "C" zero_status zero_expert_combine(const void* ys, zero_dtype dtype, con
   RowArgs a = {};
   a.in = ys, a.out = y, a.weights = weights, a.weight_type = weight_dtype, a.rows = rows;
   a.tokens = tokens, a.hidden = hidden, a.stride = hidden, a.topk = topk;
+  EXPERT_TRY(check_overlaps(fn, {Extent::block("y", y, tokens * hidden * type_bytes(dtype))},
+                            {sorted_rows("ys", a, ys, dtype), choices("rows", a, rows, 4),
+                             choices("weights", a, weights, type_bytes(weight_dtype))}));
   return run_rows(fn, RowOp::kCombine, a, dtype, stream);
 }
 
@@ -998,5 +1025,11 @@ extern "C" zero_status zero_expert_combine_backward(const void* dy, int64_t dy_s
   a.in = dy, a.ys = ys, a.weights = weights, a.weight_type = weight_dtype, a.out = dys;
   a.dweights = dweights, a.rows = rows, a.total = offsets + n_experts;
   a.tokens = tokens, a.hidden = hidden, a.stride = dy_stride, a.topk = topk;
+  EXPERT_TRY(check_overlaps(fn,
+                            {Extent::block("dys", dys, tokens * topk * hidden * type_bytes(dtype)),
+                             choices("dweights", a, dweights, type_bytes(weight_dtype))},
+                            {token_rows("dy", a, dy_stride, dy, dtype), sorted_rows("ys", a, ys, dtype),
+                             choices("weights", a, weights, type_bytes(weight_dtype)), choices("rows", a, rows, 4),
+                             Extent::block("offsets", offsets, (n_experts + INT64_C(1)) * 4)}));
   return run_rows(fn, RowOp::kCombineBackward, a, dtype, stream);
 }

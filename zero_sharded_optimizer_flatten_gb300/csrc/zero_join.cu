@@ -416,6 +416,18 @@ zero_status check_inputs(const char* fn, const zero_join_desc& d, const zero_joi
   return ZERO_OK;
 }
 
+Extent rows_extent(const char* name, const void* p, const zero_join_desc& d, int64_t stride, int type) {
+  return {name, p, d.rows, stride * type_bytes(type), d.hidden * type_bytes(type)};
+}
+Extent vector_extent(const char* name, const void* p, const zero_join_desc& d, int type) {
+  const int64_t bytes = d.hidden * type_bytes(type);
+  return {name, p, 1, bytes, bytes};
+}
+Extent gate_extent(const void* p, const zero_join_desc& d) {
+  if (d.gate_kind == ZERO_GATE_CHANNEL) return vector_extent("gate", p, d, d.gate_dtype);
+  const int64_t pitch = d.gate_stride * type_bytes(d.gate_dtype);
+  return {"gate", p, d.rows, pitch, (d.gate_kind == ZERO_GATE_FULL ? d.hidden : 1) * type_bytes(d.gate_dtype)};
+}
 zero_status pending(const char* fn) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: pending CUDA error: %s", fn, cudaGetErrorString(e));
@@ -460,6 +472,18 @@ extern "C" zero_status zero_block_join(const zero_join_desc* desc, const zero_jo
   if (n && !inputs->w_pre) return fail(ZERO_ERR_INVALID, "%s: n needs w_pre", fn);
   if (d.rows == 0) return ZERO_OK;
   if (!o && !n) return fail(ZERO_ERR_INVALID, "%s: neither o nor n is wanted", fn);
+  const zero_join_inputs& in = *inputs;
+  const int64_t count = d.rows * d.hidden;
+  JOIN_TRY(check_overlaps(fn,
+                          {Extent::block("o", o, count * type_bytes(d.res_dtype), in.x),
+                           Extent::block("n", n, count * type_bytes(d.act_dtype), in.b),
+                           Extent::block("stats", stats, d.rows * 16)},
+                          {rows_extent("x", in.x, d, d.x_stride, d.res_dtype),
+                           rows_extent("b", in.b, d, d.b_stride, d.act_dtype), gate_extent(in.gate, d),
+                           vector_extent("w_post", in.w_post, d, d.param_dtype),
+                           vector_extent("bias_post", in.bias_post, d, d.param_dtype),
+                           vector_extent("w_pre", in.w_pre, d, d.param_dtype),
+                           vector_extent("bias_pre", in.bias_pre, d, d.param_dtype)}));
   JOIN_TRY(pending(fn));
   JoinArgs a = base_args(d, *inputs);
   a.o = o;
@@ -548,6 +572,25 @@ extern "C" zero_status zero_block_join_backward(const zero_join_desc* desc, cons
                   workspace_bytes, need);
     a.partial = static_cast<float*>(workspace);
   }
+  const int64_t count = d.rows * d.hidden;
+  const int64_t gates = channel ? d.hidden : d.gate_kind == ZERO_GATE_ROW ? d.rows : count;
+  JOIN_TRY(check_overlaps(fn,
+                          {Extent::block("dx", grads->dx, count * type_bytes(d.res_dtype), d_o),
+                           Extent::block("db", grads->db, count * type_bytes(d.act_dtype), d_n),
+                           Extent::block("dgate", grads->dgate, gates * type_bytes(d.gate_dtype)),
+                           vector_extent("dw_post", grads->dw_post, d, d.param_dtype),
+                           vector_extent("dbias_post", grads->dbias_post, d, d.param_dtype),
+                           vector_extent("dw_pre", grads->dw_pre, d, d.param_dtype),
+                           vector_extent("dbias_pre", grads->dbias_pre, d, d.param_dtype),
+                           Extent::block("workspace", a.partial, join_workers(d) * a.n_sums * d.hidden * 4)},
+                          {rows_extent("x", in.x, d, d.x_stride, d.res_dtype),
+                           rows_extent("b", in.b, d, d.b_stride, d.act_dtype), gate_extent(in.gate, d),
+                           vector_extent("w_post", in.w_post, d, d.param_dtype),
+                           vector_extent("bias_post", in.bias_post, d, d.param_dtype),
+                           vector_extent("w_pre", in.w_pre, d, d.param_dtype),
+                           rows_extent("d_o", d_o, d, d.do_stride, d.res_dtype),
+                           rows_extent("d_n", d_n, d, d.dn_stride, d.act_dtype),
+                           Extent::block("stats", stats, d.rows * 16)}));
   JOIN_TRY(pending(fn));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int workers = 0;
