@@ -5,11 +5,13 @@ zero_sharded_optimizer_flatten_gb300/libzero.so.  No cmake, no torch
 extension machinery: the library has a plain C ABI and no torch types.
 _train_ops.so beside it is the compiled part of the Python binding of the
 training-step operators (csrc/train_ops_binding.cpp): it is linked against the
-library and the installed torch, and holds no arithmetic.
+library and the installed torch, and holds no arithmetic.  Without torch the
+library is built alone.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -53,9 +55,14 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _wanted() -> list:
+    """What is built: the binding only where there is a torch to bind to."""
+    return [LIB, BINDING] if importlib.util.find_spec("torch") else [LIB]
+
+
 def up_to_date() -> bool:
     newest = _deps_mtime()
-    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING))
+    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in _wanted())
 
 
 def _compile_binding() -> str:
@@ -108,16 +115,18 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if BINDING in _wanted() else None
         objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
+        if binding:
+            binding = binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    if binding:
+        _link_binding(binding)
     return LIB
 
 
