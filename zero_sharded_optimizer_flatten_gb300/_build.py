@@ -11,11 +11,13 @@ library is built alone.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -60,15 +62,45 @@ def _wanted() -> list:
     return [LIB, BINDING] if importlib.util.find_spec("torch") else [LIB]
 
 
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # on the path without its record
+        import torch
+        return torch.__version__
+
+
+def _bound_to() -> str:
+    """What a binding built now belongs to: torch and Python keep no binary
+    interface from one version to the next."""
+    spec = importlib.util.find_spec("torch")
+    return f"torch {_torch_version()} {spec.origin} {sysconfig.get_config_var('SOABI')}"
+
+
+def _bound_to_file() -> str:
+    return os.path.join(BUILD, BINDING_SOURCE + ".for")
+
+
+def binding_problem():
+    """Why the binding cannot be loaded, None when it can."""
+    if not os.path.exists(BINDING):
+        return f"{BINDING} is not built"
+    try:
+        with open(_bound_to_file()) as f:
+            same = f.read() == _bound_to()
+    except FileNotFoundError:
+        same = False
+    return None if same else f"{BINDING} was built for another torch or Python"
+
+
 def up_to_date() -> bool:
-    newest = _deps_mtime()
-    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in _wanted())
+    newest, wanted = _deps_mtime(), _wanted()
+    return (all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in wanted)
+            and (BINDING not in wanted or binding_problem() is None))
 
 
 def _compile_binding() -> str:
     """Object file of the binding (the host compiler, torch's headers)."""
-    import sysconfig
-
     import torch
     root = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
@@ -94,6 +126,8 @@ def _link_binding(obj: str):
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stderr}")
     os.replace(tmp, BINDING)
+    with open(_bound_to_file(), "w") as f:
+        f.write(_bound_to())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:

@@ -14,10 +14,10 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-import os
 
 import torch
 
+from . import _build
 from . import zero as _zero
 from .zero import _check
 
@@ -42,7 +42,6 @@ def _choice(table, value, what: str) -> int:
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
-_FAST_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_train_ops.so")
 _lib = None
 
 
@@ -61,9 +60,10 @@ def _load_fast():
     """The compiled binding (built with the library, and linked against it)."""
     global _fast
     _load()
-    if not os.path.exists(_FAST_PATH):
-        raise RuntimeError(f"{_FAST_PATH} is not built: run `python -c 'import __graft_entry__ as "
-                           "g; g.build()'`; there is no fallback implementation")
+    problem = _build.binding_problem()
+    if problem:
+        raise RuntimeError(f"{problem}: run `python -c 'import __graft_entry__ as g; g.build()'`; "
+                           "there is no fallback implementation")
     from . import _train_ops
     _train_ops.set_error(_zero.ZeroError)
     _fast = _train_ops
