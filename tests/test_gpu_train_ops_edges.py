@@ -131,3 +131,21 @@ def test_outputs_between_the_rows_of_an_input():
         Z.zero_expert_dispatch(x, order, out=big.view(-1, 64)[39:41])
     with pytest.raises(Z.ZeroError, match="o overlaps x"):
         Z.zero_block_join(x, b, w_pre=w, o=big.view(-1, 64)[40:42])
+
+
+def test_errors_name_what_is_wrong():
+    x = torch.ones(4, 16, device="cuda")
+    w = torch.ones(16, device="cuda")
+    with pytest.raises(ValueError, match=r"o: expected a contiguous Float tensor of shape \(4, 16, \), "
+                                         r"got Half \(4, 16, \)"):
+        Z.zero_block_join(x, x, w_pre=w, o=x.half())
+    with pytest.raises(ValueError, match="stats: .*got Float .*not contiguous"):
+        Z.zero_block_join_backward(x, x, x, None, torch.ones(4, 4, device="cuda").t())
+    with pytest.raises(TypeError, match="w_pre: expected float16, bfloat16 or float32"):
+        Z.zero_block_join(x, w_pre=w.double())
+    with pytest.raises(TypeError, match="d_n: expected float16, bfloat16 or float32"):
+        Z.zero_block_join_backward(x, None, None, x.double(), None, w_pre=w)
+    with pytest.raises(RuntimeError, match="ambiguous"):   # torch's own, not a SystemError about it
+        Z.zero_block_join(x, x, w_pre=w, want_o=torch.ones(2))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        Z.zero_block_join(x, x, w_pre=w, want_stats=torch.ones(2))

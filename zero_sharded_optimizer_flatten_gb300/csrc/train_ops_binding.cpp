@@ -65,6 +65,7 @@ int type_of(at::ScalarType t, const char* what) {
 }
 int type_of(const Tensor& t, const char* what) { return type_of(t.scalar_type(), what); }
 
+const char* name_of(at::ScalarType t) { return c10::toString(t); }
 std::string shape_of(at::IntArrayRef s) {
   std::string r = "(";
   for (int64_t n : s) r += std::to_string(n) + ", ";
@@ -109,7 +110,9 @@ Tensor result(const Tensor& t, const char* what, at::IntArrayRef shape, at::Scal
   if (!t.defined()) return at::empty(shape, like.options().dtype(type));
   on(t, what, like.get_device());
   if (t.scalar_type() != type || t.sizes() != shape || !t.is_contiguous())
-    value_error(what, "expected a contiguous tensor of shape " + shape_of(shape) + " and another type or layout");
+    value_error(what, std::string("expected a contiguous ") + name_of(type) + " tensor of shape " + shape_of(shape) +
+                          ", got " + name_of(t.scalar_type()) + " " + shape_of(t.sizes()) +
+                          (t.is_contiguous() ? "" : ", not contiguous"));
   return t;
 }
 
@@ -125,6 +128,11 @@ double real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw PythonError();
   return v;
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw PythonError();
+  return v != 0;
 }
 int small(PyObject* o, const char* what) {
   const int64_t v = number(o);
@@ -196,8 +204,8 @@ struct Join {
   at::ScalarType act;
 
   // a: x, b, w_post, bias_post, w_pre, bias_pre, gate, kind, scale, eps;
-  // act_like: whose type n has when there is no b (None: see below)
-  Join(PyObject* const* a, const Tensor& act_like) {
+  // act_like: whose type n has when there is no b (None: see below), and its name
+  Join(PyObject* const* a, const Tensor& act_like, const char* act_name) {
     x = tensor(a[0], "x");
     dev = device_of(x, "x");
     if (x.dim() < 1) value_error("x", "expected [..., hidden]");
@@ -210,15 +218,16 @@ struct Join {
     d.res_dtype = type_of(x, "x");
     d.x_stride = row_stride(x, "x", shape, dev);
     act = x.scalar_type();
+    const char* act_of = "x";
     if (b.defined()) {
-      act = b.scalar_type();
+      act = b.scalar_type(), act_of = "b";
       d.b_stride = row_stride(b, "b", shape, dev);
     } else if (act_like.defined()) {
-      act = act_like.scalar_type();
+      act = act_like.scalar_type(), act_of = act_name;
     } else if (act == at::kFloat && w_pre.defined()) {
-      act = w_pre.scalar_type();
+      act = w_pre.scalar_type(), act_of = "w_pre";
     }
-    d.act_dtype = d.param_dtype = d.gate_dtype = type_of(act, "b");
+    d.act_dtype = d.param_dtype = d.gate_dtype = type_of(act, act_of);
     const Tensor* first = nullptr;
     vector(w_post, "w_post", hidden, first);
     vector(bias_post, "bias_post", hidden, first);
@@ -273,15 +282,15 @@ PyObject* block_join(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
     expect_args(n_args, 14);
     Tensor o = maybe(a[10], "o"), n = maybe(a[11], "n"), stats;
-    Join j(a, n);
+    Join j(a, n, "n");
     if (n.defined() && !j.w_pre.defined()) value_error("n", "needs w_pre");
-    const bool want_o = PyObject_IsTrue(a[12]) && (j.b.defined() || o.defined());
+    const bool want_o = truth(a[12]) && (j.b.defined() || o.defined());
     if (want_o)
       o = result(o, "o", j.x.sizes(), j.x.scalar_type(), j.x);
     else
       o = Tensor();
     if (j.w_pre.defined()) n = result(n, "n", j.x.sizes(), j.act, j.x);
-    if (PyObject_IsTrue(a[13])) stats = at::empty({j.d.rows, 4}, j.x.options().dtype(at::kFloat));
+    if (truth(a[13])) stats = at::empty({j.d.rows, 4}, j.x.options().dtype(at::kFloat));
     void* stream = stream_of(j.dev);
     unlocked([&] { return zero_block_join(&j.d, &j.in, ptr(o), ptr(n), static_cast<float*>(ptr(stats)), stream); });
     if (!want_o && !j.b.defined()) o = j.x;
@@ -293,7 +302,7 @@ PyObject* block_join(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 PyObject* block_join_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
     expect_args(n_args, 10);
-    Join j(a, Tensor());
+    Join j(a, Tensor(), "");
     int64_t need = 0;
     check(zero_block_join_workspace_bytes(&j.d, &need));
     return PyLong_FromLongLong(need);
@@ -309,7 +318,7 @@ PyObject* block_join_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) 
   return guarded([&]() -> PyObject* {
     expect_args(n_args, 15);
     const Tensor d_o = maybe(a[10], "d_o"), d_n = maybe(a[11], "d_n"), stats = maybe(a[12], "stats");
-    Join j(a, d_n);
+    Join j(a, d_n, "d_n");
     if (d_o.defined()) {
       if (d_o.scalar_type() != j.x.scalar_type()) raise(PyExc_TypeError, "d_o: another type than x");
       j.d.do_stride = row_stride(d_o, "d_o", j.x.sizes(), j.dev);
@@ -349,8 +358,10 @@ PyObject* block_join_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) 
       }
       const zero_join_grads g = {at_[0], at_[1], at_[2], at_[3], at_[4], at_[5], at_[6]};
       void* stream = stream_of(j.dev);
-    unlocked([&] { return zero_block_join_backward(&j.d, &j.in, ptr(d_o), ptr(d_n), static_cast<const float*>(ptr(stats)), &g,
-                                     ptr(ws), need, stream); });
+      unlocked([&] {
+        return zero_block_join_backward(&j.d, &j.in, ptr(d_o), ptr(d_n), static_cast<const float*>(ptr(stats)), &g,
+                                        ptr(ws), need, stream);
+      });
     }
     PyObject* r = PyDict_New();
     if (!r) throw PythonError();
@@ -498,7 +509,7 @@ PyObject* expert_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n_ar
       raise(PyExc_TypeError, "dy: another type or row length than ys");
     const int wtype = order.weights(weights, dev);
     const Tensor dys = at::empty(ys.sizes(), ys.options());
-    const Tensor dw = PyObject_IsTrue(a[8]) ? at::empty(weights.sizes(), weights.options()) : Tensor();
+    const Tensor dw = truth(a[8]) ? at::empty(weights.sizes(), weights.options()) : Tensor();
     void* stream = stream_of(dev);
     unlocked([&] { return zero_expert_combine_backward(ptr(dy), stride, ptr(ys), static_cast<zero_dtype>(type), ptr(weights),
                                        static_cast<zero_dtype>(wtype), order.tokens, order.topk, hidden,
