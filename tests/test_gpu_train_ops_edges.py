@@ -10,6 +10,8 @@ import torch
 import zero_sharded_optimizer_flatten_gb300 as Z
 from zero_sharded_optimizer_flatten_gb300 import train_ops as T
 
+from .test_gpu_train_ops import check_join, join_inputs
+
 pytestmark = pytest.mark.gpu
 
 H16, B16, F32 = torch.float16, torch.bfloat16, torch.float32
@@ -149,3 +151,67 @@ def test_errors_name_what_is_wrong():
         Z.zero_block_join(x, x, w_pre=w, want_o=torch.ones(2))
     with pytest.raises(RuntimeError, match="ambiguous"):
         Z.zero_block_join(x, x, w_pre=w, want_stats=torch.ones(2))
+
+
+# Rows above 8192 channels, and those below of which no copy fits in shared
+# memory, go element by element.  The sizes stay within 8200, up to which the
+# tolerances of check_join are derived.
+
+TYPES = [(H16, H16, H16), (B16, B16, F32), (B16, F32, B16), (H16, F32, F32), (F32, F32, F32)]
+
+
+@pytest.mark.parametrize("act,res,par", TYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("gate", ["none", "channel", "row", "full"])
+def test_long_rows_of_every_kind(act, res, par, kind, gate):
+    for post, pre in ((True, True), (True, False), (False, True), (False, False)):
+        for R, H in ((5, 8200), (3, 8195)):
+            check_join(join_inputs(R, H, act, res, par, gate, post, pre, kind == "layer", R * H + post),
+                       kind, eps=1e-3)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_long_rows_with_one_gradient_strides_and_no_block(kind):
+    layer = kind == "layer"
+    for use_o, use_n in ((True, False), (False, True)):
+        for gate in ("row", "full"):
+            check_join(join_inputs(4, 8200, B16, B16, F32, gate, True, True, layer, 3), kind, eps=1e-3,
+                       use_o=use_o, use_n=use_n)
+    for pad in (1, 8):
+        check_join(join_inputs(6, 8200, B16, F32, F32, "full", True, True, layer, pad, pad=pad), kind,
+                   eps=1e-3)
+        check_join(join_inputs(6, 8195, H16, H16, H16, "row", True, True, layer, pad, pad=pad), kind,
+                   eps=1e-3)
+    check_join(join_inputs(4, 8200, B16, B16, B16, "none", False, True, layer, 5, b=False), kind, eps=1e-3)
+
+
+def test_long_rows_more_than_there_are_ctas():
+    check_join(join_inputs(2500, 8200, B16, B16, B16, "row", True, True, True, 7), "layer", eps=1e-3)
+
+
+def test_long_rows_in_place_and_on_zeros():
+    for H in (8200, 8195):
+        for gate in ("channel", "row", "full"):
+            v = join_inputs(12, H, B16, B16, B16, gate, True, True, False, 8)
+            params = {k: t for k, t in v.items() if k not in ("x", "b")}
+            o, n, _ = Z.zero_block_join(v["x"], v["b"], **params)
+            x, b = v["x"].clone(), v["b"].clone()
+            Z.zero_block_join(x, b, o=x, n=b, **params)
+            assert torch.equal(x, o) and torch.equal(b, n)
+    x = torch.zeros(2, 8200, device="cuda")
+    w = torch.ones(8200, device="cuda")
+    for kind in ("rms", "layer"):
+        o, n, _ = Z.zero_block_join(x, x, w_post=w, w_pre=w, kind=kind)
+        assert not o.any() and not n.any()
+
+
+@pytest.mark.parametrize("H", [6660, 6664, 7684, 7688, 8192])
+def test_rows_that_leave_no_room_for_their_copies(H):
+    """fp32 layer norms with a full gate: forward from 7688 channels, backward
+    from 6664."""
+    for gate in ("full", "none"):
+        check_join(join_inputs(7, H, F32, F32, F32, gate, True, True, True, H), "layer", eps=1e-3)
+    check_join(join_inputs(7, H, F32, F32, F32, "full", True, True, False, H), "rms", eps=1e-3)
+    v = join_inputs(7, H, B16, F32, F32, "full", True, True, True, H)
+    v["gate"] = v["gate"].float()
+    check_join(v, "layer", eps=1e-3)
