@@ -105,13 +105,15 @@ def _compile_binding() -> str:
     root = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, BINDING_SOURCE + ".o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-I", INCLUDE, "-I",
-           sysconfig.get_paths()["include"], "-I", root, "-I",
-           os.path.join(root, "torch", "csrc", "api", "include"), "-I", cuda, "-c",
-           os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", INCLUDE]
+    for path in (sysconfig.get_paths()["include"], root,
+                 os.path.join(root, "torch", "csrc", "api", "include"), cuda):
+        cmd += ["-isystem", path]  # their warnings are not this file's
+    cmd += ["-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{' '.join(cmd)}\n{res.stderr}")
+    sys.stderr.write(res.stderr)
     return obj
 
 
