@@ -324,13 +324,12 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_norm(const __g
       norm_tile<__nv_bfloat16>(j, t, inf_norm, s, m);
     else
       norm_tile<__half>(j, t, inf_norm, s, m);
-    // a tile is at most 71 squares, 20 of them at most in one binary32 sum,
-    // before they join a pair
-    {
-      sum.a = pair_add(sum.a, {sum2(add2(s.a[0], s.a[1])), 0.f});
-      if (s.b != 0.f) sum.b = pair_add(sum.b, {s.b, 0.f});
-      s = {{f2(0.f), f2(0.f)}, 0.f};
-    }
+    // a thread has at most 71 squares of a tile before they join a pair: all of
+    // them in one binary32 sum where values of the upper range take part, 20
+    // in each of four otherwise
+    sum.a = pair_add(sum.a, {sum2(add2(s.a[0], s.a[1])), 0.f});
+    if (s.b != 0.f) sum.b = pair_add(sum.b, {s.b, 0.f});
+    s = {{f2(0.f), f2(0.f)}, 0.f};
   }
   if (inf_norm) sum.a.hi = __uint_as_float(m);
   sum = block_join(sum, inf_norm, part);

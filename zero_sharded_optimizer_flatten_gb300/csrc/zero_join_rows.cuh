@@ -113,9 +113,6 @@ __device__ __forceinline__ F2 widen2(uint32_t w) {
   Elem<T>::unpack(w, lo, hi);
   return f2(lo, hi);
 }
-__device__ __forceinline__ F2 widen2_any(uint32_t w, int type) {
-  return type == ZERO_BF16 ? widen2<__nv_bfloat16>(w) : widen2<__half>(w);
-}
 template <class T>
 __device__ __forceinline__ uint32_t pack2(F2 v) {
   float lo, hi;

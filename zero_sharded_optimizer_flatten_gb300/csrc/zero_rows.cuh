@@ -27,12 +27,6 @@ struct Elem<float> {
   static constexpr zero_dtype kType = ZERO_FP32;
   static __device__ __forceinline__ float widen(float x) { return x; }
   static __device__ __forceinline__ float narrow(float x) { return x; }
-  static __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
   static __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -52,11 +46,6 @@ struct Elem<__half> {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  static __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    unpack(w.x, v[0], v[1]), unpack(w.y, v[2], v[3]);
-    unpack(w.z, v[4], v[5]), unpack(w.w, v[6], v[7]);
-  }
   static __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
@@ -74,11 +63,6 @@ struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    unpack(w.x, v[0], v[1]), unpack(w.y, v[2], v[3]);
-    unpack(w.z, v[4], v[5]), unpack(w.w, v[6], v[7]);
   }
   static __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(p) =
@@ -128,24 +112,6 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, int type, float v)
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
   else
     static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
-
-__device__ __forceinline__ void load8_any(const void* p, int64_t i, int type, float (&v)[8]) {
-  if (type == ZERO_FP32)
-    Elem<float>::load8(static_cast<const float*>(p) + i, v);
-  else if (type == ZERO_BF16)
-    Elem<__nv_bfloat16>::load8(static_cast<const __nv_bfloat16*>(p) + i, v);
-  else
-    Elem<__half>::load8(static_cast<const __half*>(p) + i, v);
-}
-
-__device__ __forceinline__ void store8_any(void* p, int64_t i, int type, const float (&v)[8]) {
-  if (type == ZERO_FP32)
-    Elem<float>::store8(static_cast<float*>(p) + i, v);
-  else if (type == ZERO_BF16)
-    Elem<__nv_bfloat16>::store8(static_cast<__nv_bfloat16*>(p) + i, v);
-  else
-    Elem<__half>::store8(static_cast<__half*>(p) + i, v);
 }
 
 __host__ __device__ __forceinline__ int type_bytes(int type) { return type == ZERO_FP32 ? 4 : 2; }
