@@ -4,8 +4,8 @@ Tolerances.  u(T) is the half spacing of the type an output is rounded to
 (2^-24, 2^-11, 2^-8 relative; 2^-25 absolute below fp16's normal range).  All
 arithmetic before that rounding is binary32 (2^-24 an operation):
 
-* norm: at most 72 squares are added in binary32 before they join a binary64
-  sum, so the sum is off by at most 74 * 2^-24 = 4.4e-6 relative and the norm
+* norm: at most 72 squares are added in binary32 before they join a sum held
+  as two binary32 numbers, so the sum is off by at most 74 * 2^-24 = 4.4e-6 relative and the norm
   by half of it, 2.3e-6 with its own rounding.
 * join: a row sum of H terms is a strand of at most H/32 + 40 additions; for
   the H used here (at most 8200) that is 300 * 2^-24 = 1.8e-5 of the terms'

@@ -473,7 +473,7 @@ __device__ __forceinline__ void clip_tile_to(const GradJob& j, int t, float coef
     clip_tile<S, __half>(j, t, coef);
 }
 
-// Norm and clipping of 101M bf16 values into a replica: 101 us, of which the
+// Norm and clipping of 101M bf16 values into a replica: 101-106 us, of which the
 // norm's pass 36; 74 would be every second read from L2.
 template <int CAP>
 __global__ void __launch_bounds__(kNormThreads, kNormCtas) k_grad_clip(const __grid_constant__ GradArgs<CAP> a) {

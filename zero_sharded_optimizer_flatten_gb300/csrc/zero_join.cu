@@ -18,8 +18,9 @@
 // anyway, so o's own rounding enters no gradient.
 //
 // What bounds it: bytes (forward: x, b in, o, n out; backward: x, b, do, dn
-// in, dx, db out).  The kernels here take rows above 8192 channels; the others
-// are in zero_join_rows.cuh.
+// in, dx, db out).  The kernels here take rows above 8192 channels, and those
+// below of which not one fits into shared memory; the others are in
+// zero_join_rows.cuh.
 #include <cuda_runtime.h>
 #include <inttypes.h>
 #include <math.h>
@@ -42,7 +43,10 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Rows of any length and alignment: a CTA a row, element by element, the row
-// read again for each phase (from L1 or L2).
+// read again for each phase (from L1 or L2) and o formed again from it; the
+// backward column sums are kept in the CTA's partials.  Bound by that work, not
+// by bytes: 4096 x 12288 bf16, rms norms on both sides, 457 us forward and 2165
+// backward (0.13 and 0.04 of a plain copy's bandwidth).
 
 constexpr int kAnyThreads = 256;
 constexpr int kAnyWorkers = 4 * kSMs;

@@ -10,7 +10,7 @@ namespace zero {
 // sum dn oh, sum dn, sum y go v, sum y go.
 enum JoinSum { kSumP = 0, kSumQ, kSumS, kSumB, kJoinSums };
 
-constexpr int kJoinRowMost = 8192;         // channels of the kernels that hold rows in registers
+constexpr int kJoinRowMost = 8192;         // channels of the kernels that hold rows in registers, at most
 constexpr int kJoinNarrow = 4096;          // rows above it: 16 columns a thread, rms
 constexpr int kJoinNarrowLayer = 2047;     // and layer norms forward
 constexpr int kJoinThreadsForward = 1024;  // threads of an SM's CTAs there
@@ -41,7 +41,8 @@ struct JoinSumArgs {
   void *dw_pre, *dbias_pre, *dw_post, *dbias_post, *dgate;  // dgate: channel gates only
 };
 
-// Kernels for rows of up to kJoinRowMost channels; -1: the rows do not fit.
+// Kernels for rows of up to kJoinRowMost channels; -1: the rows are longer, or
+// do not fit into shared memory.
 // *workers: CTAs launched, each leaving its partials.
 template <class A, class R>
 int launch_join_rows(const JoinArgs& a, bool backward, int* workers, cudaStream_t s);

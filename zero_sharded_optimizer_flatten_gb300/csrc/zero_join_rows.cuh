@@ -1,5 +1,10 @@
 // The block join for rows of at most 8192 channels: a row's values stay in
 // registers, 8 or 16 columns a thread, from the one read to the one write.
+// Where not one row's arrays and the folded vectors fit into shared memory the
+// launch is left to the element kernels of zero_join.cu: fp32 with layer norms
+// on both sides and a full gate (forward above 7680 channels, backward above
+// 6656), and other backward passes with seven fp32 arrays and vectors in all
+// (above 7680).
 //
 // Row split.  Above 256 channels a CTA of whole warps takes a row at a time; a
 // row's sums go through one shuffle tree a warp and one barrier.  Rows that a

@@ -208,12 +208,16 @@ def _workspace(t, need: int, device: int):
 
 
 class GradNorm:
-    """A prepared zero_grad_norm over `grads` (None entries are left out):
-    the list is checked and marshalled once, each call takes the norm of what
-    the tensors hold then.  Returns the norm as a float32 tensor without
-    dimensions, a view of `result`, which the next call overwrites.
-    workspace: device scratch of zero_grad_norm_workspace_bytes (None: its
-    own)."""
+    """A prepared zero_grad_norm over `grads` (None entries are left out): the
+    list is checked and marshalled here once, each call takes the norm of what
+    the tensors hold then.  (The C call checks the list and fills its tables
+    each time.)  Returns the norm as a float32 tensor without dimensions, a
+    view of `result`, which the next call overwrites.  workspace: device
+    scratch of zero_grad_norm_workspace_bytes (None: its own).
+
+    Calls share the result and the workspace: those on different streams are
+    the caller's to order, one after the other.  A graph that captured a call
+    needs the object alive."""
 
     _ready = None
 
