@@ -746,6 +746,61 @@ zero_status zero_expert_combine_backward(const void* dy, int64_t dy_stride, cons
                                          int32_t n_experts, const int32_t* rows, void* dys,
                                          void* dweights, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Linear softmax cross entropy over a vocabulary                           */
+/* ------------------------------------------------------------------------ */
+/*
+ * The loss of a language model's head, without its logits in memory:
+ *   z = scale * x w^T                 x [tokens, hidden], w [vocab, hidden]
+ *   lse[t] = log(sum_v exp(z[t][v]))
+ *   losses[t] = lse[t] - z[t][targets[t]]
+ * A token whose target lies outside [0, vocab) is left out: its losses and lse
+ * are 0, nothing of its row of x is read, and it costs next to nothing.
+ *   total = {sum / max(count, 1), sum, count} of the losses that are not left out
+ *   rows[0 .. n) = the tokens that are not left out, in order, then -1;
+ *   rows[tokens] = n
+ * x and w are 16-bit; products are summed in binary32, and so are the
+ * exponentials.  targets: int32 (id_bytes 4) or int64 (8).  Pointers need their
+ * element's alignment only, the workspace 256 bytes; w with rows off 16-byte
+ * boundaries is copied to the workspace first.  tokens at most 2^24, hidden
+ * 2^20, vocab 2^28; |scale| in [1e-6, 1e6].  Outputs and workspace overlap no
+ * input and no other output.  The same call gives the same bits.
+ */
+typedef enum { ZERO_LOSS_NONE = 0, ZERO_LOSS_SUM = 1, ZERO_LOSS_MEAN = 2 } zero_loss_reduction;
+
+typedef struct {
+  int64_t tokens, hidden, vocab;
+  int64_t x_stride, w_stride; /* elements between rows                 */
+  zero_dtype dtype;           /* x, w, dx: ZERO_FP16 or ZERO_BF16      */
+  int32_t id_bytes;
+  double scale;
+} zero_linear_ce_desc;
+
+/* Device workspace of the call (backward 0) or of its gradient (1). */
+zero_status zero_linear_cross_entropy_workspace_bytes(const zero_linear_ce_desc* desc, const void* w,
+                                                      int32_t backward, int64_t* bytes);
+
+/* losses, lse: float[tokens]; rows: int32[tokens + 1]; total: float[3]. */
+zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc, const void* x, const void* w,
+                                      const void* targets, float* losses, float* lse, int32_t* rows,
+                                      float* total, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
+
+/* dx [tokens, hidden] and dw [vocab, hidden], contiguous, either may be NULL,
+ * from the forward call's lse and rows; x, w and targets still hold what it
+ * read.  d_loss (device): of ZERO_LOSS_NONE float[tokens], the gradients of the
+ * losses; else one float, of their sum or of their mean (total[1], total[0]).
+ * The logits are formed again, a piece of the vocabulary at a time; their
+ * gradient is rounded to dtype (scaled by a power of two that keeps it in
+ * range) between its two products, dx and dw are rounded once.  dw_dtype:
+ * dtype or ZERO_FP32. */
+zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, const void* x,
+                                               const void* w, const void* targets, const float* lse,
+                                               const int32_t* rows, const float* d_loss,
+                                               int32_t reduction, void* dx, void* dw,
+                                               zero_dtype dw_dtype, void* workspace,
+                                               int64_t workspace_bytes, void* stream);
+
 /*
  * Measurement helper; the pages have no counterpart.  Launches, on `stream`,
  * kernels with exactly the grid, job table and memory accesses zero_step

@@ -23,12 +23,15 @@ from .zero import (AMP_STATE_BYTES, ZERO_BF16, ZERO_FP16, ZERO_PART_FLAT,  # noq
                    zero_sync, zero_version, zero_zero3_pass)
 
 
-_TRAIN_OPS = ("ClipGradNorm", "ExpertOrder", "GradNorm", "NormResult", "block_join",
-              "expert_combine", "expert_dispatch", "read_norm_result", "zero_block_join",
-              "zero_block_join_backward", "zero_block_join_workspace_bytes",
-              "zero_clip_grad_norm", "zero_expert_combine", "zero_expert_combine_backward",
-              "zero_expert_dispatch", "zero_expert_dispatch_backward", "zero_expert_sort",
-              "zero_expert_sort_workspace_bytes", "zero_grad_norm", "zero_grad_norm_workspace_bytes")
+_TRAIN_OPS = ("ClipGradNorm", "CrossEntropy", "ExpertOrder", "GradNorm", "NormResult",
+              "block_join", "expert_combine", "expert_dispatch", "linear_cross_entropy",
+              "read_norm_result", "zero_block_join", "zero_block_join_backward",
+              "zero_block_join_workspace_bytes", "zero_clip_grad_norm", "zero_expert_combine",
+              "zero_expert_combine_backward", "zero_expert_dispatch",
+              "zero_expert_dispatch_backward", "zero_expert_sort",
+              "zero_expert_sort_workspace_bytes", "zero_grad_norm",
+              "zero_grad_norm_workspace_bytes", "zero_linear_cross_entropy",
+              "zero_linear_cross_entropy_backward", "zero_linear_cross_entropy_workspace_bytes")
 
 
 def __getattr__(name):

@@ -1,5 +1,5 @@
-// Python binding of the block join and the expert permutation: checks of the
-// tensors, new outputs, the current stream, the C call of include/zero.h.
+// Python binding of the block join, the expert permutation and the head's
+// cross entropy: checks of the tensors, new outputs, the current stream, the C call of include/zero.h.
 // train_ops.py has the functions' Python signatures and documentation.
 //
 // These calls are made many times a step and their kernels can take a few
@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <string>
 #include <vector>
@@ -519,6 +520,132 @@ PyObject* expert_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n_ar
   });
 }
 
+// ---------------------------------------------------------------------------
+// linear softmax cross entropy
+
+at::ScalarType scalar_of(int type) {
+  return type == ZERO_FP16 ? at::kHalf : type == ZERO_BF16 ? at::kBFloat16 : at::kFloat;
+}
+
+// Elements between rows of a matrix whose rows are contiguous.
+int64_t matrix_stride(const Tensor& t, const char* what, int dev) {
+  on(t, what, dev);
+  if (t.dim() != 2) value_error(what, "expected a matrix, got " + shape_of(t.sizes()));
+  return row_stride(t, what, t.sizes(), dev);
+}
+
+int id_bytes_of(const Tensor& t, const char* what, int dev) {
+  on(t, what, dev);
+  if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong)
+    raise(PyExc_TypeError, std::string(what) + ": expected int32 or int64");
+  if (!t.is_contiguous()) value_error(what, "expected a contiguous tensor");
+  return static_cast<int>(t.element_size());
+}
+
+struct Head {
+  Tensor x, w, targets;
+  zero_linear_ce_desc d = {};
+  int dev;
+  // a: x, w, targets, scale
+  explicit Head(PyObject* const* a) {
+    x = tensor(a[0], "x"), w = tensor(a[1], "w"), targets = tensor(a[2], "targets");
+    dev = device_of(x, "x");
+    if (x.dim() < 1) value_error("x", "expected [..., hidden]");
+    if (x.scalar_type() != at::kHalf && x.scalar_type() != at::kBFloat16)
+      raise(PyExc_TypeError, "x: expected float16 or bfloat16");
+    d.hidden = x.size(-1);
+    d.x_stride = row_stride(x, "x", x.sizes(), dev);
+    d.w_stride = matrix_stride(w, "w", dev);
+    if (w.size(1) != d.hidden)
+      value_error("w", "shape " + shape_of(w.sizes()) + ", expected rows of " + std::to_string(d.hidden));
+    if (w.scalar_type() != x.scalar_type()) raise(PyExc_TypeError, "w: another type than x");
+    d.vocab = w.size(0);
+    d.tokens = d.hidden ? x.numel() / d.hidden : 0;
+    d.id_bytes = id_bytes_of(targets, "targets", dev);
+    if (targets.sizes() != x.sizes().slice(0, static_cast<size_t>(x.dim() - 1)))
+      value_error("targets", "shape " + shape_of(targets.sizes()) + ", expected that of x's rows");
+    // one row or none: any stride
+    if (d.tokens <= 1) d.x_stride = std::max(d.x_stride, d.hidden);
+    if (d.vocab <= 1) d.w_stride = std::max(d.w_stride, d.hidden);
+    d.dtype = static_cast<zero_dtype>(type_of(x, "x"));
+    d.scale = real(a[3]);
+  }
+  Tensor workspace(PyObject* o, bool backward, int64_t* need) const {
+    check(zero_linear_cross_entropy_workspace_bytes(&d, ptr(w), backward, need));
+    return workspace_of(o, *need, x);
+  }
+};
+
+// x, w, targets, scale, backward -> bytes
+PyObject* linear_cross_entropy_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n_args, 5);
+    const Head h(a);
+    int64_t need = 0;
+    check(zero_linear_cross_entropy_workspace_bytes(&h.d, ptr(h.w), truth(a[4]), &need));
+    return PyLong_FromLongLong(need);
+  });
+}
+
+// x, w, targets, scale, workspace -> (losses, lse, total, rows)
+PyObject* linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n_args, 5);
+    const Head h(a);
+    int64_t need = 0;
+    const Tensor ws = h.workspace(a[4], false, &need);
+    const at::TensorOptions f = h.x.options().dtype(at::kFloat);
+    const Tensor losses = at::empty(h.targets.sizes(), f), lse = at::empty(h.targets.sizes(), f),
+                 total = at::empty({3}, f), rows = at::empty({h.d.tokens + 1}, f.dtype(at::kInt));
+    void* stream = stream_of(h.dev);
+    unlocked([&] {
+      return zero_linear_cross_entropy(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets), static_cast<float*>(ptr(losses)),
+                                       static_cast<float*>(ptr(lse)), static_cast<int32_t*>(ptr(rows)),
+                                       static_cast<float*>(ptr(total)), ptr(ws), need, stream);
+    });
+    return tuple_of({losses, lse, total, rows});
+  });
+}
+
+// x, w, targets, scale, lse, rows, d_loss, reduction, want_dx, want_dw, dx, dw,
+// dw_type (-1: w's), workspace -> (dx, dw)
+PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n_args, 14);
+    const Head h(a);
+    const Tensor lse = tensor(a[4], "lse"), rows = tensor(a[5], "rows"), d_loss = tensor(a[6], "d_loss");
+    const int reduction = small(a[7], "reduction");
+    result(lse, "lse", h.targets.sizes(), at::kFloat, h.x);
+    result(rows, "rows", {h.d.tokens + 1}, at::kInt, h.x);
+    if (reduction == ZERO_LOSS_NONE) {
+      result(d_loss, "d_loss", h.targets.sizes(), at::kFloat, h.x);
+    } else {
+      on(d_loss, "d_loss", h.dev);
+      if (d_loss.scalar_type() != at::kFloat || d_loss.numel() != 1)
+        value_error("d_loss", "expected one float32 number");
+    }
+    Tensor dx = maybe(a[10], "dx"), dw = maybe(a[11], "dw");
+    const bool want_dx = truth(a[8]), want_dw = truth(a[9]);
+    if ((dx.defined() && !want_dx) || (dw.defined() && !want_dw)) value_error("want", "an output that is not wanted");
+    int type = small(a[12], "dw_dtype");
+    if (type < 0) type = dw.defined() ? type_of(dw, "dw") : static_cast<int>(h.d.dtype);
+    if (type != h.d.dtype && type != ZERO_FP32) raise(PyExc_TypeError, "dw: expected the type of w or float32");
+    int64_t need = 0;
+    const Tensor ws = h.workspace(a[13], true, &need);
+    if (want_dx) dx = result(dx, "dx", h.x.sizes(), h.x.scalar_type(), h.x);
+    if (want_dw) dw = result(dw, "dw", h.w.sizes(), scalar_of(type), h.w);
+    void* stream = stream_of(h.dev);
+    unlocked([&] {
+      return zero_linear_cross_entropy_backward(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets),
+                                                static_cast<const float*>(ptr(lse)),
+                                                static_cast<const int32_t*>(ptr(rows)),
+                                                static_cast<const float*>(ptr(d_loss)), reduction, ptr(dx), ptr(dw),
+                                                static_cast<zero_dtype>(type), ptr(ws), need, stream);
+    });
+    return tuple_of({dx, dw});
+  });
+}
+
 // The class of errors that the C calls' statuses raise.
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
@@ -542,6 +669,9 @@ PyMethodDef g_methods[] = {
     {"expert_dispatch_backward", fast(expert_dispatch_backward), METH_FASTCALL, nullptr},
     {"expert_combine", fast(expert_combine), METH_FASTCALL, nullptr},
     {"expert_combine_backward", fast(expert_combine_backward), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy", fast(linear_cross_entropy), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy_workspace_bytes", fast(linear_cross_entropy_workspace_bytes), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy_backward", fast(linear_cross_entropy_backward), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_train_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

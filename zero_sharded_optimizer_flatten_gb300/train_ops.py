@@ -554,3 +554,85 @@ def expert_dispatch(x, order: ExpertOrder):
 def expert_combine(ys, weights, order: ExpertOrder):
     """zero_expert_combine with autograd (of ys and of the weights)."""
     return _ExpertCombine.apply(ys, weights, order)
+
+
+# ----------------------------------------------------------------------------
+# linear softmax cross entropy
+
+_REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+
+
+@dataclasses.dataclass
+class CrossEntropy:
+    """What zero_linear_cross_entropy leaves on the device: losses and lse of
+    the targets' shape (0 where a token is left out), total [3] (mean, sum and
+    number of the losses), all float32; rows, which the backward call takes."""
+    losses: torch.Tensor
+    lse: torch.Tensor
+    total: torch.Tensor
+    rows: torch.Tensor
+
+
+def zero_linear_cross_entropy_workspace_bytes(x, w, targets, *, scale: float = 1.0,
+                                              backward: bool = False) -> int:
+    """Device workspace of zero_linear_cross_entropy, or of its backward call."""
+    return (_fast or _load_fast()).linear_cross_entropy_workspace_bytes(x, w, targets, scale,
+                                                                        backward)
+
+
+def zero_linear_cross_entropy(x, w, targets, *, scale: float = 1.0, workspace=None,
+                              stream=None) -> CrossEntropy:
+    """Cross entropy of the logits scale * x w^T with the targets (see zero.h),
+    the logits never in memory.  x: [..., hidden], w: [vocab, hidden], both
+    float16 or bfloat16; targets: [...], int32 or int64, a token whose target
+    lies outside [0, vocab) is left out.  workspace: 256-byte aligned device
+    scratch of zero_linear_cross_entropy_workspace_bytes (None: allocated
+    here)."""
+    return CrossEntropy(*_run_on(stream, lambda: (_fast or _load_fast()).linear_cross_entropy(
+        x, w, targets, scale, workspace)))
+
+
+def zero_linear_cross_entropy_backward(x, w, targets, ce: CrossEntropy, d_loss, *,
+                                       reduction: str = "mean", scale: float = 1.0,
+                                       want=("dx", "dw"), dx=None, dw=None, dw_dtype=None,
+                                       workspace=None, stream=None):
+    """(dx, dw) of zero_linear_cross_entropy from the gradient of its mean
+    (ce.total[0]), its sum (ce.total[1]), each one float32 number on the
+    device, or of the losses (reduction "none").  None for what is not in
+    `want`.  dw_dtype: the type of w (None) or float32."""
+    kind = _choice(_REDUCTIONS, reduction, "reduction")
+    if not set(want) <= {"dx", "dw"}:
+        raise ValueError(f"want must name dx or dw, got {want!r}")
+    if dw_dtype is not None and dw_dtype not in _TYPES:
+        raise TypeError(f"dw_dtype: expected float16, bfloat16 or float32, got {dw_dtype}")
+    code = -1 if dw_dtype is None else _TYPES[dw_dtype]
+    return _run_on(stream, lambda: (_fast or _load_fast()).linear_cross_entropy_backward(
+        x, w, targets, scale, ce.lse, ce.rows, d_loss, kind, "dx" in want, "dw" in want, dx, dw,
+        code, workspace))
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, targets, scale, reduction):
+        ce = zero_linear_cross_entropy(x, w, targets, scale=scale)
+        ctx.how = dict(scale=scale, reduction=reduction)
+        ctx.save_for_backward(x, w, targets, ce.lse, ce.rows)
+        if reduction == "none":
+            return ce.losses
+        return ce.total[1 if reduction == "sum" else 0]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d):
+        x, w, targets, lse, rows = ctx.saved_tensors
+        want = [k for k, needed in zip(("dx", "dw"), ctx.needs_input_grad) if needed]
+        dx, dw = zero_linear_cross_entropy_backward(x, w, targets, CrossEntropy(None, lse, None, rows),
+                                                    d.contiguous(), want=want, **ctx.how)
+        return dx, dw, None, None, None
+
+
+def linear_cross_entropy(x, w, targets, *, scale: float = 1.0, reduction: str = "mean"):
+    """zero_linear_cross_entropy with autograd: its mean or sum over the tokens
+    that are not left out (0 when all are), or ("none") every token's loss."""
+    _choice(_REDUCTIONS, reduction, "reduction")
+    return _LinearCrossEntropy.apply(x, w, targets, scale, reduction)
