@@ -747,6 +747,72 @@ zero_status zero_expert_combine_backward(const void* dy, int64_t dy_stride, cons
                                          void* dweights, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Router: probabilities, choices, counts and balance of sparse experts     */
+/* ------------------------------------------------------------------------ */
+/*
+ * What makes the ids and weights that the calls above take, from every token's
+ * scores z of the experts:
+ *   p = softmax(z), lse = log(sum exp z); a token whose scores are all -inf is
+ *     left out: no choice, p and lse 0
+ *   ids[t][k]     = the expert of the k-th largest score, of equal scores the
+ *                   lowest expert; -inf is never chosen: -1 (dropped by the
+ *                   sort).  NaN counts as the largest.
+ *   weights[t][k] = p of the choice, with normalize divided by the sum of the
+ *                   token's; 0 for -1
+ *   counts[e]     = how often expert e was chosen, n = tokens not left out
+ *   losses[0]     = n_experts / (topk max(n,1)^2) sum_e counts[e] sum_t p[t][e],
+ *                   1 when the experts are chosen evenly
+ *   losses[1]     = sum_t lse[t]^2 / max(n,1)
+ *   stats[t] = lse[t], stats[tokens] = n
+ * Sums are binary32 in a fixed order.  n_experts at most 1024, topk at most 32,
+ * tokens 2^24.  logits_stride: elements between rows.  Pointers need their
+ * element's alignment only.  Outputs overlap no input and no other output.
+ */
+zero_status zero_expert_route(const void* logits, int64_t logits_stride, zero_dtype dtype,
+                              int64_t tokens, int32_t n_experts, int32_t topk, int32_t normalize,
+                              int32_t* ids, float* weights, int32_t* counts, float* losses,
+                              float* stats, void* workspace, int64_t workspace_bytes, void* stream);
+zero_status zero_expert_route_workspace_bytes(int64_t tokens, int32_t n_experts, int64_t* bytes);
+
+/* d_logits (dtype, contiguous) from the gradients of the weights and of the two
+ * losses (either may be NULL: no gradient comes that way); the counts and the
+ * choices are constants.  A left-out token's row is zero. */
+zero_status zero_expert_route_backward(const void* logits, int64_t logits_stride, zero_dtype dtype,
+                                       int64_t tokens, int32_t n_experts, int32_t topk,
+                                       int32_t normalize, const int32_t* ids, const float* weights,
+                                       const int32_t* counts, const float* stats,
+                                       const float* d_weights, const float* d_losses,
+                                       void* d_logits, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Token embedding and the gradient of its table                            */
+/* ------------------------------------------------------------------------ */
+/*
+ * y[t] = scale * table[ids[t]], zero for an id outside [0, vocab), the product
+ * in binary32 and rounded once.  ids: int32 (id_bytes 4) or int64 (8); y is
+ * contiguous, of table_dtype or ZERO_FP32.  Pointers need their element's
+ * alignment only.  Outputs overlap no input and no other output.  tokens at most
+ * 2^28, vocab 2^22, hidden 2^20.
+ */
+zero_status zero_embedding(const void* ids, int32_t id_bytes, int64_t tokens, const void* table,
+                           int64_t table_stride, zero_dtype table_dtype, int64_t vocab,
+                           int64_t hidden, double scale, void* y, zero_dtype y_dtype, void* stream);
+
+/* dtable[v] = scale * sum of dy[t] over the tokens with ids[t] = v, zero for an
+ * id that no token has; accumulate: on top of what dtable holds, and only the
+ * rows of the tokens' ids are touched (a table that is also the head's takes
+ * both gradients so).  Sums are binary32 in a fixed order (the same call gives
+ * the same bits), rounded once.  dtable is contiguous; it and dy have one type,
+ * or one of them ZERO_FP32.  workspace: 256-byte aligned device scratch. */
+zero_status zero_embedding_backward(const void* dy, int64_t dy_stride, zero_dtype dy_dtype,
+                                    const void* ids, int32_t id_bytes, int64_t tokens,
+                                    int64_t vocab, int64_t hidden, double scale, int32_t accumulate,
+                                    void* dtable, zero_dtype dtable_dtype, void* workspace,
+                                    int64_t workspace_bytes, void* stream);
+zero_status zero_embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t hidden,
+                                           int64_t* bytes);
+
+/* ------------------------------------------------------------------------ */
 /* Linear softmax cross entropy over a vocabulary                           */
 /* ------------------------------------------------------------------------ */
 /*

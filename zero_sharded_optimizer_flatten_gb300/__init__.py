@@ -4,7 +4,8 @@ The compute lives in libzero.so (C ABI: include/zero.h; CUDA kernels for
 sm_103a in csrc/); this package is its Python binding.  ``engine`` wires a
 model's backward pass into it; ``train_ops`` holds the operators of a
 training step around it (gradient norm and clipping, block join, expert
-permutation); ``workloads`` holds the seeded synthetic parameter groups used
+routing and permutation, token embedding, cross entropy over the vocabulary);
+``workloads`` holds the seeded synthetic parameter groups used
 by the tests and the benchmark.
 """
 from .zero import (AMP_STATE_BYTES, ZERO_BF16, ZERO_FP16, ZERO_PART_FLAT,  # noqa: F401
@@ -23,12 +24,15 @@ from .zero import (AMP_STATE_BYTES, ZERO_BF16, ZERO_FP16, ZERO_PART_FLAT,  # noq
                    zero_sync, zero_version, zero_zero3_pass)
 
 
-_TRAIN_OPS = ("ClipGradNorm", "CrossEntropy", "ExpertOrder", "GradNorm", "NormResult",
-              "block_join", "expert_combine", "expert_dispatch", "linear_cross_entropy",
-              "read_norm_result", "zero_block_join", "zero_block_join_backward",
-              "zero_block_join_workspace_bytes", "zero_clip_grad_norm", "zero_expert_combine",
+_TRAIN_OPS = ("ClipGradNorm", "CrossEntropy", "ExpertOrder", "ExpertRoute", "GradNorm",
+              "NormResult", "block_join", "embedding", "expert_combine", "expert_dispatch",
+              "expert_route", "linear_cross_entropy", "read_norm_result", "zero_block_join",
+              "zero_block_join_backward", "zero_block_join_workspace_bytes",
+              "zero_clip_grad_norm", "zero_embedding", "zero_embedding_backward",
+              "zero_embedding_workspace_bytes", "zero_expert_combine",
               "zero_expert_combine_backward", "zero_expert_dispatch",
-              "zero_expert_dispatch_backward", "zero_expert_sort",
+              "zero_expert_dispatch_backward", "zero_expert_route", "zero_expert_route_backward",
+              "zero_expert_route_workspace_bytes", "zero_expert_sort",
               "zero_expert_sort_workspace_bytes", "zero_grad_norm",
               "zero_grad_norm_workspace_bytes", "zero_linear_cross_entropy",
               "zero_linear_cross_entropy_backward", "zero_linear_cross_entropy_workspace_bytes")

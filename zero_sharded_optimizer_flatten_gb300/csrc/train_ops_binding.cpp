@@ -1,5 +1,5 @@
-// Python binding of the block join, the expert permutation and the head's
-// cross entropy: checks of the tensors, new outputs, the current stream, the C call of include/zero.h.
+// Python binding of the block join, the expert permutation and routing, the
+// token embedding and the head's cross entropy: checks of the tensors, new outputs, the current stream, the C call of include/zero.h.
 // train_ops.py has the functions' Python signatures and documentation.
 //
 // These calls are made many times a step and their kernels can take a few
@@ -521,7 +521,7 @@ PyObject* expert_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n_ar
 }
 
 // ---------------------------------------------------------------------------
-// linear softmax cross entropy
+// router
 
 at::ScalarType scalar_of(int type) {
   return type == ZERO_FP16 ? at::kHalf : type == ZERO_BF16 ? at::kBFloat16 : at::kFloat;
@@ -541,6 +541,141 @@ int id_bytes_of(const Tensor& t, const char* what, int dev) {
   if (!t.is_contiguous()) value_error(what, "expected a contiguous tensor");
   return static_cast<int>(t.element_size());
 }
+
+// The logits' shape and stride.
+struct Scores {
+  Tensor z;
+  int dev, type;
+  int64_t tokens, stride;
+  int experts;
+  explicit Scores(PyObject* o) {
+    z = tensor(o, "logits");
+    dev = device_of(z, "logits"), type = type_of(z, "logits");
+    stride = matrix_stride(z, "logits", dev);
+    tokens = z.size(0);
+    if (z.size(1) > INT32_MAX) value_error("logits", "too many experts");
+    experts = static_cast<int>(z.size(1));
+    if (tokens <= 1) stride = std::max(stride, z.size(1));
+  }
+};
+
+// logits, topk, normalize, workspace -> (ids, weights, counts, losses, stats)
+PyObject* expert_route(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n_args, 4);
+    const Scores s(a[0]);
+    const int topk = small(a[1], "topk");
+    const bool normalize = truth(a[2]);
+    int64_t need = 0;
+    check(zero_expert_route_workspace_bytes(s.tokens, s.experts, &need));
+    if (topk < 1 || topk > s.experts) value_error("topk", "must lie in [1, n_experts]");
+    const at::TensorOptions f = s.z.options().dtype(at::kFloat), i = s.z.options().dtype(at::kInt);
+    const Tensor ids = at::empty({s.tokens, topk}, i), weights = at::empty({s.tokens, topk}, f),
+                 counts = at::empty({s.experts}, i), losses = at::empty({2}, f), stats = at::empty({s.tokens + 1}, f);
+    const Tensor ws = workspace_of(a[3], need, s.z);
+    void* stream = stream_of(s.dev);
+    unlocked([&] {
+      return zero_expert_route(ptr(s.z), s.stride, static_cast<zero_dtype>(s.type), s.tokens, s.experts, topk, normalize,
+                               static_cast<int32_t*>(ptr(ids)), static_cast<float*>(ptr(weights)),
+                               static_cast<int32_t*>(ptr(counts)), static_cast<float*>(ptr(losses)),
+                               static_cast<float*>(ptr(stats)), ptr(ws), need, stream);
+    });
+    return tuple_of({ids, weights, counts, losses, stats});
+  });
+}
+
+// logits, normalize, ids, weights, counts, stats, d_weights, d_losses, out -> d_logits
+PyObject* expert_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n_args, 9);
+    const Scores s(a[0]);
+    const bool normalize = truth(a[1]);
+    const Tensor ids = tensor(a[2], "ids"), weights = tensor(a[3], "weights"), counts = tensor(a[4], "counts"),
+                 stats = tensor(a[5], "stats"), dw = maybe(a[6], "d_weights"), dl = maybe(a[7], "d_losses");
+    if (ids.dim() != 2 || ids.size(1) > INT32_MAX) value_error("ids", "expected [tokens, topk]");
+    const int topk = static_cast<int>(ids.size(1));
+    result(ids, "ids", {s.tokens, topk}, at::kInt, s.z);
+    result(weights, "weights", {s.tokens, topk}, at::kFloat, s.z);
+    result(counts, "counts", {s.experts}, at::kInt, s.z);
+    result(stats, "stats", {s.tokens + 1}, at::kFloat, s.z);
+    if (dw.defined()) result(dw, "d_weights", {s.tokens, topk}, at::kFloat, s.z);
+    if (dl.defined()) result(dl, "d_losses", {2}, at::kFloat, s.z);
+    const Tensor out = result(maybe(a[8], "out"), "out", s.z.sizes(), s.z.scalar_type(), s.z);
+    void* stream = stream_of(s.dev);
+    unlocked([&] {
+      return zero_expert_route_backward(ptr(s.z), s.stride, static_cast<zero_dtype>(s.type), s.tokens, s.experts, topk,
+                                        normalize, static_cast<const int32_t*>(ptr(ids)),
+                                        static_cast<const float*>(ptr(weights)),
+                                        static_cast<const int32_t*>(ptr(counts)),
+                                        static_cast<const float*>(ptr(stats)), static_cast<const float*>(ptr(dw)),
+                                        static_cast<const float*>(ptr(dl)), ptr(out), stream);
+    });
+    return wrapped(out);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// token embedding
+
+// ids, table, scale, type (-1: the table's), out -> y
+PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n_args, 5);
+    const Tensor ids = tensor(a[0], "ids"), table = tensor(a[1], "table");
+    const int dev = device_of(table, "table"), from = type_of(table, "table");
+    const int id_bytes = id_bytes_of(ids, "ids", dev);
+    int64_t stride = matrix_stride(table, "table", dev);
+    if (table.size(0) <= 1) stride = std::max(stride, table.size(1));
+    const double scale = real(a[2]);
+    Tensor y = maybe(a[4], "out");
+    int type = small(a[3], "dtype");
+    if (type < 0) type = y.defined() ? type_of(y, "out") : from;
+    std::vector<int64_t> shape(ids.sizes().begin(), ids.sizes().end());
+    shape.push_back(table.size(1));
+    y = result(y, "out", shape, scalar_of(type), table);
+    void* stream = stream_of(dev);
+    unlocked([&] {
+      return zero_embedding(ptr(ids), id_bytes, ids.numel(), ptr(table), stride, static_cast<zero_dtype>(from),
+                            table.size(0), table.size(1), scale, ptr(y), static_cast<zero_dtype>(type), stream);
+    });
+    return wrapped(y);
+  });
+}
+
+// dy, ids, vocab, scale, type (-1: dy's), out, accumulate, workspace -> dtable
+PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n_args, 8);
+    const Tensor dy = tensor(a[0], "dy"), ids = tensor(a[1], "ids");
+    const int dev = device_of(dy, "dy"), from = type_of(dy, "dy");
+    const int id_bytes = id_bytes_of(ids, "ids", dev);
+    if (dy.dim() < 1 || dy.sizes().slice(0, static_cast<size_t>(dy.dim() - 1)) != ids.sizes())
+      value_error("dy", "shape " + shape_of(dy.sizes()) + ", expected " + shape_of(ids.sizes()) + " and the hidden size");
+    const int64_t tokens = ids.numel(), hidden = dy.size(-1), vocab = number(a[2]);
+    int64_t stride = row_stride(dy, "dy", dy.sizes(), dev);
+    if (tokens <= 1) stride = std::max(stride, hidden);
+    const double scale = real(a[3]);
+    Tensor out = maybe(a[5], "out");
+    const bool accumulate = truth(a[6]);
+    if (accumulate && !out.defined()) value_error("accumulate", "needs out");
+    int type = small(a[4], "dtype");
+    if (type < 0) type = out.defined() ? type_of(out, "out") : from;
+    int64_t need = 0;
+    check(zero_embedding_workspace_bytes(tokens, vocab, hidden, &need));
+    out = result(out, "out", {vocab, hidden}, scalar_of(type), dy);
+    const Tensor ws = workspace_of(a[7], need, dy);
+    void* stream = stream_of(dev);
+    unlocked([&] {
+      return zero_embedding_backward(ptr(dy), stride, static_cast<zero_dtype>(from), ptr(ids), id_bytes, tokens, vocab,
+                                     hidden, scale, accumulate, ptr(out), static_cast<zero_dtype>(type), ptr(ws), need,
+                                     stream);
+    });
+    return wrapped(out);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// linear softmax cross entropy
 
 struct Head {
   Tensor x, w, targets;
@@ -669,6 +804,10 @@ PyMethodDef g_methods[] = {
     {"expert_dispatch_backward", fast(expert_dispatch_backward), METH_FASTCALL, nullptr},
     {"expert_combine", fast(expert_combine), METH_FASTCALL, nullptr},
     {"expert_combine_backward", fast(expert_combine_backward), METH_FASTCALL, nullptr},
+    {"expert_route", fast(expert_route), METH_FASTCALL, nullptr},
+    {"expert_route_backward", fast(expert_route_backward), METH_FASTCALL, nullptr},
+    {"embedding", fast(embedding), METH_FASTCALL, nullptr},
+    {"embedding_backward", fast(embedding_backward), METH_FASTCALL, nullptr},
     {"linear_cross_entropy", fast(linear_cross_entropy), METH_FASTCALL, nullptr},
     {"linear_cross_entropy_workspace_bytes", fast(linear_cross_entropy_workspace_bytes), METH_FASTCALL, nullptr},
     {"linear_cross_entropy_backward", fast(linear_cross_entropy_backward), METH_FASTCALL, nullptr},

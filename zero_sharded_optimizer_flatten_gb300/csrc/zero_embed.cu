@@ -1,0 +1,595 @@
+// Token embedding and the gradient of its table. Argument checks, kernels,
+// launches.
+//
+//   y[t] = scale * table[ids[t]], 0 for an id outside [0, vocab)
+//   dtable[v] (+)= scale * sum of dy[t] over the tokens with ids[t] = v
+//
+// Both are bound by bytes: every row is read once and written once.
+//
+// The gradient first puts the tokens in order of their ids, those of one id in
+// their own order (k_embed_sort). The sorted tokens are then cut into chunks of
+// kChunk, whatever ids they have, so that the work is even however often an id
+// occurs (in texts the most frequent are every tenth token); a chunk adds each
+// of its runs of equal ids up in binary32 (k_embed_sums) and writes the row,
+// or, for a run that goes on in another chunk, a partial row, which k_embed_join
+// adds up in order. No atomics: the same call gives the same bits. The rows
+// without tokens are cleared by a kernel before, beside which the sort runs.
+#include <cuda_runtime.h>
+#include <inttypes.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "zero_capi_util.h"
+#include "zero_rows.cuh"
+
+namespace zero {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBuckets = 128;       // CTAs of the sort, while an SM's counters hold vocab / kBuckets ids
+constexpr int kMinorMost = 1024;
+constexpr int kBucketsMost = 4096;  // vocab up to 2^22
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortAhead = 8;
+constexpr int kChunk = 32;
+constexpr int kAhead = 8;  // rows in flight
+
+struct IdsArgs {
+  const void* ids;
+  int64_t tokens;
+  int32_t id_bytes, vocab;
+};
+__device__ __forceinline__ int load_id(const IdsArgs& a, int64_t t) {
+  if (a.id_bytes == 4) {
+    const int v = static_cast<const int*>(a.ids)[t];
+    return v >= 0 && v < a.vocab ? v : -1;
+  }
+  const long long v = static_cast<const long long*>(a.ids)[t];
+  return v >= 0 && v < a.vocab ? static_cast<int>(v) : -1;
+}
+
+// ---------------------------------------------------------------------------
+// lookup
+
+struct LookupArgs {
+  IdsArgs ids;
+  const void* table;
+  void* y;
+  int64_t stride;
+  int32_t hidden, lanes;
+  float scale;
+};
+
+// A group of 8 to 256 lanes a token, octet by octet, two at a time.
+template <class T, class Y>
+__global__ void __launch_bounds__(kThreads) k_embed(const LookupArgs a) {
+  constexpr int kParts = 2;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / a.lanes) + threadIdx.x / a.lanes;
+  if (t >= a.ids.tokens) return;
+  const int lane = threadIdx.x % a.lanes, round = 8 * a.lanes;
+  const int id = load_id(a.ids, t);
+  Y* y = static_cast<Y*>(a.y) + t * a.hidden;
+  const T* row = static_cast<const T*>(a.table) + id * a.stride;
+  for (int c0 = 8 * lane; c0 < a.hidden; c0 += kParts * round) {
+    Octet<T> v[kParts];
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      if (id >= 0 && c0 + q * round < a.hidden) v[q].load(row + c0 + q * round);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      if (c0 + q * round < a.hidden) {
+        float f[8] = {};
+        if (id >= 0) {
+          v[q].widen(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= a.scale;
+        }
+        Elem<Y>::store8(y + c0 + q * round, f);
+      }
+  }
+}
+
+// Rows that start anywhere: single columns, eight a thread.
+template <class T, class Y>
+__global__ void __launch_bounds__(kThreads) k_embed_any(const LookupArgs a) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / a.lanes) + threadIdx.x / a.lanes;
+  if (t >= a.ids.tokens) return;
+  const int lane = threadIdx.x % a.lanes;
+  const int id = load_id(a.ids, t);
+  Y* y = static_cast<Y*>(a.y) + t * a.hidden;
+  const T* row = static_cast<const T*>(a.table) + id * a.stride;
+  for (int c0 = lane; c0 < a.hidden; c0 += 8 * a.lanes) {
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (id >= 0 && c0 + i * a.lanes < a.hidden) v[i] = row[c0 + i * a.lanes];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i * a.lanes < a.hidden)
+        y[c0 + i * a.lanes] = Elem<Y>::narrow(id >= 0 ? Elem<T>::widen(v[i]) * a.scale : 0.f);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// gradient
+
+struct SortArgs {
+  IdsArgs ids;
+  int32_t bits, minors;  // id = minor << bits | bucket
+  int2* order;           // sorted: token and id
+  int32_t* starts;       // [buckets * minors + 1]: first place of each id, by (bucket, minor)
+};
+
+// One CTA a bucket of ids (id mod the number of CTAs: the frequent ids, which
+// have small numbers, fall into different ones). Every CTA looks at all ids:
+// counts its own, warp by warp, and those of the buckets before it; then goes
+// through them again and gives out places, which are in the tokens' order
+// because a warp's tokens are consecutive. Nothing passes between CTAs, so it is
+// one launch and no order depends on timing; what it costs is one read of the
+// ids from L2 for each bucket.
+__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
+  extern __shared__ int count[];  // [kSortWarps][minors], then first places; [minors]: the ids' first places
+  __shared__ int below[kSortWarps], scan[kSortWarps];
+  let_next_start();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bucket = blockIdx.x, mask = (1 << a.bits) - 1, minors = a.minors;
+  int* first = count + kSortWarps * minors;
+  for (int i = threadIdx.x; i < kSortWarps * minors; i += kSortThreads) count[i] = 0;
+  __syncthreads();
+  const int64_t size = ((a.ids.tokens + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+  const int64_t lo = min(a.ids.tokens, warp * size), hi = min(a.ids.tokens, lo + size);
+  int* mine = count + warp * minors;
+  int before = 0;
+  for (int64_t p = lo; p < hi; p += 32 * kSortAhead) {
+    int id[kSortAhead];
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) id[i] = p + 32 * i + lane < hi ? load_id(a.ids, p + 32 * i + lane) : -1;
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) {
+      if (id[i] < 0) continue;
+      const int b = id[i] & mask;
+      before += b < bucket;
+      if (b == bucket) atomicAdd(mine + (id[i] >> a.bits), 1);  // only counted here: no order
+    }
+  }
+  before = __reduce_add_sync(kFull, before);
+  if (lane == 0) below[warp] = before;
+  __syncthreads();
+  before = __reduce_add_sync(kFull, below[lane]);
+  // places of every warp's tokens of an id, and the ids' totals
+  int carry = before;
+  for (int m0 = 0; m0 < minors; m0 += kSortThreads) {
+    const int m = m0 + threadIdx.x;
+    int sum = 0;
+    if (m < minors)
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = count[w * minors + m];
+        count[w * minors + m] = sum;
+        sum += c;
+      }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int at = carry + inc - sum;
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) at += scan[w];
+      carry += scan[w];
+    }
+    if (m < minors) {
+      first[m] = at;
+      a.starts[static_cast<int64_t>(bucket) * minors + m] = at;
+    }
+    __syncthreads();
+  }
+  if (bucket == static_cast<int>(gridDim.x) - 1 && threadIdx.x == 0)
+    a.starts[static_cast<int64_t>(gridDim.x) * minors] = carry;
+  for (int64_t p = lo; p < hi; p += 32 * kSortAhead) {
+    int id[kSortAhead];
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) id[i] = p + 32 * i + lane < hi ? load_id(a.ids, p + 32 * i + lane) : -1;
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) {
+      const bool own = id[i] >= 0 && (id[i] & mask) == bucket;
+      const unsigned owners = __ballot_sync(kFull, own);
+      if (own) {
+        const int m = id[i] >> a.bits;
+        const unsigned same = __match_any_sync(owners, m);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        const int at = first[m] + mine[m] + rank;
+        __syncwarp(owners);
+        if (rank == 0) mine[m] += __popc(same);
+        a.order[at] = make_int2(static_cast<int>(p + 32 * i + lane), id[i]);
+      }
+      __syncwarp();
+    }
+  }
+  // the clearing kernel ran beside this one: what follows this grid follows both
+  wait_for_previous();
+}
+
+// Rows cleared by 16 bytes, and the bytes at the ends.
+__global__ void __launch_bounds__(kThreads) k_embed_clear(char* p, int64_t head, int64_t words, int64_t tail) {
+  let_next_start();
+  uint4* w = reinterpret_cast<uint4*>(p + head);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < words; i += step)
+    w[i] = make_uint4(0, 0, 0, 0);
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    if (threadIdx.x < head) p[threadIdx.x] = 0;
+    if (threadIdx.x < tail) p[head + words * 16 + threadIdx.x] = 0;
+  }
+}
+
+struct SumArgs {
+  const int2* order;
+  const int32_t* starts;
+  int32_t total_at;      // starts[total_at]: sorted tokens
+  int32_t bits, minors;
+  const void* dy;
+  int64_t dy_stride, part_stride;
+  void* out;
+  float* part;           // [chunks][2][part_stride]: of a run from an earlier chunk, of a run that goes on
+  int32_t hidden, out_type, add, vocab;
+  int64_t tokens;
+  float scale;
+};
+
+// What a thread holds of a row: an octet, or eight columns `step` apart.
+template <class D, bool VEC>
+struct Columns {
+  int c0, step, hidden;
+  __device__ __forceinline__ bool any() const { return c0 < hidden; }
+  __device__ __forceinline__ int at(int i) const { return c0 + (VEC ? i : i * step); }
+  __device__ __forceinline__ bool in(int i) const { return VEC || at(i) < hidden; }
+  template <class P>
+  __device__ __forceinline__ void load(const P* row, float (&v)[8]) const {
+    if constexpr (VEC) {
+      Octet<P> o;
+      o.load(row + c0);
+      o.widen(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = in(i) ? Elem<P>::widen(row[at(i)]) : 0.f;
+    }
+  }
+  template <class P>
+  __device__ __forceinline__ void store(P* row, const float (&v)[8]) const {
+    if constexpr (VEC) {
+      Elem<P>::store8(row + c0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (in(i)) row[at(i)] = Elem<P>::narrow(v[i]);
+    }
+  }
+  // scale * sum, on top of what is there
+  template <class P>
+  __device__ __forceinline__ void finish(P* row, const float (&sum)[8], float scale, bool add) const {
+    float v[8] = {};
+    if (add) load(row, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(scale, sum[i], v[i]);
+    store(row, v);
+  }
+  __device__ __forceinline__ void finish_any(const SumArgs& a, int id, const float (&sum)[8]) const {
+    const int64_t row = static_cast<int64_t>(id) * a.hidden;
+    if (a.out_type == ZERO_FP32)
+      finish(static_cast<float*>(a.out) + row, sum, a.scale, a.add);
+    else if (a.out_type == ZERO_BF16)
+      finish(static_cast<__nv_bfloat16*>(a.out) + row, sum, a.scale, a.add);
+    else
+      finish(static_cast<__half*>(a.out) + row, sum, a.scale, a.add);
+  }
+};
+
+// A chunk's sums. The rows are loaded kAhead at a time, whichever runs they
+// belong to; the runs' ends are the same for every thread.
+template <class D, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_embed_sums(const SumArgs a) {
+  __shared__ int2 item[kChunk + 2];
+  let_next_start();
+  wait_for_previous();
+  const int total = a.starts[a.total_at];
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * kChunk;
+  if (lo >= total) return;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), total - lo));
+  for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
+    const int64_t p = lo + i - 1;
+    item[i] = p >= 0 && p < total ? a.order[p] : make_int2(-1, -1);
+  }
+  __syncthreads();
+  const Columns<D, VEC> cols = {VEC ? static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) * 8
+                                    : static_cast<int>(blockIdx.y * blockDim.x * 8 + threadIdx.x),
+                                static_cast<int>(blockDim.x), a.hidden};
+  if (!cols.any()) return;
+  const D* dy = static_cast<const D*>(a.dy);
+  float sum[8] = {};
+  int run_from = 0;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float v[kAhead][8];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k < n) cols.load(dy + item[i0 + k + 1].x * a.dy_stride, v[k]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k;
+      if (i >= n) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[k][j];
+      const int id = item[i + 1].y;
+      const bool goes_on = item[i + 2].y == id;
+      if (goes_on && i + 1 < n) continue;
+      const bool from_before = run_from == 0 && item[0].y == id;
+      if (from_before || goes_on)
+        cols.store(a.part + (blockIdx.x * INT64_C(2) + (from_before ? 0 : 1)) * a.part_stride, sum);
+      else
+        cols.finish_any(a, id, sum);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+      run_from = i + 1;
+    }
+  }
+}
+
+// Runs over several chunks: the chunk in which one begins adds its parts up,
+// kJoinGroups threads a column, each a contiguous share of the chunks.
+constexpr int kJoinLanes = 32, kJoinGroups = kThreads / kJoinLanes;
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) k_embed_join(const SumArgs a) {
+  __shared__ float part[kJoinGroups][8][kJoinLanes];
+  wait_for_previous();
+  const int total = a.starts[a.total_at];
+  const int64_t chunk = blockIdx.x, hi = (chunk + 1) * kChunk;
+  if (hi >= total) return;
+  const int id = a.order[hi - 1].y;
+  if (a.order[hi].y != id) return;
+  const int64_t at = static_cast<int64_t>(id & ((1 << a.bits) - 1)) * a.minors + (id >> a.bits);
+  const int begin = a.starts[at], end = a.starts[at + 1];
+  if (begin < chunk * kChunk) return;  // begins in an earlier chunk
+  const int parts = static_cast<int>((end - 1) / kChunk - chunk);  // chunks after this one
+  const int lane = threadIdx.x % kJoinLanes, g = threadIdx.x / kJoinLanes;
+  const Columns<float, VEC> cols = {VEC ? static_cast<int>(blockIdx.y * kJoinLanes + lane) * 8
+                                        : static_cast<int>(blockIdx.y * kJoinLanes * 8 + lane),
+                                    kJoinLanes, a.hidden};
+  float sum[8] = {};
+  if (cols.any()) {
+    if (g == 0) cols.load(a.part + (chunk * 2 + 1) * a.part_stride, sum);
+    const int each = (parts + kJoinGroups - 1) / kJoinGroups;
+#pragma unroll 4
+    for (int k = g * each; k < min(parts, (g + 1) * each); ++k) {
+      float v[8];
+      cols.load(a.part + (chunk + 1 + k) * 2 * a.part_stride, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[g][j][lane] = sum[j];
+  __syncthreads();
+  if (g == 0 && cols.any()) {
+    for (int k = 1; k < kJoinGroups; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += part[k][j][lane];
+    cols.finish_any(a, id, sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+template <class... P>
+cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, bool early, cudaStream_t s, P... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
+  if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
+template <class T, class Y>
+cudaError_t launch_lookup(LookupArgs& a, bool vec, cudaStream_t s) {
+  a.lanes = 8;
+  while (a.lanes < kThreads && static_cast<int64_t>(a.lanes) * 8 < a.hidden) a.lanes *= 2;
+  const int64_t per_cta = kThreads / a.lanes, grid = (a.ids.tokens + per_cta - 1) / per_cta;
+  return launch(vec ? &k_embed<T, Y> : &k_embed_any<T, Y>, dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s,
+                static_cast<const LookupArgs>(a));
+}
+
+// The workspace of the gradient.
+struct Layout {
+  int bits, minors, buckets;
+  int64_t chunks, part_stride, order, starts, part, bytes;
+  Layout(int64_t tokens, int64_t vocab, int64_t hidden) {
+    buckets = kBuckets, bits = 7;
+    while ((vocab + buckets - 1) / buckets > kMinorMost) buckets *= 2, ++bits;
+    minors = static_cast<int>((vocab + buckets - 1) / buckets);
+    chunks = (tokens + kChunk - 1) / kChunk;
+    part_stride = (hidden + 7) / 8 * 8;
+    auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    order = 0;
+    starts = up(tokens * 8);
+    part = starts + up((static_cast<int64_t>(buckets) * minors + 1) * 4);
+    bytes = part + chunks * 2 * part_stride * 4;
+  }
+  int sort_smem() const { return (kSortWarps + 1) * minors * 4; }
+};
+constexpr int kSortSmemMost = (kSortWarps + 1) * kMinorMost * 4;
+
+template <class D, bool VEC>
+cudaError_t launch_sums(const SumArgs& a, int64_t chunks, cudaStream_t s) {
+  const int units = static_cast<int>((a.hidden + 7) / 8);  // threads that a row takes
+  // CTAs of as many warps as a row's columns fill, evenly when it takes several
+  const int ctas = (units + kThreads - 1) / kThreads;
+  const int threads = ((units + ctas - 1) / ctas + 31) / 32 * 32;
+  cudaError_t e = launch(&k_embed_sums<D, VEC>, dim3(static_cast<unsigned>(chunks), ctas), threads, 0, true, s, a);
+  if (e == cudaSuccess && chunks > 1)
+    e = launch(&k_embed_join<VEC>, dim3(static_cast<unsigned>(chunks - 1), (units + kJoinLanes - 1) / kJoinLanes),
+               kThreads, 0, true, s, a);
+  return e;
+}
+
+zero_status check_sizes(const char* fn, int64_t tokens, int64_t vocab, int64_t hidden) {
+  if (tokens < 0 || tokens > INT64_C(1) << 28)
+    return fail(ZERO_ERR_INVALID, "%s: tokens must lie in [0, 2^28]", fn);
+  if (vocab < 1 || vocab > static_cast<int64_t>(kBucketsMost) * kMinorMost)
+    return fail(ZERO_ERR_INVALID, "%s: vocab must lie in [1, 2^22]", fn);
+  if (hidden < 1 || hidden > INT64_C(1) << 20) return fail(ZERO_ERR_INVALID, "%s: hidden must lie in [1, 2^20]", fn);
+  return ZERO_OK;
+}
+
+zero_status check_ptr(const char* fn, const char* what, const void* p, int bytes, bool needed) {
+  if (needed && !p) return fail(ZERO_ERR_INVALID, "%s: %s is NULL", fn, what);
+  if (!aligned_to(p, bytes)) return fail(ZERO_ERR_ALIGN, "%s: %s is not aligned to %d bytes", fn, what, bytes);
+  return ZERO_OK;
+}
+
+zero_status check_common(const char* fn, int32_t id_bytes, double scale, int64_t stride, int64_t hidden) {
+  if (id_bytes != 4 && id_bytes != 8) return fail(ZERO_ERR_INVALID, "%s: id_bytes must be 4 or 8", fn);
+  if (!std::isfinite(scale) || !std::isfinite(static_cast<float>(scale)))
+    return fail(ZERO_ERR_INVALID, "%s: scale must be finite", fn);
+  if (stride < hidden || stride > INT64_C(1) << 36)
+    return fail(ZERO_ERR_INVALID, "%s: strides must be at least hidden", fn);
+  return ZERO_OK;
+}
+
+zero_status pending_error(const char* fn) {
+  const cudaError_t pending = cudaGetLastError();
+  if (pending != cudaSuccess)
+    return fail(ZERO_ERR_CUDA, "%s: pending CUDA error: %s", fn, cudaGetErrorString(pending));
+  return ZERO_OK;
+}
+
+#define EMBED_TRY(x)                \
+  do {                              \
+    const zero_status st_ = (x);    \
+    if (st_ != ZERO_OK) return st_; \
+  } while (0)
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" zero_status zero_embedding(const void* ids, int32_t id_bytes, int64_t tokens, const void* table,
+                                      int64_t table_stride, zero_dtype table_dtype, int64_t vocab, int64_t hidden,
+                                      double scale, void* y, zero_dtype y_dtype, void* stream) {
+  const char* fn = "zero_embedding";
+  clear_error();
+  NvtxRange range(fn);
+  EMBED_TRY(check_sizes(fn, tokens, vocab, hidden));
+  EMBED_TRY(check_common(fn, id_bytes, scale, table_stride, hidden));
+  if (!known_type(table_dtype)) return fail(ZERO_ERR_INVALID, "%s: unknown table_dtype", fn);
+  if (y_dtype != table_dtype && y_dtype != ZERO_FP32)
+    return fail(ZERO_ERR_INVALID, "%s: y_dtype must be table_dtype or ZERO_FP32", fn);
+  const bool any = tokens > 0;
+  EMBED_TRY(check_ptr(fn, "ids", ids, id_bytes, any));
+  EMBED_TRY(check_ptr(fn, "table", table, type_bytes(table_dtype), any));
+  EMBED_TRY(check_ptr(fn, "y", y, type_bytes(y_dtype), any));
+  if (!any) return ZERO_OK;
+  const int e = type_bytes(table_dtype);
+  EMBED_TRY(check_overlaps(fn, {Extent::block("y", y, tokens * hidden * type_bytes(y_dtype))},
+                           {{"table", table, vocab, table_stride * e, hidden * e},
+                            Extent::block("ids", ids, tokens * id_bytes)}));
+  EMBED_TRY(pending_error(fn));
+  LookupArgs a = {{ids, tokens, id_bytes, static_cast<int32_t>(vocab)}, table, y, table_stride,
+                  static_cast<int32_t>(hidden), 0, static_cast<float>(scale)};
+  const bool vec = hidden % 8 == 0 && table_stride * e % 16 == 0 && aligned_to(table, 16) && aligned_to(y, 16);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool wide = y_dtype == ZERO_FP32;
+  const cudaError_t r = table_dtype == ZERO_FP32   ? launch_lookup<float, float>(a, vec, s)
+                        : table_dtype == ZERO_BF16 ? (wide ? launch_lookup<__nv_bfloat16, float>(a, vec, s)
+                                                           : launch_lookup<__nv_bfloat16, __nv_bfloat16>(a, vec, s))
+                        : wide                     ? launch_lookup<__half, float>(a, vec, s)
+                                                   : launch_lookup<__half, __half>(a, vec, s);
+  if (r != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(r));
+  return ZERO_OK;
+}
+
+extern "C" zero_status zero_embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t hidden, int64_t* bytes) {
+  const char* fn = "zero_embedding_workspace_bytes";
+  clear_error();
+  if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
+  EMBED_TRY(check_sizes(fn, tokens, vocab, hidden));
+  *bytes = Layout(tokens, vocab, hidden).bytes;
+  return ZERO_OK;
+}
+
+extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride, zero_dtype dy_dtype,
+                                               const void* ids, int32_t id_bytes, int64_t tokens, int64_t vocab,
+                                               int64_t hidden, double scale, int32_t accumulate, void* dtable,
+                                               zero_dtype dtable_dtype, void* workspace, int64_t workspace_bytes,
+                                               void* stream) {
+  const char* fn = "zero_embedding_backward";
+  clear_error();
+  NvtxRange range(fn);
+  EMBED_TRY(check_sizes(fn, tokens, vocab, hidden));
+  EMBED_TRY(check_common(fn, id_bytes, scale, dy_stride, hidden));
+  if (!known_type(dy_dtype) || !known_type(dtable_dtype)) return fail(ZERO_ERR_INVALID, "%s: unknown dtype", fn);
+  if (dy_dtype != dtable_dtype && dy_dtype != ZERO_FP32 && dtable_dtype != ZERO_FP32)
+    return fail(ZERO_ERR_INVALID, "%s: dy and dtable must have one type, or one of them ZERO_FP32", fn);
+  const bool any = tokens > 0;
+  const Layout at(tokens, vocab, hidden);
+  EMBED_TRY(check_ptr(fn, "dy", dy, type_bytes(dy_dtype), any));
+  EMBED_TRY(check_ptr(fn, "ids", ids, id_bytes, any));
+  EMBED_TRY(check_ptr(fn, "dtable", dtable, type_bytes(dtable_dtype), true));
+  EMBED_TRY(check_ptr(fn, "workspace", workspace, 256, any));
+  if (any && workspace_bytes < at.bytes)
+    return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes,
+                at.bytes);
+  const int e = type_bytes(dy_dtype);
+  const int64_t out_bytes = vocab * hidden * type_bytes(dtable_dtype);
+  EMBED_TRY(check_overlaps(
+      fn, {Extent::block("dtable", dtable, out_bytes), Extent::block("workspace", any ? workspace : nullptr, at.bytes)},
+      {{"dy", dy, tokens, dy_stride * e, hidden * e}, Extent::block("ids", ids, tokens * id_bytes)}));
+  EMBED_TRY(pending_error(fn));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t r = cudaSuccess;
+  if (!accumulate) {
+    const int64_t head = std::min<int64_t>(out_bytes, (16 - (reinterpret_cast<uintptr_t>(dtable) & 15)) & 15);
+    const int64_t words = (out_bytes - head) / 16, tail = out_bytes - head - words * 16;
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kSMs * 4, (words + kThreads - 1) / kThreads));
+    r = launch(&k_embed_clear, dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s, static_cast<char*>(dtable),
+               head, words, tail);
+  }
+  if (!any || r != cudaSuccess) {
+    if (r != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(r));
+    return ZERO_OK;
+  }
+  char* ws = static_cast<char*>(workspace);
+  const SortArgs sort = {{ids, tokens, id_bytes, static_cast<int32_t>(vocab)}, at.bits, at.minors,
+                         reinterpret_cast<int2*>(ws + at.order), reinterpret_cast<int32_t*>(ws + at.starts)};
+  static KernelFacts facts;
+  r = facts.allow(reinterpret_cast<const void*>(&k_embed_sort), kSortSmemMost, kSortSmemMost);
+  if (r == cudaSuccess)
+    r = launch(&k_embed_sort, dim3(at.buckets), kSortThreads, at.sort_smem(), !accumulate, s, sort);
+  SumArgs a = {};
+  a.order = sort.order, a.starts = sort.starts, a.total_at = at.buckets * at.minors;
+  a.bits = at.bits, a.minors = at.minors, a.dy = dy, a.dy_stride = dy_stride, a.part_stride = at.part_stride;
+  a.out = dtable, a.part = reinterpret_cast<float*>(ws + at.part), a.hidden = static_cast<int32_t>(hidden);
+  a.out_type = dtable_dtype, a.add = accumulate != 0, a.vocab = static_cast<int32_t>(vocab), a.tokens = tokens;
+  a.scale = static_cast<float>(scale);
+  const bool vec = hidden % 8 == 0 && dy_stride * e % 16 == 0 && aligned_to(dy, 16) && aligned_to(dtable, 16);
+  if (r == cudaSuccess)
+    r = dy_dtype == ZERO_FP32   ? (vec ? launch_sums<float, true>(a, at.chunks, s)
+                                       : launch_sums<float, false>(a, at.chunks, s))
+        : dy_dtype == ZERO_BF16 ? (vec ? launch_sums<__nv_bfloat16, true>(a, at.chunks, s)
+                                       : launch_sums<__nv_bfloat16, false>(a, at.chunks, s))
+        : vec                   ? launch_sums<__half, true>(a, at.chunks, s)
+                                : launch_sums<__half, false>(a, at.chunks, s);
+  if (r != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(r));
+  return ZERO_OK;
+}

@@ -1,0 +1,485 @@
+// The router of sparse experts: probabilities, choices, counts and the losses
+// that keep the experts in balance, and the gradient. Argument checks, kernels,
+// launches.
+//
+//   p = softmax(z) over the experts, lse = log sum exp z
+//   choices: the topk largest z of a token, of equal ones the lowest expert
+//     first; -inf is never chosen (id -1, weight 0)
+//   weights: p of the choices, or those divided by their sum (normalize)
+//   counts_e: how often expert e was chosen; n: tokens with any z above -inf
+//   balance = E / (topk n^2) sum_e counts_e sum_t p_te,  zloss = sum_t lse_t^2 / n
+//   dz_te = p_te (a_te - sum_f p_tf a_tf) + 2 d_zloss / n lse_t p_te (+ what the
+//     normalised weights add), a_te = d_balance E counts_e / (topk n^2), plus
+//     dweights of the choices
+//
+// A warp has a token, each lane VPT neighbouring experts in registers; the
+// choices come one after the other as the warp's largest value. What bounds
+// large calls is issue slots: topk rounds of some 30 instructions a token. Each
+// CTA leaves its counts and sums of p in the workspace, added up in order by
+// k_route_finish, so the same call gives the same bits.
+#include <cuda_runtime.h>
+#include <inttypes.h>
+
+#include <algorithm>
+
+#include "zero_capi_util.h"
+#include "zero_rows.cuh"
+#include "zero_tensor_core.cuh"
+
+namespace zero {
+namespace {
+
+constexpr int kExpertsMost = 1024, kTopkMost = 32;
+constexpr int kWarps = 32, kThreads = 32 * kWarps;
+constexpr int kCtasMost = kSMs;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct RouteArgs {
+  const void* z;
+  int64_t tokens, stride;
+  int32_t experts, topk, normalize, vec;
+  int32_t* ids;
+  float* weights;
+  int32_t* counts;
+  float* losses;
+  float* stats;      // [tokens + 1]: lse, n
+  // [CTAs][experts] each, then [CTAs][2]: n and the sum of lse^2
+  int32_t* part_counts;
+  float* part_sums;
+  float* part_ends;
+  int32_t ctas;
+  // gradient
+  const float *d_weights, *d_losses;
+  void* dz;
+};
+
+// Values in order as unsigned numbers, +-0 alike, NaN last; kNone: -inf or less.
+constexpr uint32_t kNone = 0x007fffffu, kNan = 0xffffffffu;
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return v != v ? kNan : k;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  if (k == kNan) return __uint_as_float(0x7fffffffu);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// A lane's VPT values of a row, `fill` past its end.
+template <class T, int VPT>
+__device__ __forceinline__ void load_row(const T* row, int lane, int experts, bool vec, float fill, float (&v)[VPT]) {
+  if constexpr (VPT * sizeof(T) >= 16) {
+    if (vec) {
+      constexpr int kWords = VPT * sizeof(T) / 16, kEach = 16 / sizeof(T);
+      uint4 w[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(row + lane * VPT)[i];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if constexpr (sizeof(T) == 4)
+            v[i * kEach + j] = __uint_as_float(x[j]);
+          else
+            Elem<T>::unpack(x[j], v[i * kEach + 2 * j], v[i * kEach + 2 * j + 1]);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    v[j] = lane * VPT + j < experts ? Elem<T>::widen(row[lane * VPT + j]) : fill;
+}
+
+template <class T, int VPT>
+__global__ void __launch_bounds__(kThreads, VPT <= 8 ? 2 : 1) k_route(const RouteArgs a) {
+  extern __shared__ int smem[];  // [experts] counts, [kWarps][experts] sums of p
+  __shared__ float ends[kWarps][2];
+  let_next_start();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, K = a.topk;
+  float* sums = reinterpret_cast<float*>(smem + E);
+  for (int e = threadIdx.x; e < E; e += kThreads) smem[e] = 0;
+  __syncthreads();
+  float total[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) total[j] = 0.f;
+  float n = 0.f, squares = 0.f;
+  const T* z = static_cast<const T*>(a.z);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.tokens; t += step) {
+    float v[VPT];
+    load_row<T, VPT>(z + t * a.stride, lane, E, a.vec, -INFINITY, v);
+    uint32_t key[VPT];
+    uint32_t most = 0;
+    int where = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      key[j] = key_of(v[j]);
+      if (key[j] > most) most = key[j], where = j;  // the first of equal ones
+    }
+    uint32_t chosen_key = 0;
+    int chosen = -1;
+    float top = 0.f;
+    for (int k = 0; k < K; ++k) {
+      const uint32_t best = __reduce_max_sync(kFull, most);
+      if (k == 0) top = best > kNone ? value_of(best) : 0.f;
+      if (best <= kNone) break;  // the same for all lanes
+      const int owner = __ffs(__ballot_sync(kFull, most == best)) - 1;
+      const int e = __shfl_sync(kFull, lane * VPT + where, owner);
+      if (lane == k) chosen = e, chosen_key = best;
+      if (lane == owner) {
+        most = 0;
+        int next = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          if (j == where) key[j] = 0;
+          if (key[j] > most) most = key[j], next = j;
+        }
+        where = next;
+      }
+    }
+    const bool any = __shfl_sync(kFull, chosen, 0) >= 0;
+    const float top2 = top * kLog2e;
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      v[j] = any ? tc::exp2_of(fmaf(v[j], kLog2e, -top2)) : 0.f;
+      s += v[j];
+    }
+    s = warp_all_sum(s);
+    const float inv = any ? 1.f / s : 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) total[j] = fmaf(v[j], inv, total[j]);
+    const float lse = any ? top + log2f(s) * kLn2 : 0.f;
+    if (any) n += 1.f, squares = fmaf(lse, lse, squares);
+    float w = chosen >= 0 ? tc::exp2_of(fmaf(value_of(chosen_key), kLog2e, -top2)) : 0.f;
+    if (a.normalize) {
+      const float all = warp_all_sum(w);
+      w = any ? w / all : 0.f;
+    } else {
+      w *= inv;
+    }
+    if (lane < K) {
+      a.ids[t * K + lane] = chosen;
+      a.weights[t * K + lane] = w;
+      if (chosen >= 0) atomicAdd(smem + chosen, 1);
+    }
+    if (lane == 0) a.stats[t] = lse;
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    if (lane * VPT + j < E) sums[warp * E + lane * VPT + j] = total[j];
+  if (lane == 0) ends[warp][0] = n, ends[warp][1] = squares;
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    float s = 0.f;
+    for (int w = 0; w < kWarps; ++w) s += sums[w * E + e];
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * E + e;
+    a.part_counts[at] = smem[e];
+    a.part_sums[at] = s;
+  }
+  if (threadIdx.x < 2) {
+    float s = 0.f;
+    for (int w = 0; w < kWarps; ++w) s += ends[w][threadIdx.x];
+    a.part_ends[blockIdx.x * 2 + threadIdx.x] = s;
+  }
+}
+
+// The CTAs' counts and sums added up, in order; one CTA: groups of threads a
+// share of the CTAs, then the groups one after the other.
+__global__ void __launch_bounds__(kThreads) k_route_finish(const RouteArgs a) {
+  __shared__ int counts[kThreads];
+  __shared__ float sums[kThreads];
+  __shared__ float part[kWarps];
+  __shared__ float ends[2];
+  wait_for_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
+  if (warp < 2) {  // n and the sum of squares
+    float s = 0.f;
+    for (int c = lane; c < a.ctas; c += 32) s += a.part_ends[c * 2 + warp];
+    s = warp_all_sum(s);
+    if (lane == 0) ends[warp] = s;
+  }
+  const int groups = kThreads / E;  // at least one
+  const int g = threadIdx.x / E, e = threadIdx.x - g * E;
+  int count = 0;
+  float sum = 0.f;
+  if (g < groups) {
+    const int each = (a.ctas + groups - 1) / groups;
+#pragma unroll 8
+    for (int c = g * each; c < min(a.ctas, (g + 1) * each); ++c) {
+      count += a.part_counts[static_cast<int64_t>(c) * E + e];
+      sum += a.part_sums[static_cast<int64_t>(c) * E + e];
+    }
+  }
+  counts[threadIdx.x] = count, sums[threadIdx.x] = sum;
+  __syncthreads();
+  float s = 0.f;
+  if (threadIdx.x < E) {
+    for (int k = 1; k < groups; ++k) count += counts[k * E + e], sum += sums[k * E + e];
+    a.counts[e] = count;
+    s = static_cast<float>(count) * sum;
+  }
+  s = warp_all_sum(s);
+  if (lane == 0) part[warp] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.f;
+    for (int w = 0; w < kWarps; ++w) s += part[w];
+    const float n = fmaxf(ends[0], 1.f);
+    a.losses[0] = s * (static_cast<float>(E) / static_cast<float>(a.topk)) / n / n;
+    a.losses[1] = ends[1] / n;
+    a.stats[a.tokens] = ends[0];
+  }
+}
+
+template <class T, int VPT>
+__global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a) {
+  extern __shared__ float direct[];  // [warps][32 * VPT]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, K = a.topk;
+  float* mine = direct + warp * 32 * VPT;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) mine[lane * VPT + j] = 0.f;
+  __syncwarp();
+  const float n = fmaxf(a.stats[a.tokens], 1.f);
+  const float per_count = a.d_losses ? a.d_losses[0] * (static_cast<float>(E) / static_cast<float>(K)) / n / n : 0.f;
+  const float per_lse = a.d_losses ? 2.f * a.d_losses[1] / n : 0.f;
+  float load[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    load[j] = lane * VPT + j < E ? per_count * static_cast<float>(a.counts[lane * VPT + j]) : 0.f;
+  const T* z = static_cast<const T*>(a.z);
+  T* dz = static_cast<T*>(a.dz);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp; t < a.tokens; t += step) {
+    float v[VPT];
+    load_row<T, VPT>(z + t * a.stride, lane, E, a.vec, -INFINITY, v);
+    const float lse = a.stats[t], lse2 = lse * kLog2e;
+    int id = -1;
+    float w = 0.f, d = 0.f;
+    if (lane < K) {
+      id = a.ids[t * K + lane];
+      w = a.weights[t * K + lane];
+      if (a.d_weights) d = a.d_weights[t * K + lane];
+    }
+    if (id < 0 || id >= E) id = -1, w = 0.f, d = 0.f;
+    const bool any = __shfl_sync(kFull, id, 0) >= 0;
+    const float wd = warp_all_sum(id >= 0 ? w * d : 0.f);
+    if (id >= 0) mine[id] = a.normalize ? w * (d - wd) : w * d;
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      v[j] = any ? tc::exp2_of(fmaf(v[j], kLog2e, -lse2)) : 0.f;
+      s = fmaf(v[j], load[j], s);
+    }
+    s = warp_all_sum(s);
+    if (!a.normalize) s += wd;
+    const float shift = per_lse * lse - s;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) v[j] = any ? fmaf(v[j], load[j] + shift, mine[lane * VPT + j]) : 0.f;
+    __syncwarp();
+    if (id >= 0) mine[id] = 0.f;
+    T* row = dz + t * E;
+    if constexpr (VPT % 8 == 0) {
+      if (a.vec) {
+#pragma unroll
+        for (int i = 0; i < VPT; i += 8) {
+          const float o[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
+          Elem<T>::store8(row + lane * VPT + i, o);
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (lane * VPT + j < E) row[lane * VPT + j] = Elem<T>::narrow(v[j]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+template <class... P>
+cudaError_t launch(void (*fn)(P...), int64_t grid, int threads, size_t smem, bool early, cudaStream_t s, P... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
+  if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
+int ctas_for(int64_t tokens) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCtasMost, (tokens + kWarps - 1) / kWarps)));
+}
+
+template <class T, int VPT>
+cudaError_t run_route(const RouteArgs& a, bool backward, cudaStream_t s) {
+  if (backward) {
+    constexpr int kWarpsHere = 8;
+    const int64_t grid = std::min<int64_t>(kSMs * 8, (a.tokens + kWarpsHere - 1) / kWarpsHere);
+    static_assert(kWarpsHere * 32 * 32 * 4 <= 48 * 1024, "shared memory without asking");
+    return launch(&k_route_backward<T, VPT>, grid, 32 * kWarpsHere, kWarpsHere * 32 * VPT * 4, false, s, a);
+  }
+  const size_t smem = static_cast<size_t>(kWarps + 1) * a.experts * 4;
+  constexpr int kMost = (kWarps + 1) * 32 * VPT * 4;
+  static KernelFacts facts;
+  cudaError_t e = facts.allow(reinterpret_cast<const void*>(&k_route<T, VPT>), kMost, kMost);
+  if (e == cudaSuccess) e = launch(&k_route<T, VPT>, a.ctas, kThreads, smem, false, s, a);
+  if (e == cudaSuccess) e = launch(&k_route_finish, 1, kThreads, 0, true, s, a);
+  return e;
+}
+
+template <class T>
+cudaError_t run_typed(const RouteArgs& a, bool backward, cudaStream_t s) {
+  const int each = (a.experts + 31) / 32;
+  return each <= 1    ? run_route<T, 1>(a, backward, s)
+         : each <= 2  ? run_route<T, 2>(a, backward, s)
+         : each <= 4  ? run_route<T, 4>(a, backward, s)
+         : each <= 8  ? run_route<T, 8>(a, backward, s)
+         : each <= 16 ? run_route<T, 16>(a, backward, s)
+                      : run_route<T, 32>(a, backward, s);
+}
+
+// Rows of exactly a power of two times 32 experts on 16-byte boundaries.
+bool wide_rows(int experts, int64_t stride, int bytes, const void* z, const void* dz) {
+  const int each = experts / 32;
+  return experts % 32 == 0 && (each & (each - 1)) == 0 && each * bytes >= 16 && stride * bytes % 16 == 0 &&
+         aligned_to(z, 16) && aligned_to(dz, 16);
+}
+
+zero_status check_shape(const char* fn, int64_t tokens, int64_t stride, int32_t experts, int32_t topk, int dtype) {
+  if (tokens < 0 || tokens > INT64_C(1) << 24)
+    return fail(ZERO_ERR_INVALID, "%s: tokens must lie in [0, 2^24]", fn);
+  if (experts < 1 || experts > kExpertsMost)
+    return fail(ZERO_ERR_INVALID, "%s: n_experts must lie in [1, %d]", fn, kExpertsMost);
+  if (topk < 1 || topk > experts || topk > kTopkMost)
+    return fail(ZERO_ERR_INVALID, "%s: topk must lie in [1, min(n_experts, %d)]", fn, kTopkMost);
+  if (!known_type(dtype)) return fail(ZERO_ERR_INVALID, "%s: unknown dtype", fn);
+  if (stride < experts || stride > INT64_C(1) << 36)
+    return fail(ZERO_ERR_INVALID, "%s: logits_stride must be at least n_experts", fn);
+  return ZERO_OK;
+}
+
+zero_status check_ptr(const char* fn, const char* what, const void* p, int bytes, bool needed) {
+  if (needed && !p) return fail(ZERO_ERR_INVALID, "%s: %s is NULL", fn, what);
+  if (!aligned_to(p, bytes)) return fail(ZERO_ERR_ALIGN, "%s: %s is not aligned to %d bytes", fn, what, bytes);
+  return ZERO_OK;
+}
+
+int64_t workspace_of(int64_t tokens, int32_t experts) {
+  return static_cast<int64_t>(ctas_for(tokens)) * (experts * 2 + 2) * 4;
+}
+
+zero_status run(const char* fn, const RouteArgs& a, int dtype, bool backward, void* stream) {
+  const cudaError_t pending = cudaGetLastError();
+  if (pending != cudaSuccess)
+    return fail(ZERO_ERR_CUDA, "%s: pending CUDA error: %s", fn, cudaGetErrorString(pending));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == ZERO_FP32   ? run_typed<float>(a, backward, s)
+                        : dtype == ZERO_BF16 ? run_typed<__nv_bfloat16>(a, backward, s)
+                                             : run_typed<__half>(a, backward, s);
+  if (e != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return ZERO_OK;
+}
+
+#define ROUTE_TRY(x)                \
+  do {                              \
+    const zero_status st_ = (x);    \
+    if (st_ != ZERO_OK) return st_; \
+  } while (0)
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" zero_status zero_expert_route_workspace_bytes(int64_t tokens, int32_t n_experts, int64_t* bytes) {
+  const char* fn = "zero_expert_route_workspace_bytes";
+  clear_error();
+  if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
+  ROUTE_TRY(check_shape(fn, tokens, n_experts, n_experts, 1, ZERO_FP32));
+  *bytes = workspace_of(tokens, n_experts);
+  return ZERO_OK;
+}
+
+extern "C" zero_status zero_expert_route(const void* logits, int64_t logits_stride, zero_dtype dtype, int64_t tokens,
+                                         int32_t n_experts, int32_t topk, int32_t normalize, int32_t* ids,
+                                         float* weights, int32_t* counts, float* losses, float* stats,
+                                         void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* fn = "zero_expert_route";
+  clear_error();
+  NvtxRange range(fn);
+  ROUTE_TRY(check_shape(fn, tokens, logits_stride, n_experts, topk, dtype));
+  const bool any = tokens > 0;
+  const int b = type_bytes(dtype);
+  ROUTE_TRY(check_ptr(fn, "logits", logits, b, any));
+  ROUTE_TRY(check_ptr(fn, "ids", ids, 4, any));
+  ROUTE_TRY(check_ptr(fn, "weights", weights, 4, any));
+  ROUTE_TRY(check_ptr(fn, "counts", counts, 4, true));
+  ROUTE_TRY(check_ptr(fn, "losses", losses, 4, true));
+  ROUTE_TRY(check_ptr(fn, "stats", stats, 4, true));
+  ROUTE_TRY(check_ptr(fn, "workspace", workspace, 4, true));
+  const int64_t need = workspace_of(tokens, n_experts);
+  if (workspace_bytes < need)
+    return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes, need);
+  ROUTE_TRY(check_overlaps(fn,
+                           {Extent::block("ids", ids, tokens * topk * 4), Extent::block("weights", weights, tokens * topk * 4),
+                            Extent::block("counts", counts, n_experts * INT64_C(4)), Extent::block("losses", losses, 8),
+                            Extent::block("stats", stats, (tokens + 1) * 4), Extent::block("workspace", workspace, need)},
+                           {{"logits", logits, tokens, logits_stride * b, n_experts * INT64_C(1) * b}}));
+  RouteArgs a = {};
+  a.z = logits, a.tokens = tokens, a.stride = logits_stride, a.experts = n_experts, a.topk = topk;
+  a.normalize = normalize != 0, a.vec = wide_rows(n_experts, logits_stride, b, logits, nullptr);
+  a.ids = ids, a.weights = weights, a.counts = counts, a.losses = losses, a.stats = stats;
+  a.ctas = ctas_for(tokens);
+  a.part_counts = static_cast<int32_t*>(workspace);
+  a.part_sums = reinterpret_cast<float*>(a.part_counts + static_cast<int64_t>(a.ctas) * n_experts);
+  a.part_ends = a.part_sums + static_cast<int64_t>(a.ctas) * n_experts;
+  return run(fn, a, dtype, false, stream);
+}
+
+extern "C" zero_status zero_expert_route_backward(const void* logits, int64_t logits_stride, zero_dtype dtype,
+                                                  int64_t tokens, int32_t n_experts, int32_t topk, int32_t normalize,
+                                                  const int32_t* ids, const float* weights, const int32_t* counts,
+                                                  const float* stats, const float* d_weights, const float* d_losses,
+                                                  void* d_logits, void* stream) {
+  const char* fn = "zero_expert_route_backward";
+  clear_error();
+  NvtxRange range(fn);
+  ROUTE_TRY(check_shape(fn, tokens, logits_stride, n_experts, topk, dtype));
+  const bool any = tokens > 0;
+  const int b = type_bytes(dtype);
+  ROUTE_TRY(check_ptr(fn, "logits", logits, b, any));
+  ROUTE_TRY(check_ptr(fn, "ids", ids, 4, any));
+  ROUTE_TRY(check_ptr(fn, "weights", weights, 4, any));
+  ROUTE_TRY(check_ptr(fn, "counts", counts, 4, any));
+  ROUTE_TRY(check_ptr(fn, "stats", stats, 4, any));
+  ROUTE_TRY(check_ptr(fn, "d_weights", d_weights, 4, false));
+  ROUTE_TRY(check_ptr(fn, "d_losses", d_losses, 4, false));
+  ROUTE_TRY(check_ptr(fn, "d_logits", d_logits, b, any));
+  if (!any) return ZERO_OK;
+  ROUTE_TRY(check_overlaps(fn, {Extent::block("d_logits", d_logits, tokens * n_experts * b)},
+                           {{"logits", logits, tokens, logits_stride * b, n_experts * INT64_C(1) * b},
+                            Extent::block("ids", ids, tokens * topk * 4), Extent::block("weights", weights, tokens * topk * 4),
+                            Extent::block("counts", counts, n_experts * INT64_C(4)),
+                            Extent::block("stats", stats, (tokens + 1) * 4),
+                            Extent::block("d_weights", d_weights, tokens * topk * 4),
+                            Extent::block("d_losses", d_losses, 8)}));
+  RouteArgs a = {};
+  a.z = logits, a.tokens = tokens, a.stride = logits_stride, a.experts = n_experts, a.topk = topk;
+  a.normalize = normalize != 0, a.vec = wide_rows(n_experts, logits_stride, b, logits, d_logits);
+  a.ids = const_cast<int32_t*>(ids), a.weights = const_cast<float*>(weights);
+  a.counts = const_cast<int32_t*>(counts), a.stats = const_cast<float*>(stats);
+  a.d_weights = d_weights, a.d_losses = d_losses, a.dz = d_logits;
+  return run(fn, a, dtype, true, stream);
+}

@@ -1,14 +1,16 @@
 """Operators of a training step around the sharded optimizer: gradient norm
-and clipping over many tensors, the block join, the expert permutation.
+and clipping over many tensors, the block join, the expert permutation and the
+router before it, and a language model's two ends, the token embedding and the
+cross entropy over the vocabulary.
 
 The ``zero_*`` functions bind the C calls of include/zero.h under their own
-names (argument checks and marshalling only, those of the join and the experts
-compiled, csrc/train_ops_binding.cpp; the current CUDA stream unless
+names (argument checks and marshalling only, compiled but for the norm's,
+csrc/train_ops_binding.cpp; the current CUDA stream unless
 ``stream`` is given, which then makes the call's buffers too; inputs are the
 caller's to order; no fallback).  ``GradNorm`` and ``ClipGradNorm`` are the
 prepared forms for gradients whose buffers stay in place from step to step.
-``block_join``, ``expert_dispatch`` and ``expert_combine`` are the same calls
-with autograd.
+``block_join``, ``expert_route``, ``expert_dispatch``, ``expert_combine``,
+``embedding`` and ``linear_cross_entropy`` are the same calls with autograd.
 """
 from __future__ import annotations
 
@@ -557,6 +559,139 @@ def expert_combine(ys, weights, order: ExpertOrder):
 
 
 # ----------------------------------------------------------------------------
+# router
+
+
+@dataclasses.dataclass
+class ExpertRoute:
+    """What zero_expert_route leaves on the device: ids [tokens, topk] and
+    counts [n_experts] int32, weights [tokens, topk] and losses [2] (balance
+    and z loss) float32; stats, which the backward call takes."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    counts: torch.Tensor
+    losses: torch.Tensor
+    stats: torch.Tensor
+    normalize: bool
+
+
+def zero_expert_route_workspace_bytes(tokens: int, n_experts: int) -> int:
+    """Device workspace of zero_expert_route."""
+    need = ctypes.c_int64()
+    _check((_lib or _load()).zero_expert_route_workspace_bytes(tokens, n_experts, ctypes.byref(need)))
+    return need.value
+
+
+def zero_expert_route(logits, topk: int, *, normalize: bool = True, workspace=None,
+                      stream=None) -> ExpertRoute:
+    """Every token's experts with their weights, the experts' counts, and the
+    losses that keep them in balance (see zero.h).  logits: [tokens,
+    n_experts]; -inf bars an expert, a row of nothing else leaves its token
+    out (ids -1, weights 0).  workspace: device scratch of
+    zero_expert_route_workspace_bytes (None: allocated here)."""
+    got = _run_on(stream, lambda: (_fast or _load_fast()).expert_route(logits, topk, normalize,
+                                                                       workspace))
+    return ExpertRoute(*got, bool(normalize))
+
+
+def zero_expert_route_backward(logits, route: ExpertRoute, d_weights=None, d_losses=None, *,
+                               out=None, stream=None):
+    """The logits' gradient from those of the weights and of the two losses
+    (float32 [2]), either None: no gradient comes that way."""
+    return _run_on(stream, lambda: (_fast or _load_fast()).expert_route_backward(
+        logits, route.normalize, route.ids, route.weights, route.counts, route.stats, d_weights,
+        d_losses, out))
+
+
+class _ExpertRoute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk, normalize):
+        ctx.set_materialize_grads(False)
+        r = zero_expert_route(logits, topk, normalize=normalize)
+        ctx.normalize = r.normalize
+        ctx.save_for_backward(logits, r.ids, r.weights, r.counts, r.stats)
+        ctx.mark_non_differentiable(r.ids, r.counts)
+        return r.ids, r.weights, r.counts, r.losses
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _ids, d_weights, _counts, d_losses):
+        if d_weights is None and d_losses is None:
+            return None, None, None
+        logits, ids, weights, counts, stats = ctx.saved_tensors
+        route = ExpertRoute(ids, weights, counts, None, stats, ctx.normalize)
+        return zero_expert_route_backward(
+            logits, route, None if d_weights is None else d_weights.contiguous(),
+            None if d_losses is None else d_losses.contiguous()), None, None
+
+
+def expert_route(logits, topk: int, *, normalize: bool = True):
+    """zero_expert_route with autograd (of the weights and the losses): (ids,
+    weights, counts, losses)."""
+    return _ExpertRoute.apply(logits, topk, normalize)
+
+
+# ----------------------------------------------------------------------------
+# token embedding
+
+
+def _code(dtype, what: str) -> int:
+    """A type's number, -1 for None."""
+    if dtype is None:
+        return -1
+    if dtype not in _TYPES:
+        raise TypeError(f"{what}: expected float16, bfloat16 or float32, got {dtype}")
+    return _TYPES[dtype]
+
+
+def zero_embedding(ids, table, *, scale: float = 1.0, dtype=None, out=None, stream=None):
+    """scale * table[ids], zero rows for ids outside the table (see zero.h).
+    ids: [...], int32 or int64; table: [vocab, hidden].  dtype: the table's
+    (None) or float32."""
+    code = _code(dtype, "dtype")
+    return _run_on(stream, lambda: (_fast or _load_fast()).embedding(ids, table, scale, code, out))
+
+
+def zero_embedding_workspace_bytes(tokens: int, vocab: int, hidden: int) -> int:
+    """Device workspace of zero_embedding_backward."""
+    need = ctypes.c_int64()
+    _check((_lib or _load()).zero_embedding_workspace_bytes(tokens, vocab, hidden, ctypes.byref(need)))
+    return need.value
+
+
+def zero_embedding_backward(dy, ids, vocab: int, *, scale: float = 1.0, dtype=None, out=None,
+                            accumulate: bool = False, workspace=None, stream=None):
+    """The table's gradient [vocab, hidden]: scale times the sum of every id's
+    rows of dy (see zero.h).  dtype: dy's (None) or another; a 16-bit one and
+    float32 mix.  accumulate: added to `out`, whose other rows are left
+    alone.  workspace: 256-byte aligned device scratch of
+    zero_embedding_workspace_bytes (None: allocated here)."""
+    code = _code(dtype, "dtype")
+    return _run_on(stream, lambda: (_fast or _load_fast()).embedding_backward(
+        dy, ids, vocab, scale, code, out, accumulate, workspace))
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, table, scale, dtype):
+        ctx.save_for_backward(ids)
+        ctx.scale, ctx.vocab, ctx.dtype = scale, table.shape[0], table.dtype
+        return zero_embedding(ids, table, scale=scale, dtype=dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        ids, = ctx.saved_tensors
+        return None, zero_embedding_backward(_even_rows(dy), ids, ctx.vocab, scale=ctx.scale,
+                                             dtype=ctx.dtype), None, None
+
+
+def embedding(ids, table, *, scale: float = 1.0, dtype=None):
+    """zero_embedding with autograd (of the table)."""
+    return _Embedding.apply(ids, table, scale, dtype)
+
+
+# ----------------------------------------------------------------------------
 # linear softmax cross entropy
 
 _REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
@@ -603,9 +738,7 @@ def zero_linear_cross_entropy_backward(x, w, targets, ce: CrossEntropy, d_loss, 
     kind = _choice(_REDUCTIONS, reduction, "reduction")
     if not set(want) <= {"dx", "dw"}:
         raise ValueError(f"want must name dx or dw, got {want!r}")
-    if dw_dtype is not None and dw_dtype not in _TYPES:
-        raise TypeError(f"dw_dtype: expected float16, bfloat16 or float32, got {dw_dtype}")
-    code = -1 if dw_dtype is None else _TYPES[dw_dtype]
+    code = _code(dw_dtype, "dw_dtype")
     return _run_on(stream, lambda: (_fast or _load_fast()).linear_cross_entropy_backward(
         x, w, targets, scale, ce.lse, ce.rows, d_loss, kind, "dx" in want, "dw" in want, dx, dw,
         code, workspace))

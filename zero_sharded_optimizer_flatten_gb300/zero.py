@@ -127,6 +127,16 @@ def lib():
                                         vp],
                 "zero_expert_combine_backward": [vp, i64, vp, ctypes.c_int, vp, ctypes.c_int, i64,
                                                  i32, i64, vp, i32, vp, vp, vp, vp],
+                "zero_expert_route": [vp, i64, ctypes.c_int, i64, i32, i32, i32, vp, vp, vp, vp, vp,
+                                      vp, i64, vp],
+                "zero_expert_route_workspace_bytes": [i64, i32, i64p],
+                "zero_expert_route_backward": [vp, i64, ctypes.c_int, i64, i32, i32, i32, vp, vp,
+                                               vp, vp, vp, vp, vp, vp],
+                "zero_embedding": [vp, i32, i64, vp, i64, ctypes.c_int, i64, i64, ctypes.c_double,
+                                   vp, ctypes.c_int, vp],
+                "zero_embedding_backward": [vp, i64, ctypes.c_int, vp, i32, i64, i64, i64,
+                                            ctypes.c_double, i32, vp, ctypes.c_int, vp, i64, vp],
+                "zero_embedding_workspace_bytes": [i64, i64, i64, i64p],
                 "zero_linear_cross_entropy_workspace_bytes": [vp, vp, i32, i64p],
                 "zero_linear_cross_entropy": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp],
                 "zero_linear_cross_entropy_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp,
