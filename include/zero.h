@@ -756,7 +756,7 @@ zero_status zero_expert_combine_backward(const void* dy, int64_t dy_stride, cons
  *     left out: no choice, p and lse 0
  *   ids[t][k]     = the expert of the k-th largest score, of equal scores the
  *                   lowest expert; -inf is never chosen: -1 (dropped by the
- *                   sort).  NaN counts as the largest.
+ *                   sort).  NaN counts as +inf.
  *   weights[t][k] = p of the choice, with normalize divided by the sum of the
  *                   token's; 0 for -1
  *   counts[e]     = how often expert e was chosen, n = tokens not left out

@@ -2,9 +2,9 @@
 
 Tolerances.  u(T) is the half spacing of the type an output is rounded to.  y is
 one binary32 product (2^-24, and 2^-24 for the factor's own rounding) before
-that.  A row of the gradient adds a chunk of 32 rows one by one, then the
-chunks' sums: an eighth of them one by one, then eight: at most
-50 + c / 256 additions of 2^-24 of the absolute sum for an id of c tokens, and
+that.  A row of the gradient adds a chunk of 8 to 32 rows one by one, then the
+chunks' sums: a quarter of them one by one, then four: at most
+50 + c / 32 additions of 2^-24 of the absolute sum for an id of c tokens, and
 two roundings for the factor.
 """
 import gc
@@ -75,7 +75,7 @@ def exact_gradient(dy, ids, V, scale, base=None):
     out = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, at, d) * scale
     size = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, at, d.abs()) * abs(scale)
     count = torch.bincount(at, minlength=V).double()[:, None]
-    slack = size * (52 + count / 256) * 2.0 ** -24
+    slack = size * (52 + count / 32) * 2.0 ** -24
     if base is not None:
         out = out + base.double()
         slack = slack + (out.abs() + base.double().abs()) * 2.0 ** -24

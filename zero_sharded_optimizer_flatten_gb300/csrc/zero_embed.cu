@@ -32,7 +32,7 @@ constexpr int kMinorMost = 1024;
 constexpr int kBucketsMost = 4096;  // vocab up to 2^22
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 8;
-constexpr int kChunk = 32;
+constexpr int kChunk = 32;  // sorted tokens of a CTA, 16 or 8 where that leaves SMs idle
 constexpr int kAhead = 8;  // rows in flight
 
 struct IdsArgs {
@@ -40,13 +40,10 @@ struct IdsArgs {
   int64_t tokens;
   int32_t id_bytes, vocab;
 };
-__device__ __forceinline__ int load_id(const IdsArgs& a, int64_t t) {
-  if (a.id_bytes == 4) {
-    const int v = static_cast<const int*>(a.ids)[t];
-    return v >= 0 && v < a.vocab ? v : -1;
-  }
-  const long long v = static_cast<const long long*>(a.ids)[t];
-  return v >= 0 && v < a.vocab ? static_cast<int>(v) : -1;
+// An id as it lies in memory, and what it stands for (-1: outside the table).
+template <class I>
+__device__ __forceinline__ int row_of(I v, int vocab) {
+  return v >= 0 && v < vocab ? static_cast<int>(v) : -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -57,57 +54,82 @@ struct LookupArgs {
   const void* table;
   void* y;
   int64_t stride;
-  int32_t hidden, lanes;
+  int32_t hidden, log_lanes, by32;
   float scale;
 };
 
-// A group of 8 to 256 lanes a token, octet by octet, two at a time.
-template <class T, class Y>
+// Eight values of a row, 16-byte aligned. Binary32 ones go out by 32 bytes: by 16
+// a warp's store touches twice the lines for half of each.
+template <class Y>
+__device__ __forceinline__ void store_row8(Y* p, const float (&v)[8], bool by32) {
+  if constexpr (sizeof(Y) == 4) {
+    if (by32) {
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                   "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                   : "memory");
+      return;
+    }
+  }
+  Elem<Y>::store8(p, v);
+}
+
+// A group of 8 to 256 lanes takes TOKENS neighbouring tokens, octet by octet,
+// all their rows in flight together. One token a group leaves the loads of a
+// row alone in flight behind that of its id: 24 us for 32768 tokens of 768 fp16
+// and 64 us for 16384 of 4096 bf16 to fp32, with four TIME4A and TIME4B.
+template <class I, class T, class Y, int TOKENS>
 __global__ void __launch_bounds__(kThreads) k_embed(const LookupArgs a) {
-  constexpr int kParts = 2;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / a.lanes) + threadIdx.x / a.lanes;
-  if (t >= a.ids.tokens) return;
-  const int lane = threadIdx.x % a.lanes, round = 8 * a.lanes;
-  const int id = load_id(a.ids, t);
-  Y* y = static_cast<Y*>(a.y) + t * a.hidden;
-  const T* row = static_cast<const T*>(a.table) + id * a.stride;
-  for (int c0 = 8 * lane; c0 < a.hidden; c0 += kParts * round) {
-    Octet<T> v[kParts];
+  const int lane = threadIdx.x & ((1 << a.log_lanes) - 1), g = threadIdx.x >> a.log_lanes;
+  const int64_t t0 = ((static_cast<int64_t>(blockIdx.x) * kThreads >> a.log_lanes) + g) * TOKENS;
+  if (t0 >= a.ids.tokens) return;
+  const I* ids = static_cast<const I*>(a.ids.ids);
+  I raw[TOKENS];
 #pragma unroll
-    for (int q = 0; q < kParts; ++q)
-      if (id >= 0 && c0 + q * round < a.hidden) v[q].load(row + c0 + q * round);
+  for (int k = 0; k < TOKENS; ++k) raw[k] = ids[min(t0 + k, a.ids.tokens - 1)];
+  const T* row[TOKENS];
 #pragma unroll
-    for (int q = 0; q < kParts; ++q)
-      if (c0 + q * round < a.hidden) {
+  for (int k = 0; k < TOKENS; ++k) {
+    const int id = row_of(raw[k], a.ids.vocab);
+    row[k] = id >= 0 ? static_cast<const T*>(a.table) + id * a.stride : nullptr;
+  }
+  Y* y = static_cast<Y*>(a.y) + t0 * a.hidden;
+  for (int c = 8 * lane; c < a.hidden; c += 8 << a.log_lanes) {
+    Octet<T> v[TOKENS];
+#pragma unroll
+    for (int k = 0; k < TOKENS; ++k)
+      if (row[k]) v[k].load(row[k] + c);
+#pragma unroll
+    for (int k = 0; k < TOKENS; ++k)
+      if (t0 + k < a.ids.tokens) {
         float f[8] = {};
-        if (id >= 0) {
-          v[q].widen(f);
+        if (row[k]) {
+          v[k].widen(f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= a.scale;
         }
-        Elem<Y>::store8(y + c0 + q * round, f);
+        store_row8(y + static_cast<int64_t>(k) * a.hidden + c, f, a.by32);
       }
   }
 }
 
 // Rows that start anywhere: single columns, eight a thread.
-template <class T, class Y>
+template <class I, class T, class Y>
 __global__ void __launch_bounds__(kThreads) k_embed_any(const LookupArgs a) {
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / a.lanes) + threadIdx.x / a.lanes;
+  const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> a.log_lanes;
   if (t >= a.ids.tokens) return;
-  const int lane = threadIdx.x % a.lanes;
-  const int id = load_id(a.ids, t);
+  const int id = row_of(static_cast<const I*>(a.ids.ids)[t], a.ids.vocab);
   Y* y = static_cast<Y*>(a.y) + t * a.hidden;
   const T* row = static_cast<const T*>(a.table) + id * a.stride;
-  for (int c0 = lane; c0 < a.hidden; c0 += 8 * a.lanes) {
+  for (int c0 = lane; c0 < a.hidden; c0 += 8 * lanes) {
     T v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (id >= 0 && c0 + i * a.lanes < a.hidden) v[i] = row[c0 + i * a.lanes];
+      if (id >= 0 && c0 + i * lanes < a.hidden) v[i] = row[c0 + i * lanes];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c0 + i * a.lanes < a.hidden)
-        y[c0 + i * a.lanes] = Elem<Y>::narrow(id >= 0 ? Elem<T>::widen(v[i]) * a.scale : 0.f);
+      if (c0 + i * lanes < a.hidden)
+        y[c0 + i * lanes] = Elem<Y>::narrow(id >= 0 ? Elem<T>::widen(v[i]) * a.scale : 0.f);
   }
 }
 
@@ -123,34 +145,51 @@ struct SortArgs {
 
 // One CTA a bucket of ids (id mod the number of CTAs: the frequent ids, which
 // have small numbers, fall into different ones). Every CTA looks at all ids:
-// counts its own, warp by warp, and those of the buckets before it; then goes
-// through them again and gives out places, which are in the tokens' order
-// because a warp's tokens are consecutive. Nothing passes between CTAs, so it is
-// one launch and no order depends on timing; what it costs is one read of the
-// ids from L2 for each bucket.
+// counts its own, warp by warp, and those of the buckets before it, and keeps
+// its own in a list for each warp; then goes through the lists and gives out
+// places, which are in the tokens' order because a warp's tokens are
+// consecutive. (A CTA with a full list goes through the ids again.) Nothing
+// passes between CTAs, so it is one launch and no order depends on timing; what
+// it costs is one read of the ids from L2 for each bucket.
+constexpr int kListed = 256;        // of a warp's list
+constexpr int kMinorBits = 10;      // of an entry; the rest is the place among the warp's tokens
+static_assert(kMinorMost == 1 << kMinorBits, "an entry's parts");
+
+template <class I>
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
   extern __shared__ int count[];  // [kSortWarps][minors], then first places; [minors]: the ids' first places
+  __shared__ uint32_t list[kSortWarps][kListed];
   __shared__ int below[kSortWarps], scan[kSortWarps];
   let_next_start();
+  const I* ids = static_cast<const I*>(a.ids.ids);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bucket = blockIdx.x, mask = (1 << a.bits) - 1, minors = a.minors;
+  const unsigned lower = (1u << lane) - 1;
   int* first = count + kSortWarps * minors;
   for (int i = threadIdx.x; i < kSortWarps * minors; i += kSortThreads) count[i] = 0;
   __syncthreads();
   const int64_t size = ((a.ids.tokens + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const int64_t lo = min(a.ids.tokens, warp * size), hi = min(a.ids.tokens, lo + size);
   int* mine = count + warp * minors;
-  int before = 0;
+  int before = 0, listed = 0;
   for (int64_t p = lo; p < hi; p += 32 * kSortAhead) {
-    int id[kSortAhead];
+    I raw[kSortAhead];
 #pragma unroll
-    for (int i = 0; i < kSortAhead; ++i) id[i] = p + 32 * i + lane < hi ? load_id(a.ids, p + 32 * i + lane) : -1;
+    for (int i = 0; i < kSortAhead; ++i) raw[i] = ids[min(p + 32 * i + lane, hi - 1)];
 #pragma unroll
     for (int i = 0; i < kSortAhead; ++i) {
-      if (id[i] < 0) continue;
-      const int b = id[i] & mask;
-      before += b < bucket;
-      if (b == bucket) atomicAdd(mine + (id[i] >> a.bits), 1);  // only counted here: no order
+      const int id = p + 32 * i + lane < hi ? row_of(raw[i], a.ids.vocab) : -1;
+      const int b = id & mask;
+      before += id >= 0 && b < bucket;
+      const bool own = id >= 0 && b == bucket;
+      const unsigned owners = __ballot_sync(kFull, own);
+      if (!owners) continue;
+      if (own) {
+        const int m = id >> a.bits, at = listed + __popc(owners & lower);
+        atomicAdd(mine + m, 1);  // only counted here: no order
+        if (at < kListed) list[warp][at] = static_cast<uint32_t>(p - lo + 32 * i + lane) << kMinorBits | m;
+      }
+      listed += __popc(owners);
     }
   }
   before = __reduce_add_sync(kFull, before);
@@ -189,24 +228,34 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
   }
   if (bucket == static_cast<int>(gridDim.x) - 1 && threadIdx.x == 0)
     a.starts[static_cast<int64_t>(gridDim.x) * minors] = carry;
-  for (int64_t p = lo; p < hi; p += 32 * kSortAhead) {
-    int id[kSortAhead];
+  // places of 32 of the warp's tokens (m -1: not this bucket's)
+  auto place = [&](int64_t token, int m) {
+    const unsigned owners = __ballot_sync(kFull, m >= 0);
+    if (m >= 0) {
+      const unsigned same = __match_any_sync(owners, m);
+      const int rank = __popc(same & lower);
+      const int at = first[m] + mine[m] + rank;
+      __syncwarp(owners);
+      if (rank == 0) mine[m] += __popc(same);
+      a.order[at] = make_int2(static_cast<int>(token), m << a.bits | bucket);
+    }
+    __syncwarp();
+  };
+  if (listed <= kListed && size <= INT64_C(1) << (32 - kMinorBits)) {
+    for (int i = lane; i - lane < listed; i += 32) {
+      const uint32_t e = i < listed ? list[warp][i] : 0;
+      place(lo + (e >> kMinorBits), i < listed ? static_cast<int>(e & (kMinorMost - 1)) : -1);
+    }
+  } else {
+    for (int64_t p = lo; p < hi; p += 32 * kSortAhead) {
+      I raw[kSortAhead];
 #pragma unroll
-    for (int i = 0; i < kSortAhead; ++i) id[i] = p + 32 * i + lane < hi ? load_id(a.ids, p + 32 * i + lane) : -1;
+      for (int i = 0; i < kSortAhead; ++i) raw[i] = ids[min(p + 32 * i + lane, hi - 1)];
 #pragma unroll
-    for (int i = 0; i < kSortAhead; ++i) {
-      const bool own = id[i] >= 0 && (id[i] & mask) == bucket;
-      const unsigned owners = __ballot_sync(kFull, own);
-      if (own) {
-        const int m = id[i] >> a.bits;
-        const unsigned same = __match_any_sync(owners, m);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        const int at = first[m] + mine[m] + rank;
-        __syncwarp(owners);
-        if (rank == 0) mine[m] += __popc(same);
-        a.order[at] = make_int2(static_cast<int>(p + 32 * i + lane), id[i]);
+      for (int i = 0; i < kSortAhead; ++i) {
+        const int id = p + 32 * i + lane < hi ? row_of(raw[i], a.ids.vocab) : -1;
+        place(p + 32 * i + lane, id >= 0 && (id & mask) == bucket ? id >> a.bits : -1);
       }
-      __syncwarp();
     }
   }
   // the clearing kernel ran beside this one: what follows this grid follows both
@@ -235,27 +284,41 @@ struct SumArgs {
   int64_t dy_stride, part_stride;
   void* out;
   float* part;           // [chunks][2][part_stride]: of a run from an earlier chunk, of a run that goes on
-  int32_t hidden, out_type, add, vocab;
+  int2* tail;            // [chunks]: the id that begins in a chunk and goes on (-1: none), chunks that it goes on in
+  int32_t hidden, out_type, add, vocab, chunk;
   int64_t tokens;
   float scale;
 };
 
 // What a thread holds of a row: an octet, or eight columns `step` apart.
-template <class D, bool VEC>
+template <bool VEC>
 struct Columns {
   int c0, step, hidden;
   __device__ __forceinline__ bool any() const { return c0 < hidden; }
   __device__ __forceinline__ int at(int i) const { return c0 + (VEC ? i : i * step); }
   __device__ __forceinline__ bool in(int i) const { return VEC || at(i) < hidden; }
+  // As it was loaded, so that several rows' loads go out before any is used.
   template <class P>
-  __device__ __forceinline__ void load(const P* row, float (&v)[8]) const {
+  struct Raw {
+    Octet<P> octet;
+    P one[VEC ? 1 : 8];
+  };
+  template <class P>
+  __device__ __forceinline__ void load(const P* row, Raw<P>& r) const {
     if constexpr (VEC) {
-      Octet<P> o;
-      o.load(row + c0);
-      o.widen(v);
+      r.octet.load(row + c0);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = in(i) ? Elem<P>::widen(row[at(i)]) : 0.f;
+      for (int i = 0; i < 8; ++i) r.one[i] = row[in(i) ? at(i) : 0];
+    }
+  }
+  template <class P>
+  __device__ __forceinline__ void widen(const Raw<P>& r, float (&v)[8]) const {
+    if constexpr (VEC) {
+      r.octet.widen(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = Elem<P>::widen(r.one[i]);
     }
   }
   template <class P>
@@ -272,7 +335,11 @@ struct Columns {
   template <class P>
   __device__ __forceinline__ void finish(P* row, const float (&sum)[8], float scale, bool add) const {
     float v[8] = {};
-    if (add) load(row, v);
+    if (add) {
+      Raw<P> r;
+      load(row, r);
+      widen(r, v);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaf(scale, sum[i], v[i]);
     store(row, v);
@@ -288,40 +355,54 @@ struct Columns {
   }
 };
 
-// A chunk's sums. The rows are loaded kAhead at a time, whichever runs they
+// A chunk's sums. The rows are loaded AHEAD at a time, whichever runs they
 // belong to; the runs' ends are the same for every thread.
 template <class D, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_embed_sums(const SumArgs a) {
+  constexpr int AHEAD = VEC ? kAhead : 4;
   __shared__ int2 item[kChunk + 2];
   let_next_start();
   wait_for_previous();
   const int total = a.starts[a.total_at];
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * kChunk;
-  if (lo >= total) return;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), total - lo));
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
+  if (lo >= total) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) a.tail[blockIdx.x] = make_int2(-1, 0);
+    return;
+  }
+  const int n = static_cast<int>(min(static_cast<int64_t>(a.chunk), total - lo));
   for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
     const int64_t p = lo + i - 1;
     item[i] = p >= 0 && p < total ? a.order[p] : make_int2(-1, -1);
   }
   __syncthreads();
-  const Columns<D, VEC> cols = {VEC ? static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) * 8
-                                    : static_cast<int>(blockIdx.y * blockDim.x * 8 + threadIdx.x),
-                                static_cast<int>(blockDim.x), a.hidden};
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    int2 tail = make_int2(-1, 0);
+    const int id = item[n].y;
+    if (item[n + 1].y == id) {
+      const int64_t at = static_cast<int64_t>(id & ((1 << a.bits) - 1)) * a.minors + (id >> a.bits);
+      if (a.starts[at] >= lo) tail = make_int2(id, (a.starts[at + 1] - 1) / a.chunk - static_cast<int>(blockIdx.x));
+    }
+    a.tail[blockIdx.x] = tail;
+  }
+  const Columns<VEC> cols = {VEC ? static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) * 8
+                                 : static_cast<int>(blockIdx.y * blockDim.x * 8 + threadIdx.x),
+                             static_cast<int>(blockDim.x), a.hidden};
   if (!cols.any()) return;
   const D* dy = static_cast<const D*>(a.dy);
   float sum[8] = {};
   int run_from = 0;
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
-    float v[kAhead][8];
+  for (int i0 = 0; i0 < n; i0 += AHEAD) {
+    typename Columns<VEC>::template Raw<D> raw[AHEAD];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (i0 + k < n) cols.load(dy + item[i0 + k + 1].x * a.dy_stride, v[k]);
+    for (int k = 0; k < AHEAD; ++k) cols.load(dy + item[min(i0 + k, n - 1) + 1].x * a.dy_stride, raw[k]);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    for (int k = 0; k < AHEAD; ++k) {
       const int i = i0 + k;
       if (i >= n) break;
+      float v[8];
+      cols.widen(raw[k], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[k][j];
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
       const int id = item[i + 1].y;
       const bool goes_on = item[i + 2].y == id;
       if (goes_on && i + 1 < n) continue;
@@ -339,34 +420,39 @@ __global__ void __launch_bounds__(kThreads) k_embed_sums(const SumArgs a) {
 
 // Runs over several chunks: the chunk in which one begins adds its parts up,
 // kJoinGroups threads a column, each a contiguous share of the chunks.
-constexpr int kJoinLanes = 32, kJoinGroups = kThreads / kJoinLanes;
+constexpr int kJoinLanes = 64, kJoinGroups = kThreads / kJoinLanes;
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) k_embed_join(const SumArgs a) {
   __shared__ float part[kJoinGroups][8][kJoinLanes];
   wait_for_previous();
-  const int total = a.starts[a.total_at];
-  const int64_t chunk = blockIdx.x, hi = (chunk + 1) * kChunk;
-  if (hi >= total) return;
-  const int id = a.order[hi - 1].y;
-  if (a.order[hi].y != id) return;
-  const int64_t at = static_cast<int64_t>(id & ((1 << a.bits) - 1)) * a.minors + (id >> a.bits);
-  const int begin = a.starts[at], end = a.starts[at + 1];
-  if (begin < chunk * kChunk) return;  // begins in an earlier chunk
-  const int parts = static_cast<int>((end - 1) / kChunk - chunk);  // chunks after this one
+  const int64_t chunk = blockIdx.x;
+  const int2 tail = a.tail[chunk];
+  const int id = tail.x, parts = tail.y;  // parts: chunks after this one
+  if (id < 0) return;
   const int lane = threadIdx.x % kJoinLanes, g = threadIdx.x / kJoinLanes;
-  const Columns<float, VEC> cols = {VEC ? static_cast<int>(blockIdx.y * kJoinLanes + lane) * 8
-                                        : static_cast<int>(blockIdx.y * kJoinLanes * 8 + lane),
-                                    kJoinLanes, a.hidden};
+  const Columns<VEC> cols = {VEC ? static_cast<int>(blockIdx.y * kJoinLanes + lane) * 8
+                                 : static_cast<int>(blockIdx.y * kJoinLanes * 8 + lane),
+                             kJoinLanes, a.hidden};
   float sum[8] = {};
   if (cols.any()) {
-    if (g == 0) cols.load(a.part + (chunk * 2 + 1) * a.part_stride, sum);
-    const int each = (parts + kJoinGroups - 1) / kJoinGroups;
-#pragma unroll 4
-    for (int k = g * each; k < min(parts, (g + 1) * each); ++k) {
-      float v[8];
-      cols.load(a.part + (chunk + 1 + k) * 2 * a.part_stride, v);
+    constexpr int AHEAD = VEC ? 4 : 2;
+    const int each = (parts + kJoinGroups - 1) / kJoinGroups, k1 = min(parts, (g + 1) * each);
+    typename Columns<VEC>::template Raw<float> raw[AHEAD];
+    if (g == 0) {
+      cols.load(a.part + (chunk * 2 + 1) * a.part_stride, raw[0]);
+      cols.widen(raw[0], sum);
+    }
+    for (int k = g * each; k < k1; k += AHEAD) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      for (int q = 0; q < AHEAD; ++q) cols.load(a.part + (chunk + 1 + min(k + q, k1 - 1)) * 2 * a.part_stride, raw[q]);
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) {
+        if (k + q >= k1) break;
+        float v[8];
+        cols.widen(raw[q], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      }
     }
   }
 #pragma unroll
@@ -400,29 +486,42 @@ cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, bool e
   return e;
 }
 
+// One token a group while that leaves SMs without a CTA, else four.
+template <class I, class T, class Y>
+cudaError_t launch_lookup(LookupArgs& a, bool vec, cudaStream_t s) {
+  a.log_lanes = 3;
+  while (a.log_lanes < 8 && (INT64_C(8) << a.log_lanes) < a.hidden) ++a.log_lanes;
+  const int64_t per_cta = kThreads >> a.log_lanes, one = (a.ids.tokens + per_cta - 1) / per_cta;
+  const bool four = vec && one >= 8 * kSMs;
+  const int64_t grid = four ? (a.ids.tokens + 4 * per_cta - 1) / (4 * per_cta) : one;
+  return launch(four  ? &k_embed<I, T, Y, 4>
+                : vec ? &k_embed<I, T, Y, 1>
+                      : &k_embed_any<I, T, Y>,
+                dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s, static_cast<const LookupArgs>(a));
+}
 template <class T, class Y>
 cudaError_t launch_lookup(LookupArgs& a, bool vec, cudaStream_t s) {
-  a.lanes = 8;
-  while (a.lanes < kThreads && static_cast<int64_t>(a.lanes) * 8 < a.hidden) a.lanes *= 2;
-  const int64_t per_cta = kThreads / a.lanes, grid = (a.ids.tokens + per_cta - 1) / per_cta;
-  return launch(vec ? &k_embed<T, Y> : &k_embed_any<T, Y>, dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s,
-                static_cast<const LookupArgs>(a));
+  return a.ids.id_bytes == 4 ? launch_lookup<int32_t, T, Y>(a, vec, s) : launch_lookup<long long, T, Y>(a, vec, s);
 }
 
 // The workspace of the gradient.
 struct Layout {
-  int bits, minors, buckets;
-  int64_t chunks, part_stride, order, starts, part, bytes;
+  int bits, minors, buckets, chunk;
+  int64_t chunks, part_stride, order, starts, tail, part, bytes;
   Layout(int64_t tokens, int64_t vocab, int64_t hidden) {
     buckets = kBuckets, bits = 7;
     while ((vocab + buckets - 1) / buckets > kMinorMost) buckets *= 2, ++bits;
     minors = static_cast<int>((vocab + buckets - 1) / buckets);
-    chunks = (tokens + kChunk - 1) / kChunk;
+    const int64_t ctas = (hidden + 8 * kThreads - 1) / (8 * kThreads);  // of a chunk
+    chunk = kChunk;
+    while (chunk > 8 && (tokens + chunk - 1) / chunk * ctas < 4 * kSMs) chunk /= 2;
+    chunks = (tokens + chunk - 1) / chunk;
     part_stride = (hidden + 7) / 8 * 8;
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
     order = 0;
     starts = up(tokens * 8);
-    part = starts + up((static_cast<int64_t>(buckets) * minors + 1) * 4);
+    tail = starts + up((static_cast<int64_t>(buckets) * minors + 1) * 4);
+    part = tail + up(chunks * 8);
     bytes = part + chunks * 2 * part_stride * 4;
   }
   int sort_smem() const { return (kSortWarps + 1) * minors * 4; }
@@ -506,7 +605,7 @@ extern "C" zero_status zero_embedding(const void* ids, int32_t id_bytes, int64_t
                             Extent::block("ids", ids, tokens * id_bytes)}));
   EMBED_TRY(pending_error(fn));
   LookupArgs a = {{ids, tokens, id_bytes, static_cast<int32_t>(vocab)}, table, y, table_stride,
-                  static_cast<int32_t>(hidden), 0, static_cast<float>(scale)};
+                  static_cast<int32_t>(hidden), 0, aligned_to(y, 32), static_cast<float>(scale)};
   const bool vec = hidden % 8 == 0 && table_stride * e % 16 == 0 && aligned_to(table, 16) && aligned_to(y, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = y_dtype == ZERO_FP32;
@@ -572,16 +671,16 @@ extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride
   char* ws = static_cast<char*>(workspace);
   const SortArgs sort = {{ids, tokens, id_bytes, static_cast<int32_t>(vocab)}, at.bits, at.minors,
                          reinterpret_cast<int2*>(ws + at.order), reinterpret_cast<int32_t*>(ws + at.starts)};
-  static KernelFacts facts;
-  r = facts.allow(reinterpret_cast<const void*>(&k_embed_sort), kSortSmemMost, kSortSmemMost);
-  if (r == cudaSuccess)
-    r = launch(&k_embed_sort, dim3(at.buckets), kSortThreads, at.sort_smem(), !accumulate, s, sort);
+  static KernelFacts facts[2];
+  auto* sort_fn = id_bytes == 4 ? &k_embed_sort<int32_t> : &k_embed_sort<long long>;
+  r = facts[id_bytes == 4].allow(reinterpret_cast<const void*>(sort_fn), kSortSmemMost, kSortSmemMost);
+  if (r == cudaSuccess) r = launch(sort_fn, dim3(at.buckets), kSortThreads, at.sort_smem(), !accumulate, s, sort);
   SumArgs a = {};
   a.order = sort.order, a.starts = sort.starts, a.total_at = at.buckets * at.minors;
   a.bits = at.bits, a.minors = at.minors, a.dy = dy, a.dy_stride = dy_stride, a.part_stride = at.part_stride;
   a.out = dtable, a.part = reinterpret_cast<float*>(ws + at.part), a.hidden = static_cast<int32_t>(hidden);
   a.out_type = dtable_dtype, a.add = accumulate != 0, a.vocab = static_cast<int32_t>(vocab), a.tokens = tokens;
-  a.scale = static_cast<float>(scale);
+  a.scale = static_cast<float>(scale), a.tail = reinterpret_cast<int2*>(ws + at.tail), a.chunk = at.chunk;
   const bool vec = hidden % 8 == 0 && dy_stride * e % 16 == 0 && aligned_to(dy, 16) && aligned_to(dtable, 16);
   if (r == cudaSuccess)
     r = dy_dtype == ZERO_FP32   ? (vec ? launch_sums<float, true>(a, at.chunks, s)

@@ -40,7 +40,10 @@ constexpr int kHalfRows = 128;
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kHalfRows * kTileK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kThreads = 192;  // copies, products, four warps of epilogue
+constexpr int kEpilogueWarps = 8;  // two for each quarter of the rows, 128 columns each
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // copies, products, epilogue
+constexpr int kParts = kEpilogueWarps / 4;          // of a row's 256 columns
+constexpr int kPartColumns = kTileN / kParts;
 constexpr int kAccumulators = 2;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes;
 constexpr int64_t kPieceBytes = INT64_C(512) << 20;  // of dz in memory at a time
@@ -68,9 +71,10 @@ struct ProductArgs {
   int32_t bf16;
   int32_t* err;
   // kStats, kProbs
+  int32_t tile, rows_a;  // columns of a tile; rows of x in a box (fewer than 128: of one CTA, there are no more)
   float scale2;          // scale * log2(e)
   const int32_t* target;
-  float2* part;          // [column tiles][rows_cap]: maximum and sum, base 2
+  float2* part;          // [column tiles * 2][n rounded up]: maximum and sum, base 2
   float* target_z;       // base 2
   const float* lse2;
   const float* row_mul;
@@ -81,10 +85,12 @@ struct ProductArgs {
   const int32_t* rows;   // kept row -> token
   int64_t tokens;
   void* out;
+  int64_t out_stride, out_first;  // kDw: the row of out that the piece's first goes to
   int32_t out_type, out_align;
   float* sums;           // kDx: [splits][n rounded up][sums_stride]
   int64_t sums_stride;
   int32_t add, pieces, pairs;
+  int32_t direct;  // kDx: dx may be written by the product (when its sum has one part)
 };
 
 __host__ __device__ __forceinline__ int64_t up(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
@@ -99,17 +105,33 @@ __host__ __device__ __forceinline__ int split_of(int64_t tiles, int64_t depth, i
   return static_cast<int>(s < most ? s : most < 1 ? 1 : most);
 }
 
+// Columns of z that a tile takes. With few tiles the pairs' last round is mostly
+// empty: narrower tiles fill it (the eight rows of 4096 against 32000 columns:
+// 143 tiles of 224 on 76 pairs in place of 125 of 256). Above two rounds the
+// narrower tile's extra reads of x cost as much as it gains.
+inline int tile_columns(int64_t m_tiles, int64_t columns, int pairs) {
+  if (m_tiles * over(columns, kTileN) > 2 * pairs) return kTileN;
+  int best = kTileN;
+  int64_t least = over(m_tiles * over(columns, kTileN), pairs) * kTileN;
+  for (int t = kTileN - 32; t > kTileN / 2; t -= 32) {
+    const int64_t cost = over(m_tiles * over(columns, t), pairs) * t;
+    if (cost < least) best = t, least = cost;
+  }
+  return best;
+}
+
 // The tiles of a product and their order.
 template <int KIND>
 struct Tiles {
-  int m_tiles, n_tiles, splits, depth_blocks;
+  int m_tiles, n_tiles, splits, depth_blocks, columns;
   int64_t total;
   __device__ __forceinline__ Tiles(const ProductArgs& a, int n) {
     const int rows = KIND == kDw ? a.columns : n;
     const int cols = KIND == kDx || KIND == kDw ? a.hidden : a.columns;
     const int depth = KIND == kDx ? a.columns : KIND == kDw ? n : a.hidden;
     m_tiles = static_cast<int>(over(rows, kTileM));
-    n_tiles = static_cast<int>(over(cols, kTileN));
+    columns = KIND == kStats || KIND == kProbs ? a.tile : kTileN;
+    n_tiles = static_cast<int>(over(cols, columns));
     depth_blocks = static_cast<int>(over(depth, kTileK));
     splits = KIND == kDx ? split_of(static_cast<int64_t>(m_tiles) * n_tiles, a.piece, a.pairs) : 1;
     total = static_cast<int64_t>(m_tiles) * n_tiles * splits;
@@ -173,13 +195,15 @@ __device__ __forceinline__ void store32(T* p, const float (&v)[32], int left, in
   }
 }
 
-// A tile's epilogue for one row: 256 columns, 32 at a time, from tensor memory.
+// A warp's part of a tile's epilogue, a row a thread: up to 128 columns, 32 at a
+// time, from tensor memory.
 template <int KIND>
 struct Epilogue {
   const ProductArgs& a;
   int n;            // kept rows
   int64_t row;      // of the product
-  int m, col, split, k_blocks;
+  int col, split;
+  int64_t part;     // kStats: which of the row's parts this is
 
   // maximum and sum of exponentials so far
   float top = -INFINITY, sum = 0.f;
@@ -190,11 +214,12 @@ struct Epilogue {
   bool direct = true;
   int64_t sums_rows = 0;
 
-  __device__ __forceinline__ Epilogue(const ProductArgs& a_, int n_, const Tiles<KIND>& t, int m_, int nt, int split_,
-                                      int row_in_tile)
-      : a(a_), n(n_), m(m_), split(split_) {
-    row = static_cast<int64_t>(m_) * kTileM + row_in_tile;
-    col = nt * kTileN;
+  __device__ __forceinline__ Epilogue(const ProductArgs& a_, int n_, const Tiles<KIND>& t, int m, int nt, int split_,
+                                      int row_in_tile, int half)
+      : a(a_), n(n_), split(split_) {
+    row = static_cast<int64_t>(m) * kTileM + row_in_tile;
+    col = nt * t.columns;
+    part = nt * INT64_C(1) * kParts + half;
     const bool live = KIND == kDw ? row < a.columns : row < n;
     if constexpr (KIND == kStats || KIND == kProbs) {
       if (live) target = a.target[row] - a.first;
@@ -203,14 +228,14 @@ struct Epilogue {
       if (live) lse2 = a.lse2[row], mul = a.row_mul[row];
     }
     if constexpr (KIND == kDx) {
-      direct = a.pieces == 1 && t.splits == 1;
+      direct = a.direct && a.pieces == 1 && t.splits == 1;
       sums_rows = up(n, kTileM);
       if (live) token = a.rows[row];
       if (token >= a.tokens) token = -1;
       alpha = a.scales->alpha;
     }
     if constexpr (KIND == kDw) {
-      if (live) token = a.first + row;
+      if (live) token = a.out_first + row;
       alpha = a.scales->alpha;
     }
     (void)live;
@@ -244,6 +269,7 @@ struct Epilogue {
           if (rel == i) a.target_z[row] = t[i];
       }
     } else if constexpr (KIND == kProbs) {
+      if (c >= a.dz_stride) return;  // the last of narrower tiles may pass the piece
       float p[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) p[i] = tc::exp2_of(fmaf(__uint_as_float(w[i]), a.scale2, -lse2));
@@ -284,7 +310,7 @@ struct Epilogue {
       if (token < 0) return;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= alpha;
-      const int64_t at = token * a.hidden + c;
+      const int64_t at = token * a.out_stride + c;
       if (a.out_type == ZERO_FP32)
         store32(static_cast<float*>(a.out) + at, v, left, a.out_align);
       else if (a.out_type == ZERO_BF16)
@@ -295,13 +321,13 @@ struct Epilogue {
   }
 
   __device__ __forceinline__ void done() {
-    if constexpr (KIND == kStats) a.part[static_cast<int64_t>(col / kTileN) * a.rows_cap + row] = make_float2(top, sum);
+    if constexpr (KIND == kStats) a.part[part * up(n, kTileM) + row] = make_float2(top, sum);
   }
 };
 
 // A persistent pair of CTAs a tile of 256 x 256: one thread of each CTA copies
 // its half of the operands' blocks into a ring of kStages, one thread of the
-// leading CTA issues the products of both, and four warps of each CTA work on
+// leading CTA issues the products of both, and eight warps of each CTA work on
 // its half of a finished tile in tensor memory while the next one is formed in
 // the other accumulator.
 template <int KIND>
@@ -325,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::prefetch_map(&a.a);
     tc::prefetch_map(&a.b);
     for (int s = 0; s < kStages; ++s) tc::bar_init(full(s), 1), tc::bar_init(empty(s), 1);
-    for (int s = 0; s < kAccumulators; ++s) tc::bar_init(acc_full(s), 1), tc::bar_init(acc_empty(s), 8);
+    for (int s = 0; s < kAccumulators; ++s) tc::bar_init(acc_full(s), 1), tc::bar_init(acc_empty(s), 2 * kEpilogueWarps);
     tc::bar_init(drained, 1);
     tc::bar_init_fence();
   }
@@ -350,17 +376,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int m, nt, s, k0, k1;
       tiles.at(t, m, nt, s);
       tiles.depth(s, k0, k1);
-      const int row = m * kTileM + static_cast<int>(rank) * kHalfRows, col = nt * kTileN + static_cast<int>(rank) * kHalfRows;
+      const int half = tiles.columns / 2;  // of the columns: this CTA's operand rows
+      const int row = m * kTileM + static_cast<int>(rank) * kHalfRows, col = nt * tiles.columns + static_cast<int>(rank) * half;
+      const int rows_a = kAByM || KIND == kDx ? kHalfRows : a.rows_a;
+      const bool copies_a = rows_a == kHalfRows || rank == 0;
+      const uint32_t bytes = static_cast<uint32_t>((rows_a == kHalfRows ? 2 * kHalfRows : rows_a) + tiles.columns) * (kTileK * 2);
       for (int k = k0; k < k1; ++k) {
         ok = tc::bar_wait(empty(ring.slot), ring.phase ^ 1);
         if (!ok) break;
         const uint32_t dst = base + ring.slot * kStageBytes;
         const uint32_t bar = tc::in_cta(full(ring.slot), 0);
-        if (rank == 0) tc::bar_expect(full(ring.slot), 2 * kStageBytes);
+        if (rank == 0) tc::bar_expect(full(ring.slot), bytes);
         if constexpr (kAByM) {
           tc::load_box(dst, &a.a, row, k * kTileK, bar);
           tc::load_box(dst + kOperandBytes / 2, &a.a, row + 64, k * kTileK, bar);
-        } else {
+        } else if (copies_a) {
           tc::load_box(dst, &a.a, k * kTileK, row, bar);
         }
         if constexpr (kBByN) {
@@ -382,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc::bar_wait(full(static_cast<int>(j % kStages)), static_cast<uint32_t>(j / kStages) & 1);
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
-    const uint32_t instr = tc::instruction(a.bf16 != 0, kAByM, kBByN, kTileM, kTileN);
+    const uint32_t instr = tc::instruction(a.bf16 != 0, kAByM, kBByN, kTileM, tiles.columns);
     constexpr uint32_t kLead = kOperandBytes / 2;
     Ring<kStages> ring;
     Ring<kAccumulators> acc;
@@ -422,17 +452,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 2) {
     Ring<kAccumulators> acc;
     const int quarter = warp & 3;  // the rows of tensor memory that this warp may read
+    const int half = (warp - 2) / 4, c0 = half * kPartColumns, c1 = min(tiles.columns, c0 + kPartColumns);
     for (int64_t t = first; t < tiles.total && ok; t += step) {
       int m, nt, s, k0, k1;
       tiles.at(t, m, nt, s);
       tiles.depth(s, k0, k1);
-      Epilogue<KIND> e(a, n, tiles, m, nt, s, static_cast<int>(rank) * kHalfRows + quarter * 32 + lane);
+      Epilogue<KIND> e(a, n, tiles, m, nt, s, static_cast<int>(rank) * kHalfRows + quarter * 32 + lane, half);
       ok = tc::bar_wait(acc_full(acc.slot), acc.phase);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
       tc::fence_after();
       const uint32_t d = tmem + acc.slot * kTileN + (static_cast<uint32_t>(quarter * 32) << 16);
-      for (int c = 0; c < kTileN; c += 32) {
+      for (int c = c0; c < c1; c += 32) {
         uint32_t w[32];
         tc::tmem_load(d + c, w);
         tc::tmem_wait_load();
@@ -468,7 +499,7 @@ struct RowsArgs {
   int64_t x_stride, xs_stride, rows_cap;
   void* xs;
   int32_t* target;
-  int32_t vec;
+  int32_t vec, log_lanes, parts;
   // gradients
   const float* lse;
   const float* d;
@@ -481,21 +512,32 @@ struct RowsArgs {
   // losses
   const float2* part;
   const float* target_z;
-  int32_t column_tiles;
+  float* cta_sums;  // [CTAs of k_loss_finish]
   float *losses, *lse_out, *total;
 };
 
 __device__ __forceinline__ int load_target(const RowsArgs& a, int64_t t) {
-  if (a.id_bytes == 4) {
-    const int v = static_cast<const int*>(a.targets)[t];
-    return v >= 0 && v < a.vocab ? v : -1;
-  }
-  const long long v = static_cast<const long long*>(a.targets)[t];
+  const long long v = a.id_bytes == 4 ? static_cast<const int*>(a.targets)[t] : static_cast<const long long*>(a.targets)[t];
   return v >= 0 && v < a.vocab ? static_cast<int>(v) : -1;
 }
+// Whether token t0 + i * step is kept, the targets loaded together (a choice of
+// their type within the loop would make the loads wait for one another).
+template <int N>
+__device__ __forceinline__ void load_kept(const RowsArgs& a, int64_t t0, int step, bool (&kept)[N]) {
+  long long v[N];
+  if (a.id_bytes == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = static_cast<const int*>(a.targets)[min(t0 + i * step, a.tokens - 1)];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = static_cast<const long long*>(a.targets)[min(t0 + i * step, a.tokens - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) kept[i] = t0 + i * step < a.tokens && v[i] >= 0 && v[i] < a.vocab;
+}
 
-// The kept tokens, in order: one CTA, a token's target each round and thread.
-constexpr int kScanThreads = 1024, kScanEach = 4;
+// The kept tokens, in order: one CTA.
+constexpr int kScanThreads = 1024, kScanEach = 8;
 __global__ void __launch_bounds__(kScanThreads) k_loss_rows(const RowsArgs a) {
   __shared__ int counts[32];
   let_next_start();
@@ -507,11 +549,7 @@ __global__ void __launch_bounds__(kScanThreads) k_loss_rows(const RowsArgs a) {
     bool kept[kScanEach];
     unsigned votes[kScanEach];
     int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kScanEach; ++i) {
-      const int64_t t = w0 + 32 * i + lane;
-      kept[i] = t < a.tokens && load_target(a, t) >= 0;
-    }
+    load_kept(a, w0 + lane, 32, kept);
 #pragma unroll
     for (int i = 0; i < kScanEach; ++i) votes[i] = __ballot_sync(kFull, kept[i]), mine += __popc(votes[i]);
     __syncthreads();
@@ -539,152 +577,247 @@ __global__ void __launch_bounds__(kScanThreads) k_loss_rows(const RowsArgs a) {
 }
 
 // What the gradients are scaled with: every row's g times a power of two that
-// brings the largest to [2^13, 2^14), so that neither rounding to 16 bits nor
-// fp16's range costs small probabilities.
+// brings the largest (`top`) to [2^13, 2^14), so that neither rounding to 16 bits
+// nor fp16's range costs small probabilities.
+__device__ __forceinline__ Scales scales_for(float top, float g, double scale) {
+  int e = 14;
+  if (!(top <= 3.4e38f))
+    e = 127;  // infinite or NaN: the results are, too
+  else if (top > 0.f)
+    frexpf(top, &e);
+  e = max(e, -100);
+  return {ldexpf(1.f, 14 - e), static_cast<float>(ldexp(scale, e - 14)), g};
+}
+// The one of a sum or a mean; of the tokens' own gradients it takes a pass.
+__device__ __forceinline__ Scales scales_of_one(const RowsArgs& a, int n) {
+  float g = *a.d;
+  if (a.reduction == ZERO_LOSS_MEAN) g = g / static_cast<float>(max(n, 1));
+  return scales_for(fabsf(g), g, a.scale);
+}
 __global__ void __launch_bounds__(kScanThreads) k_loss_scales(const RowsArgs a) {
   __shared__ float most[32];
   let_next_start();
   const int n = a.rows[a.tokens];
-  float g = 0.f, top = 0.f;
-  if (a.reduction == ZERO_LOSS_NONE) {
-    for (int i = threadIdx.x; i < n; i += kScanThreads) {
-      const int t = a.rows[i];
-      if (t >= 0 && t < a.tokens) top = fmaxf(top, fabsf(a.d[t]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = top;
-    __syncthreads();
-    top = most[threadIdx.x & 31];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  } else {
-    g = *a.d;
-    if (a.reduction == ZERO_LOSS_MEAN) g = g / static_cast<float>(max(n, 1));
-    top = fabsf(g);
+  float top = 0.f;
+  for (int i = threadIdx.x; i < n; i += kScanThreads) {
+    const int t = a.rows[i];
+    if (t >= 0 && t < a.tokens) top = fmaxf(top, fabsf(a.d[t]));
   }
-  if (threadIdx.x == 0) {
-    int e = 14;
-    if (!(top <= 3.4e38f))
-      e = 127;  // infinite or NaN: the results are, too
-    else if (top > 0.f)
-      frexpf(top, &e);
-    e = max(e, -100);
-    *a.scales = {ldexpf(1.f, 14 - e), static_cast<float>(ldexp(a.scale, e - 14)), g};
-  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = most[threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  if (threadIdx.x == 0) *a.scales = scales_for(top, 0.f, a.scale);
 }
 
-// The kept rows copied together, zeros up to a whole tile; their targets (and,
-// for the gradients, what scales them); left-out rows of dx.
+// The kept rows copied together, in the gradients with zeros up to a whole block
+// of the depth of dz^T x; their targets (and what scales them); left-out rows of
+// dx. A group of 8 to 256 lanes has a row.
 constexpr int kGatherThreads = 256;
-template <class W, bool BACKWARD>
+constexpr int kFewTokens = 4 * kGatherThreads;  // whose list every CTA makes for itself: one launch less
+enum Gather { kForward, kForwardFew, kBackward };
+
+template <class W, Gather KIND>
 __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a) {
+  constexpr bool BACKWARD = KIND == kBackward;
+  __shared__ int few[KIND == kForwardFew ? kFewTokens : 1], counts[kGatherThreads / 32];
   let_next_start();
   wait_for_previous();
-  const int n = a.rows[a.tokens];
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kGatherThreads / 32);
+  int n;
+  if constexpr (KIND == kForwardFew) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    bool kept[4];
+    unsigned votes[4];
+    load_kept(a, warp * 128 + lane, 32, kept);
+    int mine = 0, at = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) votes[k] = __ballot_sync(kFull, kept[k]), mine += __popc(votes[k]);
+    if (lane == 0) counts[warp] = mine;
+    __syncthreads();
+    n = 0;
+    for (int w = 0; w < kGatherThreads / 32; ++w) {
+      if (w < warp) at += counts[w];
+      n += counts[w];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (kept[k]) few[at + __popc(votes[k] & ((1u << lane) - 1))] = warp * 128 + 32 * k + lane;
+      at += __popc(votes[k]);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+      for (int k = threadIdx.x; k < a.tokens; k += kGatherThreads) a.rows[k] = k < n ? few[k] : -1;
+      if (threadIdx.x == 0) a.rows[a.tokens] = n, *a.ticket = 0;
+    }
+  } else {
+    n = a.rows[a.tokens];
+  }
+  [[maybe_unused]] Scales scales = {};
+  if constexpr (BACKWARD) {
+    if (a.reduction == ZERO_LOSS_NONE) {
+      scales = *a.scales;
+    } else {
+      scales = scales_of_one(a, n);
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.scales = scales;
+    }
+  }
+  const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x) >> a.log_lanes;
   const int words = static_cast<int>(a.hidden * 2 / sizeof(W));
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kGatherThreads / 32) + (threadIdx.x >> 5); i < a.rows_cap;
-       i += warps) {
-    if (i < up(n, kTileM)) {
-      const int t = i < n ? a.rows[i] : -1;
-      W* to = reinterpret_cast<W*>(static_cast<char*>(a.xs) + i * a.xs_stride * 2);
-      if (t >= 0 && t < a.tokens) {
-        const W* from = reinterpret_cast<const W*>(static_cast<const char*>(a.x) + t * a.x_stride * 2);
-#pragma unroll 4
-        for (int c = lane; c < words; c += 32) to[c] = from[c];
-        if (lane == 0) {
-          const int target = load_target(a, t);
-          a.target[i] = target;
-          if constexpr (BACKWARD) {
-            a.lse2[i] = a.lse[t] * kLog2e;
-            const float g = a.reduction == ZERO_LOSS_NONE ? a.d[t] : a.scales->g;
-            a.row_mul[i] = target < 0 ? 0.f : g * a.scales->mul;
-          }
-        }
-      } else {
-        for (int c = lane; c < words; c += 32) to[c] = W();
-        if (lane == 0) {
-          a.target[i] = -1;
-          if constexpr (BACKWARD) a.lse2[i] = 0.f, a.row_mul[i] = 0.f;
-        }
+  W* to = reinterpret_cast<W*>(static_cast<char*>(a.xs) + i * a.xs_stride * 2);
+  const int t = i >= n ? -1 : KIND == kForwardFew ? few[i] : a.rows[i];
+  if (t >= 0 && t < a.tokens) {
+    const W* from = reinterpret_cast<const W*>(static_cast<const char*>(a.x) + t * a.x_stride * 2);
+    for (int c = lane; c < words; c += 4 * lanes) {
+      W v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = from[min(c + k * lanes, words - 1)];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + k * lanes < words) to[c + k * lanes] = v[k];
+    }
+    if (lane == 0) {
+      const int target = load_target(a, t);
+      a.target[i] = target;
+      if constexpr (BACKWARD) {
+        a.lse2[i] = a.lse[t] * kLog2e;
+        const float g = a.reduction == ZERO_LOSS_NONE ? a.d[t] : scales.g;
+        a.row_mul[i] = target < 0 ? 0.f : g * scales.mul;
       }
     }
-    if constexpr (BACKWARD) {
-      if (a.dx && i < a.tokens && load_target(a, i) < 0) {
-        W* to = reinterpret_cast<W*>(static_cast<char*>(a.dx) + i * a.hidden * 2);
-        for (int c = lane; c < words; c += 32) to[c] = W();
-      }
+  } else if (i < n || (BACKWARD && i < up(n, kTileK))) {
+    for (int c = lane; c < words; c += lanes) to[c] = W();
+    if (lane == 0 && i < n) {
+      a.target[i] = -1;
+      if constexpr (BACKWARD) a.lse2[i] = 0.f, a.row_mul[i] = 0.f;
+    }
+  }
+  if constexpr (BACKWARD) {
+    if (a.dx && i < a.tokens && load_target(a, i) < 0) {
+      W* out = reinterpret_cast<W*>(static_cast<char*>(a.dx) + i * a.hidden * 2);
+      for (int c = lane; c < words; c += lanes) out[c] = W();
     }
   }
 }
 
-// w at a stride that the bulk copies can take.
-__global__ void __launch_bounds__(kGatherThreads) k_loss_repack(const uint16_t* __restrict__ w, int64_t stride,
-                                                                uint16_t* __restrict__ to, int64_t to_stride,
-                                                                int64_t rows, int hidden) {
+// Rows to another stride: w to one that the bulk copies can take, dw back from
+// one that whole words can be stored to.
+template <class T>
+__global__ void __launch_bounds__(kGatherThreads) k_loss_repack(const T* __restrict__ from, int64_t from_stride,
+                                                                T* __restrict__ to, int64_t to_stride, int64_t rows,
+                                                                int hidden, int log_lanes) {
   let_next_start();
   wait_for_previous();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kGatherThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kGatherThreads / 32) + (threadIdx.x >> 5); i < rows; i += warps)
-#pragma unroll 8
-    for (int c = lane; c < hidden; c += 32) to[i * to_stride + c] = w[i * stride + c];
+  const int lanes = 1 << log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x) >> log_lanes;
+  if (i >= rows) return;
+  for (int c = lane; c < hidden; c += 8 * lanes) {
+    T v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = from[i * from_stride + min(c + k * lanes, hidden - 1)];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k * lanes < hidden) to[i * to_stride + c + k * lanes] = v[k];
+  }
 }
 
-// Every kept row's statistics joined over the column tiles, eight threads a
-// row; the CTA that is last adds the losses up, in one order.
-constexpr int kFinishRows = 32, kFinishThreads = 256;
+// Statistics of parts of a row, base 2: the larger maximum, the sum under it.
+__device__ __forceinline__ void join(float& top, float& sum, float other_top, float other_sum) {
+  const float most = fmaxf(top, other_top), base = most == -INFINITY ? 0.f : most;
+  sum = sum * tc::exp2_of(top - base) + other_sum * tc::exp2_of(other_top - base);
+  top = most;
+}
+
+// Every kept row's statistics joined over its parts, 32 threads a row; the CTA
+// that is last adds the losses up, in one order.
+constexpr int kFinishRows = 8, kFinishGroups = 32, kFinishThreads = kFinishRows * kFinishGroups, kFinishAhead = 8;
 __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a) {
-  __shared__ float2 part[kFinishThreads / kFinishRows][kFinishRows];
-  __shared__ float sums[kFinishThreads / 32];
+  __shared__ float2 part[kFinishGroups][kFinishRows + 1];
+  __shared__ float sums[kFinishThreads / 32], mine[kFinishRows];
   __shared__ bool last;
   wait_for_previous();
   const int n = a.rows[a.tokens];
-  const int r = threadIdx.x % kFinishRows, g = threadIdx.x / kFinishRows;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFinishRows + r;
-  float top = -INFINITY, sum = 0.f;
-  if (i < n) {
-#pragma unroll 4
-    for (int v = g; v < a.column_tiles; v += kFinishThreads / kFinishRows) {
-      const float2 p = a.part[v * a.rows_cap + i];
-      const float most = fmaxf(top, p.x), at = most == -INFINITY ? 0.f : most;
-      sum = sum * exp2f(top - at) + p.y * exp2f(p.x - at);
-      top = most;
+  const int parts = a.parts;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kFinishRows, rows = up(n, kTileM);
+  {
+    const int r = threadIdx.x % kFinishRows, g = threadIdx.x / kFinishRows;
+    float top = -INFINITY, sum = 0.f;
+    if (i0 + r < n) {
+      const float2* from = a.part + i0 + r;
+      for (int v = g; v < parts; v += kFinishAhead * kFinishGroups) {
+        float2 p[kFinishAhead];
+#pragma unroll
+        for (int k = 0; k < kFinishAhead; ++k)
+          p[k] = from[min(v + k * kFinishGroups, parts - 1) * rows];
+#pragma unroll
+        for (int k = 0; k < kFinishAhead; ++k)
+          if (v + k * kFinishGroups < parts) join(top, sum, p[k].x, p[k].y);
+      }
+    }
+    part[g][r] = make_float2(top, sum);
+  }
+  __syncthreads();
+  {
+    const int r = threadIdx.x / kFinishGroups, g = threadIdx.x % kFinishGroups;  // a warp a row
+    const int64_t i = i0 + r;
+    float2 p = part[g][r];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      join(p.x, p.y, __shfl_xor_sync(kFull, p.x, o), __shfl_xor_sync(kFull, p.y, o));
+    if (g == 0) {
+      float loss = 0.f;
+      if (i < n) {
+        const int t = a.rows[i];
+        const float lse2 = p.x + log2f(p.y);
+        loss = (lse2 - a.target_z[i]) * kLn2;
+        a.lse_out[t] = lse2 * kLn2;
+        a.losses[t] = loss;
+      }
+      mine[r] = loss;
+      if (i < a.tokens && load_target(a, i) < 0) a.lse_out[i] = 0.f, a.losses[i] = 0.f;
     }
   }
-  part[g][r] = make_float2(top, sum);
   __syncthreads();
-  if (g == 0) {
-    for (int k = 1; k < kFinishThreads / kFinishRows; ++k) {
-      const float2 p = part[k][r];
-      const float most = fmaxf(top, p.x), at = most == -INFINITY ? 0.f : most;
-      sum = sum * exp2f(top - at) + p.y * exp2f(p.x - at);
-      top = most;
+  // a CTA's losses, then in the last one the CTAs' sums, each thread's with what
+  // its additions lose
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+    for (int k = 0; k < kFinishRows; ++k) s += mine[k];
+    if (gridDim.x == 1) {
+      sums[0] = s;
+      last = true;
+    } else {
+      a.cta_sums[blockIdx.x] = s;
+      __threadfence();
+      last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
     }
-    if (i < n) {
-      const int t = a.rows[i];
-      const float lse2 = top + log2f(sum);
-      a.lse_out[t] = lse2 * kLn2;
-      a.losses[t] = (lse2 - a.target_z[i]) * kLn2;
-    }
-    if (i < a.tokens && load_target(a, i) < 0) a.lse_out[i] = 0.f, a.losses[i] = 0.f;
   }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  // a thread's sum with what its additions lose
   float s = 0.f, lost = 0.f;
-  for (int64_t t = threadIdx.x; t < a.tokens; t += kFinishThreads) {
-    const float v = __ldcg(a.losses + t), next = s + v;
-    lost += fabsf(s) >= fabsf(v) ? (s - next) + v : (v - next) + s;
-    s = next;
+  if (gridDim.x == 1) {
+    s = threadIdx.x == 0 ? sums[0] : 0.f;
+    __syncthreads();
+  } else {
+    __threadfence();
+    const int64_t ctas = gridDim.x;
+    for (int64_t t = threadIdx.x; t < ctas; t += 8 * kFinishThreads) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __ldcg(a.cta_sums + min(t + k * kFinishThreads, ctas - 1));
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (t + k * kFinishThreads < ctas) {
+          const float next = s + v[k];
+          lost += fabsf(s) >= fabsf(v[k]) ? (s - next) + v[k] : (v[k] - next) + s;
+          s = next;
+        }
+    }
+    if (isfinite(s)) s += lost;
   }
-  if (isfinite(s)) s += lost;
   s = warp_all_sum(s);
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
   __syncthreads();
@@ -697,7 +830,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
   }
 }
 
-// dx from its binary32 sums, where there is more than one part.
+// dx from its binary32 sums, where the product did not write it.
 struct JoinArgs {
   const int32_t* rows;
   int64_t tokens;
@@ -705,25 +838,56 @@ struct JoinArgs {
   int64_t sums_stride;
   const Scales* scales;
   void* dx;
-  int32_t hidden, type, piece, pieces, pairs;
+  int32_t hidden, piece, pieces, pairs, direct, log_lanes, vec;
 };
+template <class T>
 __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a) {
   wait_for_previous();
   const int n = a.rows[a.tokens];
-  const int64_t tiles = over(n, kTileM) * over(a.hidden, kTileN);
-  const int splits = split_of(tiles, a.piece, a.pairs);
-  if (splits == 1 && a.pieces == 1) return;
+  const int splits = split_of(over(n, kTileM) * over(a.hidden, kTileN), a.piece, a.pairs);
+  if (splits == 1 && a.pieces == 1 && a.direct) return;
+  const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x) >> a.log_lanes;
+  if (i >= n) return;
+  const int64_t t = a.rows[i];
+  if (t < 0 || t >= a.tokens) return;
   const float alpha = a.scales->alpha;
   const int64_t part = up(n, kTileM) * a.sums_stride;
-  const int64_t all = static_cast<int64_t>(n) * a.hidden;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x; e < all;
-       e += static_cast<int64_t>(gridDim.x) * kGatherThreads) {
-    const int64_t i = e / a.hidden, c = e - i * a.hidden;
-    const float* p = a.sums + i * a.sums_stride + c;
-    float s = 0.f;
-    for (int k = 0; k < splits; ++k) s += p[k * part];
-    const int64_t t = a.rows[i];
-    if (t >= 0 && t < a.tokens) store_any(a.dx, t * a.hidden + c, a.type, s * alpha);
+  const float* from = a.sums + i * a.sums_stride;
+  T* to = static_cast<T*>(a.dx) + t * a.hidden;
+  // eight columns side by side, or `lanes` apart where dx's rows start anywhere
+  const int next = a.vec ? 1 : lanes;
+  for (int c = a.vec ? 8 * lane : lane; c < a.hidden; c += 8 * lanes) {
+    float s[8] = {};
+    for (int k = 0; k < splits; k += 4) {
+      float v[4][8];
+      if (a.vec) {
+        Octet<float> o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q].load(from + min(k + q, splits - 1) * part + c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q].widen(v[q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[q][j] = from[min(k + q, splits - 1) * part + min(c + j * next, a.hidden - 1)];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (k + q < splits)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] += v[q][j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] *= alpha;
+    if (a.vec) {
+      Elem<T>::store8(to + c, s);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j * next < a.hidden) to[c + j * next] = Elem<T>::narrow(s[j]);
+    }
   }
 }
 
@@ -732,12 +896,13 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a) 
 
 // Where a call's scratch lies.
 struct Layout {
-  int64_t rows_cap, column_tiles, columns, pieces, xs_stride, w_stride, sums_stride;
-  int64_t xs, w, part, target_z, target, ticket, lse2, row_mul, scales, dz, sums, bytes;
+  int64_t rows_cap, columns, pieces, xs_stride, w_stride, sums_stride;
+  int64_t xs, w, part, target_z, target, ticket, cta_sums, lse2, row_mul, scales, dz, sums, dw, bytes;
+  bool whole;  // rows of dx and dw are whole 16-byte words: the products write them
 
-  Layout(const zero_linear_ce_desc& d, bool repack, bool backward, bool want_dx) {
+  Layout(const zero_linear_ce_desc& d, bool repack, bool backward) {
     rows_cap = up(std::max<int64_t>(d.tokens, 1), kTileM);
-    column_tiles = over(d.vocab, kTileN);
+    whole = d.hidden % 8 == 0;
     columns = up(d.vocab, kTileN);
     if (backward) columns = std::min(columns, std::max<int64_t>(kTileN, kPieceBytes / 2 / rows_cap / kTileN * kTileN));
     pieces = over(d.vocab, columns);
@@ -754,7 +919,9 @@ struct Layout {
     w = take(repack ? d.vocab * w_stride * 2 : 0);
     target = take(rows_cap * 4);
     ticket = take(4);
-    part = take(backward ? 0 : column_tiles * rows_cap * 8);
+    cta_sums = take(backward ? 0 : over(rows_cap, kFinishRows) * 4);
+    // kParts a tile and row; tiles narrower than 256 are at most three rounds of the pairs
+    part = take(backward ? 0 : std::max(kParts * over(d.vocab, kTileN) * rows_cap, INT64_C(3) * kParts * kPairsMost * kTileM) * 8);
     target_z = take(backward ? 0 : rows_cap * 4);
     lse2 = take(backward ? rows_cap * 4 : 0);
     row_mul = take(backward ? rows_cap * 4 : 0);
@@ -762,9 +929,8 @@ struct Layout {
     dz = take(backward ? rows_cap * columns * 2 : 0);
     // as many rows as there are tokens, or the parts of few
     const int64_t split_rows = static_cast<int64_t>(kPairsMost) * kTileM;
-    sums = take(backward && want_dx
-                    ? (pieces > 1 ? std::max(split_rows, rows_cap) : split_rows) * sums_stride * 4
-                    : 0);
+    sums = take(backward ? (pieces > 1 || !whole ? std::max(split_rows, rows_cap) : split_rows) * sums_stride * 4 : 0);
+    dw = take(backward && !whole ? columns * sums_stride * 4 : 0);
     bytes = at;
   }
 };
@@ -828,6 +994,14 @@ cudaError_t pairs_of(const void* fn, int* pairs) {
   return cudaSuccess;
 }
 
+// Lanes of a row's group, a power of two: 8 to 256, `each` columns a lane.
+int lanes_for(int64_t hidden, int each) {
+  int log_lanes = 3;
+  while (log_lanes < 8 && (static_cast<int64_t>(each) << log_lanes) < hidden) ++log_lanes;
+  return log_lanes;
+}
+int64_t ctas_for(int64_t rows, int log_lanes) { return std::max<int64_t>(1, over(rows, kGatherThreads >> log_lanes)); }
+
 template <class... P>
 cudaError_t launch(void (*fn)(P...), int64_t grid, int threads, size_t smem, bool early, cudaStream_t s, P... args) {
   cudaLaunchConfig_t cfg = {};
@@ -855,13 +1029,10 @@ cudaError_t launch_product(ProductArgs& a, cudaStream_t s) {
                 static_cast<const ProductArgs>(a));
 }
 
-cudaError_t launch_gather(const RowsArgs& a, bool backward, cudaStream_t s) {
-  const int64_t grid = std::min<int64_t>(over(a.rows_cap, kGatherThreads / 32), kSMs * 8);
-  if (a.vec)
-    return backward ? launch(&k_loss_gather<uint4, true>, grid, kGatherThreads, 0, true, s, a)
-                    : launch(&k_loss_gather<uint4, false>, grid, kGatherThreads, 0, true, s, a);
-  return backward ? launch(&k_loss_gather<uint16_t, true>, grid, kGatherThreads, 0, true, s, a)
-                  : launch(&k_loss_gather<uint16_t, false>, grid, kGatherThreads, 0, true, s, a);
+template <Gather KIND>
+cudaError_t launch_gather(const RowsArgs& a, bool early, cudaStream_t s) {
+  return launch(a.vec ? &k_loss_gather<uint4, KIND> : &k_loss_gather<uint16_t, KIND>, ctas_for(a.rows_cap, a.log_lanes),
+                kGatherThreads, 0, early, s, a);
 }
 
 zero_status check_desc(const char* fn, const zero_linear_ce_desc* d) {
@@ -916,12 +1087,13 @@ struct Call {
   template <class T>
   T* in(int64_t offset) const { return reinterpret_cast<T*>(ws + offset); }
 
+  void set_vec(bool vec) { rows.vec = vec, rows.log_lanes = lanes_for(d.hidden, vec ? 32 : 4); }
   zero_status begin(const char* fn, const void* x, const void* targets, int32_t* row_list, int32_t* err) {
     rows.targets = targets, rows.id_bytes = d.id_bytes, rows.vocab = static_cast<int32_t>(d.vocab);
     rows.tokens = d.tokens, rows.hidden = d.hidden, rows.rows = row_list, rows.ticket = in<int32_t>(at.ticket);
     rows.x = x, rows.x_stride = d.x_stride, rows.xs = in<void>(at.xs), rows.xs_stride = at.xs_stride;
     rows.rows_cap = at.rows_cap, rows.target = in<int32_t>(at.target);
-    rows.vec = d.hidden % 8 == 0 && d.x_stride % 8 == 0 && aligned_to(x, 16);
+    set_vec(d.hidden % 8 == 0 && d.x_stride % 8 == 0 && aligned_to(x, 16));
     product.count = row_list + d.tokens, product.rows_cap = at.rows_cap;
     product.vocab = static_cast<int32_t>(d.vocab), product.hidden = static_cast<int32_t>(d.hidden);
     product.bf16 = bf16, product.err = err, product.scale2 = static_cast<float>(d.scale * 1.4426950408889634);
@@ -933,21 +1105,29 @@ struct Call {
     LOSS_CUDA(facts.allow(k, kSmemBytes, kSmemBytes));
     LOSS_CUDA(pairs_of(k, &pairs));
     product.pairs = pairs;
+    product.rows_a = d.tokens < kHalfRows ? static_cast<int32_t>(up(std::max<int64_t>(d.tokens, 1), 16)) : kHalfRows;
+    return ZERO_OK;
+  }
+  template <class T>
+  zero_status copy_rows(const char* fn, const T* from, int64_t from_stride, T* to, int64_t to_stride, int64_t n) {
+    const int log_lanes = lanes_for(d.hidden, 8);
+    LOSS_CUDA(launch(&k_loss_repack<T>, ctas_for(n, log_lanes), kGatherThreads, 0, true, s, from, from_stride, to,
+                     to_stride, n, static_cast<int>(d.hidden), log_lanes));
     return ZERO_OK;
   }
   zero_status repack(const char* fn) {
     if (!wants_repack(d, w)) return ZERO_OK;
     uint16_t* to = in<uint16_t>(at.w);
-    LOSS_CUDA(launch(&k_loss_repack, std::min<int64_t>(over(d.vocab, kGatherThreads / 32), kSMs * 8), kGatherThreads, 0,
-                     true, s, static_cast<const uint16_t*>(w), d.w_stride, to, at.w_stride, d.vocab,
-                     static_cast<int>(d.hidden)));
+    LOSS_TRY(copy_rows(fn, static_cast<const uint16_t*>(w), d.w_stride, to, at.w_stride, d.vocab));
     w = to;
     return ZERO_OK;
   }
-  // rows of xs and of w, contiguous along the depth
-  bool maps_of_z() {
-    return matrix_map(&product.a, in<void>(at.xs), bf16, d.hidden, at.rows_cap, at.xs_stride, kHalfRows) &&
-           matrix_map(&product.b, w, bf16, d.hidden, d.vocab, at.w_stride, kHalfRows);
+  // rows of xs and of w, contiguous along the depth; tiles for `columns` of z
+  bool maps_of_z(int64_t columns) {
+    product.tile = tile_columns(at.rows_cap / kTileM, columns, product.pairs);
+    const void* xs = in<void>(at.xs);
+    return matrix_map(&product.a, xs, bf16, d.hidden, at.rows_cap, at.xs_stride, product.rows_a) &&
+           matrix_map(&product.b, w, bf16, d.hidden, d.vocab, at.w_stride, product.tile / 2);
   }
 };
 
@@ -981,7 +1161,7 @@ extern "C" zero_status zero_linear_cross_entropy_workspace_bytes(const zero_line
   clear_error();
   if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
   LOSS_TRY(check_desc(fn, desc));
-  *bytes = Layout(*desc, wants_repack(*desc, w), backward != 0, true).bytes;
+  *bytes = Layout(*desc, wants_repack(*desc, w), backward != 0).bytes;
   return ZERO_OK;
 }
 
@@ -1003,7 +1183,7 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
   LOSS_TRY(check_ptr(fn, "rows", rows, 4, true));
   LOSS_TRY(check_ptr(fn, "total", total, 4, true));
   LOSS_TRY(check_ptr(fn, "workspace", workspace, 256, true));
-  const Layout at(d, wants_repack(d, w), false, false);
+  const Layout at(d, wants_repack(d, w), false);
   if (workspace_bytes < at.bytes)
     return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes,
                 at.bytes);
@@ -1017,16 +1197,20 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
   LOSS_TRY(ready(fn, &err));
   Call c(d, at, workspace, stream, w);
   LOSS_TRY(c.begin(fn, x, targets, rows, err));
-  LOSS_CUDA(launch(&k_loss_rows, 1, kScanThreads, 0, false, c.s, static_cast<const RowsArgs>(c.rows)));
-  LOSS_CUDA(launch_gather(c.rows, false, c.s));
+  if (d.tokens <= kFewTokens) {
+    LOSS_CUDA(launch_gather<kForwardFew>(c.rows, false, c.s));
+  } else {
+    LOSS_CUDA(launch(&k_loss_rows, 1, kScanThreads, 0, false, c.s, static_cast<const RowsArgs>(c.rows)));
+    LOSS_CUDA(launch_gather<kForward>(c.rows, true, c.s));
+  }
   LOSS_TRY(c.repack(fn));
-  if (!c.maps_of_z()) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
+  if (!c.maps_of_z(d.vocab)) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   c.product.columns = static_cast<int32_t>(d.vocab);
   c.product.part = c.in<float2>(at.part), c.product.target_z = c.in<float>(at.target_z);
   LOSS_CUDA(launch_product<kStats>(c.product, c.s));
+  c.rows.parts = static_cast<int32_t>(kParts * over(d.vocab, c.product.tile));
   c.rows.part = c.product.part, c.rows.target_z = c.product.target_z;
-  c.rows.column_tiles = static_cast<int32_t>(at.column_tiles);
-  c.rows.losses = losses, c.rows.lse_out = lse, c.rows.total = total;
+  c.rows.cta_sums = c.in<float>(at.cta_sums), c.rows.losses = losses, c.rows.lse_out = lse, c.rows.total = total;
   LOSS_CUDA(launch(&k_loss_finish, std::max<int64_t>(1, over(d.tokens, kFinishRows)), kFinishThreads, 0, true, c.s,
                    static_cast<const RowsArgs>(c.rows)));
   return ZERO_OK;
@@ -1058,7 +1242,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   LOSS_TRY(check_ptr(fn, "workspace", workspace, 256, true));
   if (!any) dx = nullptr;
   if (!dx && !dw) return ZERO_OK;
-  const Layout at(d, wants_repack(d, w), true, true);
+  const Layout at(d, wants_repack(d, w), true);
   if (workspace_bytes < at.bytes)
     return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes,
                 at.bytes);
@@ -1077,11 +1261,13 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   c.rows.lse = lse, c.rows.d = d_loss, c.rows.reduction = reduction, c.rows.scale = d.scale;
   c.rows.scales = c.in<Scales>(at.scales), c.rows.lse2 = c.in<float>(at.lse2), c.rows.row_mul = c.in<float>(at.row_mul);
   c.rows.dx = dx;
-  c.rows.vec = c.rows.vec && aligned_to(dx, 16);
-  LOSS_CUDA(launch(&k_loss_scales, 1, kScanThreads, 0, false, c.s, static_cast<const RowsArgs>(c.rows)));
-  LOSS_CUDA(launch_gather(c.rows, true, c.s));
+  c.set_vec(c.rows.vec && aligned_to(dx, 16));
+  const bool own_gradients = reduction == ZERO_LOSS_NONE;
+  if (own_gradients)
+    LOSS_CUDA(launch(&k_loss_scales, 1, kScanThreads, 0, false, c.s, static_cast<const RowsArgs>(c.rows)));
+  LOSS_CUDA(launch_gather<kBackward>(c.rows, own_gradients, c.s));
   LOSS_TRY(c.repack(fn));
-  if (!c.maps_of_z()) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
+  if (!c.maps_of_z(std::min(at.columns, d.vocab))) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   ProductArgs z = c.product;
   z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.dz = c.in<void>(at.dz), z.dz_stride = at.columns;
   for (int64_t first = 0; first < d.vocab; first += at.columns) {
@@ -1091,26 +1277,41 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
     ProductArgs p = z;
     p.scales = c.rows.scales;
     if (dx) {
-      p.out = dx, p.out_type = d.dtype, p.out_align = align_of(dx, d.hidden * 2);
-      p.sums = c.in<float>(at.sums), p.sums_stride = at.sums_stride, p.add = first > 0;
+      p.out = dx, p.out_type = d.dtype, p.out_align = align_of(dx, d.hidden * 2), p.out_stride = d.hidden;
+      p.sums = c.in<float>(at.sums), p.sums_stride = at.sums_stride, p.add = first > 0, p.direct = at.whole;
       if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.rows_cap, at.columns, kHalfRows) ||
           !matrix_map(&p.b, c.w, c.bf16, d.hidden, d.vocab, at.w_stride, kTileK))
         return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
       LOSS_CUDA(launch_product<kDx>(p, c.s));
     }
     if (dw) {
-      p.out = dw, p.out_type = dw_dtype, p.out_align = align_of(dw, d.hidden * type_bytes(dw_dtype));
+      // rows that start anywhere are written to a padded copy first: single
+      // columns from a row a thread take 77 us where both copies take TIME_DW
+      // (5003 x 1001 fp16)
+      p.out = at.whole ? dw : c.in<void>(at.dw), p.out_type = dw_dtype;
+      p.out_first = at.whole ? first : 0, p.out_stride = at.whole ? d.hidden : at.sums_stride;
+      p.out_align = align_of(p.out, p.out_stride * type_bytes(dw_dtype));
       if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.rows_cap, at.columns, kTileK) ||
           !matrix_map(&p.b, c.in<void>(at.xs), c.bf16, d.hidden, at.rows_cap, at.xs_stride, kTileK))
         return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
       LOSS_CUDA(launch_product<kDw>(p, c.s));
+      if (!at.whole && dw_dtype == ZERO_FP32)
+        LOSS_TRY(c.copy_rows(fn, c.in<float>(at.dw), at.sums_stride, static_cast<float*>(dw) + first * d.hidden,
+                             d.hidden, columns));
+      else if (!at.whole)
+        LOSS_TRY(c.copy_rows(fn, c.in<uint16_t>(at.dw), at.sums_stride, static_cast<uint16_t*>(dw) + first * d.hidden,
+                             d.hidden, columns));
     }
   }
   if (dx) {
-    const JoinArgs j = {rows, d.tokens, c.in<float>(at.sums), at.sums_stride, c.rows.scales, dx,
-                        static_cast<int32_t>(d.hidden), d.dtype, static_cast<int32_t>(at.columns),
-                        static_cast<int32_t>(at.pieces), c.product.pairs};
-    LOSS_CUDA(launch(&k_loss_join, kSMs * 8, kGatherThreads, 0, true, c.s, j));
+    JoinArgs j = {};
+    j.rows = rows, j.tokens = d.tokens, j.sums = c.in<float>(at.sums), j.sums_stride = at.sums_stride;
+    j.scales = c.rows.scales, j.dx = dx;
+    j.hidden = static_cast<int32_t>(d.hidden), j.piece = c.product.piece, j.pieces = c.product.pieces;
+    j.pairs = c.product.pairs, j.direct = at.whole, j.vec = at.whole && aligned_to(dx, 16);
+    j.log_lanes = lanes_for(d.hidden, 8);
+    LOSS_CUDA(launch(c.bf16 ? &k_loss_join<__nv_bfloat16> : &k_loss_join<__half>, ctas_for(d.tokens, j.log_lanes),
+                     kGatherThreads, 0, true, c.s, j));
   }
   return ZERO_OK;
 }

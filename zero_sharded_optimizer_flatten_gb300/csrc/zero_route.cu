@@ -14,9 +14,10 @@
 //
 // A warp has a token, each lane VPT neighbouring experts in registers; the
 // choices come one after the other as the warp's largest value. What bounds
-// large calls is issue slots: topk rounds of some 30 instructions a token. Each
-// CTA leaves its counts and sums of p in the workspace, added up in order by
-// k_route_finish, so the same call gives the same bits.
+// large calls is issue slots (see k_route). Each CTA leaves its counts and sums
+// of p in the workspace, added up in order by k_route_finish, so the same call
+// gives the same bits; a call that one CTA does has no second launch.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <inttypes.h>
 
@@ -26,12 +27,17 @@
 #include "zero_rows.cuh"
 #include "zero_tensor_core.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace zero {
 namespace {
 
 constexpr int kExpertsMost = 1024, kTopkMost = 32;
-constexpr int kWarps = 32, kThreads = 32 * kWarps;
+constexpr int kThreads = 1024;
 constexpr int kCtasMost = kSMs;
+constexpr int kFinishCtas = 8;  // of the finishing cluster
+// Warps of a CTA: 16 experts a lane and more take more registers.
+constexpr int warps_of(int vpt) { return vpt <= 8 ? 32 : 16; }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct RouteArgs {
@@ -53,22 +59,36 @@ struct RouteArgs {
   void* dz;
 };
 
-// Values in order as unsigned numbers, +-0 alike, NaN last; kNone: -inf or less.
-constexpr uint32_t kNone = 0x007fffffu, kNan = 0xffffffffu;
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
-  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return v != v ? kNan : k;
-}
-__device__ __forceinline__ float value_of(uint32_t k) {
-  if (k == kNan) return __uint_as_float(0x7fffffffu);
-  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // A lane's VPT values of a row, `fill` past its end.
 template <class T, int VPT>
 __device__ __forceinline__ void load_row(const T* row, int lane, int experts, bool vec, float fill, float (&v)[VPT]) {
-  if constexpr (VPT * sizeof(T) >= 16) {
+  if constexpr (VPT * sizeof(T) >= 32) {
+    if (vec) {  // 32 bytes a load: by 16 a warp touches every line twice
+      constexpr int kLoads = VPT * sizeof(T) / 32, kEach = 32 / sizeof(T);
+      uint32_t w[kLoads][8];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]), "=r"(w[i][4]), "=r"(w[i][5]),
+                       "=r"(w[i][6]), "=r"(w[i][7])
+                     : "l"(row + lane * VPT + i * kEach));
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if constexpr (sizeof(T) == 4)
+            v[i * kEach + j] = __uint_as_float(w[i][j]);
+          else
+            Elem<T>::unpack(w[i][j], v[i * kEach + 2 * j], v[i * kEach + 2 * j + 1]);
+      return;
+    }
+  } else if constexpr (VPT * sizeof(T) == 16) {
     if (vec) {
       constexpr int kWords = VPT * sizeof(T) / 16, kEach = 16 / sizeof(T);
       uint4 w[kWords];
@@ -92,14 +112,49 @@ __device__ __forceinline__ void load_row(const T* row, int lane, int experts, bo
     v[j] = lane * VPT + j < experts ? Elem<T>::widen(row[lane * VPT + j]) : fill;
 }
 
+// The results that need all tokens, from the experts' counts and sums of p (of
+// thread e, up to the CTA's size at a time) and the tokens' n and sum of lse^2.
+struct Totals {
+  float product = 0.f;
+  __device__ __forceinline__ void expert(const RouteArgs& a, int e, int count, float sum) {
+    a.counts[e] = count;
+    product = fmaf(static_cast<float>(count), sum, product);
+  }
+  // every thread of the CTA; part: a float a warp
+  __device__ __forceinline__ void finish(const RouteArgs& a, float n, float squares, float* part) {
+    const float s = warp_all_sum(product);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float all = 0.f;
+      for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) all += part[w];
+      const float by = fmaxf(n, 1.f);
+      a.losses[0] = all * (static_cast<float>(a.experts) / static_cast<float>(a.topk)) / by / by;
+      a.losses[1] = squares / by;
+      a.stats[a.tokens] = n;
+    }
+  }
+};
+
+// A token's choices. The K-th largest different lane maximum is a bound that at
+// least K values reach (a redux a round); the few that do are put side by side,
+// a lane each, and every one finds its rank by comparing itself with all of
+// them. Where more than a warp of them reach it (many equal values), they are
+// taken one after the other instead: the warp's largest value, the first lane
+// that holds it and there the first place. NaN counts as +inf.
+//
+// Measured, 65536 tokens, 8 of 256 fp32 (67 MB): TIME_ROUTE us; one after the
+// other always 53, by integer keys 74.
 template <class T, int VPT>
-__global__ void __launch_bounds__(kThreads, VPT <= 8 ? 2 : 1) k_route(const RouteArgs a) {
+__global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs a) {
+  constexpr int kWarps = warps_of(VPT);
   extern __shared__ int smem[];  // [experts] counts, [kWarps][experts] sums of p
-  __shared__ float ends[kWarps][2];
+  __shared__ float ends[kWarps][2], part[kWarps];
+  __shared__ float2 candidates[kWarps][32];
   let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, K = a.topk;
   float* sums = reinterpret_cast<float*>(smem + E);
-  for (int e = threadIdx.x; e < E; e += kThreads) smem[e] = 0;
+  for (int e = threadIdx.x; e < E; e += 32 * kWarps) smem[e] = 0;
   __syncthreads();
   float total[VPT];
 #pragma unroll
@@ -110,41 +165,81 @@ __global__ void __launch_bounds__(kThreads, VPT <= 8 ? 2 : 1) k_route(const Rout
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.tokens; t += step) {
     float v[VPT];
     load_row<T, VPT>(z + t * a.stride, lane, E, a.vec, -INFINITY, v);
-    uint32_t key[VPT];
-    uint32_t most = 0;
-    int where = 0;
+    float most = -INFINITY;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      key[j] = key_of(v[j]);
-      if (key[j] > most) most = key[j], where = j;  // the first of equal ones
+      v[j] = fminf(v[j], INFINITY);  // NaN to +inf
+      most = fmaxf(most, v[j]);
     }
-    uint32_t chosen_key = 0;
-    int chosen = -1;
-    float top = 0.f;
-    for (int k = 0; k < K; ++k) {
-      const uint32_t best = __reduce_max_sync(kFull, most);
-      if (k == 0) top = best > kNone ? value_of(best) : 0.f;
-      if (best <= kNone) break;  // the same for all lanes
-      const int owner = __ffs(__ballot_sync(kFull, most == best)) - 1;
-      const int e = __shfl_sync(kFull, lane * VPT + where, owner);
-      if (lane == k) chosen = e, chosen_key = best;
-      if (lane == owner) {
-        most = 0;
-        int next = 0;
+    float bound = warp_max(most), x = most;
+    const bool any = bound > -INFINITY;
+    const float top = any ? bound : 0.f;
+    for (int k = 1; k < K; ++k) {
+      x = x == bound ? -INFINITY : x;
+      bound = warp_max(x);
+    }
+    // choice `slot` of the token, of this lane
+    float chosen_z = -INFINITY;
+    int chosen = -1, slot = lane;
+    unsigned reach[VPT];
+    int count = 0;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          if (j == where) key[j] = 0;
-          if (key[j] > most) most = key[j], next = j;
+    for (int j = 0; j < VPT; ++j) {
+      reach[j] = __ballot_sync(kFull, v[j] >= bound && v[j] > -INFINITY);
+      count += __popc(reach[j]);
+    }
+    if (count <= 32) {
+      int at = 0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        if (reach[j] >> lane & 1)
+          candidates[warp][at + __popc(reach[j] & ((1u << lane) - 1))] = make_float2(v[j], __int_as_float(lane * VPT + j));
+        at += __popc(reach[j]);
+      }
+      __syncwarp();
+      const float2 own = candidates[warp][lane];
+      const int e = __float_as_int(own.y);
+      int rank = 0;
+      for (int c = 0; c < count; ++c) {
+        const float2 other = candidates[warp][c];
+        rank += other.x > own.x || (other.x == own.x && __float_as_int(other.y) < e);
+      }
+      __syncwarp();
+      const bool takes = lane < count && rank < K;
+      if (takes) chosen = e, chosen_z = own.x, slot = rank;
+      if (count < K && lane >= count) {
+        // fewer experts left than choices: the slots after them stay empty
+      } else if (!takes) {
+        slot = K;
+      }
+    } else {
+      float w[VPT];  // what is not chosen yet
+      int where = 0;
+#pragma unroll
+      for (int j = VPT - 1; j >= 0; --j) w[j] = v[j], where = v[j] == most ? j : where;
+      for (int k = 0; k < K; ++k) {
+        const float best = warp_max(most);
+        if (best == -INFINITY) break;  // the same for all lanes
+        const int owner = __ffs(__ballot_sync(kFull, most == best)) - 1;
+        const int e = __shfl_sync(kFull, lane * VPT + where, owner);
+        if (lane == k) chosen = e, chosen_z = best;
+        if (lane == owner) {
+          most = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < VPT; ++j) {
+            w[j] = j == where ? -INFINITY : w[j];
+            most = fmaxf(most, w[j]);
+          }
+#pragma unroll
+          for (int j = VPT - 1; j >= 0; --j) where = w[j] == most ? j : where;
         }
-        where = next;
       }
     }
-    const bool any = __shfl_sync(kFull, chosen, 0) >= 0;
     const float top2 = top * kLog2e;
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      v[j] = any ? tc::exp2_of(fmaf(v[j], kLog2e, -top2)) : 0.f;
+      v[j] = tc::exp2_of(fmaf(v[j], kLog2e, -top2));  // 0 where nothing is left
       s += v[j];
     }
     s = warp_all_sum(s);
@@ -153,16 +248,16 @@ __global__ void __launch_bounds__(kThreads, VPT <= 8 ? 2 : 1) k_route(const Rout
     for (int j = 0; j < VPT; ++j) total[j] = fmaf(v[j], inv, total[j]);
     const float lse = any ? top + log2f(s) * kLn2 : 0.f;
     if (any) n += 1.f, squares = fmaf(lse, lse, squares);
-    float w = chosen >= 0 ? tc::exp2_of(fmaf(value_of(chosen_key), kLog2e, -top2)) : 0.f;
+    float weight = tc::exp2_of(fmaf(chosen_z, kLog2e, -top2));  // 0 without a choice
     if (a.normalize) {
-      const float all = warp_all_sum(w);
-      w = any ? w / all : 0.f;
+      const float all = warp_all_sum(weight);
+      weight = any ? weight / all : 0.f;
     } else {
-      w *= inv;
+      weight *= inv;
     }
-    if (lane < K) {
-      a.ids[t * K + lane] = chosen;
-      a.weights[t * K + lane] = w;
+    if (slot < K) {
+      a.ids[t * K + slot] = chosen;
+      a.weights[t * K + slot] = weight;
       if (chosen >= 0) atomicAdd(smem + chosen, 1);
     }
     if (lane == 0) a.stats[t] = lse;
@@ -172,71 +267,88 @@ __global__ void __launch_bounds__(kThreads, VPT <= 8 ? 2 : 1) k_route(const Rout
     if (lane * VPT + j < E) sums[warp * E + lane * VPT + j] = total[j];
   if (lane == 0) ends[warp][0] = n, ends[warp][1] = squares;
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
+  n = squares = 0.f;
+  for (int w = 0; w < kWarps; ++w) n += ends[w][0], squares += ends[w][1];
+  Totals totals;
+  for (int e = threadIdx.x; e < E; e += 32 * kWarps) {
     float s = 0.f;
     for (int w = 0; w < kWarps; ++w) s += sums[w * E + e];
     const int64_t at = static_cast<int64_t>(blockIdx.x) * E + e;
-    a.part_counts[at] = smem[e];
-    a.part_sums[at] = s;
+    if (gridDim.x == 1)
+      totals.expert(a, e, smem[e], s);
+    else
+      a.part_counts[at] = smem[e], a.part_sums[at] = s;
   }
-  if (threadIdx.x < 2) {
-    float s = 0.f;
-    for (int w = 0; w < kWarps; ++w) s += ends[w][threadIdx.x];
-    a.part_ends[blockIdx.x * 2 + threadIdx.x] = s;
-  }
+  if (gridDim.x == 1)
+    totals.finish(a, n, squares, part);
+  else if (threadIdx.x == 0)
+    a.part_ends[blockIdx.x * 2] = n, a.part_ends[blockIdx.x * 2 + 1] = squares;
 }
 
-// The CTAs' counts and sums added up, in order; one CTA: groups of threads a
-// share of the CTAs, then the groups one after the other.
-__global__ void __launch_bounds__(kThreads) k_route_finish(const RouteArgs a) {
+// The CTAs' counts and sums added up, in order: a cluster, whose groups of
+// threads take a share of the CTAs each, then the groups, then the cluster's
+// CTAs. (One CTA: 12 us for 152 CTAs of 256 experts.)
+__global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kThreads) k_route_finish(const RouteArgs a) {
   __shared__ int counts[kThreads];
-  __shared__ float sums[kThreads];
-  __shared__ float part[kWarps];
-  __shared__ float ends[2];
+  __shared__ float sums[kThreads], ends[2], part[32];
   wait_for_previous();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int me = static_cast<int>(cluster.block_rank());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
-  if (warp < 2) {  // n and the sum of squares
+  if (me == 0 && warp < 2) {  // n and the sum of squares
     float s = 0.f;
     for (int c = lane; c < a.ctas; c += 32) s += a.part_ends[c * 2 + warp];
     s = warp_all_sum(s);
     if (lane == 0) ends[warp] = s;
   }
-  const int groups = kThreads / E;  // at least one
+  const int here = kThreads / E, groups = here * kFinishCtas;  // here: at least one
   const int g = threadIdx.x / E, e = threadIdx.x - g * E;
+  const int each = (a.ctas + groups - 1) / groups;
   int count = 0;
   float sum = 0.f;
-  if (g < groups) {
-    const int each = (a.ctas + groups - 1) / groups;
-#pragma unroll 8
-    for (int c = g * each; c < min(a.ctas, (g + 1) * each); ++c) {
-      count += a.part_counts[static_cast<int64_t>(c) * E + e];
-      sum += a.part_sums[static_cast<int64_t>(c) * E + e];
+  if (g < here) {
+    const int c0 = (me * here + g) * each, c1 = min(a.ctas, c0 + each);
+    for (int c = c0; c < c1; c += 4) {
+      int n[4];
+      float s[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = static_cast<int64_t>(min(c + i, c1 - 1)) * E + e;
+        n[i] = a.part_counts[at], s[i] = a.part_sums[at];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < c1) count += n[i], sum += s[i];
     }
   }
   counts[threadIdx.x] = count, sums[threadIdx.x] = sum;
   __syncthreads();
-  float s = 0.f;
   if (threadIdx.x < E) {
-    for (int k = 1; k < groups; ++k) count += counts[k * E + e], sum += sums[k * E + e];
-    a.counts[e] = count;
-    s = static_cast<float>(count) * sum;
+    for (int k = 1; k < here; ++k) count += counts[k * E + e], sum += sums[k * E + e];
+    counts[e] = count, sums[e] = sum;
   }
-  s = warp_all_sum(s);
-  if (lane == 0) part[warp] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.f;
-    for (int w = 0; w < kWarps; ++w) s += part[w];
-    const float n = fmaxf(ends[0], 1.f);
-    a.losses[0] = s * (static_cast<float>(E) / static_cast<float>(a.topk)) / n / n;
-    a.losses[1] = ends[1] / n;
-    a.stats[a.tokens] = ends[0];
+  cluster.sync();
+  if (me == 0) {
+    Totals totals;
+    if (threadIdx.x < E) {
+      int n[kFinishCtas];
+      float s[kFinishCtas];
+#pragma unroll
+      for (int c = 0; c < kFinishCtas; ++c)
+        n[c] = cluster.map_shared_rank(counts, c)[e], s[c] = cluster.map_shared_rank(sums, c)[e];
+      count = 0, sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kFinishCtas; ++c) count += n[c], sum += s[c];
+      totals.expert(a, e, count, sum);
+    }
+    totals.finish(a, ends[0], ends[1], part);
   }
+  cluster.sync();  // no CTA leaves while the first one reads its sums
 }
 
 template <class T, int VPT>
 __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a) {
-  extern __shared__ float direct[];  // [warps][32 * VPT]
+  extern __shared__ __align__(16) float direct[];  // [warps][32 * VPT]: what the choices add
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, K = a.topk;
   float* mine = direct + warp * 32 * VPT;
 #pragma unroll
@@ -277,8 +389,19 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a) {
     if (!a.normalize) s += wd;
     const float shift = per_lse * lse - s;
     __syncwarp();
+    float extra[VPT];
+    if constexpr (VPT % 4 == 0) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) v[j] = any ? fmaf(v[j], load[j] + shift, mine[lane * VPT + j]) : 0.f;
+      for (int j = 0; j < VPT; j += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(mine + lane * VPT + j);
+        extra[j] = q.x, extra[j + 1] = q.y, extra[j + 2] = q.z, extra[j + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) extra[j] = mine[lane * VPT + j];
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) v[j] = any ? fmaf(v[j], load[j] + shift, extra[j]) : 0.f;
     __syncwarp();
     if (id >= 0) mine[id] = 0.f;
     T* row = dz + t * E;
@@ -286,6 +409,13 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a) {
       if (a.vec) {
 #pragma unroll
         for (int i = 0; i < VPT; i += 8) {
+          if constexpr (sizeof(T) == 4) {
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + lane * VPT + i),
+                         "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]),
+                         "f"(v[i + 6]), "f"(v[i + 7])
+                         : "memory");
+            continue;
+          }
           const float o[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
           Elem<T>::store8(row + lane * VPT + i, o);
         }
@@ -318,8 +448,9 @@ cudaError_t launch(void (*fn)(P...), int64_t grid, int threads, size_t smem, boo
   return e;
 }
 
-int ctas_for(int64_t tokens) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCtasMost, (tokens + kWarps - 1) / kWarps)));
+int ctas_for(int64_t tokens, int32_t experts) {
+  const int warps = warps_of((experts + 31) / 32);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCtasMost, (tokens + warps - 1) / warps)));
 }
 
 template <class T, int VPT>
@@ -327,15 +458,15 @@ cudaError_t run_route(const RouteArgs& a, bool backward, cudaStream_t s) {
   if (backward) {
     constexpr int kWarpsHere = 8;
     const int64_t grid = std::min<int64_t>(kSMs * 8, (a.tokens + kWarpsHere - 1) / kWarpsHere);
-    static_assert(kWarpsHere * 32 * 32 * 4 <= 48 * 1024, "shared memory without asking");
+    static_assert(kWarpsHere * 32 * VPT * 4 <= 48 * 1024, "shared memory without asking");
     return launch(&k_route_backward<T, VPT>, grid, 32 * kWarpsHere, kWarpsHere * 32 * VPT * 4, false, s, a);
   }
-  const size_t smem = static_cast<size_t>(kWarps + 1) * a.experts * 4;
-  constexpr int kMost = (kWarps + 1) * 32 * VPT * 4;
+  constexpr int kWarps = warps_of(VPT), kMost = (kWarps + 1) * 32 * VPT * 4;
   static KernelFacts facts;
   cudaError_t e = facts.allow(reinterpret_cast<const void*>(&k_route<T, VPT>), kMost, kMost);
-  if (e == cudaSuccess) e = launch(&k_route<T, VPT>, a.ctas, kThreads, smem, false, s, a);
-  if (e == cudaSuccess) e = launch(&k_route_finish, 1, kThreads, 0, true, s, a);
+  if (e == cudaSuccess)
+    e = launch(&k_route<T, VPT>, a.ctas, 32 * kWarps, static_cast<size_t>(kWarps + 1) * a.experts * 4, false, s, a);
+  if (e == cudaSuccess && a.ctas > 1) e = launch(&k_route_finish, kFinishCtas, kThreads, 0, true, s, a);
   return e;
 }
 
@@ -350,11 +481,11 @@ cudaError_t run_typed(const RouteArgs& a, bool backward, cudaStream_t s) {
                       : run_route<T, 32>(a, backward, s);
 }
 
-// Rows of exactly a power of two times 32 experts on 16-byte boundaries.
+// Rows of exactly a power of two times 32 experts on 32-byte boundaries.
 bool wide_rows(int experts, int64_t stride, int bytes, const void* z, const void* dz) {
   const int each = experts / 32;
-  return experts % 32 == 0 && (each & (each - 1)) == 0 && each * bytes >= 16 && stride * bytes % 16 == 0 &&
-         aligned_to(z, 16) && aligned_to(dz, 16);
+  return experts % 32 == 0 && (each & (each - 1)) == 0 && each * bytes >= 16 && stride * bytes % 32 == 0 &&
+         aligned_to(z, 32) && aligned_to(dz, 32);
 }
 
 zero_status check_shape(const char* fn, int64_t tokens, int64_t stride, int32_t experts, int32_t topk, int dtype) {
@@ -377,7 +508,7 @@ zero_status check_ptr(const char* fn, const char* what, const void* p, int bytes
 }
 
 int64_t workspace_of(int64_t tokens, int32_t experts) {
-  return static_cast<int64_t>(ctas_for(tokens)) * (experts * 2 + 2) * 4;
+  return static_cast<int64_t>(ctas_for(tokens, experts)) * (experts * 2 + 2) * 4;
 }
 
 zero_status run(const char* fn, const RouteArgs& a, int dtype, bool backward, void* stream) {
@@ -441,7 +572,7 @@ extern "C" zero_status zero_expert_route(const void* logits, int64_t logits_stri
   a.z = logits, a.tokens = tokens, a.stride = logits_stride, a.experts = n_experts, a.topk = topk;
   a.normalize = normalize != 0, a.vec = wide_rows(n_experts, logits_stride, b, logits, nullptr);
   a.ids = ids, a.weights = weights, a.counts = counts, a.losses = losses, a.stats = stats;
-  a.ctas = ctas_for(tokens);
+  a.ctas = ctas_for(tokens, n_experts);
   a.part_counts = static_cast<int32_t*>(workspace);
   a.part_sums = reinterpret_cast<float*>(a.part_counts + static_cast<int64_t>(a.ctas) * n_experts);
   a.part_ends = a.part_sums + static_cast<int64_t>(a.ctas) * n_experts;
