@@ -766,7 +766,9 @@ zero_status zero_expert_combine_backward(const void* dy, int64_t dy_stride, cons
  *   stats[t] = lse[t], stats[tokens] = n
  * Sums are binary32 in a fixed order.  n_experts at most 1024, topk at most 32,
  * tokens 2^24.  logits_stride: elements between rows.  Pointers need their
- * element's alignment only.  Outputs overlap no input and no other output.
+ * element's alignment only.  workspace: 4-byte aligned device scratch (NULL when
+ * zero_expert_route_workspace_bytes says 0).  Outputs overlap no input and no
+ * other output.
  */
 zero_status zero_expert_route(const void* logits, int64_t logits_stride, zero_dtype dtype,
                               int64_t tokens, int32_t n_experts, int32_t topk, int32_t normalize,

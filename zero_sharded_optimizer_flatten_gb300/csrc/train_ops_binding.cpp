@@ -572,7 +572,7 @@ PyObject* expert_route(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const at::TensorOptions f = s.z.options().dtype(at::kFloat), i = s.z.options().dtype(at::kInt);
     const Tensor ids = at::empty({s.tokens, topk}, i), weights = at::empty({s.tokens, topk}, f),
                  counts = at::empty({s.experts}, i), losses = at::empty({2}, f), stats = at::empty({s.tokens + 1}, f);
-    const Tensor ws = workspace_of(a[3], need, s.z);
+    const Tensor ws = need ? workspace_of(a[3], need, s.z) : Tensor();
     void* stream = stream_of(s.dev);
     unlocked([&] {
       return zero_expert_route(ptr(s.z), s.stride, static_cast<zero_dtype>(s.type), s.tokens, s.experts, topk, normalize,

@@ -10,13 +10,13 @@
 // others are first copied together ("kept rows"), so that all products are
 // over them alone and nothing of a left-out row is read.
 //
-// Four products of one kernel (k_loss_product) make up the two passes:
+// One kernel (k_loss_product) does the products of both passes:
 //   kStats  tiles of z, of which only every row's maximum and sum of
 //           exponentials leave the SM; joined by k_loss_finish
 //   kProbs  tiles of z again, to dz in 16 bits, a piece of the vocabulary at a
 //           time (kPieceBytes)
-//   kDx     dz w, summed over the pieces in binary32
-//   kDw     dz^T x, the piece's rows of dw
+//   kGrads  dz w, summed over the pieces in binary32 (kDx), and dz^T x, the
+//           piece's rows of dw (kDw), whose tiles fill each other's last round
 // The second forming of z is a quarter of the operations: the price of keeping
 // no logits between the passes.
 #include <cuda.h>
@@ -51,7 +51,7 @@ constexpr int kGroupM = 8;  // row tiles that run through the column tiles toget
 constexpr int kPairsMost = kSMs / 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-enum Product { kStats, kProbs, kDx, kDw };
+enum Product { kStats, kProbs, kGrads, kDx, kDw };
 
 // What the host does not know: the kept rows, and what scales them.
 struct Scales {
@@ -60,8 +60,16 @@ struct Scales {
   float g;      // d_loss as one number (sum, mean)
 };
 
+// Where a product goes: rows of `p`, the product's first to row `first`.
+struct Out {
+  void* p;
+  int64_t stride, first;
+  int32_t type, align;
+};
+
 struct ProductArgs {
-  CUtensorMap a, b;
+  CUtensorMap a, b;    // kGrads: of dx
+  CUtensorMap a2, b2;  // of dw
   const int32_t* count;  // kept rows n
   int64_t rows_cap;      // n rounded up to whole tiles at most
   int32_t vocab, hidden;
@@ -84,9 +92,7 @@ struct ProductArgs {
   const Scales* scales;
   const int32_t* rows;   // kept row -> token
   int64_t tokens;
-  void* out;
-  int64_t out_stride, out_first;  // kDw: the row of out that the piece's first goes to
-  int32_t out_type, out_align;
+  Out dx, dw;  // p null: not wanted
   float* sums;           // kDx: [splits][n rounded up][sums_stride]
   int64_t sums_stride;
   int32_t add, pieces, pairs;
@@ -150,6 +156,72 @@ struct Tiles {
   __device__ __forceinline__ void depth(int s, int& k0, int& k1) const {
     k0 = static_cast<int>(static_cast<int64_t>(depth_blocks) * s / splits);
     k1 = static_cast<int>(static_cast<int64_t>(depth_blocks) * (s + 1) / splits);
+  }
+};
+
+struct Tile {
+  int m, n, s, k0, k1;
+  bool dw;
+};
+
+// The tiles of one pair, one after the other: every `pairs`-th.
+template <int KIND>
+struct Schedule {
+  Tiles<KIND> tiles;
+  int64_t at, pairs;
+  __device__ __forceinline__ Schedule(const ProductArgs& a, int n, int64_t pair, int64_t pairs_)
+      : tiles(a, n), at(pair), pairs(pairs_) {}
+  __device__ __forceinline__ int columns() const { return tiles.columns; }
+  __device__ __forceinline__ bool next(Tile& t) {
+    if (at >= tiles.total) return false;
+    tiles.at(at, t.m, t.n, t.s);
+    tiles.depth(t.s, t.k0, t.k1);
+    t.dw = false;
+    at += pairs;
+    return true;
+  }
+};
+
+// dx's tiles first, which are the deeper ones. The pairs that have none in its
+// last round do as many of dw's instead as take about as long; then all go on
+// with dw's. (Two launches: 4% of dx's time and 3% of dw's are idle at 8192 x
+// 4096 x 32000, and each has a start and an end.)
+template <>
+struct Schedule<kGrads> {
+  Tiles<kDx> dx;
+  Tiles<kDw> dw;
+  int64_t at, pairs, pair, idle, ahead, from;
+  int stage = 0;
+  __device__ __forceinline__ Schedule(const ProductArgs& a, int n, int64_t pair_, int64_t pairs_)
+      : dx(a, n), dw(a, n), at(pair_), pairs(pairs_), pair(pair_) {
+    if (!a.dx.p) dx.total = 0;
+    if (!a.dw.p) dw.total = 0;
+    const int64_t busy = dx.total % pairs;
+    idle = busy ? pairs - busy : 0;
+    const int64_t each = dx.depth_blocks / dx.splits / max(1, dw.depth_blocks);
+    ahead = min(dw.total, each * idle);
+    from = pair - busy;  // among the idle ones
+  }
+  __device__ __forceinline__ int columns() const { return kTileN; }
+  __device__ __forceinline__ bool next(Tile& t) {
+    if (stage == 0) {
+      if (at < dx.total) {
+        dx.at(at, t.m, t.n, t.s);
+        dx.depth(t.s, t.k0, t.k1);
+        t.dw = false;
+        at += pairs;
+        return true;
+      }
+      stage = 1;
+      at = idle && from >= 0 ? from : ahead;
+    }
+    if (stage == 1 && at >= ahead) stage = 2, at = ahead + pair;
+    if (at >= dw.total) return false;
+    dw.at(at, t.m, t.n, t.s);
+    dw.depth(t.s, t.k0, t.k1);
+    t.dw = true;
+    at += stage == 1 ? idle : pairs;
+    return true;
   }
 };
 
@@ -235,7 +307,7 @@ struct Epilogue {
       alpha = a.scales->alpha;
     }
     if constexpr (KIND == kDw) {
-      if (live) token = a.out_first + row;
+      if (live) token = a.dw.first + row;
       alpha = a.scales->alpha;
     }
     (void)live;
@@ -310,17 +382,25 @@ struct Epilogue {
       if (token < 0) return;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= alpha;
-      const int64_t at = token * a.out_stride + c;
-      if (a.out_type == ZERO_FP32)
-        store32(static_cast<float*>(a.out) + at, v, left, a.out_align);
-      else if (a.out_type == ZERO_BF16)
-        store32(static_cast<__nv_bfloat16*>(a.out) + at, v, left, a.out_align);
+      const Out& out = KIND == kDx ? a.dx : a.dw;
+      const int64_t at = token * out.stride + c;
+      if (out.type == ZERO_FP32)
+        store32(static_cast<float*>(out.p) + at, v, left, out.align);
+      else if (out.type == ZERO_BF16)
+        store32(static_cast<__nv_bfloat16*>(out.p) + at, v, left, out.align);
       else
-        store32(static_cast<__half*>(a.out) + at, v, left, a.out_align);
+        store32(static_cast<__half*>(out.p) + at, v, left, out.align);
     }
   }
 
-  __device__ __forceinline__ void done() {
+  // columns [c0, c1) of the tile, of this warp's rows at d
+  __device__ __forceinline__ void run(uint32_t d, int c0, int c1, bool zero) {
+    for (int c = c0; c < c1; c += 32) {
+      uint32_t w[32];
+      tc::tmem_load(d + c, w);
+      tc::tmem_wait_load();
+      take(w, c, zero);
+    }
     if constexpr (KIND == kStats) a.part[part * up(n, kTileM) + row] = make_float2(top, sum);
   }
 };
@@ -350,6 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tc::prefetch_map(&a.a);
     tc::prefetch_map(&a.b);
+    if (KIND == kGrads) tc::prefetch_map(&a.a2), tc::prefetch_map(&a.b2);
     for (int s = 0; s < kStages; ++s) tc::bar_init(full(s), 1), tc::bar_init(empty(s), 1);
     for (int s = 0; s < kAccumulators; ++s) tc::bar_init(acc_full(s), 1), tc::bar_init(acc_empty(s), 2 * kEpilogueWarps);
     tc::bar_init(drained, 1);
@@ -364,41 +445,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   wait_for_previous();
 
   const int n = *a.count;
-  const Tiles<KIND> tiles(a, n);
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  constexpr bool kAByM = KIND == kDw, kBByN = KIND == kDx || KIND == kDw;
+  Schedule<KIND> todo(a, n, blockIdx.x >> 1, gridDim.x >> 1);
+  Tile t;
   bool ok = true;
 
   if (warp == 0 && lane == 0) {
     Ring<kStages> ring;
     int64_t issued = 0;
-    for (int64_t t = first; t < tiles.total && ok; t += step) {
-      int m, nt, s, k0, k1;
-      tiles.at(t, m, nt, s);
-      tiles.depth(s, k0, k1);
-      const int half = tiles.columns / 2;  // of the columns: this CTA's operand rows
-      const int row = m * kTileM + static_cast<int>(rank) * kHalfRows, col = nt * tiles.columns + static_cast<int>(rank) * half;
-      const int rows_a = kAByM || KIND == kDx ? kHalfRows : a.rows_a;
+    while (ok && todo.next(t)) {
+      const int half = todo.columns() / 2;  // of the columns: this CTA's operand rows
+      const int row = t.m * kTileM + static_cast<int>(rank) * kHalfRows;
+      const int col = t.n * todo.columns() + static_cast<int>(rank) * half;
+      const int rows_a = KIND == kGrads ? kHalfRows : a.rows_a;
       const bool copies_a = rows_a == kHalfRows || rank == 0;
-      const uint32_t bytes = static_cast<uint32_t>((rows_a == kHalfRows ? 2 * kHalfRows : rows_a) + tiles.columns) * (kTileK * 2);
-      for (int k = k0; k < k1; ++k) {
+      const uint32_t bytes = static_cast<uint32_t>((rows_a == kHalfRows ? 2 * kHalfRows : rows_a) + todo.columns()) * (kTileK * 2);
+      for (int k = t.k0; k < t.k1; ++k) {
         ok = tc::bar_wait(empty(ring.slot), ring.phase ^ 1);
         if (!ok) break;
-        const uint32_t dst = base + ring.slot * kStageBytes;
+        const uint32_t to_a = base + ring.slot * kStageBytes, to_b = to_a + kOperandBytes;
         const uint32_t bar = tc::in_cta(full(ring.slot), 0);
         if (rank == 0) tc::bar_expect(full(ring.slot), bytes);
-        if constexpr (kAByM) {
-          tc::load_box(dst, &a.a, row, k * kTileK, bar);
-          tc::load_box(dst + kOperandBytes / 2, &a.a, row + 64, k * kTileK, bar);
-        } else if (copies_a) {
-          tc::load_box(dst, &a.a, k * kTileK, row, bar);
-        }
-        if constexpr (kBByN) {
-          const int depth = k * kTileK + (KIND == kDx ? a.first : 0);
-          tc::load_box(dst + kOperandBytes, &a.b, col, depth, bar);
-          tc::load_box(dst + kOperandBytes + kOperandBytes / 2, &a.b, col + 64, depth, bar);
+        if (KIND == kGrads && t.dw) {
+          tc::load_box(to_a, &a.a2, row, k * kTileK, bar);
+          tc::load_box(to_a + kOperandBytes / 2, &a.a2, row + 64, k * kTileK, bar);
+          tc::load_box(to_b, &a.b2, col, k * kTileK, bar);
+          tc::load_box(to_b + kOperandBytes / 2, &a.b2, col + 64, k * kTileK, bar);
+        } else if (KIND == kGrads) {
+          tc::load_box(to_a, &a.a, k * kTileK, row, bar);
+          tc::load_box(to_b, &a.b, col, a.first + k * kTileK, bar);
+          tc::load_box(to_b + kOperandBytes / 2, &a.b, col + 64, a.first + k * kTileK, bar);
         } else {
-          tc::load_box(dst + kOperandBytes, &a.b, k * kTileK, a.first + col, bar);
+          if (copies_a) tc::load_box(to_a, &a.a, k * kTileK, row, bar);
+          tc::load_box(to_b, &a.b, k * kTileK, a.first + col, bar);
         }
         ++issued;
         ring.next();
@@ -412,31 +490,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc::bar_wait(full(static_cast<int>(j % kStages)), static_cast<uint32_t>(j / kStages) & 1);
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
-    const uint32_t instr = tc::instruction(a.bf16 != 0, kAByM, kBByN, kTileM, tiles.columns);
     constexpr uint32_t kLead = kOperandBytes / 2;
+    constexpr bool kBByN = KIND == kGrads;
+    const uint32_t plain = tc::instruction(a.bf16 != 0, false, kBByN, kTileM, todo.columns());
+    const uint32_t turned = tc::instruction(a.bf16 != 0, true, kBByN, kTileM, todo.columns());
+    // 16 deep: 32 bytes along a row, or 16 rows of 128 bytes
+    constexpr uint64_t kAlong = 32 >> 4, kAcross = 2048 >> 4;
     Ring<kStages> ring;
     Ring<kAccumulators> acc;
-    for (int64_t t = first; t < tiles.total && ok; t += step) {
-      int m, nt, s, k0, k1;
-      tiles.at(t, m, nt, s);
-      tiles.depth(s, k0, k1);
+    while (ok && todo.next(t)) {
       ok = tc::bar_wait(acc_empty(acc.slot), acc.phase ^ 1);
       if (!ok) break;
       tc::fence_after();
+      const bool a_by_m = KIND == kGrads && t.dw;
+      const uint32_t instr = a_by_m ? turned : plain;
+      const uint64_t step_a = a_by_m ? kAcross : kAlong, step_b = kBByN ? kAcross : kAlong;
       const uint32_t d = tmem + acc.slot * kTileN;
-      for (int k = k0; k < k1; ++k) {
+      for (int k = t.k0; k < t.k1; ++k) {
         ok = tc::bar_wait(full(ring.slot), ring.phase);
         if (!ok) break;
         tc::fence_after();
         const uint32_t at_a = base + ring.slot * kStageBytes, at_b = at_a + kOperandBytes;
-        const uint64_t da = tc::operand(at_a, kAByM ? kLead : 16, 1024);
+        const uint64_t da = tc::operand(at_a, a_by_m ? kLead : 16, 1024);
         const uint64_t db = tc::operand(at_b, kBByN ? kLead : 16, 1024);
 #pragma unroll
-        for (int i = 0; i < kTileK / 16; ++i) {
-          // 16 deep: 32 bytes along a row, or 16 rows of 128 bytes
-          const uint64_t step_a = (kAByM ? 2048 : 32) >> 4, step_b = (kBByN ? 2048 : 32) >> 4;
-          tc::mma(d, da + i * step_a, db + i * step_b, instr, k > k0 || i > 0);
-        }
+        for (int i = 0; i < kTileK / 16; ++i)
+          tc::mma(d, da + i * step_a, db + i * step_b, instr, k > t.k0 || i > 0);
         tc::commit(empty(ring.slot));
         ring.next();
       }
@@ -452,24 +531,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 2) {
     Ring<kAccumulators> acc;
     const int quarter = warp & 3;  // the rows of tensor memory that this warp may read
-    const int half = (warp - 2) / 4, c0 = half * kPartColumns, c1 = min(tiles.columns, c0 + kPartColumns);
-    for (int64_t t = first; t < tiles.total && ok; t += step) {
-      int m, nt, s, k0, k1;
-      tiles.at(t, m, nt, s);
-      tiles.depth(s, k0, k1);
-      Epilogue<KIND> e(a, n, tiles, m, nt, s, static_cast<int>(rank) * kHalfRows + quarter * 32 + lane, half);
-      ok = tc::bar_wait(acc_full(acc.slot), acc.phase);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
+    const int half = (warp - 2) / 4, c0 = half * kPartColumns, c1 = min(todo.columns(), c0 + kPartColumns);
+    const int row = static_cast<int>(rank) * kHalfRows + quarter * 32 + lane;
+    auto work = [&](auto& e) {
+      ok = __all_sync(kFull, tc::bar_wait(acc_full(acc.slot), acc.phase));
+      if (!ok) return;
       tc::fence_after();
-      const uint32_t d = tmem + acc.slot * kTileN + (static_cast<uint32_t>(quarter * 32) << 16);
-      for (int c = c0; c < c1; c += 32) {
-        uint32_t w[32];
-        tc::tmem_load(d + c, w);
-        tc::tmem_wait_load();
-        e.take(w, c, k0 == k1);
+      e.run(tmem + acc.slot * kTileN + (static_cast<uint32_t>(quarter * 32) << 16), c0, c1, t.k0 == t.k1);
+    };
+    while (ok && todo.next(t)) {
+      if constexpr (KIND != kGrads) {
+        Epilogue<KIND> e(a, n, todo.tiles, t.m, t.n, t.s, row, half);
+        work(e);
+      } else if (t.dw) {
+        Epilogue<kDw> e(a, n, todo.dw, t.m, t.n, t.s, row, half);
+        work(e);
+      } else {
+        Epilogue<kDx> e(a, n, todo.dx, t.m, t.n, t.s, row, half);
+        work(e);
       }
-      e.done();
+      if (!ok) break;
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::bar_arrive_cluster(tc::in_cta(acc_empty(acc.slot), 0));
@@ -1276,32 +1357,26 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
     LOSS_CUDA(launch_product<kProbs>(z, c.s));
     ProductArgs p = z;
     p.scales = c.rows.scales;
-    if (dx) {
-      p.out = dx, p.out_type = d.dtype, p.out_align = align_of(dx, d.hidden * 2), p.out_stride = d.hidden;
-      p.sums = c.in<float>(at.sums), p.sums_stride = at.sums_stride, p.add = first > 0, p.direct = at.whole;
-      if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.rows_cap, at.columns, kHalfRows) ||
-          !matrix_map(&p.b, c.w, c.bf16, d.hidden, d.vocab, at.w_stride, kTileK))
-        return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
-      LOSS_CUDA(launch_product<kDx>(p, c.s));
-    }
-    if (dw) {
-      // rows that start anywhere are written to a padded copy first: single
-      // columns from a row a thread take 77 us where both copies take TIME_DW
-      // (5003 x 1001 fp16)
-      p.out = at.whole ? dw : c.in<void>(at.dw), p.out_type = dw_dtype;
-      p.out_first = at.whole ? first : 0, p.out_stride = at.whole ? d.hidden : at.sums_stride;
-      p.out_align = align_of(p.out, p.out_stride * type_bytes(dw_dtype));
-      if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.rows_cap, at.columns, kTileK) ||
-          !matrix_map(&p.b, c.in<void>(at.xs), c.bf16, d.hidden, at.rows_cap, at.xs_stride, kTileK))
-        return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
-      LOSS_CUDA(launch_product<kDw>(p, c.s));
-      if (!at.whole && dw_dtype == ZERO_FP32)
-        LOSS_TRY(c.copy_rows(fn, c.in<float>(at.dw), at.sums_stride, static_cast<float*>(dw) + first * d.hidden,
-                             d.hidden, columns));
-      else if (!at.whole)
-        LOSS_TRY(c.copy_rows(fn, c.in<uint16_t>(at.dw), at.sums_stride, static_cast<uint16_t*>(dw) + first * d.hidden,
-                             d.hidden, columns));
-    }
+    p.sums = c.in<float>(at.sums), p.sums_stride = at.sums_stride, p.add = first > 0, p.direct = at.whole;
+    p.dx = {dx, d.hidden, 0, d.dtype, align_of(dx, d.hidden * 2)};
+    // rows that start anywhere are written to a padded copy first: single columns
+    // from a row a thread took 77 us, copy and all 24 (5003 x 1001 fp16)
+    if (dw && at.whole)
+      p.dw = {dw, d.hidden, first, dw_dtype, align_of(dw, d.hidden * type_bytes(dw_dtype))};
+    else if (dw)
+      p.dw = {c.in<void>(at.dw), at.sums_stride, 0, dw_dtype, align_of(c.in<void>(at.dw), at.sums_stride * type_bytes(dw_dtype))};
+    if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.rows_cap, at.columns, kHalfRows) ||
+        !matrix_map(&p.b, c.w, c.bf16, d.hidden, d.vocab, at.w_stride, kTileK) ||
+        !matrix_map(&p.a2, z.dz, c.bf16, columns, at.rows_cap, at.columns, kTileK) ||
+        !matrix_map(&p.b2, c.in<void>(at.xs), c.bf16, d.hidden, at.rows_cap, at.xs_stride, kTileK))
+      return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
+    LOSS_CUDA(launch_product<kGrads>(p, c.s));
+    if (dw && !at.whole && dw_dtype == ZERO_FP32)
+      LOSS_TRY(c.copy_rows(fn, c.in<float>(at.dw), at.sums_stride, static_cast<float*>(dw) + first * d.hidden, d.hidden,
+                           columns));
+    else if (dw && !at.whole)
+      LOSS_TRY(c.copy_rows(fn, c.in<uint16_t>(at.dw), at.sums_stride, static_cast<uint16_t*>(dw) + first * d.hidden,
+                           d.hidden, columns));
   }
   if (dx) {
     JoinArgs j = {};

@@ -508,7 +508,8 @@ zero_status check_ptr(const char* fn, const char* what, const void* p, int bytes
 }
 
 int64_t workspace_of(int64_t tokens, int32_t experts) {
-  return static_cast<int64_t>(ctas_for(tokens, experts)) * (experts * 2 + 2) * 4;
+  const int64_t ctas = ctas_for(tokens, experts);
+  return ctas > 1 ? ctas * (experts * 2 + 2) * 4 : 0;
 }
 
 zero_status run(const char* fn, const RouteArgs& a, int dtype, bool backward, void* stream) {
@@ -559,14 +560,14 @@ extern "C" zero_status zero_expert_route(const void* logits, int64_t logits_stri
   ROUTE_TRY(check_ptr(fn, "counts", counts, 4, true));
   ROUTE_TRY(check_ptr(fn, "losses", losses, 4, true));
   ROUTE_TRY(check_ptr(fn, "stats", stats, 4, true));
-  ROUTE_TRY(check_ptr(fn, "workspace", workspace, 4, true));
   const int64_t need = workspace_of(tokens, n_experts);
+  ROUTE_TRY(check_ptr(fn, "workspace", workspace, 4, need > 0));
   if (workspace_bytes < need)
     return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes, need);
   ROUTE_TRY(check_overlaps(fn,
                            {Extent::block("ids", ids, tokens * topk * 4), Extent::block("weights", weights, tokens * topk * 4),
                             Extent::block("counts", counts, n_experts * INT64_C(4)), Extent::block("losses", losses, 8),
-                            Extent::block("stats", stats, (tokens + 1) * 4), Extent::block("workspace", workspace, need)},
+                            Extent::block("stats", stats, (tokens + 1) * 4), Extent::block("workspace", need ? workspace : nullptr, need)},
                            {{"logits", logits, tokens, logits_stride * b, n_experts * INT64_C(1) * b}}));
   RouteArgs a = {};
   a.z = logits, a.tokens = tokens, a.stride = logits_stride, a.experts = n_experts, a.topk = topk;
