@@ -606,6 +606,11 @@ __device__ __forceinline__ int load_target(const RowsArgs& a, int64_t t) {
 template <int N>
 __device__ __forceinline__ void load_kept(const RowsArgs& a, int64_t t0, int step, bool (&kept)[N]) {
   long long v[N];
+  if (t0 >= a.tokens) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) kept[i] = false;
+    return;
+  }
   if (a.id_bytes == 4) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = static_cast<const int*>(a.targets)[min(t0 + i * step, a.tokens - 1)];
@@ -694,19 +699,57 @@ __global__ void __launch_bounds__(kScanThreads) k_loss_scales(const RowsArgs a) 
   if (threadIdx.x == 0) *a.scales = scales_for(top, 0.f, a.scale);
 }
 
+// Rows to another stride: w to one that the bulk copies can take, dw back from
+// one that whole words can be stored to. CTAs of another kernel do it beside its
+// own work.
+struct CopyArgs {
+  const void* from;
+  void* to;
+  int64_t from_stride, to_stride, rows;
+  int32_t hidden, log_lanes, words;  // words: 16-bit ones of an element
+  int64_t ctas;
+};
+template <class T>
+__device__ __forceinline__ void copy_row(const CopyArgs& a, int64_t i, int lane, int lanes) {
+  const T* from = static_cast<const T*>(a.from) + i * a.from_stride;
+  T* to = static_cast<T*>(a.to) + i * a.to_stride;
+  for (int c = lane; c < a.hidden; c += 8 * lanes) {
+    T v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = from[min(c + k * lanes, a.hidden - 1)];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k * lanes < a.hidden) to[c + k * lanes] = v[k];
+  }
+}
+__device__ __forceinline__ void copy_rows(const CopyArgs& a, int64_t cta) {
+  const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t i = (cta * blockDim.x + threadIdx.x) >> a.log_lanes;
+  if (i >= a.rows) return;
+  if (a.words == 2)
+    copy_row<uint32_t>(a, i, lane, lanes);
+  else
+    copy_row<uint16_t>(a, i, lane, lanes);
+}
+
 // The kept rows copied together, in the gradients with zeros up to a whole block
 // of the depth of dz^T x; their targets (and what scales them); left-out rows of
-// dx. A group of 8 to 256 lanes has a row.
+// dx. A group of 8 to 256 lanes has a row. The first CTAs copy w, if it takes that.
 constexpr int kGatherThreads = 256;
 constexpr int kFewTokens = 4 * kGatherThreads;  // whose list every CTA makes for itself: one launch less
 enum Gather { kForward, kForwardFew, kBackward };
 
 template <class W, Gather KIND>
-__global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a) {
+__global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a, const CopyArgs copy) {
   constexpr bool BACKWARD = KIND == kBackward;
   __shared__ int few[KIND == kForwardFew ? kFewTokens : 1], counts[kGatherThreads / 32];
   let_next_start();
   wait_for_previous();
+  if (blockIdx.x < copy.ctas) {
+    copy_rows(copy, blockIdx.x);
+    return;
+  }
+  const int64_t cta = blockIdx.x - copy.ctas;
   int n;
   if constexpr (KIND == kForwardFew) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -729,7 +772,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
       at += __popc(votes[k]);
     }
     __syncthreads();
-    if (blockIdx.x == 0) {
+    if (cta == 0) {
       for (int k = threadIdx.x; k < a.tokens; k += kGatherThreads) a.rows[k] = k < n ? few[k] : -1;
       if (threadIdx.x == 0) a.rows[a.tokens] = n, *a.ticket = 0;
     }
@@ -742,11 +785,11 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
       scales = *a.scales;
     } else {
       scales = scales_of_one(a, n);
-      if (blockIdx.x == 0 && threadIdx.x == 0) *a.scales = scales;
+      if (cta == 0 && threadIdx.x == 0) *a.scales = scales;
     }
   }
   const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x) >> a.log_lanes;
+  const int64_t i = (cta * kGatherThreads + threadIdx.x) >> a.log_lanes;
   const int words = static_cast<int>(a.hidden * 2 / sizeof(W));
   W* to = reinterpret_cast<W*>(static_cast<char*>(a.xs) + i * a.xs_stride * 2);
   const int t = i >= n ? -1 : KIND == kForwardFew ? few[i] : a.rows[i];
@@ -781,27 +824,6 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
       W* out = reinterpret_cast<W*>(static_cast<char*>(a.dx) + i * a.hidden * 2);
       for (int c = lane; c < words; c += lanes) out[c] = W();
     }
-  }
-}
-
-// Rows to another stride: w to one that the bulk copies can take, dw back from
-// one that whole words can be stored to.
-template <class T>
-__global__ void __launch_bounds__(kGatherThreads) k_loss_repack(const T* __restrict__ from, int64_t from_stride,
-                                                                T* __restrict__ to, int64_t to_stride, int64_t rows,
-                                                                int hidden, int log_lanes) {
-  let_next_start();
-  wait_for_previous();
-  const int lanes = 1 << log_lanes, lane = threadIdx.x & (lanes - 1);
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x) >> log_lanes;
-  if (i >= rows) return;
-  for (int c = lane; c < hidden; c += 8 * lanes) {
-    T v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = from[i * from_stride + min(c + k * lanes, hidden - 1)];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k * lanes < hidden) to[i * to_stride + c + k * lanes] = v[k];
   }
 }
 
@@ -911,7 +933,15 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
   }
 }
 
-// dx from its binary32 sums, where the product did not write it.
+// A copy alone: of dw between two pieces.
+__global__ void __launch_bounds__(kGatherThreads) k_loss_copy(const CopyArgs copy) {
+  let_next_start();
+  wait_for_previous();
+  copy_rows(copy, blockIdx.x);
+}
+
+// dx from its binary32 sums, where the product did not write it. The first CTAs
+// copy the last rows of dw, if it takes that.
 struct JoinArgs {
   const int32_t* rows;
   int64_t tokens;
@@ -922,13 +952,17 @@ struct JoinArgs {
   int32_t hidden, piece, pieces, pairs, direct, log_lanes, vec;
 };
 template <class T>
-__global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a) {
+__global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, const CopyArgs copy) {
   wait_for_previous();
+  if (blockIdx.x < copy.ctas) {
+    copy_rows(copy, blockIdx.x);
+    return;
+  }
   const int n = a.rows[a.tokens];
   const int splits = split_of(over(n, kTileM) * over(a.hidden, kTileN), a.piece, a.pairs);
   if (splits == 1 && a.pieces == 1 && a.direct) return;
   const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x) >> a.log_lanes;
+  const int64_t i = ((blockIdx.x - copy.ctas) * kGatherThreads + threadIdx.x) >> a.log_lanes;
   if (i >= n) return;
   const int64_t t = a.rows[i];
   if (t < 0 || t >= a.tokens) return;
@@ -1111,9 +1145,9 @@ cudaError_t launch_product(ProductArgs& a, cudaStream_t s) {
 }
 
 template <Gather KIND>
-cudaError_t launch_gather(const RowsArgs& a, bool early, cudaStream_t s) {
-  return launch(a.vec ? &k_loss_gather<uint4, KIND> : &k_loss_gather<uint16_t, KIND>, ctas_for(a.rows_cap, a.log_lanes),
-                kGatherThreads, 0, early, s, a);
+cudaError_t launch_gather(const RowsArgs& a, const CopyArgs& copy, bool early, cudaStream_t s) {
+  return launch(a.vec ? &k_loss_gather<uint4, KIND> : &k_loss_gather<uint16_t, KIND>,
+                copy.ctas + ctas_for(a.rows_cap, a.log_lanes), kGatherThreads, 0, early, s, a, copy);
 }
 
 zero_status check_desc(const char* fn, const zero_linear_ce_desc* d) {
@@ -1189,19 +1223,18 @@ struct Call {
     product.rows_a = d.tokens < kHalfRows ? static_cast<int32_t>(up(std::max<int64_t>(d.tokens, 1), 16)) : kHalfRows;
     return ZERO_OK;
   }
-  template <class T>
-  zero_status copy_rows(const char* fn, const T* from, int64_t from_stride, T* to, int64_t to_stride, int64_t n) {
+  // rows of `bytes`-wide elements to another stride
+  CopyArgs copy_of(const void* from, int64_t from_stride, void* to, int64_t to_stride, int64_t n, int bytes) const {
     const int log_lanes = lanes_for(d.hidden, 8);
-    LOSS_CUDA(launch(&k_loss_repack<T>, ctas_for(n, log_lanes), kGatherThreads, 0, true, s, from, from_stride, to,
-                     to_stride, n, static_cast<int>(d.hidden), log_lanes));
-    return ZERO_OK;
+    return {from, to, from_stride, to_stride, n, static_cast<int32_t>(d.hidden), log_lanes, bytes / 2,
+            ctas_for(n, log_lanes)};
   }
-  zero_status repack(const char* fn) {
-    if (!wants_repack(d, w)) return ZERO_OK;
-    uint16_t* to = in<uint16_t>(at.w);
-    LOSS_TRY(copy_rows(fn, static_cast<const uint16_t*>(w), d.w_stride, to, at.w_stride, d.vocab));
-    w = to;
-    return ZERO_OK;
+  // w as the bulk copies can take it, and what brings it there
+  CopyArgs repack() {
+    if (!wants_repack(d, w)) return {};
+    const CopyArgs copy = copy_of(w, d.w_stride, in<void>(at.w), at.w_stride, d.vocab, 2);
+    w = copy.to;
+    return copy;
   }
   // rows of xs and of w, contiguous along the depth; tiles for `columns` of z
   bool maps_of_z(int64_t columns) {
@@ -1278,13 +1311,13 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
   LOSS_TRY(ready(fn, &err));
   Call c(d, at, workspace, stream, w);
   LOSS_TRY(c.begin(fn, x, targets, rows, err));
+  const CopyArgs repack = c.repack();
   if (d.tokens <= kFewTokens) {
-    LOSS_CUDA(launch_gather<kForwardFew>(c.rows, false, c.s));
+    LOSS_CUDA(launch_gather<kForwardFew>(c.rows, repack, false, c.s));
   } else {
     LOSS_CUDA(launch(&k_loss_rows, 1, kScanThreads, 0, false, c.s, static_cast<const RowsArgs>(c.rows)));
-    LOSS_CUDA(launch_gather<kForward>(c.rows, true, c.s));
+    LOSS_CUDA(launch_gather<kForward>(c.rows, repack, true, c.s));
   }
-  LOSS_TRY(c.repack(fn));
   if (!c.maps_of_z(d.vocab)) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   c.product.columns = static_cast<int32_t>(d.vocab);
   c.product.part = c.in<float2>(at.part), c.product.target_z = c.in<float>(at.target_z);
@@ -1346,8 +1379,8 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   const bool own_gradients = reduction == ZERO_LOSS_NONE;
   if (own_gradients)
     LOSS_CUDA(launch(&k_loss_scales, 1, kScanThreads, 0, false, c.s, static_cast<const RowsArgs>(c.rows)));
-  LOSS_CUDA(launch_gather<kBackward>(c.rows, own_gradients, c.s));
-  LOSS_TRY(c.repack(fn));
+  LOSS_CUDA(launch_gather<kBackward>(c.rows, c.repack(), own_gradients, c.s));
+  CopyArgs copy = {};  // of dw, after a piece's products
   if (!c.maps_of_z(std::min(at.columns, d.vocab))) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   ProductArgs z = c.product;
   z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.dz = c.in<void>(at.dz), z.dz_stride = at.columns;
@@ -1371,12 +1404,12 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
         !matrix_map(&p.b2, c.in<void>(at.xs), c.bf16, d.hidden, at.rows_cap, at.xs_stride, kTileK))
       return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
     LOSS_CUDA(launch_product<kGrads>(p, c.s));
-    if (dw && !at.whole && dw_dtype == ZERO_FP32)
-      LOSS_TRY(c.copy_rows(fn, c.in<float>(at.dw), at.sums_stride, static_cast<float*>(dw) + first * d.hidden, d.hidden,
-                           columns));
-    else if (dw && !at.whole)
-      LOSS_TRY(c.copy_rows(fn, c.in<uint16_t>(at.dw), at.sums_stride, static_cast<uint16_t*>(dw) + first * d.hidden,
-                           d.hidden, columns));
+    if (dw && !at.whole) {
+      const int bytes = type_bytes(dw_dtype);
+      copy = c.copy_of(p.dw.p, p.dw.stride, static_cast<char*>(dw) + first * d.hidden * bytes, d.hidden, columns, bytes);
+      if (!dx || first + at.columns < d.vocab)
+        LOSS_CUDA(launch(&k_loss_copy, copy.ctas, kGatherThreads, 0, true, c.s, static_cast<const CopyArgs>(copy)));
+    }
   }
   if (dx) {
     JoinArgs j = {};
@@ -1385,8 +1418,8 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
     j.hidden = static_cast<int32_t>(d.hidden), j.piece = c.product.piece, j.pieces = c.product.pieces;
     j.pairs = c.product.pairs, j.direct = at.whole, j.vec = at.whole && aligned_to(dx, 16);
     j.log_lanes = lanes_for(d.hidden, 8);
-    LOSS_CUDA(launch(c.bf16 ? &k_loss_join<__nv_bfloat16> : &k_loss_join<__half>, ctas_for(d.tokens, j.log_lanes),
-                     kGatherThreads, 0, true, c.s, j));
+    LOSS_CUDA(launch(c.bf16 ? &k_loss_join<__nv_bfloat16> : &k_loss_join<__half>, copy.ctas + ctas_for(d.tokens, j.log_lanes),
+                     kGatherThreads, 0, true, c.s, static_cast<const JoinArgs>(j), static_cast<const CopyArgs>(copy)));
   }
   return ZERO_OK;
 }
