@@ -69,7 +69,7 @@ struct Out {
 
 struct ProductArgs {
   CUtensorMap a, b;    // kGrads: of dx
-  CUtensorMap a2, b2;  // of dw
+  CUtensorMap a2, b2;  // kGrads: of dw; kStats, kProbs: b2 for narrow tiles
   const int32_t* count;  // kept rows n
   int64_t rows_cap;      // n rounded up to whole tiles at most
   int32_t vocab, hidden;
@@ -79,7 +79,8 @@ struct ProductArgs {
   int32_t bf16;
   int32_t* err;
   // kStats, kProbs
-  int32_t tile, rows_a;  // columns of a tile; rows of x in a box (fewer than 128: of one CTA, there are no more)
+  int32_t narrow;        // columns of a narrow tile
+  int32_t rows_a;        // rows of x in a box (fewer than 128: of one CTA, there are no more)
   float scale2;          // scale * log2(e)
   const int32_t* target;
   float2* part;          // [column tiles * 2][n rounded up]: maximum and sum, base 2
@@ -114,16 +115,24 @@ __host__ __device__ __forceinline__ int split_of(int64_t tiles, int64_t depth, i
 // Columns of z that a tile takes. With few tiles the pairs' last round is mostly
 // empty: narrower tiles fill it (the eight rows of 4096 against 32000 columns:
 // 143 tiles of 224 on 76 pairs in place of 125 of 256). Above two rounds the
-// narrower tile's extra reads of x cost as much as it gains.
-inline int tile_columns(int64_t m_tiles, int64_t columns, int pairs) {
-  if (m_tiles * over(columns, kTileN) > 2 * pairs) return kTileN;
+// narrower tile's extra reads of x cost as much as it gains. The host chooses
+// the narrow width for as many rows as there can be, the device between it and
+// the whole one for those that are kept.
+// (32-bit numbers: 64-bit divisions in every thread of k_loss_finish took 2 us.)
+__host__ __device__ __forceinline__ int tile_cost(int m_tiles, int columns, int tile, int pairs) {
+  return (m_tiles * ((columns + tile - 1) / tile) + pairs - 1) / pairs * tile;
+}
+inline int narrow_columns(int64_t m_tiles, int64_t columns, int pairs) {
+  if (m_tiles * over(columns, kTileN) > 2 * pairs) return kTileN;  // so their product below is small
+  const int m = static_cast<int>(m_tiles), n = static_cast<int>(columns);
   int best = kTileN;
-  int64_t least = over(m_tiles * over(columns, kTileN), pairs) * kTileN;
-  for (int t = kTileN - 32; t > kTileN / 2; t -= 32) {
-    const int64_t cost = over(m_tiles * over(columns, t), pairs) * t;
-    if (cost < least) best = t, least = cost;
-  }
+  for (int t = kTileN - 32; t > kTileN / 2; t -= 32)
+    if (tile_cost(m, n, t, pairs) < tile_cost(m, n, best, pairs)) best = t;
   return best;
+}
+__device__ __forceinline__ int tile_columns(int m_tiles, int columns, int narrow, int pairs) {
+  if (narrow == kTileN) return kTileN;
+  return tile_cost(m_tiles, columns, narrow, pairs) < tile_cost(m_tiles, columns, kTileN, pairs) ? narrow : kTileN;
 }
 
 // The tiles of a product and their order.
@@ -136,7 +145,7 @@ struct Tiles {
     const int cols = KIND == kDx || KIND == kDw ? a.hidden : a.columns;
     const int depth = KIND == kDx ? a.columns : KIND == kDw ? n : a.hidden;
     m_tiles = static_cast<int>(over(rows, kTileM));
-    columns = KIND == kStats || KIND == kProbs ? a.tile : kTileN;
+    columns = KIND == kStats || KIND == kProbs ? tile_columns(m_tiles, cols, a.narrow, a.pairs) : kTileN;
     n_tiles = static_cast<int>(over(cols, columns));
     depth_blocks = static_cast<int>(over(depth, kTileK));
     splits = KIND == kDx ? split_of(static_cast<int64_t>(m_tiles) * n_tiles, a.piece, a.pairs) : 1;
@@ -198,8 +207,15 @@ struct Schedule<kGrads> {
     if (!a.dw.p) dw.total = 0;
     const int64_t busy = dx.total % pairs;
     idle = busy ? pairs - busy : 0;
-    const int64_t each = dx.depth_blocks / dx.splits / max(1, dw.depth_blocks);
-    ahead = min(dw.total, each * idle);
+    // how many ahead: what ends first, a tile costing about eight blocks beside its own
+    const int64_t deep = dx.depth_blocks / dx.splits + 8, flat = dw.depth_blocks + 8;
+    int64_t least = INT64_MAX, best = 0;
+    for (int64_t each = deep / flat, k = 0; k < 3 && idle; ++k, ++each) {
+      const int64_t rest = (max(INT64_C(0), dw.total - each * idle) + pairs - 1) / pairs * flat;
+      const int64_t end = max(deep, each * flat) + rest;
+      if (end < least) least = end, best = each;
+    }
+    ahead = min(dw.total, best * idle);
     from = pair - busy;  // among the idle ones
   }
   __device__ __forceinline__ int columns() const { return kTileN; }
@@ -430,7 +446,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tc::prefetch_map(&a.a);
     tc::prefetch_map(&a.b);
-    if (KIND == kGrads) tc::prefetch_map(&a.a2), tc::prefetch_map(&a.b2);
+    tc::prefetch_map(&a.b2);
+    if (KIND == kGrads) tc::prefetch_map(&a.a2);
     for (int s = 0; s < kStages; ++s) tc::bar_init(full(s), 1), tc::bar_init(empty(s), 1);
     for (int s = 0; s < kAccumulators; ++s) tc::bar_init(acc_full(s), 1), tc::bar_init(acc_empty(s), 2 * kEpilogueWarps);
     tc::bar_init(drained, 1);
@@ -453,6 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Ring<kStages> ring;
     int64_t issued = 0;
     while (ok && todo.next(t)) {
+      const bool whole = todo.columns() == kTileN;
       const int half = todo.columns() / 2;  // of the columns: this CTA's operand rows
       const int row = t.m * kTileM + static_cast<int>(rank) * kHalfRows;
       const int col = t.n * todo.columns() + static_cast<int>(rank) * half;
@@ -476,7 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc::load_box(to_b + kOperandBytes / 2, &a.b, col + 64, a.first + k * kTileK, bar);
         } else {
           if (copies_a) tc::load_box(to_a, &a.a, k * kTileK, row, bar);
-          tc::load_box(to_b, &a.b, k * kTileK, a.first + col, bar);
+          // (a map chosen by pointer would be copied to local memory)
+          if (whole)
+            tc::load_box(to_b, &a.b, k * kTileK, a.first + col, bar);
+          else
+            tc::load_box(to_b, &a.b2, k * kTileK, a.first + col, bar);
         }
         ++issued;
         ring.next();
@@ -580,7 +602,7 @@ struct RowsArgs {
   int64_t x_stride, xs_stride, rows_cap;
   void* xs;
   int32_t* target;
-  int32_t vec, log_lanes, parts;
+  int32_t vec, log_lanes, narrow, pairs;
   // gradients
   const float* lse;
   const float* d;
@@ -843,8 +865,13 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
   __shared__ bool last;
   wait_for_previous();
   const int n = a.rows[a.tokens];
-  const int parts = a.parts;
+  const int parts = kParts * static_cast<int>(over(a.vocab, tile_columns((n + kTileM - 1) / kTileM, a.vocab, a.narrow, a.pairs)));
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kFinishRows, rows = up(n, kTileM);
+  // of the row that this thread writes: loaded ahead of the parts
+  const int64_t own = i0 + threadIdx.x / kFinishGroups;
+  const bool writes = threadIdx.x % kFinishGroups == 0;
+  const int token = writes && own < n ? a.rows[own] : -1;
+  const float target_z = writes && own < n ? a.target_z[own] : 0.f;
   {
     const int r = threadIdx.x % kFinishRows, g = threadIdx.x / kFinishRows;
     float top = -INFINITY, sum = 0.f;
@@ -865,22 +892,20 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
   __syncthreads();
   {
     const int r = threadIdx.x / kFinishGroups, g = threadIdx.x % kFinishGroups;  // a warp a row
-    const int64_t i = i0 + r;
     float2 p = part[g][r];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
       join(p.x, p.y, __shfl_xor_sync(kFull, p.x, o), __shfl_xor_sync(kFull, p.y, o));
     if (g == 0) {
       float loss = 0.f;
-      if (i < n) {
-        const int t = a.rows[i];
+      if (own < n && token >= 0) {
         const float lse2 = p.x + log2f(p.y);
-        loss = (lse2 - a.target_z[i]) * kLn2;
-        a.lse_out[t] = lse2 * kLn2;
-        a.losses[t] = loss;
+        loss = (lse2 - target_z) * kLn2;
+        a.lse_out[token] = lse2 * kLn2;
+        a.losses[token] = loss;
       }
       mine[r] = loss;
-      if (i < a.tokens && load_target(a, i) < 0) a.lse_out[i] = 0.f, a.losses[i] = 0.f;
+      if (own < a.tokens && load_target(a, own) < 0) a.lse_out[own] = 0.f, a.losses[own] = 0.f;
     }
   }
   __syncthreads();
@@ -1238,10 +1263,11 @@ struct Call {
   }
   // rows of xs and of w, contiguous along the depth; tiles for `columns` of z
   bool maps_of_z(int64_t columns) {
-    product.tile = tile_columns(at.rows_cap / kTileM, columns, product.pairs);
+    product.narrow = narrow_columns(at.rows_cap / kTileM, columns, product.pairs);
     const void* xs = in<void>(at.xs);
     return matrix_map(&product.a, xs, bf16, d.hidden, at.rows_cap, at.xs_stride, product.rows_a) &&
-           matrix_map(&product.b, w, bf16, d.hidden, d.vocab, at.w_stride, product.tile / 2);
+           matrix_map(&product.b, w, bf16, d.hidden, d.vocab, at.w_stride, kHalfRows) &&
+           matrix_map(&product.b2, w, bf16, d.hidden, d.vocab, at.w_stride, product.narrow / 2);
   }
 };
 
@@ -1322,7 +1348,7 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
   c.product.columns = static_cast<int32_t>(d.vocab);
   c.product.part = c.in<float2>(at.part), c.product.target_z = c.in<float>(at.target_z);
   LOSS_CUDA(launch_product<kStats>(c.product, c.s));
-  c.rows.parts = static_cast<int32_t>(kParts * over(d.vocab, c.product.tile));
+  c.rows.narrow = c.product.narrow, c.rows.pairs = c.product.pairs;
   c.rows.part = c.product.part, c.rows.target_z = c.product.target_z;
   c.rows.cta_sums = c.in<float>(at.cta_sums), c.rows.losses = losses, c.rows.lse_out = lse, c.rows.total = total;
   LOSS_CUDA(launch(&k_loss_finish, std::max<int64_t>(1, over(d.tokens, kFinishRows)), kFinishThreads, 0, true, c.s,
