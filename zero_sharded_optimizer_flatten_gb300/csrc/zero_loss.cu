@@ -49,6 +49,7 @@ constexpr int kSmemBytes = 1024 + kStages * kStageBytes;
 constexpr int64_t kPieceBytes = INT64_C(512) << 20;  // of dz in memory at a time
 constexpr int kGroupM = 8;  // row tiles that run through the column tiles together (their operands stay in L2)
 constexpr int kPairsMost = kSMs / 2;
+static_assert(kTileM == kTileN, "rows of w are counted in tiles of either kind");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Product { kStats, kProbs, kGrads, kDx, kDw };
@@ -105,11 +106,10 @@ __host__ __device__ __forceinline__ int64_t over(int64_t n, int64_t unit) { retu
 
 // How many parts kDx's sum over the vocabulary is cut into, so that few row
 // tiles still fill the SMs (their sums are joined by k_loss_join).
-__host__ __device__ __forceinline__ int split_of(int64_t tiles, int64_t depth, int pairs) {
+__host__ __device__ __forceinline__ int split_of(int tiles, int depth, int pairs) {
   if (tiles < 1 || tiles * 2 > pairs) return 1;
-  const int64_t most = over(depth, 4 * kTileK);
-  const int64_t s = pairs / tiles;
-  return static_cast<int>(s < most ? s : most < 1 ? 1 : most);
+  const int most = (depth + 4 * kTileK - 1) / (4 * kTileK), s = pairs / tiles;
+  return s < most ? s : most;
 }
 
 // Columns of z that a tile takes. With few tiles the pairs' last round is mostly
@@ -135,36 +135,38 @@ __device__ __forceinline__ int tile_columns(int m_tiles, int columns, int narrow
   return tile_cost(m_tiles, columns, narrow, pairs) < tile_cost(m_tiles, columns, kTileN, pairs) ? narrow : kTileN;
 }
 
-// The tiles of a product and their order.
+// The tiles of a product and their order. (All in 32 bits: there are at most
+// 2^16 x 2^14 tiles, and a 64-bit division costs as much as a block's products.)
 template <int KIND>
 struct Tiles {
-  int m_tiles, n_tiles, splits, depth_blocks, columns;
-  int64_t total;
+  int m_tiles, n_tiles, splits, depth_blocks, columns, total;
   __device__ __forceinline__ Tiles(const ProductArgs& a, int n) {
     const int rows = KIND == kDw ? a.columns : n;
     const int cols = KIND == kDx || KIND == kDw ? a.hidden : a.columns;
     const int depth = KIND == kDx ? a.columns : KIND == kDw ? n : a.hidden;
-    m_tiles = static_cast<int>(over(rows, kTileM));
+    m_tiles = (rows + kTileM - 1) / kTileM;
     columns = KIND == kStats || KIND == kProbs ? tile_columns(m_tiles, cols, a.narrow, a.pairs) : kTileN;
-    n_tiles = static_cast<int>(over(cols, columns));
-    depth_blocks = static_cast<int>(over(depth, kTileK));
-    splits = KIND == kDx ? split_of(static_cast<int64_t>(m_tiles) * n_tiles, a.piece, a.pairs) : 1;
-    total = static_cast<int64_t>(m_tiles) * n_tiles * splits;
+    n_tiles = (cols + columns - 1) / columns;
+    depth_blocks = (depth + kTileK - 1) / kTileK;
+    splits = KIND == kDx ? split_of(m_tiles * n_tiles, a.piece, a.pairs) : 1;
+    total = m_tiles * n_tiles * splits;
   }
-  __device__ __forceinline__ void at(int64_t t, int& m, int& n, int& s) const {
-    const int64_t plane = static_cast<int64_t>(m_tiles) * n_tiles;
-    s = static_cast<int>(t / plane);
-    t -= s * plane;
-    const int64_t group = static_cast<int64_t>(kGroupM) * n_tiles;
-    const int m0 = static_cast<int>(t / group) * kGroupM;
-    const int size = min(kGroupM, m_tiles - m0);
-    t -= t / group * group;
-    n = static_cast<int>(t / size);
-    m = m0 + static_cast<int>(t % size);
+  __device__ __forceinline__ void at(int t, int& m, int& n, int& s) const {
+    s = 0;
+    if (KIND == kDx && splits > 1) {
+      const int plane = m_tiles * n_tiles;
+      s = t / plane;
+      t -= s * plane;
+    }
+    const int group = kGroupM * n_tiles, g = t / group;
+    t -= g * group;
+    const int m0 = g * kGroupM, size = min(kGroupM, m_tiles - m0);
+    n = t / size;
+    m = m0 + t - n * size;
   }
   __device__ __forceinline__ void depth(int s, int& k0, int& k1) const {
-    k0 = static_cast<int>(static_cast<int64_t>(depth_blocks) * s / splits);
-    k1 = static_cast<int>(static_cast<int64_t>(depth_blocks) * (s + 1) / splits);
+    k0 = KIND == kDx ? depth_blocks * s / splits : 0;
+    k1 = KIND == kDx ? depth_blocks * (s + 1) / splits : depth_blocks;
   }
 };
 
@@ -177,8 +179,8 @@ struct Tile {
 template <int KIND>
 struct Schedule {
   Tiles<KIND> tiles;
-  int64_t at, pairs;
-  __device__ __forceinline__ Schedule(const ProductArgs& a, int n, int64_t pair, int64_t pairs_)
+  int at, pairs;
+  __device__ __forceinline__ Schedule(const ProductArgs& a, int n, int pair, int pairs_)
       : tiles(a, n), at(pair), pairs(pairs_) {}
   __device__ __forceinline__ int columns() const { return tiles.columns; }
   __device__ __forceinline__ bool next(Tile& t) {
@@ -192,28 +194,26 @@ struct Schedule {
 };
 
 // dx's tiles first, which are the deeper ones. The pairs that have none in its
-// last round do as many of dw's instead as take about as long; then all go on
-// with dw's. (Two launches: 4% of dx's time and 3% of dw's are idle at 8192 x
+// last round do as many of dw's instead as end first with the rest; then all go
+// on with dw's. (Two launches: 4% of dx's time and 3% of dw's are idle at 8192 x
 // 4096 x 32000, and each has a start and an end.)
 template <>
 struct Schedule<kGrads> {
   Tiles<kDx> dx;
   Tiles<kDw> dw;
-  int64_t at, pairs, pair, idle, ahead, from;
-  int stage = 0;
-  __device__ __forceinline__ Schedule(const ProductArgs& a, int n, int64_t pair_, int64_t pairs_)
+  int at, pairs, pair, idle, ahead, from, stage = 0;
+  __device__ __forceinline__ Schedule(const ProductArgs& a, int n, int pair_, int pairs_)
       : dx(a, n), dw(a, n), at(pair_), pairs(pairs_), pair(pair_) {
     if (!a.dx.p) dx.total = 0;
     if (!a.dw.p) dw.total = 0;
-    const int64_t busy = dx.total % pairs;
+    const int busy = dx.total % pairs;
     idle = busy ? pairs - busy : 0;
-    // how many ahead: what ends first, a tile costing about eight blocks beside its own
-    const int64_t deep = dx.depth_blocks / dx.splits + 8, flat = dw.depth_blocks + 8;
-    int64_t least = INT64_MAX, best = 0;
-    for (int64_t each = deep / flat, k = 0; k < 3 && idle; ++k, ++each) {
-      const int64_t rest = (max(INT64_C(0), dw.total - each * idle) + pairs - 1) / pairs * flat;
-      const int64_t end = max(deep, each * flat) + rest;
-      if (end < least) least = end, best = each;
+    // a tile costs about eight blocks beside its own
+    const int deep = dx.depth_blocks / dx.splits + 8, flat = dw.depth_blocks + 8;
+    int least = INT32_MAX, best = 0;
+    for (int each = deep / flat, k = 0; k < 3 && idle; ++k, ++each) {
+      const int64_t end = max(deep, each * flat) + static_cast<int64_t>((max(0, dw.total - each * idle) + pairs - 1) / pairs) * flat;
+      if (end < least) least = static_cast<int>(end), best = each;
     }
     ahead = min(dw.total, best * idle);
     from = pair - busy;  // among the idle ones
@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, 
     return;
   }
   const int n = a.rows[a.tokens];
-  const int splits = split_of(over(n, kTileM) * over(a.hidden, kTileN), a.piece, a.pairs);
+  const int splits = split_of((n + kTileM - 1) / kTileM * ((a.hidden + kTileN - 1) / kTileN), a.piece, a.pairs);
   if (splits == 1 && a.pieces == 1 && a.direct) return;
   const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
   const int64_t i = ((blockIdx.x - copy.ctas) * kGatherThreads + threadIdx.x) >> a.log_lanes;
@@ -1180,7 +1180,7 @@ zero_status check_desc(const char* fn, const zero_linear_ce_desc* d) {
   if (d->tokens < 0 || d->tokens > 1 << 24)
     return fail(ZERO_ERR_INVALID, "%s: tokens must lie in [0, 2^24]", fn);
   if (d->hidden < 1 || d->hidden > 1 << 20) return fail(ZERO_ERR_INVALID, "%s: hidden must lie in [1, 2^20]", fn);
-  if (d->vocab < 1 || d->vocab > 1 << 28) return fail(ZERO_ERR_INVALID, "%s: vocab must lie in [1, 2^28]", fn);
+  if (d->vocab < 1 || d->vocab > 1 << 22) return fail(ZERO_ERR_INVALID, "%s: vocab must lie in [1, 2^22]", fn);
   if (d->dtype != ZERO_FP16 && d->dtype != ZERO_BF16)
     return fail(ZERO_ERR_INVALID, "%s: dtype must be ZERO_FP16 or ZERO_BF16", fn);
   if (d->id_bytes != 4 && d->id_bytes != 8) return fail(ZERO_ERR_INVALID, "%s: id_bytes must be 4 or 8", fn);
