@@ -54,7 +54,7 @@ struct LookupArgs {
   const void* table;
   void* y;
   int64_t stride;
-  int32_t hidden, log_lanes, by32;
+  int32_t hidden, by32;
   float scale;
 };
 
@@ -73,14 +73,13 @@ __device__ __forceinline__ void store_row8(Y* p, const float (&v)[8], bool by32)
   Elem<Y>::store8(p, v);
 }
 
-// A group of 8 to 256 lanes takes TOKENS neighbouring tokens, octet by octet,
-// all their rows in flight together. One token a group leaves the loads of a
-// row alone in flight behind that of its id: 24 us for 32768 tokens of 768 fp16
-// and 64 us for 16384 of 4096 bf16 to fp32, with four TIME4A and TIME4B.
+// A CTA's rows of threads (x: a token's octets, y: tokens) take TOKENS
+// neighbouring tokens each, all their rows in flight together. One token leaves a
+// row's loads alone in flight behind that of its id: 24 us for 32768 tokens of
+// 768 fp16 and 64 us for 16384 of 4096 bf16 to fp32, with four TIME4A and TIME4B.
 template <class I, class T, class Y, int TOKENS>
 __global__ void __launch_bounds__(kThreads) k_embed(const LookupArgs a) {
-  const int lane = threadIdx.x & ((1 << a.log_lanes) - 1), g = threadIdx.x >> a.log_lanes;
-  const int64_t t0 = ((static_cast<int64_t>(blockIdx.x) * kThreads >> a.log_lanes) + g) * TOKENS;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y) * TOKENS;
   if (t0 >= a.ids.tokens) return;
   const I* ids = static_cast<const I*>(a.ids.ids);
   I raw[TOKENS];
@@ -93,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(const LookupArgs a) {
     row[k] = id >= 0 ? static_cast<const T*>(a.table) + id * a.stride : nullptr;
   }
   Y* y = static_cast<Y*>(a.y) + t0 * a.hidden;
-  for (int c = 8 * lane; c < a.hidden; c += 8 << a.log_lanes) {
+  for (int c = 8 * threadIdx.x; c < a.hidden; c += 8 * blockDim.x) {
     Octet<T> v[TOKENS];
 #pragma unroll
     for (int k = 0; k < TOKENS; ++k)
@@ -115,8 +114,8 @@ __global__ void __launch_bounds__(kThreads) k_embed(const LookupArgs a) {
 // Rows that start anywhere: single columns, eight a thread.
 template <class I, class T, class Y>
 __global__ void __launch_bounds__(kThreads) k_embed_any(const LookupArgs a) {
-  const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> a.log_lanes;
+  const int lanes = blockDim.x, lane = threadIdx.x;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= a.ids.tokens) return;
   const int id = row_of(static_cast<const I*>(a.ids.ids)[t], a.ids.vocab);
   Y* y = static_cast<Y*>(a.y) + t * a.hidden;
@@ -156,7 +155,7 @@ constexpr int kMinorBits = 10;      // of an entry; the rest is the place among 
 static_assert(kMinorMost == 1 << kMinorBits, "an entry's parts");
 
 template <class I>
-__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
+__global__ void __maxnreg__(48) k_embed_sort(const SortArgs a) {
   extern __shared__ int count[];  // [kSortWarps][minors], then first places; [minors]: the ids' first places
   __shared__ uint32_t list[kSortWarps][kListed];
   __shared__ int below[kSortWarps], scan[kSortWarps];
@@ -262,13 +261,18 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
   wait_for_previous();
 }
 
-// Rows cleared by 16 bytes, and the bytes at the ends.
+// Rows cleared by 16 bytes, and the bytes at the ends. Two CTAs an SM, which
+// leave the registers that a CTA of the sort needs to run beside them.
+constexpr int kClearCtas = 2 * kSMs;
 __global__ void __launch_bounds__(kThreads) k_embed_clear(char* p, int64_t head, int64_t words, int64_t tail) {
   let_next_start();
   uint4* w = reinterpret_cast<uint4*>(p + head);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < words; i += step)
-    w[i] = make_uint4(0, 0, 0, 0);
+  int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  for (; i + 3 * step < words; i += 4 * step)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[i + k * step] = make_uint4(0, 0, 0, 0);
+  for (; i < words; i += step) w[i] = make_uint4(0, 0, 0, 0);
   if (blockIdx.x == 0 && threadIdx.x < 32) {
     if (threadIdx.x < head) p[threadIdx.x] = 0;
     if (threadIdx.x < tail) p[head + words * 16 + threadIdx.x] = 0;
@@ -470,10 +474,10 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const SumArgs a) {
 // host
 
 template <class... P>
-cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, bool early, cudaStream_t s, P... args) {
+cudaError_t launch(void (*fn)(P...), dim3 grid, dim3 threads, size_t smem, bool early, cudaStream_t s, P... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -486,21 +490,21 @@ cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, bool e
   return e;
 }
 
-// One token a group while that leaves SMs without a CTA, else four.
+// One token a row of threads while that leaves SMs without a CTA, else four.
 template <class I, class T, class Y>
-cudaError_t launch_lookup(LookupArgs& a, bool vec, cudaStream_t s) {
-  a.log_lanes = 3;
-  while (a.log_lanes < 8 && (INT64_C(8) << a.log_lanes) < a.hidden) ++a.log_lanes;
-  const int64_t per_cta = kThreads >> a.log_lanes, one = (a.ids.tokens + per_cta - 1) / per_cta;
+cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t s) {
+  const int units = (a.hidden + 7) / 8, rounds = (units + kThreads - 1) / kThreads;
+  const int lanes = (units + rounds - 1) / rounds, rows = kThreads / lanes;
+  const int64_t one = (a.ids.tokens + rows - 1) / rows;
   const bool four = vec && one >= 8 * kSMs;
-  const int64_t grid = four ? (a.ids.tokens + 4 * per_cta - 1) / (4 * per_cta) : one;
+  const int64_t grid = four ? (a.ids.tokens + 4 * rows - 1) / (4 * rows) : one;
   return launch(four  ? &k_embed<I, T, Y, 4>
                 : vec ? &k_embed<I, T, Y, 1>
                       : &k_embed_any<I, T, Y>,
-                dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s, static_cast<const LookupArgs>(a));
+                dim3(static_cast<unsigned>(grid)), dim3(lanes, rows), 0, false, s, a);
 }
 template <class T, class Y>
-cudaError_t launch_lookup(LookupArgs& a, bool vec, cudaStream_t s) {
+cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t s) {
   return a.ids.id_bytes == 4 ? launch_lookup<int32_t, T, Y>(a, vec, s) : launch_lookup<long long, T, Y>(a, vec, s);
 }
 
@@ -605,7 +609,7 @@ extern "C" zero_status zero_embedding(const void* ids, int32_t id_bytes, int64_t
                             Extent::block("ids", ids, tokens * id_bytes)}));
   EMBED_TRY(pending_error(fn));
   LookupArgs a = {{ids, tokens, id_bytes, static_cast<int32_t>(vocab)}, table, y, table_stride,
-                  static_cast<int32_t>(hidden), 0, aligned_to(y, 32), static_cast<float>(scale)};
+                  static_cast<int32_t>(hidden), aligned_to(y, 32), static_cast<float>(scale)};
   const bool vec = hidden % 8 == 0 && table_stride * e % 16 == 0 && aligned_to(table, 16) && aligned_to(y, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = y_dtype == ZERO_FP32;
@@ -660,7 +664,7 @@ extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride
   if (!accumulate) {
     const int64_t head = std::min<int64_t>(out_bytes, (16 - (reinterpret_cast<uintptr_t>(dtable) & 15)) & 15);
     const int64_t words = (out_bytes - head) / 16, tail = out_bytes - head - words * 16;
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kSMs * 4, (words + kThreads - 1) / kThreads));
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kClearCtas, (words + kThreads - 1) / kThreads));
     r = launch(&k_embed_clear, dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s, static_cast<char*>(dtable),
                head, words, tail);
   }

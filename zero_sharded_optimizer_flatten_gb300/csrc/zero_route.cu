@@ -22,6 +22,7 @@
 #include <inttypes.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "zero_capi_util.h"
 #include "zero_rows.cuh"
@@ -58,6 +59,19 @@ struct RouteArgs {
   const float *d_weights, *d_losses;
   void* dz;
 };
+
+// Within one place in the last, of sums of at least 1 (2^-22 absolutely for the
+// logarithm).
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float log2_of(float v) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 __device__ __forceinline__ float warp_max(float v) {
   float r;
@@ -150,7 +164,7 @@ __global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs
   constexpr int kWarps = warps_of(VPT);
   extern __shared__ int smem[];  // [experts] counts, [kWarps][experts] sums of p
   __shared__ float ends[kWarps][2], part[kWarps];
-  __shared__ float2 candidates[kWarps][32];
+  __shared__ __align__(16) float2 candidates[kWarps][32];
   let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, K = a.topk;
   float* sums = reinterpret_cast<float*>(smem + E);
@@ -174,6 +188,7 @@ __global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs
     float bound = warp_max(most), x = most;
     const bool any = bound > -INFINITY;
     const float top = any ? bound : 0.f;
+#pragma unroll 4
     for (int k = 1; k < K; ++k) {
       x = x == bound ? -INFINITY : x;
       bound = warp_max(x);
@@ -183,9 +198,10 @@ __global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs
     int chosen = -1, slot = lane;
     unsigned reach[VPT];
     int count = 0;
+    bound = fmaxf(bound, -FLT_MAX);  // -inf is not a choice
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      reach[j] = __ballot_sync(kFull, v[j] >= bound && v[j] > -INFINITY);
+      reach[j] = __ballot_sync(kFull, v[j] >= bound);
       count += __popc(reach[j]);
     }
     if (count <= 32) {
@@ -196,13 +212,19 @@ __global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs
           candidates[warp][at + __popc(reach[j] & ((1u << lane) - 1))] = make_float2(v[j], __int_as_float(lane * VPT + j));
         at += __popc(reach[j]);
       }
+      // up to a whole four of them, -inf after the last
+      if (lane >= count && lane < (count + 3) / 4 * 4) candidates[warp][lane] = make_float2(-INFINITY, 0.f);
       __syncwarp();
       const float2 own = candidates[warp][lane];
       const int e = __float_as_int(own.y);
       int rank = 0;
-      for (int c = 0; c < count; ++c) {
-        const float2 other = candidates[warp][c];
-        rank += other.x > own.x || (other.x == own.x && __float_as_int(other.y) < e);
+      for (int c = 0; c < count; c += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(&candidates[warp][c]);
+        const float4 q = *reinterpret_cast<const float4*>(&candidates[warp][c + 2]);
+        rank += p.x > own.x || (p.x == own.x && __float_as_int(p.y) < e);
+        rank += p.z > own.x || (p.z == own.x && __float_as_int(p.w) < e);
+        rank += q.x > own.x || (q.x == own.x && __float_as_int(q.y) < e);
+        rank += q.z > own.x || (q.z == own.x && __float_as_int(q.w) < e);
       }
       __syncwarp();
       const bool takes = lane < count && rank < K;
@@ -243,15 +265,15 @@ __global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs
       s += v[j];
     }
     s = warp_all_sum(s);
-    const float inv = any ? 1.f / s : 0.f;
+    const float inv = any ? reciprocal(s) : 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) total[j] = fmaf(v[j], inv, total[j]);
-    const float lse = any ? top + log2f(s) * kLn2 : 0.f;
+    const float lse = any ? top + log2_of(s) * kLn2 : 0.f;
     if (any) n += 1.f, squares = fmaf(lse, lse, squares);
     float weight = tc::exp2_of(fmaf(chosen_z, kLog2e, -top2));  // 0 without a choice
     if (a.normalize) {
       const float all = warp_all_sum(weight);
-      weight = any ? weight / all : 0.f;
+      weight = any ? weight * reciprocal(all) : 0.f;
     } else {
       weight *= inv;
     }
