@@ -12,8 +12,10 @@
 // occurs (in texts the most frequent are every tenth token); a chunk adds each
 // of its runs of equal ids up in binary32 (k_embed_sums) and writes the row,
 // or, for a run that goes on in another chunk, a partial row, which k_embed_join
-// adds up in order. No atomics: the same call gives the same bits. The rows
-// without tokens are cleared by a kernel before, beside which the sort runs.
+// adds up in order. No atomics: the same call gives the same bits. Other CTAs of
+// k_embed_sums clear the rows without tokens. (Clearing all rows beforehand cost
+// TIME_CLEAR us more at 32000 x 4096 bf16; beside the sort it slowed that down by more
+// than it took.)
 #include <cuda_runtime.h>
 #include <inttypes.h>
 
@@ -155,7 +157,7 @@ constexpr int kMinorBits = 10;      // of an entry; the rest is the place among 
 static_assert(kMinorMost == 1 << kMinorBits, "an entry's parts");
 
 template <class I>
-__global__ void __maxnreg__(48) k_embed_sort(const SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
   extern __shared__ int count[];  // [kSortWarps][minors], then first places; [minors]: the ids' first places
   __shared__ uint32_t list[kSortWarps][kListed];
   __shared__ int below[kSortWarps], scan[kSortWarps];
@@ -257,26 +259,6 @@ __global__ void __maxnreg__(48) k_embed_sort(const SortArgs a) {
       }
     }
   }
-  // the clearing kernel ran beside this one: what follows this grid follows both
-  wait_for_previous();
-}
-
-// Rows cleared by 16 bytes, and the bytes at the ends. Two CTAs an SM, which
-// leave the registers that a CTA of the sort needs to run beside them.
-constexpr int kClearCtas = 2 * kSMs;
-__global__ void __launch_bounds__(kThreads) k_embed_clear(char* p, int64_t head, int64_t words, int64_t tail) {
-  let_next_start();
-  uint4* w = reinterpret_cast<uint4*>(p + head);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  for (; i + 3 * step < words; i += 4 * step)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[i + k * step] = make_uint4(0, 0, 0, 0);
-  for (; i < words; i += step) w[i] = make_uint4(0, 0, 0, 0);
-  if (blockIdx.x == 0 && threadIdx.x < 32) {
-    if (threadIdx.x < head) p[threadIdx.x] = 0;
-    if (threadIdx.x < tail) p[head + words * 16 + threadIdx.x] = 0;
-  }
 }
 
 struct SumArgs {
@@ -290,6 +272,7 @@ struct SumArgs {
   float* part;           // [chunks][2][part_stride]: of a run from an earlier chunk, of a run that goes on
   int2* tail;            // [chunks]: the id that begins in a chunk and goes on (-1: none), chunks that it goes on in
   int32_t hidden, out_type, add, vocab, chunk;
+  int64_t chunks;
   int64_t tokens;
   float scale;
 };
@@ -348,6 +331,14 @@ struct Columns {
     for (int i = 0; i < 8; ++i) v[i] = fmaf(scale, sum[i], v[i]);
     store(row, v);
   }
+  __device__ __forceinline__ void clear_any(const SumArgs& a, int id) const {
+    const int64_t row = static_cast<int64_t>(id) * a.hidden;
+    const float zero[8] = {};
+    if (a.out_type == ZERO_FP32)
+      store(static_cast<float*>(a.out) + row, zero);
+    else  // 0 is 0 in both 16-bit types
+      store(static_cast<__half*>(a.out) + row, zero);
+  }
   __device__ __forceinline__ void finish_any(const SumArgs& a, int id, const float (&sum)[8]) const {
     const int64_t row = static_cast<int64_t>(id) * a.hidden;
     if (a.out_type == ZERO_FP32)
@@ -361,12 +352,30 @@ struct Columns {
 
 // A chunk's sums. The rows are loaded AHEAD at a time, whichever runs they
 // belong to; the runs' ends are the same for every thread.
+constexpr int kClearRows = 8;  // that a CTA looks at
 template <class D, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_embed_sums(const SumArgs a) {
   constexpr int AHEAD = VEC ? kAhead : 4;
   __shared__ int2 item[kChunk + 2];
   let_next_start();
   wait_for_previous();
+  const Columns<VEC> cols = {VEC ? static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) * 8
+                                 : static_cast<int>(blockIdx.y * blockDim.x * 8 + threadIdx.x),
+                             static_cast<int>(blockDim.x), a.hidden};
+  if (blockIdx.x >= a.chunks) {
+    const int first = static_cast<int>(blockIdx.x - a.chunks) * kClearRows;
+    bool empty[kClearRows];
+#pragma unroll
+    for (int i = 0; i < kClearRows; ++i) {
+      const int id = min(first + i, a.vocab - 1);
+      const int64_t at = static_cast<int64_t>(id & ((1 << a.bits) - 1)) * a.minors + (id >> a.bits);
+      empty[i] = a.starts[at] == a.starts[at + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kClearRows; ++i)
+      if (empty[i] && first + i < a.vocab && cols.any()) cols.clear_any(a, first + i);
+    return;
+  }
   const int total = a.starts[a.total_at];
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
   if (lo >= total) {
@@ -388,9 +397,6 @@ __global__ void __launch_bounds__(kThreads) k_embed_sums(const SumArgs a) {
     }
     a.tail[blockIdx.x] = tail;
   }
-  const Columns<VEC> cols = {VEC ? static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) * 8
-                                 : static_cast<int>(blockIdx.y * blockDim.x * 8 + threadIdx.x),
-                             static_cast<int>(blockDim.x), a.hidden};
   if (!cols.any()) return;
   const D* dy = static_cast<const D*>(a.dy);
   float sum[8] = {};
@@ -538,7 +544,8 @@ cudaError_t launch_sums(const SumArgs& a, int64_t chunks, cudaStream_t s) {
   // CTAs of as many warps as a row's columns fill, evenly when it takes several
   const int ctas = (units + kThreads - 1) / kThreads;
   const int threads = ((units + ctas - 1) / ctas + 31) / 32 * 32;
-  cudaError_t e = launch(&k_embed_sums<D, VEC>, dim3(static_cast<unsigned>(chunks), ctas), threads, 0, true, s, a);
+  const int64_t clear = a.add ? 0 : (a.vocab + kClearRows - 1) / kClearRows;
+  cudaError_t e = launch(&k_embed_sums<D, VEC>, dim3(static_cast<unsigned>(chunks + clear), ctas), threads, 0, true, s, a);
   if (e == cudaSuccess && chunks > 1)
     e = launch(&k_embed_join<VEC>, dim3(static_cast<unsigned>(chunks - 1), (units + kJoinLanes - 1) / kJoinLanes),
                kThreads, 0, true, s, a);
@@ -661,15 +668,9 @@ extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride
   EMBED_TRY(pending_error(fn));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t r = cudaSuccess;
-  if (!accumulate) {
-    const int64_t head = std::min<int64_t>(out_bytes, (16 - (reinterpret_cast<uintptr_t>(dtable) & 15)) & 15);
-    const int64_t words = (out_bytes - head) / 16, tail = out_bytes - head - words * 16;
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kClearCtas, (words + kThreads - 1) / kThreads));
-    r = launch(&k_embed_clear, dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s, static_cast<char*>(dtable),
-               head, words, tail);
-  }
-  if (!any || r != cudaSuccess) {
-    if (r != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(r));
+  if (!any) {
+    if (!accumulate) r = cudaMemsetAsync(dtable, 0, out_bytes, s);
+    if (r != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: clearing failed: %s", fn, cudaGetErrorString(r));
     return ZERO_OK;
   }
   char* ws = static_cast<char*>(workspace);
@@ -678,13 +679,13 @@ extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride
   static KernelFacts facts[2];
   auto* sort_fn = id_bytes == 4 ? &k_embed_sort<int32_t> : &k_embed_sort<long long>;
   r = facts[id_bytes == 4].allow(reinterpret_cast<const void*>(sort_fn), kSortSmemMost, kSortSmemMost);
-  if (r == cudaSuccess) r = launch(sort_fn, dim3(at.buckets), kSortThreads, at.sort_smem(), !accumulate, s, sort);
+  if (r == cudaSuccess) r = launch(sort_fn, dim3(at.buckets), kSortThreads, at.sort_smem(), false, s, sort);
   SumArgs a = {};
   a.order = sort.order, a.starts = sort.starts, a.total_at = at.buckets * at.minors;
   a.bits = at.bits, a.minors = at.minors, a.dy = dy, a.dy_stride = dy_stride, a.part_stride = at.part_stride;
   a.out = dtable, a.part = reinterpret_cast<float*>(ws + at.part), a.hidden = static_cast<int32_t>(hidden);
   a.out_type = dtable_dtype, a.add = accumulate != 0, a.vocab = static_cast<int32_t>(vocab), a.tokens = tokens;
-  a.scale = static_cast<float>(scale), a.tail = reinterpret_cast<int2*>(ws + at.tail), a.chunk = at.chunk;
+  a.scale = static_cast<float>(scale), a.tail = reinterpret_cast<int2*>(ws + at.tail), a.chunk = at.chunk, a.chunks = at.chunks;
   const bool vec = hidden % 8 == 0 && dy_stride * e % 16 == 0 && aligned_to(dy, 16) && aligned_to(dtable, 16);
   if (r == cudaSuccess)
     r = dy_dtype == ZERO_FP32   ? (vec ? launch_sums<float, true>(a, at.chunks, s)

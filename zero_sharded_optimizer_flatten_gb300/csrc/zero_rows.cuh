@@ -212,6 +212,25 @@ struct KernelFacts {
   }
 };
 
+// An SM divides its memory between cache and shared memory for the kernel that
+// it runs, and another division waits until it is idle. Kernels with little
+// shared memory that run just ahead of one with much ask for its division, so
+// that its CTAs can start beside theirs. Asked once for each device up to
+// kDevices, beyond in every call.
+struct LargeShared {
+  std::atomic<bool> told[KernelFacts::kDevices];
+
+  cudaError_t ask(const void* fn) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < KernelFacts::kDevices && told[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && dev < KernelFacts::kDevices) told[dev].store(true, std::memory_order_relaxed);
+    return e;
+  }
+};
+
 // Host checks shared by the operators' entry points.
 inline bool known_type(int t) { return t == ZERO_FP16 || t == ZERO_BF16 || t == ZERO_FP32; }
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
