@@ -48,6 +48,30 @@ __device__ __forceinline__ int row_of(I v, int vocab) {
   return v >= 0 && v < vocab ? static_cast<int>(v) : -1;
 }
 
+// Eight values of a row, on a boundary of 16 bytes, binary32 ones of 32: these
+// move by 32 bytes, because by 16 a warp's access touches twice the lines for
+// half of each.
+template <class P>
+__device__ __forceinline__ void load_row8(const P* p, Octet<P>& o) {
+  if constexpr (sizeof(P) == 4)
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(o.w[0].x), "=r"(o.w[0].y), "=r"(o.w[0].z), "=r"(o.w[0].w), "=r"(o.w[1].x), "=r"(o.w[1].y),
+                   "=r"(o.w[1].z), "=r"(o.w[1].w)
+                 : "l"(p)
+                 : "memory");
+  else
+    o.load(p);
+}
+template <class P>
+__device__ __forceinline__ void store_row8(P* p, const float (&v)[8]) {
+  if constexpr (sizeof(P) == 4)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  else
+    Elem<P>::store8(p, v);
+}
+
 // ---------------------------------------------------------------------------
 // lookup
 
@@ -56,24 +80,9 @@ struct LookupArgs {
   const void* table;
   void* y;
   int64_t stride;
-  int32_t hidden, by32;
+  int32_t hidden;
   float scale;
 };
-
-// Eight values of a row, 16-byte aligned. Binary32 ones go out by 32 bytes: by 16
-// a warp's store touches twice the lines for half of each.
-template <class Y>
-__device__ __forceinline__ void store_row8(Y* p, const float (&v)[8], bool by32) {
-  if constexpr (sizeof(Y) == 4) {
-    if (by32) {
-      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                   "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                   : "memory");
-      return;
-    }
-  }
-  Elem<Y>::store8(p, v);
-}
 
 // A CTA's rows of threads (x: a token's octets, y: tokens) take TOKENS
 // neighbouring tokens each, all their rows in flight together. One token leaves a
@@ -98,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(const LookupArgs a) {
     Octet<T> v[TOKENS];
 #pragma unroll
     for (int k = 0; k < TOKENS; ++k)
-      if (row[k]) v[k].load(row[k] + c);
+      if (row[k]) load_row8(row[k] + c, v[k]);
 #pragma unroll
     for (int k = 0; k < TOKENS; ++k)
       if (t0 + k < a.ids.tokens) {
@@ -108,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(const LookupArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= a.scale;
         }
-        store_row8(y + static_cast<int64_t>(k) * a.hidden + c, f, a.by32);
+        store_row8(y + static_cast<int64_t>(k) * a.hidden + c, f);
       }
   }
 }
@@ -293,7 +302,7 @@ struct Columns {
   template <class P>
   __device__ __forceinline__ void load(const P* row, Raw<P>& r) const {
     if constexpr (VEC) {
-      r.octet.load(row + c0);
+      load_row8(row + c0, r.octet);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) r.one[i] = row[in(i) ? at(i) : 0];
@@ -311,7 +320,7 @@ struct Columns {
   template <class P>
   __device__ __forceinline__ void store(P* row, const float (&v)[8]) const {
     if constexpr (VEC) {
-      Elem<P>::store8(row + c0, v);
+      store_row8(row + c0, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -576,6 +585,11 @@ zero_status check_common(const char* fn, int32_t id_bytes, double scale, int64_t
   return ZERO_OK;
 }
 
+// Rows that are taken octet by octet.
+bool wide_rows(int64_t hidden, const void* p, int64_t stride, int bytes) {
+  return hidden % 8 == 0 && stride % 8 == 0 && aligned_to(p, 8 * bytes);
+}
+
 zero_status pending_error(const char* fn) {
   const cudaError_t pending = cudaGetLastError();
   if (pending != cudaSuccess)
@@ -616,8 +630,8 @@ extern "C" zero_status zero_embedding(const void* ids, int32_t id_bytes, int64_t
                             Extent::block("ids", ids, tokens * id_bytes)}));
   EMBED_TRY(pending_error(fn));
   LookupArgs a = {{ids, tokens, id_bytes, static_cast<int32_t>(vocab)}, table, y, table_stride,
-                  static_cast<int32_t>(hidden), aligned_to(y, 32), static_cast<float>(scale)};
-  const bool vec = hidden % 8 == 0 && table_stride * e % 16 == 0 && aligned_to(table, 16) && aligned_to(y, 16);
+                  static_cast<int32_t>(hidden), static_cast<float>(scale)};
+  const bool vec = wide_rows(hidden, table, table_stride, e) && wide_rows(hidden, y, hidden, type_bytes(y_dtype));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = y_dtype == ZERO_FP32;
   const cudaError_t r = table_dtype == ZERO_FP32   ? launch_lookup<float, float>(a, vec, s)
@@ -686,7 +700,7 @@ extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride
   a.out = dtable, a.part = reinterpret_cast<float*>(ws + at.part), a.hidden = static_cast<int32_t>(hidden);
   a.out_type = dtable_dtype, a.add = accumulate != 0, a.vocab = static_cast<int32_t>(vocab), a.tokens = tokens;
   a.scale = static_cast<float>(scale), a.tail = reinterpret_cast<int2*>(ws + at.tail), a.chunk = at.chunk, a.chunks = at.chunks;
-  const bool vec = hidden % 8 == 0 && dy_stride * e % 16 == 0 && aligned_to(dy, 16) && aligned_to(dtable, 16);
+  const bool vec = wide_rows(hidden, dy, dy_stride, e) && wide_rows(hidden, dtable, hidden, type_bytes(dtable_dtype));
   if (r == cudaSuccess)
     r = dy_dtype == ZERO_FP32   ? (vec ? launch_sums<float, true>(a, at.chunks, s)
                                        : launch_sums<float, false>(a, at.chunks, s))

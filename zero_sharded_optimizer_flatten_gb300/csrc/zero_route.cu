@@ -386,17 +386,29 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a) {
   const T* z = static_cast<const T*>(a.z);
   T* dz = static_cast<T*>(a.dz);
   const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp; t < a.tokens; t += step) {
-    float v[VPT];
-    load_row<T, VPT>(z + t * a.stride, lane, E, a.vec, -INFINITY, v);
-    const float lse = a.stats[t], lse2 = lse * kLog2e;
-    int id = -1;
-    float w = 0.f, d = 0.f;
+  // a token's data, loaded while the one before it is worked on
+  float next_v[VPT], next_lse = 0.f, next_w = 0.f, next_d = 0.f;
+  int next_id = -1;
+  auto fetch = [&](int64_t t) {
+    if (t >= a.tokens) return;
+    load_row<T, VPT>(z + t * a.stride, lane, E, a.vec, -INFINITY, next_v);
+    next_lse = a.stats[t];
     if (lane < K) {
-      id = a.ids[t * K + lane];
-      w = a.weights[t * K + lane];
-      if (a.d_weights) d = a.d_weights[t * K + lane];
+      next_id = a.ids[t * K + lane];
+      next_w = a.weights[t * K + lane];
+      if (a.d_weights) next_d = a.d_weights[t * K + lane];
     }
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
+  fetch(t);
+  for (; t < a.tokens; t += step) {
+    float v[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) v[j] = next_v[j];
+    const float lse = next_lse, lse2 = lse * kLog2e;
+    int id = next_id;
+    float w = next_w, d = next_d;
+    fetch(t + step);
     if (id < 0 || id >= E) id = -1, w = 0.f, d = 0.f;
     const bool any = __shfl_sync(kFull, id, 0) >= 0;
     const float wd = warp_all_sum(id >= 0 ? w * d : 0.f);
