@@ -840,6 +840,7 @@ typedef struct {
   int64_t tokens, hidden, vocab;
   int64_t x_stride, w_stride; /* elements between rows                 */
   zero_dtype dtype;           /* x, w, dx: ZERO_FP16 or ZERO_BF16      */
+  zero_dtype dw_dtype;        /* dw: dtype or ZERO_FP32                */
   int32_t id_bytes;
   double scale;
 } zero_linear_ce_desc;
@@ -860,14 +861,14 @@ zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc, const voi
  * losses; else one float, of their sum or of their mean (total[1], total[0]).
  * The logits are formed again, a piece of the vocabulary at a time; their
  * gradient is rounded to dtype (scaled by a power of two that keeps it in
- * range) between its two products, dx and dw are rounded once.  dw_dtype:
- * dtype or ZERO_FP32. */
+ * range) between its two products, for a dw in binary32 to two numbers of dtype
+ * that hold 16 or 22 bits of it.  dx and dw are rounded once. */
 zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, const void* x,
                                                const void* w, const void* targets, const float* lse,
                                                const int32_t* rows, const float* d_loss,
                                                int32_t reduction, void* dx, void* dw,
-                                               zero_dtype dw_dtype, void* workspace,
-                                               int64_t workspace_bytes, void* stream);
+                                               void* workspace, int64_t workspace_bytes,
+                                               void* stream);
 
 /*
  * Measurement helper; the pages have no counterpart.  Launches, on `stream`,

@@ -15,7 +15,7 @@ Tolerances.  u(T) is the half spacing of the type an output is rounded to.
   below the normal range, the scale being at most 2^14 / the largest gradient),
   and by p's relative error, twice that of lse.  Its products are added as
   above, over the vocabulary; split sums add at most 80 * 2^-24 more.  dw the
-  same over the tokens.
+  same over the tokens; for a binary32 one dz is two numbers, off by u(type)^2.
 """
 import gc
 import math
@@ -68,7 +68,7 @@ def near(got, ref, slack, what):
                            f"{float((bound + torch.zeros_like(g))[bad].min())}")
 
 
-def reference(x, w, targets, scale, d=None, reduction="mean"):
+def reference(x, w, targets, scale, d=None, reduction="mean", dw_dtype=None):
     """Losses and gradients in 64 bits, with the bounds on what they are off by."""
     V, H = w.shape
     kept = ((targets >= 0) & (targets < V)).nonzero()[:, 0]
@@ -99,15 +99,18 @@ def reference(x, w, targets, scale, d=None, reduction="mean"):
     dz.scatter_add_(1, at, torch.full_like(lse[:, None], -1.0))
     dz = dz * g
     fine = UNIT[x.dtype] * 1.001 + 2.0 ** -22
+    fine_dw = UNIT[x.dtype] ** 2 * 1.01 + 2.0 ** -22 if dw_dtype == F32 else fine
     tiny = (float(g.abs().max()) * 2.0 ** -13 if n else 0.0) * (2.0 ** -25 if x.dtype == H16 else 0.0)
-    err = dz.abs() * fine + p * g.abs() * (2.1 * off_lse[:, None] + 2.0 ** -20) + tiny
+    rest = p * g.abs() * (2.1 * off_lse[:, None] + 2.0 ** -20) + tiny
+    err, err_dw = dz.abs() * fine + rest, dz.abs() * fine_dw + rest
     s = abs(scale)
     r["dx"] = torch.zeros(T, H, dtype=torch.float64, device="cuda")
     r["dx"][kept] = scale * (dz @ wd)
     r["off_dx"] = torch.zeros_like(r["dx"])
     r["off_dx"][kept] = s * ((err + dz.abs() * ((V / 16 + 2) * 2.0 ** -22 + 80 * 2.0 ** -24)) @ wd.abs())
     r["dw"] = scale * (dz.t() @ xd)
-    r["off_dw"] = s * ((err + dz.abs() * (n / 16 + 2) * 2.0 ** -22).t() @ xd.abs())
+    steps = (n / 16 + 2) * (2 if dw_dtype == F32 else 1)
+    r["off_dw"] = s * ((err_dw + dz.abs() * steps * 2.0 ** -22).t() @ xd.abs())
     return r
 
 
@@ -118,7 +121,7 @@ def check(T, H, V, dtype, *, scale=1.0, reduction="mean", d_value=1.0, dw_dtype=
     else:
         d = torch.full((), d_value, device="cuda")
     ce = Z.zero_linear_cross_entropy(x, w, targets, scale=scale)
-    ref = reference(x, w, targets, scale, d, reduction)
+    ref = reference(x, w, targets, scale, d, reduction, dw_dtype)
     near(ce.losses, ref["losses"], ref["off_loss"], "losses")
     near(ce.lse, ref["lse"], ref["off_lse"], "lse")
     near(ce.total, ref["total"], ref["off_total"], "total")

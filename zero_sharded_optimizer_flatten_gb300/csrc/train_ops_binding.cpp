@@ -702,8 +702,14 @@ struct Head {
     // one row or none: any stride
     if (d.tokens <= 1) d.x_stride = std::max(d.x_stride, d.hidden);
     if (d.vocab <= 1) d.w_stride = std::max(d.w_stride, d.hidden);
-    d.dtype = static_cast<zero_dtype>(type_of(x, "x"));
+    d.dtype = d.dw_dtype = static_cast<zero_dtype>(type_of(x, "x"));
     d.scale = real(a[3]);
+  }
+  // type of dw, -1: that of a given one, or of w
+  void dw_type(int type, const Tensor& dw) {
+    if (type < 0) type = dw.defined() ? type_of(dw, "dw") : static_cast<int>(d.dtype);
+    if (type != d.dtype && type != ZERO_FP32) raise(PyExc_TypeError, "dw: expected the type of w or float32");
+    d.dw_dtype = static_cast<zero_dtype>(type);
   }
   Tensor workspace(PyObject* o, bool backward, int64_t* need) const {
     check(zero_linear_cross_entropy_workspace_bytes(&d, ptr(w), backward, need));
@@ -711,11 +717,12 @@ struct Head {
   }
 };
 
-// x, w, targets, scale, backward -> bytes
+// x, w, targets, scale, backward, dw_type -> bytes
 PyObject* linear_cross_entropy_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 5);
-    const Head h(a);
+    expect_args(n_args, 6);
+    Head h(a);
+    h.dw_type(small(a[5], "dw_dtype"), Tensor());
     int64_t need = 0;
     check(zero_linear_cross_entropy_workspace_bytes(&h.d, ptr(h.w), truth(a[4]), &need));
     return PyLong_FromLongLong(need);
@@ -747,7 +754,7 @@ PyObject* linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
     expect_args(n_args, 14);
-    const Head h(a);
+    Head h(a);
     const Tensor lse = tensor(a[4], "lse"), rows = tensor(a[5], "rows"), d_loss = tensor(a[6], "d_loss");
     const int reduction = small(a[7], "reduction");
     result(lse, "lse", h.targets.sizes(), at::kFloat, h.x);
@@ -762,20 +769,18 @@ PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_
     Tensor dx = maybe(a[10], "dx"), dw = maybe(a[11], "dw");
     const bool want_dx = truth(a[8]), want_dw = truth(a[9]);
     if ((dx.defined() && !want_dx) || (dw.defined() && !want_dw)) value_error("want", "an output that is not wanted");
-    int type = small(a[12], "dw_dtype");
-    if (type < 0) type = dw.defined() ? type_of(dw, "dw") : static_cast<int>(h.d.dtype);
-    if (type != h.d.dtype && type != ZERO_FP32) raise(PyExc_TypeError, "dw: expected the type of w or float32");
+    h.dw_type(small(a[12], "dw_dtype"), dw);
     int64_t need = 0;
     const Tensor ws = h.workspace(a[13], true, &need);
     if (want_dx) dx = result(dx, "dx", h.x.sizes(), h.x.scalar_type(), h.x);
-    if (want_dw) dw = result(dw, "dw", h.w.sizes(), scalar_of(type), h.w);
+    if (want_dw) dw = result(dw, "dw", h.w.sizes(), scalar_of(h.d.dw_dtype), h.w);
     void* stream = stream_of(h.dev);
     unlocked([&] {
       return zero_linear_cross_entropy_backward(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets),
                                                 static_cast<const float*>(ptr(lse)),
                                                 static_cast<const int32_t*>(ptr(rows)),
                                                 static_cast<const float*>(ptr(d_loss)), reduction, ptr(dx), ptr(dw),
-                                                static_cast<zero_dtype>(type), ptr(ws), need, stream);
+                                                ptr(ws), need, stream);
     });
     return tuple_of({dx, dw});
   });

@@ -14,7 +14,8 @@
 //   kStats  tiles of z, of which only every row's maximum and sum of
 //           exponentials leave the SM; joined by k_loss_finish
 //   kProbs  tiles of z again, to dz in 16 bits, a piece of the vocabulary at a
-//           time (kPieceBytes)
+//           time (kPieceBytes); for dw in binary32 to two 16-bit numbers, dz and
+//           what its rounding lost
 //   kGrads  dz w, summed over the pieces in binary32 (kDx), and dz^T x, the
 //           piece's rows of dw (kDw), whose tiles fill each other's last round
 // The second forming of z is a quarter of the operations: the price of keeping
@@ -88,8 +89,9 @@ struct ProductArgs {
   float* target_z;       // base 2
   const float* lse2;
   const float* row_mul;
-  void* dz;              // [rows_cap][dz_stride]
+  void* dz;              // [rows_cap][dz_stride]; two: then as many rows of what rounding lost
   int64_t dz_stride;
+  int32_t two;
   // kDx, kDw
   const Scales* scales;
   const int32_t* rows;   // kept row -> token
@@ -147,7 +149,7 @@ struct Tiles {
     m_tiles = (rows + kTileM - 1) / kTileM;
     columns = KIND == kStats || KIND == kProbs ? tile_columns(m_tiles, cols, a.narrow, a.pairs) : kTileN;
     n_tiles = (cols + columns - 1) / columns;
-    depth_blocks = (depth + kTileK - 1) / kTileK;
+    depth_blocks = (depth + kTileK - 1) / kTileK * (KIND == kDw && a.two ? 2 : 1);
     splits = KIND == kDx ? split_of(m_tiles * n_tiles, a.piece, a.pairs) : 1;
     total = m_tiles * n_tiles * splits;
   }
@@ -329,6 +331,16 @@ struct Epilogue {
     (void)live;
   }
 
+  template <class T>
+  __device__ __forceinline__ void store_dz(T* to, float (&p)[32]) {
+    store32(to, p, 32, 32);
+    if (a.two) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) p[i] -= Elem<T>::widen(Elem<T>::narrow(p[i]));
+      store32(to + a.rows_cap * a.dz_stride, p, 32, 32);
+    }
+  }
+
   __device__ __forceinline__ void take(const uint32_t (&w)[32], int c0, bool zero) {
     const int c = col + c0;
     if constexpr (KIND == kStats) {
@@ -375,9 +387,9 @@ struct Epilogue {
         for (int i = 0; i < 32; ++i) p[i] = 0.f;
       }
       if (a.bf16)
-        store32(static_cast<__nv_bfloat16*>(a.dz) + row * a.dz_stride + c, p, 32, 32);
+        store_dz(static_cast<__nv_bfloat16*>(a.dz) + row * a.dz_stride + c, p);
       else
-        store32(static_cast<__half*>(a.dz) + row * a.dz_stride + c, p, 32, 32);
+        store_dz(static_cast<__half*>(a.dz) + row * a.dz_stride + c, p);
     } else {
       const int left = a.hidden - c;
       if (left <= 0) return;
@@ -484,10 +496,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t bar = tc::in_cta(full(ring.slot), 0);
         if (rank == 0) tc::bar_expect(full(ring.slot), bytes);
         if (KIND == kGrads && t.dw) {
-          tc::load_box(to_a, &a.a2, row, k * kTileK, bar);
-          tc::load_box(to_a + kOperandBytes / 2, &a.a2, row + 64, k * kTileK, bar);
-          tc::load_box(to_b, &a.b2, col, k * kTileK, bar);
-          tc::load_box(to_b + kOperandBytes / 2, &a.b2, col + 64, k * kTileK, bar);
+          // the second half of the depth: x again, with what dz's rounding lost
+          const bool again = a.two && 2 * k >= t.k1;
+          const int depth = (again ? k - t.k1 / 2 : k) * kTileK;
+          const int dz_row = depth + (again ? static_cast<int>(a.rows_cap) : 0);
+          tc::load_box(to_a, &a.a2, row, dz_row, bar);
+          tc::load_box(to_a + kOperandBytes / 2, &a.a2, row + 64, dz_row, bar);
+          tc::load_box(to_b, &a.b2, col, depth, bar);
+          tc::load_box(to_b + kOperandBytes / 2, &a.b2, col + 64, depth, bar);
         } else if (KIND == kGrads) {
           tc::load_box(to_a, &a.a, k * kTileK, row, bar);
           tc::load_box(to_b, &a.b, col, a.first + k * kTileK, bar);
@@ -1036,7 +1052,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, 
 
 // Where a call's scratch lies.
 struct Layout {
-  int64_t rows_cap, columns, pieces, xs_stride, w_stride, sums_stride;
+  int64_t rows_cap, dz_rows, columns, pieces, xs_stride, w_stride, sums_stride;
   int64_t xs, w, part, target_z, target, ticket, cta_sums, lse2, row_mul, scales, dz, sums, dw, bytes;
   bool whole;  // rows of dx and dw are whole 16-byte words: the products write them
 
@@ -1044,7 +1060,8 @@ struct Layout {
     rows_cap = up(std::max<int64_t>(d.tokens, 1), kTileM);
     whole = d.hidden % 8 == 0;
     columns = up(d.vocab, kTileN);
-    if (backward) columns = std::min(columns, std::max<int64_t>(kTileN, kPieceBytes / 2 / rows_cap / kTileN * kTileN));
+    dz_rows = rows_cap * (d.dw_dtype == ZERO_FP32 ? 2 : 1);
+    if (backward) columns = std::min(columns, std::max<int64_t>(kTileN, kPieceBytes / 2 / dz_rows / kTileN * kTileN));
     pieces = over(d.vocab, columns);
     xs_stride = up(d.hidden, 8);
     w_stride = repack ? up(d.hidden, 8) : d.w_stride;
@@ -1066,7 +1083,7 @@ struct Layout {
     lse2 = take(backward ? rows_cap * 4 : 0);
     row_mul = take(backward ? rows_cap * 4 : 0);
     scales = take(sizeof(Scales));
-    dz = take(backward ? rows_cap * columns * 2 : 0);
+    dz = take(backward ? dz_rows * columns * 2 : 0);
     // as many rows as there are tokens, or the parts of few
     const int64_t split_rows = static_cast<int64_t>(kPairsMost) * kTileM;
     sums = take(backward ? (pieces > 1 || !whole ? std::max(split_rows, rows_cap) : split_rows) * sums_stride * 4 : 0);
@@ -1187,6 +1204,8 @@ zero_status check_desc(const char* fn, const zero_linear_ce_desc* d) {
   if (d->vocab < 1 || d->vocab > 1 << 22) return fail(ZERO_ERR_INVALID, "%s: vocab must lie in [1, 2^22]", fn);
   if (d->dtype != ZERO_FP16 && d->dtype != ZERO_BF16)
     return fail(ZERO_ERR_INVALID, "%s: dtype must be ZERO_FP16 or ZERO_BF16", fn);
+  if (d->dw_dtype != d->dtype && d->dw_dtype != ZERO_FP32)
+    return fail(ZERO_ERR_INVALID, "%s: dw_dtype must be dtype or ZERO_FP32", fn);
   if (d->id_bytes != 4 && d->id_bytes != 8) return fail(ZERO_ERR_INVALID, "%s: id_bytes must be 4 or 8", fn);
   if (!std::isfinite(d->scale) || d->scale == 0.0 || std::fabs(d->scale) > 1e6 || std::fabs(d->scale) < 1e-6)
     return fail(ZERO_ERR_INVALID, "%s: the magnitude of scale must lie in [1e-6, 1e6]", fn);
@@ -1363,7 +1382,7 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
 extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, const void* x,
                                                           const void* w, const void* targets, const float* lse,
                                                           const int32_t* rows, const float* d_loss, int32_t reduction,
-                                                          void* dx, void* dw, zero_dtype dw_dtype, void* workspace,
+                                                          void* dx, void* dw, void* workspace,
                                                           int64_t workspace_bytes, void* stream) {
   const char* fn = "zero_linear_cross_entropy_backward";
   clear_error();
@@ -1373,8 +1392,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   const bool any = d.tokens > 0;
   if (reduction != ZERO_LOSS_NONE && reduction != ZERO_LOSS_SUM && reduction != ZERO_LOSS_MEAN)
     return fail(ZERO_ERR_INVALID, "%s: unknown reduction", fn);
-  if (!known_type(dw_dtype) || (dw_dtype != d.dtype && dw_dtype != ZERO_FP32))
-    return fail(ZERO_ERR_INVALID, "%s: dw_dtype must be dtype or ZERO_FP32", fn);
+  const zero_dtype dw_dtype = d.dw_dtype;
   LOSS_TRY(check_ptr(fn, "x", x, 2, any));
   LOSS_TRY(check_ptr(fn, "w", w, 2, true));
   LOSS_TRY(check_ptr(fn, "targets", targets, d.id_bytes, any));
@@ -1414,6 +1432,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   if (!c.maps_of_z(std::min(at.columns, d.vocab))) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   ProductArgs z = c.product;
   z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.dz = c.in<void>(at.dz), z.dz_stride = at.columns;
+  z.two = dw && dw_dtype == ZERO_FP32;
   for (int64_t first = 0; first < d.vocab; first += at.columns) {
     const int64_t columns = std::min(at.columns, d.vocab - first);
     z.first = static_cast<int32_t>(first), z.columns = static_cast<int32_t>(columns);
@@ -1430,7 +1449,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
       p.dw = {c.in<void>(at.dw), at.sums_stride, 0, dw_dtype, align_of(c.in<void>(at.dw), at.sums_stride * type_bytes(dw_dtype))};
     if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.rows_cap, at.columns, kHalfRows) ||
         !matrix_map(&p.b, c.w, c.bf16, d.hidden, d.vocab, at.w_stride, kTileK) ||
-        !matrix_map(&p.a2, z.dz, c.bf16, columns, at.rows_cap, at.columns, kTileK) ||
+        !matrix_map(&p.a2, z.dz, c.bf16, columns, at.dz_rows, at.columns, kTileK) ||
         !matrix_map(&p.b2, c.in<void>(at.xs), c.bf16, d.hidden, at.rows_cap, at.xs_stride, kTileK))
       return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
     LOSS_CUDA(launch_product<kGrads>(p, c.s));

@@ -139,8 +139,8 @@ def lib():
                 "zero_embedding_workspace_bytes": [i64, i64, i64, i64p],
                 "zero_linear_cross_entropy_workspace_bytes": [vp, vp, i32, i64p],
                 "zero_linear_cross_entropy": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp],
-                "zero_linear_cross_entropy_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp,
-                                                       ctypes.c_int, vp, i64, vp],
+                "zero_linear_cross_entropy_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp,
+                                                       i64, vp],
                 "zero_zero3_pass": [vp, ctypes.POINTER(_LayerC), i32, vpp, i32, ctypes.c_int,
                                     ctypes.c_int, hp, i64, vp, vp],
             }
