@@ -31,6 +31,7 @@
 #include "zero_internal.h"
 #include "zero_rows.cuh"
 #include "zero_tensor_core.cuh"
+#include "zero_windows.cuh"
 
 namespace zero {
 namespace {
@@ -747,27 +748,35 @@ struct CopyArgs {
   int32_t hidden, log_lanes, words;  // words: 16-bit ones of an element
   int64_t ctas;
 };
+// By 16-byte pieces of the row that is written, four in flight; `inner` keeps the
+// reads of a row that may begin or end its storage within it. (Single columns:
+// 163 us for 38759 rows of 4271 bf16 to padded ones and 263 back, in place of
+// 117 and 130, 0.8 of what a plain copy of them takes.)
 template <class T>
-__device__ __forceinline__ void copy_row(const CopyArgs& a, int64_t i, int lane, int lanes) {
-  const T* from = static_cast<const T*>(a.from) + i * a.from_stride;
-  T* to = static_cast<T*>(a.to) + i * a.to_stride;
-  for (int c = lane; c < a.hidden; c += 8 * lanes) {
-    T v[8];
+__device__ __forceinline__ void copy_row(const T* from, T* to, int hidden, bool inner, int lane, int lanes) {
+  const Frame<T> f(to, hidden, inner, inner);
+  const int shift = Window<T>::shift(from + f.head);
+  for (int u = lane; u < f.pieces; u += 4 * lanes) {
+    Window<T> v[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = from[min(c + k * lanes, a.hidden - 1)];
+    for (int k = 0; k < 4; ++k) v[k].load(from + f.column(min(u + k * lanes, f.pieces - 1)));
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k * lanes < a.hidden) to[c + k * lanes] = v[k];
+    for (int k = 0; k < 4; ++k)
+      if (u + k * lanes < f.pieces) v[k].shifted(shift).store(to + f.column(u + k * lanes));
   }
+  for (int e = lane; e < f.ends; e += lanes) to[f.end_column(e)] = from[f.end_column(e)];
 }
 __device__ __forceinline__ void copy_rows(const CopyArgs& a, int64_t cta) {
   const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
   const int64_t i = (cta * blockDim.x + threadIdx.x) >> a.log_lanes;
   if (i >= a.rows) return;
+  const bool inner = i == 0 || i == a.rows - 1;
   if (a.words == 2)
-    copy_row<uint32_t>(a, i, lane, lanes);
+    copy_row(static_cast<const float*>(a.from) + i * a.from_stride, static_cast<float*>(a.to) + i * a.to_stride,
+             a.hidden, inner, lane, lanes);
   else
-    copy_row<uint16_t>(a, i, lane, lanes);
+    copy_row(static_cast<const __half*>(a.from) + i * a.from_stride, static_cast<__half*>(a.to) + i * a.to_stride,
+             a.hidden, inner, lane, lanes);
 }
 
 // The kept rows copied together, in the gradients with zeros up to a whole block
@@ -833,13 +842,18 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
   const int t = i >= n ? -1 : KIND == kForwardFew ? few[i] : a.rows[i];
   if (t >= 0 && t < a.tokens) {
     const W* from = reinterpret_cast<const W*>(static_cast<const char*>(a.x) + t * a.x_stride * 2);
-    for (int c = lane; c < words; c += 4 * lanes) {
-      W v[4];
+    if constexpr (sizeof(W) == 2) {  // rows that start anywhere
+      copy_row(reinterpret_cast<const __half*>(from), reinterpret_cast<__half*>(to), words, t == 0 || t == a.tokens - 1,
+               lane, lanes);
+    } else {
+      for (int c = lane; c < words; c += 4 * lanes) {
+        W v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = from[min(c + k * lanes, words - 1)];
+        for (int k = 0; k < 4; ++k) v[k] = from[min(c + k * lanes, words - 1)];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c + k * lanes < words) to[c + k * lanes] = v[k];
+        for (int k = 0; k < 4; ++k)
+          if (c + k * lanes < words) to[c + k * lanes] = v[k];
+      }
     }
     if (lane == 0) {
       const int target = load_target(a, t);
@@ -1250,7 +1264,7 @@ struct Call {
   template <class T>
   T* in(int64_t offset) const { return reinterpret_cast<T*>(ws + offset); }
 
-  void set_vec(bool vec) { rows.vec = vec, rows.log_lanes = lanes_for(d.hidden, vec ? 32 : 4); }
+  void set_vec(bool vec) { rows.vec = vec, rows.log_lanes = lanes_for(d.hidden, 32); }
   zero_status begin(const char* fn, const void* x, const void* targets, int32_t* row_list, int32_t* err) {
     rows.targets = targets, rows.id_bytes = d.id_bytes, rows.vocab = static_cast<int32_t>(d.vocab);
     rows.tokens = d.tokens, rows.hidden = d.hidden, rows.rows = row_list, rows.ticket = in<int32_t>(at.ticket);
@@ -1273,7 +1287,7 @@ struct Call {
   }
   // rows of `bytes`-wide elements to another stride
   CopyArgs copy_of(const void* from, int64_t from_stride, void* to, int64_t to_stride, int64_t n, int bytes) const {
-    const int log_lanes = lanes_for(d.hidden, 8);
+    const int log_lanes = lanes_for(d.hidden, 32);
     return {from, to, from_stride, to_stride, n, static_cast<int32_t>(d.hidden), log_lanes, bytes / 2,
             ctas_for(n, log_lanes)};
   }
