@@ -679,11 +679,12 @@ extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride
   EMBED_TRY(check_overlaps(
       fn, {Extent::block("dtable", dtable, out_bytes), Extent::block("workspace", any ? workspace : nullptr, at.bytes)},
       {{"dy", dy, tokens, dy_stride * e, hidden * e}, Extent::block("ids", ids, tokens * id_bytes)}));
+  if (!any && accumulate) return ZERO_OK;
   EMBED_TRY(pending_error(fn));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t r = cudaSuccess;
   if (!any) {
-    if (!accumulate) r = cudaMemsetAsync(dtable, 0, out_bytes, s);
+    r = cudaMemsetAsync(dtable, 0, out_bytes, s);
     if (r != cudaSuccess) return fail(ZERO_ERR_CUDA, "%s: clearing failed: %s", fn, cudaGetErrorString(r));
     return ZERO_OK;
   }
