@@ -862,7 +862,8 @@ zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc, const voi
  * The logits are formed again, a piece of the vocabulary at a time; their
  * gradient is rounded to dtype (scaled by a power of two that keeps it in
  * range) between its two products, for a dw in binary32 to two numbers of dtype
- * that hold 16 or 22 bits of it.  dx and dw are rounded once. */
+ * that hold 16 or 22 bits of it, which doubles dw's product.  dx and dw are
+ * rounded once. */
 zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, const void* x,
                                                const void* w, const void* targets, const float* lse,
                                                const int32_t* rows, const float* d_loss,

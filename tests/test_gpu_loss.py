@@ -99,7 +99,8 @@ def reference(x, w, targets, scale, d=None, reduction="mean", dw_dtype=None):
     dz.scatter_add_(1, at, torch.full_like(lse[:, None], -1.0))
     dz = dz * g
     fine = UNIT[x.dtype] * 1.001 + 2.0 ** -22
-    fine_dw = UNIT[x.dtype] ** 2 * 1.01 + 2.0 ** -22 if dw_dtype == F32 else fine
+    terms = 2 if dw_dtype == F32 else 1
+    fine_dw = UNIT[x.dtype] ** terms * 1.01 + 2.0 ** -22
     tiny = (float(g.abs().max()) * 2.0 ** -13 if n else 0.0) * (2.0 ** -25 if x.dtype == H16 else 0.0)
     rest = p * g.abs() * (2.1 * off_lse[:, None] + 2.0 ** -20) + tiny
     err, err_dw = dz.abs() * fine + rest, dz.abs() * fine_dw + rest
@@ -109,7 +110,7 @@ def reference(x, w, targets, scale, d=None, reduction="mean", dw_dtype=None):
     r["off_dx"] = torch.zeros_like(r["dx"])
     r["off_dx"][kept] = s * ((err + dz.abs() * ((V / 16 + 2) * 2.0 ** -22 + 80 * 2.0 ** -24)) @ wd.abs())
     r["dw"] = scale * (dz.t() @ xd)
-    steps = (n / 16 + 2) * (2 if dw_dtype == F32 else 1)
+    steps = (n / 16 + 2) * terms
     r["off_dw"] = s * ((err_dw + dz.abs() * steps * 2.0 ** -22).t() @ xd.abs())
     return r
 

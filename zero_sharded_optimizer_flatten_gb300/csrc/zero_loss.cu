@@ -15,8 +15,8 @@
 //           exponentials leave the SM; joined by k_loss_finish (kStatsLong: for a
 //           long depth, summed in several accumulators)
 //   kProbs  tiles of z again, to dz in 16 bits, a piece of the vocabulary at a
-//           time (kPieceBytes); for dw in binary32 to two 16-bit numbers, dz and
-//           what its rounding lost
+//           time (kPieceBytes); for dw in binary32 to two 16-bit numbers
+//           ("terms"), the second what the first one's rounding lost
 //   kGrads  dz w, summed over the pieces in binary32 (kDx), and dz^T x, the
 //           piece's rows of dw (kDw), whose tiles fill each other's last round
 // The second forming of z is a quarter of the operations: the price of keeping
@@ -48,12 +48,14 @@ constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // copies, products, epilogu
 constexpr int kParts = kEpilogueWarps / 4;          // of a row's 256 columns
 constexpr int kPartColumns = kTileN / kParts;
 constexpr int kAccumulators = 2;
-// Blocks of the depth that one accumulator of kStatsLong sums up; they are added
-// up in the epilogue. The tensor cores' additions are rounded less well
-// than binary32 ones: at a depth of 4096 the losses are off by 8e-7 of their size
-// in one sum, by 4e-7 in two and by 2e-7 in four, which costs 3% of
-// the time.
-constexpr int kSegment = 32;
+// Blocks of the depth that one accumulator of kStatsLong, and of dw in
+// kGradsLong, sums up; they are added up in the epilogue, because the tensor
+// cores' additions are rounded less well than binary32 ones. Losses of 4096
+// channels are off by 8e-7 of their size in one sum, by 4e-7 in two (of 32
+// blocks), by 2e-7 in four, which costs 3% of the time. A binary32 dw of 4096
+// tokens, 131072 x 1024, is off by 2.4e-6 in sums of 32 blocks, 8e-7 of 8 and 6e-7
+// of 4, which costs 7%.
+constexpr int kSegment = 32, kSegmentDw = 8;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes;
 constexpr int64_t kPieceBytes = INT64_C(512) << 20;  // of dz in memory at a time
 constexpr int kGroupM = 8;  // row tiles that run through the column tiles together (their operands stay in L2)
@@ -61,8 +63,9 @@ constexpr int kPairsMost = kSMs / 2;
 static_assert(kTileM == kTileN, "rows of w are counted in tiles of either kind");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-enum Product { kStats, kStatsLong, kProbs, kGrads, kDx, kDw };
+enum Product { kStats, kStatsLong, kProbs, kGrads, kGradsLong, kDx, kDw };
 constexpr bool is_stats(int kind) { return kind == kStats || kind == kStatsLong; }
+constexpr bool is_grads(int kind) { return kind == kGrads || kind == kGradsLong; }
 constexpr bool is_z(int kind) { return is_stats(kind) || kind == kProbs; }
 
 // What the host does not know: the kept rows, and what scales them.
@@ -99,9 +102,9 @@ struct ProductArgs {
   float* target_z;       // base 2
   const float* lse2;
   const float* row_mul;
-  void* dz;              // [rows_cap][dz_stride]; two: then as many rows of what rounding lost
+  void* dz;              // [terms][rows_cap][dz_stride]
   int64_t dz_stride;
-  int32_t two;
+  int32_t terms;
   // kDx, kDw
   const Scales* scales;
   const int32_t* rows;   // kept row -> token
@@ -159,7 +162,7 @@ struct Tiles {
     m_tiles = (rows + kTileM - 1) / kTileM;
     columns = is_z(KIND) ? tile_columns(m_tiles, cols, a.narrow, a.pairs) : kTileN;
     n_tiles = (cols + columns - 1) / columns;
-    depth_blocks = (depth + kTileK - 1) / kTileK * (KIND == kDw && a.two ? 2 : 1);
+    depth_blocks = (depth + kTileK - 1) / kTileK * (KIND == kDw ? a.terms : 1);
     splits = KIND == kDx ? split_of(m_tiles * n_tiles, a.piece, a.pairs) : 1;
     total = m_tiles * n_tiles * splits;
   }
@@ -209,12 +212,11 @@ struct Schedule {
 // last round do as many of dw's instead as end first with the rest; then all go
 // on with dw's. (Two launches: 4% of dx's time and 3% of dw's are idle at 8192 x
 // 4096 x 32000, and each has a start and an end.)
-template <>
-struct Schedule<kGrads> {
+struct GradsSchedule {
   Tiles<kDx> dx;
   Tiles<kDw> dw;
   int at, pairs, pair, idle, ahead, from, stage = 0;
-  __device__ __forceinline__ Schedule(const ProductArgs& a, int n, int pair_, int pairs_)
+  __device__ __forceinline__ GradsSchedule(const ProductArgs& a, int n, int pair_, int pairs_)
       : dx(a, n), dw(a, n), at(pair_), pairs(pairs_), pair(pair_) {
     if (!a.dx.p) dx.total = 0;
     if (!a.dw.p) dw.total = 0;
@@ -251,6 +253,15 @@ struct Schedule<kGrads> {
     at += stage == 1 ? idle : pairs;
     return true;
   }
+};
+
+template <>
+struct Schedule<kGrads> : GradsSchedule {
+  using GradsSchedule::GradsSchedule;
+};
+template <>
+struct Schedule<kGradsLong> : GradsSchedule {
+  using GradsSchedule::GradsSchedule;
 };
 
 // A phase-counting position in a ring of `size` slots.
@@ -297,7 +308,7 @@ __device__ __forceinline__ void store32(T* p, const float (&v)[32], int left, in
 
 // A warp's part of a tile's epilogue, a row a thread: up to 128 columns, 32 at a
 // time, from tensor memory.
-template <int KIND>
+template <int KIND, bool WIDE = false>  // WIDE: to binary32
 struct Epilogue {
   const ProductArgs& a;
   int n;            // kept rows
@@ -344,10 +355,11 @@ struct Epilogue {
   template <class T>
   __device__ __forceinline__ void store_dz(T* to, float (&p)[32]) {
     store32(to, p, 32, 32);
-    if (a.two) {
+    for (int k = 1; k < a.terms; ++k) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) p[i] -= Elem<T>::widen(Elem<T>::narrow(p[i]));
-      store32(to + a.rows_cap * a.dz_stride, p, 32, 32);
+      to += a.rows_cap * a.dz_stride;
+      store32(to, p, 32, 32);
     }
   }
 
@@ -408,34 +420,39 @@ struct Epilogue {
       else
         store_dz(static_cast<__half*>(a.dz) + row * a.dz_stride + c, p);
     } else {
-      const int left = a.hidden - c;
-      if (left <= 0) return;
       float v[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = zero ? 0.f : __uint_as_float(w[i]);
-      if (KIND == kDx && !direct) {
-        if (row >= n) return;
-        float* p = a.sums + (split * sums_rows + row) * a.sums_stride + c;
-        if (a.add) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < left) v[i] += p[i];
-        }
-        store32(p, v, left, 16);
-        return;
-      }
-      if (token < 0) return;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= alpha;
-      const Out& out = KIND == kDx ? a.dx : a.dw;
-      const int64_t at = token * out.stride + c;
-      if (out.type == ZERO_FP32)
-        store32(static_cast<float*>(out.p) + at, v, left, out.align);
-      else if (out.type == ZERO_BF16)
-        store32(static_cast<__nv_bfloat16*>(out.p) + at, v, left, out.align);
-      else
-        store32(static_cast<__half*>(out.p) + at, v, left, out.align);
+      write(v, c);
     }
+  }
+
+  // 32 values of dx or dw, unscaled, from column c on
+  __device__ __forceinline__ void write(float (&v)[32], int c) {
+    const int left = a.hidden - c;
+    if (left <= 0) return;
+    if (KIND == kDx && !direct) {
+      if (row >= n) return;
+      float* p = a.sums + (split * sums_rows + row) * a.sums_stride + c;
+      if (a.add) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < left) v[i] += p[i];
+      }
+      store32(p, v, left, 16);
+      return;
+    }
+    if (token < 0) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= alpha;
+    const Out& out = KIND == kDx ? a.dx : a.dw;
+    const int64_t at = token * out.stride + c;
+    if (WIDE || out.type == ZERO_FP32)
+      store32(static_cast<float*>(out.p) + at, v, left, out.align);
+    else if (out.type == ZERO_BF16)
+      store32(static_cast<__nv_bfloat16*>(out.p) + at, v, left, out.align);
+    else
+      store32(static_cast<__half*>(out.p) + at, v, left, out.align);
   }
 
   // columns [c0, c1) of the tile, of this warp's rows at d
@@ -455,7 +472,7 @@ struct Epilogue {
   // the same of a sum in several accumulators: next() gives the place of each
   // (false: given up), free() hands it back
   template <class Next, class Free>
-  __device__ __forceinline__ bool run_segments(int segments, int c0, int c1, Next next, Free free) {
+  __device__ __forceinline__ bool run_segments(int segments, int c0, int c1, bool zero, Next next, Free free) {
     constexpr int kChunks = kPartColumns / 32;
     float z[kChunks][32];
     for (int q = 0; q < segments; ++q) {
@@ -470,14 +487,22 @@ struct Epilogue {
             tc::tmem_load16(d + c0 + 32 * k + h, w);
             tc::tmem_wait_load();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[k][h + i] = q ? z[k][h + i] + __uint_as_float(w[i]) : __uint_as_float(w[i]);
+            for (int i = 0; i < 16; ++i) {
+              const float v = zero ? 0.f : __uint_as_float(w[i]);
+              z[k][h + i] = q ? z[k][h + i] + v : v;
+            }
           }
         }
       free();
     }
 #pragma unroll
     for (int k = 0; k < kChunks; ++k)
-      if (c0 + 32 * k < c1) stats(z[k], col + c0 + 32 * k);
+      if (c0 + 32 * k < c1) {
+        if constexpr (is_stats(KIND))
+          stats(z[k], col + c0 + 32 * k);
+        else
+          write(z[k], col + c0 + 32 * k);
+      }
     done();
     return true;
   }
@@ -509,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::prefetch_map(&a.a);
     tc::prefetch_map(&a.b);
     tc::prefetch_map(&a.b2);
-    if (KIND == kGrads) tc::prefetch_map(&a.a2);
+    if (is_grads(KIND)) tc::prefetch_map(&a.a2);
     for (int s = 0; s < kStages; ++s) tc::bar_init(full(s), 1), tc::bar_init(empty(s), 1);
     for (int s = 0; s < kAccumulators; ++s) tc::bar_init(acc_full(s), 1), tc::bar_init(acc_empty(s), 2 * kEpilogueWarps);
     tc::bar_init(drained, 1);
@@ -526,6 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int n = *a.count;
   Schedule<KIND> todo(a, n, blockIdx.x >> 1, gridDim.x >> 1);
   Tile t;
+  constexpr int kLong = KIND == kGradsLong ? kSegmentDw : kSegment;
   bool ok = true;
 
   if (warp == 0 && lane == 0) {
@@ -533,10 +559,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int64_t issued = 0;
     while (ok && todo.next(t)) {
       const bool whole = todo.columns() == kTileN;
+      [[maybe_unused]] const int blocks = max(1, t.k1 / (is_grads(KIND) ? a.terms : 1));
       const int half = todo.columns() / 2;  // of the columns: this CTA's operand rows
       const int row = t.m * kTileM + static_cast<int>(rank) * kHalfRows;
       const int col = t.n * todo.columns() + static_cast<int>(rank) * half;
-      const int rows_a = KIND == kGrads ? kHalfRows : a.rows_a;
+      const int rows_a = is_grads(KIND) ? kHalfRows : a.rows_a;
       const bool copies_a = rows_a == kHalfRows || rank == 0;
       const uint32_t bytes = static_cast<uint32_t>((rows_a == kHalfRows ? 2 * kHalfRows : rows_a) + todo.columns()) * (kTileK * 2);
       for (int k = t.k0; k < t.k1; ++k) {
@@ -545,16 +572,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t to_a = base + ring.slot * kStageBytes, to_b = to_a + kOperandBytes;
         const uint32_t bar = tc::in_cta(full(ring.slot), 0);
         if (rank == 0) tc::bar_expect(full(ring.slot), bytes);
-        if (KIND == kGrads && t.dw) {
-          // the second half of the depth: x again, with what dz's rounding lost
-          const bool again = a.two && 2 * k >= t.k1;
-          const int depth = (again ? k - t.k1 / 2 : k) * kTileK;
-          const int dz_row = depth + (again ? static_cast<int>(a.rows_cap) : 0);
+        if (is_grads(KIND) && t.dw) {
+          // the depth once for each term of dz, with x again
+          const int depth = k % blocks * kTileK, dz_row = depth + k / blocks * static_cast<int>(a.rows_cap);
           tc::load_box(to_a, &a.a2, row, dz_row, bar);
           tc::load_box(to_a + kOperandBytes / 2, &a.a2, row + 64, dz_row, bar);
           tc::load_box(to_b, &a.b2, col, depth, bar);
           tc::load_box(to_b + kOperandBytes / 2, &a.b2, col + 64, depth, bar);
-        } else if (KIND == kGrads) {
+        } else if (is_grads(KIND)) {
           tc::load_box(to_a, &a.a, k * kTileK, row, bar);
           tc::load_box(to_b, &a.b, col, a.first + k * kTileK, bar);
           tc::load_box(to_b + kOperandBytes / 2, &a.b, col + 64, a.first + k * kTileK, bar);
@@ -579,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     constexpr uint32_t kLead = kOperandBytes / 2;
-    constexpr bool kBByN = KIND == kGrads;
+    constexpr bool kBByN = is_grads(KIND);
     const uint32_t plain = tc::instruction(a.bf16 != 0, false, kBByN, kTileM, todo.columns());
     const uint32_t turned = tc::instruction(a.bf16 != 0, true, kBByN, kTileM, todo.columns());
     // 16 deep: 32 bytes along a row, or 16 rows of 128 bytes
@@ -590,13 +615,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = tc::bar_wait(acc_empty(acc.slot), acc.phase ^ 1);
       if (!ok) break;
       tc::fence_after();
-      const bool a_by_m = KIND == kGrads && t.dw;
+      const bool a_by_m = is_grads(KIND) && t.dw;
       const uint32_t instr = a_by_m ? turned : plain;
       const uint64_t step_a = a_by_m ? kAcross : kAlong, step_b = kBByN ? kAcross : kAlong;
       uint32_t d = tmem + acc.slot * kTileN;
       int start = t.k0;  // of the sum
       for (int k = t.k0; k < t.k1; ++k) {
-        if (KIND == kStatsLong && k == start + kSegment) {
+        if ((KIND == kStatsLong || (KIND == kGradsLong && t.dw)) && k == start + kLong) {
           tc::commit(acc_full(acc.slot));
           acc.next();
           ok = tc::bar_wait(acc_empty(acc.slot), acc.phase ^ 1);
@@ -648,21 +673,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       e.run(place(), c0, c1, t.k0 == t.k1);
       free();
     };
+    [[maybe_unused]] auto next = [&](uint32_t& d) {
+      if (!wait()) return false;
+      d = place();
+      return true;
+    };
+    [[maybe_unused]] auto segments = [&] { return max(1, (t.k1 - t.k0 + kLong - 1) / kLong); };
     while (ok && todo.next(t)) {
       if constexpr (KIND == kStatsLong) {
         Epilogue<KIND> e(a, n, todo.tiles, t.m, t.n, t.s, row, half);
-        auto next = [&](uint32_t& d) {
-          if (!wait()) return false;
-          d = place();
-          return true;
-        };
-        e.run_segments((t.k1 - t.k0 + kSegment - 1) / kSegment, c0, c1, next, free);
-      } else if constexpr (KIND != kGrads) {
+        e.run_segments(segments(), c0, c1, false, next, free);
+      } else if constexpr (!is_grads(KIND)) {
         Epilogue<KIND> e(a, n, todo.tiles, t.m, t.n, t.s, row, half);
         work(e);
       } else if (t.dw) {
-        Epilogue<kDw> e(a, n, todo.dw, t.m, t.n, t.s, row, half);
-        work(e);
+        Epilogue<kDw, KIND == kGradsLong> e(a, n, todo.dw, t.m, t.n, t.s, row, half);
+        if constexpr (KIND == kGradsLong)
+          e.run_segments(segments(), c0, c1, t.k0 == t.k1, next, free);
+        else
+          work(e);
       } else {
         Epilogue<kDx> e(a, n, todo.dx, t.m, t.n, t.s, row, half);
         work(e);
@@ -1141,13 +1170,15 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, 
 struct Layout {
   int64_t rows_cap, dz_rows, columns, pieces, xs_stride, w_stride, sums_stride;
   int64_t xs, w, part, target_z, target, ticket, cta_sums, lse2, row_mul, scales, dz, sums, dw, bytes;
+  int terms;   // of dz: 16 (bf16) or 22 (fp16) bits for a dw in binary32
   bool whole;  // rows of dx and dw are whole 16-byte words: the products write them
 
   Layout(const zero_linear_ce_desc& d, bool repack, bool backward) {
     rows_cap = up(std::max<int64_t>(d.tokens, 1), kTileM);
     whole = d.hidden % 8 == 0;
     columns = up(d.vocab, kTileN);
-    dz_rows = rows_cap * (d.dw_dtype == ZERO_FP32 ? 2 : 1);
+    terms = d.dw_dtype == ZERO_FP32 ? 2 : 1;
+    dz_rows = rows_cap * terms;
     if (backward) columns = std::min(columns, std::max<int64_t>(kTileN, kPieceBytes / 2 / dz_rows / kTileN * kTileN));
     pieces = over(d.vocab, columns);
     xs_stride = up(d.hidden, 8);
@@ -1520,7 +1551,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   if (!c.maps_of_z(std::min(at.columns, d.vocab))) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   ProductArgs z = c.product;
   z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.dz = c.in<void>(at.dz), z.dz_stride = at.columns;
-  z.two = dw && dw_dtype == ZERO_FP32;
+  z.terms = dw ? at.terms : 1;
   for (int64_t first = 0; first < d.vocab; first += at.columns) {
     const int64_t columns = std::min(at.columns, d.vocab - first);
     z.first = static_cast<int32_t>(first), z.columns = static_cast<int32_t>(columns);
@@ -1540,7 +1571,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
         !matrix_map(&p.a2, z.dz, c.bf16, columns, at.dz_rows, at.columns, kTileK) ||
         !matrix_map(&p.b2, c.in<void>(at.xs), c.bf16, d.hidden, at.rows_cap, at.xs_stride, kTileK))
       return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
-    LOSS_CUDA(launch_product<kGrads>(p, c.s));
+    LOSS_CUDA(z.terms > 1 ? launch_product<kGradsLong>(p, c.s) : launch_product<kGrads>(p, c.s));
     if (dw && !at.whole) {
       const int bytes = type_bytes(dw_dtype);
       copy = c.copy_of(p.dw.p, p.dw.stride, static_cast<char*>(dw) + first * d.hidden * bytes, d.hidden, columns, bytes);

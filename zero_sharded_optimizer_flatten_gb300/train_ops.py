@@ -735,7 +735,7 @@ def zero_linear_cross_entropy_backward(x, w, targets, ce: CrossEntropy, d_loss, 
     (ce.total[0]), its sum (ce.total[1]), each one float32 number on the
     device, or of the losses (reduction "none").  None for what is not in
     `want`.  dw_dtype: the type of w (None) or float32, for which the logits'
-    gradient is held in twice 16 bits: half as many operations more."""
+    gradient is held in two 16-bit numbers: a quarter more operations."""
     kind = _choice(_REDUCTIONS, reduction, "reduction")
     if not set(want) <= {"dx", "dw"}:
         raise ValueError(f"want must name dx or dw, got {want!r}")
