@@ -74,8 +74,8 @@ typedef enum {
   ZERO_ERR_UNSUPPORTED = 6  /* valid request this build does not implement       */
 } zero_status;
 
-/* ZERO_FP32 belongs to the gradient-list, block and expert calls below; the
- * optimizer's calls take the two 16-bit types. */
+/* ZERO_FP32 belongs to the gradient-list, block, expert, embedding and head calls
+ * below; the optimizer's calls take the two 16-bit types. */
 typedef enum { ZERO_FP16 = 0, ZERO_BF16 = 1, ZERO_FP32 = 2 } zero_dtype;
 typedef enum { ZERO_PART_FLAT = 0, ZERO_PART_ROUND_ROBIN = 1 } zero_part_mode;
 typedef enum { ZERO_REDUCE_SUM = 0, ZERO_REDUCE_AVG = 1 } zero_reduce_op;

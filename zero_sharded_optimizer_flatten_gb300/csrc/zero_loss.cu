@@ -75,6 +75,11 @@ struct Scales {
   float g;      // d_loss as one number (sum, mean)
 };
 
+// The kept rows, however the caller's list was treated since.
+__device__ __forceinline__ int kept_rows(const int32_t* count, int64_t tokens) {
+  return min(max(*count, 0), static_cast<int>(tokens));
+}
+
 // Where a product goes: rows of `p`, the product's first to row `first`.
 struct Out {
   void* p;
@@ -342,7 +347,7 @@ struct Epilogue {
       direct = a.direct && a.pieces == 1 && t.splits == 1;
       sums_rows = up(n, kTileM);
       if (live) token = a.rows[row];
-      if (token >= a.tokens) token = -1;
+      if (token >= a.tokens) token = -1;  // negative ones are not written either
       alpha = a.scales->alpha;
     }
     if constexpr (KIND == kDw) {
@@ -548,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   wait_for_previous();
 
-  const int n = *a.count;
+  const int n = kept_rows(a.count, a.tokens);
   Schedule<KIND> todo(a, n, blockIdx.x >> 1, gridDim.x >> 1);
   Tile t;
   constexpr int kLong = KIND == kGradsLong ? kSegmentDw : kSegment;
@@ -824,7 +829,7 @@ __device__ __forceinline__ Scales scales_of_one(const RowsArgs& a, int n) {
 __global__ void __launch_bounds__(kScanThreads) k_loss_scales(const RowsArgs a) {
   __shared__ float most[32];
   let_next_start();
-  const int n = a.rows[a.tokens];
+  const int n = kept_rows(a.rows + a.tokens, a.tokens);
   float top = 0.f;
   for (int i = threadIdx.x; i < n; i += kScanThreads) {
     const int t = a.rows[i];
@@ -926,7 +931,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
       if (threadIdx.x == 0) a.rows[a.tokens] = n, *a.ticket = 0;
     }
   } else {
-    n = a.rows[a.tokens];
+    n = kept_rows(a.rows + a.tokens, a.tokens);
   }
   [[maybe_unused]] Scales scales = {};
   if constexpr (BACKWARD) {
@@ -996,7 +1001,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
   __shared__ float sums[kFinishThreads / 32], mine[kFinishRows];
   __shared__ bool last;
   wait_for_previous();
-  const int n = a.rows[a.tokens];
+  const int n = kept_rows(a.rows + a.tokens, a.tokens);
   const int parts = kParts * static_cast<int>(over(a.vocab, tile_columns((n + kTileM - 1) / kTileM, a.vocab, a.narrow, a.pairs)));
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kFinishRows, rows = up(n, kTileM);
   // of the row that this thread writes: loaded ahead of the parts
@@ -1115,7 +1120,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, 
     copy_rows(copy, blockIdx.x);
     return;
   }
-  const int n = a.rows[a.tokens];
+  const int n = kept_rows(a.rows + a.tokens, a.tokens);
   const int splits = split_of((n + kTileM - 1) / kTileM * ((a.hidden + kTileN - 1) / kTileN), a.piece, a.pairs);
   if (splits == 1 && a.pieces == 1 && a.direct) return;
   const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
