@@ -213,37 +213,49 @@ struct Schedule {
   }
 };
 
-// dx's tiles first, which are the deeper ones. The pairs that have none in its
-// last round do as many of dw's instead as end first with the rest; then all go
-// on with dw's. (Two launches: 4% of dx's time and 3% of dw's are idle at 8192 x
-// 4096 x 32000, and each has a start and an end.)
+// The deeper of dx's and dw's tiles first. The pairs that have none in their last
+// round do as many of the others instead as end first with the rest; then all go
+// on with the others. (Two launches: 4% of dx's time and 3% of dw's are idle at
+// 8192 x 4096 x 32000, and each has a start and an end.)
 struct GradsSchedule {
   Tiles<kDx> dx;
   Tiles<kDw> dw;
-  int at, pairs, pair, idle, ahead, from, stage = 0;
+  int at, pairs, pair, deep_total, flat_total, idle, ahead, from, stage = 0;
+  bool dw_first;
   __device__ __forceinline__ GradsSchedule(const ProductArgs& a, int n, int pair_, int pairs_)
       : dx(a, n), dw(a, n), at(pair_), pairs(pairs_), pair(pair_) {
     if (!a.dx.p) dx.total = 0;
     if (!a.dw.p) dw.total = 0;
-    const int busy = dx.total % pairs;
-    idle = busy ? pairs - busy : 0;
     // a tile costs about eight blocks beside its own
-    const int deep = dx.depth_blocks / dx.splits + 8, flat = dw.depth_blocks + 8;
+    const int of_dx = dx.depth_blocks / dx.splits + 8, of_dw = dw.depth_blocks + 8;
+    dw_first = of_dw > of_dx;
+    const int deep = max(of_dx, of_dw), flat = min(of_dx, of_dw);
+    deep_total = dw_first ? dw.total : dx.total, flat_total = dw_first ? dx.total : dw.total;
+    const int busy = deep_total % pairs;
+    idle = busy ? pairs - busy : 0;
     int least = INT32_MAX, best = 0;
     for (int each = deep / flat, k = 0; k < 3 && idle; ++k, ++each) {
-      const int64_t end = max(deep, each * flat) + static_cast<int64_t>((max(0, dw.total - each * idle) + pairs - 1) / pairs) * flat;
+      const int64_t end = max(deep, each * flat) + static_cast<int64_t>((max(0, flat_total - each * idle) + pairs - 1) / pairs) * flat;
       if (end < least) least = static_cast<int>(end), best = each;
     }
-    ahead = min(dw.total, best * idle);
+    ahead = static_cast<int>(min(static_cast<int64_t>(flat_total), static_cast<int64_t>(best) * idle));
     from = pair - busy;  // among the idle ones
   }
   __device__ __forceinline__ int columns() const { return kTileN; }
+  __device__ __forceinline__ void take(bool of_dw, Tile& t) const {
+    t.dw = of_dw;
+    if (of_dw) {
+      dw.at(at, t.m, t.n, t.s);
+      dw.depth(t.s, t.k0, t.k1);
+    } else {
+      dx.at(at, t.m, t.n, t.s);
+      dx.depth(t.s, t.k0, t.k1);
+    }
+  }
   __device__ __forceinline__ bool next(Tile& t) {
     if (stage == 0) {
-      if (at < dx.total) {
-        dx.at(at, t.m, t.n, t.s);
-        dx.depth(t.s, t.k0, t.k1);
-        t.dw = false;
+      if (at < deep_total) {
+        take(dw_first, t);
         at += pairs;
         return true;
       }
@@ -251,15 +263,12 @@ struct GradsSchedule {
       at = idle && from >= 0 ? from : ahead;
     }
     if (stage == 1 && at >= ahead) stage = 2, at = ahead + pair;
-    if (at >= dw.total) return false;
-    dw.at(at, t.m, t.n, t.s);
-    dw.depth(t.s, t.k0, t.k1);
-    t.dw = true;
+    if (at >= flat_total) return false;
+    take(!dw_first, t);
     at += stage == 1 ? idle : pairs;
     return true;
   }
 };
-
 template <>
 struct Schedule<kGrads> : GradsSchedule {
   using GradsSchedule::GradsSchedule;
@@ -360,11 +369,10 @@ struct Epilogue {
   template <class T>
   __device__ __forceinline__ void store_dz(T* to, float (&p)[32]) {
     store32(to, p, 32, 32);
-    for (int k = 1; k < a.terms; ++k) {
+    if (a.terms == 2) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) p[i] -= Elem<T>::widen(Elem<T>::narrow(p[i]));
-      to += a.rows_cap * a.dz_stride;
-      store32(to, p, 32, 32);
+      store32(to + a.rows_cap * a.dz_stride, p, 32, 32);
     }
   }
 
@@ -564,7 +572,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int64_t issued = 0;
     while (ok && todo.next(t)) {
       const bool whole = todo.columns() == kTileN;
-      [[maybe_unused]] const int blocks = max(1, t.k1 / (is_grads(KIND) ? a.terms : 1));
+      // of dw: the depth once for each term of dz, with x again
+      [[maybe_unused]] const int depth_end = is_grads(KIND) ? t.k1 / a.terms * kTileK : 0;
+      [[maybe_unused]] int depth = 0, term = 0;  // term: its first row of dz
       const int half = todo.columns() / 2;  // of the columns: this CTA's operand rows
       const int row = t.m * kTileM + static_cast<int>(rank) * kHalfRows;
       const int col = t.n * todo.columns() + static_cast<int>(rank) * half;
@@ -578,12 +588,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t bar = tc::in_cta(full(ring.slot), 0);
         if (rank == 0) tc::bar_expect(full(ring.slot), bytes);
         if (is_grads(KIND) && t.dw) {
-          // the depth once for each term of dz, with x again
-          const int depth = k % blocks * kTileK, dz_row = depth + k / blocks * static_cast<int>(a.rows_cap);
-          tc::load_box(to_a, &a.a2, row, dz_row, bar);
-          tc::load_box(to_a + kOperandBytes / 2, &a.a2, row + 64, dz_row, bar);
+          tc::load_box(to_a, &a.a2, row, term + depth, bar);
+          tc::load_box(to_a + kOperandBytes / 2, &a.a2, row + 64, term + depth, bar);
           tc::load_box(to_b, &a.b2, col, depth, bar);
           tc::load_box(to_b + kOperandBytes / 2, &a.b2, col + 64, depth, bar);
+          depth += kTileK;
+          if (depth == depth_end) depth = 0, term += static_cast<int>(a.rows_cap);
         } else if (is_grads(KIND)) {
           tc::load_box(to_a, &a.a, k * kTileK, row, bar);
           tc::load_box(to_b, &a.b, col, a.first + k * kTileK, bar);
