@@ -283,7 +283,6 @@ struct SumArgs {
   int2* tail;            // [chunks]: the id that begins in a chunk and goes on (-1: none), chunks that it goes on in
   int32_t hidden, out_type, add, vocab, chunk;
   int64_t chunks;
-  int64_t tokens;
   float scale;
 };
 
@@ -700,7 +699,7 @@ extern "C" zero_status zero_embedding_backward(const void* dy, int64_t dy_stride
   a.order = sort.order, a.starts = sort.starts, a.total_at = at.buckets * at.minors;
   a.bits = at.bits, a.minors = at.minors, a.dy = dy, a.dy_stride = dy_stride, a.part_stride = at.part_stride;
   a.out = dtable, a.part = reinterpret_cast<float*>(ws + at.part), a.hidden = static_cast<int32_t>(hidden);
-  a.out_type = dtable_dtype, a.add = accumulate != 0, a.vocab = static_cast<int32_t>(vocab), a.tokens = tokens;
+  a.out_type = dtable_dtype, a.add = accumulate != 0, a.vocab = static_cast<int32_t>(vocab);
   a.scale = static_cast<float>(scale), a.tail = reinterpret_cast<int2*>(ws + at.tail), a.chunk = at.chunk, a.chunks = at.chunks;
   const bool vec = wide_rows(hidden, dy, dy_stride, e) && wide_rows(hidden, dtable, hidden, type_bytes(dtable_dtype));
   if (r == cudaSuccess)

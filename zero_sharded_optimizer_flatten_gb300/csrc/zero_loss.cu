@@ -92,7 +92,7 @@ struct ProductArgs {
   CUtensorMap a2, b2;  // kGrads: of dw; kStats, kProbs: b2 for narrow tiles
   const int32_t* count;  // kept rows n
   int64_t rows_cap;      // n rounded up to whole tiles at most
-  int32_t vocab, hidden;
+  int32_t hidden;
   int32_t first;         // the piece's first column of z
   int32_t columns;       // of the piece
   int32_t piece;         // columns of a whole piece
@@ -1391,7 +1391,7 @@ struct Call {
     rows.rows_cap = at.rows_cap, rows.target = in<int32_t>(at.target);
     set_vec(d.hidden % 8 == 0 && d.x_stride % 8 == 0 && aligned_to(x, 16));
     product.count = row_list + d.tokens, product.rows_cap = at.rows_cap;
-    product.vocab = static_cast<int32_t>(d.vocab), product.hidden = static_cast<int32_t>(d.hidden);
+    product.hidden = static_cast<int32_t>(d.hidden);
     product.bf16 = bf16, product.err = err, product.scale2 = static_cast<float>(d.scale * 1.4426950408889634);
     product.target = rows.target, product.rows = row_list, product.tokens = d.tokens;
     product.pieces = static_cast<int32_t>(at.pieces), product.piece = static_cast<int32_t>(at.columns);
