@@ -67,6 +67,24 @@ __device__ __forceinline__ float reciprocal(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// exp(z - top), 0 for -inf.  The difference comes first: top * log2(e) rounded
+// beforehand would leave up to 2^-24 of its size in every exponent, all of p for
+// rows around -1e9, and infinities for rows at the type's end.  In pairs it costs
+// what one multiplication and addition of single values did.
+__device__ __forceinline__ float exp_from(float z, float top) { return tc::exp2_of((z - top) * kLog2e); }
+template <int VPT>
+__device__ __forceinline__ void exp_from(float (&z)[VPT], float top) {
+  if constexpr (VPT == 1) {
+    z[0] = exp_from(z[0], top);
+  } else {
+    const F2 minus = f2(-top), by = f2(kLog2e);
+#pragma unroll
+    for (int j = 0; j < VPT; j += 2) {
+      f2_out(mul2(add2(f2(z[j], z[j + 1]), minus), by), z[j], z[j + 1]);
+      z[j] = tc::exp2_of(z[j]), z[j + 1] = tc::exp2_of(z[j + 1]);
+    }
+  }
+}
 __device__ __forceinline__ float log2_of(float v) {
   float r;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -257,20 +275,17 @@ __global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs
         }
       }
     }
-    const float top2 = top * kLog2e;
+    exp_from(v, top);
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      v[j] = tc::exp2_of(fmaf(v[j], kLog2e, -top2));  // 0 where nothing is left
-      s += v[j];
-    }
+    for (int j = 0; j < VPT; ++j) s += v[j];
     s = warp_all_sum(s);
     const float inv = any ? reciprocal(s) : 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) total[j] = fmaf(v[j], inv, total[j]);
     const float lse = any ? top + log2_of(s) * kLn2 : 0.f;
     if (any) n += 1.f, squares = fmaf(lse, lse, squares);
-    float weight = tc::exp2_of(fmaf(chosen_z, kLog2e, -top2));  // 0 without a choice
+    float weight = exp_from(chosen_z, top);  // 0 without a choice
     if (a.normalize) {
       const float all = warp_all_sum(weight);
       weight = any ? weight * reciprocal(all) : 0.f;
