@@ -114,3 +114,51 @@ def test_a_padded_token_under_a_mask_of_the_lowest_value(dtype):
     assert torch.equal(r.weights[::5], torch.full((100, 4), 0.25, device="cuda"))
     balance = definition(z.double(), 4, True)[3]
     near(r.losses[:1], balance[None], balance[None] * REL, "balance")
+
+
+def gradient(z, K, normalize, dw, dl):
+    """In 64 bits, with the size of its terms."""
+    z64 = z.double().requires_grad_()
+    chosen, kept, w, balance, zloss, lse, p, counts, n = definition(z64, K, normalize)
+    loss = (w * dw.double()).sum() + dl[0].double() * balance + dl[1].double() * zloss
+    grad, = torch.autograd.grad(loss, z64)
+    grad = torch.nan_to_num(grad)
+    with torch.no_grad():
+        E = z.shape[1]
+        load = counts.double() * E / (K * n * n) * abs(float(dl[0]))
+        wd = w * dw.double().abs()
+        direct = wd + w * wd.sum(1, keepdim=True) if normalize else wd
+        size = p * (load + (p * load).sum(1, keepdim=True) + 2 / n * abs(float(dl[1])) * lse.abs()[:, None])
+        if not normalize:
+            size = size + p * wd.sum(1, keepdim=True)
+        size = size.scatter_add(1, chosen, direct * kept)
+    return grad, size
+
+
+@pytest.mark.parametrize("dtype", list(SIZES), ids=str)
+@pytest.mark.parametrize("experts", [8, 17, 64, 256, 1000])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gradient_of_rows_of_any_size(experts, dtype, normalize):
+    K = 3
+    z = rows(experts, dtype, SIZES[dtype])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(experts)
+    dw = torch.randn(z.shape[0], K, device="cuda", generator=g)
+    r = Z.zero_expert_route(z, K, normalize=normalize)
+    for dl in (torch.tensor([7.0, 0.0], device="cuda"), torch.tensor([0.0, 0.0], device="cuda"),
+               torch.tensor([7.0, 1e-3], device="cuda")):
+        if float(dl[1]) and dtype == F32:
+            continue   # lse as a factor: past binary32's end for the largest rows
+        got = Z.zero_expert_route_backward(z, r, dw, dl)
+        grad, size = gradient(z, K, normalize, dw, dl)
+        near(got, grad, size * 4 * REL + 2.0 ** -44 * size.sum(1, keepdim=True), "d_logits")
+
+
+def test_a_token_masked_with_a_large_value_gets_the_gradient_of_equal_choices():
+    """Scores that are all -1e9: probabilities 1/8, so the gradient of the
+    balance loss is that of any token with equal scores."""
+    z = torch.zeros(6, 8, device="cuda")
+    z[2:] = -1e9
+    dl = torch.tensor([1.0, 0.0], device="cuda")
+    d = Z.zero_expert_route_backward(z, Z.zero_expert_route(z, 2), None, dl)
+    assert torch.equal(d[2:], d[:1].expand(4, 8)) and bool((d != 0).any())
