@@ -162,3 +162,25 @@ def test_a_token_masked_with_a_large_value_gets_the_gradient_of_equal_choices():
     dl = torch.tensor([1.0, 0.0], device="cuda")
     d = Z.zero_expert_route_backward(z, Z.zero_expert_route(z, 2), None, dl)
     assert torch.equal(d[2:], d[:1].expand(4, 8)) and bool((d != 0).any())
+
+
+@pytest.mark.parametrize("experts", [4, 40, 256])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_the_same_experts_in_another_order_token_after_token(experts, normalize):
+    """The same few experts are every token's choices, in turning order, so that
+    one expert's place is cleared for a token and taken for the next by another
+    thread; several tokens a warp."""
+    T, K = 40_000, 4
+    turn = (torch.arange(T, device="cuda")[:, None] // 9728 + torch.arange(K, device="cuda")) % K
+    z = torch.full((T, experts), -9.0, device="cuda")
+    z.scatter_(1, turn, torch.linspace(2.0, 0.5, K, device="cuda").expand(T, K).contiguous())
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    dw, dl = torch.randn(T, K, device="cuda", generator=g), torch.zeros(2, device="cuda")
+    r = Z.zero_expert_route(z, K, normalize=normalize)
+    assert torch.equal(r.ids, turn.to(torch.int32))
+    got = Z.zero_expert_route_backward(z, r, dw, dl)
+    grad, size = gradient(z, K, normalize, dw, dl)
+    near(got, grad, size * 4 * REL + 2.0 ** -44 * size.sum(1, keepdim=True), "d_logits")
+    for _ in range(3):
+        assert torch.equal(got, Z.zero_expert_route_backward(z, r, dw, dl))

@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(256, backward_ctas(VPT)) k_route_backward(cons
     for (int j = 0; j < VPT; ++j) v[j] = any ? fmaf(v[j] * inv, load[j] + shift, extra[j]) : 0.f;
     __syncwarp();
     if (id >= 0) mine[id] = 0.f;
+    __syncwarp();  // another lane may have the same expert of the next token
     T* row = dz + t * E;
     if constexpr (VPT % 8 == 0) {
       if (a.vec) {
