@@ -7,8 +7,8 @@ once, its product with log2(e) twice (the constant as well): an exponent in base
 where exp does not vanish in binary32.  ex2 is off by 2^-22 relative, a row's
 sum of up to 1024 by 48 * 2^-24 and its reciprocal by 2^-23, so p and the
 weights by REL = 104 * 4.4 * 2^-24 + 2^-18 < 2^-15 relative and 2^-126 absolutely
-(ex2 flushes what is smaller).  lse is top and a logarithm below 7, rounded: 2^-23
-of it and REL.  Sums of p over the tokens add (T / 4864 + 220) 2^-24, the
+(ex2 flushes what is smaller).  lse is top and a logarithm below 7 (off by 2^-22 of itself),
+rounded: 2^-23 of it and REL.  Sums of p over the tokens add (T / 4864 + 220) 2^-24, the
 gradient's sums over the experts 4 REL of the terms' absolute sums.
 """
 import gc
@@ -184,3 +184,15 @@ def test_the_same_experts_in_another_order_token_after_token(experts, normalize)
     near(got, grad, size * 4 * REL + 2.0 ** -44 * size.sum(1, keepdim=True), "d_logits")
     for _ in range(3):
         assert torch.equal(got, Z.zero_expert_route_backward(z, r, dw, dl))
+
+
+def test_lse_of_equal_scores():
+    """The sum of E ones is exact, and so is 0 + log(E) but for the base-2
+    logarithm's 2^-22 and its product with log(2), 2^-24 and 2^-25 for the
+    constant."""
+    for experts in range(1, 1025):
+        if experts > 64 and experts % 37 and experts & (experts - 1):
+            continue
+        r = Z.zero_expert_route(torch.zeros(2, experts, device="cuda"), 1)
+        want = math.log(experts)
+        assert abs(float(r.stats[0].double()) - want) <= want * 1.376 * 2.0 ** -22, experts

@@ -60,8 +60,10 @@ struct RouteArgs {
   void* dz;
 };
 
-// Within one place in the last, of sums of at least 1 (2^-22 absolutely for the
-// logarithm).
+// Of sums of at least 1: within one place in the last; the logarithm within 2^-22
+// of itself (absolutely only below 2), up to 1.7e-6 of 1024 experts' lse, where
+// it goes into lse and the z loss alone. (logf: 43.1 us in place of 41.1 for 65536 x
+// 256.)
 __device__ __forceinline__ float reciprocal(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
