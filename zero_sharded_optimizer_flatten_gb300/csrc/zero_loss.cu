@@ -11,9 +11,9 @@
 // over them alone and nothing of a left-out row is read.
 //
 // One kernel (k_loss_product) does the products of both passes:
-//   kStats  tiles of z, of which only every row's maximum and sum of
-//           exponentials leave the SM; joined by k_loss_finish (kStatsLong: for a
-//           long depth, summed in several accumulators)
+//   kStats  tiles of z, of which only every row's target and the others'
+//           maximum and sum of exponentials leave the SM; joined by k_loss_finish
+//           (kStatsLong: for a long depth, summed in several accumulators)
 //   kProbs  tiles of z again, to dz in 16 bits, a piece of the vocabulary at a
 //           time (kPieceBytes); for dw in binary32 to two 16-bit numbers
 //           ("terms"), the second what the first one's rounding lost
@@ -103,7 +103,7 @@ struct ProductArgs {
   int32_t rows_a;        // rows of x in a box (fewer than 128: of one CTA, there are no more)
   float scale2;          // scale * log2(e)
   const int32_t* target;
-  float2* part;          // [column tiles * 2][n rounded up]: maximum and sum, base 2
+  float2* part;          // [column tiles * 2][n rounded up]: maximum and sum without the target's, base 2
   float* target_z;       // base 2
   const float* lse2;
   const float* row_mul;
@@ -385,6 +385,14 @@ struct Epilogue {
       for (int i = 0; i < 32; ++i)
         if (c + i >= a.columns) t[i] = -INFINITY;
     }
+    // the target stands apart: a sum with its 1 in it would lose what a confident
+    // token's loss consists of
+    const int rel = target - c;
+    if (__any_sync(kFull, rel >= 0 && rel < 32)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (rel == i) a.target_z[row] = t[i], t[i] = -INFINITY;
+    }
     float most = t[0];
 #pragma unroll
     for (int i = 1; i < 32; ++i) most = fmaxf(most, t[i]);
@@ -395,12 +403,6 @@ struct Epilogue {
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += tc::exp2_of(t[i] - base);
     sum = s, top = most;
-    const int rel = target - c;
-    if (__any_sync(kFull, rel >= 0 && rel < 32)) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (rel == i) a.target_z[row] = t[i];
-    }
   }
 
   __device__ __forceinline__ void take(const uint32_t (&w)[32], int c0, bool zero) {
@@ -1003,8 +1005,8 @@ __device__ __forceinline__ void join(float& top, float& sum, float other_top, fl
   top = most;
 }
 
-// Every kept row's statistics joined over its parts, 32 threads a row; the CTA
-// that is last adds the losses up, in one order.
+// Every kept row's statistics joined over its parts, 32 threads a row, and with
+// its target; the CTA that is last adds the losses up, in one order.
 constexpr int kFinishRows = 8, kFinishGroups = 32, kFinishThreads = kFinishRows * kFinishGroups, kFinishAhead = 8;
 __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a) {
   __shared__ float2 part[kFinishGroups][kFinishRows + 1];
@@ -1046,9 +1048,11 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
     if (g == 0) {
       float loss = 0.f;
       if (own < n && token >= 0) {
-        const float lse2 = p.x + log2f(p.y);
-        loss = (lse2 - target_z) * kLn2;
-        a.lse_out[token] = lse2 * kLn2;
+        // loss = log(1 + 2^d), d what the others' log2 of the sum is above the
+        // target: differences first, so that small losses keep all their bits
+        const float rest = log2f(p.y), d = (p.x - target_z) + rest, less = log1pf(exp2f(-fabsf(d)));
+        loss = target_z < INFINITY ? fmaf(fmaxf(d, 0.f), kLn2, less) : NAN;
+        a.lse_out[token] = fmaf(d > 0.f ? p.x + rest : target_z, kLn2, less);
         a.losses[token] = loss;
       }
       mine[r] = loss;
