@@ -855,6 +855,13 @@ zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc, const voi
                                       float* total, void* workspace, int64_t workspace_bytes,
                                       void* stream);
 
+/* The same with one more output: rest[t] = 1 - p[targets[t]], the others'
+ * probability, 0 for a left-out token; float[tokens]. */
+zero_status zero_linear_cross_entropy_rest(const zero_linear_ce_desc* desc, const void* x, const void* w,
+                                           const void* targets, float* losses, float* lse, float* rest,
+                                           int32_t* rows, float* total, void* workspace,
+                                           int64_t workspace_bytes, void* stream);
+
 /* dx [tokens, hidden] and dw [vocab, hidden], contiguous, either may be NULL,
  * from the forward call's lse and rows; x, w and targets still hold what it
  * read.  d_loss (device): of ZERO_LOSS_NONE float[tokens], the gradients of the
@@ -870,6 +877,18 @@ zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, 
                                                int32_t reduction, void* dx, void* dw,
                                                void* workspace, int64_t workspace_bytes,
                                                void* stream);
+
+/* The same with the rest that zero_linear_cross_entropy_rest left: the gradient
+ * of the target's logit is -rest, to its last places.  The call above forms it
+ * as p - 1 from lse, off by up to 2^-22 |lse|, which is all of it where the
+ * target is that certain. */
+zero_status zero_linear_cross_entropy_rest_backward(const zero_linear_ce_desc* desc, const void* x,
+                                                    const void* w, const void* targets,
+                                                    const float* lse, const float* rest,
+                                                    const int32_t* rows, const float* d_loss,
+                                                    int32_t reduction, void* dx, void* dw,
+                                                    void* workspace, int64_t workspace_bytes,
+                                                    void* stream);
 
 /*
  * Measurement helper; the pages have no counterpart.  Launches, on `stream`,

@@ -7,6 +7,11 @@ together), the difference of two and the logarithm of a sum are rounded after
 that; a sum of exponentials is off by less than 400 * 2^-24 of itself.  All of it
 is relative in the others' probability, which is what a small loss is:
 REL = 2 * 1.45 * |z| 2^-23 + 400 * 2^-24 + 2^-20.
+
+Gradients: dz is g (p - [target]) rounded to the inputs' type (fp16: or by 2^-25
+of its scale, 2^14 / g), the others' p off by 2^-21 (|lse| + |z|) besides; products
+and sums of dx over V and of dw over T columns as in the tests of the cross
+entropy: (V/16 + 2) 2^-22 + 80 2^-24 of the sum of their sizes.
 """
 import gc
 
@@ -34,6 +39,10 @@ def _cuda_cleanup():
 
 def near(got, ref, slack, what):
     bound = slack + ref.abs() * UNIT[got.dtype] * 1.001 + TINY[got.dtype]
+    if got.dtype == H16:
+        # 65504 is binary16's largest number and 32 half its step: from 65520 on nearest is infinity, of the same sign
+        past = (ref.abs() >= 65520.0 + slack) & (got.double() == ref.sign() * float("inf"))
+        got, ref = torch.where(past, torch.zeros_like(got), got), torch.where(past, torch.zeros_like(ref), ref)
     bad = ~((got.double() - ref).abs() <= bound)
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}: "
                            f"{float(got[bad][0])} for {float(ref[bad][0])}")
@@ -106,3 +115,56 @@ def test_scores_that_are_not_finite():
     ce = Z.zero_linear_cross_entropy(x, w, targets)
     # inf * 0 is NaN in the other rows' products with those channels
     assert not bool(ce.losses.isfinite()[:3].any()) and not bool(ce.total[:2].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", [H16, B16], ids=str)
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_gradients_of_confident_tokens(case, dtype):
+    T, V, margins, lift = case
+    x, w, targets = confident(T, V, margins, dtype, lift)
+    ce = Z.zero_linear_cross_entropy(x, w, targets)
+    losses, lse, rest, rel = reference(x, w, targets)
+    near(ce.rest, rest, rest * rel, "rest")
+    d = torch.full((), 2.0 ** 12, device="cuda")
+    xd, wd = x.double(), w.double()
+    z = xd @ wd.t()
+    p = torch.exp(z - lse[:, None])
+    dz = p.scatter(1, targets[:, None], -rest[:, None]) * float(d)
+    off = dz.abs() * (UNIT[dtype] * 1.001 + 2.0 ** -20 + 2.0 ** -21 * (lse.abs() + z.abs().amax(1))[:, None])
+    off = off + (float(d) * 2.0 ** -13 * 2.0 ** -25 if dtype == H16 else 0.0)
+    refs = {"dx": dz @ wd, "dw": dz.t() @ xd}
+    slack = {"dx": (off + dz.abs() * ((V / 16 + 2) * 2.0 ** -22 + 80 * 2.0 ** -24)) @ wd.abs(),
+             "dw": (off + dz.abs() * ((T / 16 + 2) * 2.0 ** -22)).t() @ xd.abs()}
+    dx, dw = Z.zero_linear_cross_entropy_backward(x, w, targets, ce, d, reduction="sum")
+    near(dx, refs["dx"], slack["dx"], "dx")
+    near(dw, refs["dw"], slack["dw"], "dw")
+    a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+    (Z.linear_cross_entropy(a, b, targets, reduction="sum") * d).backward()
+    assert torch.equal(a.grad, dx) and torch.equal(b.grad, dw)
+
+
+def test_gradients_of_changed_losses_and_without_rest():
+    """What a caller makes of the losses does not enter; without `rest` the
+    gradient of ordinary tokens is the same but for roundings."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    x = torch.randn(90, 64, device="cuda", generator=g).to(B16)
+    w = (torch.randn(400, 64, device="cuda", generator=g) / 8).to(B16)
+    targets = torch.randint(-1, 400, (90,), device="cuda", generator=g)
+    ce = Z.zero_linear_cross_entropy(x, w, targets)
+    one = torch.ones((), device="cuda")
+    dx, dw = Z.zero_linear_cross_entropy_backward(x, w, targets, ce, one)
+    assert bool((ce.rest[targets < 0] == 0).all())
+    ce.losses.mul_(3.0)
+    again = Z.zero_linear_cross_entropy_backward(x, w, targets, ce, one)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    a = x.clone().requires_grad_()
+    out = Z.linear_cross_entropy(a, w, targets, reduction="none")
+    out.mul_(2.0)
+    out.sum().backward()
+    assert bool(a.grad.isfinite().all()) and bool(a.grad.any())
+    ce.rest = None
+    less = Z.zero_linear_cross_entropy_backward(x, w, targets, ce, one)
+    # at most a rounding step of dz's largest entries apart
+    assert float((less[0].double() - dx.double()).abs().max()) <= 2.0 ** -7 * float(dx.abs().max())
+    assert float((less[1].double() - dw.double()).abs().max()) <= 2.0 ** -7 * float(dw.abs().max())

@@ -35,7 +35,8 @@ _TRAIN_OPS = ("ClipGradNorm", "CrossEntropy", "ExpertOrder", "ExpertRoute", "Gra
               "zero_expert_route_workspace_bytes", "zero_expert_sort",
               "zero_expert_sort_workspace_bytes", "zero_grad_norm",
               "zero_grad_norm_workspace_bytes", "zero_linear_cross_entropy",
-              "zero_linear_cross_entropy_backward", "zero_linear_cross_entropy_workspace_bytes")
+              "zero_linear_cross_entropy_backward", "zero_linear_cross_entropy_rest",
+              "zero_linear_cross_entropy_rest_backward", "zero_linear_cross_entropy_workspace_bytes")
 
 
 def __getattr__(name):

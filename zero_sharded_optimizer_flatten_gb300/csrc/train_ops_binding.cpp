@@ -1,5 +1,6 @@
 // Python binding of the block join, the expert permutation and routing, the
-// token embedding and the head's cross entropy: checks of the tensors, new outputs, the current stream, the C call of include/zero.h.
+// token embedding and the head's cross entropy: checks of the tensors, new
+// outputs, the current stream, the C call of include/zero.h.
 // train_ops.py has the functions' Python signatures and documentation.
 //
 // These calls are made many times a step and their kernels can take a few
@@ -729,7 +730,7 @@ PyObject* linear_cross_entropy_workspace_bytes(PyObject*, PyObject* const* a, Py
   });
 }
 
-// x, w, targets, scale, workspace -> (losses, lse, total, rows)
+// x, w, targets, scale, workspace -> (losses, lse, total, rows, rest)
 PyObject* linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
     expect_args(n_args, 5);
@@ -738,26 +739,30 @@ PyObject* linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     const Tensor ws = h.workspace(a[4], false, &need);
     const at::TensorOptions f = h.x.options().dtype(at::kFloat);
     const Tensor losses = at::empty(h.targets.sizes(), f), lse = at::empty(h.targets.sizes(), f),
-                 total = at::empty({3}, f), rows = at::empty({h.d.tokens + 1}, f.dtype(at::kInt));
+                 total = at::empty({3}, f), rows = at::empty({h.d.tokens + 1}, f.dtype(at::kInt)),
+                 rest = at::empty(h.targets.sizes(), f);
     void* stream = stream_of(h.dev);
     unlocked([&] {
-      return zero_linear_cross_entropy(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets), static_cast<float*>(ptr(losses)),
-                                       static_cast<float*>(ptr(lse)), static_cast<int32_t*>(ptr(rows)),
-                                       static_cast<float*>(ptr(total)), ptr(ws), need, stream);
+      return zero_linear_cross_entropy_rest(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets), static_cast<float*>(ptr(losses)),
+                                            static_cast<float*>(ptr(lse)), static_cast<float*>(ptr(rest)),
+                                            static_cast<int32_t*>(ptr(rows)), static_cast<float*>(ptr(total)), ptr(ws),
+                                            need, stream);
     });
-    return tuple_of({losses, lse, total, rows});
+    return tuple_of({losses, lse, total, rows, rest});
   });
 }
 
 // x, w, targets, scale, lse, rows, d_loss, reduction, want_dx, want_dw, dx, dw,
-// dw_type (-1: w's), workspace -> (dx, dw)
+// dw_type (-1: w's), workspace, rest (None: from lse) -> (dx, dw)
 PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    expect_args(n_args, 14);
+    expect_args(n_args, 15);
     Head h(a);
-    const Tensor lse = tensor(a[4], "lse"), rows = tensor(a[5], "rows"), d_loss = tensor(a[6], "d_loss");
+    const Tensor lse = tensor(a[4], "lse"), rows = tensor(a[5], "rows"), d_loss = tensor(a[6], "d_loss"),
+                 rest = maybe(a[14], "rest");
     const int reduction = small(a[7], "reduction");
     result(lse, "lse", h.targets.sizes(), at::kFloat, h.x);
+    if (rest.defined()) result(rest, "rest", h.targets.sizes(), at::kFloat, h.x);
     result(rows, "rows", {h.d.tokens + 1}, at::kInt, h.x);
     if (reduction == ZERO_LOSS_NONE) {
       result(d_loss, "d_loss", h.targets.sizes(), at::kFloat, h.x);
@@ -776,11 +781,14 @@ PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_
     if (want_dw) dw = result(dw, "dw", h.w.sizes(), scalar_of(h.d.dw_dtype), h.w);
     void* stream = stream_of(h.dev);
     unlocked([&] {
-      return zero_linear_cross_entropy_backward(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets),
-                                                static_cast<const float*>(ptr(lse)),
-                                                static_cast<const int32_t*>(ptr(rows)),
-                                                static_cast<const float*>(ptr(d_loss)), reduction, ptr(dx), ptr(dw),
-                                                ptr(ws), need, stream);
+      const float *of_lse = static_cast<const float*>(ptr(lse)), *d = static_cast<const float*>(ptr(d_loss));
+      const int32_t* list = static_cast<const int32_t*>(ptr(rows));
+      if (!rest.defined())
+        return zero_linear_cross_entropy_backward(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets), of_lse, list, d, reduction,
+                                                  ptr(dx), ptr(dw), ptr(ws), need, stream);
+      return zero_linear_cross_entropy_rest_backward(&h.d, ptr(h.x), ptr(h.w), ptr(h.targets), of_lse,
+                                                     static_cast<const float*>(ptr(rest)), list, d, reduction, ptr(dx),
+                                                     ptr(dw), ptr(ws), need, stream);
     });
     return tuple_of({dx, dw});
   });

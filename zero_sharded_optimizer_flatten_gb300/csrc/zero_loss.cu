@@ -107,6 +107,7 @@ struct ProductArgs {
   float* target_z;       // base 2
   const float* lse2;
   const float* row_mul;
+  const float* rest;     // 1 - p of the targets, or null: from lse2
   void* dz;              // [terms][rows_cap][dz_stride]
   int64_t dz_stride;
   int32_t terms;
@@ -333,7 +334,7 @@ struct Epilogue {
   // maximum and sum of exponentials so far
   float top = -INFINITY, sum = 0.f;
   int target = -1;
-  float lse2 = 0.f, mul = 0.f;
+  float lse2 = 0.f, mul = 0.f, rest = 0.f;
   float alpha = 0.f;
   int64_t token = -1;
   bool direct = true;
@@ -351,6 +352,7 @@ struct Epilogue {
     }
     if constexpr (KIND == kProbs) {
       if (live) lse2 = a.lse2[row], mul = a.row_mul[row];
+      if (live && a.rest) rest = a.rest[row];
     }
     if constexpr (KIND == kDx) {
       direct = a.direct && a.pieces == 1 && t.splits == 1;
@@ -421,7 +423,7 @@ struct Epilogue {
       if (__any_sync(kFull, rel >= 0 && rel < 32)) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (rel == i) p[i] -= 1.f;
+          if (rel == i) p[i] = a.rest ? -rest : p[i] - 1.f;
       }
       if (row < n) {
 #pragma unroll
@@ -740,19 +742,18 @@ struct RowsArgs {
   int32_t* target;
   int32_t vec, log_lanes, narrow, pairs;
   // gradients
-  const float* lse;
+  const float *lse, *rest;
   const float* d;
   int32_t reduction;
   double scale;
   Scales* scales;
-  float *lse2, *row_mul;
+  float *lse2, *row_mul, *row_rest;
   void* dx;
-  int32_t dx_bytes;
   // losses
   const float2* part;
   const float* target_z;
   float* cta_sums;  // [CTAs of k_loss_finish]
-  float *losses, *lse_out, *total;
+  float *losses, *lse_out, *rest_out, *total;
 };
 
 __device__ __forceinline__ int load_target(const RowsArgs& a, int64_t t) {
@@ -981,13 +982,17 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
         a.lse2[i] = a.lse[t] * kLog2e;
         const float g = a.reduction == ZERO_LOSS_NONE ? a.d[t] : scales.g;
         a.row_mul[i] = target < 0 ? 0.f : g * scales.mul;
+        if (a.rest) a.row_rest[i] = a.rest[t];
       }
     }
   } else if (i < n || (BACKWARD && i < up(n, kTileK))) {
     for (int c = lane; c < words; c += lanes) to[c] = W();
     if (lane == 0 && i < n) {
       a.target[i] = -1;
-      if constexpr (BACKWARD) a.lse2[i] = 0.f, a.row_mul[i] = 0.f;
+      if constexpr (BACKWARD) {
+        a.lse2[i] = 0.f, a.row_mul[i] = 0.f;
+        if (a.rest) a.row_rest[i] = 0.f;
+      }
     }
   }
   if constexpr (BACKWARD) {
@@ -1050,13 +1055,18 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
       if (own < n && token >= 0) {
         // loss = log(1 + 2^d), d what the others' log2 of the sum is above the
         // target: differences first, so that small losses keep all their bits
-        const float rest = log2f(p.y), d = (p.x - target_z) + rest, less = log1pf(exp2f(-fabsf(d)));
+        const float log_sum = log2f(p.y), d = (p.x - target_z) + log_sum, e = exp2f(-fabsf(d)), less = log1pf(e);
         loss = target_z < INFINITY ? fmaf(fmaxf(d, 0.f), kLn2, less) : NAN;
-        a.lse_out[token] = fmaf(d > 0.f ? p.x + rest : target_z, kLn2, less);
+        a.lse_out[token] = fmaf(d > 0.f ? p.x + log_sum : target_z, kLn2, less);
         a.losses[token] = loss;
+        // the others' probability, 2^d / (1 + 2^d)
+        if (a.rest_out) a.rest_out[token] = target_z < INFINITY ? (d > 0.f ? 1.f : e) / (1.f + e) : NAN;
       }
       mine[r] = loss;
-      if (own < a.tokens && load_target(a, own) < 0) a.lse_out[own] = 0.f, a.losses[own] = 0.f;
+      if (own < a.tokens && load_target(a, own) < 0) {
+        a.lse_out[own] = 0.f, a.losses[own] = 0.f;
+        if (a.rest_out) a.rest_out[own] = 0.f;
+      }
     }
   }
   __syncthreads();
@@ -1188,7 +1198,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, 
 // Where a call's scratch lies.
 struct Layout {
   int64_t rows_cap, dz_rows, columns, pieces, xs_stride, w_stride, sums_stride;
-  int64_t xs, w, part, target_z, target, ticket, cta_sums, lse2, row_mul, scales, dz, sums, dw, bytes;
+  int64_t xs, w, part, target_z, target, ticket, cta_sums, lse2, row_mul, row_rest, scales, dz, sums, dw, bytes;
   int terms;   // of dz: 16 (bf16) or 22 (fp16) bits for a dw in binary32
   bool whole;  // rows of dx and dw are whole 16-byte words: the products write them
 
@@ -1219,6 +1229,7 @@ struct Layout {
     target_z = take(backward ? 0 : rows_cap * 4);
     lse2 = take(backward ? rows_cap * 4 : 0);
     row_mul = take(backward ? rows_cap * 4 : 0);
+    row_rest = take(backward ? rows_cap * 4 : 0);
     scales = take(sizeof(Scales));
     dz = take(backward ? dz_rows * columns * 2 : 0);
     // as many rows as there are tokens, or the parts of few
@@ -1450,26 +1461,9 @@ Extent by_rows(const char* name, const void* p, int64_t rows, int64_t stride, in
   return {name, p, rows, stride * 2, hidden * 2};
 }
 
-}  // namespace
-}  // namespace zero
-
-using namespace zero;
-
-extern "C" zero_status zero_linear_cross_entropy_workspace_bytes(const zero_linear_ce_desc* desc, const void* w,
-                                                                 int32_t backward, int64_t* bytes) {
-  const char* fn = "zero_linear_cross_entropy_workspace_bytes";
-  clear_error();
-  if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
-  LOSS_TRY(check_desc(fn, desc));
-  *bytes = Layout(*desc, wants_repack(*desc, w), backward != 0).bytes;
-  return ZERO_OK;
-}
-
-extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc, const void* x, const void* w,
-                                                 const void* targets, float* losses, float* lse, int32_t* rows,
-                                                 float* total, void* workspace, int64_t workspace_bytes,
-                                                 void* stream) {
-  const char* fn = "zero_linear_cross_entropy";
+zero_status forward(const char* fn, const zero_linear_ce_desc* desc, const void* x, const void* w, const void* targets,
+                    float* losses, float* lse, float* rest, bool with_rest, int32_t* rows, float* total,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
   clear_error();
   NvtxRange range(fn);
   LOSS_TRY(check_desc(fn, desc));
@@ -1480,6 +1474,7 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
   LOSS_TRY(check_ptr(fn, "targets", targets, d.id_bytes, any));
   LOSS_TRY(check_ptr(fn, "losses", losses, 4, any));
   LOSS_TRY(check_ptr(fn, "lse", lse, 4, any));
+  LOSS_TRY(check_ptr(fn, "rest", rest, 4, any && with_rest));
   LOSS_TRY(check_ptr(fn, "rows", rows, 4, true));
   LOSS_TRY(check_ptr(fn, "total", total, 4, true));
   LOSS_TRY(check_ptr(fn, "workspace", workspace, 256, true));
@@ -1489,7 +1484,7 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
                 at.bytes);
   LOSS_TRY(check_overlaps(fn,
                           {Extent::block("losses", losses, d.tokens * 4), Extent::block("lse", lse, d.tokens * 4),
-                           Extent::block("rows", rows, (d.tokens + 1) * 4), Extent::block("total", total, 12),
+                           Extent::block("rest", rest, d.tokens * 4), Extent::block("rows", rows, (d.tokens + 1) * 4), Extent::block("total", total, 12),
                            Extent::block("workspace", workspace, at.bytes)},
                           {by_rows("x", x, d.tokens, d.x_stride, d.hidden), by_rows("w", w, d.vocab, d.w_stride, d.hidden),
                            Extent::block("targets", targets, d.tokens * d.id_bytes)}));
@@ -1511,18 +1506,17 @@ extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc
                                          : launch_product<kStats>(c.product, c.s));
   c.rows.narrow = c.product.narrow, c.rows.pairs = c.product.pairs;
   c.rows.part = c.product.part, c.rows.target_z = c.product.target_z;
-  c.rows.cta_sums = c.in<float>(at.cta_sums), c.rows.losses = losses, c.rows.lse_out = lse, c.rows.total = total;
+  c.rows.cta_sums = c.in<float>(at.cta_sums), c.rows.losses = losses, c.rows.lse_out = lse;
+  c.rows.rest_out = rest, c.rows.total = total;
   LOSS_CUDA(launch(&k_loss_finish, std::max<int64_t>(1, over(d.tokens, kFinishRows)), kFinishThreads, 0, true, c.s,
                    static_cast<const RowsArgs>(c.rows)));
   return ZERO_OK;
 }
 
-extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, const void* x,
-                                                          const void* w, const void* targets, const float* lse,
-                                                          const int32_t* rows, const float* d_loss, int32_t reduction,
-                                                          void* dx, void* dw, void* workspace,
-                                                          int64_t workspace_bytes, void* stream) {
-  const char* fn = "zero_linear_cross_entropy_backward";
+zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void* x, const void* w,
+                     const void* targets, const float* lse, const float* rest, bool with_rest, const int32_t* rows,
+                     const float* d_loss, int32_t reduction, void* dx, void* dw, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
   clear_error();
   NvtxRange range(fn);
   LOSS_TRY(check_desc(fn, desc));
@@ -1535,6 +1529,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   LOSS_TRY(check_ptr(fn, "w", w, 2, true));
   LOSS_TRY(check_ptr(fn, "targets", targets, d.id_bytes, any));
   LOSS_TRY(check_ptr(fn, "lse", lse, 4, any));
+  LOSS_TRY(check_ptr(fn, "rest", rest, 4, any && with_rest));
   LOSS_TRY(check_ptr(fn, "rows", rows, 4, true));
   LOSS_TRY(check_ptr(fn, "d_loss", d_loss, 4, any || reduction != ZERO_LOSS_NONE));
   LOSS_TRY(check_ptr(fn, "dx", dx, 2, false));
@@ -1552,7 +1547,8 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
                            Extent::block("workspace", workspace, at.bytes)},
                           {by_rows("x", x, d.tokens, d.x_stride, d.hidden), by_rows("w", w, d.vocab, d.w_stride, d.hidden),
                            Extent::block("targets", targets, d.tokens * d.id_bytes),
-                           Extent::block("lse", lse, d.tokens * 4), Extent::block("rows", rows, (d.tokens + 1) * 4),
+                           Extent::block("lse", lse, d.tokens * 4), Extent::block("rest", rest, d.tokens * 4),
+                           Extent::block("rows", rows, (d.tokens + 1) * 4),
                            Extent::block("d_loss", d_loss, reduction == ZERO_LOSS_NONE ? d.tokens * 4 : 4)}));
   int32_t* err = nullptr;
   LOSS_TRY(ready(fn, &err));
@@ -1560,7 +1556,7 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   LOSS_TRY(c.begin(fn, x, targets, const_cast<int32_t*>(rows), err));
   c.rows.lse = lse, c.rows.d = d_loss, c.rows.reduction = reduction, c.rows.scale = d.scale;
   c.rows.scales = c.in<Scales>(at.scales), c.rows.lse2 = c.in<float>(at.lse2), c.rows.row_mul = c.in<float>(at.row_mul);
-  c.rows.dx = dx;
+  c.rows.rest = rest, c.rows.row_rest = c.in<float>(at.row_rest), c.rows.dx = dx;
   c.set_vec(c.rows.vec && aligned_to(dx, 16));
   const bool own_gradients = reduction == ZERO_LOSS_NONE;
   if (own_gradients)
@@ -1569,7 +1565,8 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
   CopyArgs copy = {};  // of dw, after a piece's products
   if (!c.maps_of_z(std::min(at.columns, d.vocab))) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   ProductArgs z = c.product;
-  z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.dz = c.in<void>(at.dz), z.dz_stride = at.columns;
+  z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.rest = rest ? c.rows.row_rest : nullptr;
+  z.dz = c.in<void>(at.dz), z.dz_stride = at.columns;
   z.terms = dw ? at.terms : 1;
   for (int64_t first = 0; first < d.vocab; first += at.columns) {
     const int64_t columns = std::min(at.columns, d.vocab - first);
@@ -1609,4 +1606,54 @@ extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_d
                      kGatherThreads, 0, true, c.s, static_cast<const JoinArgs>(j), static_cast<const CopyArgs>(copy)));
   }
   return ZERO_OK;
+}
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" zero_status zero_linear_cross_entropy_workspace_bytes(const zero_linear_ce_desc* desc, const void* w,
+                                                                 int32_t backward, int64_t* bytes) {
+  const char* fn = "zero_linear_cross_entropy_workspace_bytes";
+  clear_error();
+  if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
+  LOSS_TRY(check_desc(fn, desc));
+  *bytes = Layout(*desc, wants_repack(*desc, w), backward != 0).bytes;
+  return ZERO_OK;
+}
+
+extern "C" zero_status zero_linear_cross_entropy(const zero_linear_ce_desc* desc, const void* x, const void* w,
+                                                 const void* targets, float* losses, float* lse, int32_t* rows,
+                                                 float* total, void* workspace, int64_t workspace_bytes,
+                                                 void* stream) {
+  return forward("zero_linear_cross_entropy", desc, x, w, targets, losses, lse, nullptr, false, rows, total, workspace,
+                 workspace_bytes, stream);
+}
+
+extern "C" zero_status zero_linear_cross_entropy_rest(const zero_linear_ce_desc* desc, const void* x, const void* w,
+                                                      const void* targets, float* losses, float* lse, float* rest,
+                                                      int32_t* rows, float* total, void* workspace,
+                                                      int64_t workspace_bytes, void* stream) {
+  return forward("zero_linear_cross_entropy_rest", desc, x, w, targets, losses, lse, rest, true, rows, total, workspace,
+                 workspace_bytes, stream);
+}
+
+extern "C" zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, const void* x,
+                                                          const void* w, const void* targets, const float* lse,
+                                                          const int32_t* rows, const float* d_loss, int32_t reduction,
+                                                          void* dx, void* dw, void* workspace,
+                                                          int64_t workspace_bytes, void* stream) {
+  return backward("zero_linear_cross_entropy_backward", desc, x, w, targets, lse, nullptr, false, rows, d_loss,
+                  reduction, dx, dw, workspace, workspace_bytes, stream);
+}
+
+extern "C" zero_status zero_linear_cross_entropy_rest_backward(const zero_linear_ce_desc* desc, const void* x,
+                                                               const void* w, const void* targets, const float* lse,
+                                                               const float* rest, const int32_t* rows,
+                                                               const float* d_loss, int32_t reduction, void* dx,
+                                                               void* dw, void* workspace, int64_t workspace_bytes,
+                                                               void* stream) {
+  return backward("zero_linear_cross_entropy_rest_backward", desc, x, w, targets, lse, rest, true, rows, d_loss,
+                  reduction, dx, dw, workspace, workspace_bytes, stream);
 }

@@ -701,11 +701,14 @@ _REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 class CrossEntropy:
     """What zero_linear_cross_entropy leaves on the device: losses and lse of
     the targets' shape (0 where a token is left out), total [3] (mean, sum and
-    number of the losses), all float32; rows, which the backward call takes."""
+    number of the losses), all float32; rows and rest (1 - p of the targets),
+    which the backward call takes.  Without rest it forms 1 - p from lse, of
+    which little is left where p is near 1."""
     losses: torch.Tensor
     lse: torch.Tensor
     total: torch.Tensor
     rows: torch.Tensor
+    rest: torch.Tensor | None = None
 
 
 def zero_linear_cross_entropy_workspace_bytes(x, w, targets, *, scale: float = 1.0,
@@ -742,7 +745,12 @@ def zero_linear_cross_entropy_backward(x, w, targets, ce: CrossEntropy, d_loss, 
     code = _code(dw_dtype, "dw_dtype")
     return _run_on(stream, lambda: (_fast or _load_fast()).linear_cross_entropy_backward(
         x, w, targets, scale, ce.lse, ce.rows, d_loss, kind, "dx" in want, "dw" in want, dx, dw,
-        code, workspace))
+        code, workspace, ce.rest))
+
+
+# These make and take `rest`.
+zero_linear_cross_entropy_rest = zero_linear_cross_entropy
+zero_linear_cross_entropy_rest_backward = zero_linear_cross_entropy_backward
 
 
 class _LinearCrossEntropy(torch.autograd.Function):
@@ -750,7 +758,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
     def forward(ctx, x, w, targets, scale, reduction):
         ce = zero_linear_cross_entropy(x, w, targets, scale=scale)
         ctx.how = dict(scale=scale, reduction=reduction)
-        ctx.save_for_backward(x, w, targets, ce.lse, ce.rows)
+        ctx.save_for_backward(x, w, targets, ce.lse, ce.rows, ce.rest)
         if reduction == "none":
             return ce.losses
         return ce.total[1 if reduction == "sum" else 0]
@@ -758,9 +766,9 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d):
-        x, w, targets, lse, rows = ctx.saved_tensors
+        x, w, targets, lse, rows, rest = ctx.saved_tensors
         want = [k for k, needed in zip(("dx", "dw"), ctx.needs_input_grad) if needed]
-        dx, dw = zero_linear_cross_entropy_backward(x, w, targets, CrossEntropy(None, lse, None, rows),
+        dx, dw = zero_linear_cross_entropy_backward(x, w, targets, CrossEntropy(None, lse, None, rows, rest),
                                                     d.contiguous(), want=want, **ctx.how)
         return dx, dw, None, None, None
 

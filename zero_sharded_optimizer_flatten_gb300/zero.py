@@ -141,6 +141,9 @@ def lib():
                 "zero_linear_cross_entropy": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp],
                 "zero_linear_cross_entropy_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp,
                                                        i64, vp],
+                "zero_linear_cross_entropy_rest": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp],
+                "zero_linear_cross_entropy_rest_backward": [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp,
+                                                            vp, vp, i64, vp],
                 "zero_zero3_pass": [vp, ctypes.POINTER(_LayerC), i32, vpp, i32, ctypes.c_int,
                                     ctypes.c_int, hp, i64, vp, vp],
             }
