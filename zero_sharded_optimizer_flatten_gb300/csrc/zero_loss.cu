@@ -26,6 +26,7 @@
 #include <inttypes.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "zero_capi_util.h"
@@ -822,13 +823,12 @@ __global__ void __launch_bounds__(kScanThreads) k_loss_rows(const RowsArgs a) {
 }
 
 // What the gradients are scaled with: every row's g times a power of two that
-// brings the largest (`top`) to [2^13, 2^14), so that neither rounding to 16 bits
-// nor fp16's range costs small probabilities.
+// brings the largest finite one (`top`) to [2^13, 2^14), so that neither rounding
+// to 16 bits nor fp16's range costs small probabilities. A row whose g is infinite
+// or NaN stays that, whatever it is scaled with.
 __device__ __forceinline__ Scales scales_for(float top, float g, double scale) {
   int e = 14;
-  if (!(top <= 3.4e38f))
-    e = 127;  // infinite or NaN: the results are, too
-  else if (top > 0.f)
+  if (top > 0.f && top <= FLT_MAX)
     frexpf(top, &e);
   e = max(e, -100);
   return {ldexpf(1.f, 14 - e), static_cast<float>(ldexp(scale, e - 14)), g};
@@ -846,7 +846,8 @@ __global__ void __launch_bounds__(kScanThreads) k_loss_scales(const RowsArgs a) 
   float top = 0.f;
   for (int i = threadIdx.x; i < n; i += kScanThreads) {
     const int t = a.rows[i];
-    if (t >= 0 && t < a.tokens) top = fmaxf(top, fabsf(a.d[t]));
+    const float g = t >= 0 && t < a.tokens ? fabsf(a.d[t]) : 0.f;
+    if (g <= FLT_MAX) top = fmaxf(top, g);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
