@@ -867,10 +867,13 @@ zero_status zero_linear_cross_entropy_rest(const zero_linear_ce_desc* desc, cons
  * read.  d_loss (device): of ZERO_LOSS_NONE float[tokens], the gradients of the
  * losses; else one float, of their sum or of their mean (total[1], total[0]).
  * The logits are formed again, a piece of the vocabulary at a time; their
- * gradient is rounded to dtype (scaled by a power of two that keeps it in
- * range) between its two products, for a dw in binary32 to two numbers of dtype
- * that hold 16 or 22 bits of it, which doubles dw's product.  dx and dw are
- * rounded once. */
+ * gradient is rounded to dtype between its two products, scaled by the power of
+ * two that brings the largest finite |d_loss| to [2^13, 2^14) (for dx in fp16
+ * every token's own, once they lie 2^16 apart); for a dw in binary32 it is rounded
+ * to two numbers of dtype that hold 16 or 22 bits of it, which doubles dw's
+ * product.  So to an fp16 call's dw a token adds nothing where its |d_loss| p is
+ * below 2^-39 of the largest |d_loss|, and of less than 11 bits where it is below
+ * 2^-27.  dx and dw are rounded once. */
 zero_status zero_linear_cross_entropy_backward(const zero_linear_ce_desc* desc, const void* x,
                                                const void* w, const void* targets, const float* lse,
                                                const int32_t* rows, const float* d_loss,

@@ -16,7 +16,9 @@
 //           (kStatsLong: for a long depth, summed in several accumulators)
 //   kProbs  tiles of z again, to dz in 16 bits, a piece of the vocabulary at a
 //           time (kPieceBytes); for dw in binary32 to two 16-bit numbers
-//           ("terms"), the second what the first one's rounding lost
+//           ("terms"), the second what the first one's rounding lost; of fp16
+//           tokens with gradients of their own once more for dx, every row with
+//           a scale of its own
 //   kGrads  dz w, summed over the pieces in binary32 (kDx), and dz^T x, the
 //           piece's rows of dw (kDw), whose tiles fill each other's last round
 // The second forming of z is a quarter of the operations: the price of keeping
@@ -74,6 +76,7 @@ struct Scales {
   float mul;    // of dz before it is rounded, a power of two: largest |dz| below 2^14
   float alpha;  // of the products, scale / mul
   float g;      // d_loss as one number (sum, mean)
+  int32_t own;  // rows of fp16 have a scale each for dx (see own_scales)
 };
 
 // The kept rows, however the caller's list was treated since.
@@ -108,12 +111,14 @@ struct ProductArgs {
   float* target_z;       // base 2
   const float* lse2;
   const float* row_mul;
+  const float* row_own;  // or null: dz once more, times this, behind the terms (if scales say so)
   const float* rest;     // 1 - p of the targets, or null: from lse2
-  void* dz;              // [terms][rows_cap][dz_stride]
+  void* dz;              // [terms (+ 1)][rows_cap][dz_stride]
   int64_t dz_stride;
   int32_t terms;
   // kDx, kDw
   const Scales* scales;
+  const float* row_alpha;  // kDx: the rows', or null: scales'
   const int32_t* rows;   // kept row -> token
   int64_t tokens;
   Out dx, dw;  // p null: not wanted
@@ -335,10 +340,10 @@ struct Epilogue {
   // maximum and sum of exponentials so far
   float top = -INFINITY, sum = 0.f;
   int target = -1;
-  float lse2 = 0.f, mul = 0.f, rest = 0.f;
+  float lse2 = 0.f, mul = 0.f, own = 0.f, rest = 0.f;
   float alpha = 0.f;
   int64_t token = -1;
-  bool direct = true;
+  bool direct = true, twice = false;
   int64_t sums_rows = 0;
 
   __device__ __forceinline__ Epilogue(const ProductArgs& a_, int n_, const Tiles<KIND>& t, int m, int nt, int split_,
@@ -354,13 +359,15 @@ struct Epilogue {
     if constexpr (KIND == kProbs) {
       if (live) lse2 = a.lse2[row], mul = a.row_mul[row];
       if (live && a.rest) rest = a.rest[row];
+      twice = a.row_own && a.scales->own;
+      if (live && twice) own = a.row_own[row];
     }
     if constexpr (KIND == kDx) {
       direct = a.direct && a.pieces == 1 && t.splits == 1;
       sums_rows = up(n, kTileM);
       if (live) token = a.rows[row];
       if (token >= a.tokens) token = -1;  // negative ones are not written either
-      alpha = a.scales->alpha;
+      alpha = !a.row_alpha ? a.scales->alpha : live ? a.row_alpha[row] : 0.f;
     }
     if constexpr (KIND == kDw) {
       if (live) token = a.dw.first + row;
@@ -426,13 +433,18 @@ struct Epilogue {
         for (int i = 0; i < 32; ++i)
           if (rel == i) p[i] = a.rest ? -rest : p[i] - 1.f;
       }
-      if (row < n) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) p[i] *= mul;
-      } else {
+      if (row >= n) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) p[i] = 0.f;
       }
+      if (twice) {  // fp16
+        float q[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) q[i] = p[i] * own;
+        store32(static_cast<__half*>(a.dz) + (a.terms * a.rows_cap + row) * a.dz_stride + c, q, 32, 32);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) p[i] *= mul;
       if (a.bf16)
         store_dz(static_cast<__nv_bfloat16*>(a.dz) + row * a.dz_stride + c, p);
       else
@@ -573,6 +585,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp == 0 && lane == 0) {
+    // dx's rows of dz
+    [[maybe_unused]] const int own_rows =
+        is_grads(KIND) && a.row_own && a.scales->own ? a.terms * static_cast<int>(a.rows_cap) : 0;
     Ring<kStages> ring;
     int64_t issued = 0;
     while (ok && todo.next(t)) {
@@ -600,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           depth += kTileK;
           if (depth == depth_end) depth = 0, term += static_cast<int>(a.rows_cap);
         } else if (is_grads(KIND)) {
-          tc::load_box(to_a, &a.a, k * kTileK, row, bar);
+          tc::load_box(to_a, &a.a, k * kTileK, own_rows + row, bar);
           tc::load_box(to_b, &a.b, col, a.first + k * kTileK, bar);
           tc::load_box(to_b + kOperandBytes / 2, &a.b, col + 64, a.first + k * kTileK, bar);
         } else {
@@ -749,6 +764,7 @@ struct RowsArgs {
   double scale;
   Scales* scales;
   float *lse2, *row_mul, *row_rest;
+  float *row_own, *row_alpha;  // or null: see own_scales
   void* dx;
   // losses
   const float2* part;
@@ -831,7 +847,7 @@ __device__ __forceinline__ Scales scales_for(float top, float g, double scale) {
   if (top > 0.f && top <= FLT_MAX)
     frexpf(top, &e);
   e = max(e, -100);
-  return {ldexpf(1.f, 14 - e), static_cast<float>(ldexp(scale, e - 14)), g};
+  return {ldexpf(1.f, 14 - e), static_cast<float>(ldexp(scale, e - 14)), g, 0};
 }
 // The one of a sum or a mean; of the tokens' own gradients it takes a pass.
 __device__ __forceinline__ Scales scales_of_one(const RowsArgs& a, int n) {
@@ -840,23 +856,30 @@ __device__ __forceinline__ Scales scales_of_one(const RowsArgs& a, int n) {
   return scales_for(fabsf(g), g, a.scale);
 }
 __global__ void __launch_bounds__(kScanThreads) k_loss_scales(const RowsArgs a) {
-  __shared__ float most[32];
+  __shared__ float most[32], fewest[32];
   let_next_start();
   const int n = kept_rows(a.rows + a.tokens, a.tokens);
-  float top = 0.f;
+  float top = 0.f, low = FLT_MAX;
   for (int i = threadIdx.x; i < n; i += kScanThreads) {
     const int t = a.rows[i];
     const float g = t >= 0 && t < a.tokens ? fabsf(a.d[t]) : 0.f;
-    if (g <= FLT_MAX) top = fmaxf(top, g);
+    if (g > 0.f && g <= FLT_MAX) top = fmaxf(top, g), low = fminf(low, g);
   }
+  auto join = [&] {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = top;
+    for (int o = 16; o > 0; o >>= 1)
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, o)), low = fminf(low, __shfl_xor_sync(kFull, low, o));
+  };
+  join();
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = top, fewest[threadIdx.x >> 5] = low;
   __syncthreads();
-  top = most[threadIdx.x & 31];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  if (threadIdx.x == 0) *a.scales = scales_for(top, 0.f, a.scale);
+  top = most[threadIdx.x & 31], low = fewest[threadIdx.x & 31];
+  join();
+  if (threadIdx.x == 0) {
+    Scales s = scales_for(top, 0.f, a.scale);
+    s.own = a.row_alpha && low * 65536.f < top;
+    *a.scales = s;
+  }
 }
 
 // Rows to another stride: w to one that the bulk copies can take, dw back from
@@ -984,6 +1007,11 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
         const float g = a.reduction == ZERO_LOSS_NONE ? a.d[t] : scales.g;
         a.row_mul[i] = target < 0 ? 0.f : g * scales.mul;
         if (a.rest) a.row_rest[i] = a.rest[t];
+        if (a.row_alpha) {
+          const Scales own = scales.own ? scales_for(fabsf(g), g, a.scale) : scales;
+          (a.row_own ? a.row_own : a.row_mul)[i] = target < 0 ? 0.f : g * own.mul;
+          a.row_alpha[i] = own.alpha;
+        }
       }
     }
   } else if (i < n || (BACKWARD && i < up(n, kTileK))) {
@@ -993,6 +1021,8 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
       if constexpr (BACKWARD) {
         a.lse2[i] = 0.f, a.row_mul[i] = 0.f;
         if (a.rest) a.row_rest[i] = 0.f;
+        if (a.row_own) a.row_own[i] = 0.f;
+        if (a.row_alpha) a.row_alpha[i] = 0.f;
       }
     }
   }
@@ -1135,6 +1165,7 @@ struct JoinArgs {
   const float* sums;
   int64_t sums_stride;
   const Scales* scales;
+  const float* row_alpha;
   void* dx;
   int32_t hidden, piece, pieces, pairs, direct, log_lanes, vec;
 };
@@ -1153,7 +1184,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, 
   if (i >= n) return;
   const int64_t t = a.rows[i];
   if (t < 0 || t >= a.tokens) return;
-  const float alpha = a.scales->alpha;
+  const float alpha = a.row_alpha ? a.row_alpha[i] : a.scales->alpha;
   const int64_t part = up(n, kTileM) * a.sums_stride;
   const float* from = a.sums + i * a.sums_stride;
   T* to = static_cast<T*>(a.dx) + t * a.hidden;
@@ -1196,20 +1227,32 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, 
 // ---------------------------------------------------------------------------
 // host
 
-// Where a call's scratch lies.
+// Tokens with gradients of their own in fp16: one scale for all would round the
+// rows of dx whose gradients lie far below the largest to few bits or none, so
+// they get one each once the smallest is below 2^-16 of the largest. (Up to there
+// probabilities above 2^-10 keep all their bits and none is off by more than 2^-22,
+// which sums over 131072 columns to less than dx's own rounding, 2^-12.) dw's sums
+// mix the rows, so it keeps dz with the one scale, and dz is written twice: 168 us
+// in place of 150 at 1024 x 1024 x 32000. (bf16 has binary32's exponents.)
+bool own_scales(const zero_linear_ce_desc& d, int reduction, const void* dx) {
+  return d.dtype == ZERO_FP16 && reduction == ZERO_LOSS_NONE && dx;
+}
+
+// Where a call's scratch lies. both: room for dx's dz apart from dw's.
 struct Layout {
-  int64_t rows_cap, dz_rows, columns, pieces, xs_stride, w_stride, sums_stride;
-  int64_t xs, w, part, target_z, target, ticket, cta_sums, lse2, row_mul, row_rest, scales, dz, sums, dw, bytes;
+  int64_t rows_cap, dz_rows, all_rows, columns, pieces, xs_stride, w_stride, sums_stride;
+  int64_t xs, w, part, target_z, target, ticket, cta_sums, lse2, row_mul, row_rest, row_own, row_alpha, scales, dz, sums, dw, bytes;
   int terms;   // of dz: 16 (bf16) or 22 (fp16) bits for a dw in binary32
   bool whole;  // rows of dx and dw are whole 16-byte words: the products write them
 
-  Layout(const zero_linear_ce_desc& d, bool repack, bool backward) {
+  Layout(const zero_linear_ce_desc& d, bool repack, bool backward, bool both = false) {
     rows_cap = up(std::max<int64_t>(d.tokens, 1), kTileM);
     whole = d.hidden % 8 == 0;
     columns = up(d.vocab, kTileN);
     terms = d.dw_dtype == ZERO_FP32 ? 2 : 1;
     dz_rows = rows_cap * terms;
-    if (backward) columns = std::min(columns, std::max<int64_t>(kTileN, kPieceBytes / 2 / dz_rows / kTileN * kTileN));
+    all_rows = dz_rows + (both ? rows_cap : 0);
+    if (backward) columns = std::min(columns, std::max<int64_t>(kTileN, kPieceBytes / 2 / all_rows / kTileN * kTileN));
     pieces = over(d.vocab, columns);
     xs_stride = up(d.hidden, 8);
     w_stride = repack ? up(d.hidden, 8) : d.w_stride;
@@ -1231,8 +1274,10 @@ struct Layout {
     lse2 = take(backward ? rows_cap * 4 : 0);
     row_mul = take(backward ? rows_cap * 4 : 0);
     row_rest = take(backward ? rows_cap * 4 : 0);
+    row_own = take(backward && d.dtype == ZERO_FP16 ? rows_cap * 4 : 0);
+    row_alpha = take(backward && d.dtype == ZERO_FP16 ? rows_cap * 4 : 0);
     scales = take(sizeof(Scales));
-    dz = take(backward ? dz_rows * columns * 2 : 0);
+    dz = take(backward ? all_rows * columns * 2 : 0);
     // as many rows as there are tokens, or the parts of few
     const int64_t split_rows = static_cast<int64_t>(kPairsMost) * kTileM;
     sums = take(backward ? (pieces > 1 || !whole ? std::max(split_rows, rows_cap) : split_rows) * sums_stride * 4 : 0);
@@ -1243,6 +1288,13 @@ struct Layout {
 
 bool wants_repack(const zero_linear_ce_desc& d, const void* w) {
   return d.w_stride % 8 != 0 || !aligned_to(w, 16);
+}
+
+// Of any reduction.
+int64_t workspace_of(const zero_linear_ce_desc& d, const void* w, bool backward) {
+  const bool repack = wants_repack(d, w);
+  const int64_t bytes = Layout(d, repack, backward).bytes;
+  return backward && d.dtype == ZERO_FP16 ? std::max(bytes, Layout(d, repack, true, true).bytes) : bytes;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1538,14 +1590,15 @@ zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void
   LOSS_TRY(check_ptr(fn, "workspace", workspace, 256, true));
   if (!any) dx = nullptr;
   if (!dx && !dw) return ZERO_OK;
-  const Layout at(d, wants_repack(d, w), true);
-  if (workspace_bytes < at.bytes)
-    return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes,
-                at.bytes);
+  const bool own = own_scales(d, reduction, dx);
+  const Layout at(d, wants_repack(d, w), true, own && dw);
+  const int64_t need = workspace_of(d, w, true);
+  if (workspace_bytes < need)
+    return fail(ZERO_ERR_INVALID, "%s: workspace holds %" PRId64 " bytes, needs %" PRId64, fn, workspace_bytes, need);
   LOSS_TRY(check_overlaps(fn,
                           {Extent::block("dx", dx, d.tokens * d.hidden * 2),
                            Extent::block("dw", dw, d.vocab * d.hidden * type_bytes(dw_dtype)),
-                           Extent::block("workspace", workspace, at.bytes)},
+                           Extent::block("workspace", workspace, need)},
                           {by_rows("x", x, d.tokens, d.x_stride, d.hidden), by_rows("w", w, d.vocab, d.w_stride, d.hidden),
                            Extent::block("targets", targets, d.tokens * d.id_bytes),
                            Extent::block("lse", lse, d.tokens * 4), Extent::block("rest", rest, d.tokens * 4),
@@ -1558,6 +1611,7 @@ zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void
   c.rows.lse = lse, c.rows.d = d_loss, c.rows.reduction = reduction, c.rows.scale = d.scale;
   c.rows.scales = c.in<Scales>(at.scales), c.rows.lse2 = c.in<float>(at.lse2), c.rows.row_mul = c.in<float>(at.row_mul);
   c.rows.rest = rest, c.rows.row_rest = c.in<float>(at.row_rest), c.rows.dx = dx;
+  if (own) c.rows.row_alpha = c.in<float>(at.row_alpha), c.rows.row_own = dw ? c.in<float>(at.row_own) : nullptr;
   c.set_vec(c.rows.vec && aligned_to(dx, 16));
   const bool own_gradients = reduction == ZERO_LOSS_NONE;
   if (own_gradients)
@@ -1566,7 +1620,8 @@ zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void
   CopyArgs copy = {};  // of dw, after a piece's products
   if (!c.maps_of_z(std::min(at.columns, d.vocab))) return fail(ZERO_ERR_CUDA, "%s: the tensor maps could not be made", fn);
   ProductArgs z = c.product;
-  z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.rest = rest ? c.rows.row_rest : nullptr;
+  z.lse2 = c.rows.lse2, z.row_mul = c.rows.row_mul, z.row_own = c.rows.row_own, z.row_alpha = c.rows.row_alpha;
+  z.scales = c.rows.scales, z.rest = rest ? c.rows.row_rest : nullptr;
   z.dz = c.in<void>(at.dz), z.dz_stride = at.columns;
   z.terms = dw ? at.terms : 1;
   for (int64_t first = 0; first < d.vocab; first += at.columns) {
@@ -1574,7 +1629,6 @@ zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void
     z.first = static_cast<int32_t>(first), z.columns = static_cast<int32_t>(columns);
     LOSS_CUDA(launch_product<kProbs>(z, c.s));
     ProductArgs p = z;
-    p.scales = c.rows.scales;
     p.sums = c.in<float>(at.sums), p.sums_stride = at.sums_stride, p.add = first > 0, p.direct = at.whole;
     p.dx = {dx, d.hidden, 0, d.dtype, align_of(dx, d.hidden * 2)};
     // rows that start anywhere are written to a padded copy first: single columns
@@ -1583,7 +1637,7 @@ zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void
       p.dw = {dw, d.hidden, first, dw_dtype, align_of(dw, d.hidden * type_bytes(dw_dtype))};
     else if (dw)
       p.dw = {c.in<void>(at.dw), at.sums_stride, 0, dw_dtype, align_of(c.in<void>(at.dw), at.sums_stride * type_bytes(dw_dtype))};
-    if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.rows_cap, at.columns, kHalfRows) ||
+    if (!matrix_map(&p.a, z.dz, c.bf16, columns, at.all_rows, at.columns, kHalfRows) ||
         !matrix_map(&p.b, c.w, c.bf16, d.hidden, d.vocab, at.w_stride, kTileK) ||
         !matrix_map(&p.a2, z.dz, c.bf16, columns, at.dz_rows, at.columns, kTileK) ||
         !matrix_map(&p.b2, c.in<void>(at.xs), c.bf16, d.hidden, at.rows_cap, at.xs_stride, kTileK))
@@ -1599,7 +1653,7 @@ zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void
   if (dx) {
     JoinArgs j = {};
     j.rows = rows, j.tokens = d.tokens, j.sums = c.in<float>(at.sums), j.sums_stride = at.sums_stride;
-    j.scales = c.rows.scales, j.dx = dx;
+    j.scales = c.rows.scales, j.row_alpha = c.rows.row_alpha, j.dx = dx;
     j.hidden = static_cast<int32_t>(d.hidden), j.piece = c.product.piece, j.pieces = c.product.pieces;
     j.pairs = c.product.pairs, j.direct = at.whole, j.vec = at.whole && aligned_to(dx, 16);
     j.log_lanes = lanes_for(d.hidden, 8);
@@ -1620,7 +1674,7 @@ extern "C" zero_status zero_linear_cross_entropy_workspace_bytes(const zero_line
   clear_error();
   if (!bytes) return fail(ZERO_ERR_INVALID, "%s: bytes is NULL", fn);
   LOSS_TRY(check_desc(fn, desc));
-  *bytes = Layout(*desc, wants_repack(*desc, w), backward != 0).bytes;
+  *bytes = workspace_of(*desc, w, backward != 0);
   return ZERO_OK;
 }
 
