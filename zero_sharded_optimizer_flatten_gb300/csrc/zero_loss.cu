@@ -32,6 +32,7 @@
 #include <cmath>
 
 #include "zero_capi_util.h"
+#include "zero_drain.h"
 #include "zero_internal.h"
 #include "zero_rows.cuh"
 #include "zero_tensor_core.cuh"
@@ -542,13 +543,15 @@ struct Epilogue {
 // its half of the operands' blocks into a ring of kStages, one thread of the
 // leading CTA issues the products of both, and eight warps of each CTA work on
 // its half of a finished tile in tensor memory while the next one is formed in
-// the other accumulator.
+// the other accumulator. Where a wait gives up, the products issued so far and the
+// copies in flight are waited for before the pair leaves its memory.
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_loss_product(const __grid_constant__ ProductArgs a) {
   extern __shared__ char raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kAccumulators + 1];
-  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t tmem_slot, stopped;     // stopped: a wait of the pair gave up
+  __shared__ __align__(8) uint64_t issued_by[2];  // in the leading CTA: copies of each
   const uint32_t base = (tc::smem_of(raw) + 1023) & ~1023u;
   const uint32_t bar0 = tc::smem_of(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
@@ -569,6 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kAccumulators; ++s) tc::bar_init(acc_full(s), 1), tc::bar_init(acc_empty(s), 2 * kEpilogueWarps);
     tc::bar_init(drained, 1);
     tc::bar_init_fence();
+    stopped = 0;
   }
   if (warp == 1) tc::tmem_alloc(tc::smem_of(&tmem_slot), kAccumulators * kTileN);
   tc::fence_before();
@@ -583,13 +587,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Tile t;
   constexpr int kLong = KIND == kGradsLong ? kSegmentDw : kSegment;
   bool ok = true;
+  auto give_up = [&] {
+    atomicExch(a.err, 1);
+    for (uint32_t r = 0; r < 2; ++r) tc::store_cluster(tc::in_cta(tc::smem_of(&stopped), r), 1u);
+  };
 
   if (warp == 0 && lane == 0) {
     // dx's rows of dz
     [[maybe_unused]] const int own_rows =
         is_grads(KIND) && a.row_own && a.scales->own ? a.terms * static_cast<int>(a.rows_cap) : 0;
     Ring<kStages> ring;
-    int64_t issued = 0;
+    uint64_t issued = 0;
     while (ok && todo.next(t)) {
       const bool whole = todo.columns() == kTileN;
       // of dw: the depth once for each term of dz, with x again
@@ -630,13 +638,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ring.next();
       }
     }
-    if (!ok) {
-      // given up: wait for the copies of both CTAs before the memory goes
-      atomicExch(a.err, 1);
-      if (rank == 0)
-        for (int64_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
-          tc::bar_wait(full(static_cast<int>(j % kStages)), static_cast<uint32_t>(j / kStages) & 1);
-    }
+    tc::store_cluster(tc::in_cta(tc::smem_of(&issued_by[rank]), 0), issued);
+    if (!ok) give_up();
   } else if (warp == 1 && lane == 0 && rank == 0) {
     constexpr uint32_t kLead = kOperandBytes / 2;
     constexpr bool kBByN = is_grads(KIND);
@@ -681,11 +684,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::commit(acc_full(acc.slot));
       acc.next();
     }
-    if (!ok) {
-      atomicExch(a.err, 1);
-      tc::commit(drained);
-      tc::bar_wait(drained, 0);
-    }
+    // the last products: an epilogue that gives up does not wait for them
+    tc::commit_here(drained);
+    ok = tc::bar_wait(drained, 0) && ok;
+    if (!ok) give_up();
   } else if (warp >= 2) {
     Ring<kAccumulators> acc;
     const int quarter = warp & 3;  // the rows of tensor memory that this warp may read
@@ -732,12 +734,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         work(e);
       }
     }
-    if (!ok && lane == 0) atomicExch(a.err, 1);
+    if (!ok && lane == 0) give_up();
   }
   __syncwarp();
   tc::fence_before();
   __syncthreads();
   tc::cluster_sync();  // no CTA leaves while the other may still write to it
+  if (stopped) {       // the same in both
+    if (rank == 0 && threadIdx.x == 0) {
+      const int half = todo.columns() / 2, rows_b = is_grads(KIND) || a.rows_a == kHalfRows ? kHalfRows : 0;
+      const uint32_t others = static_cast<uint32_t>(rows_b + half) * (kTileK * 2);  // bytes of the other CTA's copies
+      const Drain d(static_cast<int64_t>(issued_by[0]), static_cast<int64_t>(issued_by[1]), kStages);
+      for (int64_t j = d.first; j < d.last; ++j) {
+        const uint32_t bar = full(static_cast<int>(j % kStages));
+        if (d.announce(j))
+          tc::bar_expect(bar, others);
+        else if (d.forgo(j))
+          tc::bar_count(bar, others);
+        tc::bar_wait(bar, static_cast<uint32_t>(j / kStages) & 1);
+      }
+    }
+    tc::cluster_sync();
+  }
   tc::fence_after();
   if (warp == 1) tc::tmem_free(tmem, kAccumulators * kTileN);
 }
