@@ -832,7 +832,10 @@ zero_status zero_embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_
  * element's alignment only, the workspace 256 bytes; w with rows off 16-byte
  * boundaries is copied to the workspace first.  tokens at most 2^24, hidden
  * 2^20, vocab 2^22; |scale| in [1e-6, 1e6].  Outputs and workspace overlap no
- * input and no other output.  The same call gives the same bits.
+ * input and no other output.  The same call gives the same bits.  Where a bounded
+ * wait on the device gave up, in this call or in one that zero_sync has not
+ * reported yet, the losses, lse and gradients of kept tokens, the total and dw
+ * are NaN.
  */
 typedef enum { ZERO_LOSS_NONE = 0, ZERO_LOSS_SUM = 1, ZERO_LOSS_MEAN = 2 } zero_loss_reduction;
 

@@ -23,6 +23,10 @@
 //           piece's rows of dw (kDw), whose tiles fill each other's last round
 // The second forming of z is a quarter of the operations: the price of keeping
 // no logits between the passes.
+//
+// Every wait is bounded. One that gives up raises the device error word and the
+// call's own flag, which k_loss_gather clears (or raises, while the error word has
+// not been reported); k_loss_finish and k_loss_join read it and write NaN.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <inttypes.h>
@@ -102,7 +106,7 @@ struct ProductArgs {
   int32_t columns;       // of the piece
   int32_t piece;         // columns of a whole piece
   int32_t bf16;
-  int32_t* err;
+  int32_t *err, *gave_up;
   // kStats, kProbs
   int32_t narrow;        // columns of a narrow tile
   int32_t rows_a;        // rows of x in a box (fewer than 128: of one CTA, there are no more)
@@ -589,6 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool ok = true;
   auto give_up = [&] {
     atomicExch(a.err, 1);
+    atomicExch(a.gave_up, 1);
     for (uint32_t r = 0; r < 2; ++r) tc::store_cluster(tc::in_cta(tc::smem_of(&stopped), r), 1u);
   };
 
@@ -769,6 +774,7 @@ struct RowsArgs {
   int64_t tokens, hidden;
   int32_t* rows;  // [tokens + 1]: the kept tokens in order; the last entry is their number
   int32_t* ticket;
+  int32_t *err, *gave_up;
   // gathering
   const void* x;
   int64_t x_stride, xs_stride, rows_cap;
@@ -959,6 +965,8 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
     return;
   }
   const int64_t cta = blockIdx.x - copy.ctas;
+  const bool first = cta == 0 && threadIdx.x == 0;
+  const int err = first ? *a.err : 0;  // stored at the end: nothing waits for it
   int n;
   if constexpr (KIND == kForwardFew) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1050,6 +1058,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
       for (int c = lane; c < words; c += lanes) out[c] = W();
     }
   }
+  if (first) *a.gave_up = err != 0;
 }
 
 // Statistics of parts of a row, base 2: the larger maximum, the sum under it.
@@ -1067,6 +1076,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
   __shared__ float sums[kFinishThreads / 32], mine[kFinishRows];
   __shared__ bool last;
   wait_for_previous();
+  const int gave_up = *a.gave_up;
   const int n = kept_rows(a.rows + a.tokens, a.tokens);
   const int parts = kParts * static_cast<int>(over(a.vocab, tile_columns((n + kTileM - 1) / kTileM, a.vocab, a.narrow, a.pairs)));
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kFinishRows, rows = up(n, kTileM);
@@ -1104,7 +1114,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
       if (own < n && token >= 0) {
         // loss = log(1 + 2^d), d what the others' log2 of the sum is above the
         // target: differences first, so that small losses keep all their bits
-        const float log_sum = log2f(p.y), d = (p.x - target_z) + log_sum, e = exp2f(-fabsf(d)), less = log1pf(e);
+        const float log_sum = gave_up ? NAN : log2f(p.y), d = (p.x - target_z) + log_sum, e = exp2f(-fabsf(d)), less = log1pf(e);
         loss = target_z < INFINITY ? fmaf(fmaxf(d, 0.f), kLn2, less) : NAN;
         a.lse_out[token] = fmaf(d > 0.f ? p.x + log_sum : target_z, kLn2, less);
         a.losses[token] = loss;
@@ -1176,7 +1186,8 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_copy(const CopyArgs cop
 }
 
 // dx from its binary32 sums, where the product did not write it. The first CTAs
-// copy the last rows of dw, if it takes that.
+// copy the last rows of dw, if it takes that. After a wait that gave up: NaN for
+// all that was to be written, by whichever CTAs there are.
 struct JoinArgs {
   const int32_t* rows;
   int64_t tokens;
@@ -1184,17 +1195,36 @@ struct JoinArgs {
   int64_t sums_stride;
   const Scales* scales;
   const float* row_alpha;
-  void* dx;
-  int32_t hidden, piece, pieces, pairs, direct, log_lanes, vec;
+  void *dx, *dw;
+  int64_t dw_size;
+  const int32_t* gave_up;
+  int32_t hidden, piece, pieces, pairs, direct, log_lanes, vec, dw_type;
 };
+template <class T>
+__device__ __forceinline__ void write_nan(const JoinArgs& a) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGatherThreads;
+  const int64_t size = a.dx ? kept_rows(a.rows + a.tokens, a.tokens) * static_cast<int64_t>(a.hidden) : 0;
+  for (int64_t i = first; i < size; i += step) {
+    const int64_t row = i / a.hidden, t = a.rows[row];
+    if (t >= 0 && t < a.tokens) static_cast<T*>(a.dx)[t * a.hidden + i - row * a.hidden] = Elem<T>::narrow(NAN);
+  }
+  for (int64_t i = first; a.dw && i < a.dw_size; i += step) store_any(a.dw, i, a.dw_type, NAN);
+}
 template <class T>
 __global__ void __launch_bounds__(kGatherThreads) k_loss_join(const JoinArgs a, const CopyArgs copy) {
   wait_for_previous();
+  const int gave_up = *a.gave_up;
+  const int n = kept_rows(a.rows + a.tokens, a.tokens);
+  if (gave_up) {
+    write_nan<T>(a);
+    return;
+  }
   if (blockIdx.x < copy.ctas) {
     copy_rows(copy, blockIdx.x);
     return;
   }
-  const int n = kept_rows(a.rows + a.tokens, a.tokens);
+  if (!a.dx) return;
   const int splits = split_of((n + kTileM - 1) / kTileM * ((a.hidden + kTileN - 1) / kTileN), a.piece, a.pairs);
   if (splits == 1 && a.pieces == 1 && a.direct) return;
   const int lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
@@ -1284,7 +1314,7 @@ struct Layout {
     xs = take(rows_cap * xs_stride * 2);
     w = take(repack ? d.vocab * w_stride * 2 : 0);
     target = take(rows_cap * 4);
-    ticket = take(4);
+    ticket = take(8);  // and the flag of a wait that gave up
     cta_sums = take(backward ? 0 : over(rows_cap, kFinishRows) * 4);
     // kParts a tile and row; tiles narrower than 256 are at most three rounds of the pairs
     part = take(backward ? 0 : std::max(kParts * over(d.vocab, kTileN) * rows_cap, INT64_C(3) * kParts * kPairsMost * kTileM) * 8);
@@ -1473,12 +1503,13 @@ struct Call {
   zero_status begin(const char* fn, const void* x, const void* targets, int32_t* row_list, int32_t* err) {
     rows.targets = targets, rows.id_bytes = d.id_bytes, rows.vocab = static_cast<int32_t>(d.vocab);
     rows.tokens = d.tokens, rows.hidden = d.hidden, rows.rows = row_list, rows.ticket = in<int32_t>(at.ticket);
+    rows.err = product.err = err, rows.gave_up = product.gave_up = rows.ticket + 1;
     rows.x = x, rows.x_stride = d.x_stride, rows.xs = in<void>(at.xs), rows.xs_stride = at.xs_stride;
     rows.rows_cap = at.rows_cap, rows.target = in<int32_t>(at.target);
     set_vec(d.hidden % 8 == 0 && d.x_stride % 8 == 0 && aligned_to(x, 16));
     product.count = row_list + d.tokens, product.rows_cap = at.rows_cap;
     product.hidden = static_cast<int32_t>(d.hidden);
-    product.bf16 = bf16, product.err = err, product.scale2 = static_cast<float>(d.scale * 1.4426950408889634);
+    product.bf16 = bf16, product.scale2 = static_cast<float>(d.scale * 1.4426950408889634);
     product.target = rows.target, product.rows = row_list, product.tokens = d.tokens;
     product.pieces = static_cast<int32_t>(at.pieces), product.piece = static_cast<int32_t>(at.columns);
     int pairs = 0;
@@ -1664,20 +1695,21 @@ zero_status backward(const char* fn, const zero_linear_ce_desc* desc, const void
     if (dw && !at.whole) {
       const int bytes = type_bytes(dw_dtype);
       copy = c.copy_of(p.dw.p, p.dw.stride, static_cast<char*>(dw) + first * d.hidden * bytes, d.hidden, columns, bytes);
-      if (!dx || first + at.columns < d.vocab)
+      if (first + at.columns < d.vocab)
         LOSS_CUDA(launch(&k_loss_copy, copy.ctas, kGatherThreads, 0, true, c.s, static_cast<const CopyArgs>(copy)));
     }
   }
-  if (dx) {
-    JoinArgs j = {};
-    j.rows = rows, j.tokens = d.tokens, j.sums = c.in<float>(at.sums), j.sums_stride = at.sums_stride;
-    j.scales = c.rows.scales, j.row_alpha = c.rows.row_alpha, j.dx = dx;
-    j.hidden = static_cast<int32_t>(d.hidden), j.piece = c.product.piece, j.pieces = c.product.pieces;
-    j.pairs = c.product.pairs, j.direct = at.whole, j.vec = at.whole && aligned_to(dx, 16);
-    j.log_lanes = lanes_for(d.hidden, 8);
-    LOSS_CUDA(launch(c.bf16 ? &k_loss_join<__nv_bfloat16> : &k_loss_join<__half>, copy.ctas + ctas_for(d.tokens, j.log_lanes),
-                     kGatherThreads, 0, true, c.s, static_cast<const JoinArgs>(j), static_cast<const CopyArgs>(copy)));
-  }
+  // dw alone as well: it is the last to look whether a wait gave up
+  JoinArgs j = {};
+  j.rows = rows, j.tokens = d.tokens, j.sums = c.in<float>(at.sums), j.sums_stride = at.sums_stride;
+  j.scales = c.rows.scales, j.row_alpha = c.rows.row_alpha, j.gave_up = c.rows.gave_up;
+  j.dx = dx, j.dw = dw, j.dw_size = d.vocab * d.hidden, j.dw_type = dw_dtype;
+  j.hidden = static_cast<int32_t>(d.hidden), j.piece = c.product.piece, j.pieces = c.product.pieces;
+  j.pairs = c.product.pairs, j.direct = at.whole, j.vec = at.whole && aligned_to(dx, 16);
+  j.log_lanes = lanes_for(d.hidden, 8);
+  const int64_t join_ctas = dx ? ctas_for(d.tokens, j.log_lanes) : copy.ctas ? 0 : kSMs;
+  LOSS_CUDA(launch(c.bf16 ? &k_loss_join<__nv_bfloat16> : &k_loss_join<__half>, copy.ctas + join_ctas, kGatherThreads, 0,
+                   true, c.s, static_cast<const JoinArgs>(j), static_cast<const CopyArgs>(copy)));
   return ZERO_OK;
 }
 
