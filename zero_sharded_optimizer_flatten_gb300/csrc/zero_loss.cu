@@ -1326,8 +1326,11 @@ struct Layout {
     row_alpha = take(backward && d.dtype == ZERO_FP16 ? rows_cap * 4 : 0);
     scales = take(sizeof(Scales));
     dz = take(backward ? all_rows * columns * 2 : 0);
-    // as many rows as there are tokens, or the parts of few
-    const int64_t split_rows = static_cast<int64_t>(kPairsMost) * kTileM;
+    // as many rows as there are tokens, or the parts of few: splits x row tiles x
+    // column tiles are at most the pairs (see split_of), none where one row tile's
+    // columns pass half of them
+    const int64_t n_tiles = over(d.hidden, kTileN);
+    const int64_t split_rows = 2 * n_tiles > kPairsMost ? 0 : kPairsMost / n_tiles * kTileM;
     sums = take(backward ? (pieces > 1 || !whole ? std::max(split_rows, rows_cap) : split_rows) * sums_stride * 4 : 0);
     dw = take(backward && !whole ? columns * sums_stride * 4 : 0);
     bytes = at;
