@@ -348,12 +348,12 @@ struct Epilogue {
   float lse2 = 0.f, mul = 0.f, own = 0.f, rest = 0.f;
   float alpha = 0.f;
   int64_t token = -1;
-  bool direct = true, twice = false;
+  bool direct = true, twice;
   int64_t sums_rows = 0;
 
   __device__ __forceinline__ Epilogue(const ProductArgs& a_, int n_, const Tiles<KIND>& t, int m, int nt, int split_,
-                                      int row_in_tile, int half)
-      : a(a_), n(n_), split(split_) {
+                                      int row_in_tile, int half, bool twice_)
+      : a(a_), n(n_), split(split_), twice(twice_) {
     row = static_cast<int64_t>(m) * kTileM + row_in_tile;
     col = nt * t.columns;
     part = nt * INT64_C(1) * kParts + half;
@@ -364,7 +364,6 @@ struct Epilogue {
     if constexpr (KIND == kProbs) {
       if (live) lse2 = a.lse2[row], mul = a.row_mul[row];
       if (live && a.rest) rest = a.rest[row];
-      twice = a.row_own && a.scales->own;
       if (live && twice) own = a.row_own[row];
     }
     if constexpr (KIND == kDx) {
@@ -586,6 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   wait_for_previous();
 
+  const bool own = !is_stats(KIND) && a.row_own && a.scales->own;
   const int n = kept_rows(a.count, a.tokens);
   Schedule<KIND> todo(a, n, blockIdx.x >> 1, gridDim.x >> 1);
   Tile t;
@@ -600,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     // dx's rows of dz
     [[maybe_unused]] const int own_rows =
-        is_grads(KIND) && a.row_own && a.scales->own ? a.terms * static_cast<int>(a.rows_cap) : 0;
+        is_grads(KIND) && own ? a.terms * static_cast<int>(a.rows_cap) : 0;
     Ring<kStages> ring;
     uint64_t issued = 0;
     while (ok && todo.next(t)) {
@@ -723,19 +723,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     [[maybe_unused]] auto segments = [&] { return max(1, (t.k1 - t.k0 + kLong - 1) / kLong); };
     while (ok && todo.next(t)) {
       if constexpr (KIND == kStatsLong) {
-        Epilogue<KIND> e(a, n, todo.tiles, t.m, t.n, t.s, row, half);
+        Epilogue<KIND> e(a, n, todo.tiles, t.m, t.n, t.s, row, half, own);
         e.run_segments(segments(), c0, c1, false, next, free);
       } else if constexpr (!is_grads(KIND)) {
-        Epilogue<KIND> e(a, n, todo.tiles, t.m, t.n, t.s, row, half);
+        Epilogue<KIND> e(a, n, todo.tiles, t.m, t.n, t.s, row, half, own);
         work(e);
       } else if (t.dw) {
-        Epilogue<kDw, KIND == kGradsLong> e(a, n, todo.dw, t.m, t.n, t.s, row, half);
+        Epilogue<kDw, KIND == kGradsLong> e(a, n, todo.dw, t.m, t.n, t.s, row, half, own);
         if constexpr (KIND == kGradsLong)
           e.run_segments(segments(), c0, c1, t.k0 == t.k1, next, free);
         else
           work(e);
       } else {
-        Epilogue<kDx> e(a, n, todo.dx, t.m, t.n, t.s, row, half);
+        Epilogue<kDx> e(a, n, todo.dx, t.m, t.n, t.s, row, half, own);
         work(e);
       }
     }
@@ -1012,6 +1012,17 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
   const int t = i >= n ? -1 : KIND == kForwardFew ? few[i] : a.rows[i];
   if (t >= 0 && t < a.tokens) {
     const W* from = reinterpret_cast<const W*>(static_cast<const char*>(a.x) + t * a.x_stride * 2);
+    // one lane's, loaded ahead of the row
+    int target = -1;
+    [[maybe_unused]] float lse = 0.f, rest = 0.f, g = scales.g;
+    if (lane == 0) {
+      target = load_target(a, t);
+      if constexpr (BACKWARD) {
+        lse = a.lse[t];
+        if (a.rest) rest = a.rest[t];
+        if (a.reduction == ZERO_LOSS_NONE) g = a.d[t];
+      }
+    }
     if constexpr (sizeof(W) == 2) {  // rows that start anywhere
       copy_row(reinterpret_cast<const __half*>(from), reinterpret_cast<__half*>(to), words, t == 0 || t == a.tokens - 1,
                lane, lanes);
@@ -1026,13 +1037,11 @@ __global__ void __launch_bounds__(kGatherThreads) k_loss_gather(const RowsArgs a
       }
     }
     if (lane == 0) {
-      const int target = load_target(a, t);
       a.target[i] = target;
       if constexpr (BACKWARD) {
-        a.lse2[i] = a.lse[t] * kLog2e;
-        const float g = a.reduction == ZERO_LOSS_NONE ? a.d[t] : scales.g;
+        a.lse2[i] = lse * kLog2e;
         a.row_mul[i] = target < 0 ? 0.f : g * scales.mul;
-        if (a.rest) a.row_rest[i] = a.rest[t];
+        if (a.rest) a.row_rest[i] = rest;
         if (a.row_alpha) {
           const Scales own = scales.own ? scales_for(fabsf(g), g, a.scale) : scales;
           (a.row_own ? a.row_own : a.row_mul)[i] = target < 0 ? 0.f : g * own.mul;
@@ -1085,6 +1094,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
   const bool writes = threadIdx.x % kFinishGroups == 0;
   const int token = writes && own < n ? a.rows[own] : -1;
   const float target_z = writes && own < n ? a.target_z[own] : 0.f;
+  const bool left_out = writes && own < a.tokens && load_target(a, own) < 0;
   {
     const int r = threadIdx.x % kFinishRows, g = threadIdx.x / kFinishRows;
     float top = -INFINITY, sum = 0.f;
@@ -1122,7 +1132,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const RowsArgs a
         if (a.rest_out) a.rest_out[token] = target_z < INFINITY ? (d > 0.f ? 1.f : e) / (1.f + e) : NAN;
       }
       mine[r] = loss;
-      if (own < a.tokens && load_target(a, own) < 0) {
+      if (left_out) {
         a.lse_out[own] = 0.f, a.losses[own] = 0.f;
         if (a.rest_out) a.rest_out[own] = 0.f;
       }

@@ -397,11 +397,12 @@ __global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kThreads) 
 }
 
 // CTAs an SM: one fewer at 8 experts a lane (70 registers in place of 64) took
-// 30.6 us in place of 26.8 (65536 x 256 fp32).
+// 30.6 us in place of 26.7 (65536 x 256 fp32).
 constexpr int backward_ctas(int vpt) { return vpt <= 4 ? 5 : vpt <= 8 ? 4 : 1; }
 
 template <class T, int VPT>
 __global__ void __launch_bounds__(256, backward_ctas(VPT)) k_route_backward(const RouteArgs a) {
+  constexpr int P = (VPT + 1) / 2;  // pairs of a lane's experts, the last of one expert half empty
   extern __shared__ __align__(16) float direct[];  // [warps][32 * VPT]: what the choices add
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, K = a.topk;
   float* mine = direct + warp * 32 * VPT;
@@ -411,10 +412,12 @@ __global__ void __launch_bounds__(256, backward_ctas(VPT)) k_route_backward(cons
   const float n = fmaxf(a.stats[a.tokens], 1.f);
   const float per_count = a.d_losses ? a.d_losses[0] * (static_cast<float>(E) / static_cast<float>(K)) / n / n : 0.f;
   const float per_lse = a.d_losses ? 2.f * a.d_losses[1] / n : 0.f;
-  float load[VPT];
+  auto load_of = [&](int j) {
+    return j < VPT && lane * VPT + j < E ? per_count * static_cast<float>(a.counts[lane * VPT + j]) : 0.f;
+  };
+  F2 load[P];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
-    load[j] = lane * VPT + j < E ? per_count * static_cast<float>(a.counts[lane * VPT + j]) : 0.f;
+  for (int q = 0; q < P; ++q) load[q] = f2(load_of(2 * q), load_of(2 * q + 1));
   const T* z = static_cast<const T*>(a.z);
   T* dz = static_cast<T*>(a.dz);
   const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -434,9 +437,9 @@ __global__ void __launch_bounds__(256, backward_ctas(VPT)) k_route_backward(cons
   int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
   fetch(t);
   for (; t < a.tokens; t += step) {
-    float v[VPT];
+    F2 e[P];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) v[j] = next_v[j];
+    for (int q = 0; q < P; ++q) e[q] = f2(next_v[2 * q], 2 * q + 1 < VPT ? next_v[VPT == 1 ? 0 : 2 * q + 1] : -INFINITY);
     const float lse = next_lse;
     int id = next_id;
     float w = next_w, d = next_d;
@@ -445,22 +448,25 @@ __global__ void __launch_bounds__(256, backward_ctas(VPT)) k_route_backward(cons
     const bool any = __shfl_sync(kFull, id, 0) >= 0;
     const float wd = warp_all_sum(id >= 0 ? w * d : 0.f);
     if (id >= 0) mine[id] = a.normalize ? w * (d - wd) : w * d;
-    // p from the row itself, as forward: lse alone has lost log(sum) where the scores are large
-    float most = -INFINITY;
+    // p is exp(z - lse) over the sum of these: lse as it was rounded has lost
+    // log(sum) where the scores are large, but lies less than 14 above the largest
+    F2 total2 = f2(0.f), s2 = total2;
+    const F2 minus = f2(-lse), log2e = f2(kLog2e);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) most = fmaxf(most, v[j]);
-    most = warp_max(most);
-    exp_from(v, any ? most : 0.f);
-    float total = 0.f, s = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) total += v[j], s = fmaf(v[j], load[j], s);
+    for (int q = 0; q < P; ++q) {
+      float lo, hi;
+      f2_out(mul2(add2(e[q], minus), log2e), lo, hi);
+      e[q] = f2(tc::exp2_of(lo), tc::exp2_of(hi));
+      total2 = add2(total2, e[q]), s2 = fma2(e[q], load[q], s2);
+    }
+    float total = sum2(total2), s = sum2(s2);
     sum_both(total, s);
     const float inv = any ? reciprocal(total) : 0.f;
     s *= inv;
     if (!a.normalize) s += wd;
-    const float shift = per_lse * lse - s;
+    const F2 by = f2(inv), shift = f2((per_lse * lse - s) * inv);
     __syncwarp();
-    float extra[VPT];
+    float extra[2 * P];
     if constexpr (VPT % 4 == 0) {
 #pragma unroll
       for (int j = 0; j < VPT; j += 4) {
@@ -469,10 +475,16 @@ __global__ void __launch_bounds__(256, backward_ctas(VPT)) k_route_backward(cons
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) extra[j] = mine[lane * VPT + j];
+      for (int j = 0; j < 2 * P; ++j) extra[j] = j < VPT ? mine[lane * VPT + j] : 0.f;
     }
+    float v[2 * P];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) v[j] = any ? fmaf(v[j] * inv, load[j] + shift, extra[j]) : 0.f;
+    for (int q = 0; q < P; ++q)
+      f2_out(fma2(e[q], fma2(load[q], by, shift), f2(extra[2 * q], extra[2 * q + 1])), v[2 * q], v[2 * q + 1]);
+    if (!any) {
+#pragma unroll
+      for (int j = 0; j < 2 * P; ++j) v[j] = 0.f;
+    }
     __syncwarp();
     if (id >= 0) mine[id] = 0.f;
     __syncwarp();  // another lane may have the same expert of the next token
