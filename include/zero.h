@@ -869,7 +869,8 @@ zero_status zero_linear_cross_entropy_rest(const zero_linear_ce_desc* desc, cons
  * from the forward call's lse and rows; x, w and targets still hold what it
  * read.  d_loss (device): of ZERO_LOSS_NONE float[tokens], the gradients of the
  * losses; else one float, of their sum or of their mean (total[1], total[0]).
- * The logits are formed again, a piece of the vocabulary at a time; their
+ * The logits are formed again, a piece of the vocabulary at a time, p of them to
+ * 2^-22 |lse| of itself; their
  * gradient is rounded to dtype between its two products, scaled by the power of
  * two that brings the largest finite |d_loss| to [2^13, 2^14) (for dx in fp16
  * every token's own, once they lie 2^16 apart); for a dw in binary32 it is rounded
@@ -927,8 +928,8 @@ zero_status zero_sync(void* stream);
  * ever completes, gives up after limit_ns nanoseconds (1e3 .. 1e10) and
  * raises the device error word, so the next zero_sync(stream) returns
  * ZERO_ERR_TIMEOUT.  No fault and no hang: the context stays usable.  The
- * library's only waiting kernels (the optional bulk-copy staging of the
- * fused step) give up the same way, after one second.
+ * library's waiting kernels (the cross entropy's products) give up the same way,
+ * after two seconds.
  */
 zero_status zero_selftest_wait_timeout(int64_t limit_ns, void* stream);
 

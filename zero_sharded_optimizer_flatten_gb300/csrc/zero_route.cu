@@ -188,7 +188,7 @@ struct Totals {
 // taken one after the other instead: the warp's largest value, the first lane
 // that holds it and there the first place. NaN counts as +inf.
 //
-// Measured, 65536 tokens, 8 of 256 fp32 (67 MB): 39 us (493
+// Measured, 65536 tokens, 8 of 256 fp32 (67 MB): 38-40 us (498
 // instructions a token); one after the other always 53, by integer keys 74.
 template <class T, int VPT>
 __global__ void __launch_bounds__(32 * warps_of(VPT), 1) k_route(const RouteArgs a) {
